@@ -15,6 +15,9 @@ Entry points (same names as the C ABI):
 * ``qm_matmul_q4_0_algo(A, wq, N, algo, out=None, stream=None)``
 * ``qm_gemv_q4_0_list(problems, M, counters=None, stream=None)``: a list of
   GEMV problems ``(A, wq, C, N, wait_for)`` in one persistent launch
+* ``KVCache(k_pages, v_pages, page_table, lengths, ...)``: a paged 4-bit
+  key/value cache, with ``qm_kv_append_q4_0``, ``qm_kv_read_q4_0``,
+  ``qm_attn_q4_0`` and ``qm_kv_evict_q4_0`` over it
 * ``qm_device_status(stream=None, clear=True)``, ``qm_status_string(code)``,
   ``qm_version()``
 
@@ -40,6 +43,8 @@ __all__ = [
     "QM_ALGO_GEMV_PK", "qm_gemv_plan", "GEMV_PLAN_FIELDS", "qm_gemm_plan", "GEMM_PLAN_FIELDS",
     "EXPORTED_SYMBOLS", "QmGemvProblem", "qm_gemv_q4_0_list_ptr", "qm_gemv_q4_0_list",
     "gemv_problem_array",
+    "QM_ERR_RANGE", "QM_ERR_WORKSPACE", "QM_F32", "QM_BF16", "QmKVCache", "QmAttnArgs", "KVCache", "kv_page_bytes",
+    "qm_kv_append_q4_0", "qm_kv_read_q4_0", "qm_attn_q4_0", "qm_attn_workspace", "qm_kv_evict_q4_0",
 ]
 
 QM_OK = 0
@@ -52,6 +57,11 @@ QM_ERR_TIMEOUT = -6
 QM_ERR_UNSUPPORTED = -7
 QM_ERR_POINTER = -8
 QM_ERR_TOO_LARGE = -9
+QM_ERR_RANGE = -10
+QM_ERR_WORKSPACE = -11
+
+QM_F32 = 0
+QM_BF16 = 1
 
 QM_ALGO_AUTO = 0
 QM_ALGO_GEMV = 1
@@ -69,7 +79,8 @@ EXPORTED_SYMBOLS = ("qm_version", "qm_status_string", "qm_dequant_q4_0", "qm_mat
                     "qm_matmul_q4_0_algo", "qm_device_status", "qm_launch_count", "qm_gemv_plan", "qm_gemm_plan",
                     "qm_matmul_q4_0_noalloc", "qm_dequant_q8_0", "qm_quantize_q8_0",
                     "qm_selftest_wait_timeout", "qm_gemv_q4_0_list", "qm_matmul_q4_0_q8act",
-                    "qm_gemv_q4_0_q8act_list")
+                    "qm_gemv_q4_0_q8act_list", "qm_kv_append_q4_0", "qm_kv_read_q4_0", "qm_attn_q4_0",
+                    "qm_attn_workspace", "qm_kv_evict_q4_0")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libqm.so")
@@ -82,6 +93,24 @@ class QmGemvProblem(ctypes.Structure):
     _fields_ = [("A", ctypes.c_void_p), ("wq", ctypes.c_void_p), ("C", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("wait_for", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class QmKVCache(ctypes.Structure):
+    """The C struct qm_kv_cache (see include/qm.h)."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("max_len", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class QmAttnArgs(ctypes.Structure):
+    """The C struct qm_attn_args (see include/qm.h)."""
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("q_starts", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64), ("n_tokens", ctypes.c_int64), ("max_q", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("weights_stride", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("n_heads", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class QMError(RuntimeError):
@@ -137,6 +166,16 @@ def load_library() -> ctypes.CDLL:
             lib.qm_gemv_q4_0_list.restype = i32
             lib.qm_gemv_q4_0_q8act_list.argtypes = [p, i64, i64, p, p]
             lib.qm_gemv_q4_0_q8act_list.restype = i32
+            lib.qm_kv_append_q4_0.argtypes = [p, p, p, i32, i64, i64, i64, p, p]
+            lib.qm_kv_append_q4_0.restype = i32
+            lib.qm_kv_read_q4_0.argtypes = [p, p, p, i64, p, p]
+            lib.qm_kv_read_q4_0.restype = i32
+            lib.qm_attn_q4_0.argtypes = [p, p, p]
+            lib.qm_attn_q4_0.restype = i32
+            lib.qm_attn_workspace.argtypes = [p, i64, i64, i64, i32]
+            lib.qm_attn_workspace.restype = i64
+            lib.qm_kv_evict_q4_0.argtypes = [p, p, p, i64, i64, i64, i64, p, p, i64, p]
+            lib.qm_kv_evict_q4_0.restype = i32
             lib.qm_launch_count.argtypes = []
             lib.qm_launch_count.restype = ctypes.c_uint64
             _lib = lib
@@ -411,3 +450,222 @@ def qm_device_status(stream=None, clear: bool = True) -> int:
     """Synchronize the stream and return the device error status (QM_OK or
     QM_ERR_TIMEOUT); see include/qm.h."""
     return load_library().qm_device_status(_stream_handle(stream), 1 if clear else 0)
+
+
+# ------------------------------------------------------- the 4-bit key/value cache
+
+def kv_page_bytes(page_tokens: int, head_dim: int) -> int:
+    """Bytes of one page of one kv head (keys or values)."""
+    return page_tokens // 16 * 9 * head_dim
+
+
+class KVCache:
+    """A paged 4-bit key/value cache over the caller's tensors (see
+    include/qm.h for the layout): ``k_pages`` and ``v_pages`` uint8 ``[n_pages,
+    n_kv_heads, kv_page_bytes(page_tokens, head_dim)]``, ``page_table`` int32
+    ``[n_seqs, pages]``, ``lengths`` int32 ``[n_seqs]``.  ``max_len`` bounds the
+    lengths (default, and at most: what the page table can hold); a tighter
+    bound may be set at any time and gives smaller launches.  Keeps the tensors alive, and
+    one attention workspace for each stream it is used on."""
+
+    def __init__(self, k_pages, v_pages, page_table, lengths, head_dim: int, page_tokens: int, max_len=None):
+        import torch
+        for t, dtype, dims, name in ((k_pages, torch.uint8, 3, "k_pages"), (v_pages, torch.uint8, 3, "v_pages"),
+                                     (page_table, torch.int32, 2, "page_table"), (lengths, torch.int32, 1, "lengths")):
+            _require(t, dtype, name)
+            if t.dim() != dims:
+                raise ValueError(f"{name} must be {dims}-D")
+            if t.device != k_pages.device:
+                raise ValueError(f"{name} is on another device than k_pages")
+        if page_tokens < 16 or head_dim < 32 or k_pages.shape[2] != kv_page_bytes(page_tokens, head_dim):
+            raise ValueError("a page of k_pages is not page_tokens / 16 cells of 9 * head_dim bytes")
+        if v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages differ in shape")
+        if page_table.shape[0] != lengths.shape[0]:
+            raise ValueError("page_table and lengths differ in their number of sequences")
+        self.k_pages, self.v_pages, self.page_table, self.lengths = k_pages, v_pages, page_table, lengths
+        self.n_seqs, self.n_kv_heads, self.head_dim = lengths.shape[0], k_pages.shape[1], head_dim
+        self.struct = QmKVCache(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), lengths.data_ptr(),
+                                k_pages.shape[0], page_table.shape[1], 0, self.n_seqs, self.n_kv_heads, head_dim,
+                                page_tokens, 0)
+        self.ref = ctypes.addressof(self.struct)
+        self.capacity = page_table.shape[1] * page_tokens
+        self.max_len = self.capacity if max_len is None else max_len
+        self._workspaces = {}
+        self._sizes = {}
+
+    @property
+    def max_len(self) -> int:
+        return self.struct.max_len
+
+    @max_len.setter
+    def max_len(self, n: int):
+        if n < 0:
+            raise ValueError("max_len is negative")
+        self.struct.max_len = min(n, self.capacity)
+
+    def _workspace(self, n_heads: int, n_tokens: int, max_q: int, weights: bool, stream: int):
+        key = (n_heads, n_tokens, max_q, weights, self.struct.max_len)
+        need = self._sizes.get(key)
+        if need is None:
+            need = load_library().qm_attn_workspace(self.ref, n_heads, n_tokens, max_q, 1 if weights else 0)
+            if need < 0:
+                raise QMError(need, "qm_attn_workspace")
+            if len(self._sizes) > 256:
+                self._sizes.clear()
+            self._sizes[key] = need
+        if need == 0:
+            return None
+        ws = self._workspaces.get(stream)
+        if ws is None or ws.numel() < need:
+            import torch
+            with torch.cuda.device(self.k_pages.device), \
+                    torch.cuda.stream(torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()):
+                ws = torch.zeros(need, dtype=torch.uint8, device=self.k_pages.device)
+            self._workspaces[stream] = ws
+        return ws
+
+
+def _rows(t, heads, dim, name):
+    """Check a [n_tokens, heads, dim] tensor whose rows may be strided; (dtype code, row stride)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.float32:
+        code = QM_F32
+    elif t.dtype == torch.bfloat16:
+        code = QM_BF16
+    else:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
+        raise ValueError(f"{name} must be [n_tokens, heads, {dim}]")
+    stride = t.stride()
+    if stride[2] != 1 or stride[1] != dim:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return code, (stride[0] if shape[0] > 1 else shape[1] * dim)
+
+
+def _starts(q_starts, n_seqs):
+    import torch
+    if q_starts is None:
+        return 0
+    _require(q_starts, torch.int32, "q_starts")
+    if q_starts.numel() != n_seqs + 1:
+        raise ValueError("q_starts must have n_seqs + 1 entries")
+    return q_starts.data_ptr()
+
+
+def qm_kv_append_q4_0(cache, k, v, q_starts=None, stream=None):
+    """Quantize k and v (f32 or bf16 ``[n_tokens, n_kv_heads, head_dim]``, rows
+    may be strided) into the last places of their sequences; ``cache.lengths``
+    already counts them.  Row ranges ``q_starts`` int32 ``[n_seqs + 1]``, or
+    None for the same number of rows each."""
+    code, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k")
+    code_v, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v")
+    if code != code_v or v.shape != k.shape:
+        raise ValueError("k and v differ in type or shape")
+    _check(load_library().qm_kv_append_q4_0(cache.ref, k.data_ptr(), v.data_ptr(), code, k.shape[0], ks, vs,
+                                            _starts(q_starts, cache.n_seqs), _stream_handle(stream)),
+           "qm_kv_append_q4_0")
+
+
+def qm_kv_read_q4_0(cache, n_tokens: int, q_starts=None, k=None, v=None, stream=None):
+    """The f32 values of the last rows of each sequence, ``(k, v)`` of shape
+    ``[n_tokens, n_kv_heads, head_dim]``."""
+    import torch
+    shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.float32, device=cache.k_pages.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.float32, device=cache.k_pages.device)
+    for t, name in ((k, "k"), (v, "v")):
+        _require(t, torch.float32, name)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}")
+    _check(load_library().qm_kv_read_q4_0(cache.ref, k.data_ptr(), v.data_ptr(), n_tokens,
+                                          _starts(q_starts, cache.n_seqs), _stream_handle(stream)),
+           "qm_kv_read_q4_0")
+    return k, v
+
+
+def qm_attn_workspace(cache, n_heads: int, n_tokens: int, max_q: int, weights: bool = False) -> int:
+    """Bytes of workspace that qm_attn_q4_0 needs (see include/qm.h)."""
+    n = load_library().qm_attn_workspace(cache.ref, n_heads, n_tokens, max_q, 1 if weights else 0)
+    if n < 0:
+        raise QMError(n, "qm_attn_workspace")
+    return n
+
+
+def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts=None, max_q=None, weights=None,
+                 return_lse: bool = False, out=None, lse=None, stream=None):
+    """Causal attention of the rows ``q`` (f32 or bf16 ``[n_tokens, n_heads,
+    head_dim]``, rows may be strided) over the cache; returns ``out``, or
+    ``(out, lse)`` with ``return_lse`` (or an ``lse`` tensor).  ``scale`` defaults
+    to head_dim ** -0.5; ``window`` > 0 with ``sinks`` limits what a row sees to
+    its last ``window`` tokens and the first ``sinks``; ``weights`` f32 ``[n_seqs,
+    n_kv_heads, >= max_len]`` is added each token's attention weight; ``max_q``
+    bounds the rows of one sequence (default: all rows).  The workspace is the
+    cache's own, one per stream."""
+    import torch
+    code, qs = _rows(q, None, cache.head_dim, "q")
+    n_tokens, n_heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    code_o, os_ = _rows(out, n_heads, cache.head_dim, "out")
+    if code_o != code or out.shape[0] != n_tokens:
+        raise ValueError("out differs from q in type or shape")
+    if lse is None and return_lse:
+        lse = torch.empty((n_tokens, n_heads), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _require(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (n_tokens, n_heads):
+            raise ValueError("lse must be [n_tokens, n_heads]")
+    ws_stride = 0
+    if weights is not None:
+        _require(weights, torch.float32, "weights")
+        if weights.dim() != 3 or weights.shape[0] != cache.n_seqs or weights.shape[1] != cache.n_kv_heads:
+            raise ValueError("weights must be [n_seqs, n_kv_heads, max_len]")
+        ws_stride = weights.shape[2]
+    starts = _starts(q_starts, cache.n_seqs)
+    if q_starts is None:
+        max_q = n_tokens // cache.n_seqs if cache.n_seqs else 0
+    elif max_q is None:
+        max_q = n_tokens
+    handle = _stream_handle(stream)
+    ws = cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle)
+    args = QmAttnArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                      weights.data_ptr() if weights is not None else None, starts or None,
+                      ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, n_tokens, max_q,
+                      qs, os_, ws_stride, window, sinks, n_heads,
+                      cache.head_dim ** -0.5 if scale is None else scale, code, 0)
+    _check(load_library().qm_attn_q4_0(cache.ref, ctypes.addressof(args), handle), "qm_attn_q4_0")
+    return out if lse is None else (out, lse)
+
+
+def qm_kv_evict_q4_0(cache, to, weights, budget: int, sinks: int = 0, recent: int = 0, kept=None, weights_out=None,
+                     stream=None):
+    """Cut every sequence and kv head of ``cache`` back to ``budget`` tokens,
+    ranked by ``weights`` (f32 ``[n_seqs, n_kv_heads, >= max_len]``), into the
+    cache ``to`` (or in place, with ``to`` the same cache); see include/qm.h.
+    Returns ``(kept, weights_out)``."""
+    import torch
+    lists = (cache.n_seqs, cache.n_kv_heads)
+    _require(weights, torch.float32, "weights")
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != lists:
+        raise ValueError("weights must be [n_seqs, n_kv_heads, max_len]")
+    if kept is None:
+        kept = torch.empty((*lists, budget), dtype=torch.int32, device=weights.device)
+    if weights_out is None:
+        weights_out = torch.empty((*lists, budget), dtype=torch.float32, device=weights.device)
+    _require(kept, torch.int32, "kept")
+    _require(weights_out, torch.float32, "weights_out")
+    if tuple(kept.shape) != (*lists, budget) or weights_out.dim() != 3 or tuple(weights_out.shape[:2]) != lists:
+        raise ValueError("kept must be [n_seqs, n_kv_heads, budget], weights_out [n_seqs, n_kv_heads, >= budget]")
+    _check(load_library().qm_kv_evict_q4_0(cache.ref, to.ref, weights.data_ptr(), weights.shape[2], budget, sinks,
+                                           recent, kept.data_ptr(), weights_out.data_ptr(), weights_out.shape[2],
+                                           _stream_handle(stream)),
+           "qm_kv_evict_q4_0")
+    return kept, weights_out

@@ -1,0 +1,176 @@
+// Attention over the paged Q4_0 key/value cache, for any head dimension and
+// any number of rows: the plain kernels.
+#include <algorithm>
+
+#include "kv_cache.cuh"
+
+namespace qm {
+
+__device__ unsigned int g_attn_error = 0;
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// Value of dim 32 blk + lane of the token in `slot` of a cell.
+__device__ __forceinline__ float cell_value(const uint8_t* cell, int dim, int slot, int blk, int lane) {
+    const uint32_t byte = cell[blk * 256 + slot * 16 + (lane & 15)];
+    const uint32_t q = lane < 16 ? (byte & 15u) : (byte >> 4);
+    const float d = f16_bits_to_float(
+        *reinterpret_cast<const uint16_t*>(cell + cell_scales(dim) + (slot * (dim >> 5) + blk) * 2));
+    return magic_minus8(q | kMagicBits) * d;
+}
+
+// One warp per row and query head; lane l holds dims 32 i + l.  The softmax
+// runs in one pass over the tokens with a running maximum and sum, in f32.
+template <int NB, typename T>
+__global__ void __launch_bounds__(kWarps * 32) attn_plain_kernel(KvView c, KvRows r, AttnCall a, float* lse) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (item >= static_cast<int64_t>(r.n_tokens) * a.heads) return;
+    const int row = static_cast<int>(item / a.heads), head = static_cast<int>(item % a.heads);
+    const int b = kv_seq_of_row(r, c.n_seqs, row);
+    if (b < 0) return;
+    int first, count;
+    kv_rows(r, b, &first, &count, &g_attn_error);
+    if (row - first >= count) return;
+    const int pos = kv_length(c, b, &g_attn_error) - count + (row - first);
+    const int h = head / (a.heads / c.heads);
+    const T* q = static_cast<const T*>(a.q) + row * a.q_stride + static_cast<int64_t>(head) * c.dim;
+    float qv[NB], o[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        qv[i] = load1(q + 32 * i + lane) * (a.scale * kLog2e);
+        o[i] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;
+    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    for (int j = a.window > 0 && a.sinks > 0 ? 0 : lo; j <= pos; ++j) {
+        if (j < lo && j >= a.sinks) j = lo;
+        if (j > pos) break;
+        const int64_t off = kv_cell(c, b, h, j, &g_attn_error);
+        if (off < 0) continue;
+        const int slot = j & 15;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) s = fmaf(qv[i], cell_value(c.k + off, c.dim, slot, i, lane), s);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
+        const float m2 = fmaxf(m, s);
+        const float base = m2 == -INFINITY ? 0.f : m2;
+        const float keep = exp2f(m - base), p = exp2f(s - base);
+        m = m2;
+        l = fmaf(l, keep, p);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) o[i] = fmaf(p, cell_value(c.v + off, c.dim, slot, i, lane), o[i] * keep);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* out = static_cast<T*>(a.out) + row * a.out_stride + static_cast<int64_t>(head) * c.dim;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) store1(out + 32 * i + lane, o[i] * inv);
+    if (lse && lane == 0) lse[item] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// weights[b][h][j] += sum over the sequence's rows that see token j and the
+// group's query heads of exp(scale q . k_j - lse).  One warp per token, so
+// the sum has one owner and a fixed order.
+template <int NB, typename T>
+__global__ void __launch_bounds__(kWarps * 32) attn_weights_plain_kernel(KvView c, KvRows r, AttnCall a, const float* lse) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int j = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int L = kv_length(c, b, &g_attn_error);
+    if (j >= L) return;
+    int first, count;
+    kv_rows(r, b, &first, &count, &g_attn_error);
+    const int64_t off = kv_cell(c, b, h, j, &g_attn_error);
+    if (off < 0) return;
+    float k[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) k[i] = cell_value(c.k + off, c.dim, j & 15, i, lane) * (a.scale * kLog2e);
+    const int group = a.heads / c.heads;
+    float acc = 0.f;
+    for (int i = max(0, j - (L - count)); i < count; ++i) {  // rows at positions >= j
+        const int pos = L - count + i;
+        if (a.window > 0 && j <= pos - a.window && j >= a.sinks) break;
+        for (int g = 0; g < group; ++g) {
+            const int head = h * group + g;
+            const T* q = static_cast<const T*>(a.q) + (first + i) * a.q_stride + static_cast<int64_t>(head) * c.dim;
+            float s = 0.f;
+#pragma unroll
+            for (int x = 0; x < NB; ++x) s = fmaf(load1(q + 32 * x + lane), k[x], s);
+#pragma unroll
+            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
+            acc += exp2f(s - lse[static_cast<int64_t>(first + i) * a.heads + head] * kLog2e);
+        }
+    }
+    if (lane == 0) {
+        float* w = a.weights + (static_cast<int64_t>(b) * c.heads + h) * a.weights_stride + j;
+        *w += acc;
+    }
+}
+
+template <int NB, typename T>
+cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
+    float* lse = a.lse ? a.lse : a.weights ? reinterpret_cast<float*>(a.ws) : nullptr;
+    const int64_t items = static_cast<int64_t>(r.n_tokens) * a.heads;
+    note_launch();
+    cudaError_t err = launch_pdl(attn_plain_kernel<NB, T>, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)),
+                                 dim3(kWarps * 32), 0, stream, c, r, a, lse);
+    if (err != cudaSuccess || !a.weights || c.max_len == 0) return err;
+    note_launch();
+    return launch_pdl(attn_weights_plain_kernel<NB, T>,
+                      dim3(static_cast<unsigned>((c.max_len + kWarps - 1) / kWarps), c.heads, c.n_seqs),
+                      dim3(kWarps * 32), 0, stream, c, r, a, lse);
+}
+
+template <int NB>
+cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
+    return a.type == KvType::kF32 ? launch_plain<NB, float>(c, r, a, stream)
+                                  : launch_plain<NB, __nv_bfloat16>(c, r, a, stream);
+}
+
+}  // namespace
+
+int64_t attn_workspace_bytes(const KvView&, int heads, int64_t n_tokens, int64_t, bool weights) {
+    return weights ? n_tokens * heads * 4 : 0;
+}
+
+cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,
+                        const DeviceInfo&) {
+    switch (c.dim / 32) {
+        case 1: return launch_plain<1>(c, r, a, stream);
+        case 2: return launch_plain<2>(c, r, a, stream);
+        case 3: return launch_plain<3>(c, r, a, stream);
+        case 4: return launch_plain<4>(c, r, a, stream);
+        case 5: return launch_plain<5>(c, r, a, stream);
+        case 6: return launch_plain<6>(c, r, a, stream);
+        case 7: return launch_plain<7>(c, r, a, stream);
+        default: return launch_plain<8>(c, r, a, stream);
+    }
+}
+
+cudaError_t attn_read_device_error(unsigned int* bits, bool clear) {
+    unsigned int v = 0;
+    cudaError_t err = cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(v));
+    if (err != cudaSuccess) return err;
+    *bits |= v;
+    if (clear && v) {
+        const unsigned int zero = 0;
+        err = cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero));
+    }
+    return err;
+}
+
+}  // namespace qm

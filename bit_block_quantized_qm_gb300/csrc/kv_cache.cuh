@@ -1,0 +1,71 @@
+// The paged Q4_0 key/value cache as the kernels see it: layout of cells and
+// pages, the rows of a call, and bounds-checked look-ups.
+#pragma once
+
+#include "qm_device.cuh"
+#include "qm_internal.h"
+
+namespace qm {
+
+// A cell holds 16 tokens of one kv head: [D/32][16 tokens][16 quant bytes],
+// then [16 tokens][D/32] f16 scales.  Eight tokens' quants of one block are
+// 128 consecutive bytes, which is what ldmatrix reads without bank conflicts,
+// and a token's scales are one aligned word or two.
+constexpr int kCellTokens = 16;
+__host__ __device__ constexpr int cell_bytes(int D) { return 9 * D; }
+__host__ __device__ constexpr int cell_scales(int D) { return 8 * D; }  // offset of the scales
+
+// Tokens in the cache of sequence b, and what is wrong with the number.
+__device__ __forceinline__ int kv_length(const KvView& c, int b, unsigned int* err) {
+    const int n = __ldg(c.lengths + b);
+    if (n < 0 || n > c.max_len) {
+        atomicOr(err, kErrRange);
+        return n < 0 ? 0 : static_cast<int>(c.max_len);
+    }
+    return n;
+}
+
+// First row and number of rows of sequence b in this call.
+__device__ __forceinline__ void kv_rows(const KvRows& r, int b, int* first, int* count, unsigned int* err) {
+    if (!r.starts) {
+        *first = b * r.uniform;
+        *count = r.uniform;
+        return;
+    }
+    int a = __ldg(r.starts + b), e = __ldg(r.starts + b + 1);
+    if (a < 0 || e < a || e > r.n_tokens || e - a > r.max_q) {
+        atomicOr(err, kErrRange);
+        a = min(max(a, 0), r.n_tokens);
+        e = min(min(max(e, a), r.n_tokens), a + r.max_q);
+    }
+    *first = a;
+    *count = e - a;
+}
+
+// Byte offset in the pool of the cell that holds token `pos` of sequence b and
+// kv head h, or -1 (and the error bit) where the page table has no page for it.
+__device__ __forceinline__ int64_t kv_cell(const KvView& c, int b, int h, int pos, unsigned int* err) {
+    const int page = pos >> c.page_shift;
+    int id = -1;
+    if (page < c.table_stride) id = __ldg(c.table + b * c.table_stride + page);
+    if (id < 0 || id >= c.n_pages) {
+        atomicOr(err, kErrRange);
+        return -1;
+    }
+    const int cells = 1 << (c.page_shift - 4);
+    return ((static_cast<int64_t>(id) * c.heads + h) * cells + ((pos >> 4) & (cells - 1))) * cell_bytes(c.dim);
+}
+
+// The sequence that row `row` belongs to, or -1.
+__device__ __forceinline__ int kv_seq_of_row(const KvRows& r, int n_seqs, int row) {
+    if (!r.starts) return row / r.uniform;
+    int lo = 0, hi = n_seqs;  // the last b with starts[b] <= row
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(r.starts + mid + 1) <= row) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo < n_seqs && __ldg(r.starts + lo) <= row ? lo : -1;
+}
+
+}  // namespace qm

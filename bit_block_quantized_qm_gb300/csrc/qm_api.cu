@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "qm.h"
+#include "qm_checks.h"
 #include "qm_internal.h"
 #ifdef QM_TEST_HOOKS
 #include <atomic>
@@ -119,41 +120,10 @@ namespace {
 
 constexpr int kVersion = 100;  // 0.1.0
 
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > INT64_MAX / a) return false;
-    *out = a * b;
-    return true;
-}
-
-bool overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    if (a_bytes <= 0 || b_bytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + static_cast<uintptr_t>(b_bytes) && b0 < a0 + static_cast<uintptr_t>(a_bytes);
-}
-
-// The pointer must be device-accessible memory of `device`: device or managed
-// memory, or host memory registered/mapped with a device address.
-int check_pointer(const void* p, int device) {
-    cudaPointerAttributes attr;
-    cudaError_t err = cudaPointerGetAttributes(&attr, p);
-    if (err != cudaSuccess) {
-        cudaGetLastError();
-        return QM_ERR_POINTER;
-    }
-    switch (attr.type) {
-        case cudaMemoryTypeDevice:
-            return attr.device == device ? QM_OK : QM_ERR_POINTER;
-        case cudaMemoryTypeManaged:
-            return QM_OK;
-        case cudaMemoryTypeHost:
-            return attr.devicePointer == p ? QM_OK : QM_ERR_POINTER;
-        default:
-            return QM_ERR_POINTER;
-    }
-}
-
-int from_cuda(cudaError_t err) { return err == cudaSuccess ? QM_OK : QM_ERR_CUDA; }
+using qm::check_pointer;
+using qm::from_cuda;
+using qm::mul_ok;
+using qm::overlaps;
 
 int run_matmul(const float* A, const void* wq, float* C, int64_t M, int64_t N, int64_t K, int algo,
                cudaStream_t s, const qm::DeviceInfo& dev);
@@ -240,6 +210,8 @@ const char* qm_status_string(int status) {
         case QM_ERR_UNSUPPORTED: return "the forced algorithm cannot run this shape";
         case QM_ERR_POINTER: return "a pointer is not device memory of the current device";
         case QM_ERR_TOO_LARGE: return "beyond the fixed scratch of qm_matmul_q4_0_noalloc (M > 8)";
+        case QM_ERR_RANGE: return "a page table entry, a length or a row offset on the device was out of range";
+        case QM_ERR_WORKSPACE: return "the workspace is smaller than qm_attn_workspace says";
         default: return "unknown status";
     }
 }
@@ -520,7 +492,10 @@ int qm_device_status(void* stream, int clear) {
     if (qm::gemm_tc_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
     if (qm::gemv_tc_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
     if (qm::gemv_list_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
-    return bits ? QM_ERR_TIMEOUT : QM_OK;
+    if (qm::kv_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
+    if (qm::attn_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
+    if (bits & qm::kErrWaitTimeout) return QM_ERR_TIMEOUT;
+    return bits ? QM_ERR_RANGE : QM_OK;
 }
 
 #ifdef QM_TEST_HOOKS

@@ -8,6 +8,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "qm_internal.h"
+
 namespace qm {
 
 constexpr int kBlockBytes = 18;  // Q4_0 block: f16 d + 16 quant bytes
@@ -17,9 +19,6 @@ constexpr int kBlockElems = 32;
 // float 2^23 + v exactly; subtracting 2^23 + 8 then leaves (v - 8) exactly.
 constexpr uint32_t kMagicBits = 0x4B000000u;
 constexpr float kMagicPlus8 = 8388616.0f;  // 2^23 + 8
-
-// Device error bits (one word per translation unit that waits on copies).
-constexpr unsigned int kErrWaitTimeout = 1u;
 
 // Polls of an mbarrier before a wait gives up.  try_wait blocks for a
 // hardware-defined slice per poll, so this bounds a wait to well under a

@@ -7,6 +7,11 @@
 
 namespace qm {
 
+// Device error bits (one word per translation unit that sets them; read back
+// by qm_device_status).
+constexpr unsigned int kErrWaitTimeout = 1u;  // a bounded wait gave up
+constexpr unsigned int kErrRange = 2u;  // a page, length or row offset that only the device sees is out of range
+
 struct DeviceInfo {
     int device = 0;
     int sm_count = 0;
@@ -144,6 +149,69 @@ cudaError_t gemm_tc_read_device_error(unsigned int* bits, bool clear);
 cudaError_t launch_gemm_q4_0_simt(const float* A, const uint8_t* wq, float* C, int64_t M,
                                   int64_t N, int64_t K, cudaStream_t stream,
                                   const DeviceInfo& dev);
+
+// ---- the paged Q4_0 key/value cache (kv_cache.cu, attn*.cu) ----------------
+
+struct KvView {
+    uint8_t* k;  // pools: [n_pages][heads][page_tokens / 16] cells of 9 * dim bytes
+    uint8_t* v;
+    const int32_t* table;    // [n_seqs][table_stride] page numbers
+    const int32_t* lengths;  // [n_seqs] tokens in the cache
+    int64_t table_stride;
+    int64_t max_len;  // no length is above it
+    int n_pages;
+    int n_seqs;
+    int heads;
+    int dim;
+    int page_shift;  // log2(page_tokens)
+};
+
+// The rows of a call: sequence b owns rows starts[b] .. starts[b + 1] - 1, or
+// `uniform` rows each without starts.  They are its last tokens.
+struct KvRows {
+    const int32_t* starts;
+    int uniform;
+    int n_tokens;
+    int max_q;  // no sequence has more rows
+};
+
+// IO types of keys, values, queries and outputs.
+enum class KvType { kF32, kBF16 };
+
+cudaError_t launch_kv_append(const KvView& c, const KvRows& r, const void* k, const void* v, KvType type,
+                             int64_t k_stride, int64_t v_stride, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvView& c, const KvRows& r, float* k, float* v, cudaStream_t stream);
+
+struct AttnCall {
+    const void* q;
+    void* out;
+    float* lse;      // [n_tokens][heads] or null
+    float* weights;  // [n_seqs][kv heads][weights_stride] or null
+    int64_t q_stride, out_stride, weights_stride;
+    int heads;       // query heads
+    int window, sinks;
+    float scale;
+    KvType type;
+    uint8_t* ws;     // workspace (attn_workspace_bytes), its counters zero
+};
+
+// Bytes of workspace that launch_attn needs for these sizes.
+int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
+cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,
+                        const DeviceInfo& dev);
+
+struct EvictCall {
+    const float* weights;
+    float* weights_out;
+    int32_t* kept;  // [n_seqs][kv heads][budget]
+    int32_t* lengths_out;
+    int64_t weights_stride, out_stride;
+    int budget, sinks, recent;
+};
+cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCall& e, cudaStream_t stream,
+                            const DeviceInfo& dev);
+cudaError_t kv_read_device_error(unsigned int* bits, bool clear);
+cudaError_t attn_read_device_error(unsigned int* bits, bool clear);
 
 // Count one kernel enqueued by the library.
 void note_launch();

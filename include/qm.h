@@ -1,7 +1,7 @@
 /*
  * qm.h — C ABI of libqm: the GGML Q4_0 x f32 quantized matmul, the Q4_0
- * dequant and the Q8_0 dequant and quantize, as hand-written CUDA kernels for
- * sm_103a (GB300).
+ * dequant, the Q8_0 dequant and quantize, and a 4-bit key/value cache with its
+ * attention, as hand-written CUDA kernels for sm_103a (GB300).
  *
  * Operations (defined in "fuel-vulkan-kernels — quantized (GGML) kernel
  * contracts", fuel-dispatch 0.20.71, kernel-contracts/vulkan/quantized.fkc.md):
@@ -41,10 +41,12 @@
  *     launch, so one may start its prologue while the previous kernel on the
  *     stream finishes; it reads and writes memory only after that kernel has
  *     completed, so stream order is kept exactly as for ordinary launches.
- *   - Operands are contiguous; no strides, offsets or broadcasts.
+ *   - Operands are contiguous; no strides, offsets or broadcasts (but the rows
+ *     that the key/value cache's entry points take may be strided).
  *   - Arguments are checked on the host before anything is enqueued; a
  *     failed check returns a negative status and leaves memory untouched.
  *   - An output never aliases an input: overlapping byte ranges are rejected.
+ *     (qm_kv_evict_q4_0 names its exceptions.)
  */
 #ifndef QM_H
 #define QM_H
@@ -76,6 +78,15 @@ extern "C" {
                                    device                                        */
 #define QM_ERR_TOO_LARGE (-9)   /* beyond the fixed scratch of
                                    qm_matmul_q4_0_noalloc (M > 8)               */
+#define QM_ERR_RANGE (-10)      /* a page number, length or row offset in device
+                                   memory was out of range (see
+                                   qm_device_status)                             */
+#define QM_ERR_WORKSPACE (-11)  /* the workspace is smaller than
+                                   qm_attn_workspace says                        */
+
+/* Element types of keys, values, queries and attention outputs. */
+#define QM_F32 0
+#define QM_BF16 1
 
 /* Algorithms for qm_matmul_q4_0_algo. */
 #define QM_ALGO_AUTO 0      /* what qm_matmul_q4_0 picks: GEMV_PK for M <= 2 and
@@ -176,9 +187,11 @@ QM_API int qm_matmul_q4_0_algo(const float* A, const void* wq, float* C, int64_t
  * qm_device_status — synchronizes `stream` and reads the library's device
  * error word for the current device.  Kernels that wait on asynchronous
  * copies give up after a bounded number of polls, set this word and return
- * early (their output is then incomplete).  Returns QM_OK if the word is
- * clear, QM_ERR_TIMEOUT if a wait gave up, QM_ERR_CUDA if the synchronize or
- * the read failed.  With clear != 0 the word is reset after reading.
+ * early (their output is then incomplete); the key/value cache's kernels set
+ * it where a page number, a length or a row offset in device memory is out of
+ * range, and skip the access.  Returns QM_OK if the word is clear,
+ * QM_ERR_TIMEOUT if a wait gave up, QM_ERR_RANGE if only such a number was out
+ * of range, QM_ERR_CUDA if the synchronize or the read failed.  With clear != 0 the word is reset after reading.
  */
 QM_API int qm_device_status(void* stream, int clear);
 
@@ -342,6 +355,164 @@ QM_API int qm_gemm_plan(int64_t M, int64_t N, int64_t K, int sm_count, int fit2,
  */
 QM_API int qm_gemv_plan(int64_t M, int64_t N, int64_t K, int packed, int sm_count, int smem_optin,
                         int fit2, int fit4, int fit8, int noalloc, int64_t* out);
+
+/* ------------------------------------------------------------------------
+ * A 4-bit key/value cache: append, read back, attend, evict.  No counterpart
+ * on the kernel-contract pages, which stop at the products: this is what a
+ * decoder built on them keeps between its steps.  Keys and values are held as
+ * Q4_0 values, (nibble - 8) * d with one binary16 scale d for each 32 elements
+ * along the head dimension, in pages.
+ *
+ * Layout.  A cell holds 16 tokens of one kv head, 9 * head_dim bytes:
+ * [head_dim / 32 blocks][16 tokens][16 quant bytes], then the scales
+ * [16 tokens][head_dim / 32] in binary16.  The 16 quant bytes of a block are
+ * those of a Q4_0 block (element j the low nibble of byte j, element j + 16 its
+ * high nibble).  A page is page_tokens / 16 cells of one kv head in token
+ * order; a pool is [n_pages][n_kv_heads] pages, one pool for keys and one for
+ * values, same page numbers.  Token t of sequence b lives in page
+ * page_table[b * table_stride + t / page_tokens].
+ *
+ * Rows of a call.  lengths[b] counts the tokens of sequence b including the
+ * call's own; the call's rows of sequence b are its last ones, rows
+ * q_starts[b] .. q_starts[b + 1] - 1 of the tensors (a device array of
+ * n_seqs + 1; NULL gives every sequence n_tokens / n_seqs rows).  So a step
+ * raises lengths, appends, then attends.  Rows that no sequence has are not
+ * touched.
+ *
+ * What the host cannot see (page numbers, lengths, offsets) the kernels check:
+ * a token whose page is missing or out of range, a length outside 0 .. max_len
+ * or an offset outside the rows sets the device error word (QM_ERR_RANGE from
+ * qm_device_status); the access is skipped and the outputs of that sequence
+ * are unspecified.  Entries of page_table past a sequence's length are not
+ * read.
+ * ------------------------------------------------------------------------ */
+typedef struct qm_kv_cache {
+    void* k_pages;             /* n_pages * n_kv_heads pages, 16-byte aligned     */
+    void* v_pages;             /* likewise                                        */
+    const int32_t* page_table; /* device, [n_seqs][table_stride]                  */
+    int32_t* lengths;          /* device, [n_seqs]                                */
+    int64_t n_pages;
+    int64_t table_stride;      /* page table entries per sequence                 */
+    int64_t max_len;           /* no length is above it; <= table_stride *
+                                  page_tokens and <= 2^30                         */
+    int32_t n_seqs;            /* 0 .. 65535                                      */
+    int32_t n_kv_heads;        /* 1 .. 32767                                      */
+    int32_t head_dim;          /* a multiple of 32, 32 .. 256                     */
+    int32_t page_tokens;       /* a power of two, 16 .. 65536                     */
+    int32_t reserved;          /* 0                                               */
+} qm_kv_cache;
+
+/*
+ * qm_kv_append_q4_0 — quantizes the call's rows of k and v into their places.
+ *   k, v : [n_tokens][n_kv_heads][head_dim] of `dtype`, rows k_stride and
+ *          v_stride elements apart (multiples of 4; so slices of a joint
+ *          projection can be passed), 16-byte aligned (8-byte for QM_BF16).
+ * Each block of 32 takes m, its first element of largest magnitude, d = m / -8
+ * and r = 1 / d (each one correctly rounded f32 division), quants min(15,
+ * floor(x r + 8.5)) (product and sum rounded to f32), and keeps d narrowed to
+ * binary16, round to nearest even.  NaN elements do not raise the maximum and
+ * become 8 (the value 0), as do all of a block whose m is 0; a magnitude past
+ * 8 * 65504 makes d infinite.  Deterministic.  lengths is not changed.
+ * Returns QM_OK or a negative status.
+ */
+QM_API int qm_kv_append_q4_0(const qm_kv_cache* cache, const void* k, const void* v, int dtype,
+                             int64_t n_tokens, int64_t k_stride, int64_t v_stride,
+                             const int32_t* q_starts, void* stream);
+
+/*
+ * qm_kv_read_q4_0 — the inverse: the values of the call's rows (the last ones
+ * of each sequence) as f32, contiguous [n_tokens][n_kv_heads][head_dim],
+ * 16-byte aligned.  Exact, as qm_dequant_q4_0.
+ */
+QM_API int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t n_tokens,
+                           const int32_t* q_starts, void* stream);
+
+/*
+ * qm_attn_q4_0 — causal attention of the call's rows over the cache, grouped
+ * query heads: query head h reads kv head h / (n_heads / n_kv_heads).
+ *   s_j   = scale * q . k_j, for every token j that the row sees,
+ *   out   = sum_j p_j v_j with p = softmax(s), lse = log sum_j exp(s_j).
+ * A row at position p (0-based) of its sequence sees token j when j <= p and,
+ * with window > 0, also j > p - window or j < sinks: a sliding window and a few
+ * first tokens that stay visible.  A row that sees no token (its sequence is
+ * shorter than its rows) gets out = +0 and lse = -infinity.
+ *   q, out   : [n_tokens][n_heads][head_dim] of `dtype`, rows q_stride and
+ *              out_stride elements apart (multiples of 4), 16-byte aligned
+ *              (8-byte for QM_BF16).
+ *   lse      : NULL, or [n_tokens][n_heads] f32, natural logarithm.
+ *   weights  : NULL, or [n_seqs][n_kv_heads][weights_stride] f32 (weights_stride
+ *              >= max_len): each token's accumulated attention weight;
+ *              weights[b][h][j] += the sum of p_j over the sequence's rows and
+ *              the query heads that read kv head h.  What qm_kv_evict_q4_0
+ *              ranks by.
+ *   max_q    : no sequence has more rows than this in the call (ignored
+ *              without q_starts).
+ *   workspace: qm_attn_workspace bytes, 16-byte aligned, zeroed once before its
+ *              first use; every call leaves it fit for the next one.  Calls
+ *              that may run at the same time need a workspace each.
+ * Precision: scores, statistics and sums in f32; products to about 2^-21 of
+ * each |q_i k_i| and |p_j v_j| for QM_F32; for QM_BF16, where the output keeps
+ * 8 bits, probabilities (and in long calls keys and values) may be rounded to
+ * 11 bits.  Tokens that a row does not see do not reach it, whatever their
+ * bytes hold.  A token that a row sees and whose scales are not finite makes
+ * at least those entries of the row non-finite that the formula does.  The
+ * same call on the same inputs gives bitwise the same results (no atomics
+ * on floating values).
+ * Returns QM_OK or a negative status.
+ */
+typedef struct qm_attn_args {
+    const void* q;
+    void* out;
+    float* lse;
+    float* weights;
+    const int32_t* q_starts;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t n_tokens;
+    int64_t max_q;
+    int64_t q_stride;
+    int64_t out_stride;
+    int64_t weights_stride;
+    int64_t window; /* 0: none */
+    int64_t sinks;
+    int64_t n_heads; /* a multiple of n_kv_heads */
+    float scale;
+    int32_t dtype;    /* QM_F32 or QM_BF16 */
+    int32_t reserved; /* 0 */
+} qm_attn_args;
+
+QM_API int qm_attn_q4_0(const qm_kv_cache* cache, const qm_attn_args* args, void* stream);
+
+/*
+ * qm_attn_workspace — bytes of workspace that qm_attn_q4_0 needs for calls of
+ * at most these sizes (weights != 0: with accumulated weights).  Host only.
+ * Returns the bytes (0: none is needed) or a negative status.
+ */
+QM_API int64_t qm_attn_workspace(const qm_kv_cache* cache, int64_t n_heads, int64_t n_tokens,
+                                 int64_t max_q, int weights);
+
+/*
+ * qm_kv_evict_q4_0 — cuts every (sequence, kv head) of `from` back to `budget`
+ * tokens and writes them, in order, to the first places of `to`.  A sequence
+ * of length L <= budget keeps all its tokens.  Of a longer one stay its first
+ * `sinks` tokens, its last `recent` ones (sinks + recent <= budget), and of
+ * those between, the ones with the largest weights; of equal weights the
+ * lowest positions; NaN ranks below every number and -0 equals +0.
+ *   weights     : [n_seqs][n_kv_heads][weights_stride] f32.
+ *   kept        : [n_seqs][n_kv_heads][budget] int32, the kept positions in
+ *                 ascending order, then -1.
+ *   weights_out : [n_seqs][n_kv_heads][out_stride] f32 (out_stride >= budget):
+ *                 the kept tokens' weights, then 0 up to budget.  May be
+ *                 `weights` itself (with the same stride).
+ *   to->lengths is set to min(L, budget).  `to` is another cache (it may share
+ *   pools, on other pages, and have pages of another size), or `from` itself:
+ *   then the cache is cut back in place.  from->lengths may be to->lengths.
+ * Cells are moved byte for byte; a kept token's position becomes its place.
+ * Returns QM_OK or a negative status.
+ */
+QM_API int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float* weights,
+                            int64_t weights_stride, int64_t budget, int64_t sinks, int64_t recent,
+                            int32_t* kept, float* weights_out, int64_t out_stride, void* stream);
 
 /*
  * qm_launch_count — the number of kernels this library has enqueued in this
