@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int64_t kLseOff = 4096;  // the workspace's first bytes are the step's counters
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_weights_plain_kernel(KvView 
 
 template <int NB, typename T>
 cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
-    float* lse = a.lse ? a.lse : a.weights ? reinterpret_cast<float*>(a.ws) : nullptr;
+    float* lse = a.lse ? a.lse : a.weights ? reinterpret_cast<float*>(a.ws + kLseOff) : nullptr;
     const int64_t items = static_cast<int64_t>(r.n_tokens) * a.heads;
     note_launch();
     cudaError_t err = launch_pdl(attn_plain_kernel<NB, T>, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)),
@@ -143,12 +144,14 @@ cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cu
 
 }  // namespace
 
-int64_t attn_workspace_bytes(const KvView&, int heads, int64_t n_tokens, int64_t, bool weights) {
-    return weights ? n_tokens * heads * 4 : 0;
+int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {
+    if (attn_step_takes(c, heads, max_q)) return attn_step_workspace(c, heads, n_tokens, max_q, weights);
+    return weights ? kLseOff + n_tokens * heads * 4 : 0;
 }
 
 cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,
                         const DeviceInfo&) {
+    if (attn_step_takes(c, a.heads, r.max_q)) return launch_attn_step(c, r, a, stream);
     switch (c.dim / 32) {
         case 1: return launch_plain<1>(c, r, a, stream);
         case 2: return launch_plain<2>(c, r, a, stream);

@@ -200,6 +200,33 @@ int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64
 cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,
                         const DeviceInfo& dev);
 
+// Few rows (attn_step.cu): head dimensions 64 and 128, at most kStepRows rows
+// (tokens times query heads of a kv head) per sequence and kv head.
+constexpr int kStepRows = 32;
+bool attn_step_takes(const KvView& c, int heads, int64_t max_q);
+int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
+cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);
+cudaError_t attn_step_read_device_error(unsigned int* bits, bool clear);
+
+// Opts a kernel into `bytes` of dynamic shared memory, once per device: one
+// static object per kernel.
+class SmemOnce {
+public:
+    template <typename... KArgs>
+    cudaError_t set(void (*kernel)(KArgs...), int bytes) {
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        if (dev < 64 && ((__atomic_load_n(&done_, __ATOMIC_ACQUIRE) >> dev) & 1u)) return cudaSuccess;
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err == cudaSuccess && dev < 64) __atomic_fetch_or(&done_, uint64_t(1) << dev, __ATOMIC_RELEASE);
+        return err;
+    }
+
+private:
+    uint64_t done_ = 0;
+};
+
 struct EvictCall {
     const float* weights;
     float* weights_out;
