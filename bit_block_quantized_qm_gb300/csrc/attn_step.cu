@@ -22,12 +22,14 @@
 // the FP32 pipe alone (one FMA per quant and query row) would need 3 times
 // that at four rows.
 //
-// Split.  A CTA of four warps takes one (sequence, kv head, 4 or 8 rows) and a
-// range of 64-token tiles; each warp runs its own tiles through its own
-// two-stage ring, filled with bulk copies (a cell is contiguous, a page is
-// too), and meets the others once at the end.  Ranges of one sequence meet in
-// the workspace: the last CTA to arrive adds them up in range order, so the
-// result does not depend on which one that is.
+// Split.  All (sequence, kv head, 4 or 8 rows) lists of 64-token tiles lie end to
+// end, and every CTA of a grid that fills the GPU once takes an equal stretch
+// of them, so sequences of any lengths keep all SMs busy to the end.  A CTA's
+// four warps take the tiles of a list in turn, each through its own two-stage
+// ring, filled with bulk copies (a cell is contiguous, a page is too), and
+// meet once at the list's or the stretch's end.  Where a list is cut, its
+// parts meet in the workspace: the last CTA to arrive adds them up in order,
+// so the result does not depend on which one that is.
 #include <algorithm>
 
 #include "kv_cache.cuh"
@@ -42,24 +44,25 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;  // tokens of a warp's tile
 constexpr int kStages = 2;
-constexpr float kTiny = 0x1p-23f;
+constexpr float kTiny = 0x1p-23f, kTinyLog = -23.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The grid: as many CTAs as the GPU holds at once (three per SM), each with an
+// equal share of all tiles.
+constexpr int kMaxCtas = 152 * 3;
+
 struct StepPlan {
-    int tiles_per_cta;  // of one range
-    int splits;         // ranges at most
-    int groups;         // row groups
-    int pad_len;        // tokens per row of the stashed scores (0: none)
+    int groups;   // row groups
+    int pad_len;  // tokens per row of the stashed scores (0: none)
     int64_t part_off, stash_off, lse_off, bytes;  // offsets in the workspace
+    uint32_t k1024;                               // two f16 1024
 };
 
 // The workspace begins with arrival counters, zero between calls: 4 KB of it
-// are never anything else, whatever calls share the workspace.  Ranges are cut
-// only where there are at most kTargetCtas / 2 of (sequence, kv head, rows).
-constexpr int kTargetCtas = 152 * 3 * 4;
+// are never anything else, whatever calls share the workspace.
 constexpr int64_t kCtrBytes = 4096;
-static_assert(kTargetCtas / 2 * 4 <= kCtrBytes, "a counter for each");
+static_assert(kMaxCtas * 4 <= kCtrBytes, "a counter for each");
 
 // Tiles that rows at positions pos0 .. L - 1 read: all of 0 .. L - 1, or the
 // first ones' and those from the window's lower end on.
@@ -138,13 +141,22 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t w[N]) {
 
 // n - 8 as f16 pairs for the low nibbles n of bytes 0 and 2 of w, and for their
 // high nibbles: OR-ed into the mantissa of 1024 a nibble reads 1024 + n (or
-// 1024 + 16 n), and one packed operation, exact, takes the rest away.
-__device__ __forceinline__ uint32_t minus8_low(uint32_t w) {
-    return as_word(__hadd2(as_half2((w & 0x000F000Fu) | 0x64006400u), as_half2(0xE408E408u)));  // - 1032
+// 1024 + 16 n), and one packed operation, exact, takes the rest away.  `k1024`
+// (two f16 1024) comes from memory: with both constants known the compiler
+// makes two logic instructions of the AND and the OR, and those bound the
+// kernel (131 of 432 instructions per 16 tokens, at half rate).
+__device__ __forceinline__ uint32_t minus8_low(uint32_t w, uint32_t k1024) {
+    return as_word(__hadd2(as_half2((w & 0x000F000Fu) | k1024), as_half2(0xE408E408u)));  // - 1032
 }
-__device__ __forceinline__ uint32_t minus8_high(uint32_t w) {
-    return as_word(__hfma2(as_half2((w & 0x00F000F0u) | 0x64006400u), as_half2(0x2C002C00u),  // / 16
-                           as_half2(0xD480D480u)));                                            // - 72
+__device__ __forceinline__ uint32_t minus8_high(uint32_t w, uint32_t k1024) {
+    return as_word(__hfma2(as_half2((w & 0x00F000F0u) | k1024), as_half2(0x2C002C00u),  // / 16
+                           as_half2(0xD480D480u)));                                      // - 72
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // 2^e for e in -126 .. 127.
@@ -160,6 +172,42 @@ struct StepShape {
     static_assert(kRows * D * 4 + 2 * kRows * 4 <= kRing, "a warp's sums fit in its ring");
 };
 
+// Tiles of sequence b for one kv head and row group: at least one where it has
+// rows (their outputs are written even if they see nothing).
+__device__ __forceinline__ TileList seq_tiles(const KvView& c, const KvRows& r, const AttnCall& a, int b, int* first,
+                                              int* count, int* L) {
+    kv_rows(r, b, first, count, &g_attn_step_error);
+    *L = kv_length(c, b, &g_attn_step_error);
+    TileList t{0, 0, 0};
+    if (*count > 0) {
+        t = tile_list(*L, max(*L - *count, 0), a.window, a.sinks);
+        t.count = max(t.count, 1);
+    }
+    return t;
+}
+
+// Sum of `v` over the threads before this one (*total: over all of them).
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+    }
+    __syncthreads();
+    *total = all;
+    return before + x - v;
+}
+
 template <int D, int NT, typename T>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     attn_step_kernel(KvView c, KvRows r, AttnCall a, StepPlan plan) {
@@ -167,32 +215,79 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     constexpr int NB = S::kBlocks;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t bars[kWarps][kStages];
-    __shared__ int s_last;
+    __shared__ int64_t scan[kWarps];
+    __shared__ int s_seq, s_last;
+    __shared__ int64_t s_seq_off;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     if (threadIdx.x < kWarps * kStages) mbar_init(&bars[0][0] + threadIdx.x, 1);
+    if (threadIdx.x == 0) s_seq = -1;
     fence_barrier_init();
     __syncthreads();
     grid_launch_dependents();
     grid_dependency_wait();
 
-    const int split = blockIdx.x % plan.splits, rg = blockIdx.x / plan.splits;
-    const int h = blockIdx.y, b = blockIdx.z;
-    int first, count;
-    kv_rows(r, b, &first, &count, &g_attn_step_error);
-    const int L = kv_length(c, b, &g_attn_step_error);
+    // All tiles of the call in one order (sequence, kv head, row group, tile):
+    // CTA x takes tiles x per .. (x + 1) per - 1 of it.
+    const int64_t lists = static_cast<int64_t>(c.heads) * plan.groups;  // tile lists per sequence
+    int64_t total = 0;
+    for (int b0 = 0; b0 < c.n_seqs; b0 += kThreads) {
+        int f, n, L;
+        const int bb = b0 + threadIdx.x;
+        int64_t all;
+        cta_scan(bb < c.n_seqs ? seq_tiles(c, r, a, bb, &f, &n, &L).count * lists : 0, scan, &all);
+        total += all;
+    }
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    per = max(static_cast<int64_t>(kWarps), (per + kWarps - 1) / kWarps * kWarps);
+    int64_t tile_at = per * blockIdx.x;
+    const int64_t tile_stop = min(total, tile_at + per);
+    if (tile_at >= tile_stop) return;
+    {
+        int64_t seen = 0;
+        for (int b0 = 0; b0 < c.n_seqs; b0 += kThreads) {
+            int f, n, L;
+            const int bb = b0 + threadIdx.x;
+            int64_t all;
+            const int64_t mine = bb < c.n_seqs ? seq_tiles(c, r, a, bb, &f, &n, &L).count * lists : 0;
+            const int64_t off = seen + cta_scan(mine, scan, &all);
+            if (off <= tile_at && tile_at < off + mine) {
+                s_seq = bb;
+                s_seq_off = off;
+            }
+            seen += all;
+            if (seen > tile_at) break;
+        }
+        __syncthreads();
+    }
+    int b = s_seq;
+    int64_t seq_off = s_seq_off;  // of sequence b's first tile
+    int first, count, L;
+    TileList tiles = seq_tiles(c, r, a, b, &first, &count, &L);
     const int group = a.heads / c.heads;
+    int n = 0;  // tiles that this warp has been through, for its ring
+    bool ok = true;
+
+    while (tile_at < tile_stop) {
+    while (tile_at >= seq_off + tiles.count * lists) {  // on to the next sequence with rows
+        seq_off += tiles.count * lists;
+        tiles = seq_tiles(c, r, a, ++b, &first, &count, &L);
+    }
+    const int list = static_cast<int>((tile_at - seq_off) / tiles.count);
+    const int64_t list_off = seq_off + static_cast<int64_t>(list) * tiles.count;
+    const int h = list / plan.groups, rg = list % plan.groups;
+    const int seg_begin = static_cast<int>(tile_at - list_off);
+    const int tile_end = static_cast<int>(min(tile_stop - list_off, static_cast<int64_t>(tiles.count)));
+    const bool at_range_start = tile_at == per * blockIdx.x;
+    tile_at = list_off + tile_end;
+
     const int n_rows = count * group;  // rows of this (sequence, kv head): token-major, then query head
     const int row0 = rg * S::kRows;
-    if (row0 >= n_rows) return;
     const int base_pos = L - count;  // position of the sequence's first row (may be negative)
+    if (row0 >= n_rows) continue;    // (a sequence with fewer rows than others: every thread alike)
     const int pos_lo = base_pos + row0 / group;
     const int pos_hi = base_pos + min(n_rows - 1, row0 + S::kRows - 1) / group;
     const int seen_len = max(0, min(L, pos_hi + 1));
-    const TileList tiles = tile_list(seen_len, max(pos_lo, 0), a.window, a.sinks);
-    const int n_splits = max(1, (tiles.count + plan.tiles_per_cta - 1) / plan.tiles_per_cta);
-    if (split >= n_splits) return;
-    const int tile_end = min(tiles.count, (split + 1) * plan.tiles_per_cta);
 
     // This thread's query row in score and output accumulators is 4 j + t; in
     // the operands it feeds it is 4 j + g / 2, piece g % 2.
@@ -245,26 +340,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     }
 
     uint8_t* my_ring = ring + warp * S::kRing;
-    // Lanes 0..7 copy a tile: keys' cells 0..3, then values'.  Where a page
-    // holds a tile, one copy takes all four cells.
+    // Eight lanes copy a tile: keys' cells 0..3, then values'.  Where a page
+    // holds a tile, one copy takes all four cells.  Lanes 8 u .. 8 u + 7 look
+    // up the pages of this warp's tile 4 x + u, four tiles at a time.
     const bool whole = c.page_shift >= 6;
-    auto source = [&](int i) -> int64_t {  // byte offset of this lane's part of tile i, -1: nothing to copy
-        if (lane >= 8 || i >= tile_end) return -1;
-        const int cell = lane & 3;
-        const int p = tiles.at(i) * kTile + cell * 16;
-        if (p >= seen_len || (whole && cell)) return -1;
+    const int tile_first = seg_begin + warp;
+    auto look_up = [&](int x) -> int64_t {  // for this warp's tiles 4 x .. 4 x + 3
+        const int i = tile_first + (4 * x + (lane >> 3)) * kWarps;
+        if (i >= tile_end) return -1;
+        const int p = tiles.at(i) * kTile + (lane & 3) * 16;
+        if (p >= seen_len || (whole && (lane & 3))) return -1;
         return kv_cell(c, b, h, p, &g_attn_step_error);
     };
-    auto issue = [&](int i, int stage, int64_t off) {
-        const int left = seen_len - tiles.at(i) * kTile;
+    int64_t off4 = look_up(0), off4_next = look_up(1);
+    auto issue = [&](int x, int stage) {  // this warp's tile x, looked up
+        const int left = seen_len - tiles.at(tile_first + x * kWarps) * kTile;
+        const bool mine = (lane >> 3) == (x & 3) && off4 >= 0;
         const int cells = whole ? min(4, (left + 15) >> 4) : 1;
-        const uint32_t bytes = off >= 0 ? static_cast<uint32_t>(cells * cell_bytes(D)) : 0u;
-        const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
-        if (lane == 0) mbar_arrive_expect_tx(&bars[warp][stage], total);
+        const uint32_t bytes = static_cast<uint32_t>(cells * cell_bytes(D));
+        const uint32_t copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(&bars[warp][stage], copies * bytes);
         __syncwarp();
-        if (off >= 0) {
-            uint8_t* dst = my_ring + stage * 2 * S::kHalf + (lane >> 2) * S::kHalf + (lane & 3) * cell_bytes(D);
-            bulk_load_1d(dst, ((lane & 4) ? c.v : c.k) + off, bytes, &bars[warp][stage]);
+        if (mine) {
+            uint8_t* dst = my_ring + stage * 2 * S::kHalf + ((lane >> 2) & 1) * S::kHalf + (lane & 3) * cell_bytes(D);
+            bulk_load_1d(dst, ((lane & 4) ? c.v : c.k) + off4, bytes, &bars[warp][stage]);
         }
     };
 
@@ -279,70 +378,74 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][k][0][e] = o[j][k][1][e] = 0.f;
     }
-    int v_up = 15;  // p is scaled by 2^v_up
+    int v_up = 14;  // p is scaled by 2^v_up
+    const uint32_t k1024 = plan.k1024;
 
-    const int tile_first = split * plan.tiles_per_cta + warp;
+    const int my_tiles = ok && tile_first < tile_end ? (tile_end - tile_first + kWarps - 1) / kWarps : 0;
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) {
-        const int i = tile_first + s * kWarps;
-        if (i < tile_end) issue(i, s, source(i));
-    }
-    int64_t off_next = source(tile_first + kStages * kWarps);  // looked up a tile ahead
+    for (int x = 0; x < kStages; ++x)
+        if (x < my_tiles) issue(x, (n + x) % kStages);
 
-    int n = 0, i = tile_first;
-    bool ok = true;
-    for (; i < tile_end; i += kWarps, ++n) {
+    int x = 0;
+    for (; x < my_tiles; ++x, ++n) {
         const int stage = n % kStages;
+        const int i = tile_first + x * kWarps;
         const uint8_t* kt = my_ring + stage * 2 * S::kHalf;
         uint8_t* vt = my_ring + stage * 2 * S::kHalf + S::kHalf;
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bars[warp][stage], (n / kStages) & 1, &g_attn_step_error));
         if (!ok) break;
         const int key0 = tiles.at(i) * kTile;
 
-        // The largest scale of the values; tokens past the end do not count.
+        // Scales of the values: where none reaches 2 (a bit of the exponent)
+        // and no token is past the end, nothing is to be done.
         uint32_t bad0 = 0, bad1 = 0;  // tokens with a scale that is not finite
         {
-            uint32_t top = 0;
-            bool odd = false;
+            uint32_t w[NB];
+            load_words<NB>(vt + (lane >> 3) * cell_bytes(D) + cell_scales(D) + (lane & 7) * 4 * NB, w);
+            uint32_t any = w[0];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int key = u * 32 + lane;
-                uint8_t* sc = vt + (key >> 4) * cell_bytes(D) + cell_scales(D) + (key & 15) * 2 * NB;
-                uint32_t w[NB / 2];
-                load_words<NB / 2>(sc, w);
-                uint32_t mx = w[0] & 0x7FFF7FFFu;
+            for (int e = 1; e < NB; ++e) any |= w[e];
+            if (__any_sync(0xFFFFFFFFu, (any & 0x40004000u) != 0) || key0 + kTile > seen_len) {
+                uint32_t top = 0;
 #pragma unroll
-                for (int e = 1; e < NB / 2; ++e) mx = __vmaxu2(mx, w[e] & 0x7FFF7FFFu);
-                mx = max(mx & 0xFFFFu, mx >> 16);
-                const bool past = key0 + key >= seen_len;
-                const bool wild = !past && mx >= 0x7C00u;
-                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, wild);
-                if (u == 0) bad0 = bits;
-                else bad1 = bits;
-                if (past || wild) {
+                for (int u = 0; u < 2; ++u) {
+                    const int key = u * 32 + lane;
+                    uint8_t* sc = vt + (key >> 4) * cell_bytes(D) + cell_scales(D) + (key & 15) * 2 * NB;
+                    uint32_t y[NB / 2];
+                    load_words<NB / 2>(sc, y);
+                    uint32_t mx = y[0] & 0x7FFF7FFFu;
 #pragma unroll
-                    for (int e = 0; e < NB / 2; ++e) reinterpret_cast<uint32_t*>(sc)[e] = 0u;
-                    odd = true;
-                    mx = 0;
+                    for (int e = 1; e < NB / 2; ++e) mx = __vmaxu2(mx, y[e] & 0x7FFF7FFFu);
+                    mx = max(mx & 0xFFFFu, mx >> 16);
+                    const bool past = key0 + key >= seen_len;
+                    const bool wild = !past && mx >= 0x7C00u;
+                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, wild);
+                    if (u == 0) bad0 = bits;
+                    else bad1 = bits;
+                    if (past || wild) {  // such tokens' products are 0; NaN comes with the scores
+#pragma unroll
+                        for (int e = 0; e < NB / 2; ++e) reinterpret_cast<uint32_t*>(sc)[e] = 0u;
+                        mx = 0;
+                    }
+                    top = max(top, mx);
                 }
-                top = max(top, mx);
-            }
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            if (__any_sync(0xFFFFFFFFu, odd)) __syncwarp();
-            // 2^v_up d <= 2^15 for d < 2^(exponent + 1).
-            const int need = min(15, 14 - (static_cast<int>(top >> 10) - 15));
-            if (need < v_up) {
-                const float down = pow2(need - v_up);
-                v_up = need;
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                __syncwarp();
+                // p 2^v_up d < 2^15 for d < 2^(exponent + 1).
+                const int need = min(14, 14 - (static_cast<int>(top >> 10) - 15));
+                if (need < v_up) {
+                    const float down = pow2(need - v_up);
+                    v_up = need;
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                    for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int k = 0; k < NB; ++k)
+                        for (int k = 0; k < NB; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[j][k][0][e] *= down;
-                            o[j][k][1][e] *= down;
-                        }
+                            for (int e = 0; e < 4; ++e) {
+                                o[j][k][0][e] *= down;
+                                o[j][k][1][e] *= down;
+                            }
+                }
             }
         }
 
@@ -365,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     const int k = k2 + u;
                     const uint32_t w0 = w[2 * u], w1 = w[2 * u + 1];
                     const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
-                    const uint32_t l0 = minus8_low(w0), l1 = minus8_low(w1), l2 = minus8_low(y0), l3 = minus8_low(y1);
-                    const uint32_t h0 = minus8_high(w0), h1 = minus8_high(w1), h2 = minus8_high(y0),
-                                   h3 = minus8_high(y1);
+                    const uint32_t l0 = minus8_low(w0, k1024), l1 = minus8_low(w1, k1024), l2 = minus8_low(y0, k1024), l3 = minus8_low(y1, k1024);
+                    const uint32_t h0 = minus8_high(w0, k1024), h1 = minus8_high(w1, k1024), h2 = minus8_high(y0, k1024),
+                                   h3 = minus8_high(y1, k1024);
                     const float2 dd0 = __half22float2(as_half2(d0[k2 / 2]));
                     const float2 dd1 = __half22float2(as_half2(d1[k2 / 2]));
                     const float e0 = u ? dd0.y : dd0.x, e1 = u ? dd1.y : dd1.x;
@@ -386,24 +489,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         // To base 2, masked where some row does not see some token.
         const bool all_seen = key0 + kTile <= min(pos_lo + 1, L) && !(bad0 | bad1) &&
                               (a.window == 0 || key0 > pos_hi - a.window || key0 + kTile <= a.sinks);
+        bool more = false;  // some token's p is below kTiny, but not 0
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            float mx = -INFINITY;
+            float mx = -INFINITY, mn = INFINITY;
 #pragma unroll
             for (int cell = 0; cell < 4; ++cell) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float x = s[cell][j][e] * to_log2[j];
+                    float y = x;
                     if (!all_seen) {
                         const int in_tile = 16 * cell + 8 * e + g;
                         const int key = key0 + in_tile;
                         const bool sees = key <= pos[j] && key < L &&
                                           (a.window == 0 || key > pos[j] - a.window || key < a.sinks);
                         if (((in_tile < 32 ? bad0 : bad1) >> (in_tile & 31)) & 1u) x = NAN;
-                        if (!sees) x = -INFINITY;
+                        if (!sees) x = -INFINITY, y = INFINITY;
                     }
                     s[cell][j][e] = x;
                     mx = fmaxf(mx, x);
+                    mn = fminf(mn, y);
                 }
             }
             if (plan.pad_len) {
@@ -423,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             const float m2 = fmaxf(m[j], mx);
             const float base = m2 == -INFINITY ? 0.f : m2;
             if (mx > m[j]) {
-                const float keep = exp2f(m[j] - base);
+                const float keep = exp2_approx(m[j] - base);
                 l[j] *= keep;
 #pragma unroll
                 for (int k = 0; k < NB; ++k)
@@ -434,10 +540,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     }
             }
             m[j] = m2;
+            more |= mn - base < kTinyLog;
 #pragma unroll
             for (int cell = 0; cell < 4; ++cell) {
-                s[cell][j][0] = exp2f(s[cell][j][0] - base);
-                s[cell][j][1] = exp2f(s[cell][j][1] - base);
+                s[cell][j][0] = exp2_approx(s[cell][j][0] - base);
+                s[cell][j][1] = exp2_approx(s[cell][j][1] - base);
                 l[j] += s[cell][j][0] + s[cell][j][1];
             }
         }
@@ -451,13 +558,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         float lift = 1.f;
         for (;;) {
             float rest[4][NT][2];
-            bool more = false;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int cell = 0; cell < 4; ++cell)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) more |= s[cell][j][e] < kTiny && s[cell][j][e] > 0.f;
             more = __any_sync(0xFFFFFFFFu, more) && lift < 0x1p69f;
             if (more) {
 #pragma unroll
@@ -508,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                         const uint32_t sel = u ? 0x7632u : 0x5410u;
                         const __half2 da = as_half2(__byte_perm(dw[0][k2 / 2], dw[0][NB / 2 + k2 / 2], sel));
                         const __half2 db = as_half2(__byte_perm(dw[1][k2 / 2], dw[1][NB / 2 + k2 / 2], sel));
-                        const uint32_t l0 = minus8_low(w0), l1 = minus8_low(y0), l2 = minus8_low(w1), l3 = minus8_low(y1);
-                        const uint32_t h0 = minus8_high(w0), h1 = minus8_high(y0), h2 = minus8_high(w1),
-                                       h3 = minus8_high(y1);
+                        const uint32_t l0 = minus8_low(w0, k1024), l1 = minus8_low(y0, k1024), l2 = minus8_low(w1, k1024), l3 = minus8_low(y1, k1024);
+                        const uint32_t h0 = minus8_high(w0, k1024), h1 = minus8_high(y0, k1024), h2 = minus8_high(w1, k1024),
+                                       h3 = minus8_high(y1, k1024);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
                             const __half2 pa = as_half2(ph[j][0]), pb = as_half2(ph[j][1]);
@@ -526,10 +626,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             }
             if (!more) break;
             lift *= 1.f / kTiny;
+            more = false;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
 #pragma unroll
-                for (int cell = 0; cell < 4; ++cell) s[cell][j][0] = rest[cell][j][0], s[cell][j][1] = rest[cell][j][1];
+                for (int cell = 0; cell < 4; ++cell)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        s[cell][j][e] = rest[cell][j][e];
+                        more |= s[cell][j][e] < kTiny && s[cell][j][e] > 0.f;
+                    }
 #pragma unroll
                 for (int k = 0; k < NB; ++k)
 #pragma unroll
@@ -553,14 +659,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         }
 
         __syncwarp();
-        const int nx = i + kStages * kWarps;
-        if (nx < tile_end) {
+        const int nx = x + kStages;
+        if (nx < my_tiles) {
+            if ((nx & 3) == 0) {
+                off4 = off4_next;
+                off4_next = look_up((nx >> 2) + 1);
+            }
             fence_proxy_async_shared();  // scales zeroed above, then overwritten by the copy
-            issue(nx, stage, off_next);
-            off_next = source(nx + kWarps);
+            issue(nx, stage);
         }
     }
-    if (!ok && i + kWarps < tile_end) {  // a copy that did not land: wait for the other stage's too
+    if (!ok && x + 1 < my_tiles) {  // a copy that did not land: wait for the other stage's too
         mbar_wait_bounded(&bars[warp][(n + 1) % kStages], ((n + 1) / kStages) & 1, &g_attn_step_error);
     }
 
@@ -602,9 +711,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         }
     };
 
-    const int64_t pair = (static_cast<int64_t>(b) * c.heads + h) * plan.groups + rg;
-    constexpr int kPart = S::kRows * (D + 2);  // floats of one range's sums
-    float* part = reinterpret_cast<float*>(a.ws + plan.part_off) + (pair * plan.splits + split) * kPart;
+    constexpr int kPart = S::kRows * (D + 2);  // floats of one segment's sums
+    const bool alone = seg_begin == 0 && tile_end == tiles.count;  // the whole list
+    // A CTA's first segment has slot 0, its last one (if another) slot 1.
+    float* parts = reinterpret_cast<float*>(a.ws + plan.part_off);
+    float* part = parts + (static_cast<int64_t>(blockIdx.x) * 2 + (at_range_start ? 0 : 1)) * kPart;
     for (int it = threadIdx.x; it < S::kRows * D / 4; it += kThreads) {
         const int rl = it / (D / 4), d4 = (it % (D / 4)) * 4;
         float mm = -INFINITY;
@@ -620,15 +731,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float* src = reinterpret_cast<const float*>(ring + w * S::kRing);
-            const float f = exp2f(mw[w] - base);
+            const float f = exp2_approx(mw[w] - base);
             ll = fmaf(f, src[S::kRows * D + S::kRows + rl], ll);
-            const float4 x = *reinterpret_cast<const float4*>(src + rl * D + d4);
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            v.z = fmaf(f, x.z, v.z);
-            v.w = fmaf(f, x.w, v.w);
+            const float4 y = *reinterpret_cast<const float4*>(src + rl * D + d4);
+            v.x = fmaf(f, y.x, v.x);
+            v.y = fmaf(f, y.y, v.y);
+            v.z = fmaf(f, y.z, v.z);
+            v.w = fmaf(f, y.w, v.w);
         }
-        if (n_splits == 1) {
+        if (alone) {
             if (row0 + rl < n_rows) finish(row0 + rl, d4, v, mm, ll);
         } else {
             *reinterpret_cast<float4*>(part + rl * D + d4) = v;
@@ -638,42 +749,51 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             }
         }
     }
-    if (n_splits == 1) return;
-
-    // The last range to arrive adds all of them up, in order.
-    __threadfence();
-    __syncthreads();
-    unsigned* ctr = reinterpret_cast<unsigned*>(a.ws) + pair;
-    if (threadIdx.x == 0) {
-        const unsigned before = atomicAdd(ctr, 1u);
-        s_last = before == static_cast<unsigned>(n_splits) - 1;
-        if (s_last) *ctr = 0;  // fit for the next call
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const float* parts = reinterpret_cast<const float*>(a.ws + plan.part_off) + pair * plan.splits * kPart;
-    for (int it = threadIdx.x; it < S::kRows * D / 4; it += kThreads) {
-        const int rl = it / (D / 4), d4 = (it % (D / 4)) * 4;
-        if (row0 + rl >= n_rows) continue;
-        float mm = -INFINITY;
-        for (int x = 0; x < n_splits; ++x) mm = fmaxf(mm, __ldcg(parts + x * kPart + S::kRows * D + rl));
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int x = 0; x < n_splits; ++x) {
-            const float* p = parts + x * kPart;
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + rl * D + d4));
-            const float f = exp2f(__ldcg(p + S::kRows * D + rl) - base);
-            ll = fmaf(f, __ldcg(p + S::kRows * D + S::kRows + rl), ll);
-            v.x = fmaf(f, y.x, v.x);
-            v.y = fmaf(f, y.y, v.y);
-            v.z = fmaf(f, y.z, v.z);
-            v.w = fmaf(f, y.w, v.w);
+    if (!alone) {
+        // The last segment of a list to arrive adds all of them up, in order.
+        const int64_t c0 = list_off / per, c1 = (list_off + tiles.count - 1) / per;  // CTAs of the list
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            // No two lists that are cut begin in the same CTA.
+            unsigned* ctr = reinterpret_cast<unsigned*>(a.ws) + c0;
+            const unsigned before = atomicAdd(ctr, 1u);
+            s_last = before == static_cast<unsigned>(c1 - c0);
+            if (s_last) *ctr = 0;  // fit for the next call
         }
-        finish(row0 + rl, d4, v, mm, ll);
+        __syncthreads();
+        if (s_last) {
+            __threadfence();
+            const int n_parts = static_cast<int>(c1 - c0) + 1;
+            const float* p0 = parts + (c0 * 2 + (list_off == c0 * per ? 0 : 1)) * kPart;
+            auto part_of = [&](int y) { return y == 0 ? p0 : parts + (c0 + y) * 2 * kPart; };
+            for (int it = threadIdx.x; it < S::kRows * D / 4; it += kThreads) {
+                const int rl = it / (D / 4), d4 = (it % (D / 4)) * 4;
+                if (row0 + rl >= n_rows) continue;
+                float mm = -INFINITY;
+#pragma unroll 8
+                for (int y = 0; y < n_parts; ++y) mm = fmaxf(mm, __ldcg(part_of(y) + S::kRows * D + rl));
+                const float base = mm == -INFINITY ? 0.f : mm;
+                float ll = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int y = 0; y < n_parts; ++y) {
+                    const float* p = part_of(y);
+                    const float4 w = __ldcg(reinterpret_cast<const float4*>(p + rl * D + d4));
+                    const float f = exp2_approx(__ldcg(p + S::kRows * D + rl) - base);
+                    ll = fmaf(f, __ldcg(p + S::kRows * D + S::kRows + rl), ll);
+                    v.x = fmaf(f, w.x, v.x);
+                    v.y = fmaf(f, w.y, v.y);
+                    v.z = fmaf(f, w.z, v.z);
+                    v.w = fmaf(f, w.w, v.w);
+                }
+                finish(row0 + rl, d4, v, mm, ll);
+            }
+        }
     }
+    fence_proxy_async_shared();
+    __syncthreads();  // the rings are free for the next segment's copies
+    }  // segments
 }
 
 // weights[b][h][j] += sum over rows of exp(s - lse), from the scores that the
@@ -700,7 +820,7 @@ __global__ void __launch_bounds__(256) attn_step_weights_kernel(KvView c, KvRows
         if (a.window > 0 && j <= pos - a.window && j >= a.sinks) break;
         for (int x = 0; x < group; ++x) {
             const float s = __ldcs(stash + static_cast<int64_t>(i * group + x) * plan.pad_len);
-            acc += exp2f(s - __ldg(lse + static_cast<int64_t>(first + i) * a.heads + h * group + x));
+            acc += exp2_approx(s - __ldg(lse + static_cast<int64_t>(first + i) * a.heads + h * group + x));
         }
     }
     float* w = a.weights + (static_cast<int64_t>(b) * c.heads + h) * a.weights_stride + j;
@@ -710,37 +830,21 @@ __global__ void __launch_bounds__(256) attn_step_weights_kernel(KvView c, KvRows
 // Rows of a CTA: 4 where that is all there are, else 8.
 int row_tiles(int rows) { return rows <= 4 ? 1 : 2; }
 
-StepPlan make_plan(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, int window, int sinks, bool weights) {
+StepPlan make_plan(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {
     StepPlan p = {};
+    p.k1024 = 0x64006400u;
     const int64_t rows = max_q * (heads / c.heads);
     const int per = 4 * row_tiles(static_cast<int>(rows));
     p.groups = static_cast<int>((rows + per - 1) / per);
-    int64_t tiles = (c.max_len + kTile - 1) / kTile;
-    if (window > 0)
-        tiles = std::min<int64_t>(tiles, (sinks + kTile - 1) / kTile + (window + max_q + kTile - 1) / kTile + 1);
-    tiles = std::max<int64_t>(tiles, 1);
-    // Ranges long enough that their ends cost little, and enough of them to
-    // fill the SMs several times over when sequences differ in length.
-    const int64_t pairs = static_cast<int64_t>(c.n_seqs) * c.heads * p.groups;
-    const int64_t want = std::max<int64_t>(1, kTargetCtas / std::max<int64_t>(1, pairs));
-    int64_t per_cta = (tiles + want - 1) / want;
-    per_cta = (per_cta + kWarps - 1) / kWarps * kWarps;
-    p.tiles_per_cta = static_cast<int>(per_cta);
-    p.splits = static_cast<int>((tiles + per_cta - 1) / per_cta);
-    // Room for the partial sums of the most ranges that any window gives.
-    const int64_t most = std::min<int64_t>(want, (c.max_len + kTile * kWarps - 1) / (kTile * kWarps));
     auto take = [&](int64_t bytes) {
         const int64_t at = p.bytes;
         p.bytes += (bytes + 255) / 256 * 256;
         return at;
     };
-    if (most > 1) {
-        take(kCtrBytes);
-        p.part_off = take(pairs * most * per * (c.dim + 2) * 4);
-    }
+    take(kCtrBytes);
+    p.part_off = take(static_cast<int64_t>(kMaxCtas) * 2 * per * (c.dim + 2) * 4);
     if (weights) {
         p.pad_len = static_cast<int>((c.max_len + kTile - 1) / kTile * kTile);
-        if (most <= 1) take(kCtrBytes);
         p.lse_off = take(n_tokens * heads * 4);
         p.stash_off = take(static_cast<int64_t>(c.n_seqs) * c.heads * rows * p.pad_len * 4);
     }
@@ -754,8 +858,10 @@ cudaError_t launch_step(const KvView& c, const KvRows& r, const AttnCall& a, con
     cudaError_t err = once.set(attn_step_kernel<D, NT, T>, S::kSmem);
     if (err != cudaSuccess) return err;
     note_launch();
-    err = launch_pdl(attn_step_kernel<D, NT, T>, dim3(p.splits * p.groups, c.heads, c.n_seqs),
-                                 dim3(kThreads), S::kSmem, stream, c, r, a, p);
+    // At most this many tiles (a window or shorter sequences make fewer).
+    const int64_t tiles = std::max<int64_t>(1, (c.max_len + kTile - 1) / kTile) * c.n_seqs * c.heads * p.groups;
+    const int grid = static_cast<int>(std::min<int64_t>(kMaxCtas / 3 * (NT == 1 ? 3 : 2), (tiles + kWarps - 1) / kWarps));
+    err = launch_pdl(attn_step_kernel<D, NT, T>, dim3(grid), dim3(kThreads), S::kSmem, stream, c, r, a, p);
     if (err != cudaSuccess || !a.weights || c.max_len == 0) return err;
     note_launch();
     return launch_pdl(attn_step_weights_kernel, dim3(static_cast<unsigned>((c.max_len + 255) / 256), c.heads, c.n_seqs),
@@ -764,7 +870,7 @@ cudaError_t launch_step(const KvView& c, const KvRows& r, const AttnCall& a, con
 
 template <int D, typename T>
 cudaError_t launch_step(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
-    const StepPlan p = make_plan(c, a.heads, r.n_tokens, r.max_q, a.window, a.sinks, a.weights != nullptr);
+    const StepPlan p = make_plan(c, a.heads, r.n_tokens, r.max_q, a.weights != nullptr);
     return row_tiles(r.max_q * (a.heads / c.heads)) == 1 ? launch_step<D, 1, T>(c, r, a, p, stream)
                                                          : launch_step<D, 2, T>(c, r, a, p, stream);
 }
@@ -776,7 +882,7 @@ bool attn_step_takes(const KvView& c, int heads, int64_t max_q) {
 }
 
 int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {
-    return make_plan(c, heads, n_tokens, max_q, 0, 0, weights).bytes;
+    return make_plan(c, heads, n_tokens, max_q, weights).bytes;
 }
 
 cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
