@@ -43,14 +43,15 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;  // tokens of a warp's tile
-constexpr int kStages = 2;
+constexpr int kStages = 2;  // tiles in a warp's ring
+constexpr int kCtasPerSm = 3;
 constexpr float kTiny = 0x1p-23f, kTinyLog = -23.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The grid: as many CTAs as the GPU holds at once (three per SM), each with an
 // equal share of all tiles.
-constexpr int kMaxCtas = 152 * 3;
+constexpr int kMaxCtas = 152 * kCtasPerSm;
 
 struct StepPlan {
     int groups;   // row groups
@@ -98,11 +99,19 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t r[4]) 
 }
 __device__ __forceinline__ void mma_f16(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_first(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // lo in bits 0..15
@@ -209,7 +218,7 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* warp_sums, int64
 }
 
 template <int D, int NT, typename T>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
     attn_step_kernel(KvView c, KvRows r, AttnCall a, StepPlan plan) {
     using S = StepShape<D, NT>;
     constexpr int NB = S::kBlocks;
@@ -227,21 +236,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     grid_launch_dependents();
     grid_dependency_wait();
 
-    // All tiles of the call in one order (sequence, kv head, row group, tile):
-    // CTA x takes tiles x per .. (x + 1) per - 1 of it.
+    // How the tiles go to CTAs.  Where lists are few or short, every list is cut
+    // into ranges of `per` tiles and every range has a CTA; else the lists lie
+    // end to end and CTA x takes tiles x per .. (x + 1) per - 1 of them all.
     const int64_t lists = static_cast<int64_t>(c.heads) * plan.groups;  // tile lists per sequence
-    int64_t total = 0;
-    for (int b0 = 0; b0 < c.n_seqs; b0 += kThreads) {
-        int f, n, L;
-        const int bb = b0 + threadIdx.x;
-        int64_t all;
-        cta_scan(bb < c.n_seqs ? seq_tiles(c, r, a, bb, &f, &n, &L).count * lists : 0, scan, &all);
-        total += all;
-    }
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    auto sum_over = [&](auto&& of) {  // sum over the sequences of of(tiles of it) * lists
+        int64_t total = 0;
+        for (int b0 = 0; b0 < c.n_seqs; b0 += kThreads) {
+            int f, n, L;
+            const int bb = b0 + threadIdx.x;
+            int64_t all;
+            cta_scan(bb < c.n_seqs ? of(seq_tiles(c, r, a, bb, &f, &n, &L).count) * lists : 0, scan, &all);
+            total += all;
+        }
+        return total;
+    };
+    const int64_t grid = gridDim.x;
+    int64_t total = sum_over([](int n) -> int64_t { return n; });
+    int64_t per = (total + grid - 1) / grid;
     per = max(static_cast<int64_t>(kWarps), (per + kWarps - 1) / kWarps * kWarps);
-    int64_t tile_at = per * blockIdx.x;
-    const int64_t tile_stop = min(total, tile_at + per);
+    bool ranges = false;
+    for (int64_t p = per; p <= max(per + per / 4, static_cast<int64_t>(2 * kWarps)); p += kWarps) {
+        const int64_t n = sum_over([p](int n) -> int64_t { return (n + p - 1) / p; });
+        if (n <= grid) {
+            ranges = true;
+            per = p;
+            total = n;  // of ranges from here on
+            break;
+        }
+    }
+    int64_t tile_at = ranges ? blockIdx.x : per * blockIdx.x;
+    const int64_t tile_stop = ranges ? min(total, tile_at + 1) : min(total, tile_at + per);
     if (tile_at >= tile_stop) return;
     {
         int64_t seen = 0;
@@ -249,7 +274,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             int f, n, L;
             const int bb = b0 + threadIdx.x;
             int64_t all;
-            const int64_t mine = bb < c.n_seqs ? seq_tiles(c, r, a, bb, &f, &n, &L).count * lists : 0;
+            int64_t mine = bb < c.n_seqs ? seq_tiles(c, r, a, bb, &f, &n, &L).count : 0;
+            mine = (ranges ? (mine + per - 1) / per : mine) * lists;
             const int64_t off = seen + cta_scan(mine, scan, &all);
             if (off <= tile_at && tile_at < off + mine) {
                 s_seq = bb;
@@ -261,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         __syncthreads();
     }
     int b = s_seq;
-    int64_t seq_off = s_seq_off;  // of sequence b's first tile
+    int64_t seq_off = s_seq_off;  // of sequence b's first tile (or range)
     int first, count, L;
     TileList tiles = seq_tiles(c, r, a, b, &first, &count, &L);
     const int group = a.heads / c.heads;
@@ -269,17 +295,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     bool ok = true;
 
     while (tile_at < tile_stop) {
-    while (tile_at >= seq_off + tiles.count * lists) {  // on to the next sequence with rows
-        seq_off += tiles.count * lists;
-        tiles = seq_tiles(c, r, a, ++b, &first, &count, &L);
+    // This segment: tiles seg_begin .. tile_end - 1 of a list, one of n_parts of it.
+    int list, seg_begin, tile_end, n_parts;
+    int64_t c0;     // the CTA that has the list's first tiles
+    bool first_in;  // ... as its first segment
+    bool at_start = true;
+    if (ranges) {
+        n_parts = static_cast<int>((tiles.count + per - 1) / per);
+        const int64_t x = tile_at - seq_off;
+        list = static_cast<int>(x / n_parts);
+        const int part = static_cast<int>(x % n_parts);
+        c0 = tile_at - part;
+        first_in = true;
+        seg_begin = static_cast<int>(part * per);
+        tile_end = static_cast<int>(min(seg_begin + per, static_cast<int64_t>(tiles.count)));
+        ++tile_at;
+    } else {
+        while (tile_at >= seq_off + tiles.count * lists) {  // on to the next sequence with rows
+            seq_off += tiles.count * lists;
+            tiles = seq_tiles(c, r, a, ++b, &first, &count, &L);
+        }
+        list = static_cast<int>((tile_at - seq_off) / tiles.count);
+        const int64_t list_off = seq_off + static_cast<int64_t>(list) * tiles.count;
+        seg_begin = static_cast<int>(tile_at - list_off);
+        tile_end = static_cast<int>(min(tile_stop - list_off, static_cast<int64_t>(tiles.count)));
+        at_start = tile_at == per * blockIdx.x;
+        c0 = list_off / per;
+        first_in = list_off == c0 * per;
+        n_parts = static_cast<int>((list_off + tiles.count - 1) / per - c0) + 1;
+        tile_at = list_off + tile_end;
     }
-    const int list = static_cast<int>((tile_at - seq_off) / tiles.count);
-    const int64_t list_off = seq_off + static_cast<int64_t>(list) * tiles.count;
     const int h = list / plan.groups, rg = list % plan.groups;
-    const int seg_begin = static_cast<int>(tile_at - list_off);
-    const int tile_end = static_cast<int>(min(tile_stop - list_off, static_cast<int64_t>(tiles.count)));
-    const bool at_range_start = tile_at == per * blockIdx.x;
-    tile_at = list_off + tile_end;
 
     const int n_rows = count * group;  // rows of this (sequence, kv head): token-major, then query head
     const int row0 = rg * S::kRows;
@@ -288,6 +334,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     const int pos_lo = base_pos + row0 / group;
     const int pos_hi = base_pos + min(n_rows - 1, row0 + S::kRows - 1) / group;
     const int seen_len = max(0, min(L, pos_hi + 1));
+
+    uint8_t* my_ring = ring + warp * S::kRing;
+    // Eight lanes copy a tile: keys' cells 0..3, then values'.  Where a page
+    // holds a tile, one copy takes all four cells.  Lanes 8 u .. 8 u + 7 look
+    // up the pages of this warp's tile 4 x + u, four tiles at a time and four
+    // ahead.
+    const bool whole = c.page_shift >= 6;
+    const int tile_first = seg_begin + warp;
+    const int my_tiles = ok && tile_first < tile_end ? (tile_end - tile_first + kWarps - 1) / kWarps : 0;
+    auto look_up = [&](int x) -> int64_t {  // for this warp's tiles 4 x .. 4 x + 3
+        const int i = tile_first + (4 * x + (lane >> 3)) * kWarps;
+        if (i >= tile_end) return -1;
+        const int p = tiles.at(i) * kTile + (lane & 3) * 16;
+        if (p >= seen_len || (whole && (lane & 3))) return -1;
+        return kv_cell(c, b, h, p, &g_attn_step_error);
+    };
+    int64_t off4 = look_up(0), off4_next = look_up(1);
+    auto issue = [&](int x, int stage) {  // this warp's tile x, looked up
+        const int left = seen_len - tiles.at(tile_first + x * kWarps) * kTile;
+        const bool mine = (lane >> 3) == (x & 3) && off4 >= 0;
+        const int cells = whole ? min(4, (left + 15) >> 4) : 1;
+        const uint32_t bytes = static_cast<uint32_t>(cells * cell_bytes(D));
+        const uint32_t copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(&bars[warp][stage], copies * bytes);
+        __syncwarp();
+        if (mine) {
+            uint8_t* dst = my_ring + stage * 2 * S::kHalf + ((lane >> 2) & 1) * S::kHalf + (lane & 3) * cell_bytes(D);
+            bulk_load_1d(dst, ((lane & 4) ? c.v : c.k) + off4, bytes, &bars[warp][stage]);
+        }
+    };
+#pragma unroll
+    for (int x = 0; x < kStages; ++x)
+        if (x < my_tiles) issue(x, (n + x) % kStages);
 
     // This thread's query row in score and output accumulators is 4 j + t; in
     // the operands it feeds it is 4 j + g / 2, piece g % 2.
@@ -339,34 +418,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         pos[j] = mine < n_rows ? base_pos + mine / group : -1;
     }
 
-    uint8_t* my_ring = ring + warp * S::kRing;
-    // Eight lanes copy a tile: keys' cells 0..3, then values'.  Where a page
-    // holds a tile, one copy takes all four cells.  Lanes 8 u .. 8 u + 7 look
-    // up the pages of this warp's tile 4 x + u, four tiles at a time.
-    const bool whole = c.page_shift >= 6;
-    const int tile_first = seg_begin + warp;
-    auto look_up = [&](int x) -> int64_t {  // for this warp's tiles 4 x .. 4 x + 3
-        const int i = tile_first + (4 * x + (lane >> 3)) * kWarps;
-        if (i >= tile_end) return -1;
-        const int p = tiles.at(i) * kTile + (lane & 3) * 16;
-        if (p >= seen_len || (whole && (lane & 3))) return -1;
-        return kv_cell(c, b, h, p, &g_attn_step_error);
-    };
-    int64_t off4 = look_up(0), off4_next = look_up(1);
-    auto issue = [&](int x, int stage) {  // this warp's tile x, looked up
-        const int left = seen_len - tiles.at(tile_first + x * kWarps) * kTile;
-        const bool mine = (lane >> 3) == (x & 3) && off4 >= 0;
-        const int cells = whole ? min(4, (left + 15) >> 4) : 1;
-        const uint32_t bytes = static_cast<uint32_t>(cells * cell_bytes(D));
-        const uint32_t copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-        if (lane == 0) mbar_arrive_expect_tx(&bars[warp][stage], copies * bytes);
-        __syncwarp();
-        if (mine) {
-            uint8_t* dst = my_ring + stage * 2 * S::kHalf + ((lane >> 2) & 1) * S::kHalf + (lane & 3) * cell_bytes(D);
-            bulk_load_1d(dst, ((lane & 4) ? c.v : c.k) + off4, bytes, &bars[warp][stage]);
-        }
-    };
-
     float m[NT], l[NT];
     float o[NT][NB][2][4];  // [low, high nibbles][accumulator]
 #pragma unroll
@@ -381,20 +432,123 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     int v_up = 14;  // p is scaled by 2^v_up
     const uint32_t k1024 = plan.k1024;
 
-    const int my_tiles = ok && tile_first < tile_end ? (tile_end - tile_first + kWarps - 1) / kWarps : 0;
+    // Scores of a tile, to base 2: s[cell][j][0] of token 16 cell + g, [1]: 8 further.
+    auto score_cell = [&](const uint8_t* kt, int cell, float (&s)[4][NT][2]) {
+        const uint8_t* cp = kt + cell * cell_bytes(D);
+        uint32_t d0[NB / 2], d1[NB / 2];
+        load_words<NB / 2>(cp + cell_scales(D) + g * 2 * NB, d0);
+        load_words<NB / 2>(cp + cell_scales(D) + (g + 8) * 2 * NB, d1);
 #pragma unroll
-    for (int x = 0; x < kStages; ++x)
-        if (x < my_tiles) issue(x, (n + x) % kStages);
+        for (int j = 0; j < NT; ++j) s[cell][j][0] = s[cell][j][1] = 0.f;
+#pragma unroll
+        for (int k2 = 0; k2 < NB; k2 += 2) {
+            uint32_t w[4];
+            ldmatrix_x4(smem_addr(cp) + k2 * 256 + lane * 16, w);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = k2 + u;
+                const uint32_t w0 = w[2 * u], w1 = w[2 * u + 1];
+                const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
+                const uint32_t l0 = minus8_low(w0, k1024), l1 = minus8_low(w1, k1024), l2 = minus8_low(y0, k1024),
+                               l3 = minus8_low(y1, k1024);
+                const uint32_t h0 = minus8_high(w0, k1024), h1 = minus8_high(w1, k1024), h2 = minus8_high(y0, k1024),
+                               h3 = minus8_high(y1, k1024);
+                const float2 dd0 = __half22float2(as_half2(d0[k2 / 2]));
+                const float2 dd1 = __half22float2(as_half2(d1[k2 / 2]));
+                const float e0 = u ? dd0.y : dd0.x, e1 = u ? dd1.y : dd1.x;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float acc[4];
+                    mma_f16_first(acc, l0, l1, l2, l3, bq[j][k][0], bq[j][k][1]);
+                    mma_f16(acc, h0, h1, h2, h3, bq[j][k][2], bq[j][k][3]);
+                    s[cell][j][0] = fmaf(e0, acc[0] + acc[1], s[cell][j][0]);
+                    s[cell][j][1] = fmaf(e1, acc[2] + acc[3], s[cell][j][1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            s[cell][j][0] *= to_log2[j];
+            s[cell][j][1] *= to_log2[j];
+        }
+    };
+    // o += sum over the cell's tokens of 2^v_up p d (n - 8); s holds p.
+    auto output_cell = [&](const uint8_t* vt, int cell, const float (&s)[4][NT][2], float up) {
+        const uint8_t* cp = vt + cell * cell_bytes(D);
+        // p of tokens 2 t, 2 t + 1 and 8 further, of row 4 j + g / 2: f16 value
+        // and remainder, fetched from the lanes that hold them.
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float p0 = s[cell][j][0] * up, p1 = s[cell][j][1] * up;
+            const uint32_t hw = pack_f16(p0, p1);
+            const float2 hf = __half22float2(as_half2(hw));
+            const uint32_t lw = pack_f16(p0 - hf.x, p1 - hf.y);
+            const uint32_t x0 = __byte_perm(hw, lw, 0x5410), x1 = __byte_perm(hw, lw, 0x7632);
+            const int from = 8 * t + (g >> 1);
+            const uint32_t a0 = __shfl_sync(0xFFFFFFFFu, x0, from), a1 = __shfl_sync(0xFFFFFFFFu, x0, from + 4);
+            const uint32_t c0 = __shfl_sync(0xFFFFFFFFu, x1, from), c1 = __shfl_sync(0xFFFFFFFFu, x1, from + 4);
+            ph[j][0] = __byte_perm(a0, a1, 0x5410);
+            pl[j][0] = __byte_perm(a0, a1, 0x7632);
+            ph[j][1] = __byte_perm(c0, c1, 0x5410);
+            pl[j][1] = __byte_perm(c0, c1, 0x7632);
+        }
+        // Scales of tokens 2 t, 2 t + 1 and 8 further.
+        uint32_t dw[2][NB];
+        load_words<NB>(cp + cell_scales(D) + 2 * t * 2 * NB, dw[0]);
+        load_words<NB>(cp + cell_scales(D) + (2 * t + 8) * 2 * NB, dw[1]);
+#pragma unroll
+        for (int k2 = 0; k2 < NB; k2 += 2) {
+            uint32_t w[4];
+            ldmatrix_x4_trans(smem_addr(cp) + k2 * 256 + lane * 16, w);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = k2 + u;
+                const uint32_t w0 = w[2 * u], w1 = w[2 * u + 1];
+                const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
+                const uint32_t sel = u ? 0x7632u : 0x5410u;
+                const __half2 da = as_half2(__byte_perm(dw[0][k2 / 2], dw[0][NB / 2 + k2 / 2], sel));
+                const __half2 db = as_half2(__byte_perm(dw[1][k2 / 2], dw[1][NB / 2 + k2 / 2], sel));
+                const uint32_t l0 = minus8_low(w0, k1024), l1 = minus8_low(y0, k1024), l2 = minus8_low(w1, k1024),
+                               l3 = minus8_low(y1, k1024);
+                const uint32_t h0 = minus8_high(w0, k1024), h1 = minus8_high(y0, k1024), h2 = minus8_high(w1, k1024),
+                               h3 = minus8_high(y1, k1024);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const __half2 pa = as_half2(ph[j][0]), pb = as_half2(ph[j][1]);
+                    const __half2 xa = __hmul2(pa, da), xb = __hmul2(pb, db);
+                    const __half2 ra = __hfma2(as_half2(pl[j][0]), da, __hfma2(pa, da, __hneg2(xa)));
+                    const __half2 rb = __hfma2(as_half2(pl[j][1]), db, __hfma2(pb, db, __hneg2(xb)));
+                    const uint32_t b0 = as_word((g & 1) ? ra : xa), b1 = as_word((g & 1) ? rb : xb);
+                    mma_f16(o[j][k][0], l0, l1, l2, l3, b0, b1);
+                    mma_f16(o[j][k][1], h0, h1, h2, h3, b0, b1);
+                }
+            }
+        }
+    };
+    auto scale_o = [&](float f) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[j][k][0][e] *= f;
+                    o[j][k][1][e] *= f;
+                }
+    };
 
+    float s[4][NT][2];
     int x = 0;
     for (; x < my_tiles; ++x, ++n) {
         const int stage = n % kStages;
-        const int i = tile_first + x * kWarps;
         const uint8_t* kt = my_ring + stage * 2 * S::kHalf;
         uint8_t* vt = my_ring + stage * 2 * S::kHalf + S::kHalf;
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bars[warp][stage], (n / kStages) & 1, &g_attn_step_error));
         if (!ok) break;
-        const int key0 = tiles.at(i) * kTile;
+        const int key0 = tiles.at(tile_first + x * kWarps) * kTile;
+#pragma unroll
+        for (int cell = 0; cell < 4; ++cell) score_cell(kt, cell, s);
 
         // Scales of the values: where none reaches 2 (a bit of the exponent)
         // and no token is past the end, nothing is to be done.
@@ -434,85 +588,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                 // p 2^v_up d < 2^15 for d < 2^(exponent + 1).
                 const int need = min(14, 14 - (static_cast<int>(top >> 10) - 15));
                 if (need < v_up) {
-                    const float down = pow2(need - v_up);
+                    scale_o(pow2(need - v_up));
                     v_up = need;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int k = 0; k < NB; ++k)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                o[j][k][0][e] *= down;
-                                o[j][k][1][e] *= down;
-                            }
                 }
             }
         }
 
-        // Scores of the tile: s[cell][j][0]: token 16 cell + g, [1]: + 8.
-        float s[4][NT][2];
-#pragma unroll
-        for (int cell = 0; cell < 4; ++cell) {
-            const uint8_t* cp = kt + cell * cell_bytes(D);
-            uint32_t d0[NB / 2], d1[NB / 2];
-            load_words<NB / 2>(cp + cell_scales(D) + g * 2 * NB, d0);
-            load_words<NB / 2>(cp + cell_scales(D) + (g + 8) * 2 * NB, d1);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) s[cell][j][0] = s[cell][j][1] = 0.f;
-#pragma unroll
-            for (int k2 = 0; k2 < NB; k2 += 2) {
-                uint32_t w[4];
-                ldmatrix_x4(smem_addr(cp) + k2 * 256 + lane * 16, w);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int k = k2 + u;
-                    const uint32_t w0 = w[2 * u], w1 = w[2 * u + 1];
-                    const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
-                    const uint32_t l0 = minus8_low(w0, k1024), l1 = minus8_low(w1, k1024), l2 = minus8_low(y0, k1024), l3 = minus8_low(y1, k1024);
-                    const uint32_t h0 = minus8_high(w0, k1024), h1 = minus8_high(w1, k1024), h2 = minus8_high(y0, k1024),
-                                   h3 = minus8_high(y1, k1024);
-                    const float2 dd0 = __half22float2(as_half2(d0[k2 / 2]));
-                    const float2 dd1 = __half22float2(as_half2(d1[k2 / 2]));
-                    const float e0 = u ? dd0.y : dd0.x, e1 = u ? dd1.y : dd1.x;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_f16(acc, l0, l1, l2, l3, bq[j][k][0], bq[j][k][1]);
-                        mma_f16(acc, h0, h1, h2, h3, bq[j][k][2], bq[j][k][3]);
-                        s[cell][j][0] = fmaf(e0, acc[0] + acc[1], s[cell][j][0]);
-                        s[cell][j][1] = fmaf(e1, acc[2] + acc[3], s[cell][j][1]);
-                    }
-                }
-            }
-        }
-
-        // To base 2, masked where some row does not see some token.
+        // What a row does not see, and tokens whose values are not finite.
         const bool all_seen = key0 + kTile <= min(pos_lo + 1, L) && !(bad0 | bad1) &&
                               (a.window == 0 || key0 > pos_hi - a.window || key0 + kTile <= a.sinks);
-        bool more = false;  // some token's p is below kTiny, but not 0
+        if (!all_seen) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float mx = -INFINITY, mn = INFINITY;
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int cell = 0; cell < 4; ++cell) {
+                for (int cell = 0; cell < 4; ++cell)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = s[cell][j][e] * to_log2[j];
-                    float y = x;
-                    if (!all_seen) {
+                    for (int e = 0; e < 2; ++e) {
                         const int in_tile = 16 * cell + 8 * e + g;
                         const int key = key0 + in_tile;
                         const bool sees = key <= pos[j] && key < L &&
                                           (a.window == 0 || key > pos[j] - a.window || key < a.sinks);
-                        if (((in_tile < 32 ? bad0 : bad1) >> (in_tile & 31)) & 1u) x = NAN;
-                        if (!sees) x = -INFINITY, y = INFINITY;
+                        if (((in_tile < 32 ? bad0 : bad1) >> (in_tile & 31)) & 1u) s[cell][j][e] = NAN;
+                        if (!sees) s[cell][j][e] = -INFINITY;
                     }
-                    s[cell][j][e] = x;
-                    mx = fmaxf(mx, x);
-                    mn = fminf(mn, y);
-                }
-            }
-            if (plan.pad_len) {
+        }
+        if (plan.pad_len) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
                 const int rr = row0 + 4 * j + t;
                 if (rr < n_rows) {
                     float* st = reinterpret_cast<float*>(a.ws + plan.stash_off) +
@@ -524,8 +626,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     }
                 }
             }
+        }
+        bool small = false;  // some token's p is below kTiny, but not 0
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+        for (int j = 0; j < NT; ++j) {
+            float mx = -INFINITY, mn = INFINITY;
+#pragma unroll
+            for (int cell = 0; cell < 4; ++cell)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx = fmaxf(mx, s[cell][j][e]);
+                    mn = fminf(mn, s[cell][j][e]);
+                }
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, y));
             const float m2 = fmaxf(m[j], mx);
             const float base = m2 == -INFINITY ? 0.f : m2;
             if (mx > m[j]) {
@@ -540,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     }
             }
             m[j] = m2;
-            more |= mn - base < kTinyLog;
+            small |= mn - base < kTinyLog;  // (masked tokens too: their p is 0 below)
 #pragma unroll
             for (int cell = 0; cell < 4; ++cell) {
                 s[cell][j][0] = exp2_approx(s[cell][j][0] - base);
@@ -548,116 +662,71 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                 l[j] += s[cell][j][0] + s[cell][j][1];
             }
         }
-
-        // Output of the tile.  An f16 pair holds p to 2^-17 of itself down to
-        // 2^-23 of the running maximum.  Tokens below that (rare: 16 in natural
-        // logarithm) go in a pass of their own with everything lifted by 2^23,
-        // so a dim where the large ones happen to be 0 keeps its precision;
-        // below 2^-92 they count as 0.
         const float up = pow2(v_up);
-        float lift = 1.f;
-        for (;;) {
+        small = __any_sync(0xFFFFFFFFu, small);
+        if (small) {
+            // An f16 pair holds p to 2^-17 of itself down to 2^-23 of the running
+            // maximum.  Tokens below that (rare: 16 in natural logarithm) go in
+            // passes of their own with everything lifted by 2^23, so a dim where
+            // the large ones happen to be 0 keeps its precision; below 2^-92
+            // they count as 0.
             float rest[4][NT][2];
-            more = __any_sync(0xFFFFFFFFu, more) && lift < 0x1p69f;
-            if (more) {
+            float lift = 1.f;
+#pragma unroll 1
+            for (;;) {
+                bool more = false;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int cell = 0; cell < 4; ++cell)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const bool small = s[cell][j][e] < kTiny;  // (false for NaN)
-                            rest[cell][j][e] = small ? s[cell][j][e] * (1.f / kTiny) : 0.f;
-                            if (small) s[cell][j][e] = 0.f;
+                            const float p = s[cell][j][e];
+                            const bool below = p < kTiny;  // (false for NaN)
+                            more |= below && p > 0.f;
+                            rest[cell][j][e] = below ? p * (1.f / kTiny) : 0.f;
+                            if (below) s[cell][j][e] = 0.f;
                         }
-            }
+                more = __any_sync(0xFFFFFFFFu, more) && lift < 0x1p69f;
+                if (!more) break;
+                // The tokens at hand now, the others lifted next.
+#pragma unroll 1
+                for (int cell = 0; cell < 4; ++cell) {
+                    float one[4][NT][2];
 #pragma unroll
-            for (int cell = 0; cell < 4; ++cell) {
-                const uint8_t* cp = vt + cell * cell_bytes(D);
-                // p of tokens 2 t, 2 t + 1 and 8 further, of row 4 j + g / 2: f16
-                // value and remainder, fetched from the lanes that hold them.
-                uint32_t ph[NT][2], pl[NT][2];
+                    for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const float p0 = s[cell][j][0] * up, p1 = s[cell][j][1] * up;
-                    const uint32_t hw = pack_f16(p0, p1);
-                    const float2 hf = __half22float2(as_half2(hw));
-                    const uint32_t lw = pack_f16(p0 - hf.x, p1 - hf.y);
-                    const uint32_t x0 = __byte_perm(hw, lw, 0x5410), x1 = __byte_perm(hw, lw, 0x7632);
-                    const int from = 8 * t + (g >> 1);
-                    const uint32_t a0 = __shfl_sync(0xFFFFFFFFu, x0, from), a1 = __shfl_sync(0xFFFFFFFFu, x0, from + 4);
-                    const uint32_t c0 = __shfl_sync(0xFFFFFFFFu, x1, from), c1 = __shfl_sync(0xFFFFFFFFu, x1, from + 4);
-                    ph[j][0] = __byte_perm(a0, a1, 0x5410);
-                    pl[j][0] = __byte_perm(a0, a1, 0x7632);
-                    ph[j][1] = __byte_perm(c0, c1, 0x5410);
-                    pl[j][1] = __byte_perm(c0, c1, 0x7632);
+                        for (int e = 0; e < 2; ++e)
+                            one[0][j][e] = cell == 0 ? s[0][j][e] : cell == 1 ? s[1][j][e] : cell == 2 ? s[2][j][e] : s[3][j][e];
+                    output_cell(vt + cell * cell_bytes(D), 0, one, up);
                 }
-                // Scales of tokens 2 t, 2 t + 1 and 8 further.
-                uint32_t dw[2][NB];
-                load_words<NB>(cp + cell_scales(D) + 2 * t * 2 * NB, dw[0]);
-                load_words<NB>(cp + cell_scales(D) + (2 * t + 8) * 2 * NB, dw[1]);
+                lift *= 1.f / kTiny;
+                scale_o(1.f / kTiny);
 #pragma unroll
-                for (int k2 = 0; k2 < NB; k2 += 2) {
-                    uint32_t w[4];
-                    ldmatrix_x4_trans(smem_addr(cp) + k2 * 256 + lane * 16, w);
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int k = k2 + u;
-                        const uint32_t w0 = w[2 * u], w1 = w[2 * u + 1];
-                        const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
-                        const uint32_t sel = u ? 0x7632u : 0x5410u;
-                        const __half2 da = as_half2(__byte_perm(dw[0][k2 / 2], dw[0][NB / 2 + k2 / 2], sel));
-                        const __half2 db = as_half2(__byte_perm(dw[1][k2 / 2], dw[1][NB / 2 + k2 / 2], sel));
-                        const uint32_t l0 = minus8_low(w0, k1024), l1 = minus8_low(y0, k1024), l2 = minus8_low(w1, k1024), l3 = minus8_low(y1, k1024);
-                        const uint32_t h0 = minus8_high(w0, k1024), h1 = minus8_high(y0, k1024), h2 = minus8_high(w1, k1024),
-                                       h3 = minus8_high(y1, k1024);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const __half2 pa = as_half2(ph[j][0]), pb = as_half2(ph[j][1]);
-                            const __half2 xa = __hmul2(pa, da), xb = __hmul2(pb, db);
-                            const __half2 ra = __hfma2(as_half2(pl[j][0]), da, __hfma2(pa, da, __hneg2(xa)));
-                            const __half2 rb = __hfma2(as_half2(pl[j][1]), db, __hfma2(pb, db, __hneg2(xb)));
-                            const uint32_t b0 = as_word((g & 1) ? ra : xa), b1 = as_word((g & 1) ? rb : xb);
-                            mma_f16(o[j][k][0], l0, l1, l2, l3, b0, b1);
-                            mma_f16(o[j][k][1], h0, h1, h2, h3, b0, b1);
-                        }
-                    }
-                }
+                    for (int cell = 0; cell < 4; ++cell) s[cell][j][0] = rest[cell][j][0], s[cell][j][1] = rest[cell][j][1];
             }
-            if (!more) break;
-            lift *= 1.f / kTiny;
-            more = false;
+            if (lift != 1.f) {  // the last pass, below, adds at the lifted scale: taken here instead
+#pragma unroll 1
+                for (int cell = 0; cell < 4; ++cell) {
+                    float one[4][NT][2];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+                    for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int cell = 0; cell < 4; ++cell)
+                        for (int e = 0; e < 2; ++e)
+                            one[0][j][e] = cell == 0 ? s[0][j][e] : cell == 1 ? s[1][j][e] : cell == 2 ? s[2][j][e] : s[3][j][e];
+                    output_cell(vt + cell * cell_bytes(D), 0, one, up);
+                }
+                scale_o(1.f / lift);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        s[cell][j][e] = rest[cell][j][e];
-                        more |= s[cell][j][e] < kTiny && s[cell][j][e] > 0.f;
-                    }
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int k = 0; k < NB; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[j][k][0][e] *= 1.f / kTiny;
-                        o[j][k][1][e] *= 1.f / kTiny;
-                    }
+                    for (int cell = 0; cell < 4; ++cell) s[cell][j][0] = s[cell][j][1] = 0.f;
             }
         }
-        if (lift != 1.f) {
-            const float back = 1.f / lift;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int k = 0; k < NB; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[j][k][0][e] *= back;
-                        o[j][k][1][e] *= back;
-                    }
-        }
-
+        for (int cell = 0; cell < 4; ++cell) output_cell(vt, cell, s, up);
         __syncwarp();
         const int nx = x + kStages;
         if (nx < my_tiles) {
@@ -669,8 +738,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             issue(nx, stage);
         }
     }
-    if (!ok && x + 1 < my_tiles) {  // a copy that did not land: wait for the other stage's too
-        mbar_wait_bounded(&bars[warp][(n + 1) % kStages], ((n + 1) / kStages) & 1, &g_attn_step_error);
+    if (!ok) {  // a copy that did not land: wait for the other stage's too
+        if (x + 1 < my_tiles)
+            mbar_wait_bounded(&bars[warp][(n + 1) % kStages], ((n + 1) / kStages) & 1, &g_attn_step_error);
     }
 
     // The warps' sums meet in shared memory: [row][D] sums, then maxima, then l.
@@ -712,10 +782,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     };
 
     constexpr int kPart = S::kRows * (D + 2);  // floats of one segment's sums
-    const bool alone = seg_begin == 0 && tile_end == tiles.count;  // the whole list
+    const bool alone = n_parts == 1;
     // A CTA's first segment has slot 0, its last one (if another) slot 1.
     float* parts = reinterpret_cast<float*>(a.ws + plan.part_off);
-    float* part = parts + (static_cast<int64_t>(blockIdx.x) * 2 + (at_range_start ? 0 : 1)) * kPart;
+    float* part = parts + (static_cast<int64_t>(blockIdx.x) * 2 + (at_start ? 0 : 1)) * kPart;
     for (int it = threadIdx.x; it < S::kRows * D / 4; it += kThreads) {
         const int rl = it / (D / 4), d4 = (it % (D / 4)) * 4;
         float mm = -INFINITY;
@@ -751,21 +821,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     }
     if (!alone) {
         // The last segment of a list to arrive adds all of them up, in order.
-        const int64_t c0 = list_off / per, c1 = (list_off + tiles.count - 1) / per;  // CTAs of the list
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) {
             // No two lists that are cut begin in the same CTA.
             unsigned* ctr = reinterpret_cast<unsigned*>(a.ws) + c0;
             const unsigned before = atomicAdd(ctr, 1u);
-            s_last = before == static_cast<unsigned>(c1 - c0);
+            s_last = before == static_cast<unsigned>(n_parts) - 1;
             if (s_last) *ctr = 0;  // fit for the next call
         }
         __syncthreads();
         if (s_last) {
             __threadfence();
-            const int n_parts = static_cast<int>(c1 - c0) + 1;
-            const float* p0 = parts + (c0 * 2 + (list_off == c0 * per ? 0 : 1)) * kPart;
+            const float* p0 = parts + (c0 * 2 + (first_in ? 0 : 1)) * kPart;
             auto part_of = [&](int y) { return y == 0 ? p0 : parts + (c0 + y) * 2 * kPart; };
             for (int it = threadIdx.x; it < S::kRows * D / 4; it += kThreads) {
                 const int rl = it / (D / 4), d4 = (it % (D / 4)) * 4;
@@ -858,9 +926,10 @@ cudaError_t launch_step(const KvView& c, const KvRows& r, const AttnCall& a, con
     cudaError_t err = once.set(attn_step_kernel<D, NT, T>, S::kSmem);
     if (err != cudaSuccess) return err;
     note_launch();
+    const int64_t n_lists = static_cast<int64_t>(c.n_seqs) * c.heads * p.groups;
     // At most this many tiles (a window or shorter sequences make fewer).
-    const int64_t tiles = std::max<int64_t>(1, (c.max_len + kTile - 1) / kTile) * c.n_seqs * c.heads * p.groups;
-    const int grid = static_cast<int>(std::min<int64_t>(kMaxCtas / 3 * (NT == 1 ? 3 : 2), (tiles + kWarps - 1) / kWarps));
+    const int64_t tiles = std::max<int64_t>(1, (c.max_len + kTile - 1) / kTile) * n_lists;
+    const int grid = static_cast<int>(std::min<int64_t>(152 * (NT == 1 ? kCtasPerSm : 2), std::max((tiles + kWarps - 1) / kWarps, n_lists)));
     err = launch_pdl(attn_step_kernel<D, NT, T>, dim3(grid), dim3(kThreads), S::kSmem, stream, c, r, a, p);
     if (err != cudaSuccess || !a.weights || c.max_len == 0) return err;
     note_launch();
