@@ -12,8 +12,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int64_t kLseOff = 4096;  // the workspace's first bytes are the step's counters
+// The workspace: 4 KB that are zero between calls (the step kernel's counters,
+// and last the number of rows to be done again); then such rows' list, and
+// logarithms to base 2.
+constexpr int64_t kRedoCount = 4080, kRedoOff = 4096;
 constexpr float kLn2 = 0.6931471805599453f;
+
+int64_t lse_off(int64_t n_tokens, int heads) { return kRedoOff + (n_tokens * heads * 4 + 255) / 256 * 256; }
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -29,15 +34,13 @@ __device__ __forceinline__ float cell_value(const uint8_t* cell, int dim, int sl
     return magic_minus8(q | kMagicBits) * d;
 }
 
-// One warp per row and query head; lane l holds dims 32 i + l.  The softmax
-// runs in one pass over the tokens with a running maximum and sum, in f32.
+// One warp per row and query head (item = row * heads + head); lane l holds
+// dims 32 i + l.  The softmax runs in one pass over the tokens with a running
+// maximum and sum, in f32.
 template <int NB, typename T>
-__global__ void __launch_bounds__(kWarps * 32) attn_plain_kernel(KvView c, KvRows r, AttnCall a, float* lse) {
-    grid_launch_dependents();
-    grid_dependency_wait();
+__device__ __forceinline__ void attn_plain_row(const KvView& c, const KvRows& r, const AttnCall& a, float* lse,
+                                               int64_t item) {
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (item >= static_cast<int64_t>(r.n_tokens) * a.heads) return;
     const int row = static_cast<int>(item / a.heads), head = static_cast<int>(item % a.heads);
     const int b = kv_seq_of_row(r, c.n_seqs, row);
     if (b < 0) return;
@@ -78,7 +81,36 @@ __global__ void __launch_bounds__(kWarps * 32) attn_plain_kernel(KvView c, KvRow
     T* out = static_cast<T*>(a.out) + row * a.out_stride + static_cast<int64_t>(head) * c.dim;
 #pragma unroll
     for (int i = 0; i < NB; ++i) store1(out + 32 * i + lane, o[i] * inv);
-    if (lse && lane == 0) lse[item] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (lane == 0) {
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        if (a.lse) a.lse[item] = lse2 * kLn2;
+        if (lse) lse[item] = lse2;
+    }
+}
+
+template <int NB, typename T>
+__global__ void __launch_bounds__(kWarps * 32) attn_plain_kernel(KvView c, KvRows r, AttnCall a, float* lse) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (item < static_cast<int64_t>(r.n_tokens) * a.heads) attn_plain_row<NB, T>(c, r, a, lse, item);
+}
+
+// The rows that the prompt kernel listed in `redo` (redo_n[0] of them, redo_n[1]
+// counts CTAs); the last CTA to finish leaves the list empty for the next call.
+template <int NB, typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+    attn_redo_kernel(KvView c, KvRows r, AttnCall a, float* lse, unsigned* redo_n, const unsigned* redo) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const unsigned n = __ldcg(redo_n);
+    for (unsigned i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < n; i += gridDim.x * kWarps)
+        attn_plain_row<NB, T>(c, r, a, lse, __ldcg(redo + i));
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(redo_n + 1, 1u) == gridDim.x - 1) redo_n[0] = redo_n[1] = 0;
+    }
 }
 
 // weights[b][h][j] += sum over the sequence's rows that see token j and the
@@ -113,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_weights_plain_kernel(KvView 
             for (int x = 0; x < NB; ++x) s = fmaf(load1(q + 32 * x + lane), k[x], s);
 #pragma unroll
             for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-            acc += exp2f(s - lse[static_cast<int64_t>(first + i) * a.heads + head] * kLog2e);
+            acc += exp2f(s - lse[static_cast<int64_t>(first + i) * a.heads + head]);
         }
     }
     if (lane == 0) {
@@ -124,11 +156,23 @@ __global__ void __launch_bounds__(kWarps * 32) attn_weights_plain_kernel(KvView 
 
 template <int NB, typename T>
 cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
-    float* lse = a.lse ? a.lse : a.weights ? reinterpret_cast<float*>(a.ws + kLseOff) : nullptr;
+    float* lse = a.weights ? reinterpret_cast<float*>(a.ws + lse_off(r.n_tokens, a.heads)) : nullptr;  // to base 2
     const int64_t items = static_cast<int64_t>(r.n_tokens) * a.heads;
-    note_launch();
-    cudaError_t err = launch_pdl(attn_plain_kernel<NB, T>, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)),
-                                 dim3(kWarps * 32), 0, stream, c, r, a, lse);
+    cudaError_t err;
+    if (attn_prompt_takes(c)) {
+        unsigned* redo_n = reinterpret_cast<unsigned*>(a.ws + kRedoCount);
+        unsigned* redo = reinterpret_cast<unsigned*>(a.ws + kRedoOff);
+        err = launch_attn_prompt(c, r, a, lse, redo_n, redo, stream);
+        if (err == cudaSuccess && a.type == KvType::kBF16) {
+            note_launch();
+            err = launch_pdl(attn_redo_kernel<NB, T>, dim3(152), dim3(kWarps * 32), 0, stream, c, r, a, lse, redo_n,
+                             redo);
+        }
+    } else {
+        note_launch();
+        err = launch_pdl(attn_plain_kernel<NB, T>, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)),
+                         dim3(kWarps * 32), 0, stream, c, r, a, lse);
+    }
     if (err != cudaSuccess || !a.weights || c.max_len == 0) return err;
     note_launch();
     return launch_pdl(attn_weights_plain_kernel<NB, T>,
@@ -146,7 +190,7 @@ cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cu
 
 int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {
     if (attn_step_takes(c, heads, max_q)) return attn_step_workspace(c, heads, n_tokens, max_q, weights);
-    return weights ? kLseOff + n_tokens * heads * 4 : 0;
+    return attn_prompt_takes(c) || weights ? lse_off(n_tokens, heads) + (weights ? n_tokens * heads * 4 : 0) : 0;
 }
 
 cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,

@@ -1,0 +1,894 @@
+// Attention of many rows over the paged Q4_0 cache (prompts and their chunks)
+// on the 5th-generation tensor cores.
+//
+// Mathematics.  Tiles of 128 query rows (token-major, then the query heads of a
+// kv head) meet tiles of 128 tokens: S = Q K^T and P V as tcgen05.mma into TMEM,
+// one pass with a running maximum and sum per row.  A query row is scaled to the
+// top of f16's range, a key tile by the power of two that takes its largest
+// scale to 2^11 .. 2^12; both are then f16 pieces.
+//   f32 rows: two pieces of Q (22 bits) and of K (exact); S takes the three
+//     products that are not 2^-22 of the first, smallest first.  P is two bf16
+//     pieces (2^-18 of itself over the whole range of f32, where f16 would lose
+//     the small ones), V exactly two bf16 pieces; all four products, smallest
+//     first, start from 0 for every token tile, and the row's sums are kept in
+//     registers: the tensor cores cut their sums off instead of rounding them,
+//     which over a long row would show (2e-6 at 300 tokens, growing).
+//   bf16 rows: one piece each (queries exact, keys, P and V to 11 bits), and the
+//     output accumulates in TMEM.  A value tile too is scaled by a power of two,
+//     which P takes on (P = exp2(s + e - maximum of s + e)), so f16's range
+//     serves any scale.  What that range loses are tokens 2^-26 below a row's
+//     maximum.  They can matter only to an output element to which all large
+//     tokens add up to about nothing: rows that have both are listed and done
+//     again by the plain kernel.
+//
+// What bounds it: f32 rows the tensor cores (7 products of 2^21 MACs per pair of
+// tiles at D = 128); bf16 rows (2 products) the tensor cores and the issue slots
+// about equally (softmax 6 instructions per score, unpacking 13 per 8 quants,
+// shared by two row tiles).
+//
+// Structure, one CTA of 16 warps per (sequence, kv head, 128 or 2 x 128 rows):
+//   a loader warp fetches raw cells with bulk copies;
+//   4 or 8 decode warps unpack them into 128-byte swizzled tiles (dims of a block
+//     in the order the nibbles unpack; Q and the output follow it);
+//   one thread issues the MMAs: S of the next tile is queued before P V of this
+//     one (f32), or two row tiles take turns (bf16), so the softmax of one
+//     always has products of another to run beside;
+//   4 warps per row tile hold a row per thread: maximum, exponentials, P back to
+//     TMEM over S (P is the A operand from there).  bf16: only when a row's
+//     maximum grows by more than 2^3 is its accumulator scaled down.
+// Code is kept short on purpose (rolled loops over 32-column chunks): unrolled,
+// the roles of the four schedulers evicted one another's instructions (805 us
+// against 449 for a prompt of 4096 f32 rows).
+// f32 rows' registers: 512 threads x 128 at launch; then 128 x 232 + 256 x 96 +
+// 128 x 56 = 61440 of those 65536.
+// Every wait is bounded; a wait that gives up sets the device error word.
+#include <algorithm>
+#include <type_traits>
+
+#include "kv_cache.cuh"
+
+namespace qm {
+
+__device__ unsigned int g_attn_prompt_error = 0;
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;  // rows of a row tile, tokens of a token tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, bool F32>
+struct Shape {
+    static constexpr int kBlocks = D / 32;
+    static constexpr int kM = F32 ? 1 : 2;            // row tiles of a CTA
+    static constexpr int kPieces = F32 ? 2 : 1;       // of Q, K, V and P
+    static constexpr int kStages = F32 ? 1 : 2;       // K tiles, V tiles
+    static constexpr int kRawSlots = 3;               // raw tiles, of keys and values in turn
+    static constexpr int kPiece = kTile * D * 2;      // bytes of one piece of a tile
+    static constexpr int kOperand = kPieces * kPiece;
+    static constexpr int kRaw = kTile / 16 * 9 * D;   // raw cells of a tile
+    static constexpr int kVScales = kTile * 2 * kBlocks;
+    static constexpr int kSlot = kRaw + kVScales;     // keys come with the scales of the values
+    static constexpr int kSoftmaxWarps = 4 * kM;
+    static constexpr int kDecodeWarps = F32 ? 8 : 4;
+    static constexpr int kSmem = kM * kOperand + 2 * kStages * kOperand + kRawSlots * kSlot + 1024;
+    static_assert(kSmem <= 232448 - 3072, "shared memory of one CTA");
+};
+
+// TMEM columns: S and P over it 0 .. 255 in two buffers (f32: tiles in turn, the
+// pieces of 32 scores' P in 16 columns each; bf16: a row tile each), then P V in
+// two buffers of 128 likewise.
+constexpr uint32_t kTmemO = 256;
+constexpr float kLazy = 3.f;      // bf16: how far (log2) a maximum may be overtaken
+constexpr float kPTop = 12.f;     // bf16: P is 2^12 at the maximum in use
+constexpr float kFarBelow = 24.f; // bf16: P this far (log2) below the maximum loses bits
+
+__device__ __forceinline__ uint64_t desc_base(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(lbo >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;  // 8 rows of 128 bytes
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;  // 128-byte swizzle
+    return d;
+}
+
+// D f32; both operands f16 (type 0) or bf16 (1); M = 128.
+constexpr uint32_t idesc(int type, int n, bool b_mn_major) {
+    return (1u << 4) | (static_cast<uint32_t>(type) << 7) | (static_cast<uint32_t>(type) << 10) |
+           (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float v[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float v[32]) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t r[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ uint32_t word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ uint32_t word(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ __nv_bfloat162 bf2_of(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+
+__device__ __forceinline__ float4 load_q4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load_q4(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store_o4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store_o4(__nv_bfloat16* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(word(__floats2bfloat162_rn(v.x, v.y)), word(__floats2bfloat162_rn(v.z, v.w)));
+}
+
+// Byte offset of 16-byte chunk `chunk` (of 8 elements; D / 8 of them) of row
+// `row` in a piece of a tile: 64-element columns of [128 rows][128 bytes], the
+// chunks of a row permuted by row % 8.
+__device__ __forceinline__ int tile_off(int row, int chunk) {
+    return (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// Token tiles that rows at positions pos_lo .. pos_hi read.
+struct TileList {
+    int n1, t2, count;
+    __device__ __forceinline__ int at(int i) const { return i < n1 ? i : t2 + (i - n1); }
+};
+__device__ __forceinline__ TileList tile_list(int seen_len, int pos_lo, int window, int sinks) {
+    const int total = (seen_len + kTile - 1) / kTile;
+    TileList t{0, 0, total};
+    if (window > 0) {
+        const int lo = max(0, pos_lo - window + 1);
+        t.n1 = min((min(sinks, lo) + kTile - 1) / kTile, total);
+        t.t2 = max(t.n1, lo / kTile);
+        t.count = t.n1 + max(0, total - t.t2);
+    }
+    return t;
+}
+
+// Keys of one block of a token: 16 quant bytes and the tile-scaled f16 d ->
+// four chunks of 8, each word's quants in the order they unpack.
+template <bool F32>
+__device__ __forceinline__ void decode_keys(uint4 q, float d, int row, int blk, uint8_t* hi, uint8_t* lo, uint32_t k1024) {
+    const __half2 dd = __float2half2_rn(d);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t y = w[k] >> 8;
+        const __half2 m1032 = half2_of(0xE408E408u), sixteenth = half2_of(0x2C002C00u), m72 = half2_of(0xD480D480u);
+        const __half2 n[4] = {__hadd2(half2_of((w[k] & 0x000F000Fu) | k1024), m1032),
+                              __hadd2(half2_of((y & 0x000F000Fu) | k1024), m1032),
+                              __hfma2(half2_of((w[k] & 0x00F000F0u) | k1024), sixteenth, m72),
+                              __hfma2(half2_of((y & 0x00F000F0u) | k1024), sixteenth, m72)};
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __half2 x = __hmul2(n[e], dd);
+            h[e] = word(x);
+            if (F32) l[e] = word(__hfma2(n[e], dd, __hneg2(x)));
+        }
+        const int off = tile_off(row, 4 * blk + k);
+        *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (F32) *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+// Values of one block of a token as bf16: d = dh + dl exactly (8 and 3 bits), so
+// (n - 8) dl is exact, one FMA rounds (n - 8) d once, and what that leaves is
+// exact again.
+__device__ __forceinline__ void decode_values(uint4 q, float d, int row, int blk, uint8_t* hi, uint8_t* lo,
+                                              uint32_t k128) {
+    const float df = __bfloat162float(__float2bfloat16_rn(d));
+    const __nv_bfloat162 dh = __float2bfloat162_rn(df), dl = __float2bfloat162_rn(d - df);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t src[4] = {w[k], w[k] >> 8, w[k] >> 4, w[k] >> 12};
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 n = __hadd2(bf2_of((src[e] & 0x000F000Fu) | k128), bf2_of(0xC308C308u));  // - 136
+            const __nv_bfloat162 t = __hmul2(n, dl);
+            const __nv_bfloat162 x = __hfma2(n, dh, t);
+            h[e] = word(x);
+            l[e] = word(__hadd2(__hfma2(n, dh, __hneg2(x)), t));
+        }
+        const int off = tile_off(row, 4 * blk + k);
+        *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+struct PromptPlan {
+    int items_per_list;  // row tiles (or pairs of them) of a (sequence, kv head) at most
+    uint32_t k1024, k128;  // constants of the unpacking, kept from the compiler (see attn_step.cu)
+    float* lse2;         // logarithms to base 2 for the weights, or null
+    unsigned* redo_n;    // bf16: how many rows are listed,
+    unsigned* redo;      // and which: row * heads + head
+};
+
+struct Bars {
+    uint64_t raw_full[3], raw_empty[3];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+};
+
+template <int D, bool F32, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(KvView c, KvRows r, AttnCall a, PromptPlan plan) {
+    using S = Shape<D, F32>;
+    constexpr int NB = S::kBlocks;
+    constexpr int kM = S::kM;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ Bars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ float row_unit[kM * kTile];  // 1 / (power of two that a row of Q was scaled by)
+    __shared__ float key_unit[4];           // the same of a key tile, tile i in i % 4
+    __shared__ float value_exp[4];          // log2 of the same of a value tile (bf16)
+    __shared__ __align__(16) uint8_t wild[4][32];         // bit t of byte l: token 4 l + t of tile i has a wild value scale
+    uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t* q_sm = base;                             // [kM][pieces]
+    uint8_t* k_sm = q_sm + kM * S::kOperand;          // [stages][pieces]
+    uint8_t* v_sm = k_sm + S::kStages * S::kOperand;  // [stages][pieces]
+    uint8_t* raw = v_sm + S::kStages * S::kOperand;   // [slots][cells, scales of the values]
+    unsigned int* const err = &g_attn_prompt_error;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kRawSlots; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], S::kDecodeWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.k_full[i], S::kDecodeWarps);
+            mbar_init(&bar.v_full[i], S::kDecodeWarps);
+            mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.pv_done[i], 1);
+            mbar_init(&bar.o_free[i], 4);
+        }
+        fence_barrier_init();
+    }
+    grid_dependency_wait();
+
+    // Work item: the longest lists of token tiles first.
+    const int lists = c.n_seqs * c.heads;
+    const int item = plan.items_per_list - 1 - static_cast<int>(blockIdx.x) / lists;
+    const int list = static_cast<int>(blockIdx.x) % lists;
+    const int b = list / c.heads, h = list % c.heads;
+    int first, count;
+    kv_rows(r, b, &first, &count, err);
+    const int L = kv_length(c, b, err);
+    const int group = a.heads / c.heads;
+    const int n_rows = count * group;
+    const int row0 = item * kM * kTile;
+    if (row0 >= n_rows) return;
+    const int base_pos = L - count;
+    const int pos_lo = base_pos + row0 / group;
+    const int pos_hi = base_pos + min(n_rows - 1, row0 + kM * kTile - 1) / group;
+    const int seen_len = max(0, min(L, pos_hi + 1));
+    const TileList tiles = tile_list(seen_len, max(pos_lo, 0), a.window, a.sinks);
+    const int n_tiles = tiles.count;
+
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // Q: four threads per row, each a quarter of the dims; a row is scaled by the
+    // power of two that takes its largest value to 2^13 .. 2^14.
+    const float sign = a.scale < 0.f ? -1.f : 1.f;
+#pragma unroll 1
+    for (int m = 0; m < kM; ++m) {
+        const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
+        const int rr = row0 + m * kTile + row;
+        const bool in = rr < n_rows;
+        const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(first + (in ? rr / group : 0)) * a.q_stride +
+                     static_cast<int64_t>(h * group + (in ? rr % group : 0)) * D;
+        constexpr int kEach = D / 32;  // chunks of 8 elements of this thread
+        float4 x[kEach][2];
+        float amax = 0.f;
+#pragma unroll
+        for (int y = 0; y < kEach; ++y) {
+            const int chunk = part * kEach + y, blk = chunk >> 2, k = chunk & 3;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[y][u] = in ? load_q4(q + 32 * blk + 16 * u + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[y][u].x), fabsf(x[y][u].y)),
+                                         fmaxf(fabsf(x[y][u].z), fabsf(x[y][u].w))));
+            }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+        const int up = min(126, 13 - ex);
+        const float f = sign * pow2(up);
+        if (part == 0) row_unit[m * kTile + row] = pow2(-up);
+#pragma unroll
+        for (int y = 0; y < kEach; ++y) {
+            // The order in which a word's quants unpack (decode_keys).
+            const float v[8] = {x[y][0].x, x[y][0].z, x[y][0].y, x[y][0].w, x[y][1].x, x[y][1].z, x[y][1].y, x[y][1].w};
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v0 = v[2 * e] * f, v1 = v[2 * e + 1] * f;
+                const __half2 hh = __floats2half2_rn(v0, v1);
+                const float2 back = __half22float2(hh);
+                hw[e] = word(hh);
+                lw[e] = word(__floats2half2_rn(v0 - back.x, v1 - back.y));
+            }
+            uint8_t* dst = q_sm + m * S::kOperand + tile_off(row, part * kEach + y);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            if (F32) *reinterpret_cast<uint4*>(dst + S::kPiece) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        }
+    }
+    fence_proxy_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < S::kSoftmaxWarps) {
+        // ---- softmax: this thread's row
+        if (F32) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int m = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const int row = 32 * (warp & 3) + lane;
+        const int rr = row0 + m * kTile + row;
+        const bool in = rr < n_rows;
+        const int pos = in ? base_pos + rr / group : -1;
+        const int win_lo = a.window > 0 ? pos - a.window + 1 : 0;  // tokens from here on, and below sinks
+        const int wr0 = row0 + m * kTile + 32 * (warp & 3);        // the warp's rows' extreme positions
+        const int w_lo = base_pos + wr0 / group, w_hi = base_pos + (wr0 + 31) / group;
+        const float unit = fabsf(a.scale) * kLog2e * row_unit[m * kTile + row];
+        const uint32_t t_o = tmem + lanes + kTmemO + m * 128;  // (bf16)
+        float mx_used = -INFINITY, sum = 0.f;
+        float lowest = INFINITY;  // bf16: of the row's scores (with the value tile's exponent)
+        float o[F32 ? D : 1];
+        float keep_last = 0.f;  // f32: what the sums before the last tile's products are scaled by
+#pragma unroll
+        for (int e = 0; e < (F32 ? D : 1); ++e) o[e] = 0.f;
+        bool ok = true;
+        // f32: o = o keep + P V of tile i.
+        auto collect = [&](int i) {
+            const int buf = i & 1;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[buf], (i >> 1) & 1, err));
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                float v[32];
+                tmem_ld32(tmem + lanes + kTmemO + buf * 128 + 32 * q, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[32 * q + e < (F32 ? D : 1) ? 32 * q + e : 0] =
+                    fmaf(o[32 * q + e < (F32 ? D : 1) ? 32 * q + e : 0], keep_last, v[e]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.o_free[buf]);
+        };
+#pragma unroll 1
+        for (int i = 0; i < n_tiles; ++i) {
+            const int buf = F32 ? (i & 1) : m;
+            const uint32_t t_s = tmem + lanes + buf * 128;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.s_full[buf], F32 ? (i >> 1) & 1 : i & 1, err));
+            if (!ok) break;
+            tc_fence_after();
+            const int key0 = tiles.at(i) * kTile;
+            const float f = unit * key_unit[i & 3];
+            const float v_exp = F32 ? 0.f : value_exp[i & 3];
+            bool any_wild;
+            {
+                const uint4 w0 = *reinterpret_cast<const uint4*>(wild[i & 3]);
+                const uint4 w1 = *reinterpret_cast<const uint4*>(wild[i & 3] + 16);
+                any_wild = (w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w) != 0;
+            }
+            const bool masked = any_wild || key0 + kTile > min(w_lo + 1, L) ||
+                                (a.window > 0 && key0 <= w_hi - a.window && key0 + kTile > a.sinks);
+            // Two passes over the row's scores in TMEM: its maximum, then P.  Token
+            // key0 + k counts as -infinity where the row does not see it, as NaN
+            // where it does and its values are not finite.
+            const int k_hi = min(pos, L - 1) - key0, k_lo = win_lo - key0, k_sink = a.sinks - key0;
+            auto tile = [&](auto kMask, auto kWild) {
+                auto sees = [&](int k) { return !kMask || (k <= k_hi && (k >= k_lo || k < k_sink)); };
+                auto score = [&](float s, int k) {
+                    if (kWild && ((wild[i & 3][k >> 2] >> (k & 3)) & 1)) s = NAN;
+                    return sees(k) ? s : -INFINITY;
+                };
+                float v[32];
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float mn4[2] = {INFINITY, INFINITY};
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    tmem_ld32(t_s + 32 * q, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        mx4[e & 3] = fmaxf(mx4[e & 3], score(v[e], 32 * q + e));
+                        if (!F32) mn4[e & 1] = fminf(mn4[e & 1], sees(32 * q + e) ? v[e] : INFINITY);
+                    }
+                }
+                const float mx = fmaf(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), f, v_exp);
+                float off;
+                if (F32) {
+                    const float next = fmaxf(mx_used, mx);
+                    off = next == -INFINITY ? 0.f : next;
+                    keep_last = exp2_approx(mx_used - off);  // applied when this tile's products are collected
+                    mx_used = next;
+                    sum *= keep_last;
+                } else {
+                    lowest = fminf(lowest, fmaf(fminf(mn4[0], mn4[1]), f, v_exp));
+                    // The maximum in use follows only where it is overtaken by 2^3.
+                    const bool grow = mx > mx_used + kLazy;
+                    if (__any_sync(0xFFFFFFFFu, grow)) {
+                        const float next = grow ? mx : mx_used;
+                        const float keep = grow ? exp2_approx(mx_used - next) : 1.f;
+                        mx_used = next;
+                        sum *= keep;
+                        if (i > 0) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 32; ++q) {
+                                tmem_ld32(t_o + 32 * q, v);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] *= keep;
+                                tmem_st32(t_o + 32 * q, v);
+                            }
+                            tc_wait_st();
+                        }
+                    }
+                    off = (mx_used == -INFINITY ? 0.f : mx_used) - v_exp - kPTop;
+                }
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    tmem_ld32(t_s + 32 * q, v);
+                    tc_wait_ld();
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float p0 = exp2_approx(score(fmaf(v[e], f, -off), 32 * q + e));
+                        const float p1 = exp2_approx(score(fmaf(v[e + 1], f, -off), 32 * q + e + 1));
+                        part[e / 2 & 3] += p0 + p1;
+                        if (F32) {
+                            const uint32_t w = word(__floats2bfloat162_rn(p0, p1));
+                            hi[e / 2] = w;
+                            lo[e / 2] = word(__floats2bfloat162_rn(p0 - __uint_as_float(w << 16),
+                                                                   p1 - __uint_as_float(w & 0xFFFF0000u)));
+                        } else {
+                            hi[e / 2] = word(__floats2half2_rn(p0, p1));
+                        }
+                    }
+                    if (F32) {
+                        tmem_st16(t_s + 32 * q, hi);
+                        tmem_st16(t_s + 32 * q + 16, lo);
+                    } else {
+                        tmem_st16(t_s + 16 * q, hi);
+                    }
+                }
+                const float all = (part[0] + part[1]) + (part[2] + part[3]);
+                sum += F32 ? all : all * exp2_approx(-v_exp);
+            };
+            const float keep_before = keep_last;
+            if (any_wild) tile(std::true_type(), std::true_type());
+            else if (masked) tile(std::true_type(), std::false_type());
+            else tile(std::false_type(), std::false_type());
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[buf]);
+            if (F32 && i > 0) {
+                const float keep_now = keep_last;
+                keep_last = keep_before;
+                collect(i - 1);
+                keep_last = keep_now;
+                if (!ok) break;
+            }
+        }
+        if (ok && n_tiles > 0) {
+            if (F32) collect(n_tiles - 1);
+            else ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[m], (n_tiles - 1) & 1, err));
+        }
+        tc_fence_after();
+        // The output: columns in the order the quants unpack.
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t orow = first + (in ? rr / group : 0);
+        const int head = h * group + (in ? rr % group : 0);
+        T* out = static_cast<T*>(a.out) + orow * a.out_stride + static_cast<int64_t>(head) * D;
+        float least = INFINITY;
+        auto store8 = [&](const float y[8], int q, int k) {
+            store_o4(out + 32 * q + 4 * k, make_float4(y[0], y[2], y[1], y[3]));
+            store_o4(out + 32 * q + 16 + 4 * k, make_float4(y[4], y[6], y[5], y[7]));
+        };
+        if (F32) {
+            if (in) {
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int x = 32 * q + 8 * k + e;
+                            y[e] = sum == 0.f ? 0.f : o[x < (F32 ? D : 1) ? x : 0] * inv;
+                        }
+                        store8(y, q, k);
+                    }
+            }
+        } else {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+                float v[32];
+                if (n_tiles > 0) {
+                    tmem_ld32(t_o + 32 * q, v);
+                    tc_wait_ld();
+                }
+                if (in) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            least = fminf(least, fabsf(v[8 * k + e]));
+                            y[e] = sum == 0.f ? 0.f : v[8 * k + e] * inv;
+                        }
+                        store8(y, q, k);
+                    }
+                }
+            }
+        }
+        if (in) {
+            const float lse2 = sum == 0.f ? -INFINITY : mx_used + log2f(sum) - (F32 ? 0.f : kPTop);
+            if (a.lse) a.lse[orow * a.heads + head] = lse2 * kLn2;
+            if (plan.lse2) plan.lse2[orow * a.heads + head] = lse2;
+            // Every P is off by at most 2^-25 where it is small, times a value of
+            // at most 2^6: could that be 2^-11 of some element?
+            if (!F32 && lowest < mx_used - kFarBelow && least < static_cast<float>(n_tiles) * (kTile * 0x1p-8f)) {
+                const unsigned at = atomicAdd(plan.redo_n, 1u);  // (at most once per row)
+                plan.redo[at] = static_cast<unsigned>(orow * a.heads + head);
+            }
+        }
+    } else if (warp < S::kSoftmaxWarps + S::kDecodeWarps) {
+        // ---- decode: raw cells -> swizzled tiles; keys one tile ahead of values
+        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        const int dt = threadIdx.x - S::kSoftmaxWarps * 32;
+        const bool chief = dt < 32;  // this warp also writes what the softmax reads
+        bool ok = true;
+        // Raw tiles come in the order they are used: keys 0, keys 1, values 0, keys 2, ...
+        int slot = 0, round = 0;
+        float v_scale = 1.f, v_scale_next = 1.f;  // bf16: powers of two of a value tile and the next
+        auto next_slot = [&] {
+            if (++slot == S::kRawSlots) slot = 0, ++round;
+        };
+        auto keys = [&](int i) {
+            const int stage = i % S::kStages;
+            ok = __all_sync(0xFFFFFFFFu,
+                            mbar_wait_bounded(&bar.raw_full[slot], round & 1, err) &&
+                                (i < S::kStages || mbar_wait_bounded(&bar.k_empty[stage], (i / S::kStages - 1) & 1, err)));
+            if (!ok) return;
+            const uint8_t* rawk = raw + slot * S::kSlot;
+            const uint8_t* vsc = rawk + S::kRaw;
+            const int left = seen_len - tiles.at(i) * kTile;  // tokens of the tile that count
+            // The largest scales: lane l looks at tokens 4 l .. 4 l + 3.
+            uint32_t top = 0, top_v = 0, bad = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int tok = 4 * lane + u;
+                const uint8_t* sc = rawk + (tok >> 4) * cell_bytes(D) + cell_scales(D) + (tok & 15) * 2 * NB;
+                const uint8_t* sv = vsc + tok * 2 * NB;
+                bool wild_v = false;
+#pragma unroll
+                for (int e = 0; e < NB / 2; ++e) {
+                    const uint32_t x = reinterpret_cast<const uint32_t*>(sc)[e] & 0x7FFF7FFFu;
+                    const uint32_t v = reinterpret_cast<const uint32_t*>(sv)[e] & 0x7FFF7FFFu;
+                    const uint32_t x0 = x & 0xFFFFu, x1 = x >> 16, v0 = v & 0xFFFFu, v1 = v >> 16;
+                    if (tok < left) {
+                        if (x0 < 0x7C00u) top = max(top, x0);
+                        if (x1 < 0x7C00u) top = max(top, x1);
+                        if (v0 < 0x7C00u) top_v = max(top_v, v0);
+                        else wild_v = true;
+                        if (v1 < 0x7C00u) top_v = max(top_v, v1);
+                        else wild_v = true;
+                    }
+                }
+                if (wild_v) bad |= 1u << u;
+            }
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            const int up = 26 - max(1, static_cast<int>(top >> 10));  // largest scale to 2^11 .. 2^12
+            const float f = pow2(up);
+            int up_v = 0;
+            if (!F32) {
+                top_v = __reduce_max_sync(0xFFFFFFFFu, top_v);
+                up_v = 17 - max(1, static_cast<int>(top_v >> 10));  // to 2^2 .. 2^3
+                v_scale_next = pow2(up_v);
+            }
+            if (chief) {
+                wild[i & 3][lane] = static_cast<uint8_t>(bad);
+                if (lane == 0) {
+                    key_unit[i & 3] = pow2(-up);
+                    value_exp[i & 3] = static_cast<float>(-up_v);
+                }
+            }
+            uint8_t* hi = k_sm + stage * S::kOperand;
+#pragma unroll 1
+            for (int y = 0; y < kTile * NB / (S::kDecodeWarps * 32); ++y) {
+                const int task = dt + y * S::kDecodeWarps * 32;
+                const int tok = task & (kTile - 1), blk = task / kTile;
+                const uint8_t* cell = rawk + (tok >> 4) * cell_bytes(D);
+                const uint4 q = *reinterpret_cast<const uint4*>(cell + blk * 256 + (tok & 15) * 16);
+                const float d = f16_bits_to_float(
+                    *reinterpret_cast<const uint16_t*>(cell + cell_scales(D) + ((tok & 15) * NB + blk) * 2));
+                decode_keys<F32>(q, d * f, tok, blk, hi, hi + S::kPiece, plan.k1024);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar.raw_empty[slot]);
+                mbar_arrive(&bar.k_full[stage]);
+            }
+            next_slot();
+        };
+        auto values = [&](int i) {
+            const int stage = i % S::kStages;
+            ok = __all_sync(0xFFFFFFFFu,
+                            mbar_wait_bounded(&bar.raw_full[slot], round & 1, err) &&
+                                (i < S::kStages || mbar_wait_bounded(&bar.v_empty[stage], (i / S::kStages - 1) & 1, err)));
+            if (!ok) return;
+            const uint8_t* rawv = raw + slot * S::kSlot;
+            const int left = seen_len - tiles.at(i) * kTile;
+            uint8_t* hi = v_sm + stage * S::kOperand;
+#pragma unroll 1
+            for (int y = 0; y < kTile * NB / (S::kDecodeWarps * 32); ++y) {
+                const int task = dt + y * S::kDecodeWarps * 32;
+                const int tok = task & (kTile - 1), blk = task / kTile;
+                const uint8_t* cell = rawv + (tok >> 4) * cell_bytes(D);
+                const uint4 q = *reinterpret_cast<const uint4*>(cell + blk * 256 + (tok & 15) * 16);
+                const uint32_t bits =
+                    *reinterpret_cast<const uint16_t*>(cell + cell_scales(D) + ((tok & 15) * NB + blk) * 2);
+                // Past the end, or not finite (NaN then comes with the scores): 0.
+                const float d = tok >= left || (bits & 0x7C00u) == 0x7C00u ? 0.f : f16_bits_to_float(bits);
+                if (F32) decode_values(q, d, tok, blk, hi, hi + S::kPiece, plan.k128);
+                else decode_keys<false>(q, d * v_scale, tok, blk, hi, hi, plan.k1024);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar.raw_empty[slot]);
+                mbar_arrive(&bar.v_full[stage]);
+            }
+            next_slot();
+        };
+        // (Twice through one loop body, so that its code is there once.)
+#pragma unroll 1
+        for (int i = -1; i < n_tiles && ok; ++i) {
+            v_scale = v_scale_next;
+            if (i + 1 < n_tiles) keys(i + 1);
+            if (ok && i >= 0) values(i);
+        }
+    } else {
+        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 12) {
+        // ---- MMA issue
+        if (lane == 0 && n_tiles > 0) {
+            constexpr uint32_t id_s = idesc(0, kTile, false), id_o = idesc(F32 ? 1 : 0, D, true);
+            bool ok = true;
+            auto scores = [&](int i, int m) {
+                const int stage = i % S::kStages;
+                ok = ok && mbar_wait_bounded(&bar.k_full[stage], (i / S::kStages) & 1, err);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t t_s = tmem + (F32 ? (i & 1) : m) * 128;
+                const uint32_t q0 = smem_addr(q_sm + m * S::kOperand), k0 = smem_addr(k_sm + stage * S::kOperand);
+                constexpr int kProducts = F32 ? 3 : 1;  // low x high, high x low, high x high
+#pragma unroll 1
+                for (int p = 0; p < kProducts; ++p) {
+                    const uint64_t da = desc_base(q0 + (F32 && p == 0 ? S::kPiece : 0), 16);
+                    const uint64_t db = desc_base(k0 + (F32 && p == 1 ? S::kPiece : 0), 16);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t o = static_cast<uint64_t>((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                        mma_ss(t_s, da + o, db + o, id_s, (p | kk) != 0);
+                    }
+                }
+                mma_commit(&bar.s_full[F32 ? (i & 1) : m]);
+                if (m == kM - 1) mma_commit(&bar.k_empty[stage]);
+            };
+            auto output = [&](int i, int m) {
+                const int stage = i % S::kStages, buf = F32 ? (i & 1) : m;
+                ok = ok && mbar_wait_bounded(&bar.p_full[buf], F32 ? (i >> 1) & 1 : i & 1, err) &&
+                     mbar_wait_bounded(&bar.v_full[stage], (i / S::kStages) & 1, err);
+                if (!ok) return;
+                // f32: the buffer's last products have been collected.
+                if (F32 && i > 1) ok = mbar_wait_bounded(&bar.o_free[buf], ((i >> 1) - 1) & 1, err);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t t_o = tmem + kTmemO + buf * 128;
+                const uint32_t v0 = smem_addr(v_sm + stage * S::kOperand);
+                constexpr int kProducts = S::kPieces * S::kPieces;  // low x low first, high x high last
+#pragma unroll 1
+                for (int p = kProducts - 1; p >= 0; --p) {
+                    const uint32_t t_p = tmem + buf * 128 + ((p >> 1) ? 16 : 0);
+                    // V is [token][dim]: rows are the contraction, 64-dim columns kTile * 128 bytes apart.
+                    const uint64_t db = desc_base(v0 + ((p & 1) ? S::kPiece : 0), kTile * 128);
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_ts(t_o, t_p + (F32 ? (kk >> 1) * 32 + (kk & 1) * 8 : 8 * kk),
+                               db + (static_cast<uint64_t>(kk * 16 * 128) >> 4), id_o,
+                               (F32 ? (kProducts - 1 - p) | kk : i | kk) != 0);
+                }
+                mma_commit(&bar.pv_done[buf]);
+                if (m == kM - 1) mma_commit(&bar.v_empty[stage]);
+            };
+            if (F32) {
+                scores(0, 0);
+                for (int i = 0; i < n_tiles && ok; ++i) {
+                    if (i + 1 < n_tiles) scores(i + 1, 0);
+                    output(i, 0);
+                }
+            } else {
+                for (int m = 0; m < kM; ++m) scores(0, m);
+                for (int i = 0; i < n_tiles && ok; ++i) {
+                    for (int m = 0; m < kM; ++m) {
+                        output(i, m);
+                        if (i + 1 < n_tiles) scores(i + 1, m);
+                    }
+                }
+            }
+        }
+    } else if (warp == 13) {
+        // ---- loader: lanes 0 .. 7 a cell of the tile each (the first of a page's
+        // run copies it whole), lanes 8 .. 15 the scales of a cell of values.
+        const int run = min(8, 1 << (c.page_shift - 4));
+        auto cell_at = [&](int i) -> int64_t {
+            if (lane >= 16 || i >= n_tiles) return -1;
+            const int p = tiles.at(i) * kTile + (lane & 7) * 16;
+            return p < seen_len ? kv_cell(c, b, h, p, err) : -1;
+        };
+        bool ok = true;
+        int slot = 0, round = 0;
+        auto fetch = [&](int i, bool v, int64_t off) {
+            if (round) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_empty[slot], (round - 1) & 1, err));
+            if (!ok) return;
+            const int cells = min(8, (seen_len - tiles.at(i) * kTile + 15) >> 4);
+            uint8_t* dst = raw + slot * S::kSlot;
+            uint32_t bytes = 0;
+            if (lane < 8 && lane % run == 0 && off >= 0)
+                bytes = static_cast<uint32_t>(min(run, cells - lane) * cell_bytes(D));
+            else if (lane >= 8 && lane < 16 && !v && off >= 0) bytes = 32 * NB;
+            const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
+            if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], total);
+            __syncwarp();
+            if (bytes) {
+                if (lane < 8)
+                    bulk_load_1d(dst + lane * cell_bytes(D), (v ? c.v : c.k) + off, bytes, &bar.raw_full[slot]);
+                else
+                    bulk_load_1d(dst + S::kRaw + (lane - 8) * 32 * NB, c.v + off + cell_scales(D), bytes,
+                                 &bar.raw_full[slot]);
+            }
+            if (++slot == S::kRawSlots) slot = 0, ++round;
+        };
+        int64_t off = -1, off_next = cell_at(0);  // tile i's, tile i + 1's
+#pragma unroll 1
+        for (int i = -1; i < n_tiles && ok; ++i) {
+            if (i + 1 < n_tiles) fetch(i + 1, false, off_next);
+            if (ok && i >= 0) fetch(i, true, off);
+            off = off_next;
+            off_next = cell_at(i + 2);
+        }
+    }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <int D, bool F32, typename T>
+cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, unsigned* redo_n, unsigned* redo,
+                          cudaStream_t stream) {
+    using S = Shape<D, F32>;
+    static SmemOnce once;
+    cudaError_t err = once.set(attn_prompt_kernel<D, F32, T>, S::kSmem);
+    if (err != cudaSuccess) return err;
+    const int64_t rows = static_cast<int64_t>(r.max_q) * (a.heads / c.heads);
+    PromptPlan p = {};
+    p.items_per_list = static_cast<int>((rows + S::kM * kTile - 1) / (S::kM * kTile));
+    p.k1024 = 0x64006400u;
+    p.k128 = 0x43004300u;
+    p.lse2 = lse2;
+    p.redo_n = redo_n;
+    p.redo = redo;
+    const int64_t grid = static_cast<int64_t>(p.items_per_list) * c.n_seqs * c.heads;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    note_launch();
+    return launch_pdl(attn_prompt_kernel<D, F32, T>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, stream,
+                      c, r, a, p);
+}
+
+}  // namespace
+
+bool attn_prompt_takes(const KvView& c) { return c.dim == 64 || c.dim == 128; }
+
+cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, unsigned* redo_n, unsigned* redo,
+                               cudaStream_t stream) {
+    if (c.dim == 64)
+        return a.type == KvType::kF32 ? launch_prompt<64, true, float>(c, r, a, lse2, redo_n, redo, stream)
+                                      : launch_prompt<64, false, __nv_bfloat16>(c, r, a, lse2, redo_n, redo, stream);
+    return a.type == KvType::kF32 ? launch_prompt<128, true, float>(c, r, a, lse2, redo_n, redo, stream)
+                                  : launch_prompt<128, false, __nv_bfloat16>(c, r, a, lse2, redo_n, redo, stream);
+}
+
+cudaError_t attn_prompt_read_device_error(unsigned int* bits, bool clear) {
+    unsigned int v = 0;
+    cudaError_t err = cudaMemcpyFromSymbol(&v, g_attn_prompt_error, sizeof(v));
+    if (err != cudaSuccess) return err;
+    *bits |= v;
+    if (clear && v) {
+        const unsigned int zero = 0;
+        err = cudaMemcpyToSymbol(g_attn_prompt_error, &zero, sizeof(zero));
+    }
+    return err;
+}
+
+}  // namespace qm

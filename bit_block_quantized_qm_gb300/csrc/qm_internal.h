@@ -208,6 +208,15 @@ int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_
 cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);
 cudaError_t attn_step_read_device_error(unsigned int* bits, bool clear);
 
+// Many rows (attn_prompt.cu): head dimensions 64 and 128.  lse2, when not null,
+// gets [n_tokens][heads] logarithms to base 2 of the sums.  bf16 rows: redo
+// (n_tokens * heads words) gets the (row * heads + head) that the plain kernel
+// is to do again, *redo_n (zero before) their number.
+bool attn_prompt_takes(const KvView& c);
+cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, unsigned* redo_n, unsigned* redo,
+                               cudaStream_t stream);
+cudaError_t attn_prompt_read_device_error(unsigned int* bits, bool clear);
+
 // Opts a kernel into `bytes` of dynamic shared memory, once per device: one
 // static object per kernel.
 class SmemOnce {
