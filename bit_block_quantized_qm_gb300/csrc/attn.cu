@@ -34,12 +34,14 @@ __device__ __forceinline__ float cell_value(const uint8_t* cell, int dim, int sl
     return magic_minus8(q | kMagicBits) * d;
 }
 
-// One warp per row and query head (item = row * heads + head); lane l holds
-// dims 32 i + l.  The softmax runs in one pass over the tokens with a running
-// maximum and sum, in f32.
-template <int NB, typename T>
+// One row and query head (item = row * heads + head) by the `parts` warps of a
+// CTA that call this with part = 0 .. parts - 1, or by one warp; lane l holds dims
+// 32 i + l.  The softmax runs in one pass over the tokens with a running maximum
+// and sum, in f32, four tokens at a time so that their loads overlap; the warps'
+// sums meet in shared memory.
+template <int NB, typename T, int kParts>
 __device__ __forceinline__ void attn_plain_row(const KvView& c, const KvRows& r, const AttnCall& a, float* lse,
-                                               int64_t item) {
+                                               int64_t item, int part) {
     const int lane = threadIdx.x & 31;
     const int row = static_cast<int>(item / a.heads), head = static_cast<int>(item % a.heads);
     const int b = kv_seq_of_row(r, c.n_seqs, row);
@@ -57,25 +59,70 @@ __device__ __forceinline__ void attn_plain_row(const KvView& c, const KvRows& r,
         o[i] = 0.f;
     }
     float m = -INFINITY, l = 0.f;
+    // The tokens seen: 0 .. n_first - 1 and lo .. pos, numbered in a row.
     const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    for (int j = a.window > 0 && a.sinks > 0 ? 0 : lo; j <= pos; ++j) {
-        if (j < lo && j >= a.sinks) j = lo;
-        if (j > pos) break;
-        const int64_t off = kv_cell(c, b, h, j, &g_attn_error);
-        if (off < 0) continue;
-        const int slot = j & 15;
-        float s = 0.f;
+    const int n_first = a.window > 0 ? min(min(a.sinks, lo), pos + 1) : 0;
+    const int n = n_first + max(0, pos - lo + 1);
+    for (int x0 = 4 * part; x0 < n; x0 += 4 * kParts) {
+        float s[4], v[4][NB];
+        float top = m;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) s = fmaf(qv[i], cell_value(c.k + off, c.dim, slot, i, lane), s);
+        for (int u = 0; u < 4; ++u) {
+            const int x = min(x0 + u, n - 1);
+            const int j = x < n_first ? x : lo + (x - n_first);
+            const int64_t off = kv_cell(c, b, h, j, &g_attn_error);
+            s[u] = 0.f;
 #pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        const float m2 = fmaxf(m, s);
-        const float base = m2 == -INFINITY ? 0.f : m2;
-        const float keep = exp2f(m - base), p = exp2f(s - base);
-        m = m2;
-        l = fmaf(l, keep, p);
+            for (int i = 0; i < NB; ++i) {
+                s[u] = off < 0 ? 0.f : fmaf(qv[i], cell_value(c.k + off, c.dim, j & 15, i, lane), s[u]);
+                v[u][i] = off < 0 ? 0.f : cell_value(c.v + off, c.dim, j & 15, i, lane);
+            }
+        }
 #pragma unroll
-        for (int i = 0; i < NB; ++i) o[i] = fmaf(p, cell_value(c.v + off, c.dim, slot, i, lane), o[i] * keep);
+        for (int y = 16; y; y >>= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xFFFFFFFFu, s[u], y);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (x0 + u >= n) s[u] = -INFINITY;
+            top = fmaxf(top, s[u]);
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        const float keep = exp2f(m - base);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) o[i] *= keep;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float p = exp2f(s[u] - base);
+            l += p;
+            if (x0 + u < n) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) o[i] = fmaf(p, v[u][i], o[i]);
+            }
+        }
+    }
+    if constexpr (kParts > 1) {
+        __shared__ float s_o[kParts][NB * 32], s_m[kParts], s_l[kParts];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) s_o[part][32 * i + lane] = o[i];
+        if (lane == 0) s_m[part] = m, s_l[part] = l;
+        __syncthreads();
+        m = -INFINITY;
+        for (int y = 0; y < kParts; ++y) m = fmaxf(m, s_m[y]);
+        const float base = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) o[i] = 0.f;
+        for (int y = 0; y < kParts; ++y) {
+            const float f = exp2f(s_m[y] - base);
+            l = fmaf(f, s_l[y], l);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) o[i] = fmaf(f, s_o[y][32 * i + lane], o[i]);
+        }
+        __syncthreads();
+        if (part) return;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* out = static_cast<T*>(a.out) + row * a.out_stride + static_cast<int64_t>(head) * c.dim;
@@ -93,19 +140,21 @@ __global__ void __launch_bounds__(kWarps * 32) attn_plain_kernel(KvView c, KvRow
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (item < static_cast<int64_t>(r.n_tokens) * a.heads) attn_plain_row<NB, T>(c, r, a, lse, item);
+    if (item < static_cast<int64_t>(r.n_tokens) * a.heads) attn_plain_row<NB, T, 1>(c, r, a, lse, item, 0);
 }
 
 // The rows that the prompt kernel listed in `redo` (redo_n[0] of them, redo_n[1]
-// counts CTAs); the last CTA to finish leaves the list empty for the next call.
+// counts CTAs), a CTA each; the last CTA to finish leaves the list empty for
+// the next call.
+constexpr int kRedoWarps = 8;
 template <int NB, typename T>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kRedoWarps * 32)
     attn_redo_kernel(KvView c, KvRows r, AttnCall a, float* lse, unsigned* redo_n, const unsigned* redo) {
     grid_launch_dependents();
     grid_dependency_wait();
     const unsigned n = __ldcg(redo_n);
-    for (unsigned i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < n; i += gridDim.x * kWarps)
-        attn_plain_row<NB, T>(c, r, a, lse, __ldcg(redo + i));
+    for (unsigned i = blockIdx.x; i < n; i += gridDim.x)
+        attn_plain_row<NB, T, kRedoWarps>(c, r, a, lse, __ldcg(redo + i), threadIdx.x >> 5);
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
@@ -163,9 +212,9 @@ cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cu
         unsigned* redo_n = reinterpret_cast<unsigned*>(a.ws + kRedoCount);
         unsigned* redo = reinterpret_cast<unsigned*>(a.ws + kRedoOff);
         err = launch_attn_prompt(c, r, a, lse, redo_n, redo, stream);
-        if (err == cudaSuccess && a.type == KvType::kBF16) {
+        if (err == cudaSuccess) {
             note_launch();
-            err = launch_pdl(attn_redo_kernel<NB, T>, dim3(152), dim3(kWarps * 32), 0, stream, c, r, a, lse, redo_n,
+            err = launch_pdl(attn_redo_kernel<NB, T>, dim3(152), dim3(kRedoWarps * 32), 0, stream, c, r, a, lse, redo_n,
                              redo);
         }
     } else {

@@ -6,22 +6,23 @@
 // one pass with a running maximum and sum per row.  A query row is scaled to the
 // top of f16's range, a key tile by the power of two that takes its largest
 // scale to 2^11 .. 2^12; both are then f16 pieces.
-//   f32 rows: two pieces of Q (22 bits) and of K (exact); S takes the three
-//     products that are not 2^-22 of the first, smallest first.  P is two bf16
-//     pieces (2^-18 of itself over the whole range of f32, where f16 would lose
-//     the small ones), V exactly two bf16 pieces; all four products, smallest
-//     first, start from 0 for every token tile, and the row's sums are kept in
-//     registers: the tensor cores cut their sums off instead of rounding them,
-//     which over a long row would show (2e-6 at 300 tokens, growing).
-//   bf16 rows: one piece each (queries exact, keys, P and V to 11 bits), and the
-//     output accumulates in TMEM.  A value tile too is scaled by a power of two,
-//     which P takes on (P = exp2(s + e - maximum of s + e)), so f16's range
-//     serves any scale.  What that range loses are tokens 2^-26 below a row's
-//     maximum.  They can matter only to an output element to which all large
-//     tokens add up to about nothing: rows that have both are listed and done
-//     again by the plain kernel.
+// A value tile is scaled likewise, and P takes that on (P = exp2(s + e - maximum of
+// s + e)), so f16's range serves any scale.
+//   f32 rows: two pieces each (22 bits of Q and P, K and V exact) and the three
+//     products that are not 2^-22 of the first, smallest first.  P's second
+//     piece is kept 2^11 up, with an accumulator of its own.  Every token tile's
+//     P V starts from 0 and is added to the row's sums in registers: the tensor
+//     cores cut their sums off instead of rounding them, which over a long row
+//     would show (2e-6 at 300 tokens, growing).
+//   bf16 rows: one piece each (queries exact, the others 11 bits), and the output
+//     accumulates in TMEM.
+// What f16's range loses are tokens 2^-33 (bf16: 2^-24) below a row's maximum.
+// They can matter only to an output element to which all larger tokens add up
+// to about nothing: rows that have both are listed and done again by the plain
+// kernel.  (bf16 pieces, which have the range, need 4 products for 2^-17, or
+// give 2^-9.)
 //
-// What bounds it: f32 rows the tensor cores (7 products of 2^21 MACs per pair of
+// What bounds it: f32 rows the tensor cores (6 products of 2^21 MACs per pair of
 // tiles at D = 128); bf16 rows (2 products) the tensor cores and the issue slots
 // about equally (softmax 6 instructions per score, unpacking 13 per 8 quants,
 // shared by two row tiles).
@@ -39,11 +40,10 @@
 // Code is kept short on purpose (rolled loops over 32-column chunks): unrolled,
 // the roles of the four schedulers evicted one another's instructions (805 us
 // against 449 for a prompt of 4096 f32 rows).
-// f32 rows' registers: 512 threads x 128 at launch; then 128 x 232 + 256 x 96 +
-// 128 x 56 = 61440 of those 65536.
+// f32 rows' registers: 640 threads x 96 at launch; then 256 x 136 + 256 x 72 +
+// 128 x 40 = 58368 of those 61440.
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include <algorithm>
-#include <type_traits>
 
 #include "kv_cache.cuh"
 
@@ -53,8 +53,10 @@ __device__ unsigned int g_attn_prompt_error = 0;
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTile = 128;  // rows of a row tile, tokens of a token tile
+constexpr int kSoftmaxWarps = 8, kDecodeWarps = 8;  // then MMA issue, loader, examiner, an idle one
+constexpr int kRing = 8;    // tiles whose scale factors are kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -70,19 +72,28 @@ struct Shape {
     static constexpr int kRaw = kTile / 16 * 9 * D;   // raw cells of a tile
     static constexpr int kVScales = kTile * 2 * kBlocks;
     static constexpr int kSlot = kRaw + kVScales;     // keys come with the scales of the values
-    static constexpr int kSoftmaxWarps = 4 * kM;
-    static constexpr int kDecodeWarps = F32 ? 8 : 4;
+    static constexpr int kHalves = F32 ? 2 : 1;       // softmax threads of a row
     static constexpr int kSmem = kM * kOperand + 2 * kStages * kOperand + kRawSlots * kSlot + 1024;
     static_assert(kSmem <= 232448 - 3072, "shared memory of one CTA");
 };
 
 // TMEM columns: S and P over it 0 .. 255 in two buffers (f32: tiles in turn, the
 // pieces of 32 scores' P in 16 columns each; bf16: a row tile each), then P V in
-// two buffers of 128 likewise.
+// two of 128 (f32: with P's first and second piece; bf16: a row tile each).
 constexpr uint32_t kTmemO = 256;
-constexpr float kLazy = 3.f;      // bf16: how far (log2) a maximum may be overtaken
-constexpr float kPTop = 12.f;     // bf16: P is 2^12 at the maximum in use
-constexpr float kFarBelow = 24.f; // bf16: P this far (log2) below the maximum loses bits
+constexpr float kLazy = 3.f;  // bf16: how far (log2) a maximum may be overtaken
+// P is 2^kPTop at the maximum in use, and loses bits kFarBelow (log2) below it.
+template <bool F32>
+constexpr float kPTop = F32 ? 15.f : 12.f;
+template <bool F32>
+constexpr float kFarBelow = F32 ? 34.f : 28.f;
+// An element is safe from what is lost if it is this much times the square root
+// of the number of tokens: each one's error is at most 2^-25 in P's last piece
+// times a value of at most 2^6, either sign, to be 2^-18 (2^-11) of the element
+// with a margin of 4.
+template <bool F32>
+constexpr float kSafe = F32 ? 0x1p-10f : 0x1p-6f;
+constexpr float kLowUp = 2048.f;  // f32: what P's second piece is scaled by
 
 __device__ __forceinline__ uint64_t desc_base(uint32_t saddr, uint32_t lbo) {
     uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
@@ -162,7 +173,6 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 __device__ __forceinline__ uint32_t word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ uint32_t word(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
-__device__ __forceinline__ __nv_bfloat162 bf2_of(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 
 __device__ __forceinline__ float4 load_q4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load_q4(const __nv_bfloat16* p) {
@@ -200,10 +210,11 @@ __device__ __forceinline__ TileList tile_list(int seen_len, int pos_lo, int wind
     return t;
 }
 
-// Keys of one block of a token: 16 quant bytes and the tile-scaled f16 d ->
-// four chunks of 8, each word's quants in the order they unpack.
+// One block of a token: 16 quant bytes and the tile-scaled f16 d -> four chunks of
+// 8, each word's quants in the order they unpack, (n - 8) d rounded to f16 and
+// (f32 rows) the exact rest.
 template <bool F32>
-__device__ __forceinline__ void decode_keys(uint4 q, float d, int row, int blk, uint8_t* hi, uint8_t* lo, uint32_t k1024) {
+__device__ __forceinline__ void decode_block(uint4 q, float d, int row, int blk, uint8_t* hi, uint8_t* lo, uint32_t k1024) {
     const __half2 dd = __float2half2_rn(d);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -227,42 +238,16 @@ __device__ __forceinline__ void decode_keys(uint4 q, float d, int row, int blk, 
     }
 }
 
-// Values of one block of a token as bf16: d = dh + dl exactly (8 and 3 bits), so
-// (n - 8) dl is exact, one FMA rounds (n - 8) d once, and what that leaves is
-// exact again.
-__device__ __forceinline__ void decode_values(uint4 q, float d, int row, int blk, uint8_t* hi, uint8_t* lo,
-                                              uint32_t k128) {
-    const float df = __bfloat162float(__float2bfloat16_rn(d));
-    const __nv_bfloat162 dh = __float2bfloat162_rn(df), dl = __float2bfloat162_rn(d - df);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t src[4] = {w[k], w[k] >> 8, w[k] >> 4, w[k] >> 12};
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 n = __hadd2(bf2_of((src[e] & 0x000F000Fu) | k128), bf2_of(0xC308C308u));  // - 136
-            const __nv_bfloat162 t = __hmul2(n, dl);
-            const __nv_bfloat162 x = __hfma2(n, dh, t);
-            h[e] = word(x);
-            l[e] = word(__hadd2(__hfma2(n, dh, __hneg2(x)), t));
-        }
-        const int off = tile_off(row, 4 * blk + k);
-        *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-}
-
 struct PromptPlan {
     int items_per_list;  // row tiles (or pairs of them) of a (sequence, kv head) at most
-    uint32_t k1024, k128;  // constants of the unpacking, kept from the compiler (see attn_step.cu)
+    uint32_t k1024;      // two f16 1024, kept from the compiler (see attn_step.cu)
     float* lse2;         // logarithms to base 2 for the weights, or null
-    unsigned* redo_n;    // bf16: how many rows are listed,
+    unsigned* redo_n;    // how many rows are listed to be done again,
     unsigned* redo;      // and which: row * heads + head
 };
 
 struct Bars {
-    uint64_t raw_full[3], raw_empty[3];
+    uint64_t raw_full[3], raw_empty[3], exam[3];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
 };
@@ -277,9 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Bars bar;
     __shared__ uint32_t tmem_slot;
     __shared__ float row_unit[kM * kTile];  // 1 / (power of two that a row of Q was scaled by)
-    __shared__ float key_unit[4];           // the same of a key tile, tile i in i % 4
-    __shared__ float value_exp[4];          // log2 of the same of a value tile (bf16)
-    __shared__ __align__(16) uint8_t wild[4][32];         // bit t of byte l: token 4 l + t of tile i has a wild value scale
+    __shared__ float key_unit[kRing];       // the same of a key tile, tile i in i % kRing
+    __shared__ float value_exp[kRing];          // log2 of the same of a value tile
+    __shared__ float key_up[kRing], value_up[kRing];  // the powers of two themselves
+    __shared__ __align__(16) uint8_t wild[kRing][32];     // bit t of byte l: token 4 l + t of tile i has a wild value scale
+    __shared__ float half_max[2][S::kHalves][kM * kTile];  // f32: what the two threads of a row tell each other
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_sm = base;                             // [kM][pieces]
     uint8_t* k_sm = q_sm + kM * S::kOperand;          // [stages][pieces]
@@ -292,17 +279,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kRawSlots; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], S::kDecodeWarps);
+            mbar_init(&bar.raw_empty[i], kDecodeWarps + 1);  // and the examiner
+            mbar_init(&bar.exam[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.k_full[i], S::kDecodeWarps);
-            mbar_init(&bar.v_full[i], S::kDecodeWarps);
+            mbar_init(&bar.k_full[i], kDecodeWarps);
+            mbar_init(&bar.v_full[i], kDecodeWarps);
             mbar_init(&bar.k_empty[i], 1);
             mbar_init(&bar.v_empty[i], 1);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.p_full[i], 4 * S::kHalves);
             mbar_init(&bar.pv_done[i], 1);
-            mbar_init(&bar.o_free[i], 4);
+            mbar_init(&bar.o_free[i], 4 * S::kHalves);
         }
         fence_barrier_init();
     }
@@ -327,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const TileList tiles = tile_list(seen_len, max(pos_lo, 0), a.window, a.sinks);
     const int n_tiles = tiles.count;
 
-    if (warp == 12) {
+    if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -336,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // power of two that takes its largest value to 2^13 .. 2^14.
     const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll 1
-    for (int m = 0; m < kM; ++m) {
+    for (int m = 0; m < kM && threadIdx.x < 4 * kTile; ++m) {
         const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
         const int rr = row0 + m * kTile + row;
         const bool in = rr < n_rows;
@@ -363,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part == 0) row_unit[m * kTile + row] = pow2(-up);
 #pragma unroll
         for (int y = 0; y < kEach; ++y) {
-            // The order in which a word's quants unpack (decode_keys).
+            // The order in which a word's quants unpack (decode_block).
             const float v[8] = {x[y][0].x, x[y][0].z, x[y][0].y, x[y][0].w, x[y][1].x, x[y][1].z, x[y][1].y, x[y][1].w};
             uint32_t hw[4], lw[4];
 #pragma unroll
@@ -385,10 +373,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    if (warp < S::kSoftmaxWarps) {
+    if (warp < kSoftmaxWarps) {
         // ---- softmax: this thread's row
-        if (F32) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        const int m = warp >> 2;
+        if (F32) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+        // f32: the warps w and w + 4 share 32 rows, each has half of a tile's columns
+        // and half of the dims; bf16: they have a row tile each.
+        const int m = F32 ? 0 : warp >> 2, half = F32 ? warp >> 2 : 0;
+        constexpr int kChunks = 4 / S::kHalves;     // of 32 columns, this thread's of a tile
+        constexpr int kDims = D / S::kHalves;       // this thread's of the output
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const int row = 32 * (warp & 3) + lane;
         const int rr = row0 + m * kTile + row;
@@ -398,84 +390,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wr0 = row0 + m * kTile + 32 * (warp & 3);        // the warp's rows' extreme positions
         const int w_lo = base_pos + wr0 / group, w_hi = base_pos + (wr0 + 31) / group;
         const float unit = fabsf(a.scale) * kLog2e * row_unit[m * kTile + row];
-        const uint32_t t_o = tmem + lanes + kTmemO + m * 128;  // (bf16)
+        const uint32_t t_o = tmem + lanes + kTmemO + (F32 ? half * kDims : m * 128);
         float mx_used = -INFINITY, sum = 0.f;
-        float lowest = INFINITY;  // bf16: of the row's scores (with the value tile's exponent)
-        float o[F32 ? D : 1];
-        float keep_last = 0.f;  // f32: what the sums before the last tile's products are scaled by
+        float lowest = INFINITY;  // of the row's scores (with the value tile's exponent)
+        float o[F32 ? kDims : 1];
+        float keep_now = 0.f, keep_last = 0.f;  // f32: what a tile, and the one before it, scale the sums so far by
 #pragma unroll
-        for (int e = 0; e < (F32 ? D : 1); ++e) o[e] = 0.f;
+        for (int e = 0; e < (F32 ? kDims : 1); ++e) o[e] = 0.f;
         bool ok = true;
+        // f32: what the row's other thread has.
+        auto other = [&](float x, int buf) {
+            half_max[buf][half][row] = x;
+            named_barrier_sync(1 + (warp & 3), 64);
+            return half_max[buf][half ^ 1][row];
+        };
         // f32: o = o keep + P V of tile i.
-        auto collect = [&](int i) {
-            const int buf = i & 1;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[buf], (i >> 1) & 1, err));
+        auto collect = [&](int i, float keep) {
+            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[0], i & 1, err));
             if (!ok) return;
             tc_fence_after();
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                float v[32];
-                tmem_ld32(tmem + lanes + kTmemO + buf * 128 + 32 * q, v);
+            for (int q = 0; q < kDims / 32; ++q) {
+                float v[32], w[32];
+                tmem_ld32(t_o + 32 * q, v);
+                tmem_ld32(t_o + 128 + 32 * q, w);
                 tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[32 * q + e < (F32 ? D : 1) ? 32 * q + e : 0] =
-                    fmaf(o[32 * q + e < (F32 ? D : 1) ? 32 * q + e : 0], keep_last, v[e]);
+                for (int e = 0; e < 32; ++e) {
+                    float& y = o[F32 ? 32 * q + e : 0];
+                    y = fmaf(y, keep, fmaf(w[e], 1.f / kLowUp, v[e]));
+                }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.o_free[buf]);
+            if (lane == 0) mbar_arrive(&bar.o_free[0]);
         };
 #pragma unroll 1
         for (int i = 0; i < n_tiles; ++i) {
             const int buf = F32 ? (i & 1) : m;
-            const uint32_t t_s = tmem + lanes + buf * 128;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.s_full[buf], F32 ? (i >> 1) & 1 : i & 1, err));
-            if (!ok) break;
+            const uint32_t t_s = tmem + lanes + buf * 128 + half * 64;
+            // (After a wait that gave up, none is begun: the two warps of a row go on
+            // through their barriers to the end.)
+            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.s_full[buf], F32 ? (i >> 1) & 1 : i & 1, err));
             tc_fence_after();
             const int key0 = tiles.at(i) * kTile;
-            const float f = unit * key_unit[i & 3];
-            const float v_exp = F32 ? 0.f : value_exp[i & 3];
+            const float f = fmaxf(unit * key_unit[i % kRing], 0x1p-100f);  // (not 0: it meets -infinity)
+            const float v_exp = value_exp[i % kRing];
+            const uint8_t* wild_i = wild[i % kRing];
             bool any_wild;
             {
-                const uint4 w0 = *reinterpret_cast<const uint4*>(wild[i & 3]);
-                const uint4 w1 = *reinterpret_cast<const uint4*>(wild[i & 3] + 16);
+                const uint4 w0 = *reinterpret_cast<const uint4*>(wild_i);
+                const uint4 w1 = *reinterpret_cast<const uint4*>(wild_i + 16);
                 any_wild = (w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w) != 0;
             }
             const bool masked = any_wild || key0 + kTile > min(w_lo + 1, L) ||
                                 (a.window > 0 && key0 <= w_hi - a.window && key0 + kTile > a.sinks);
-            // Two passes over the row's scores in TMEM: its maximum, then P.  Token
-            // key0 + k counts as -infinity where the row does not see it, as NaN
-            // where it does and its values are not finite.
-            const int k_hi = min(pos, L - 1) - key0, k_lo = win_lo - key0, k_sink = a.sinks - key0;
-            auto tile = [&](auto kMask, auto kWild) {
-                auto sees = [&](int k) { return !kMask || (k <= k_hi && (k >= k_lo || k < k_sink)); };
-                auto score = [&](float s, int k) {
-                    if (kWild && ((wild[i & 3][k >> 2] >> (k & 3)) & 1)) s = NAN;
-                    return sees(k) ? s : -INFINITY;
-                };
-                float v[32];
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                float mn4[2] = {INFINITY, INFINITY};
+            // Tokens that the row does not see become -infinity, those that it sees
+            // and whose values are not finite NaN, in TMEM, where there are any.
+            const int k0 = key0 + half * 64;
+            float mn = INFINITY;
+            if (masked) {
+                const int k_end = min(pos, L - 1) + 1 - k0, k_lo = win_lo - k0, k_sink = a.sinks - k0;
+                auto below = [](int n) -> uint32_t { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kChunks; ++q) {
+                    const uint32_t sees = below(k_end - 32 * q) & (~below(k_lo - 32 * q) | below(k_sink - 32 * q));
+                    float v[32];
                     tmem_ld32(t_s + 32 * q, v);
                     tc_wait_ld();
+                    if (any_wild) {
+                        uint32_t bad = 0;
+#pragma unroll 1
+                        for (int y = 0; y < 8; ++y)
+                            bad |= static_cast<uint32_t>(wild_i[16 * half + 8 * q + y]) << (4 * y);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((bad >> e) & 1u) v[e] = NAN;
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        mx4[e & 3] = fmaxf(mx4[e & 3], score(v[e], 32 * q + e));
-                        if (!F32) mn4[e & 1] = fminf(mn4[e & 1], sees(32 * q + e) ? v[e] : INFINITY);
+                        if ((sees >> e) & 1u) mn = fminf(mn, v[e]);
+                        else v[e] = -INFINITY;
                     }
+                    tmem_st32(t_s + 32 * q, v);
                 }
-                const float mx = fmaf(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), f, v_exp);
-                float off;
+                tc_wait_st();
+            }
+            // Two passes over the row's scores: its maximum, then P.
+            {
+                float mx = -INFINITY, low = INFINITY;
+#pragma unroll 1
+                for (int q = 0; q < kChunks; ++q) {
+                    float v[32];
+                    tmem_ld32(t_s + 32 * q, v);
+                    tc_wait_ld();
+                    float mx2 = -INFINITY, low2 = INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        mx = fmaxf(fmaxf(mx, v[e]), v[e + 1]);
+                        mx2 = fmaxf(fmaxf(mx2, v[e + 2]), v[e + 3]);
+                        low = fminf(fminf(low, v[e]), v[e + 1]);
+                        low2 = fminf(fminf(low2, v[e + 2]), v[e + 3]);
+                    }
+                    mx = fmaxf(mx, mx2);
+                    low = fminf(low, low2);
+                }
+                if (!masked) mn = low;
+                lowest = fminf(lowest, fmaf(mn, f, v_exp));
+                mx = fmaf(mx, f, v_exp);
                 if (F32) {
-                    const float next = fmaxf(mx_used, mx);
-                    off = next == -INFINITY ? 0.f : next;
-                    keep_last = exp2_approx(mx_used - off);  // applied when this tile's products are collected
+                    const float next = fmaxf(mx_used, fmaxf(mx, other(mx, i & 1)));
+                    keep_now = exp2_approx(mx_used - (next == -INFINITY ? 0.f : next));
                     mx_used = next;
-                    sum *= keep_last;
+                    sum *= keep_now;
                 } else {
-                    lowest = fminf(lowest, fmaf(fminf(mn4[0], mn4[1]), f, v_exp));
                     // The maximum in use follows only where it is overtaken by 2^3.
                     const bool grow = mx > mx_used + kLazy;
                     if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -486,35 +514,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i > 0) {
 #pragma unroll 1
                             for (int q = 0; q < D / 32; ++q) {
-                                tmem_ld32(t_o + 32 * q, v);
+                                float w[32];
+                                tmem_ld32(t_o + 32 * q, w);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] *= keep;
-                                tmem_st32(t_o + 32 * q, v);
+                                for (int e = 0; e < 32; ++e) w[e] *= keep;
+                                tmem_st32(t_o + 32 * q, w);
                             }
                             tc_wait_st();
                         }
                     }
-                    off = (mx_used == -INFINITY ? 0.f : mx_used) - v_exp - kPTop;
                 }
+                const float off = (mx_used == -INFINITY ? 0.f : mx_used) - v_exp - kPTop<F32>;
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kChunks; ++q) {
+                    float v[32];
                     tmem_ld32(t_s + 32 * q, v);
                     tc_wait_ld();
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float p0 = exp2_approx(score(fmaf(v[e], f, -off), 32 * q + e));
-                        const float p1 = exp2_approx(score(fmaf(v[e + 1], f, -off), 32 * q + e + 1));
+                        const float p0 = exp2_approx(fmaf(v[e], f, -off));
+                        const float p1 = exp2_approx(fmaf(v[e + 1], f, -off));
                         part[e / 2 & 3] += p0 + p1;
+                        const __half2 hw = __floats2half2_rn(p0, p1);
+                        hi[e / 2] = word(hw);
                         if (F32) {
-                            const uint32_t w = word(__floats2bfloat162_rn(p0, p1));
-                            hi[e / 2] = w;
-                            lo[e / 2] = word(__floats2bfloat162_rn(p0 - __uint_as_float(w << 16),
-                                                                   p1 - __uint_as_float(w & 0xFFFF0000u)));
-                        } else {
-                            hi[e / 2] = word(__floats2half2_rn(p0, p1));
+                            const float2 back = __half22float2(hw);
+                            lo[e / 2] = word(__floats2half2_rn((p0 - back.x) * kLowUp, (p1 - back.y) * kLowUp));
                         }
                     }
                     if (F32) {
@@ -524,55 +552,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(t_s + 16 * q, hi);
                     }
                 }
-                const float all = (part[0] + part[1]) + (part[2] + part[3]);
-                sum += F32 ? all : all * exp2_approx(-v_exp);
-            };
-            const float keep_before = keep_last;
-            if (any_wild) tile(std::true_type(), std::true_type());
-            else if (masked) tile(std::true_type(), std::false_type());
-            else tile(std::false_type(), std::false_type());
+                sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), exp2_approx(-v_exp), sum);
+            }
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.p_full[buf]);
-            if (F32 && i > 0) {
-                const float keep_now = keep_last;
-                keep_last = keep_before;
-                collect(i - 1);
-                keep_last = keep_now;
-                if (!ok) break;
-            }
+            if (F32 && i > 0) collect(i - 1, keep_last);
+            keep_last = keep_now;
         }
-        if (ok && n_tiles > 0) {
-            if (F32) collect(n_tiles - 1);
-            else ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[m], (n_tiles - 1) & 1, err));
+        if (n_tiles > 0) {
+            if (F32) collect(n_tiles - 1, keep_last);
+            else if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[m], (n_tiles - 1) & 1, err));
         }
         tc_fence_after();
+        if (F32) {
+            sum += other(sum, n_tiles & 1);
+            lowest = fminf(lowest, other(lowest, (n_tiles + 1) & 1));
+        }
         // The output: columns in the order the quants unpack.
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t orow = first + (in ? rr / group : 0);
         const int head = h * group + (in ? rr % group : 0);
-        T* out = static_cast<T*>(a.out) + orow * a.out_stride + static_cast<int64_t>(head) * D;
+        T* out = static_cast<T*>(a.out) + orow * a.out_stride + static_cast<int64_t>(head) * D + half * kDims;
         float least = INFINITY;
-        auto store8 = [&](const float y[8], int q, int k) {
-            store_o4(out + 32 * q + 4 * k, make_float4(y[0], y[2], y[1], y[3]));
-            store_o4(out + 32 * q + 16 + 4 * k, make_float4(y[4], y[6], y[5], y[7]));
-        };
-        if (F32) {
-            if (in) {
+        auto store32 = [&](const float* v, int q) {
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q)
+            for (int k = 0; k < 4; ++k) {
+                float y[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int x = 32 * q + 8 * k + e;
-                            y[e] = sum == 0.f ? 0.f : o[x < (F32 ? D : 1) ? x : 0] * inv;
-                        }
-                        store8(y, q, k);
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    least = fminf(least, fabsf(v[8 * k + e]));
+                    y[e] = sum == 0.f ? 0.f : v[8 * k + e] * inv;
+                }
+                if (in) {
+                    store_o4(out + 32 * q + 4 * k, make_float4(y[0], y[2], y[1], y[3]));
+                    store_o4(out + 32 * q + 16 + 4 * k, make_float4(y[4], y[6], y[5], y[7]));
+                }
             }
+        };
+        if constexpr (F32) {
+#pragma unroll
+            for (int q = 0; q < kDims / 32; ++q) store32(o + 32 * q, q);
+            least = fminf(least, other(least, n_tiles & 1));
         } else {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -580,155 +602,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n_tiles > 0) {
                     tmem_ld32(t_o + 32 * q, v);
                     tc_wait_ld();
-                }
-                if (in) {
+                } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            least = fminf(least, fabsf(v[8 * k + e]));
-                            y[e] = sum == 0.f ? 0.f : v[8 * k + e] * inv;
-                        }
-                        store8(y, q, k);
-                    }
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 }
+                store32(v, q);
             }
         }
-        if (in) {
-            const float lse2 = sum == 0.f ? -INFINITY : mx_used + log2f(sum) - (F32 ? 0.f : kPTop);
+        if (in && half == 0) {
+            const float lse2 = sum == 0.f ? -INFINITY : mx_used + log2f(sum) - kPTop<F32>;
             if (a.lse) a.lse[orow * a.heads + head] = lse2 * kLn2;
             if (plan.lse2) plan.lse2[orow * a.heads + head] = lse2;
-            // Every P is off by at most 2^-25 where it is small, times a value of
-            // at most 2^6: could that be 2^-11 of some element?
-            if (!F32 && lowest < mx_used - kFarBelow && least < static_cast<float>(n_tiles) * (kTile * 0x1p-8f)) {
+            if (lowest < mx_used - kFarBelow<F32> && least < sqrtf(static_cast<float>(n_tiles * kTile)) * kSafe<F32>) {
                 const unsigned at = atomicAdd(plan.redo_n, 1u);  // (at most once per row)
                 plan.redo[at] = static_cast<unsigned>(orow * a.heads + head);
             }
         }
-    } else if (warp < S::kSoftmaxWarps + S::kDecodeWarps) {
+    } else if (warp < kSoftmaxWarps + kDecodeWarps) {
         // ---- decode: raw cells -> swizzled tiles; keys one tile ahead of values
-        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        const int dt = threadIdx.x - S::kSoftmaxWarps * 32;
-        const bool chief = dt < 32;  // this warp also writes what the softmax reads
+        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int dt = threadIdx.x - kSoftmaxWarps * 32;
         bool ok = true;
-        // Raw tiles come in the order they are used: keys 0, keys 1, values 0, keys 2, ...
+        // Raw tiles come in the order they are used: keys 0, keys 1, values 0, keys
+        // 2, ...; the scales of a tile have been looked at when `exam` says so.
         int slot = 0, round = 0;
-        float v_scale = 1.f, v_scale_next = 1.f;  // bf16: powers of two of a value tile and the next
-        auto next_slot = [&] {
-            if (++slot == S::kRawSlots) slot = 0, ++round;
-        };
-        auto keys = [&](int i) {
-            const int stage = i % S::kStages;
-            ok = __all_sync(0xFFFFFFFFu,
-                            mbar_wait_bounded(&bar.raw_full[slot], round & 1, err) &&
-                                (i < S::kStages || mbar_wait_bounded(&bar.k_empty[stage], (i / S::kStages - 1) & 1, err)));
-            if (!ok) return;
-            const uint8_t* rawk = raw + slot * S::kSlot;
-            const uint8_t* vsc = rawk + S::kRaw;
-            const int left = seen_len - tiles.at(i) * kTile;  // tokens of the tile that count
-            // The largest scales: lane l looks at tokens 4 l .. 4 l + 3.
-            uint32_t top = 0, top_v = 0, bad = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int tok = 4 * lane + u;
-                const uint8_t* sc = rawk + (tok >> 4) * cell_bytes(D) + cell_scales(D) + (tok & 15) * 2 * NB;
-                const uint8_t* sv = vsc + tok * 2 * NB;
-                bool wild_v = false;
-#pragma unroll
-                for (int e = 0; e < NB / 2; ++e) {
-                    const uint32_t x = reinterpret_cast<const uint32_t*>(sc)[e] & 0x7FFF7FFFu;
-                    const uint32_t v = reinterpret_cast<const uint32_t*>(sv)[e] & 0x7FFF7FFFu;
-                    const uint32_t x0 = x & 0xFFFFu, x1 = x >> 16, v0 = v & 0xFFFFu, v1 = v >> 16;
-                    if (tok < left) {
-                        if (x0 < 0x7C00u) top = max(top, x0);
-                        if (x1 < 0x7C00u) top = max(top, x1);
-                        if (v0 < 0x7C00u) top_v = max(top_v, v0);
-                        else wild_v = true;
-                        if (v1 < 0x7C00u) top_v = max(top_v, v1);
-                        else wild_v = true;
-                    }
-                }
-                if (wild_v) bad |= 1u << u;
-            }
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            const int up = 26 - max(1, static_cast<int>(top >> 10));  // largest scale to 2^11 .. 2^12
-            const float f = pow2(up);
-            int up_v = 0;
-            if (!F32) {
-                top_v = __reduce_max_sync(0xFFFFFFFFu, top_v);
-                up_v = 17 - max(1, static_cast<int>(top_v >> 10));  // to 2^2 .. 2^3
-                v_scale_next = pow2(up_v);
-            }
-            if (chief) {
-                wild[i & 3][lane] = static_cast<uint8_t>(bad);
-                if (lane == 0) {
-                    key_unit[i & 3] = pow2(-up);
-                    value_exp[i & 3] = static_cast<float>(-up_v);
-                }
-            }
-            uint8_t* hi = k_sm + stage * S::kOperand;
+        uint32_t exam_phase = 0;  // bit s: parity of the next exam of slot s
+        // One body for keys and values: the code of all roles together has to stay
+        // in the instruction cache.
 #pragma unroll 1
-            for (int y = 0; y < kTile * NB / (S::kDecodeWarps * 32); ++y) {
-                const int task = dt + y * S::kDecodeWarps * 32;
-                const int tok = task & (kTile - 1), blk = task / kTile;
-                const uint8_t* cell = rawk + (tok >> 4) * cell_bytes(D);
-                const uint4 q = *reinterpret_cast<const uint4*>(cell + blk * 256 + (tok & 15) * 16);
-                const float d = f16_bits_to_float(
-                    *reinterpret_cast<const uint16_t*>(cell + cell_scales(D) + ((tok & 15) * NB + blk) * 2));
-                decode_keys<F32>(q, d * f, tok, blk, hi, hi + S::kPiece, plan.k1024);
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.raw_empty[slot]);
-                mbar_arrive(&bar.k_full[stage]);
-            }
-            next_slot();
-        };
-        auto values = [&](int i) {
+        for (int step = 0; step < 2 * n_tiles; ++step) {
+            const bool v = step > 0 && ((step & 1) == 0 || step == 2 * n_tiles - 1);
+            const int i = v ? (step - 1) >> 1 : (step + 1) >> 1;
             const int stage = i % S::kStages;
-            ok = __all_sync(0xFFFFFFFFu,
-                            mbar_wait_bounded(&bar.raw_full[slot], round & 1, err) &&
-                                (i < S::kStages || mbar_wait_bounded(&bar.v_empty[stage], (i / S::kStages - 1) & 1, err)));
-            if (!ok) return;
-            const uint8_t* rawv = raw + slot * S::kSlot;
-            const int left = seen_len - tiles.at(i) * kTile;
-            uint8_t* hi = v_sm + stage * S::kOperand;
+            ok = mbar_wait_bounded(&bar.raw_full[slot], round & 1, err);
+            if (ok && !v) {
+                ok = mbar_wait_bounded(&bar.exam[slot], (exam_phase >> slot) & 1, err);
+                exam_phase ^= 1u << slot;
+            }
+            if (ok && i >= S::kStages)
+                ok = mbar_wait_bounded((v ? bar.v_empty : bar.k_empty) + stage, (i / S::kStages - 1) & 1, err);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            const uint8_t* cells = raw + slot * S::kSlot;
+            const int left = v ? seen_len - tiles.at(i) * kTile : kTile;
+            const float f = v ? value_up[i % kRing] : key_up[i % kRing];
+            uint8_t* hi = (v ? v_sm : k_sm) + stage * S::kOperand;
 #pragma unroll 1
-            for (int y = 0; y < kTile * NB / (S::kDecodeWarps * 32); ++y) {
-                const int task = dt + y * S::kDecodeWarps * 32;
+            for (int y = 0; y < kTile * NB / (kDecodeWarps * 32); ++y) {
+                const int task = dt + y * kDecodeWarps * 32;
                 const int tok = task & (kTile - 1), blk = task / kTile;
-                const uint8_t* cell = rawv + (tok >> 4) * cell_bytes(D);
+                const uint8_t* cell = cells + (tok >> 4) * cell_bytes(D);
                 const uint4 q = *reinterpret_cast<const uint4*>(cell + blk * 256 + (tok & 15) * 16);
                 const uint32_t bits =
                     *reinterpret_cast<const uint16_t*>(cell + cell_scales(D) + ((tok & 15) * NB + blk) * 2);
-                // Past the end, or not finite (NaN then comes with the scores): 0.
-                const float d = tok >= left || (bits & 0x7C00u) == 0x7C00u ? 0.f : f16_bits_to_float(bits);
-                if (F32) decode_values(q, d, tok, blk, hi, hi + S::kPiece, plan.k128);
-                else decode_keys<false>(q, d * v_scale, tok, blk, hi, hi, plan.k1024);
+                // Values past the end, or not finite (NaN then comes with the scores): 0.
+                const float d = tok >= left || (v && (bits & 0x7C00u) == 0x7C00u) ? 0.f : f16_bits_to_float(bits);
+                decode_block<F32>(q, d * f, tok, blk, hi, hi + S::kPiece, plan.k1024);
             }
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&bar.raw_empty[slot]);
-                mbar_arrive(&bar.v_full[stage]);
+                mbar_arrive((v ? bar.v_full : bar.k_full) + stage);
             }
-            next_slot();
-        };
-        // (Twice through one loop body, so that its code is there once.)
-#pragma unroll 1
-        for (int i = -1; i < n_tiles && ok; ++i) {
-            v_scale = v_scale_next;
-            if (i + 1 < n_tiles) keys(i + 1);
-            if (ok && i >= 0) values(i);
+            if (++slot == S::kRawSlots) slot = 0, ++round;
         }
     } else {
-        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12) {
+        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 16) {
         // ---- MMA issue
         if (lane == 0 && n_tiles > 0) {
-            constexpr uint32_t id_s = idesc(0, kTile, false), id_o = idesc(F32 ? 1 : 0, D, true);
+            constexpr uint32_t id_s = idesc(0, kTile, false), id_o = idesc(0, D, true);
             bool ok = true;
             auto scores = [&](int i, int m) {
                 const int stage = i % S::kStages;
@@ -756,44 +699,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && mbar_wait_bounded(&bar.p_full[buf], F32 ? (i >> 1) & 1 : i & 1, err) &&
                      mbar_wait_bounded(&bar.v_full[stage], (i / S::kStages) & 1, err);
                 if (!ok) return;
-                // f32: the buffer's last products have been collected.
-                if (F32 && i > 1) ok = mbar_wait_bounded(&bar.o_free[buf], ((i >> 1) - 1) & 1, err);
+                // f32: the products of the tile before have been collected.
+                if (F32 && i > 0) ok = mbar_wait_bounded(&bar.o_free[0], (i - 1) & 1, err);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t t_o = tmem + kTmemO + buf * 128;
                 const uint32_t v0 = smem_addr(v_sm + stage * S::kOperand);
-                constexpr int kProducts = S::kPieces * S::kPieces;  // low x low first, high x high last
+                constexpr int kProducts = F32 ? 3 : 1;  // low x high apart, high x low, high x high
 #pragma unroll 1
-                for (int p = kProducts - 1; p >= 0; --p) {
-                    const uint32_t t_p = tmem + buf * 128 + ((p >> 1) ? 16 : 0);
+                for (int p = 0; p < kProducts; ++p) {
+                    const uint32_t t_p = tmem + buf * 128 + (F32 && p == 0 ? 16 : 0);
+                    const uint32_t t_o = tmem + kTmemO + (F32 ? (p == 0 ? 128 : 0) : m * 128);
                     // V is [token][dim]: rows are the contraction, 64-dim columns kTile * 128 bytes apart.
-                    const uint64_t db = desc_base(v0 + ((p & 1) ? S::kPiece : 0), kTile * 128);
+                    const uint64_t db = desc_base(v0 + (F32 && p == 1 ? S::kPiece : 0), kTile * 128);
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         mma_ts(t_o, t_p + (F32 ? (kk >> 1) * 32 + (kk & 1) * 8 : 8 * kk),
                                db + (static_cast<uint64_t>(kk * 16 * 128) >> 4), id_o,
-                               (F32 ? (kProducts - 1 - p) | kk : i | kk) != 0);
+                               (F32 ? (p == 2) | kk : i | kk) != 0);
                 }
-                mma_commit(&bar.pv_done[buf]);
+                mma_commit(&bar.pv_done[m]);
                 if (m == kM - 1) mma_commit(&bar.v_empty[stage]);
             };
             if (F32) {
-                scores(0, 0);
-                for (int i = 0; i < n_tiles && ok; ++i) {
+#pragma unroll 1
+                for (int i = -1; i < n_tiles && ok; ++i) {
                     if (i + 1 < n_tiles) scores(i + 1, 0);
-                    output(i, 0);
+                    if (i >= 0) output(i, 0);
                 }
             } else {
-                for (int m = 0; m < kM; ++m) scores(0, m);
-                for (int i = 0; i < n_tiles && ok; ++i) {
-                    for (int m = 0; m < kM; ++m) {
-                        output(i, m);
-                        if (i + 1 < n_tiles) scores(i + 1, m);
-                    }
+#pragma unroll 1
+                for (int x = -kM; x < kM * n_tiles && ok; ++x) {  // x = kM i + m
+                    const int i = (x + kM) / kM - 1, m = (x + kM) % kM;
+                    if (i >= 0) output(i, m);
+                    if (i + 1 < n_tiles) scores(i + 1, m);
                 }
             }
         }
-    } else if (warp == 13) {
+    } else if (warp == 17) {
         // ---- loader: lanes 0 .. 7 a cell of the tile each (the first of a page's
         // run copies it whole), lanes 8 .. 15 the scales of a cell of values.
         const int run = min(8, 1 << (c.page_shift - 4));
@@ -825,13 +767,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (++slot == S::kRawSlots) slot = 0, ++round;
         };
-        int64_t off = -1, off_next = cell_at(0);  // tile i's, tile i + 1's
+        // In the order of use: keys 0, keys 1, values 0, keys 2, ..., values n - 1.
+        int64_t off = -1, off_next = cell_at(0);  // of the tile whose values are next, and of the one after
 #pragma unroll 1
-        for (int i = -1; i < n_tiles && ok; ++i) {
-            if (i + 1 < n_tiles) fetch(i + 1, false, off_next);
-            if (ok && i >= 0) fetch(i, true, off);
-            off = off_next;
-            off_next = cell_at(i + 2);
+        for (int step = 0; step < 2 * n_tiles && ok; ++step) {
+            const bool v = step > 0 && ((step & 1) == 0 || step == 2 * n_tiles - 1);
+            const int i = v ? (step - 1) >> 1 : (step + 1) >> 1;
+            fetch(i, v, v ? off : off_next);
+            if (v || step == 0) {
+                off = off_next;
+                off_next = cell_at(i + (v ? 2 : 1));
+            }
+        }
+    } else if (warp == 18) {
+        // ---- examiner: what the decode warps and the softmax need to know of a
+        // tile's scales.  Lane l looks at tokens 4 l .. 4 l + 3.  It follows the
+        // whole sequence of raw tiles and frees every slot too (else a slot's
+        // barrier could run past the phase that it waits for).
+        bool ok = true;
+        int slot = 0, round = 0;
+        auto pass = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.raw_empty[slot]);
+            if (++slot == S::kRawSlots) slot = 0, ++round;
+        };
+#pragma unroll 1
+        for (int i = 0; i < n_tiles && ok; ++i) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_full[slot], round & 1, err));
+            if (!ok) break;
+            const uint8_t* rawk = raw + slot * S::kSlot;
+            const int left = seen_len - tiles.at(i) * kTile;  // tokens of the tile that count
+            uint32_t top = 0, top_v = 0, bad = 0;
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {
+                const int tok = 4 * lane + u;
+                const uint8_t* sc = rawk + (lane >> 2) * cell_bytes(D) + cell_scales(D) + (tok & 15) * 2 * NB;
+                const uint8_t* sv = rawk + S::kRaw + tok * 2 * NB;
+#pragma unroll
+                for (int e = 0; e < NB; ++e) {
+                    const uint32_t x = reinterpret_cast<const uint16_t*>(sc)[e] & 0x7FFFu;
+                    const uint32_t v = reinterpret_cast<const uint16_t*>(sv)[e] & 0x7FFFu;
+                    if (tok < left && x < 0x7C00u) top = max(top, x);
+                    if (tok < left && v < 0x7C00u) top_v = max(top_v, v);
+                    if (tok < left && v >= 0x7C00u) bad |= 1u << u;
+                }
+            }
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            top_v = __reduce_max_sync(0xFFFFFFFFu, top_v);
+            wild[i % kRing][lane] = static_cast<uint8_t>(bad);
+            if (lane == 0) {
+                const int up = 26 - max(1, static_cast<int>(top >> 10));      // largest scale to 2^11 .. 2^12
+                const int up_v = 17 - max(1, static_cast<int>(top_v >> 10));  // to 2^2 .. 2^3
+                key_up[i % kRing] = pow2(up);
+                key_unit[i % kRing] = pow2(-up);
+                value_up[i % kRing] = pow2(up_v);
+                value_exp[i % kRing] = static_cast<float>(-up_v);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.exam[slot]);
+            pass();
+            if (i > 0 || n_tiles == 1) {  // values of the tile before (or of the only one)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_full[slot], round & 1, err));
+                if (ok) pass();
+            }
+        }
+        if (ok && n_tiles > 1) {  // the last values
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_full[slot], round & 1, err));
+            if (ok) pass();
         }
     }
     }
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) {
+    if (warp == 16) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
@@ -855,7 +857,6 @@ cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, f
     PromptPlan p = {};
     p.items_per_list = static_cast<int>((rows + S::kM * kTile - 1) / (S::kM * kTile));
     p.k1024 = 0x64006400u;
-    p.k128 = 0x43004300u;
     p.lse2 = lse2;
     p.redo_n = redo_n;
     p.redo = redo;

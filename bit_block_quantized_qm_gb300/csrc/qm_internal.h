@@ -209,7 +209,7 @@ cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a
 cudaError_t attn_step_read_device_error(unsigned int* bits, bool clear);
 
 // Many rows (attn_prompt.cu): head dimensions 64 and 128.  lse2, when not null,
-// gets [n_tokens][heads] logarithms to base 2 of the sums.  bf16 rows: redo
+// gets [n_tokens][heads] logarithms to base 2 of the sums.  redo
 // (n_tokens * heads words) gets the (row * heads + head) that the plain kernel
 // is to do again, *redo_n (zero before) their number.
 bool attn_prompt_takes(const KvView& c);
