@@ -22,8 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqm.so")
 SOURCES = ("qm_api.cu", "dequant.cu", "q8_0.cu", "gemv.cu", "gemv_tc.cu", "gemv_list.cu", "gemv_q8act.cu", "gemm.cu",
-           "gemm_tc.cu", "kv_api.cu", "kv_cache.cu", "attn.cu", "attn_step.cu", "attn_prompt.cu")
-HEADERS = ("qm_device.cuh", "qm_internal.h", "qm_checks.h", "kv_cache.cuh")
+           "gemm_tc.cu", "kv_api.cu", "kv_cache.cu", "attn.cu", "attn_step.cu", "attn_prompt.cu", "attn_weights.cu")
+HEADERS = ("qm_device.cuh", "qm_internal.h", "qm_checks.h", "kv_cache.cuh", "tcgen05.cuh")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]

@@ -12,13 +12,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-// The workspace: 4 KB that are zero between calls (the step kernel's counters,
-// and last the number of rows to be done again); then such rows' list, and
-// logarithms to base 2.
-constexpr int64_t kRedoCount = 4080, kRedoOff = 4096;
+// Of the workspace's first 4 KB, zero between calls, the step kernel has all but
+// the last 16 bytes; there is the number of the rows to be done again.
+constexpr int64_t kRedoCount = 4080;
 constexpr float kLn2 = 0.6931471805599453f;
-
-int64_t lse_off(int64_t n_tokens, int heads) { return kRedoOff + (n_tokens * heads * 4 + 255) / 256 * 256; }
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -203,25 +200,46 @@ __global__ void __launch_bounds__(kWarps * 32) attn_weights_plain_kernel(KvView 
     }
 }
 
+// The workspace of calls that the step kernel does not take: 4 KB that are zero
+// between calls; the rows to be done again; with weights, logarithms to base 2
+// and (head dimensions of the prompt kernel) the queries' tiles and units.
+struct Room {
+    int64_t redo = 4096, lse = 0, units = 0, images = 0, bytes = 0, per_head = 0;
+};
+Room room_of(const KvView& c, int heads, int64_t n_tokens, bool weights) {
+    Room m;
+    const bool tiles = attn_prompt_takes(c);
+    auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    m.lse = m.redo + (tiles ? up(n_tokens * heads * 4) : 0);
+    m.units = m.lse + (weights ? up(n_tokens * heads * 4) : 0);
+    m.per_head = query_tiles_per_head(n_tokens, heads / c.heads, c.n_seqs);
+    m.images = m.units + (weights && tiles ? up(c.heads * m.per_head * 128 * 4) : 0);
+    m.bytes = m.images + (weights && tiles ? c.heads * m.per_head * 128 * 4 * c.dim : 0);
+    if (!tiles && !weights) m.bytes = 0;
+    return m;
+}
+
 template <int NB, typename T>
 cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
-    float* lse = a.weights ? reinterpret_cast<float*>(a.ws + lse_off(r.n_tokens, a.heads)) : nullptr;  // to base 2
-    const int64_t items = static_cast<int64_t>(r.n_tokens) * a.heads;
+    const Room m = room_of(c, a.heads, r.n_tokens, a.weights != nullptr);
+    float* lse = a.weights ? reinterpret_cast<float*>(a.ws + m.lse) : nullptr;  // to base 2
     cudaError_t err;
     if (attn_prompt_takes(c)) {
         unsigned* redo_n = reinterpret_cast<unsigned*>(a.ws + kRedoCount);
-        unsigned* redo = reinterpret_cast<unsigned*>(a.ws + kRedoOff);
-        err = launch_attn_prompt(c, r, a, lse, redo_n, redo, stream);
-        if (err == cudaSuccess) {
-            note_launch();
-            err = launch_pdl(attn_redo_kernel<NB, T>, dim3(152), dim3(kRedoWarps * 32), 0, stream, c, r, a, lse, redo_n,
-                             redo);
-        }
-    } else {
+        unsigned* redo = reinterpret_cast<unsigned*>(a.ws + m.redo);
+        const QueryTiles qt = {a.weights ? a.ws + m.images : nullptr, reinterpret_cast<float*>(a.ws + m.units), m.per_head};
+        err = launch_attn_prompt(c, r, a, lse, qt, redo_n, redo, stream);
+        if (err != cudaSuccess) return err;
         note_launch();
-        err = launch_pdl(attn_plain_kernel<NB, T>, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)),
-                         dim3(kWarps * 32), 0, stream, c, r, a, lse);
+        err = launch_pdl(attn_redo_kernel<NB, T>, dim3(152), dim3(kRedoWarps * 32), 0, stream, c, r, a, lse, redo_n,
+                         static_cast<const unsigned*>(redo));
+        if (err != cudaSuccess || !a.weights) return err;
+        return launch_attn_weights(c, r, a, qt, lse, stream);
     }
+    const int64_t items = static_cast<int64_t>(r.n_tokens) * a.heads;
+    note_launch();
+    err = launch_pdl(attn_plain_kernel<NB, T>, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)),
+                     dim3(kWarps * 32), 0, stream, c, r, a, lse);
     if (err != cudaSuccess || !a.weights || c.max_len == 0) return err;
     note_launch();
     return launch_pdl(attn_weights_plain_kernel<NB, T>,
@@ -239,7 +257,7 @@ cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cu
 
 int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {
     if (attn_step_takes(c, heads, max_q)) return attn_step_workspace(c, heads, n_tokens, max_q, weights);
-    return attn_prompt_takes(c) || weights ? lse_off(n_tokens, heads) + (weights ? n_tokens * heads * 4 : 0) : 0;
+    return room_of(c, heads, n_tokens, weights).bytes;
 }
 
 cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,

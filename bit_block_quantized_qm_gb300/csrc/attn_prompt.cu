@@ -45,7 +45,7 @@
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include <algorithm>
 
-#include "kv_cache.cuh"
+#include "tcgen05.cuh"
 
 namespace qm {
 
@@ -54,7 +54,6 @@ __device__ unsigned int g_attn_prompt_error = 0;
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kTile = 128;  // rows of a row tile, tokens of a token tile
 constexpr int kSoftmaxWarps = 8, kDecodeWarps = 8;  // then MMA issue, loader, examiner, an idle one
 constexpr int kRing = 8;    // tiles whose scale factors are kept
 constexpr float kLog2e = 1.4426950408889634f;
@@ -95,104 +94,6 @@ template <bool F32>
 constexpr float kSafe = F32 ? 0x1p-10f : 0x1p-6f;
 constexpr float kLowUp = 2048.f;  // f32: what P's second piece is scaled by
 
-__device__ __forceinline__ uint64_t desc_base(uint32_t saddr, uint32_t lbo) {
-    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(lbo >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;  // 8 rows of 128 bytes
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;  // 128-byte swizzle
-    return d;
-}
-
-// D f32; both operands f16 (type 0) or bf16 (1); M = 128.
-constexpr uint32_t idesc(int type, int n, bool b_mn_major) {
-    return (1u << 4) | (static_cast<uint32_t>(type) << 7) | (static_cast<uint32_t>(type) << 10) |
-           (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc));
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float v[32]) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float v[32]) {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t r[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-__device__ __forceinline__ uint32_t word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-__device__ __forceinline__ uint32_t word(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
-
-__device__ __forceinline__ float4 load_q4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load_q4(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xFFFF0000u));
-}
-__device__ __forceinline__ void store_o4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store_o4(__nv_bfloat16* p, float4 v) {
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(word(__floats2bfloat162_rn(v.x, v.y)), word(__floats2bfloat162_rn(v.z, v.w)));
-}
-
-// Byte offset of 16-byte chunk `chunk` (of 8 elements; D / 8 of them) of row
-// `row` in a piece of a tile: 64-element columns of [128 rows][128 bytes], the
-// chunks of a row permuted by row % 8.
-__device__ __forceinline__ int tile_off(int row, int chunk) {
-    return (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-}
-
 // Token tiles that rows at positions pos_lo .. pos_hi read.
 struct TileList {
     int n1, t2, count;
@@ -210,38 +111,11 @@ __device__ __forceinline__ TileList tile_list(int seen_len, int pos_lo, int wind
     return t;
 }
 
-// One block of a token: 16 quant bytes and the tile-scaled f16 d -> four chunks of
-// 8, each word's quants in the order they unpack, (n - 8) d rounded to f16 and
-// (f32 rows) the exact rest.
-template <bool F32>
-__device__ __forceinline__ void decode_block(uint4 q, float d, int row, int blk, uint8_t* hi, uint8_t* lo, uint32_t k1024) {
-    const __half2 dd = __float2half2_rn(d);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t y = w[k] >> 8;
-        const __half2 m1032 = half2_of(0xE408E408u), sixteenth = half2_of(0x2C002C00u), m72 = half2_of(0xD480D480u);
-        const __half2 n[4] = {__hadd2(half2_of((w[k] & 0x000F000Fu) | k1024), m1032),
-                              __hadd2(half2_of((y & 0x000F000Fu) | k1024), m1032),
-                              __hfma2(half2_of((w[k] & 0x00F000F0u) | k1024), sixteenth, m72),
-                              __hfma2(half2_of((y & 0x00F000F0u) | k1024), sixteenth, m72)};
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __half2 x = __hmul2(n[e], dd);
-            h[e] = word(x);
-            if (F32) l[e] = word(__hfma2(n[e], dd, __hneg2(x)));
-        }
-        const int off = tile_off(row, 4 * blk + k);
-        *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (F32) *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-}
-
 struct PromptPlan {
     int items_per_list;  // row tiles (or pairs of them) of a (sequence, kv head) at most
     uint32_t k1024;      // two f16 1024, kept from the compiler (see attn_step.cu)
     float* lse2;         // logarithms to base 2 for the weights, or null
+    QueryTiles q;        // where the queries' pieces go, if they are wanted
     unsigned* redo_n;    // how many rows are listed to be done again,
     unsigned* redo;      // and which: row * heads + head
 };
@@ -372,6 +246,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    if (plan.q.images) {
+        const int64_t tile = query_tile(plan.q, h, first, b, group) + item * kM;
+        if (threadIdx.x == 0) bulk_store_1d(plan.q.images + tile * S::kOperand, q_sm, kM * S::kOperand);
+        if (threadIdx.x < kM * kTile)
+            plan.q.units[tile * kTile + threadIdx.x] = fabsf(a.scale) * kLog2e * row_unit[threadIdx.x];
+    }
 
     if (warp < kSoftmaxWarps) {
         // ---- softmax: this thread's row
@@ -671,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 16) {
         // ---- MMA issue
         if (lane == 0 && n_tiles > 0) {
-            constexpr uint32_t id_s = idesc(0, kTile, false), id_o = idesc(0, D, true);
+            constexpr uint32_t id_s = idesc_f16(kTile, false), id_o = idesc_f16(D, true);
             bool ok = true;
             auto scores = [&](int i, int m) {
                 const int stage = i % S::kStages;
@@ -838,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     }
 
+    if (plan.q.images && threadIdx.x == 0) bulk_store_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -847,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool F32, typename T>
-cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, unsigned* redo_n, unsigned* redo,
-                          cudaStream_t stream) {
+cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, const QueryTiles& qt,
+                          unsigned* redo_n, unsigned* redo, cudaStream_t stream) {
     using S = Shape<D, F32>;
     static SmemOnce once;
     cudaError_t err = once.set(attn_prompt_kernel<D, F32, T>, S::kSmem);
@@ -858,6 +739,7 @@ cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, f
     p.items_per_list = static_cast<int>((rows + S::kM * kTile - 1) / (S::kM * kTile));
     p.k1024 = 0x64006400u;
     p.lse2 = lse2;
+    p.q = qt;
     p.redo_n = redo_n;
     p.redo = redo;
     const int64_t grid = static_cast<int64_t>(p.items_per_list) * c.n_seqs * c.heads;
@@ -871,13 +753,13 @@ cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, f
 
 bool attn_prompt_takes(const KvView& c) { return c.dim == 64 || c.dim == 128; }
 
-cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, unsigned* redo_n, unsigned* redo,
-                               cudaStream_t stream) {
+cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, const QueryTiles& qt,
+                               unsigned* redo_n, unsigned* redo, cudaStream_t stream) {
     if (c.dim == 64)
-        return a.type == KvType::kF32 ? launch_prompt<64, true, float>(c, r, a, lse2, redo_n, redo, stream)
-                                      : launch_prompt<64, false, __nv_bfloat16>(c, r, a, lse2, redo_n, redo, stream);
-    return a.type == KvType::kF32 ? launch_prompt<128, true, float>(c, r, a, lse2, redo_n, redo, stream)
-                                  : launch_prompt<128, false, __nv_bfloat16>(c, r, a, lse2, redo_n, redo, stream);
+        return a.type == KvType::kF32 ? launch_prompt<64, true, float>(c, r, a, lse2, qt, redo_n, redo, stream)
+                                      : launch_prompt<64, false, __nv_bfloat16>(c, r, a, lse2, qt, redo_n, redo, stream);
+    return a.type == KvType::kF32 ? launch_prompt<128, true, float>(c, r, a, lse2, qt, redo_n, redo, stream)
+                                  : launch_prompt<128, false, __nv_bfloat16>(c, r, a, lse2, qt, redo_n, redo, stream);
 }
 
 cudaError_t attn_prompt_read_device_error(unsigned int* bits, bool clear) {

@@ -213,8 +213,30 @@ cudaError_t attn_step_read_device_error(unsigned int* bits, bool clear);
 // (n_tokens * heads words) gets the (row * heads + head) that the plain kernel
 // is to do again, *redo_n (zero before) their number.
 bool attn_prompt_takes(const KvView& c);
-cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, unsigned* redo_n, unsigned* redo,
-                               cudaStream_t stream);
+
+// The queries as the prompt kernel multiplies them, for attn_weights.cu (images
+// null: not wanted): tiles of 128 rows of a (sequence, kv head), f16 pieces in
+// swizzled operand layout, and for each row |scale| log2 e over the power of two
+// it was scaled by.  per_head tiles are set aside for each kv head.
+struct QueryTiles {
+    uint8_t* images;
+    float* units;
+    int64_t per_head;
+};
+// Tiles that n_tokens rows in n_seqs sequences need at most.
+inline int64_t query_tiles_per_head(int64_t n_tokens, int group, int n_seqs) {
+    return n_tokens * group / 128 + 2 * static_cast<int64_t>(n_seqs) + 2;
+}
+// The first tile of sequence b's rows from `first` on.  A sequence of n rows
+// times query heads has at most n / 128 + 2 (whole pairs), so none overlap.
+__host__ __device__ inline int64_t query_tile(const QueryTiles& t, int h, int first, int b, int group) {
+    return h * t.per_head + static_cast<int64_t>(first) * group / 128 + 2 * static_cast<int64_t>(b);
+}
+cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall& a, float* lse2, const QueryTiles& qt,
+                               unsigned* redo_n, unsigned* redo, cudaStream_t stream);
+cudaError_t launch_attn_weights(const KvView& c, const KvRows& r, const AttnCall& a, const QueryTiles& qt,
+                                const float* lse2, cudaStream_t stream);
+cudaError_t attn_weights_read_device_error(unsigned int* bits, bool clear);
 cudaError_t attn_prompt_read_device_error(unsigned int* bits, bool clear);
 
 // Opts a kernel into `bytes` of dynamic shared memory, once per device: one
