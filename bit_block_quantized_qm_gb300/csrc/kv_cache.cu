@@ -12,136 +12,185 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+__device__ __forceinline__ void load8(const float* p, float x[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+// (8-byte aligned)
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float x[8]) {
+    const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
 }
 
-// Q4_0 quantization of a block of 32 by 8 lanes of 4 elements each: m = the
-// first element of largest magnitude, d = m / -8, r = 1 / d (both correctly
-// rounded f32 divisions), q = min(15, floor(x r + 8.5)) with the product and
-// the sum each rounded to f32; the stored scale is d narrowed to binary16.
-// With m mapped to q = 0 the other sign gets only 7 steps: taking the signed
-// maximum gives the larger side the extra one.  NaN elements do not raise the
-// maximum; q = 8 (the value 0) where x r is NaN or d is 0.
-// Returns the four quants as bytes (element 4 i + e in byte e); *scale = d's bits.
-__device__ __forceinline__ uint32_t quantize_q4_lane(float4 x4, int i, uint32_t* scale) {
-    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-    float amax = 0.f;
+// Q4_0 quantization of a block of 32 by 4 lanes of 8 elements each (i: the lane's
+// number in the block): m = the first element of largest magnitude, d = m / -8,
+// r = 1 / d (both correctly rounded f32 divisions), q = min(15, floor(x r + 8.5))
+// with the product and the sum each rounded to f32; the stored scale is d
+// narrowed to binary16.  With m mapped to q = 0 the other sign gets only 7 steps:
+// taking the signed maximum gives the larger side the extra one.  NaN elements
+// do not raise the maximum; q = 8 (the value 0) where x r is NaN or d is 0.
+// Returns the eight quants as bytes; *scale = d's bits.
+__device__ __forceinline__ uint2 quantize_q4_lane(const float x[8], int i, uint32_t* scale) {
+    float hi = 0.f, lo = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    for (int e = 0; e < 8; e += 2) {
+        hi = fmaxf(fmaxf(hi, x[e]), x[e + 1]);
+        lo = fminf(fminf(lo, x[e]), x[e + 1]);
+    }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    // Sign of the first element of that magnitude: the smallest 2 * index + sign.
-    uint32_t at = 0x7FFFFFFFu;
+    for (int o = 1; o < 4; o <<= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    }
+    float m = hi > -lo ? hi : lo;
+    if (__any_sync(0xFFFFFFFFu, hi == -lo && hi > 0.f)) {  // both signs: the first one counts
+        uint32_t at = 0x7FFFFFFFu;  // smallest 2 * index + sign
 #pragma unroll
-    for (int e = 3; e >= 0; --e)
-        if (fabsf(x[e]) == amax) at = 2u * (4 * i + e) + (__float_as_uint(x[e]) >> 31);
+        for (int e = 7; e >= 0; --e)
+            if (fabsf(x[e]) == hi) at = 2u * (8 * i + e) + (__float_as_uint(x[e]) >> 31);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) at = min(at, __shfl_xor_sync(0xFFFFFFFFu, at, o));
-    const float m = (at & 1u) ? -amax : amax;
+        for (int o = 1; o < 4; o <<= 1) at = min(at, __shfl_xor_sync(0xFFFFFFFFu, at, o));
+        if (hi == -lo && !(at & 1u)) m = hi;
+    }
     const float d = __fdiv_rn(m, -8.f);
     const float r = d == 0.f ? 0.f : __frcp_rn(d);
     *scale = f16_bits_rn(d);
-    uint32_t w = 0;
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float t = floorf(__fadd_rn(__fmul_rn(x[e], r), 8.5f));
-        const uint32_t q = isnan(t) ? 8u : static_cast<uint32_t>(fminf(fmaxf(t, 0.f), 15.f));
-        w |= q << (8 * e);
+    for (int e = 0; e < 8; ++e) {
+        float t = __fadd_rn(__fmul_rn(x[e], r), 8.5f);
+        t = t == t ? fminf(fmaxf(t, 0.f), 15.5f) : 8.5f;
+        // Adding 2^23 toward zero leaves floor(t) in the low bits.
+        w[e >> 2] |= (__float_as_uint(__fadd_rz(t, 8388608.f)) & 15u) << (8 * (e & 3));
     }
-    return w;
+    return make_uint2(w[0], w[1]);
 }
 
-// One lane per 4 elements of a key or value row, 8 lanes per block; the lanes
-// of a warp run over the blocks of a row, then the kv heads, then K and V.
-// Memory-bound: 4 (or 2) bytes read and 9/16 written per element.
-template <typename T>
+// How the rows of a call go to warps: eight blocks at a time, i.e. one kv head of
+// kTokens consecutive rows; a warp takes `heads_each` heads of them, of keys or of
+// values, one after another.  Lane 4 s + i has elements 8 i .. 8 i + 7 of block
+// s % NB of row s / NB.
+template <int NB>
+struct RowWork {
+    static constexpr int kTokens = 8 / NB;
+    int row, blk, i, h_first, h_end, pos;
+    bool is_v, in;         // `in`: this lane has a row with a place in the cache
+    int64_t cell0, h_step;  // byte offset of its cell of head 0, and from head to head
+    __device__ RowWork(const KvView& c, const KvRows& r, int heads_each, unsigned int* err) {
+        const int lane = threadIdx.x & 31;
+        const int parts = (c.heads + heads_each - 1) / heads_each;
+        const unsigned unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+        const unsigned group = unit / (2 * parts);
+        const int rest = static_cast<int>(unit - group * 2 * parts);
+        is_v = rest >= parts;
+        h_first = (is_v ? rest - parts : rest) * heads_each;
+        h_end = min(c.heads, h_first + heads_each);
+        const int s = lane >> 2;
+        i = lane & 3;
+        blk = s % NB;
+        const int64_t at = static_cast<int64_t>(group) * kTokens + s / NB;
+        in = s / NB < kTokens && at < r.n_tokens;
+        row = in ? static_cast<int>(at) : 0;
+        pos = 0;
+        cell0 = h_step = 0;
+        if (!in) return;
+        const int b = kv_seq_of_row(r, c.n_seqs, row);
+        in = b >= 0;
+        if (!in) return;
+        int first, count;
+        kv_rows(r, b, &first, &count, err);
+        pos = kv_length(c, b, err) - count + (row - first);
+        if (row - first >= count || pos < 0) {
+            atomicOr(err, kErrRange);
+            in = false;
+            return;
+        }
+        cell0 = kv_cell(c, b, 0, pos, err);
+        in = cell0 >= 0;
+        h_step = static_cast<int64_t>(1 << (c.page_shift - 4)) * cell_bytes(32 * NB);
+    }
+};
+
+// Memory-bound: 4 (or 2) bytes read and 9/16 written per element; about 100
+// instructions per 8 elements of a lane.
+template <int NB, typename T>
 __global__ void __launch_bounds__(kThreads)
-    kv_append_kernel(KvView c, KvRows r, const T* k, const T* v, int64_t k_stride, int64_t v_stride, int64_t n4) {
+    kv_append_kernel(KvView c, KvRows r, const T* k, const T* v, int64_t k_stride, int64_t v_stride, int heads_each) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const bool in = t < n4;  // n4 is a multiple of 8: whole blocks
-    const int per_row = c.heads * c.dim / 4;  // lanes of one token's K (or V)
-    const int64_t tt = in ? t : 0;
-    const int row = static_cast<int>(tt / (2 * per_row));
-    int rest = static_cast<int>(tt - static_cast<int64_t>(row) * 2 * per_row);
-    const bool is_v = rest >= per_row;
-    if (is_v) rest -= per_row;
-    const T* src = (is_v ? v + row * v_stride : k + row * k_stride) + 4 * rest;
-    const float4 x = in ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-    uint32_t scale;
-    const int i = threadIdx.x & 7;
-    uint32_t w = quantize_q4_lane(x, i, &scale);
-    w |= __shfl_down_sync(0xFFFFFFFFu, w, 4) << 4;  // lanes 0..3 of a block: low nibbles, 4..7: high
-    if (!in) return;
-    const int b = kv_seq_of_row(r, c.n_seqs, row);
-    if (b < 0) return;
-    int first, count;
-    kv_rows(r, b, &first, &count, &g_kv_error);
-    const int pos = kv_length(c, b, &g_kv_error) - count + (row - first);
-    if (row - first >= count || pos < 0) {
-        atomicOr(&g_kv_error, kErrRange);
-        return;
+    const RowWork<NB> w(c, r, heads_each, &g_kv_error);
+    const T* src = (w.is_v ? v + w.row * v_stride : k + w.row * k_stride) + 32 * w.blk + 8 * w.i;
+    uint8_t* pool = w.is_v ? c.v : c.k;
+    const int slot = w.pos & 15;
+    float next[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (w.in && w.h_first < w.h_end) load8(src + w.h_first * (32 * NB), next);
+#pragma unroll 2
+    for (int h = w.h_first; h < w.h_end; ++h) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = next[e];
+        if (w.in && h + 1 < w.h_end) load8(src + (h + 1) * (32 * NB), next);
+        uint32_t scale;
+        uint2 q = quantize_q4_lane(y, w.i, &scale);
+        // Lanes 0, 1 of a block have the low nibbles of bytes 0 .. 7, 8 .. 15, lanes 2, 3 the high ones.
+        q.x |= __shfl_down_sync(0xFFFFFFFFu, q.x, 2) << 4;
+        q.y |= __shfl_down_sync(0xFFFFFFFFu, q.y, 2) << 4;
+        if (w.in) {
+            uint8_t* cell = pool + w.cell0 + h * w.h_step;
+            if (w.i < 2) *reinterpret_cast<uint2*>(cell + w.blk * 256 + slot * 16 + 8 * w.i) = q;
+            if (w.i == 2)
+                *reinterpret_cast<uint16_t*>(cell + cell_scales(32 * NB) + (slot * NB + w.blk) * 2) =
+                    static_cast<uint16_t>(scale);
+        }
     }
-    const int h = rest * 4 / c.dim;
-    const int blk = (rest * 4 - h * c.dim) >> 5;
-    const int64_t off = kv_cell(c, b, h, pos, &g_kv_error);
-    if (off < 0) return;
-    uint8_t* cell = (is_v ? c.v : c.k) + off;
-    const int slot = pos & 15;
-    if (i < 4) *reinterpret_cast<uint32_t*>(cell + blk * 256 + slot * 16 + 4 * i) = w;
-    if (i == 4)
-        *reinterpret_cast<uint16_t*>(cell + cell_scales(c.dim) + (slot * (c.dim >> 5) + blk) * 2) =
-            static_cast<uint16_t>(scale);
 }
 
 // The inverse: f32 values of the call's rows, contiguous [n_tokens][heads][dim].
-__global__ void __launch_bounds__(kThreads)
-    kv_read_kernel(KvView c, KvRows r, float* k, float* v, int64_t n4) {
+template <int NB>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(KvView c, KvRows r, float* k, float* v, int heads_each) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (t >= n4) return;
-    const int per_row = c.heads * c.dim / 4;
-    const int row = static_cast<int>(t / (2 * per_row));
-    int rest = static_cast<int>(t - static_cast<int64_t>(row) * 2 * per_row);
-    const bool is_v = rest >= per_row;
-    if (is_v) rest -= per_row;
-    const int b = kv_seq_of_row(r, c.n_seqs, row);
-    if (b < 0) return;
-    int first, count;
-    kv_rows(r, b, &first, &count, &g_kv_error);
-    const int pos = kv_length(c, b, &g_kv_error) - count + (row - first);
-    const int h = rest * 4 / c.dim;
-    const int blk = (rest * 4 - h * c.dim) >> 5;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    int64_t off = -1;
-    if (row - first < count && pos >= 0) off = kv_cell(c, b, h, pos, &g_kv_error);
-    else atomicOr(&g_kv_error, kErrRange);
-    if (off >= 0) {
-        const uint8_t* cell = (is_v ? c.v : c.k) + off;
-        const int slot = pos & 15;
-        const int i = rest & 7;
-        uint32_t w = *reinterpret_cast<const uint32_t*>(cell + blk * 256 + slot * 16 + 4 * (i & 3));
-        if (i >= 4) w >>= 4;
-        const float d = f16_bits_to_float(*reinterpret_cast<const uint16_t*>(
-            cell + cell_scales(c.dim) + (slot * (c.dim >> 5) + blk) * 2));
-        x.x = magic_minus8((w & 15u) | kMagicBits) * d;
-        x.y = magic_minus8(((w >> 8) & 15u) | kMagicBits) * d;
-        x.z = magic_minus8(((w >> 16) & 15u) | kMagicBits) * d;
-        x.w = magic_minus8(((w >> 24) & 15u) | kMagicBits) * d;
+    const RowWork<NB> w(c, r, heads_each, &g_kv_error);
+    if (!w.in) return;
+    const uint8_t* pool = w.is_v ? c.v : c.k;
+    const int slot = w.pos & 15;
+    float* dst = (w.is_v ? v : k) + (static_cast<int64_t>(w.row) * c.heads) * (32 * NB) + 32 * w.blk + 8 * w.i;
+#pragma unroll 4
+    for (int h = w.h_first; h < w.h_end; ++h) {
+        const uint8_t* cell = pool + w.cell0 + h * w.h_step;
+        const uint2 q = *reinterpret_cast<const uint2*>(cell + w.blk * 256 + slot * 16 + 8 * (w.i & 1));
+        const float d = f16_bits_to_float(
+            *reinterpret_cast<const uint16_t*>(cell + cell_scales(32 * NB) + (slot * NB + w.blk) * 2));
+        const uint32_t n[2] = {w.i < 2 ? q.x : q.x >> 4, w.i < 2 ? q.y : q.y >> 4};
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = magic_minus8(((n[e >> 2] >> (8 * (e & 3))) & 15u) | kMagicBits) * d;
+        float4* to = reinterpret_cast<float4*>(dst + h * (32 * NB));
+        to[0] = make_float4(y[0], y[1], y[2], y[3]);
+        to[1] = make_float4(y[4], y[5], y[6], y[7]);
     }
-    float* dst = (is_v ? v : k) + static_cast<int64_t>(row) * per_row * 4 + 4 * rest;
-    *reinterpret_cast<float4*>(dst) = x;
+}
+
+// Warps of RowWork, and how many heads each takes: one where that is what fills
+// the GPU, else up to eight.
+template <int NB>
+unsigned row_warps(const KvView& c, const KvRows& r, int* heads_each) {
+    const int64_t groups = (static_cast<int64_t>(r.n_tokens) + RowWork<NB>::kTokens - 1) / RowWork<NB>::kTokens;
+    int each = 1;
+    while (each < 8 && each < c.heads && groups * 2 * c.heads / (2 * each) >= 152 * 64) each *= 2;
+    *heads_each = each;
+    return static_cast<unsigned>(groups * 2 * ((c.heads + each - 1) / each));
 }
 
 // ---- eviction --------------------------------------------------------------
 
 constexpr int kSelThreads = 1024;
+constexpr int kEach = 8;  // consecutive tokens of a thread in the last pass
 
 // Unsigned order of a score: larger score, larger key; NaN below everything.
 __device__ __forceinline__ uint32_t score_key(float w) {
@@ -150,94 +199,117 @@ __device__ __forceinline__ uint32_t score_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, kv head): finds the smallest kept key by a radix
-// select (four passes of 8 bits over the scores), then writes the kept tokens
-// in ascending order with a block-wide scan per 1024 tokens.
-__global__ void __launch_bounds__(kSelThreads)
-    kv_select_kernel(KvView c, EvictCall e) {
+// Sum of v over the threads before this one; *total: over all of them.
+__device__ __forceinline__ int sel_scan(int v, int* warp_sums, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // warp_sums of the scan before have been read
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += y;
+    }
+    *total = __shfl_sync(0xFFFFFFFFu, w, 31);
+    const int before = warp ? __shfl_sync(0xFFFFFFFFu, w, warp - 1) : 0;
+    return before + x - v;
+}
+
+// One CTA per (sequence, kv head): finds the smallest kept key by a radix select
+// (three passes of 11, 11 and 10 bits: the first digit takes the exponent and
+// two bits more, so ordinary scores do not all count in one bin), then
+// writes the kept tokens in ascending order, 8192 at a time.
+__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(KvView c, EvictCall e, int set_lengths) {
     grid_launch_dependents();
     grid_dependency_wait();
-    __shared__ unsigned hist[256];
-    __shared__ unsigned warp_n[2][32];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
+    __shared__ int hist[2048];
+    __shared__ int warp_sums[32];
+    __shared__ int s_bin, s_need;
     const int h = blockIdx.x, b = blockIdx.y;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int L = kv_length(c, b, &g_kv_error);
     const float* w = e.weights + (static_cast<int64_t>(b) * c.heads + h) * e.weights_stride;
     float* wo = e.weights_out + (static_cast<int64_t>(b) * c.heads + h) * e.out_stride;
     int32_t* kept = e.kept + (static_cast<int64_t>(b) * c.heads + h) * e.budget;
     const int n_keep = min(L, e.budget);
-    const int lo = min(e.sinks, L);             // tokens below lo and from hi on stay
+    if (set_lengths && h == 0 && tid == 0) e.lengths_out[b] = n_keep;
+    const int lo = min(e.sinks, L);            // tokens below lo and from hi on stay
     const int hi = max(lo, L - e.recent);
-    const int need0 = n_keep - lo - (L - hi);   // of the tokens between
-    uint32_t prefix = 0;
-    int need = need0;
+    const int need0 = n_keep - lo - (L - hi);  // of the tokens between
     const bool all = L <= e.budget;
+    uint32_t prefix = 0, known = 0;  // the digits found so far, and their mask
+    int need = need0;
     if (!all && need > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+            hist[tid] = 0;
+            hist[tid + 1024] = 0;
             __syncthreads();
-            const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
             for (int j = lo + tid; j < hi; j += kSelThreads) {
                 const uint32_t key = score_key(w[j]);
-                if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+                if ((key & known) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
             }
             __syncthreads();
-            if (tid == 0) {
-                int left = need;
-                int bin = 255;
-                while (bin > 0 && static_cast<int>(hist[bin]) < left) left -= hist[bin--];
-                s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-                s_need = left;
-            }
+            // Bins from the top: this thread's are bins - 1 - 2 tid and the one below.
+            const int top = bins - 1 - 2 * tid;
+            const int n1 = top >= 0 ? hist[top] : 0, n2 = top >= 1 ? hist[top - 1] : 0;
+            int total;
+            const int before = sel_scan(n1 + n2, warp_sums, &total);
+            if (before < need && need <= before + n1) s_bin = top, s_need = need - before;
+            if (before + n1 < need && need <= before + n1 + n2) s_bin = top - 1, s_need = need - before - n1;
             __syncthreads();
-            prefix = s_prefix;
+            prefix |= static_cast<uint32_t>(s_bin) << shift;
+            known |= static_cast<uint32_t>(bins - 1) << shift;
             need = s_need;
         }
     }
     // Keys above `prefix` are kept, and the first `need` equal to it.
     int base_keep = 0, base_tie = 0;
-    for (int j0 = 0; j0 < L; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        float score = 0.f;
-        bool keep = false, tie = false;
-        if (j < L) {
-            score = w[j];
-            if (all || j < lo || j >= hi) keep = true;
-            else if (need0 > 0) {
-                const uint32_t key = score_key(score);
-                keep = key > prefix;
-                tie = key == prefix;
+#pragma unroll 1
+    for (int j0 = 0; j0 < L; j0 += kSelThreads * kEach) {
+        const int j = j0 + tid * kEach;
+        float score[kEach];
+        uint32_t keep = 0, tie = 0;  // a bit per token
+#pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+            score[x] = j + x < L ? w[j + x] : 0.f;
+            if (j + x < L) {
+                if (all || j + x < lo || j + x >= hi) keep |= 1u << x;
+                else if (need0 > 0) {
+                    const uint32_t key = score_key(score[x]);
+                    if (key > prefix) keep |= 1u << x;
+                    if (key == prefix) tie |= 1u << x;
+                }
             }
         }
-        const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
-        if (lane == 0) warp_n[0][warp] = __popc(tb);
-        __syncthreads();
-        int before = base_tie, total_tie = 0;
-        for (int i = 0; i < 32; ++i) {
-            if (i < warp) before += warp_n[0][i];
-            total_tie += warp_n[0][i];
-        }
-        if (tie && before + __popc(tb & ((1u << lane) - 1u)) < need) keep = true;
-        const unsigned kb = __ballot_sync(0xFFFFFFFFu, keep);
-        if (lane == 0) warp_n[1][warp] = __popc(kb);
-        __syncthreads();
-        int at = base_keep, total_keep = 0;
-        for (int i = 0; i < 32; ++i) {
-            if (i < warp) at += warp_n[1][i];
-            total_keep += warp_n[1][i];
-        }
-        at += __popc(kb & ((1u << lane) - 1u));
-        // In place (weights_out == weights): at <= j, and every thread of the
-        // CTA has read its score of this chunk before the barriers above.
-        if (keep && at < n_keep) {
-            kept[at] = j;
-            wo[at] = score;
-        }
-        base_keep += total_keep;
-        base_tie += total_tie;
-        __syncthreads();
+        int total;
+        int rank = base_tie + sel_scan(__popc(tie), warp_sums, &total);
+        base_tie += total;
+#pragma unroll
+        for (int x = 0; x < kEach; ++x)
+            if ((tie >> x) & 1u) {
+                if (rank < need) keep |= 1u << x;
+                ++rank;
+            }
+        // (In place, weights_out == weights: a place is never above its token's, and
+        // every score of this round has been read before the scans' barriers.)
+        int at = base_keep + sel_scan(__popc(keep), warp_sums, &total);
+        base_keep += total;
+#pragma unroll
+        for (int x = 0; x < kEach; ++x)
+            if ((keep >> x) & 1u) {
+                kept[at] = j + x;
+                wo[at] = score[x];
+                ++at;
+            }
     }
     for (int i = n_keep + tid; i < e.budget; i += kSelThreads) {
         kept[i] = -1;
@@ -245,63 +317,54 @@ __global__ void __launch_bounds__(kSelThreads)
     }
 }
 
-// Copies the kept tokens' quants and scales to the first places of dst.
-// Thread: one 16-byte quant row of a token (or its scales); a CTA takes
-// `cells` destination cells.  With in_place one CTA walks all of them: a kept
-// token never moves up, so reading a batch before writing it is enough.
+// Copies the kept tokens' quants and scales, of keys and values, to the first
+// places of dst: a token per thread, all its pieces (16-byte quant rows, 256 bytes
+// contiguous over 16 tokens) in flight together.  With in_place one CTA walks all
+// of a head's tokens: a kept token never moves up, so reading a round before
+// writing it is enough.
+template <int NB>
 __global__ void __launch_bounds__(kThreads)
-    kv_move_kernel(KvView src, KvView dst, const int32_t* kept_all, int budget, int cells, int in_place) {
+    kv_move_kernel(KvView src, KvView dst, const int32_t* kept_all, int budget, int in_place) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int h = blockIdx.y % src.heads;
-    const bool is_v = blockIdx.y >= static_cast<unsigned>(src.heads);
-    const int b = blockIdx.z;
+    const int h = blockIdx.y, b = blockIdx.z;
     const int32_t* kept = kept_all + (static_cast<int64_t>(b) * src.heads + h) * budget;
     const int n_keep = min(kv_length(src, b, &g_kv_error), budget);
-    const int pieces = src.dim / 32 + 1;  // quant rows of a token, then its scales
-    const int per_cell = kCellTokens * pieces;
-    const uint8_t* from = is_v ? src.v : src.k;
-    uint8_t* to = is_v ? dst.v : dst.k;
-    const int n_cells = (n_keep + kCellTokens - 1) / kCellTokens;
-    const int end = in_place ? n_cells : min(n_cells, static_cast<int>(blockIdx.x + 1) * cells);
-    const int step = kThreads / kCellTokens;  // (cell, piece) pairs per pass
-    const int first = in_place ? 0 : blockIdx.x * cells;
-    for (int p0 = first * pieces; p0 < end * pieces; p0 += step) {
-        const int p = p0 + threadIdx.x / kCellTokens;
-        const int cell = p / pieces, piece = p - cell * pieces;
-        const int slot = threadIdx.x & 15;
-        const int at = cell * kCellTokens + slot;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        const uint8_t* s = nullptr;
-        uint8_t* d = nullptr;
-        if (cell < end && at < n_keep) {
+    const int end = in_place ? n_keep : min(n_keep, static_cast<int>(blockIdx.x + 1) * kThreads);
+    for (int at0 = in_place ? 0 : blockIdx.x * kThreads; at0 < end; at0 += kThreads) {
+        const int at = at0 + threadIdx.x;
+        uint4 q[2][NB];
+        uint16_t sc[2][NB];
+        int64_t to = -1;
+        if (at < end) {
             const int token = kept[at];
-            const int64_t so = kv_cell(src, b, h, token, &g_kv_error);
-            const int64_t dd = kv_cell(dst, b, h, at, &g_kv_error);
-            if (so >= 0 && dd >= 0) {
-                s = from + so;
-                d = to + dd;
-                if (piece < src.dim / 32) {
-                    x = *reinterpret_cast<const uint4*>(s + piece * 256 + (token & 15) * 16);
-                } else {
-                    const int nb = src.dim / 32;
-                    const uint16_t* sc = reinterpret_cast<const uint16_t*>(s + cell_scales(src.dim)) + (token & 15) * nb;
-                    uint16_t hsc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    for (int i = 0; i < nb; ++i) hsc[i] = sc[i];
-                    x = make_uint4(hsc[0] | (hsc[1] << 16), hsc[2] | (hsc[3] << 16), hsc[4] | (hsc[5] << 16),
-                                   hsc[6] | (hsc[7] << 16));
+            const int64_t from = kv_cell(src, b, h, token, &g_kv_error);
+            to = kv_cell(dst, b, h, at, &g_kv_error);
+            if (from < 0) to = -1;
+            if (to >= 0) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const uint8_t* cell = (p ? src.v : src.k) + from;
+                    const uint16_t* s = reinterpret_cast<const uint16_t*>(cell + cell_scales(32 * NB)) + (token & 15) * NB;
+#pragma unroll
+                    for (int x = 0; x < NB; ++x) {
+                        q[p][x] = *reinterpret_cast<const uint4*>(cell + x * 256 + (token & 15) * 16);
+                        sc[p][x] = s[x];
+                    }
                 }
             }
         }
         if (in_place) __syncthreads();
-        if (d) {
-            if (piece < src.dim / 32) {
-                *reinterpret_cast<uint4*>(d + piece * 256 + slot * 16) = x;
-            } else {
-                const int nb = src.dim / 32;
-                uint16_t* sc = reinterpret_cast<uint16_t*>(d + cell_scales(src.dim)) + slot * nb;
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                for (int i = 0; i < nb; ++i) sc[i] = static_cast<uint16_t>(xs[i >> 1] >> (16 * (i & 1)));
+        if (to >= 0) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint8_t* cell = (p ? dst.v : dst.k) + to;
+                uint16_t* s = reinterpret_cast<uint16_t*>(cell + cell_scales(32 * NB)) + (at & 15) * NB;
+#pragma unroll
+                for (int x = 0; x < NB; ++x) {
+                    *reinterpret_cast<uint4*>(cell + x * 256 + (at & 15) * 16) = q[p][x];
+                    s[x] = sc[p][x];
+                }
             }
         }
         if (in_place) __syncthreads();
@@ -317,41 +380,89 @@ __global__ void kv_lengths_kernel(KvView src, int32_t* out, int budget) {
 
 }  // namespace
 
+namespace {
+
+// F<NB> for the blocks of a head, 1 .. 8.
+template <template <int> class F, typename... Args>
+cudaError_t by_blocks(int dim, Args&&... args) {
+    switch (dim / 32) {
+        case 1: return F<1>::run(args...);
+        case 2: return F<2>::run(args...);
+        case 3: return F<3>::run(args...);
+        case 4: return F<4>::run(args...);
+        case 5: return F<5>::run(args...);
+        case 6: return F<6>::run(args...);
+        case 7: return F<7>::run(args...);
+        default: return F<8>::run(args...);
+    }
+}
+
+template <int NB>
+struct Append {
+    static cudaError_t run(const KvView& c, const KvRows& r, const void* k, const void* v, KvType type, int64_t k_stride,
+                           int64_t v_stride, cudaStream_t stream) {
+        int each;
+        const unsigned warps = row_warps<NB>(c, r, &each);
+        const dim3 grid((warps + kThreads / 32 - 1) / (kThreads / 32));
+        note_launch();
+        if (type == KvType::kF32)
+            return launch_pdl(kv_append_kernel<NB, float>, grid, dim3(kThreads), 0, stream, c, r,
+                              static_cast<const float*>(k), static_cast<const float*>(v), k_stride, v_stride, each);
+        return launch_pdl(kv_append_kernel<NB, __nv_bfloat16>, grid, dim3(kThreads), 0, stream, c, r,
+                          static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), k_stride, v_stride,
+                          each);
+    }
+};
+
+template <int NB>
+struct Read {
+    static cudaError_t run(const KvView& c, const KvRows& r, float* k, float* v, cudaStream_t stream) {
+        int each;
+        const unsigned warps = row_warps<NB>(c, r, &each);
+        note_launch();
+        return launch_pdl(kv_read_kernel<NB>, dim3((warps + kThreads / 32 - 1) / (kThreads / 32)), dim3(kThreads), 0,
+                          stream, c, r, k, v, each);
+    }
+};
+
+template <int NB>
+struct Move {
+    static cudaError_t run(const KvView& src, const KvView& dst, const EvictCall& e, unsigned chunks, int in_place,
+                           cudaStream_t stream) {
+        note_launch();
+        return launch_pdl(kv_move_kernel<NB>, dim3(chunks, src.heads, src.n_seqs), dim3(kThreads), 0, stream, src, dst,
+                          static_cast<const int32_t*>(e.kept), e.budget, in_place);
+    }
+};
+
+}  // namespace
+
 cudaError_t launch_kv_append(const KvView& c, const KvRows& r, const void* k, const void* v, KvType type,
                              int64_t k_stride, int64_t v_stride, cudaStream_t stream) {
-    const int64_t n4 = static_cast<int64_t>(r.n_tokens) * 2 * c.heads * (c.dim / 4);
-    const dim3 grid(static_cast<unsigned>((n4 + kThreads - 1) / kThreads));
-    note_launch();
-    if (type == KvType::kF32)
-        return launch_pdl(kv_append_kernel<float>, grid, dim3(kThreads), 0, stream, c, r, static_cast<const float*>(k),
-                          static_cast<const float*>(v), k_stride, v_stride, n4);
-    return launch_pdl(kv_append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, c, r,
-                      static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), k_stride, v_stride,
-                      n4);
+    return by_blocks<Append>(c.dim, c, r, k, v, type, k_stride, v_stride, stream);
 }
 
 cudaError_t launch_kv_read(const KvView& c, const KvRows& r, float* k, float* v, cudaStream_t stream) {
-    const int64_t n4 = static_cast<int64_t>(r.n_tokens) * 2 * c.heads * (c.dim / 4);
-    note_launch();
-    return launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>((n4 + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                      stream, c, r, k, v, n4);
+    return by_blocks<Read>(c.dim, c, r, k, v, stream);
 }
 
 cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCall& e, cudaStream_t stream,
                             const DeviceInfo& /*dev*/) {
+    // The lengths are read until the last cell has moved: where the new ones go to
+    // the same array they are written by a kernel of their own.
+    const bool same_lengths = src.lengths == e.lengths_out;
     note_launch();
-    cudaError_t err = launch_pdl(kv_select_kernel, dim3(src.heads, src.n_seqs), dim3(kSelThreads), 0, stream, src, e);
+    cudaError_t err = launch_pdl(kv_select_kernel, dim3(src.heads, src.n_seqs), dim3(kSelThreads), 0, stream, src, e,
+                                 same_lengths ? 0 : 1);
     if (err != cudaSuccess) return err;
     const bool in_place = src.table == dst.table && src.k == dst.k;
     const int64_t most = std::min<int64_t>(e.budget, src.max_len);
-    const int cells = 8;
-    const int64_t chunks = in_place ? 1 : (most + cells * kCellTokens - 1) / (cells * kCellTokens);
     if (most > 0) {
-        note_launch();
-        err = launch_pdl(kv_move_kernel, dim3(static_cast<unsigned>(chunks), 2 * src.heads, src.n_seqs), dim3(kThreads),
-                         0, stream, src, dst, e.kept, e.budget, cells, in_place ? 1 : 0);
+        const int64_t chunks = in_place ? 1 : (most + kThreads - 1) / kThreads;
+        err = by_blocks<Move>(src.dim, src, dst, e, static_cast<unsigned>(chunks), in_place ? 1 : 0, stream);
         if (err != cudaSuccess) return err;
     }
+    if (!same_lengths) return cudaSuccess;
     note_launch();
     return launch_pdl(kv_lengths_kernel, dim3((src.n_seqs + 127) / 128), dim3(128), 0, stream, src, e.lengths_out,
                       e.budget);
