@@ -27,21 +27,22 @@
 // about equally (softmax 6 instructions per score, unpacking 13 per 8 quants,
 // shared by two row tiles).
 //
-// Structure, one CTA of 16 warps per (sequence, kv head, 128 or 2 x 128 rows):
-//   a loader warp fetches raw cells with bulk copies;
-//   4 or 8 decode warps unpack them into 128-byte swizzled tiles (dims of a block
-//     in the order the nibbles unpack; Q and the output follow it);
+// Structure, one CTA of 24 (bf16: 20) warps per (sequence, kv head, 128 or 2 x 128 rows):
+//   8 decode warps read cells, a step ahead, and unpack them into 128-byte
+//     swizzled tiles (dims of a block in the order the nibbles unpack; Q and the
+//     output follow it); an examiner warp finds each tile's largest scales;
 //   one thread issues the MMAs: S of the next tile is queued before P V of this
 //     one (f32), or two row tiles take turns (bf16), so the softmax of one
 //     always has products of another to run beside;
-//   4 warps per row tile hold a row per thread: maximum, exponentials, P back to
-//     TMEM over S (P is the A operand from there).  bf16: only when a row's
-//     maximum grows by more than 2^3 is its accumulator scaled down.
+//   8 softmax warps hold a row per thread (f32: half a row): maximum, exponentials,
+//     P back to TMEM over S (P is the A operand from there).  bf16: only when a
+//     row's maximum grows by more than 2^3 is its accumulator scaled down;
+//   f32: 4 collector warps add the tiles' products up.
 // Code is kept short on purpose (rolled loops over 32-column chunks): unrolled,
 // the roles of the four schedulers evicted one another's instructions (805 us
 // against 449 for a prompt of 4096 f32 rows).
-// f32 rows' registers: 640 threads x 96 at launch; then 256 x 136 + 256 x 72 +
-// 128 x 40 = 58368 of those 61440.
+// f32 rows' registers: 768 threads x 80 at launch; then 256 x 72 (softmax) + 256 x
+// 64 (decode) + 128 x 168 (collectors) + 128 x 40 = 61440, all of them.
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include <algorithm>
 
@@ -53,9 +54,9 @@ __device__ unsigned int g_attn_prompt_error = 0;
 
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kSoftmaxWarps = 8, kDecodeWarps = 8;  // then MMA issue, loader, examiner, an idle one
-constexpr int kRing = 8;    // tiles whose scale factors are kept
+constexpr int kSoftmaxWarps = 8, kDecodeWarps = 8;
+constexpr int kRing = 8;      // tiles whose scale factors are kept
+constexpr int kKeepRing = 4;  // tiles whose rows' factors are kept for the collectors
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -65,14 +66,14 @@ struct Shape {
     static constexpr int kM = F32 ? 1 : 2;            // row tiles of a CTA
     static constexpr int kPieces = F32 ? 2 : 1;       // of Q, K, V and P
     static constexpr int kStages = F32 ? 1 : 2;       // K tiles, V tiles
-    static constexpr int kRawSlots = 3;               // raw tiles, of keys and values in turn
     static constexpr int kPiece = kTile * D * 2;      // bytes of one piece of a tile
     static constexpr int kOperand = kPieces * kPiece;
-    static constexpr int kRaw = kTile / 16 * 9 * D;   // raw cells of a tile
-    static constexpr int kVScales = kTile * 2 * kBlocks;
-    static constexpr int kSlot = kRaw + kVScales;     // keys come with the scales of the values
     static constexpr int kHalves = F32 ? 2 : 1;       // softmax threads of a row
-    static constexpr int kSmem = kM * kOperand + 2 * kStages * kOperand + kRawSlots * kSlot + 1024;
+    // Warps: softmax, decode, (f32) collectors, then MMA issue, examiner, two idle.
+    static constexpr int kCollectWarps = F32 ? 4 : 0;
+    static constexpr int kIssuer = kSoftmaxWarps + kDecodeWarps + kCollectWarps;
+    static constexpr int kThreads = (kIssuer + 4) * 32;
+    static constexpr int kSmem = kM * kOperand + 2 * kStages * kOperand + 1024;
     static_assert(kSmem <= 232448 - 3072, "shared memory of one CTA");
 };
 
@@ -120,14 +121,58 @@ struct PromptPlan {
     unsigned* redo;      // and which: row * heads + head
 };
 
+// A row's end: its output, 32 dims at a time, its logarithm, and the list of rows
+// to be done again.
+template <int D, bool F32, typename T>
+struct RowEnd {
+    const AttnCall& a;
+    const PromptPlan& plan;
+    int64_t item;  // row * heads + head
+    T* out;
+    bool in;
+    float sum, inv, least = INFINITY;
+    __device__ RowEnd(const AttnCall& a_, const PromptPlan& plan_, int first, int group, int h, int rr, bool in_, float sum_)
+        : a(a_), plan(plan_), in(in_), sum(sum_), inv(sum_ == 0.f ? 0.f : 1.f / sum_) {
+        const int64_t row = first + (in ? rr / group : 0);
+        const int head = h * group + (in ? rr % group : 0);
+        item = row * a.heads + head;
+        out = static_cast<T*>(a.out) + row * a.out_stride + static_cast<int64_t>(head) * D;
+    }
+    __device__ __forceinline__ void store32(const float v[32], int q) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                least = fminf(least, fabsf(v[8 * k + e]));
+                y[e] = sum == 0.f ? 0.f : v[8 * k + e] * inv;
+            }
+            if (in) {
+                store_o4(out + 32 * q + 4 * k, make_float4(y[0], y[2], y[1], y[3]));
+                store_o4(out + 32 * q + 16 + 4 * k, make_float4(y[4], y[6], y[5], y[7]));
+            }
+        }
+    }
+    __device__ __forceinline__ void finish(float top, float lowest, int n_tiles) {
+        if (!in) return;
+        const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum) - kPTop<F32>;
+        if (a.lse) a.lse[item] = lse2 * kLn2;
+        if (plan.lse2) plan.lse2[item] = lse2;
+        if (lowest < top - kFarBelow<F32> && least < sqrtf(static_cast<float>(n_tiles * kTile)) * kSafe<F32>) {
+            const unsigned at = atomicAdd(plan.redo_n, 1u);  // (at most once per row)
+            plan.redo[at] = static_cast<unsigned>(item);
+        }
+    }
+};
+
 struct Bars {
-    uint64_t raw_full[3], raw_empty[3], exam[3];
+    uint64_t exam, exam_go;
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
 };
 
 template <int D, bool F32, typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
     attn_prompt_kernel(KvView c, KvRows r, AttnCall a, PromptPlan plan) {
     using S = Shape<D, F32>;
     constexpr int NB = S::kBlocks;
@@ -140,22 +185,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float value_exp[kRing];          // log2 of the same of a value tile
     __shared__ float key_up[kRing], value_up[kRing];  // the powers of two themselves
     __shared__ __align__(16) uint8_t wild[kRing][32];     // bit t of byte l: token 4 l + t of tile i has a wild value scale
-    __shared__ float half_max[2][S::kHalves][kM * kTile];  // f32: what the two threads of a row tell each other
+    // f32: what the two softmax threads of a row tell each other, and the collector.
+    __shared__ float half_max[2][S::kHalves][kM * kTile];
+    __shared__ float row_keep[F32 ? kKeepRing : 1][kTile], row_top[F32 ? kTile : 1];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_sm = base;                             // [kM][pieces]
     uint8_t* k_sm = q_sm + kM * S::kOperand;          // [stages][pieces]
     uint8_t* v_sm = k_sm + S::kStages * S::kOperand;  // [stages][pieces]
-    uint8_t* raw = v_sm + S::kStages * S::kOperand;   // [slots][cells, scales of the values]
     unsigned int* const err = &g_attn_prompt_error;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kRawSlots; ++i) {
-            mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], kDecodeWarps + 1);  // and the examiner
-            mbar_init(&bar.exam[i], 1);
-        }
+        mbar_init(&bar.exam, 1);
+        mbar_init(&bar.exam_go, kDecodeWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.k_full[i], kDecodeWarps);
             mbar_init(&bar.v_full[i], kDecodeWarps);
@@ -164,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 4 * S::kHalves);
             mbar_init(&bar.pv_done[i], 1);
-            mbar_init(&bar.o_free[i], 4 * S::kHalves);
+            mbar_init(&bar.o_free[i], 4);
         }
         fence_barrier_init();
     }
@@ -189,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const TileList tiles = tile_list(seen_len, max(pos_lo, 0), a.window, a.sinks);
     const int n_tiles = tiles.count;
 
-    if (warp == 16) {
+    if (warp == S::kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -255,12 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftmaxWarps) {
         // ---- softmax: this thread's row
-        if (F32) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // f32: the warps w and w + 4 share 32 rows, each has half of a tile's columns
         // and half of the dims; bf16: they have a row tile each.
         const int m = F32 ? 0 : warp >> 2, half = F32 ? warp >> 2 : 0;
         constexpr int kChunks = 4 / S::kHalves;     // of 32 columns, this thread's of a tile
-        constexpr int kDims = D / S::kHalves;       // this thread's of the output
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const int row = 32 * (warp & 3) + lane;
         const int rr = row0 + m * kTile + row;
@@ -270,40 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wr0 = row0 + m * kTile + 32 * (warp & 3);        // the warp's rows' extreme positions
         const int w_lo = base_pos + wr0 / group, w_hi = base_pos + (wr0 + 31) / group;
         const float unit = fabsf(a.scale) * kLog2e * row_unit[m * kTile + row];
-        const uint32_t t_o = tmem + lanes + kTmemO + (F32 ? half * kDims : m * 128);
+        const uint32_t t_o = tmem + lanes + kTmemO + m * 128;  // (bf16)
         float mx_used = -INFINITY, sum = 0.f;
         float lowest = INFINITY;  // of the row's scores (with the value tile's exponent)
-        float o[F32 ? kDims : 1];
-        float keep_now = 0.f, keep_last = 0.f;  // f32: what a tile, and the one before it, scale the sums so far by
-#pragma unroll
-        for (int e = 0; e < (F32 ? kDims : 1); ++e) o[e] = 0.f;
         bool ok = true;
         // f32: what the row's other thread has.
         auto other = [&](float x, int buf) {
             half_max[buf][half][row] = x;
             named_barrier_sync(1 + (warp & 3), 64);
             return half_max[buf][half ^ 1][row];
-        };
-        // f32: o = o keep + P V of tile i.
-        auto collect = [&](int i, float keep) {
-            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[0], i & 1, err));
-            if (!ok) return;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < kDims / 32; ++q) {
-                float v[32], w[32];
-                tmem_ld32(t_o + 32 * q, v);
-                tmem_ld32(t_o + 128 + 32 * q, w);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float& y = o[F32 ? 32 * q + e : 0];
-                    y = fmaf(y, keep, fmaf(w[e], 1.f / kLowUp, v[e]));
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.o_free[0]);
         };
 #pragma unroll 1
         for (int i = 0; i < n_tiles; ++i) {
@@ -380,9 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx = fmaf(mx, f, v_exp);
                 if (F32) {
                     const float next = fmaxf(mx_used, fmaxf(mx, other(mx, i & 1)));
-                    keep_now = exp2_approx(mx_used - (next == -INFINITY ? 0.f : next));
+                    const float keep = exp2_approx(mx_used - (next == -INFINITY ? 0.f : next));
                     mx_used = next;
-                    sum *= keep_now;
+                    sum *= keep;
+                    if (half == 0) row_keep[F32 ? i % kKeepRing : 0][row] = keep;  // what the sums so far are scaled by
                 } else {
                     // The maximum in use follows only where it is overtaken by 2^3.
                     const bool grow = mx > mx_used + kLazy;
@@ -438,44 +456,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.p_full[buf]);
-            if (F32 && i > 0) collect(i - 1, keep_last);
-            keep_last = keep_now;
         }
-        if (n_tiles > 0) {
-            if (F32) collect(n_tiles - 1, keep_last);
-            else if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[m], (n_tiles - 1) & 1, err));
-        }
-        tc_fence_after();
-        if (F32) {
+        // A row's output (columns in the order the quants unpack) and logarithm.
+        if constexpr (F32) {
             sum += other(sum, n_tiles & 1);
             lowest = fminf(lowest, other(lowest, (n_tiles + 1) & 1));
-        }
-        // The output: columns in the order the quants unpack.
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t orow = first + (in ? rr / group : 0);
-        const int head = h * group + (in ? rr % group : 0);
-        T* out = static_cast<T*>(a.out) + orow * a.out_stride + static_cast<int64_t>(head) * D + half * kDims;
-        float least = INFINITY;
-        auto store32 = [&](const float* v, int q) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    least = fminf(least, fabsf(v[8 * k + e]));
-                    y[e] = sum == 0.f ? 0.f : v[8 * k + e] * inv;
-                }
-                if (in) {
-                    store_o4(out + 32 * q + 4 * k, make_float4(y[0], y[2], y[1], y[3]));
-                    store_o4(out + 32 * q + 16 + 4 * k, make_float4(y[4], y[6], y[5], y[7]));
-                }
+            // To the collector: its barrier comes after these.
+            if (half == 0) {
+                row_top[row] = mx_used;
+                half_max[n_tiles & 1][0][row] = sum;
+                half_max[n_tiles & 1][1][row] = lowest;
             }
-        };
-        if constexpr (F32) {
-#pragma unroll
-            for (int q = 0; q < kDims / 32; ++q) store32(o + 32 * q, q);
-            least = fminf(least, other(least, n_tiles & 1));
+            named_barrier_sync(5, (kSoftmaxWarps + S::kCollectWarps) * 32);
         } else {
+            if (n_tiles > 0 && ok)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[m], (n_tiles - 1) & 1, err));
+            tc_fence_after();
+            RowEnd<D, false, T> end(a, plan, first, group, h, rr, in, sum);
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 float v[32];
@@ -486,27 +483,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 }
-                store32(v, q);
+                end.store32(v, q);
             }
-        }
-        if (in && half == 0) {
-            const float lse2 = sum == 0.f ? -INFINITY : mx_used + log2f(sum) - kPTop<F32>;
-            if (a.lse) a.lse[orow * a.heads + head] = lse2 * kLn2;
-            if (plan.lse2) plan.lse2[orow * a.heads + head] = lse2;
-            if (lowest < mx_used - kFarBelow<F32> && least < sqrtf(static_cast<float>(n_tiles * kTile)) * kSafe<F32>) {
-                const unsigned at = atomicAdd(plan.redo_n, 1u);  // (at most once per row)
-                plan.redo[at] = static_cast<unsigned>(orow * a.heads + head);
-            }
+            end.finish(mx_used, lowest, n_tiles);
         }
     } else if (warp < kSoftmaxWarps + kDecodeWarps) {
-        // ---- decode: raw cells -> swizzled tiles; keys one tile ahead of values
-        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---- decode: cells -> swizzled tiles, keys one tile ahead of values: keys 0,
+        // keys 1, values 0, keys 2, ...  A thread has a token and every other
+        // (D = 64: one) block of it; what it needs next is on its way while it
+        // unpacks.
+        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         const int dt = threadIdx.x - kSoftmaxWarps * 32;
+        const int tok = dt & (kTile - 1), blk0 = dt / kTile;
+        constexpr int kTurns = kTile * NB / (kDecodeWarps * 32), kStride = kDecodeWarps * 32 / kTile;
         bool ok = true;
-        // Raw tiles come in the order they are used: keys 0, keys 1, values 0, keys
-        // 2, ...; the scales of a tile have been looked at when `exam` says so.
-        int slot = 0, round = 0;
-        uint32_t exam_phase = 0;  // bit s: parity of the next exam of slot s
+        auto cell_at = [&](int i) -> int64_t {  // of this token in tile i
+            const int p = i < n_tiles ? tiles.at(i) * kTile + tok : seen_len;
+            return p < seen_len ? kv_cell(c, b, h, p, err) : -1;
+        };
+        uint4 q[kTurns];
+        uint32_t sc[kTurns];
+        auto fetch = [&](const uint8_t* pool, int64_t off) {
+#pragma unroll
+            for (int y = 0; y < kTurns; ++y) {
+                q[y] = make_uint4(0, 0, 0, 0);
+                sc[y] = 0;
+                if (off >= 0) {
+                    const int blk = blk0 + y * kStride;
+                    q[y] = __ldg(reinterpret_cast<const uint4*>(pool + off + blk * 256 + (tok & 15) * 16));
+                    sc[y] = __ldg(reinterpret_cast<const uint16_t*>(pool + off + cell_scales(D) + ((tok & 15) * NB + blk) * 2));
+                }
+            }
+        };
+        int64_t off_v = -1, off_k = cell_at(0);  // of the tile whose values come next, and of the one after
+        fetch(c.k, off_k);
         // One body for keys and values: the code of all roles together has to stay
         // in the instruction cache.
 #pragma unroll 1
@@ -514,41 +524,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool v = step > 0 && ((step & 1) == 0 || step == 2 * n_tiles - 1);
             const int i = v ? (step - 1) >> 1 : (step + 1) >> 1;
             const int stage = i % S::kStages;
-            ok = mbar_wait_bounded(&bar.raw_full[slot], round & 1, err);
-            if (ok && !v) {
-                ok = mbar_wait_bounded(&bar.exam[slot], (exam_phase >> slot) & 1, err);
-                exam_phase ^= 1u << slot;
+            if (!v) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam, i & 1, err));
+                if (ok && lane == 0) mbar_arrive(&bar.exam_go);
             }
             if (ok && i >= S::kStages)
                 ok = mbar_wait_bounded((v ? bar.v_empty : bar.k_empty) + stage, (i / S::kStages - 1) & 1, err);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            const uint8_t* cells = raw + slot * S::kSlot;
-            const int left = v ? seen_len - tiles.at(i) * kTile : kTile;
             const float f = v ? value_up[i % kRing] : key_up[i % kRing];
             uint8_t* hi = (v ? v_sm : k_sm) + stage * S::kOperand;
-#pragma unroll 1
-            for (int y = 0; y < kTile * NB / (kDecodeWarps * 32); ++y) {
-                const int task = dt + y * kDecodeWarps * 32;
-                const int tok = task & (kTile - 1), blk = task / kTile;
-                const uint8_t* cell = cells + (tok >> 4) * cell_bytes(D);
-                const uint4 q = *reinterpret_cast<const uint4*>(cell + blk * 256 + (tok & 15) * 16);
-                const uint32_t bits =
-                    *reinterpret_cast<const uint16_t*>(cell + cell_scales(D) + ((tok & 15) * NB + blk) * 2);
-                // Values past the end, or not finite (NaN then comes with the scores): 0.
-                const float d = tok >= left || (v && (bits & 0x7C00u) == 0x7C00u) ? 0.f : f16_bits_to_float(bits);
-                decode_block<F32>(q, d * f, tok, blk, hi, hi + S::kPiece, plan.k1024);
+            uint4 now[kTurns];
+            float d[kTurns];
+#pragma unroll
+            for (int y = 0; y < kTurns; ++y) {
+                now[y] = q[y];
+                // Values that are not finite (NaN then comes with the scores): 0.
+                d[y] = v && (sc[y] & 0x7C00u) == 0x7C00u ? 0.f : f16_bits_to_float(sc[y]) * f;
             }
+            // The next step: keys i + 1 (i + 2 after values i), or values i - 1.
+            if (v || step == 0) {
+                off_v = off_k;
+                off_k = cell_at(i + (v ? 2 : 1));
+                if (step + 1 == 2 * n_tiles - 1) fetch(c.v, off_v);  // no more keys
+                else fetch(c.k, off_k);
+            } else {
+                fetch(c.v, off_v);
+            }
+#pragma unroll
+            for (int y = 0; y < kTurns; ++y)
+                decode_block<F32>(now[y], d[y], tok, blk0 + y * kStride, hi, hi + S::kPiece, plan.k1024);
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.raw_empty[slot]);
-                mbar_arrive((v ? bar.v_full : bar.k_full) + stage);
+            if (lane == 0) mbar_arrive((v ? bar.v_full : bar.k_full) + stage);
+        }
+    } else if (warp < S::kIssuer) {
+        // ---- collectors (f32): a row's sums in registers, o = o keep + P V tile by tile.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const int row = 32 * (warp & 3) + lane, rr = row0 + row;
+        float o[F32 ? D : 1];
+#pragma unroll
+        for (int e = 0; e < (F32 ? D : 1); ++e) o[e] = 0.f;
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < n_tiles; ++i) {
+            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[0], i & 1, err));
+            if (!ok) break;
+            tc_fence_after();
+            const float keep = row_keep[F32 ? i % kKeepRing : 0][row];
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                float v[16], w[16];
+                tmem_ld16(tmem + lanes + kTmemO + 16 * x, v);
+                tmem_ld16(tmem + lanes + kTmemO + 128 + 16 * x, w);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float& y = o[F32 ? 16 * x + e : 0];
+                    y = fmaf(y, keep, fmaf(w[e], 1.f / kLowUp, v[e]));
+                }
             }
-            if (++slot == S::kRawSlots) slot = 0, ++round;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.o_free[0]);
+        }
+        named_barrier_sync(5, (kSoftmaxWarps + S::kCollectWarps) * 32);
+        if constexpr (F32) {
+            RowEnd<D, true, T> end(a, plan, first, group, h, rr, rr < n_rows, half_max[n_tiles & 1][0][row]);
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) end.store32(o + 32 * x, x);
+            end.finish(row_top[row], half_max[n_tiles & 1][1][row], n_tiles);
         }
     } else {
         if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 16) {
+    if (warp == S::kIssuer) {
         // ---- MMA issue
         if (lane == 0 && n_tiles > 0) {
             constexpr uint32_t id_s = idesc_f16(kTile, false), id_o = idesc_f16(D, true);
@@ -615,85 +664,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == 17) {
-        // ---- loader: lanes 0 .. 7 a cell of the tile each (the first of a page's
-        // run copies it whole), lanes 8 .. 15 the scales of a cell of values.
-        const int run = min(8, 1 << (c.page_shift - 4));
-        auto cell_at = [&](int i) -> int64_t {
-            if (lane >= 16 || i >= n_tiles) return -1;
-            const int p = tiles.at(i) * kTile + (lane & 7) * 16;
-            return p < seen_len ? kv_cell(c, b, h, p, err) : -1;
-        };
-        bool ok = true;
-        int slot = 0, round = 0;
-        auto fetch = [&](int i, bool v, int64_t off) {
-            if (round) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_empty[slot], (round - 1) & 1, err));
-            if (!ok) return;
-            const int cells = min(8, (seen_len - tiles.at(i) * kTile + 15) >> 4);
-            uint8_t* dst = raw + slot * S::kSlot;
-            uint32_t bytes = 0;
-            if (lane < 8 && lane % run == 0 && off >= 0)
-                bytes = static_cast<uint32_t>(min(run, cells - lane) * cell_bytes(D));
-            else if (lane >= 8 && lane < 16 && !v && off >= 0) bytes = 32 * NB;
-            const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
-            if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], total);
-            __syncwarp();
-            if (bytes) {
-                if (lane < 8)
-                    bulk_load_1d(dst + lane * cell_bytes(D), (v ? c.v : c.k) + off, bytes, &bar.raw_full[slot]);
-                else
-                    bulk_load_1d(dst + S::kRaw + (lane - 8) * 32 * NB, c.v + off + cell_scales(D), bytes,
-                                 &bar.raw_full[slot]);
-            }
-            if (++slot == S::kRawSlots) slot = 0, ++round;
-        };
-        // In the order of use: keys 0, keys 1, values 0, keys 2, ..., values n - 1.
-        int64_t off = -1, off_next = cell_at(0);  // of the tile whose values are next, and of the one after
-#pragma unroll 1
-        for (int step = 0; step < 2 * n_tiles && ok; ++step) {
-            const bool v = step > 0 && ((step & 1) == 0 || step == 2 * n_tiles - 1);
-            const int i = v ? (step - 1) >> 1 : (step + 1) >> 1;
-            fetch(i, v, v ? off : off_next);
-            if (v || step == 0) {
-                off = off_next;
-                off_next = cell_at(i + (v ? 2 : 1));
-            }
-        }
-    } else if (warp == 18) {
+    } else if (warp == S::kIssuer + 1) {
         // ---- examiner: what the decode warps and the softmax need to know of a
-        // tile's scales.  Lane l looks at tokens 4 l .. 4 l + 3.  It follows the
-        // whole sequence of raw tiles and frees every slot too (else a slot's
-        // barrier could run past the phase that it waits for).
-        bool ok = true;
-        int slot = 0, round = 0;
-        auto pass = [&] {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.raw_empty[slot]);
-            if (++slot == S::kRawSlots) slot = 0, ++round;
+        // tile's scales.  Lane l looks at tokens 4 l .. 4 l + 3 (of one cell).
+        constexpr int kWords = 2 * NB;  // of four tokens' scales
+        uint32_t x[kWords], v[kWords];
+        auto fetch = [&](int i) {
+            const int p = i < n_tiles ? tiles.at(i) * kTile + 4 * lane : seen_len;
+            const int64_t off = p < seen_len ? kv_cell(c, b, h, p, err) : -1;
+            const int64_t at = off + cell_scales(D) + (p & 15) * 2 * NB;
+#pragma unroll
+            for (int e = 0; e < kWords; e += 4) {
+                uint4 y = make_uint4(0, 0, 0, 0), z = y;
+                if (off >= 0) {
+                    y = __ldg(reinterpret_cast<const uint4*>(c.k + at + 4 * e));
+                    z = __ldg(reinterpret_cast<const uint4*>(c.v + at + 4 * e));
+                }
+                x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
+                v[e] = z.x, v[e + 1] = z.y, v[e + 2] = z.z, v[e + 3] = z.w;
+            }
         };
+        fetch(0);
+        bool ok = true;
 #pragma unroll 1
         for (int i = 0; i < n_tiles && ok; ++i) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_full[slot], round & 1, err));
-            if (!ok) break;
-            const uint8_t* rawk = raw + slot * S::kSlot;
-            const int left = seen_len - tiles.at(i) * kTile;  // tokens of the tile that count
+            const int left = seen_len - tiles.at(i) * kTile - 4 * lane;  // of this lane's tokens that count
             uint32_t top = 0, top_v = 0, bad = 0;
-#pragma unroll 1
-            for (int u = 0; u < 4; ++u) {
-                const int tok = 4 * lane + u;
-                const uint8_t* sc = rawk + (lane >> 2) * cell_bytes(D) + cell_scales(D) + (tok & 15) * 2 * NB;
-                const uint8_t* sv = rawk + S::kRaw + tok * 2 * NB;
 #pragma unroll
-                for (int e = 0; e < NB; ++e) {
-                    const uint32_t x = reinterpret_cast<const uint16_t*>(sc)[e] & 0x7FFFu;
-                    const uint32_t v = reinterpret_cast<const uint16_t*>(sv)[e] & 0x7FFFu;
-                    if (tok < left && x < 0x7C00u) top = max(top, x);
-                    if (tok < left && v < 0x7C00u) top_v = max(top_v, v);
-                    if (tok < left && v >= 0x7C00u) bad |= 1u << u;
+            for (int e = 0; e < kWords; ++e) {
+                const int u = e / (NB / 2);
+                const uint32_t a0 = x[e] & 0x7FFFu, a1 = (x[e] >> 16) & 0x7FFFu;
+                const uint32_t v0 = v[e] & 0x7FFFu, v1 = (v[e] >> 16) & 0x7FFFu;
+                if (u < left) {
+                    top = max(top, max(a0 < 0x7C00u ? a0 : 0u, a1 < 0x7C00u ? a1 : 0u));
+                    top_v = max(top_v, max(v0 < 0x7C00u ? v0 : 0u, v1 < 0x7C00u ? v1 : 0u));
+                    if (v0 >= 0x7C00u || v1 >= 0x7C00u) bad |= 1u << u;
                 }
             }
+            fetch(i + 1);
             top = __reduce_max_sync(0xFFFFFFFFu, top);
             top_v = __reduce_max_sync(0xFFFFFFFFu, top_v);
+            // The decode warps have begun tile i - 1, so at most kRing tiles are in use.
+            if (i > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam_go, (i - 1) & 1, err));
             wild[i % kRing][lane] = static_cast<uint8_t>(bad);
             if (lane == 0) {
                 const int up = 26 - max(1, static_cast<int>(top >> 10));      // largest scale to 2^11 .. 2^12
@@ -704,16 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 value_exp[i % kRing] = static_cast<float>(-up_v);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.exam[slot]);
-            pass();
-            if (i > 0 || n_tiles == 1) {  // values of the tile before (or of the only one)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_full[slot], round & 1, err));
-                if (ok) pass();
-            }
-        }
-        if (ok && n_tiles > 1) {  // the last values
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.raw_full[slot], round & 1, err));
-            if (ok) pass();
+            if (ok && lane == 0) mbar_arrive(&bar.exam);
         }
     }
     }
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 16) {
+    if (warp == S::kIssuer) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
@@ -745,7 +748,7 @@ cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, f
     const int64_t grid = static_cast<int64_t>(p.items_per_list) * c.n_seqs * c.heads;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
     note_launch();
-    return launch_pdl(attn_prompt_kernel<D, F32, T>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, stream,
+    return launch_pdl(attn_prompt_kernel<D, F32, T>, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), S::kSmem, stream,
                       c, r, a, p);
 }
 
