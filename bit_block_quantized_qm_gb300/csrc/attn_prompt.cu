@@ -60,6 +60,17 @@ constexpr int kKeepRing = 4;  // tiles whose rows' factors are kept for the coll
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Bounded wait for up to three barriers in one loop: what costs a wait on the
+// issuing thread is not the barrier but fetching the wait's code.
+__device__ __forceinline__ bool wait_all(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc,
+                                         unsigned int* err) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kMaxWaitPolls; ++i)
+        if (mbar_try_wait(a, pa) && mbar_try_wait(b, pb) && mbar_try_wait(c, pc)) return true;
+    atomicOr(err, kErrWaitTimeout);
+    return false;
+}
+
 template <int D, bool F32>
 struct Shape {
     static constexpr int kBlocks = D / 32;
@@ -625,11 +636,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             };
             auto output = [&](int i, int m) {
                 const int stage = i % S::kStages, buf = F32 ? (i & 1) : m;
-                ok = ok && mbar_wait_bounded(&bar.p_full[buf], F32 ? (i >> 1) & 1 : i & 1, err) &&
-                     mbar_wait_bounded(&bar.v_full[stage], (i / S::kStages) & 1, err);
-                if (!ok) return;
-                // f32: the products of the tile before have been collected.
-                if (F32 && i > 0) ok = mbar_wait_bounded(&bar.o_free[0], (i - 1) & 1, err);
+                // P, V, and (f32) the accumulators that the collectors have read.
+                uint64_t* const freed = F32 && i > 0 ? &bar.o_free[0] : &bar.p_full[buf];
+                const uint32_t p_phase = F32 ? (i >> 1) & 1 : i & 1;
+                ok = ok && wait_all(&bar.p_full[buf], p_phase, &bar.v_full[stage], (i / S::kStages) & 1, freed,
+                                    F32 && i > 0 ? (i - 1) & 1 : p_phase, err);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t v0 = smem_addr(v_sm + stage * S::kOperand);
