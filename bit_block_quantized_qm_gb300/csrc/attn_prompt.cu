@@ -610,12 +610,13 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
         if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == S::kIssuer) {
         // ---- MMA issue
-        if (lane == 0 && n_tiles > 0) {
+        if (n_tiles > 0) {
+            const uint32_t lead = elect_one();
             constexpr uint32_t id_s = idesc_f16(kTile, false), id_o = idesc_f16(D, true);
             bool ok = true;
             auto scores = [&](int i, int m) {
                 const int stage = i % S::kStages;
-                ok = ok && mbar_wait_bounded(&bar.k_full[stage], (i / S::kStages) & 1, err);
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.k_full[stage], (i / S::kStages) & 1, err));
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t t_s = tmem + (F32 ? (i & 1) : m) * 128;
@@ -628,19 +629,20 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t o = static_cast<uint64_t>((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-                        mma_ss(t_s, da + o, db + o, id_s, (p | kk) != 0);
+                        mma_ss(t_s, da + o, db + o, id_s, (p | kk) != 0, lead);
                     }
                 }
-                mma_commit(&bar.s_full[F32 ? (i & 1) : m]);
-                if (m == kM - 1) mma_commit(&bar.k_empty[stage]);
+                mma_commit(&bar.s_full[F32 ? (i & 1) : m], lead);
+                if (m == kM - 1) mma_commit(&bar.k_empty[stage], lead);
             };
             auto output = [&](int i, int m) {
                 const int stage = i % S::kStages, buf = F32 ? (i & 1) : m;
                 // P, V, and (f32) the accumulators that the collectors have read.
                 uint64_t* const freed = F32 && i > 0 ? &bar.o_free[0] : &bar.p_full[buf];
                 const uint32_t p_phase = F32 ? (i >> 1) & 1 : i & 1;
-                ok = ok && wait_all(&bar.p_full[buf], p_phase, &bar.v_full[stage], (i / S::kStages) & 1, freed,
-                                    F32 && i > 0 ? (i - 1) & 1 : p_phase, err);
+                ok = ok && __all_sync(0xFFFFFFFFu, wait_all(&bar.p_full[buf], p_phase, &bar.v_full[stage],
+                                                            (i / S::kStages) & 1, freed,
+                                                            F32 && i > 0 ? (i - 1) & 1 : p_phase, err));
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t v0 = smem_addr(v_sm + stage * S::kOperand);
@@ -655,10 +657,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         mma_ts(t_o, t_p + (F32 ? (kk >> 1) * 32 + (kk & 1) * 8 : 8 * kk),
                                db + (static_cast<uint64_t>(kk * 16 * 128) >> 4), id_o,
-                               (F32 ? (p == 2) | kk : i | kk) != 0);
+                               (F32 ? (p == 2) | kk : i | kk) != 0, lead);
                 }
-                mma_commit(&bar.pv_done[m]);
-                if (m == kM - 1) mma_commit(&bar.v_empty[stage]);
+                mma_commit(&bar.pv_done[m], lead);
+                if (m == kM - 1) mma_commit(&bar.v_empty[stage], lead);
             };
             if (F32) {
 #pragma unroll 1

@@ -177,14 +177,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             *w += acc + half_sum[tok];
         }
     } else if (warp == kSumWarps) {
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect_one();
             constexpr uint32_t id = idesc_f16(kTile, false);
             bool ok = true;
 #pragma unroll 1
             for (int t = t_lo, n = 0; t <= t_hi && ok; ++t, ++n) {
                 const int buf = n & 1;
-                ok = mbar_wait_bounded(&q_full[buf], (n >> 1) & 1, err) &&
-                     (n < 2 || mbar_wait_bounded(&s_free[buf], ((n >> 1) - 1) & 1, err));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&q_full[buf], (n >> 1) & 1, err) &&
+                                                 (n < 2 || mbar_wait_bounded(&s_free[buf], ((n >> 1) - 1) & 1, err)));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t k0 = smem_addr(k_sm), q0 = smem_addr(q_sm + buf * S::kQ);
@@ -196,11 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t o = static_cast<uint64_t>((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-                        mma_ss(tmem + 128 * buf, da + o, db + o, id, (p | kk) != 0);
+                        mma_ss(tmem + 128 * buf, da + o, db + o, id, (p | kk) != 0, lead);
                     }
                 }
-                mma_commit(&q_empty[buf]);
-                mma_commit(&s_full[buf]);
+                mma_commit(&q_empty[buf], lead);
+                mma_commit(&s_full[buf], lead);
             }
         }
     } else {
