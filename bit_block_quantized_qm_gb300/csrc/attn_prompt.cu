@@ -16,33 +16,40 @@
 //     would show (2e-6 at 300 tokens, growing).
 //   bf16 rows: one piece each (queries exact, the others 11 bits), and the output
 //     accumulates in TMEM.
-// What f16's range loses are tokens 2^-33 (bf16: 2^-24) below a row's maximum.
+// What f16's range loses are tokens 2^-33 (bf16: 2^-26) below a row's maximum.
 // They can matter only to an output element to which all larger tokens add up
 // to about nothing: rows that have both are listed and done again by the plain
 // kernel.  (bf16 pieces, which have the range, need 4 products for 2^-17, or
 // give 2^-9.)
 //
 // What bounds it: f32 rows the tensor cores (6 products of 2^21 MACs per pair of
-// tiles at D = 128); bf16 rows (2 products) the tensor cores and the issue slots
-// about equally (softmax 6 instructions per score, unpacking 13 per 8 quants,
-// shared by two row tiles).
+// tiles at D = 128) behind the roles' waits for one another; bf16 rows (2
+// products) those waits: at 4096 rows, 32 heads, D = 128 (causal) the tensor
+// pipe is active 36% and the issue slots 47% of the time.  Measured: f32 rows,
+// prompt of 4096 / 8192: 379 / 1284 us, 362 / 428 TFLOP/s of the formula's
+// operations (three times that in products); bf16, 8192: 561 us, 980 TFLOP/s,
+// D = 64 541 us (the softmax is the same).
 //
 // Structure, one CTA of 24 (bf16: 20) warps per (sequence, kv head, 128 or 2 x 128 rows):
 //   8 decode warps read cells, a step ahead, and unpack them into 128-byte
 //     swizzled tiles (dims of a block in the order the nibbles unpack; Q and the
 //     output follow it); an examiner warp finds each tile's largest scales;
-//   one thread issues the MMAs: S of the next tile is queued before P V of this
+//   one warp issues the MMAs: S of the next tile is queued before P V of this
 //     one (f32), or two row tiles take turns (bf16), so the softmax of one
-//     always has products of another to run beside;
+//     always has products of another to run beside (bf16 with 64-token tiles, of
+//     which two S per row tile fit TMEM: 755 us against 560 for 8192 rows, a
+//     step's fixed costs double);
 //   8 softmax warps hold a row per thread (f32: half a row): maximum, exponentials,
 //     P back to TMEM over S (P is the A operand from there).  bf16: only when a
-//     row's maximum grows by more than 2^3 is its accumulator scaled down;
+//     row's maximum grows by more than 2^5 is its accumulator scaled down
+//     (by 2^3 that came in every sixth tile: 4% slower);
 //   f32: 4 collector warps add the tiles' products up.
 // Code is kept short on purpose (rolled loops over 32-column chunks): unrolled,
 // the roles of the four schedulers evicted one another's instructions (805 us
 // against 449 for a prompt of 4096 f32 rows).
-// f32 rows' registers: 768 threads x 80 at launch; then 256 x 72 (softmax) + 256 x
-// 64 (decode) + 128 x 168 (collectors) + 128 x 40 = 61440, all of them.
+// Registers move between the warps (setmaxnreg), from what the CTA has at launch:
+// f32 768 x 80 = 256 x 72 (softmax) + 256 x 64 (decode) + 128 x 168 (collectors) +
+// 128 x 40; bf16 640 x 96 >= 256 x 136 + 256 x 80 + 128 x 40.
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include <algorithm>
 
@@ -71,6 +78,15 @@ __device__ __forceinline__ bool wait_all(uint64_t* a, uint32_t pa, uint64_t* b, 
     return false;
 }
 
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int D, bool F32>
 struct Shape {
     static constexpr int kBlocks = D / 32;
@@ -79,12 +95,18 @@ struct Shape {
     static constexpr int kStages = F32 ? 1 : 2;       // K tiles, V tiles
     static constexpr int kPiece = kTile * D * 2;      // bytes of one piece of a tile
     static constexpr int kOperand = kPieces * kPiece;
+    static constexpr int kAhead = F32 ? 2 : 1;        // tiles whose S of a row tile is queued
     static constexpr int kHalves = F32 ? 2 : 1;       // softmax threads of a row
     // Warps: softmax, decode, (f32) collectors, then MMA issue, examiner, two idle.
     static constexpr int kCollectWarps = F32 ? 4 : 0;
     static constexpr int kIssuer = kSoftmaxWarps + kDecodeWarps + kCollectWarps;
     static constexpr int kThreads = (kIssuer + 4) * 32;
     static constexpr int kSmem = kM * kOperand + 2 * kStages * kOperand + 1024;
+    // Registers of a thread: the kernel's, and what setmaxnreg makes of them.
+    static constexpr int kRegs = F32 ? 80 : 96, kSoftmaxRegs = F32 ? 72 : 136, kDecodeRegs = F32 ? 64 : 80;
+    static constexpr int kCollectRegs = 168, kOtherRegs = 40;
+    static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kDecodeWarps * kDecodeRegs + kCollectWarps * kCollectRegs +
+                        4 * kOtherRegs) <= kThreads * kRegs, "registers of one CTA");
     static_assert(kSmem <= 232448 - 3072, "shared memory of one CTA");
 };
 
@@ -92,12 +114,12 @@ struct Shape {
 // pieces of 32 scores' P in 16 columns each; bf16: a row tile each), then P V in
 // two of 128 (f32: with P's first and second piece; bf16: a row tile each).
 constexpr uint32_t kTmemO = 256;
-constexpr float kLazy = 3.f;  // bf16: how far (log2) a maximum may be overtaken
+constexpr float kLazy = 5.f;  // bf16: how far (log2) a maximum may be overtaken
 // P is 2^kPTop at the maximum in use, and loses bits kFarBelow (log2) below it.
 template <bool F32>
-constexpr float kPTop = F32 ? 15.f : 12.f;
+constexpr float kPTop = F32 ? 15.f : 10.f;
 template <bool F32>
-constexpr float kFarBelow = F32 ? 34.f : 28.f;
+constexpr float kFarBelow = F32 ? 34.f : 26.f;
 // An element is safe from what is lost if it is this much times the square root
 // of the number of tokens: each one's error is at most 2^-25 in P's last piece
 // times a value of at most 2^6, either sign, to be 2^-18 (2^-11) of the element
@@ -179,7 +201,8 @@ struct RowEnd {
 struct Bars {
     uint64_t exam, exam_go;
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t s_full[2], p_full[2], pv_done[2];  // f32: of tile i at i % 2; bf16: of row tile m
+    uint64_t o_free;
 };
 
 template <int D, bool F32, typename T>
@@ -218,8 +241,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 4 * S::kHalves);
             mbar_init(&bar.pv_done[i], 1);
-            mbar_init(&bar.o_free[i], 4);
         }
+        mbar_init(&bar.o_free, 4);
         fence_barrier_init();
     }
     grid_dependency_wait();
@@ -309,11 +332,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
 
     if (warp < kSoftmaxWarps) {
         // ---- softmax: this thread's row
-        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (F32) regs_down<S::kSoftmaxRegs>();
+        else regs_up<S::kSoftmaxRegs>();
         // f32: the warps w and w + 4 share 32 rows, each has half of a tile's columns
         // and half of the dims; bf16: they have a row tile each.
         const int m = F32 ? 0 : warp >> 2, half = F32 ? warp >> 2 : 0;
-        constexpr int kChunks = 4 / S::kHalves;     // of 32 columns, this thread's of a tile
+        constexpr int kChunks = kTile / 32 / S::kHalves;     // of 32 columns, this thread's of a tile
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const int row = 32 * (warp & 3) + lane;
         const int rr = row0 + m * kTile + row;
@@ -335,8 +359,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
         };
 #pragma unroll 1
         for (int i = 0; i < n_tiles; ++i) {
-            const int buf = F32 ? (i & 1) : m;
-            const uint32_t t_s = tmem + lanes + buf * 128 + half * 64;
+            const int buf = F32 ? i & 1 : m;
+            const uint32_t t_s = tmem + lanes + buf * kTile + half * 64;
             // (After a wait that gave up, none is begun: the two warps of a row go on
             // through their barriers to the end.)
             if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.s_full[buf], F32 ? (i >> 1) & 1 : i & 1, err));
@@ -384,17 +408,20 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                 }
                 tc_wait_st();
             }
-            // Two passes over the row's scores: its maximum, then P.
+            // f32: two passes over the row's scores in TMEM, its maximum, then P;
+            // bf16: the scores stay in registers between the two.
             {
+                constexpr int kHeld = F32 ? 32 : 64;
+                float v[kHeld];
                 float mx = -INFINITY, low = INFINITY;
 #pragma unroll 1
-                for (int q = 0; q < kChunks; ++q) {
-                    float v[32];
-                    tmem_ld32(t_s + 32 * q, v);
+                for (int q = 0; q < kTile / S::kHalves / kHeld; ++q) {
+#pragma unroll
+                    for (int y = 0; y < kHeld; y += 32) tmem_ld32(t_s + kHeld * q + y, v + y);
                     tc_wait_ld();
                     float mx2 = -INFINITY, low2 = INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
+                    for (int e = 0; e < kHeld; e += 4) {
                         mx = fmaxf(fmaxf(mx, v[e]), v[e + 1]);
                         mx2 = fmaxf(fmaxf(mx2, v[e + 2]), v[e + 3]);
                         low = fminf(fminf(low, v[e]), v[e + 1]);
@@ -413,7 +440,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                     sum *= keep;
                     if (half == 0) row_keep[F32 ? i % kKeepRing : 0][row] = keep;  // what the sums so far are scaled by
                 } else {
-                    // The maximum in use follows only where it is overtaken by 2^3.
+                    // The maximum in use follows only where it is overtaken by 2^5.
                     const bool grow = mx > mx_used + kLazy;
                     if (__any_sync(0xFFFFFFFFu, grow)) {
                         const float next = grow ? mx : mx_used;
@@ -435,33 +462,35 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                     }
                 }
                 const float off = (mx_used == -INFINITY ? 0.f : mx_used) - v_exp - kPTop<F32>;
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 f2 = make_float2(f, f), off2 = make_float2(-off, -off);
+                float2 part[2] = {};
 #pragma unroll 1
-                for (int q = 0; q < kChunks; ++q) {
-                    float v[32];
-                    tmem_ld32(t_s + 32 * q, v);
-                    tc_wait_ld();
-                    uint32_t hi[16], lo[16];
+                for (int q = 0; q < kTile / S::kHalves / kHeld; ++q) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float p0 = exp2_approx(fmaf(v[e], f, -off));
-                        const float p1 = exp2_approx(fmaf(v[e + 1], f, -off));
-                        part[e / 2 & 3] += p0 + p1;
-                        const __half2 hw = __floats2half2_rn(p0, p1);
+                    for (int y = 0; y < kHeld; y += 32) tmem_ld32(t_s + kHeld * q + y, v + y);
+                    tc_wait_ld();
+                    uint32_t hi[kHeld / 2], lo[16];
+#pragma unroll
+                    for (int e = 0; e < kHeld; e += 2) {
+                        const float2 x = fma2(make_float2(v[e], v[e + 1]), f2, off2);
+                        const float2 pp = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        part[e / 2 & 1] = add2(part[e / 2 & 1], pp);
+                        const __half2 hw = __floats2half2_rn(pp.x, pp.y);
                         hi[e / 2] = word(hw);
                         if (F32) {
                             const float2 back = __half22float2(hw);
-                            lo[e / 2] = word(__floats2half2_rn((p0 - back.x) * kLowUp, (p1 - back.y) * kLowUp));
+                            lo[e / 2 & 15] = word(__floats2half2_rn((pp.x - back.x) * kLowUp, (pp.y - back.y) * kLowUp));
                         }
                     }
                     if (F32) {
                         tmem_st16(t_s + 32 * q, hi);
                         tmem_st16(t_s + 32 * q + 16, lo);
                     } else {
-                        tmem_st16(t_s + 16 * q, hi);
+#pragma unroll
+                        for (int y = 0; y < kHeld / 2; y += 16) tmem_st16(t_s + kHeld / 2 * q + y, hi + y);
                     }
                 }
-                sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), exp2_approx(-v_exp), sum);
+                sum = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), exp2_approx(-v_exp), sum);
             }
             tc_wait_st();
             tc_fence_before();
@@ -499,78 +528,115 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             end.finish(mx_used, lowest, n_tiles);
         }
     } else if (warp < kSoftmaxWarps + kDecodeWarps) {
-        // ---- decode: cells -> swizzled tiles, keys one tile ahead of values: keys 0,
-        // keys 1, values 0, keys 2, ...  A thread has a token and every other
-        // (D = 64: one) block of it; what it needs next is on its way while it
-        // unpacks.
-        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ---- decode: cells -> swizzled tiles.  A thread has a token and every other
+        // block of it (D = 64 and bf16: one at most); what it needs next is on its
+        // way while it unpacks.
+        regs_down<S::kDecodeRegs>();
         const int dt = threadIdx.x - kSoftmaxWarps * 32;
         const int tok = dt & (kTile - 1), blk0 = dt / kTile;
-        constexpr int kTurns = kTile * NB / (kDecodeWarps * 32), kStride = kDecodeWarps * 32 / kTile;
+        constexpr int kStride = kDecodeWarps * 32 / kTile, kTurns = NB / kStride;
         bool ok = true;
-        auto cell_at = [&](int i) -> int64_t {  // of this token in tile i
-            const int p = i < n_tiles ? tiles.at(i) * kTile + tok : seen_len;
-            return p < seen_len ? kv_cell(c, b, h, p, err) : -1;
+        auto pos_at = [&](int i) { return i < n_tiles ? tiles.at(i) * kTile + tok : seen_len; };
+        auto page_at = [&](int i) {  // of this token in tile i
+            const int p = pos_at(i);
+            return p < seen_len ? kv_page_id(c, b, p) : 0;
         };
-        uint4 q[kTurns];
-        uint32_t sc[kTurns];
-        auto fetch = [&](const uint8_t* pool, int64_t off) {
+        auto cell_at = [&](int i, int id) -> int64_t {
+            const int p = pos_at(i);
+            return p < seen_len ? kv_cell_in(c, id, h, p, err) : -1;
+        };
+        // What this thread unpacks next of a tile's keys (f32: or values) and values.
+        const int in_cell = blk0 * 256 + (tok & 15) * 16, in_scales = cell_scales(D) + ((tok & 15) * NB + blk0) * 2;
+        struct Blocks {
+            uint4 q[kTurns];
+            uint32_t sc[kTurns];
+        };
+        auto fetch = [&](Blocks& x, const uint8_t* pool, int64_t off) {
 #pragma unroll
             for (int y = 0; y < kTurns; ++y) {
-                q[y] = make_uint4(0, 0, 0, 0);
-                sc[y] = 0;
+                x.q[y] = make_uint4(0, 0, 0, 0);
+                x.sc[y] = 0;
                 if (off >= 0) {
-                    const int blk = blk0 + y * kStride;
-                    q[y] = __ldg(reinterpret_cast<const uint4*>(pool + off + blk * 256 + (tok & 15) * 16));
-                    sc[y] = __ldg(reinterpret_cast<const uint16_t*>(pool + off + cell_scales(D) + ((tok & 15) * NB + blk) * 2));
+                    x.q[y] = __ldg(reinterpret_cast<const uint4*>(pool + off + in_cell + y * kStride * 256));
+                    x.sc[y] = __ldg(reinterpret_cast<const uint16_t*>(pool + off + in_scales + y * kStride * 2));
                 }
             }
         };
-        int64_t off_v = -1, off_k = cell_at(0);  // of the tile whose values come next, and of the one after
-        fetch(c.k, off_k);
-        // One body for keys and values: the code of all roles together has to stay
-        // in the instruction cache.
-#pragma unroll 1
-        for (int step = 0; step < 2 * n_tiles; ++step) {
-            const bool v = step > 0 && ((step & 1) == 0 || step == 2 * n_tiles - 1);
-            const int i = v ? (step - 1) >> 1 : (step + 1) >> 1;
-            const int stage = i % S::kStages;
-            if (!v) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam, i & 1, err));
-                if (ok && lane == 0) mbar_arrive(&bar.exam_go);
-            }
-            if (ok && i >= S::kStages)
-                ok = mbar_wait_bounded((v ? bar.v_empty : bar.k_empty) + stage, (i / S::kStages - 1) & 1, err);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            const float f = v ? value_up[i % kRing] : key_up[i % kRing];
-            uint8_t* hi = (v ? v_sm : k_sm) + stage * S::kOperand;
-            uint4 now[kTurns];
-            float d[kTurns];
+        auto unpack = [&](const Blocks& x, bool v, float f, uint8_t* hi) {
 #pragma unroll
             for (int y = 0; y < kTurns; ++y) {
-                now[y] = q[y];
                 // Values that are not finite (NaN then comes with the scores): 0.
-                d[y] = v && (sc[y] & 0x7C00u) == 0x7C00u ? 0.f : f16_bits_to_float(sc[y]) * f;
+                const float d = v && (x.sc[y] & 0x7C00u) == 0x7C00u ? 0.f : f16_bits_to_float(x.sc[y]) * f;
+                decode_block<F32>(x.q[y], d, tok, blk0 + y * kStride, hi, hi + S::kPiece, plan.k1024);
             }
-            // The next step: keys i + 1 (i + 2 after values i), or values i - 1.
-            if (v || step == 0) {
-                off_v = off_k;
-                off_k = cell_at(i + (v ? 2 : 1));
-                if (step + 1 == 2 * n_tiles - 1) fetch(c.v, off_v);  // no more keys
-                else fetch(c.k, off_k);
-            } else {
-                fetch(c.v, off_v);
+        };
+        if constexpr (!F32) {
+            // Keys and values of a tile in one step: v_empty of a stage comes after k_empty.
+            Blocks k, v;
+            int64_t off = cell_at(0, page_at(0));
+            fetch(k, c.k, off);
+            fetch(v, c.v, off);
+            int page = page_at(1);
+#pragma unroll 1
+            for (int i = 0; i < n_tiles; ++i) {
+                const int stage = i % S::kStages;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam, i & 1, err));
+                if (ok && lane == 0) mbar_arrive(&bar.exam_go);
+                if (ok && i >= S::kStages) ok = mbar_wait_bounded(&bar.v_empty[stage], (i / S::kStages - 1) & 1, err);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                const Blocks k_now = k, v_now = v;
+                off = cell_at(i + 1, page);
+                page = page_at(i + 2);
+                fetch(k, c.k, off);
+                fetch(v, c.v, off);
+                unpack(k_now, false, key_up[i % kRing], k_sm + stage * S::kOperand);
+                unpack(v_now, true, value_up[i % kRing], v_sm + stage * S::kOperand);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.k_full[stage]);
             }
-#pragma unroll
-            for (int y = 0; y < kTurns; ++y)
-                decode_block<F32>(now[y], d[y], tok, blk0 + y * kStride, hi, hi + S::kPiece, plan.k1024);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive((v ? bar.v_full : bar.k_full) + stage);
+        } else {
+            int64_t off_v = -1, off_k = cell_at(0, page_at(0));  // of the tile whose values come next, and of the one after
+            Blocks x;
+            fetch(x, c.k, off_k);
+            int page_k = page_at(1);  // of the keys to fetch after those
+            // Keys one tile ahead of values: keys 0, keys 1, values 0, keys 2, ...
+            // One body for keys and values: the code of all roles together has to stay
+            // in the instruction cache.
+#pragma unroll 1
+            for (int step = 0; step < 2 * n_tiles; ++step) {
+                const bool v = step > 0 && ((step & 1) == 0 || step == 2 * n_tiles - 1);
+                const int i = v ? (step - 1) >> 1 : (step + 1) >> 1;
+                const int stage = i % S::kStages;
+                if (!v) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam, i & 1, err));
+                    if (ok && lane == 0) mbar_arrive(&bar.exam_go);
+                }
+                if (ok && i >= S::kStages)
+                    ok = mbar_wait_bounded((v ? bar.v_empty : bar.k_empty) + stage, (i / S::kStages - 1) & 1, err);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                const float f = v ? value_up[i % kRing] : key_up[i % kRing];
+                uint8_t* hi = (v ? v_sm : k_sm) + stage * S::kOperand;
+                const Blocks now = x;
+                // The next step: keys i + 1 (i + 2 after values i), or values i - 1.
+                if (v || step == 0) {
+                    off_v = off_k;
+                    off_k = cell_at(i + (v ? 2 : 1), page_k);
+                    if (step + 1 == 2 * n_tiles - 1) fetch(x, c.v, off_v);  // no more keys
+                    else fetch(x, c.k, off_k);
+                } else {
+                    fetch(x, c.v, off_v);
+                    page_k = page_at(i + 1);
+                }
+                unpack(now, v, f, hi);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive((v ? bar.v_full : bar.k_full) + stage);
+            }
         }
     } else if (warp < S::kIssuer) {
         // ---- collectors (f32): a row's sums in registers, o = o keep + P V tile by tile.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        regs_up<S::kCollectRegs>();
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const int row = 32 * (warp & 3) + lane, rr = row0 + row;
         float o[F32 ? D : 1];
@@ -579,7 +645,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
         bool ok = true;
 #pragma unroll 1
         for (int i = 0; i < n_tiles; ++i) {
-            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[0], i & 1, err));
+            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.pv_done[i & 1], (i >> 1) & 1, err));
             if (!ok) break;
             tc_fence_after();
             const float keep = row_keep[F32 ? i % kKeepRing : 0][row];
@@ -597,7 +663,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.o_free[0]);
+            if (lane == 0) mbar_arrive(&bar.o_free);
         }
         named_barrier_sync(5, (kSoftmaxWarps + S::kCollectWarps) * 32);
         if constexpr (F32) {
@@ -607,7 +673,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             end.finish(row_top[row], half_max[n_tiles & 1][1][row], n_tiles);
         }
     } else {
-        if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        regs_down<S::kOtherRegs>();
     if (warp == S::kIssuer) {
         // ---- MMA issue
         if (n_tiles > 0) {
@@ -619,7 +685,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                 ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.k_full[stage], (i / S::kStages) & 1, err));
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t t_s = tmem + (F32 ? (i & 1) : m) * 128;
+                const uint32_t t_s = tmem + (F32 ? i & 1 : m) * kTile;
                 const uint32_t q0 = smem_addr(q_sm + m * S::kOperand), k0 = smem_addr(k_sm + stage * S::kOperand);
                 constexpr int kProducts = F32 ? 3 : 1;  // low x high, high x low, high x high
 #pragma unroll 1
@@ -632,24 +698,26 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                         mma_ss(t_s, da + o, db + o, id_s, (p | kk) != 0, lead);
                     }
                 }
-                mma_commit(&bar.s_full[F32 ? (i & 1) : m], lead);
-                if (m == kM - 1) mma_commit(&bar.k_empty[stage], lead);
+                mma_commit(&bar.s_full[F32 ? i & 1 : m], lead);
+                if (F32) mma_commit(&bar.k_empty[stage], lead);
             };
             auto output = [&](int i, int m) {
-                const int stage = i % S::kStages, buf = F32 ? (i & 1) : m;
-                // P, V, and (f32) the accumulators that the collectors have read.
-                uint64_t* const freed = F32 && i > 0 ? &bar.o_free[0] : &bar.p_full[buf];
+                const int stage = i % S::kStages, buf = F32 ? i & 1 : m;
                 const uint32_t p_phase = F32 ? (i >> 1) & 1 : i & 1;
-                ok = ok && __all_sync(0xFFFFFFFFu, wait_all(&bar.p_full[buf], p_phase, &bar.v_full[stage],
-                                                            (i / S::kStages) & 1, freed,
-                                                            F32 && i > 0 ? (i - 1) & 1 : p_phase, err));
+                if (F32) {  // P, V, and the accumulators that the collectors have read
+                    ok = ok && __all_sync(0xFFFFFFFFu, wait_all(&bar.p_full[buf], p_phase, &bar.v_full[stage],
+                                                                (i / S::kStages) & 1, i > 0 ? &bar.o_free : &bar.p_full[buf],
+                                                                i > 0 ? (i - 1) & 1 : p_phase, err));
+                } else {  // (V came with K)
+                    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.p_full[buf], p_phase, err));
+                }
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t v0 = smem_addr(v_sm + stage * S::kOperand);
                 constexpr int kProducts = F32 ? 3 : 1;  // low x high apart, high x low, high x high
 #pragma unroll 1
                 for (int p = 0; p < kProducts; ++p) {
-                    const uint32_t t_p = tmem + buf * 128 + (F32 && p == 0 ? 16 : 0);
+                    const uint32_t t_p = tmem + buf * kTile + (F32 && p == 0 ? 16 : 0);
                     const uint32_t t_o = tmem + kTmemO + (F32 ? (p == 0 ? 128 : 0) : m * 128);
                     // V is [token][dim]: rows are the contraction, 64-dim columns kTile * 128 bytes apart.
                     const uint64_t db = desc_base(v0 + (F32 && p == 1 ? S::kPiece : 0), kTile * 128);
@@ -659,22 +727,14 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                                db + (static_cast<uint64_t>(kk * 16 * 128) >> 4), id_o,
                                (F32 ? (p == 2) | kk : i | kk) != 0, lead);
                 }
-                mma_commit(&bar.pv_done[m], lead);
+                mma_commit(&bar.pv_done[buf], lead);
                 if (m == kM - 1) mma_commit(&bar.v_empty[stage], lead);
             };
-            if (F32) {
 #pragma unroll 1
-                for (int i = -1; i < n_tiles && ok; ++i) {
-                    if (i + 1 < n_tiles) scores(i + 1, 0);
-                    if (i >= 0) output(i, 0);
-                }
-            } else {
-#pragma unroll 1
-                for (int x = -kM; x < kM * n_tiles && ok; ++x) {  // x = kM i + m
-                    const int i = (x + kM) / kM - 1, m = (x + kM) % kM;
-                    if (i >= 0) output(i, m);
-                    if (i + 1 < n_tiles) scores(i + 1, m);
-                }
+            for (int x = -S::kAhead * kM; x < kM * n_tiles && ok; ++x) {  // x = kM i + m
+                const int i = (x + S::kAhead * kM) / kM - S::kAhead, m = (x + S::kAhead * kM) % kM;
+                if (i >= 0) output(i, m);
+                if (i + S::kAhead < n_tiles) scores(i + S::kAhead, m);
             }
         }
     } else if (warp == S::kIssuer + 1) {
@@ -748,7 +808,7 @@ cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, f
                           unsigned* redo_n, unsigned* redo, cudaStream_t stream) {
     using S = Shape<D, F32>;
     static SmemOnce once;
-    cudaError_t err = once.set(attn_prompt_kernel<D, F32, T>, S::kSmem);
+    cudaError_t err = once.set(attn_prompt_kernel<D, F32, T>, S::kSmem, S::kRegs);
     if (err != cudaSuccess) return err;
     const int64_t rows = static_cast<int64_t>(r.max_q) * (a.heads / c.heads);
     PromptPlan p = {};

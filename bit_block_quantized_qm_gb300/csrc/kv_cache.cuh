@@ -42,18 +42,23 @@ __device__ __forceinline__ void kv_rows(const KvRows& r, int b, int* first, int*
     *count = e - a;
 }
 
-// Byte offset in the pool of the cell that holds token `pos` of sequence b and
-// kv head h, or -1 (and the error bit) where the page table has no page for it.
-__device__ __forceinline__ int64_t kv_cell(const KvView& c, int b, int h, int pos, unsigned int* err) {
+// The page that holds token `pos` of sequence b; -1 past the page table.
+__device__ __forceinline__ int kv_page_id(const KvView& c, int b, int pos) {
     const int page = pos >> c.page_shift;
-    int id = -1;
-    if (page < c.table_stride) id = __ldg(c.table + b * c.table_stride + page);
+    return page < c.table_stride ? __ldg(c.table + b * c.table_stride + page) : -1;
+}
+// Byte offset in the pool of the cell that holds token `pos` of a sequence, in page
+// `id`, of kv head h; -1 (and the error bit) where `id` is no page.
+__device__ __forceinline__ int64_t kv_cell_in(const KvView& c, int id, int h, int pos, unsigned int* err) {
     if (id < 0 || id >= c.n_pages) {
         atomicOr(err, kErrRange);
         return -1;
     }
     const int cells = 1 << (c.page_shift - 4);
     return ((static_cast<int64_t>(id) * c.heads + h) * cells + ((pos >> 4) & (cells - 1))) * cell_bytes(c.dim);
+}
+__device__ __forceinline__ int64_t kv_cell(const KvView& c, int b, int h, int pos, unsigned int* err) {
+    return kv_cell_in(c, kv_page_id(c, b, pos), h, pos, err);
 }
 
 // The sequence that row `row` belongs to, or -1.

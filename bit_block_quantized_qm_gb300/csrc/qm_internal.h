@@ -244,11 +244,17 @@ cudaError_t attn_prompt_read_device_error(unsigned int* bits, bool clear);
 class SmemOnce {
 public:
     template <typename... KArgs>
-    cudaError_t set(void (*kernel)(KArgs...), int bytes) {
+    cudaError_t set(void (*kernel)(KArgs...), int bytes, int least_regs = 0) {
         int dev = 0;
         cudaError_t err = cudaGetDevice(&dev);
         if (err != cudaSuccess) return err;
         if (dev < 64 && ((__atomic_load_n(&done_, __ATOMIC_ACQUIRE) >> dev) & 1u)) return cudaSuccess;
+        if (least_regs > 0) {  // a kernel that hands registers from warp to warp was built with these
+            cudaFuncAttributes attr;
+            err = cudaFuncGetAttributes(&attr, kernel);
+            if (err != cudaSuccess) return err;
+            if (attr.numRegs < least_regs) return cudaErrorLaunchOutOfResources;
+        }
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (err == cudaSuccess && dev < 64) __atomic_fetch_or(&done_, uint64_t(1) << dev, __ATOMIC_RELEASE);
         return err;

@@ -130,6 +130,23 @@ __device__ __forceinline__ void store_o4(__nv_bfloat16* p, float4 v) {
         make_uint2(word(__floats2bfloat162_rn(v.x, v.y)), word(__floats2bfloat162_rn(v.z, v.w)));
 }
 
+// Two f32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+        "fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // Byte offset of 16-byte chunk `chunk` (of 8 elements; D / 8 of them) of row
 // `row` in a piece of a tile: 64-element columns of [128 rows][128 bytes], the
 // chunks of a row permuted by row % 8.
