@@ -260,8 +260,7 @@ int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64
     return room_of(c, heads, n_tokens, weights).bytes;
 }
 
-cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,
-                        const DeviceInfo&) {
+cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
     if (attn_step_takes(c, a.heads, r.max_q)) return launch_attn_step(c, r, a, stream);
     switch (c.dim / 32) {
         case 1: return launch_plain<1>(c, r, a, stream);

@@ -13,7 +13,7 @@
 //     to the top of f16's range; each block of 32 is scaled by d_jb in f32.
 //   output  o = sum_j (p_j d_jb) (n_j - 8): dims are the rows, query rows again
 //     two columns each, p_j d_jb as f16 and the exact f16 remainder (two packed
-//     FMAs per two tokens).  p is scaled by 2^15, or less where the largest
+//     FMAs per two tokens).  p is scaled by 2^14, or less where the largest
 //     scale seen would take p d out of f16's range (then the sums follow).
 // The softmax runs in one pass with a running maximum and sum in f32.
 //
@@ -947,7 +947,9 @@ cudaError_t launch_step(const KvView& c, const KvRows& r, const AttnCall& a, cud
 }  // namespace
 
 bool attn_step_takes(const KvView& c, int heads, int64_t max_q) {
-    return (c.dim == 64 || c.dim == 128) && max_q * (heads / c.heads) <= kStepRows;
+    if (c.dim != 64 && c.dim != 128) return false;
+    const int64_t rows = max_q * (heads / c.heads), all = c.n_seqs * max_q * heads;
+    return rows <= kStepRows || (rows <= kStepRowsFew && all <= kStepAll);
 }
 
 int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {

@@ -220,7 +220,7 @@ int qm_attn_q4_0(const qm_kv_cache* cache, const qm_attn_args* a, void* stream) 
                          static_cast<int>(a->sinks < view.max_len ? a->sinks : view.max_len), a->scale,
                          a->dtype == QM_F32 ? qm::KvType::kF32 : qm::KvType::kBF16,
                          static_cast<uint8_t*>(a->workspace)};
-    return from_cuda(qm::launch_attn(view, rows, call, static_cast<cudaStream_t>(stream), dev));
+    return from_cuda(qm::launch_attn(view, rows, call, static_cast<cudaStream_t>(stream)));
 }
 
 int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float* weights, int64_t weights_stride,
@@ -265,7 +265,7 @@ int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float
     if (rc != QM_OK) return rc;
     const qm::EvictCall e = {weights, weights_out, kept, to->lengths, weights_stride, out_stride,
                              static_cast<int>(budget), static_cast<int>(sinks), static_cast<int>(recent)};
-    return from_cuda(qm::launch_kv_evict(src, dst, e, static_cast<cudaStream_t>(stream), dev));
+    return from_cuda(qm::launch_kv_evict(src, dst, e, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -446,8 +446,7 @@ cudaError_t launch_kv_read(const KvView& c, const KvRows& r, float* k, float* v,
     return by_blocks<Read>(c.dim, c, r, k, v, stream);
 }
 
-cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCall& e, cudaStream_t stream,
-                            const DeviceInfo& /*dev*/) {
+cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCall& e, cudaStream_t stream) {
     // The lengths are read until the last cell has moved: where the new ones go to
     // the same array they are written by a kernel of their own.
     const bool same_lengths = src.lengths == e.lengths_out;

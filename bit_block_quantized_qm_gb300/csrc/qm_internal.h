@@ -197,12 +197,24 @@ struct AttnCall {
 
 // Bytes of workspace that launch_attn needs for these sizes.
 int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
-cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream,
-                        const DeviceInfo& dev);
+cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);
 
-// Few rows (attn_step.cu): head dimensions 64 and 128, at most kStepRows rows
-// (tokens times query heads of a kv head) per sequence and kv head.
-constexpr int kStepRows = 32;
+// Few rows (attn_step.cu): head dimensions 64 and 128.  Its time grows with the
+// rows (tokens times query heads of a kv head); the prompt kernel's hardly does
+// up to 128, but each of its CTAs reads a whole context alone.  So it takes few
+// rows of a list, kStepRows, and up to kStepRowsFew where there are few in all,
+// kStepAll over all sequences and heads.  Both sides, this kernel against the prompt kernel
+// (f32; its bf16 form is 15% faster), 32 heads of 8 kv heads, context 4096:
+//   16 sequences:  16 rows 61 / 93 us, 32 rows 113 / 93, 64 rows 211 / 95
+//   1 sequence:    128 rows (1024 in all) 37 / 93, 256 (2048) 60 / 93,
+//                  384 (3072) 89 / 94, 512 (4096) 109 / 94
+//   context 1024:  256 rows (2048) 20 / 35, 512 (4096) 47 / 35
+// and with weights, whose kernel goes through a list's rows one by one (the rule
+// does not look at them, so that asking for them changes no output):
+//   1 sequence:    128 rows (1024) 64 / 111 us, 256 (2048) 110 / 117
+//   context 1024:  64 rows (512) 27 / 41, 256 (2048) 60 / 50
+//   2 kv heads of 4: 256 rows (512) 68 / 95, 1024 (2048) 234 / 110
+constexpr int kStepRows = 24, kStepRowsFew = 256, kStepAll = 2048;
 bool attn_step_takes(const KvView& c, int heads, int64_t max_q);
 int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
 cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);
@@ -272,8 +284,7 @@ struct EvictCall {
     int64_t weights_stride, out_stride;
     int budget, sinks, recent;
 };
-cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCall& e, cudaStream_t stream,
-                            const DeviceInfo& dev);
+cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCall& e, cudaStream_t stream);
 cudaError_t kv_read_device_error(unsigned int* bits, bool clear);
 cudaError_t attn_read_device_error(unsigned int* bits, bool clear);
 

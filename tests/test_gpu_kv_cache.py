@@ -154,6 +154,41 @@ def test_attention_scale_and_sharp_scores(qm, dtype, new):
     check_attend(qm, c, [new, min(new, 90)], 8, dtype, scale=-0.07)
 
 
+# Between the two: more rows than a step's and few in all, and long prompts
+# (more token tiles than any ring in the kernels has slots, windows that skip some).
+BETWEEN = [
+    ([1700], [50], 2, 4, 128, 16, 0, 0),
+    ([900, 33, 400], [40, 33, 2], 1, 6, 64, 32, 0, 0),
+    ([1500, 700], [25, 17], 2, 8, 128, 128, 300, 5),
+    ([70], [63], 4, 4, 128, 64, 0, 0),
+    ([1650, 1100], [90, 700], 1, 4, 128, 64, 0, 0),
+    ([1650], [1650], 1, 2, 64, 16, 0, 0),
+    ([2100, 300], [400, 300], 2, 2, 128, 32, 700, 150),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("weights", [False, True], ids=["", "weights"])
+@pytest.mark.parametrize("case", BETWEEN, ids=lambda c: "-".join(str(x).replace(" ", "") for x in c))
+def test_attention_between_and_long(qm, case, weights, dtype):
+    lengths, new, kv, group, dim, page, window, sinks = case
+    c = ko.Cache(lengths, kv, dim, page, seed=len(lengths) + page)
+    check_attend(qm, c, new, kv * group, dtype, window, sinks, weights=weights)
+
+
+def test_attention_calls_share_a_workspace(qm):
+    """Steps, drafts, chunks and prompts in turn on one cache, with weights and without, twice over."""
+    c = ko.Cache([640, 300], 2, 128, 32, seed=9)
+    cache = device(qm, c)
+    first = []
+    for turn in range(2):
+        for k, (new, weights) in enumerate([(1, True), (200, False), (1, False), (7, True), (130, True), (3, False), (60, False)]):
+            out, lse = check_attend(qm, c, [new, new], 8, F32, weights=weights, cache=cache)
+            if turn == 0:
+                first.append((out.clone(), lse.clone()))
+            assert torch.equal(out, first[k][0]) and torch.equal(lse, first[k][1])
+
+
 @pytest.mark.parametrize("v_scale", [2.0 ** -13, 37.0, 6000.0])
 @pytest.mark.parametrize("k_scale", [2.0 ** -12, 1.0, 7000.0])
 @pytest.mark.parametrize("new", [1, 70], ids=["step", "prompt"])
