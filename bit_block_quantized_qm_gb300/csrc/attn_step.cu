@@ -17,10 +17,13 @@
 //     scale seen would take p d out of f16's range (then the sums follow).
 // The softmax runs in one pass with a running maximum and sum in f32.
 //
-// Bytes bound it: 9 D / 8 per token and kv head.  A tensor-core product covers
+// Bytes are its floor: 9 D / 8 per token and kv head.  A tensor-core product covers
 // 256 quants = 144 bytes, which HBM delivers in 6 cycles per SM; unpacking on
 // the FP32 pipe alone (one FMA per quant and query row) would need 3 times
-// that at four rows.
+// that at four rows.  What bounds it as it is: 345 instructions per 16 tokens,
+// keys, softmax and values together (issue slots 60% busy).  Measured, 32 heads
+// of 8 kv heads, D = 128: 64 sequences of 8192 tokens 129 us, 4.7 TB/s; ragged
+// ones of up to 8192 97 us, 3.9 TB/s; one of 131071 47 us, 3.2 TB/s.
 //
 // Split.  All (sequence, kv head, 4 or 8 rows) lists of 64-token tiles lie end to
 // end, and every CTA of a grid that fills the GPU once takes an equal stretch
@@ -867,30 +870,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
 // weights[b][h][j] += sum over rows of exp(s - lse), from the scores that the
 // step left in the workspace: one thread per token.  Reads 4 bytes per row
 // and token; recomputing the scores would read the keys again (72 bytes per
-// token at D = 128, as much as 18 rows).
+// token at D = 128, as much as 18 rows).  32 sequences of 4096 (ragged), 4 rows
+// each: 14 us beside the step's 40.
+constexpr int kMostRows = std::max(kStepRows, kStepRowsFew);  // of a list
 __global__ void __launch_bounds__(256) attn_step_weights_kernel(KvView c, KvRows r, AttnCall a, StepPlan plan) {
     grid_launch_dependents();
     grid_dependency_wait();
+    __shared__ float row_lse[kMostRows];
     const int h = blockIdx.y, b = blockIdx.z;
     const int j = blockIdx.x * 256 + threadIdx.x;
     int first, count;
     kv_rows(r, b, &first, &count, &g_attn_step_error);
     const int L = kv_length(c, b, &g_attn_step_error);
-    if (j >= L) return;
     const int group = a.heads / c.heads;
+    const float* lse = reinterpret_cast<const float*>(a.ws + plan.lse_off) + h * group;
+    for (int x = threadIdx.x; x < count * group; x += 256) {
+        const int i = x / group;
+        row_lse[x] = __ldg(lse + static_cast<int64_t>(first + i) * a.heads + (x - i * group));
+    }
+    __syncthreads();
+    if (j >= L) return;
     const int base_pos = L - count;
     const float* stash = reinterpret_cast<const float*>(a.ws + plan.stash_off) +
                          (static_cast<int64_t>(b) * c.heads + h) * (r.max_q * group) * plan.pad_len + j;
-    const float* lse = reinterpret_cast<const float*>(a.ws + plan.lse_off);
+    // The rows that see token j lie together.
+    const int end = a.window > 0 && j >= a.sinks ? min(count, max(0, j + a.window - base_pos)) : count;
     float acc = 0.f;
-    for (int i = max(0, j - base_pos); i < count; ++i) {
-        const int pos = base_pos + i;
-        if (a.window > 0 && j <= pos - a.window && j >= a.sinks) break;
-        for (int x = 0; x < group; ++x) {
-            const float s = __ldcs(stash + static_cast<int64_t>(i * group + x) * plan.pad_len);
-            acc += exp2_approx(s - __ldg(lse + static_cast<int64_t>(first + i) * a.heads + h * group + x));
-        }
-    }
+#pragma unroll 8
+    for (int x = max(0, j - base_pos) * group; x < end * group; ++x)
+        acc += exp2_approx(__ldcs(stash + static_cast<int64_t>(x) * plan.pad_len) - row_lse[x]);
     float* w = a.weights + (static_cast<int64_t>(b) * c.heads + h) * a.weights_stride + j;
     *w += acc;
 }
