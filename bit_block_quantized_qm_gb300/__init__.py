@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = [
@@ -111,6 +112,10 @@ class QmAttnArgs(ctypes.Structure):
                 ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("weights_stride", ctypes.c_int64),
                 ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("n_heads", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+_ATTN_ARGS = struct.Struct("@6P9qfii4x")  # the same, packed
+assert _ATTN_ARGS.size == ctypes.sizeof(QmAttnArgs)
 
 
 class QMError(RuntimeError):
@@ -269,8 +274,21 @@ def qm_gemv_q4_0_q8act_list_ptr(problems, M: int, counters: int = 0, stream: int
 
 # ------------------------------------------------------------ torch tensors
 
+_torch = None
+
+
+def _torch_module():
+    """torch, which the package itself does not import: an import statement in
+    every call costs a small call 2 us of its 18."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream_handle(stream) -> int:
-    import torch
+    torch = _torch or _torch_module()
     if stream is None:
         # The current stream's handle without building a Stream object around it
         # (6 us of a small call's 25).
@@ -282,7 +300,7 @@ def _stream_handle(stream) -> int:
 
 
 def _require(t, dtype, name):
-    import torch
+    torch = _torch or _torch_module()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -535,7 +553,7 @@ class KVCache:
 
 def _rows(t, heads, dim, name):
     """Check a [n_tokens, heads, dim] tensor whose rows may be strided; (dtype code, row stride)."""
-    import torch
+    torch = _torch or _torch_module()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype == torch.float32:
@@ -556,7 +574,7 @@ def _rows(t, heads, dim, name):
 
 
 def _starts(q_starts, n_seqs):
-    import torch
+    torch = _torch or _torch_module()
     if q_starts is None:
         return 0
     _require(q_starts, torch.int32, "q_starts")
@@ -582,16 +600,17 @@ def qm_kv_append_q4_0(cache, k, v, q_starts=None, stream=None):
 def qm_kv_read_q4_0(cache, n_tokens: int, q_starts=None, k=None, v=None, stream=None):
     """The f32 values of the last rows of each sequence, ``(k, v)`` of shape
     ``[n_tokens, n_kv_heads, head_dim]``."""
-    import torch
+    torch = _torch or _torch_module()
     shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _require(t, torch.float32, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {shape}")
     if k is None:
         k = torch.empty(shape, dtype=torch.float32, device=cache.k_pages.device)
     if v is None:
         v = torch.empty(shape, dtype=torch.float32, device=cache.k_pages.device)
-    for t, name in ((k, "k"), (v, "v")):
-        _require(t, torch.float32, name)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {shape}")
     _check(load_library().qm_kv_read_q4_0(cache.ref, k.data_ptr(), v.data_ptr(), n_tokens,
                                           _starts(q_starts, cache.n_seqs), _stream_handle(stream)),
            "qm_kv_read_q4_0")
@@ -616,17 +635,19 @@ def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts
     n_kv_heads, >= max_len]`` is added each token's attention weight; ``max_q``
     bounds the rows of one sequence (default: all rows).  The workspace is the
     cache's own, one per stream."""
-    import torch
+    torch = _torch or _torch_module()
     code, qs = _rows(q, None, cache.head_dim, "q")
     n_tokens, n_heads = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    code_o, os_ = _rows(out, n_heads, cache.head_dim, "out")
-    if code_o != code or out.shape[0] != n_tokens:
-        raise ValueError("out differs from q in type or shape")
-    if lse is None and return_lse:
-        lse = torch.empty((n_tokens, n_heads), dtype=torch.float32, device=q.device)
-    if lse is not None:
+        out, os_ = torch.empty(q.shape, dtype=q.dtype, device=q.device), n_heads * cache.head_dim
+    else:
+        code_o, os_ = _rows(out, n_heads, cache.head_dim, "out")
+        if code_o != code or out.shape[0] != n_tokens:
+            raise ValueError("out differs from q in type or shape")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((n_tokens, n_heads), dtype=torch.float32, device=q.device)
+    else:
         _require(lse, torch.float32, "lse")
         if tuple(lse.shape) != (n_tokens, n_heads):
             raise ValueError("lse must be [n_tokens, n_heads]")
@@ -643,12 +664,13 @@ def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts
         max_q = n_tokens
     handle = _stream_handle(stream)
     ws = cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle)
-    args = QmAttnArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                      weights.data_ptr() if weights is not None else None, starts or None,
-                      ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, n_tokens, max_q,
-                      qs, os_, ws_stride, window, sinks, n_heads,
-                      cache.head_dim ** -0.5 if scale is None else scale, code, 0)
-    _check(load_library().qm_attn_q4_0(cache.ref, ctypes.addressof(args), handle), "qm_attn_q4_0")
+    # (The struct's bytes; filling a ctypes object field by field takes 2 us more.)
+    args = _ATTN_ARGS.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
+                           weights.data_ptr() if weights is not None else 0, starts,
+                           ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0, n_tokens, max_q,
+                           qs, os_, ws_stride, window, sinks, n_heads,
+                           cache.head_dim ** -0.5 if scale is None else scale, code, 0)
+    _check(load_library().qm_attn_q4_0(cache.ref, args, handle), "qm_attn_q4_0")
     return out if lse is None else (out, lse)
 
 
@@ -658,17 +680,19 @@ def qm_kv_evict_q4_0(cache, to, weights, budget: int, sinks: int = 0, recent: in
     ranked by ``weights`` (f32 ``[n_seqs, n_kv_heads, >= max_len]``), into the
     cache ``to`` (or in place, with ``to`` the same cache); see include/qm.h.
     Returns ``(kept, weights_out)``."""
-    import torch
+    torch = _torch or _torch_module()
     lists = (cache.n_seqs, cache.n_kv_heads)
     _require(weights, torch.float32, "weights")
     if weights.dim() != 3 or tuple(weights.shape[:2]) != lists:
         raise ValueError("weights must be [n_seqs, n_kv_heads, max_len]")
     if kept is None:
         kept = torch.empty((*lists, budget), dtype=torch.int32, device=weights.device)
+    else:
+        _require(kept, torch.int32, "kept")
     if weights_out is None:
         weights_out = torch.empty((*lists, budget), dtype=torch.float32, device=weights.device)
-    _require(kept, torch.int32, "kept")
-    _require(weights_out, torch.float32, "weights_out")
+    else:
+        _require(weights_out, torch.float32, "weights_out")
     if tuple(kept.shape) != (*lists, budget) or weights_out.dim() != 3 or tuple(weights_out.shape[:2]) != lists:
         raise ValueError("kept must be [n_seqs, n_kv_heads, budget], weights_out [n_seqs, n_kv_heads, >= budget]")
     _check(load_library().qm_kv_evict_q4_0(cache.ref, to.ref, weights.data_ptr(), weights.shape[2], budget, sinks,
