@@ -12,20 +12,34 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void load8(const float* p, float x[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-// (8-byte aligned)
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float x[8]) {
-    const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+// Eight elements as they lie in memory (bf16: 8-byte aligned), and as floats.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     }
-}
+    __device__ __forceinline__ void get(float x[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+    uint2 a, b;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
+    }
+    __device__ __forceinline__ void get(float x[8]) const {
+        const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+};
 
 // Q4_0 quantization of a block of 32 by 4 lanes of 8 elements each (i: the lane's
 // number in the block): m = the first element of largest magnitude, d = m / -8,
@@ -118,10 +132,11 @@ struct RowWork {
 
 // Memory-bound: 4 (or 2) bytes read and 9/16 written per element; about 100
 // instructions per 8 elements of a lane.  Measured: 8 ragged prompts of up to 4096
-// rows, 8 kv heads, D = 128, bf16: 47 us, 3.1 TB/s (latency of the rows' first loads
-// and a head's at a time after them).
+// rows, 8 kv heads, D = 128, bf16: 42 us, 3.5 TB/s; with the read back 89 us.
+// Warps to switch between matter more than loads in flight: 6 CTAs per SM with
+// 32 bytes a lane ahead 89 us, 4 with 64 bytes 94, 8 (which spills) 102.
 template <int NB, typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
     kv_append_kernel(KvView c, KvRows r, const T* k, const T* v, int64_t k_stride, int64_t v_stride, int heads_each) {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -129,14 +144,18 @@ __global__ void __launch_bounds__(kThreads)
     const T* src = (w.is_v ? v + w.row * v_stride : k + w.row * k_stride) + 32 * w.blk + 8 * w.i;
     uint8_t* pool = w.is_v ? c.v : c.k;
     const int slot = w.pos & 15;
-    float next[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (w.in && w.h_first < w.h_end) load8(src + w.h_first * (32 * NB), next);
-#pragma unroll 2
+    constexpr int kAhead = 4 / sizeof(T);  // heads whose elements are on their way: 32 bytes a lane
+    Eight<T> ahead[kAhead] = {};
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x)
+        if (w.in && w.h_first + x < w.h_end) ahead[x].load(src + (w.h_first + x) * (32 * NB));
+#pragma unroll 1
     for (int h = w.h_first; h < w.h_end; ++h) {
         float y[8];
+        ahead[0].get(y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = next[e];
-        if (w.in && h + 1 < w.h_end) load8(src + (h + 1) * (32 * NB), next);
+        for (int x = 0; x + 1 < kAhead; ++x) ahead[x] = ahead[x + 1];
+        if (w.in && h + kAhead < w.h_end) ahead[kAhead - 1].load(src + (h + kAhead) * (32 * NB));
         uint32_t scale;
         uint2 q = quantize_q4_lane(y, w.i, &scale);
         // Lanes 0, 1 of a block have the low nibbles of bytes 0 .. 7, 8 .. 15, lanes 2, 3 the high ones.
