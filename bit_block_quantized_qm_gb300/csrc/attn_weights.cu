@@ -9,15 +9,17 @@
 // tiles, two stages), with log2 units and the rows' logarithms beside them.
 //   f32 rows: the three products of attn_prompt.cu; bf16 rows: the query's one
 //   piece by both pieces of the key (here the sums keep f32's bits).
-// 2 D flops per row and token and product.  A tile's MMAs need 1.5 K cycles (f32)
-// and its exponentials 1 K; what bounds it is the way of a row tile's pieces (64 KB)
-// from L2 through two stages, 4.8 K cycles a tile, 3.3 TB/s over the GPU.  Measured:
-// two prompts of 2047 f32 rows, window 1024: 202 us (234 with the row factors read
-// after the wait for their place); 4096 bf16 rows, causal: 166 us.
+// 2 D flops per row and token and product.  A tile's MMAs need 1.5 K cycles (f32;
+// bf16 1 K) and its exponentials 1 K; what bounds it is the way of a row tile's
+// pieces (64 KB; bf16 32 KB) from L2, 10 to 14 bytes a cycle and SM, which the
+// number of copies that a tile is fetched in does not change.  Measured: two
+// prompts of 2047 f32 rows, window 1024: 150 us (202 with 8 summing warps, 234 also
+// with the row factors read after the wait for their place); 4096 bf16 rows,
+// causal: 156 us (173 with two stages).
 //
-// A CTA of 10 warps per (sequence, kv head, 128 tokens), the tokens that most rows
-// see first: eight warps sum (two per 32 tokens, half of the rows each), one
-// thread issues the MMAs into two TMEM buffers, one warp loads.
+// A CTA of 18 warps per (sequence, kv head, 128 tokens), the tokens that most rows
+// see first: 16 warps sum (four per 32 tokens, a quarter of the rows each), one
+// issues the MMAs into two TMEM buffers, one loads.
 #include "tcgen05.cuh"
 
 namespace qm {
@@ -26,16 +28,18 @@ __device__ unsigned int g_attn_weights_error = 0;
 
 namespace {
 
-constexpr int kSumWarps = 8;
+constexpr int kSumWarps = 16;
 constexpr int kThreads = (kSumWarps + 2) * 32;
-constexpr int kRing = 4;  // row tiles whose factors and positions are kept
+constexpr int kRing = 8;  // row tiles whose factors and positions are kept
 
 template <int D, bool F32>
 struct WShape {
     static constexpr int kBlocks = D / 32;
     static constexpr int kPiece = kTile * D * 2;
     static constexpr int kQ = (F32 ? 2 : 1) * kPiece;
-    static constexpr int kSmem = 2 * kPiece + 2 * kQ + 1024;
+    static constexpr int kStages = D == 128 && F32 ? 2 : 4;  // row tiles on their way or in use
+    static constexpr int kSmem = 2 * kPiece + kStages * kQ + 1024;
+    static_assert(kStages + 2 <= kRing, "a place is free when MMAs two tiles after its own have begun");
 };
 
 template <int D, bool F32>
@@ -44,25 +48,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     using S = WShape<D, F32>;
     constexpr int NB = S::kBlocks;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], f_full[kRing];
+    __shared__ uint64_t q_full[S::kStages], q_empty[S::kStages], s_full[2], s_free[2], f_full[kRing];
     __shared__ uint32_t tmem_slot;
     __shared__ unsigned s_top;
     // Of rows 2 r, 2 r + 1: the units of their scores, minus the log2 of their sums.
     __shared__ __align__(16) float factor[kRing][2 * kTile];
     __shared__ int row_pos[kRing][kTile];
-    __shared__ float half_sum[kTile];
+    __shared__ float part_sum[3][kTile];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* k_sm = base;                 // [2 pieces]
-    uint8_t* q_sm = k_sm + 2 * S::kPiece;  // [2 stages][pieces]
+    uint8_t* q_sm = k_sm + 2 * S::kPiece;  // [stages][pieces]
     unsigned int* const err = &g_attn_weights_error;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&s_free[i], kSumWarps);
+        }
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
         }
         for (int i = 0; i < kRing; ++i) mbar_init(&f_full[i], 1);
         fence_barrier_init();
@@ -134,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_slot;
 
     if (warp < kSumWarps) {
-        const int half = warp >> 2;
+        const int part = warp >> 2;  // this warp's 32 rows of a row tile
         const int tok = 32 * (warp & 3) + lane, key = key0 + tok;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         float acc = 0.f;
@@ -149,37 +155,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int p_lo = base_pos + t * kTile / group, p_hi = base_pos + (t * kTile + kTile - 1) / group;
             const bool masked = key0 + kTile - 1 > p_lo ||
                                 (a.window > 0 && key0 <= p_hi - a.window && key0 + kTile > a.sinks);
-            float2 part = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-                float v[32];
-                const int col = 64 * half + 32 * q;
-                tmem_ld32(tmem + lanes + 128 * buf + col, v);
-                tc_wait_ld();
-                if (masked) {
+            float2 sum = make_float2(0.f, 0.f);
+            float v[32];
+            const int col = 32 * part;
+            tmem_ld32(tmem + lanes + 128 * buf + col, v);
+            tc_wait_ld();
+            if (masked) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int p = row_pos[at][col + e];
-                        if (key > p || (a.window > 0 && key <= p - a.window && key >= a.sinks)) v[e] = -INFINITY;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float4 f = *reinterpret_cast<const float4*>(&factor[at][2 * (col + e)]);  // units, then logarithms
-                    const float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
-                    part = add2(part, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+                for (int e = 0; e < 32; ++e) {
+                    const int p = row_pos[at][col + e];
+                    if (key > p || (a.window > 0 && key <= p - a.window && key >= a.sinks)) v[e] = -INFINITY;
                 }
             }
-            acc += part.x + part.y;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float4 f = *reinterpret_cast<const float4*>(&factor[at][2 * (col + e)]);  // units, then logarithms
+                const float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+                sum = add2(sum, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+            }
+            acc += sum.x + sum.y;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_free[buf]);
         }
-        if (half == 1) half_sum[tok] = acc;
+        if (part > 0) part_sum[part - 1][tok] = acc;
         named_barrier_sync(1, kSumWarps * 32);
-        if (half == 0 && key < L) {
+        if (part == 0 && key < L) {
             float* w = a.weights + (static_cast<int64_t>(b) * c.heads + h) * a.weights_stride + key;
-            *w += acc + half_sum[tok];
+            *w += (acc + part_sum[0][tok]) + (part_sum[1][tok] + part_sum[2][tok]);
         }
     } else if (warp == kSumWarps) {
         {
@@ -188,12 +191,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
 #pragma unroll 1
             for (int t = t_lo, n = 0; t <= t_hi && ok; ++t, ++n) {
-                const int buf = n & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&q_full[buf], (n >> 1) & 1, err) &&
+                const int buf = n & 1, stage = n % S::kStages;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&q_full[stage], (n / S::kStages) & 1, err) &&
                                                  (n < 2 || mbar_wait_bounded(&s_free[buf], ((n >> 1) - 1) & 1, err)));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t k0 = smem_addr(k_sm), q0 = smem_addr(q_sm + buf * S::kQ);
+                const uint32_t k0 = smem_addr(k_sm), q0 = smem_addr(q_sm + stage * S::kQ);
                 constexpr int kProducts = F32 ? 3 : 2;  // low x high, (high x low,) high x high
 #pragma unroll 1
                 for (int p = 0; p < kProducts; ++p) {
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_ss(tmem + 128 * buf, da + o, db + o, id, (p | kk) != 0, lead);
                     }
                 }
-                mma_commit(&q_empty[buf], lead);
+                mma_commit(&q_empty[stage], lead);
                 mma_commit(&s_full[buf], lead);
             }
         }
@@ -230,13 +233,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
 #pragma unroll 1
         for (int t = t_lo, n = 0; t <= t_hi && ok; ++t, ++n) {
-            const int buf = n & 1, at = n % kRing;
-            // (The MMAs of tile n - 2 came after the sums of tile n - 4.)
-            if (n >= 2) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&q_empty[buf], ((n >> 1) - 1) & 1, err));
+            const int stage = n % S::kStages, at = n % kRing;
+            // (The MMAs of tile n - kStages came after the sums of two tiles before it.)
+            if (n >= S::kStages)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&q_empty[stage], (n / S::kStages - 1) & 1, err));
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&q_full[buf], S::kQ);
-                bulk_load_1d(q_sm + buf * S::kQ, qt.images + (tile0 + t) * S::kQ, S::kQ, &q_full[buf]);
+                mbar_arrive_expect_tx(&q_full[stage], S::kQ);
+                bulk_load_1d(q_sm + stage * S::kQ, qt.images + (tile0 + t) * S::kQ, S::kQ, &q_full[stage]);
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
