@@ -6,16 +6,14 @@
 // sum stays in its thread and has one owner and a fixed order.  The keys are
 // unpacked once per CTA; the queries come as the f16 pieces that the attention
 // kernel before it made of them and left in the workspace (bulk copies of whole
-// tiles, two stages), with log2 units and the rows' logarithms beside them.
+// tiles), with log2 units and the rows' logarithms beside them.
 //   f32 rows: the three products of attn_prompt.cu; bf16 rows: the query's one
 //   piece by both pieces of the key (here the sums keep f32's bits).
 // 2 D flops per row and token and product.  A tile's MMAs need 1.5 K cycles (f32;
-// bf16 1 K) and its exponentials 1 K; what bounds it is the way of a row tile's
-// pieces (64 KB; bf16 32 KB) from L2, 10 to 14 bytes a cycle and SM, which the
-// number of copies that a tile is fetched in does not change.  Measured: two
-// prompts of 2047 f32 rows, window 1024: 150 us (202 with 8 summing warps, 234 also
-// with the row factors read after the wait for their place); 4096 bf16 rows,
-// causal: 156 us (173 with two stages).
+// bf16 1 K) and its exponentials 1 K.  Measured: two prompts of 2047 f32 rows,
+// window 1024: 87 us, tensor pipe active 54% of the time (150 with masks taken from
+// positions in shared memory, 202 also with 8 summing warps); 4096 bf16 rows, causal:
+// 140 us, as long as the CTA takes whose tokens all rows see.
 //
 // A CTA of 18 warps per (sequence, kv head, 128 tokens), the tokens that most rows
 // see first: 16 warps sum (four per 32 tokens, a quarter of the rows each), one
@@ -30,7 +28,7 @@ namespace {
 
 constexpr int kSumWarps = 16;
 constexpr int kThreads = (kSumWarps + 2) * 32;
-constexpr int kRing = 8;  // row tiles whose factors and positions are kept
+constexpr int kRing = 8;  // row tiles whose factors are kept
 
 template <int D, bool F32>
 struct WShape {
@@ -53,7 +51,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ unsigned s_top;
     // Of rows 2 r, 2 r + 1: the units of their scores, minus the log2 of their sums.
     __shared__ __align__(16) float factor[kRing][2 * kTile];
-    __shared__ int row_pos[kRing][kTile];
     __shared__ float part_sum[3][kTile];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* k_sm = base;                 // [2 pieces]
@@ -143,6 +140,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int part = warp >> 2;  // this warp's 32 rows of a row tile
         const int tok = 32 * (warp & 3) + lane, key = key0 + tok;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        // The rows that see this token lie together: from position key on, and (a window)
+        // up to key + window - 1.
+        const int r_first = min(max(key - base_pos, 0), count) * group;
+        const int64_t last = a.window > 0 && key >= a.sinks ? static_cast<int64_t>(key) + a.window - base_pos : count;
+        const int r_end = key < L ? static_cast<int>(min(max(last, static_cast<int64_t>(0)), static_cast<int64_t>(count))) * group : 0;
+        auto below = [](int n) -> uint32_t { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
         float acc = 0.f;
         bool ok = true;
 #pragma unroll 1
@@ -152,28 +155,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              mbar_wait_bounded(&s_full[buf], (n >> 1) & 1, err));
             if (!ok) break;
             tc_fence_after();
-            const int p_lo = base_pos + t * kTile / group, p_hi = base_pos + (t * kTile + kTile - 1) / group;
-            const bool masked = key0 + kTile - 1 > p_lo ||
-                                (a.window > 0 && key0 <= p_hi - a.window && key0 + kTile > a.sinks);
-            float2 sum = make_float2(0.f, 0.f);
-            float v[32];
-            const int col = 32 * part;
-            tmem_ld32(tmem + lanes + 128 * buf + col, v);
-            tc_wait_ld();
-            if (masked) {
+            const int col = 32 * part, r0 = t * kTile + col;
+            const uint32_t sees = below(r_end - r0) & ~below(r_first - r0);
+            if (__any_sync(0xFFFFFFFFu, sees != 0)) {
+                float2 sum = make_float2(0.f, 0.f);
+                float v[32];
+                tmem_ld32(tmem + lanes + 128 * buf + col, v);
+                tc_wait_ld();
+                if (__any_sync(0xFFFFFFFFu, sees != ~0u)) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int p = row_pos[at][col + e];
-                    if (key > p || (a.window > 0 && key <= p - a.window && key >= a.sinks)) v[e] = -INFINITY;
+                    for (int e = 0; e < 32; ++e)
+                        if (!((sees >> e) & 1u)) v[e] = -INFINITY;
                 }
-            }
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float4 f = *reinterpret_cast<const float4*>(&factor[at][2 * (col + e)]);  // units, then logarithms
-                const float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
-                sum = add2(sum, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 f = *reinterpret_cast<const float4*>(&factor[at][2 * (col + e)]);  // units, then logarithms
+                    const float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+                    sum = add2(sum, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+                }
+                acc += sum.x + sum.y;
             }
-            acc += sum.x + sum.y;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_free[buf]);
@@ -215,17 +216,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // Loads.  A row's logarithm and unit are read a tile ahead.
         float z[4], u[4];
-        int pos[4];
         auto fetch = [&](int t) {
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const int row = 32 * y + lane, rr = t * kTile + row, i = rr / group;
                 z[y] = -INFINITY, u[y] = 0.f;  // no such row
-                pos[y] = -1;
                 if (t <= t_hi && rr < count * group) {
                     z[y] = __ldcg(lse2 + static_cast<int64_t>(first + i) * a.heads + h * group + (rr - i * group));
                     u[y] = __ldcg(qt.units + (tile0 + t) * kTile + row);
-                    pos[y] = base_pos + i;
                 }
             }
         };
@@ -250,7 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* f = &factor[at][4 * (row >> 1) + (row & 1)];
                 f[0] = sees ? fmaxf(u[y] * key_unit, 0x1p-100f) : 1.f;
                 f[2] = sees ? -z[y] : -INFINITY;
-                row_pos[at][row] = pos[y];
             }
             fetch(t + 1);
             __syncwarp();
