@@ -107,7 +107,7 @@ struct Shape {
     static constexpr int kCollectRegs = 168, kOtherRegs = 40;
     static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kDecodeWarps * kDecodeRegs + kCollectWarps * kCollectRegs +
                         4 * kOtherRegs) <= kThreads * kRegs, "registers of one CTA");
-    static_assert(kSmem <= 232448 - 3072, "shared memory of one CTA");
+    static_assert(kSmem <= 232448 - 8192, "shared memory of one CTA, with the static arrays");
 };
 
 // TMEM columns: S and P over it 0 .. 255 in two buffers (f32: tiles in turn, the

@@ -207,7 +207,7 @@ cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cud
 // (f32; its bf16 form is 15% faster), 32 heads of 8 kv heads, context 4096:
 //   16 sequences:  16 rows 61 / 93 us, 32 rows 113 / 93, 64 rows 211 / 95
 //   1 sequence:    128 rows (1024 in all) 37 / 93, 256 (2048) 60 / 93,
-//                  384 (3072) 89 / 94, 512 (4096) 109 / 94
+//                  512 (4096) 109 / 94
 //   context 1024:  256 rows (2048) 20 / 35, 512 (4096) 47 / 35
 // and with weights, whose kernel goes through a list's rows one by one (the rule
 // does not look at them, so that asking for them changes no output):
