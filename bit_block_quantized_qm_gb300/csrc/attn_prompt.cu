@@ -14,8 +14,10 @@
 //     P V starts from 0 and is added to the row's sums in registers: the tensor
 //     cores cut their sums off instead of rounding them, which over a long row
 //     would show (2e-6 at 300 tokens, growing).
-//   bf16 rows: one piece each (queries exact, the others 11 bits), and the output
-//     accumulates in TMEM.
+//   bf16 rows: Q in one piece (exact) and K in two, so scores, maxima and sums are as
+//     exact as an f32 row's: K cut to 11 bits would move a score by 2^-12 of itself,
+//     2e-3 in lse at scores of deviation 3, and a row's weights off 1 by as much. P and
+//     V in one piece (11 bits; the output keeps 8), and the output accumulates in TMEM.
 // What f16's range loses are tokens 2^-33 (bf16: 2^-26) below a row's maximum.
 // They can matter only to an output element to which all larger tokens add up
 // to about nothing: rows that have both are listed and done again by the plain
@@ -23,12 +25,12 @@
 // give 2^-9.)
 //
 // What bounds it: f32 rows the tensor cores (6 products of 2^21 MACs per pair of
-// tiles at D = 128) behind the roles' waits for one another; bf16 rows (2
-// products) those waits: at 4096 rows, 32 heads, D = 128 (causal) the tensor
-// pipe is active 36% and the issue slots 47% of the time.  Measured: f32 rows,
-// prompt of 4096 / 8192: 379 / 1284 us, 362 / 428 TFLOP/s of the formula's
-// operations (three times that in products); bf16, 8192: 561 us, 980 TFLOP/s,
-// D = 64 541 us (the softmax is the same).
+// tiles at D = 128) behind the roles' waits for one another; bf16 rows (3
+// products) those waits.  Measured, 32 heads of 8 kv heads, D = 128, causal: f32 rows,
+// prompt of 4096 / 8192: 379 / 1280 us, 362 / 428 TFLOP/s of the formula's
+// operations (three times that in products); bf16, 8192: 648 us, 848 TFLOP/s (562 us
+// with K in one piece; 693 with one tile of K and two of V in shared memory, where
+// there is room for three in all), D = 64 596 us (the softmax is the same).
 //
 // Structure, one CTA of 24 (bf16: 20) warps per (sequence, kv head, 128 or 2 x 128 rows):
 //   8 decode warps read cells, a step ahead, and unpack them into 128-byte
@@ -37,8 +39,8 @@
 //   one warp issues the MMAs: S of the next tile is queued before P V of this
 //     one (f32), or two row tiles take turns (bf16), so the softmax of one
 //     always has products of another to run beside (bf16 with 64-token tiles, of
-//     which two S per row tile fit TMEM: 755 us against 560 for 8192 rows, a
-//     step's fixed costs double);
+//     which two S per row tile fit TMEM: 755 us against 560 for 8192 rows with K in
+//     one piece, a step's fixed costs double);
 //   8 softmax warps hold a row per thread (f32: half a row): maximum, exponentials,
 //     P back to TMEM over S (P is the A operand from there).  bf16: only when a
 //     row's maximum grows by more than 2^5 is its accumulator scaled down
@@ -52,6 +54,7 @@
 // 128 x 40; bf16 640 x 96 >= 256 x 136 + 256 x 80 + 128 x 40.
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include <algorithm>
+#include <type_traits>
 
 #include "tcgen05.cuh"
 
@@ -91,23 +94,23 @@ template <int D, bool F32>
 struct Shape {
     static constexpr int kBlocks = D / 32;
     static constexpr int kM = F32 ? 1 : 2;            // row tiles of a CTA
-    static constexpr int kPieces = F32 ? 2 : 1;       // of Q, K, V and P
-    static constexpr int kStages = F32 ? 1 : 2;       // K tiles, V tiles
+    static constexpr int kPieces = F32 ? 2 : 1;       // of Q, V and P (K always has two)
+    static constexpr int kStagesK = F32 ? 1 : 2, kStagesV = F32 || D == 128 ? 1 : 2;  // tiles of K, of V
     static constexpr int kPiece = kTile * D * 2;      // bytes of one piece of a tile
-    static constexpr int kOperand = kPieces * kPiece;
+    static constexpr int kOperand = kPieces * kPiece, kOperandK = 2 * kPiece;
     static constexpr int kAhead = F32 ? 2 : 1;        // tiles whose S of a row tile is queued
     static constexpr int kHalves = F32 ? 2 : 1;       // softmax threads of a row
     // Warps: softmax, decode, (f32) collectors, then MMA issue, examiner, two idle.
     static constexpr int kCollectWarps = F32 ? 4 : 0;
     static constexpr int kIssuer = kSoftmaxWarps + kDecodeWarps + kCollectWarps;
     static constexpr int kThreads = (kIssuer + 4) * 32;
-    static constexpr int kSmem = kM * kOperand + 2 * kStages * kOperand + 1024;
+    static constexpr int kSmem = kM * kOperand + kStagesK * kOperandK + kStagesV * kOperand + 1024;
     // Registers of a thread: the kernel's, and what setmaxnreg makes of them.
     static constexpr int kRegs = F32 ? 80 : 96, kSoftmaxRegs = F32 ? 72 : 136, kDecodeRegs = F32 ? 64 : 80;
     static constexpr int kCollectRegs = 168, kOtherRegs = 40;
     static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kDecodeWarps * kDecodeRegs + kCollectWarps * kCollectRegs +
                         4 * kOtherRegs) <= kThreads * kRegs, "registers of one CTA");
-    static_assert(kSmem <= 232448 - 8192, "shared memory of one CTA, with the static arrays");
+    static_assert(kSmem + (F32 ? 6144 : 2048) <= 232448, "shared memory of one CTA, with the static arrays");
 };
 
 // TMEM columns: S and P over it 0 .. 255 in two buffers (f32: tiles in turn, the
@@ -220,12 +223,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
     __shared__ float key_up[kRing], value_up[kRing];  // the powers of two themselves
     __shared__ __align__(16) uint8_t wild[kRing][32];     // bit t of byte l: token 4 l + t of tile i has a wild value scale
     // f32: what the two softmax threads of a row tell each other, and the collector.
-    __shared__ float half_max[2][S::kHalves][kM * kTile];
+    __shared__ float half_max[F32 ? 2 : 1][S::kHalves][F32 ? kTile : 1];
     __shared__ float row_keep[F32 ? kKeepRing : 1][kTile], row_top[F32 ? kTile : 1];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_sm = base;                             // [kM][pieces]
     uint8_t* k_sm = q_sm + kM * S::kOperand;          // [stages][pieces]
-    uint8_t* v_sm = k_sm + S::kStages * S::kOperand;  // [stages][pieces]
+    uint8_t* v_sm = k_sm + S::kStagesK * S::kOperandK;  // [stages][pieces]
     unsigned int* const err = &g_attn_prompt_error;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -562,38 +565,50 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                 }
             }
         };
-        auto unpack = [&](const Blocks& x, bool v, float f, uint8_t* hi) {
+        auto unpack = [&](auto two, const Blocks& x, bool v, float f, uint8_t* hi) {
 #pragma unroll
             for (int y = 0; y < kTurns; ++y) {
                 // Values that are not finite (NaN then comes with the scores): 0.
                 const float d = v && (x.sc[y] & 0x7C00u) == 0x7C00u ? 0.f : f16_bits_to_float(x.sc[y]) * f;
-                decode_block<F32>(x.q[y], d, tok, blk0 + y * kStride, hi, hi + S::kPiece, plan.k1024);
+                decode_block<decltype(two)::value>(x.q[y], d, tok, blk0 + y * kStride, hi, hi + S::kPiece, plan.k1024);
             }
         };
         if constexpr (!F32) {
-            // Keys and values of a tile in one step: v_empty of a stage comes after k_empty.
+            // Keys a tile ahead of values.
             Blocks k, v;
-            int64_t off = cell_at(0, page_at(0));
+            int64_t off = cell_at(0, page_at(0)), off_next = -1;  // of this thread's token in tile i, and in tile i + 1
             fetch(k, c.k, off);
             fetch(v, c.v, off);
             int page = page_at(1);
 #pragma unroll 1
-            for (int i = 0; i < n_tiles; ++i) {
-                const int stage = i % S::kStages;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam, i & 1, err));
-                if (ok && lane == 0) mbar_arrive(&bar.exam_go);
-                if (ok && i >= S::kStages) ok = mbar_wait_bounded(&bar.v_empty[stage], (i / S::kStages - 1) & 1, err);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                const Blocks k_now = k, v_now = v;
-                off = cell_at(i + 1, page);
-                page = page_at(i + 2);
-                fetch(k, c.k, off);
-                fetch(v, c.v, off);
-                unpack(k_now, false, key_up[i % kRing], k_sm + stage * S::kOperand);
-                unpack(v_now, true, value_up[i % kRing], v_sm + stage * S::kOperand);
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.k_full[stage]);
+            for (int i = 0; i <= n_tiles; ++i) {
+                if (i < n_tiles) {
+                    const int at = i % S::kStagesK;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam, i & 1, err));
+                    if (ok && lane == 0) mbar_arrive(&bar.exam_go);
+                    if (ok && i >= S::kStagesK) ok = mbar_wait_bounded(&bar.k_empty[at], (i / S::kStagesK - 1) & 1, err);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                    const Blocks now = k;
+                    off_next = cell_at(i + 1, page);
+                    page = page_at(i + 2);
+                    fetch(k, c.k, off_next);
+                    unpack(std::true_type{}, now, false, key_up[i % kRing], k_sm + at * S::kOperandK);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.k_full[at]);
+                }
+                if (i > 0) {
+                    const int at = (i - 1) % S::kStagesV;
+                    if (i > S::kStagesV) ok = mbar_wait_bounded(&bar.v_empty[at], ((i - 1) / S::kStagesV - 1) & 1, err);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                    const Blocks now = v;
+                    fetch(v, c.v, off);
+                    unpack(std::false_type{}, now, true, value_up[(i - 1) % kRing], v_sm + at * S::kOperand);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.v_full[at]);
+                }
+                off = off_next;
             }
         } else {
             int64_t off_v = -1, off_k = cell_at(0, page_at(0));  // of the tile whose values come next, and of the one after
@@ -607,16 +622,15 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             for (int step = 0; step < 2 * n_tiles; ++step) {
                 const bool v = step > 0 && ((step & 1) == 0 || step == 2 * n_tiles - 1);
                 const int i = v ? (step - 1) >> 1 : (step + 1) >> 1;
-                const int stage = i % S::kStages;
+                static_assert(!F32 || (S::kStagesK == 1 && S::kStagesV == 1), "one tile of each");
                 if (!v) {
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam, i & 1, err));
                     if (ok && lane == 0) mbar_arrive(&bar.exam_go);
                 }
-                if (ok && i >= S::kStages)
-                    ok = mbar_wait_bounded((v ? bar.v_empty : bar.k_empty) + stage, (i / S::kStages - 1) & 1, err);
+                if (ok && i >= 1) ok = mbar_wait_bounded(v ? bar.v_empty : bar.k_empty, (i - 1) & 1, err);
                 if (!__all_sync(0xFFFFFFFFu, ok)) break;
                 const float f = v ? value_up[i % kRing] : key_up[i % kRing];
-                uint8_t* hi = (v ? v_sm : k_sm) + stage * S::kOperand;
+                uint8_t* hi = v ? v_sm : k_sm;
                 const Blocks now = x;
                 // The next step: keys i + 1 (i + 2 after values i), or values i - 1.
                 if (v || step == 0) {
@@ -628,10 +642,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                     fetch(x, c.v, off_v);
                     page_k = page_at(i + 1);
                 }
-                unpack(now, v, f, hi);
+                unpack(std::true_type{}, now, v, f, hi);
                 fence_proxy_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive((v ? bar.v_full : bar.k_full) + stage);
+                if (lane == 0) mbar_arrive(v ? bar.v_full : bar.k_full);
             }
         }
     } else if (warp < S::kIssuer) {
@@ -681,17 +695,17 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             constexpr uint32_t id_s = idesc_f16(kTile, false), id_o = idesc_f16(D, true);
             bool ok = true;
             auto scores = [&](int i, int m) {
-                const int stage = i % S::kStages;
-                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.k_full[stage], (i / S::kStages) & 1, err));
+                const int stage = i % S::kStagesK;
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.k_full[stage], (i / S::kStagesK) & 1, err));
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t t_s = tmem + (F32 ? i & 1 : m) * kTile;
-                const uint32_t q0 = smem_addr(q_sm + m * S::kOperand), k0 = smem_addr(k_sm + stage * S::kOperand);
-                constexpr int kProducts = F32 ? 3 : 1;  // low x high, high x low, high x high
+                const uint32_t q0 = smem_addr(q_sm + m * S::kOperand), k0 = smem_addr(k_sm + stage * S::kOperandK);
+                constexpr int kProducts = F32 ? 3 : 2;  // (low x high,) high x low, high x high
 #pragma unroll 1
                 for (int p = 0; p < kProducts; ++p) {
                     const uint64_t da = desc_base(q0 + (F32 && p == 0 ? S::kPiece : 0), 16);
-                    const uint64_t db = desc_base(k0 + (F32 && p == 1 ? S::kPiece : 0), 16);
+                    const uint64_t db = desc_base(k0 + (p == kProducts - 2 ? S::kPiece : 0), 16);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t o = static_cast<uint64_t>((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
@@ -699,18 +713,15 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                     }
                 }
                 mma_commit(&bar.s_full[F32 ? i & 1 : m], lead);
-                if (F32) mma_commit(&bar.k_empty[stage], lead);
+                if (m == kM - 1) mma_commit(&bar.k_empty[stage], lead);
             };
             auto output = [&](int i, int m) {
-                const int stage = i % S::kStages, buf = F32 ? i & 1 : m;
+                const int stage = i % S::kStagesV, buf = F32 ? i & 1 : m;
                 const uint32_t p_phase = F32 ? (i >> 1) & 1 : i & 1;
-                if (F32) {  // P, V, and the accumulators that the collectors have read
-                    ok = ok && __all_sync(0xFFFFFFFFu, wait_all(&bar.p_full[buf], p_phase, &bar.v_full[stage],
-                                                                (i / S::kStages) & 1, i > 0 ? &bar.o_free : &bar.p_full[buf],
-                                                                i > 0 ? (i - 1) & 1 : p_phase, err));
-                } else {  // (V came with K)
-                    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.p_full[buf], p_phase, err));
-                }
+                // P, V, and (f32) the accumulators that the collectors have read.
+                ok = ok && __all_sync(0xFFFFFFFFu, wait_all(&bar.p_full[buf], p_phase, &bar.v_full[stage],
+                                                            (i / S::kStagesV) & 1, F32 && i > 0 ? &bar.o_free : &bar.p_full[buf],
+                                                            F32 && i > 0 ? (i - 1) & 1 : p_phase, err));
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t v0 = smem_addr(v_sm + stage * S::kOperand);

@@ -452,8 +452,8 @@ QM_API int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t
  *              that may run at the same time need a workspace each.
  * Precision: scores, statistics and sums in f32; products to about 2^-21 of
  * each |q_i k_i| and |p_j v_j| for QM_F32; for QM_BF16, where the output keeps
- * 8 bits, probabilities (and in long calls keys and values) may be rounded to
- * 11 bits.  Tokens that a row does not see do not reach it, whatever their
+ * 8 bits, the probabilities and values of its sum may be rounded to 11 bits
+ * (lse and weights are those of a QM_F32 call on the same queries).  Tokens that a row does not see do not reach it, whatever their
  * bytes hold.  A token that a row sees and whose scales are not finite makes
  * at least those entries of the row non-finite that the formula does.  The
  * same call on the same inputs gives bitwise the same results (no atomics
