@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_plain_kernel(KvView c, KvRow
     if (item < static_cast<int64_t>(r.n_tokens) * a.heads) attn_plain_row<NB, T, 1>(c, r, a, lse, item, 0);
 }
 
-// The rows that the prompt kernel listed in `redo` (redo_n[0] of them, redo_n[1]
-// counts CTAs), a CTA each; the last CTA to finish leaves the list empty for
+// The rows that the prompt kernel listed in `redo` (redo_n[0] of them, but no more
+// than there are rows; redo_n[1] counts CTAs), a CTA each; the last CTA to finish leaves the list empty for
 // the next call.
 constexpr int kRedoWarps = 8;
 template <int NB, typename T>
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kRedoWarps * 32)
     attn_redo_kernel(KvView c, KvRows r, AttnCall a, float* lse, unsigned* redo_n, const unsigned* redo) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const unsigned n = __ldcg(redo_n);
+    const unsigned n = min(__ldcg(redo_n), static_cast<unsigned>(static_cast<int64_t>(r.n_tokens) * a.heads));
     for (unsigned i = blockIdx.x; i < n; i += gridDim.x)
         attn_plain_row<NB, T, kRedoWarps>(c, r, a, lse, __ldcg(redo + i), threadIdx.x >> 5);
     __syncthreads();

@@ -155,6 +155,7 @@ struct PromptPlan {
     QueryTiles q;        // where the queries' pieces go, if they are wanted
     unsigned* redo_n;    // how many rows are listed to be done again,
     unsigned* redo;      // and which: row * heads + head
+    unsigned redo_room;  // entries that the list has room for: each row once
 };
 
 // A row's end: its output, 32 dims at a time, its logarithm, and the list of rows
@@ -195,8 +196,10 @@ struct RowEnd {
         if (a.lse) a.lse[item] = lse2 * kLn2;
         if (plan.lse2) plan.lse2[item] = lse2;
         if (lowest < top - kFarBelow<F32> && least < sqrtf(static_cast<float>(n_tiles * kTile)) * kSafe<F32>) {
-            const unsigned at = atomicAdd(plan.redo_n, 1u);  // (at most once per row)
-            plan.redo[at] = static_cast<unsigned>(item);
+            // (Once per row, unless row offsets that go back give a row to two sequences.)
+            const unsigned at = atomicAdd(plan.redo_n, 1u);
+            if (at < plan.redo_room) plan.redo[at] = static_cast<unsigned>(item);
+            else atomicOr(&g_attn_prompt_error, kErrRange);
         }
     }
 };
@@ -829,6 +832,7 @@ cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, f
     p.q = qt;
     p.redo_n = redo_n;
     p.redo = redo;
+    p.redo_room = static_cast<unsigned>(static_cast<int64_t>(r.n_tokens) * a.heads);
     const int64_t grid = static_cast<int64_t>(p.items_per_list) * c.n_seqs * c.heads;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
     note_launch();

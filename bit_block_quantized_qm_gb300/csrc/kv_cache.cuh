@@ -36,7 +36,7 @@ __device__ __forceinline__ void kv_rows(const KvRows& r, int b, int* first, int*
     if (a < 0 || e < a || e > r.n_tokens || e - a > r.max_q) {
         atomicOr(err, kErrRange);
         a = min(max(a, 0), r.n_tokens);
-        e = min(min(max(e, a), r.n_tokens), a + r.max_q);
+        e = a + min(min(max(e, a), r.n_tokens) - a, r.max_q);
     }
     *first = a;
     *count = e - a;
