@@ -25,6 +25,7 @@ The ``*_ptr`` variants take raw device addresses (ints) instead of tensors.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -45,6 +46,7 @@ __all__ = [
     "EXPORTED_SYMBOLS", "QmGemvProblem", "qm_gemv_q4_0_list_ptr", "qm_gemv_q4_0_list",
     "gemv_problem_array",
     "QM_ERR_RANGE", "QM_ERR_WORKSPACE", "QM_F32", "QM_BF16", "QmKVCache", "QmAttnArgs", "KVCache", "kv_page_bytes",
+    "ATTN_WORKSPACE_ZEROED",
     "qm_kv_append_q4_0", "qm_kv_read_q4_0", "qm_attn_q4_0", "qm_attn_workspace", "qm_kv_evict_q4_0",
 ]
 
@@ -63,6 +65,8 @@ QM_ERR_WORKSPACE = -11
 
 QM_F32 = 0
 QM_BF16 = 1
+
+ATTN_WORKSPACE_ZEROED = 4096
 
 QM_ALGO_AUTO = 0
 QM_ALGO_GEMV = 1
@@ -491,7 +495,7 @@ class KVCache:
     ``[n_seqs, pages]``, ``lengths`` int32 ``[n_seqs]``.  ``max_len`` bounds the
     lengths (default, and at most: what the page table can hold); a tighter
     bound may be set at any time and gives smaller launches.  Keeps the tensors alive, and
-    one attention workspace for each stream it is used on."""
+    one attention workspace for each stream it is used on (see qm_attn_q4_0)."""
 
     def __init__(self, k_pages, v_pages, page_table, lengths, head_dim: int, page_tokens: int, max_len=None):
         import torch
@@ -529,7 +533,7 @@ class KVCache:
             raise ValueError("max_len is negative")
         self.struct.max_len = min(n, self.capacity)
 
-    def _workspace(self, n_heads: int, n_tokens: int, max_q: int, weights: bool, stream: int):
+    def _workspace(self, n_heads: int, n_tokens: int, max_q: int, weights: bool, stream: int, current: bool):
         key = (n_heads, n_tokens, max_q, weights, self.struct.max_len)
         need = self._sizes.get(key)
         if need is None:
@@ -541,14 +545,31 @@ class KVCache:
             self._sizes[key] = need
         if need == 0:
             return None
-        ws = self._workspaces.get(stream)
+        torch = _torch or _torch_module()
+        if current:
+            capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            with _on_stream(self.k_pages.device, stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+        # A graph keeps the address and replays the fill, so a call that is captured has a
+        # workspace of its own, from the graph's memory, and no other call ever uses it.
+        ws = None if capturing else self._workspaces.get(stream)
         if ws is None or ws.numel() < need:
-            import torch
-            with torch.cuda.device(self.k_pages.device), \
-                    torch.cuda.stream(torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()):
-                ws = torch.zeros(need, dtype=torch.uint8, device=self.k_pages.device)
-            self._workspaces[stream] = ws
+            with _on_stream(self.k_pages.device, stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=self.k_pages.device)
+                ws[:ATTN_WORKSPACE_ZEROED].zero_()
+            if not capturing:
+                self._workspaces[stream] = ws
         return ws
+
+
+@contextlib.contextmanager
+def _on_stream(device, handle: int):
+    """Makes the stream with this handle torch's current one."""
+    torch = _torch or _torch_module()
+    with torch.cuda.device(device), \
+            torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
+        yield
 
 
 def _rows(t, heads, dim, name):
@@ -626,15 +647,21 @@ def qm_attn_workspace(cache, n_heads: int, n_tokens: int, max_q: int, weights: b
 
 
 def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts=None, max_q=None, weights=None,
-                 return_lse: bool = False, out=None, lse=None, stream=None):
+                 return_lse: bool = False, out=None, lse=None, stream=None, workspace=None):
     """Causal attention of the rows ``q`` (f32 or bf16 ``[n_tokens, n_heads,
     head_dim]``, rows may be strided) over the cache; returns ``out``, or
     ``(out, lse)`` with ``return_lse`` (or an ``lse`` tensor).  ``scale`` defaults
     to head_dim ** -0.5; ``window`` > 0 with ``sinks`` limits what a row sees to
     its last ``window`` tokens and the first ``sinks``; ``weights`` f32 ``[n_seqs,
     n_kv_heads, >= max_len]`` is added each token's attention weight; ``max_q``
-    bounds the rows of one sequence (default: all rows).  The workspace is the
-    cache's own, one per stream."""
+    bounds the rows of one sequence (default: all rows).
+
+    ``workspace``: a uint8 tensor of at least ``qm_attn_workspace`` bytes whose first
+    ``ATTN_WORKSPACE_ZEROED`` were zeroed once; calls that cannot run at the same time
+    can share it, those of other caches too (the layers of a model).  Without it the
+    cache has its own, one per stream, kept at its largest size; a call that is
+    captured into a CUDA graph gets one from the graph's memory, and a fill of those
+    first bytes is captured with it."""
     torch = _torch or _torch_module()
     code, qs = _rows(q, None, cache.head_dim, "q")
     n_tokens, n_heads = q.shape[0], q.shape[1]
@@ -663,7 +690,11 @@ def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts
     elif max_q is None:
         max_q = n_tokens
     handle = _stream_handle(stream)
-    ws = cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle)
+    if workspace is None:
+        ws = cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle, stream is None)
+    else:
+        ws = workspace
+        _require(ws, torch.uint8, "workspace")
     # (The struct's bytes; filling a ctypes object field by field takes 2 us more.)
     args = _ATTN_ARGS.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
                            weights.data_ptr() if weights is not None else 0, starts,

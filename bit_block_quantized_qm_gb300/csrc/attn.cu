@@ -14,7 +14,7 @@ constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 // Of the workspace's first 4 KB, zero between calls, the step kernel has all but
 // the last 16 bytes; there is the number of the rows to be done again.
-constexpr int64_t kRedoCount = 4080;
+constexpr int64_t kRedoCount = kAttnZeroed - 16;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_weights_plain_kernel(KvView 
 // between calls; the rows to be done again; with weights, logarithms to base 2
 // and (head dimensions of the prompt kernel) the queries' tiles and units.
 struct Room {
-    int64_t redo = 4096, lse = 0, units = 0, images = 0, bytes = 0, per_head = 0;
+    int64_t redo = kAttnZeroed, lse = 0, units = 0, images = 0, bytes = 0, per_head = 0;
 };
 Room room_of(const KvView& c, int heads, int64_t n_tokens, bool weights) {
     Room m;

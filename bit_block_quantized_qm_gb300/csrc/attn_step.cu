@@ -65,7 +65,7 @@ struct StepPlan {
 
 // The workspace begins with arrival counters, zero between calls: 4 KB of it
 // are never anything else, whatever calls share the workspace.
-constexpr int64_t kCtrBytes = 4096;
+constexpr int64_t kCtrBytes = kAttnZeroed;
 static_assert(kMaxCtas * 4 <= kCtrBytes - 16, "a counter for each (the last 16 bytes are the prompt kernel's)");
 
 // Tiles that rows at positions pos0 .. L - 1 read: all of 0 .. L - 1, or the

@@ -19,6 +19,7 @@ using qm::mul_ok;
 using qm::overlaps;
 
 constexpr int64_t kMaxLen = int64_t(1) << 30;
+static_assert(qm::kAttnZeroed == QM_ATTN_WORKSPACE_ZEROED, "the header's number");
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

@@ -195,6 +195,8 @@ struct AttnCall {
     uint8_t* ws;     // workspace (attn_workspace_bytes), its counters zero
 };
 
+// Bytes at the start of the workspace that are zero between calls.
+constexpr int64_t kAttnZeroed = 4096;
 // Bytes of workspace that launch_attn needs for these sizes.
 int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
 cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);

@@ -88,6 +88,9 @@ extern "C" {
 #define QM_F32 0
 #define QM_BF16 1
 
+/* Bytes at the start of qm_attn_q4_0's workspace that are zero between calls. */
+#define QM_ATTN_WORKSPACE_ZEROED 4096
+
 /* Algorithms for qm_matmul_q4_0_algo. */
 #define QM_ALGO_AUTO 0      /* what qm_matmul_q4_0 picks: GEMV_PK for M <= 2 and
                                N <= 1024, GEMV for M <= 8, otherwise GEMM_TC
@@ -447,9 +450,11 @@ QM_API int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t
  *              ranks by.
  *   max_q    : no sequence has more rows than this in the call (ignored
  *              without q_starts).
- *   workspace: qm_attn_workspace bytes, 16-byte aligned, zeroed once before its
- *              first use; every call leaves it fit for the next one.  Calls
- *              that may run at the same time need a workspace each.
+ *   workspace: qm_attn_workspace bytes, 16-byte aligned, its first
+ *              QM_ATTN_WORKSPACE_ZEROED bytes zeroed once before its first use;
+ *              every call leaves it fit for the next one, of this cache or
+ *              another.  Calls that may run at the same time need a workspace
+ *              each, and one that a CUDA graph uses lives as long as the graph.
  * Precision: scores, statistics and sums in f32; products to about 2^-21 of
  * each |q_i k_i| and |p_j v_j| for QM_F32; for QM_BF16, where the output keeps
  * 8 bits, the probabilities and values of its sum may be rounded to 11 bits

@@ -72,3 +72,124 @@ def test_the_sharp_rows_are_right(qm):  # noqa: F811
     c, q = sharp(300, 90)
     for dtype in (F32, BF16):
         check_attend(qm, c, [90], 4, dtype, q=q)
+
+
+# ---- workspaces and CUDA graphs
+
+def captured(cache, qm, q, side, **kw):  # noqa: F811
+    """A graph of one call on `q` (captured on `side`), its output and its weights."""
+    out = torch.empty_like(q)
+    w = torch.zeros((cache.n_seqs, cache.n_kv_heads, cache.max_len), device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        qm.qm_attn_q4_0(cache, q, out=out, weights=w, **kw)
+    return g, out, w
+
+
+def replay(g, out, w):
+    w.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    return out.clone(), w.clone()
+
+
+@pytest.mark.parametrize("new", [1, 3, 90], ids=["step", "draft", "prompt"])
+def test_a_graph_keeps_its_workspace(qm, new):  # noqa: F811
+    """Capture after a warm-up, then larger calls on the same stream and new tensors in
+    whatever memory became free: replays write nothing but their outputs, and answer as before."""
+    c = ko.Cache([900, 1200, 700], 2, 128, 64, seed=43)
+    cache = device(qm, c)
+    side = torch.cuda.Stream()
+    q = torch.randn((3 * new, 8, 128), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        want = qm.qm_attn_q4_0(cache, q, weights=torch.zeros((3, 2, cache.max_len), device="cuda"))
+    g, out, w = captured(cache, qm, q, side)
+    first = replay(g, out, w)
+    assert torch.equal(first[0], want)
+    with torch.cuda.stream(side):  # needs more than the call that was captured
+        qm.qm_attn_q4_0(cache, torch.randn((3 * 400, 8, 128), device="cuda"),
+                        weights=torch.zeros((3, 2, cache.max_len), device="cuda"))
+    torch.cuda.synchronize()
+    others = []
+    with torch.cuda.stream(side):
+        for size in (1 << 12, 1 << 18, 1 << 21, 1 << 23) * 3:
+            others.append(torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        again = replay(g, out, w)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+        assert all(bool((x == 0x5A).all()) for x in others)
+
+
+def test_captures_without_a_call_before_and_on_two_streams(qm):  # noqa: F811
+    """Two graphs captured on one stream that has seen no call, replayed alone, in turn
+    and at the same time on two streams, with eager calls between."""
+    c = ko.Cache([5000, 3000], 2, 128, 64, seed=44)
+    cache = device(qm, c)
+    qs = [torch.randn((2 * n, 8, 128), device="cuda") for n in (1, 2)]
+    side = torch.cuda.Stream()
+    graphs = [captured(cache, qm, q, side) for q in qs]
+    fresh = device(qm, c)
+    want = []
+    for q in qs:
+        w = torch.zeros((2, 2, cache.max_len), device="cuda")
+        want.append((qm.qm_attn_q4_0(fresh, q, weights=w), w))
+    for order in ((1,), (0, 1), (1, 0, 0)):  # (the second graph first)
+        for i in order:
+            got = replay(*graphs[i])
+            assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1])
+    with torch.cuda.stream(side):
+        assert torch.equal(qm.qm_attn_q4_0(cache, qs[0]), want[0][0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for _, _, w in graphs:
+            w.zero_()
+        torch.cuda.synchronize()
+        for s, (g, _, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for i, (_, out, w) in enumerate(graphs):
+            assert torch.equal(out, want[i][0]) and torch.equal(w, want[i][1])
+
+
+def test_a_workspace_of_the_callers(qm):  # noqa: F811
+    """One workspace for two caches, in eager and captured calls; too small or the wrong
+    type is refused."""
+    caches = [device(qm, ko.Cache([900, 1200], 2, 128, 64, seed=s)) for s in (45, 46)]
+    q = torch.randn((2, 8, 128), device="cuda")
+    p = torch.randn((160, 8, 128), device="cuda")
+    want = [[qm.qm_attn_q4_0(x, y) for y in (q, p)] for x in caches]
+    need = max(qm.qm_attn_workspace(x, 8, n, n // 2) for x in caches for n in (2, 160))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ws[:qm.ATTN_WORKSPACE_ZEROED] = 0
+    for x, (a, b) in zip(caches, want):
+        for _ in range(2):
+            assert torch.equal(qm.qm_attn_q4_0(x, q, workspace=ws), a)
+            assert torch.equal(qm.qm_attn_q4_0(x, p, workspace=ws), b)
+    assert (ws[:qm.ATTN_WORKSPACE_ZEROED] == 0).all()
+    out = torch.empty_like(q)
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        qm.qm_attn_q4_0(caches[0], q, out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0][0])
+    with pytest.raises(qm.QMError) as e:
+        qm.qm_attn_q4_0(caches[0], q, workspace=ws[:need // 4])
+    assert e.value.code == qm.QM_ERR_WORKSPACE
+    with pytest.raises(TypeError):
+        qm.qm_attn_q4_0(caches[0], q, workspace=ws.float())
+    with pytest.raises(ValueError):
+        qm.qm_attn_q4_0(caches[0], q, workspace=ws.cpu())
+    # an explicit stream, eager and captured
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = qm.qm_attn_q4_0(caches[1], q, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want[1][0])
