@@ -85,7 +85,7 @@ EXPORTED_SYMBOLS = ("qm_version", "qm_status_string", "qm_dequant_q4_0", "qm_mat
                     "qm_matmul_q4_0_noalloc", "qm_dequant_q8_0", "qm_quantize_q8_0",
                     "qm_selftest_wait_timeout", "qm_gemv_q4_0_list", "qm_matmul_q4_0_q8act",
                     "qm_gemv_q4_0_q8act_list", "qm_kv_append_q4_0", "qm_kv_read_q4_0", "qm_attn_q4_0",
-                    "qm_attn_workspace", "qm_kv_evict_q4_0")
+                    "qm_attn_workspace", "qm_attn_workspace_exact", "qm_kv_evict_q4_0")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libqm.so")
@@ -185,6 +185,8 @@ def load_library() -> ctypes.CDLL:
             lib.qm_attn_q4_0.restype = i32
             lib.qm_attn_workspace.argtypes = [p, i64, i64, i64, i32]
             lib.qm_attn_workspace.restype = i64
+            lib.qm_attn_workspace_exact.argtypes = [p, i64, i64, i64, i32]
+            lib.qm_attn_workspace_exact.restype = i64
             lib.qm_kv_evict_q4_0.argtypes = [p, p, p, i64, i64, i64, i64, p, p, i64, p]
             lib.qm_kv_evict_q4_0.restype = i32
             lib.qm_launch_count.argtypes = []
@@ -537,9 +539,7 @@ class KVCache:
         key = (n_heads, n_tokens, max_q, weights, self.struct.max_len)
         need = self._sizes.get(key)
         if need is None:
-            need = load_library().qm_attn_workspace(self.ref, n_heads, n_tokens, max_q, 1 if weights else 0)
-            if need < 0:
-                raise QMError(need, "qm_attn_workspace")
+            need = qm_attn_workspace(self, n_heads, n_tokens, max_q, weights, exact=True)
             if len(self._sizes) > 256:
                 self._sizes.clear()
             self._sizes[key] = need
@@ -638,9 +638,12 @@ def qm_kv_read_q4_0(cache, n_tokens: int, q_starts=None, k=None, v=None, stream=
     return k, v
 
 
-def qm_attn_workspace(cache, n_heads: int, n_tokens: int, max_q: int, weights: bool = False) -> int:
-    """Bytes of workspace that qm_attn_q4_0 needs (see include/qm.h)."""
-    n = load_library().qm_attn_workspace(cache.ref, n_heads, n_tokens, max_q, 1 if weights else 0)
+def qm_attn_workspace(cache, n_heads: int, n_tokens: int, max_q: int, weights: bool = False, exact: bool = False) -> int:
+    """Bytes of workspace that qm_attn_q4_0 needs for any call of at most these
+    sizes, or (``exact``) for a call of these sizes; see include/qm.h."""
+    lib = load_library()
+    n = (lib.qm_attn_workspace_exact if exact else lib.qm_attn_workspace)(cache.ref, n_heads, n_tokens, max_q,
+                                                                         1 if weights else 0)
     if n < 0:
         raise QMError(n, "qm_attn_workspace")
     return n

@@ -260,6 +260,14 @@ int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64
     return room_of(c, heads, n_tokens, weights).bytes;
 }
 
+int64_t attn_workspace_most(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {
+    // Both kernels' needs grow with the rows and with weights; the step kernel takes calls up to a number of rows.
+    const int64_t step = attn_step_most(c, heads, max_q);
+    int64_t most = step > 0 ? attn_step_workspace(c, heads, n_tokens, step, weights) : 0;
+    if (step < max_q) most = std::max(most, room_of(c, heads, n_tokens, weights).bytes);
+    return most;
+}
+
 cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream) {
     if (attn_step_takes(c, a.heads, r.max_q)) return launch_attn_step(c, r, a, stream);
     switch (c.dim / 32) {

@@ -960,6 +960,13 @@ bool attn_step_takes(const KvView& c, int heads, int64_t max_q) {
     return rows <= kStepRows || (rows <= kStepRowsFew && all <= kStepAll);
 }
 
+int64_t attn_step_most(const KvView& c, int heads, int64_t max_q) {
+    if (c.dim != 64 && c.dim != 128) return 0;
+    const int64_t group = heads / c.heads, all = static_cast<int64_t>(c.n_seqs) * heads;
+    const int64_t few = all > 0 ? std::min(kStepRowsFew / group, kStepAll / all) : kStepRowsFew / group;
+    return std::min(max_q, std::max(kStepRows / group, few));
+}
+
 int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights) {
     return make_plan(c, heads, n_tokens, max_q, weights).bytes;
 }

@@ -87,6 +87,17 @@ int attn_sizes(const qm_kv_cache* c, int64_t n_heads) {
     return n_heads < 1 || n_heads > 0x7FFFFFFF / 256 || n_heads % c->n_kv_heads ? QM_ERR_SHAPE : QM_OK;
 }
 
+// The sizes that a workspace is asked for.  The rows' layout does not matter
+// there: as if there were offsets.
+int check_workspace(const qm_kv_cache* c, int64_t n_heads, int64_t n_tokens, int64_t max_q, qm::KvView* view,
+                    qm::KvRows* rows) {
+    int64_t pool;
+    int rc = check_cache(c, view, &pool);
+    if (rc == QM_OK) rc = attn_sizes(c, n_heads);
+    if (rc == QM_OK) rc = check_rows(c, n_tokens, max_q, c->lengths, rows);
+    return rc;
+}
+
 }  // namespace
 
 extern "C" {
@@ -151,11 +162,15 @@ int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t n_toke
 int64_t qm_attn_workspace(const qm_kv_cache* cache, int64_t n_heads, int64_t n_tokens, int64_t max_q, int weights) {
     qm::KvView view;
     qm::KvRows rows;
-    int64_t pool;
-    int rc = check_cache(cache, &view, &pool);
-    if (rc == QM_OK) rc = attn_sizes(cache, n_heads);
-    // The rows' layout does not matter here: as if there were offsets.
-    if (rc == QM_OK) rc = check_rows(cache, n_tokens, max_q, cache->lengths, &rows);
+    const int rc = check_workspace(cache, n_heads, n_tokens, max_q, &view, &rows);
+    if (rc != QM_OK) return rc;
+    return qm::attn_workspace_most(view, static_cast<int>(n_heads), rows.n_tokens, rows.max_q, weights != 0);
+}
+
+int64_t qm_attn_workspace_exact(const qm_kv_cache* cache, int64_t n_heads, int64_t n_tokens, int64_t max_q, int weights) {
+    qm::KvView view;
+    qm::KvRows rows;
+    const int rc = check_workspace(cache, n_heads, n_tokens, max_q, &view, &rows);
     if (rc != QM_OK) return rc;
     return qm::attn_workspace_bytes(view, static_cast<int>(n_heads), rows.n_tokens, rows.max_q, weights != 0);
 }

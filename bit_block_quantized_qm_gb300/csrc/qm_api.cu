@@ -211,7 +211,7 @@ const char* qm_status_string(int status) {
         case QM_ERR_POINTER: return "a pointer is not device memory of the current device";
         case QM_ERR_TOO_LARGE: return "beyond the fixed scratch of qm_matmul_q4_0_noalloc (M > 8)";
         case QM_ERR_RANGE: return "a page table entry, a length or a row offset on the device was out of range";
-        case QM_ERR_WORKSPACE: return "the workspace is smaller than qm_attn_workspace says";
+        case QM_ERR_WORKSPACE: return "the workspace is smaller than qm_attn_workspace_exact says";
         default: return "unknown status";
     }
 }

@@ -199,6 +199,8 @@ struct AttnCall {
 constexpr int64_t kAttnZeroed = 4096;
 // Bytes of workspace that launch_attn needs for these sizes.
 int64_t attn_workspace_bytes(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
+// The same for the neediest call of at most these sizes.
+int64_t attn_workspace_most(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
 cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);
 
 // Few rows (attn_step.cu): head dimensions 64 and 128.  Its time grows with the
@@ -218,6 +220,8 @@ cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cud
 //   2 kv heads of 4: 256 rows (512) 68 / 95, 1024 (2048) 234 / 110
 constexpr int kStepRows = 24, kStepRowsFew = 256, kStepAll = 2048;
 bool attn_step_takes(const KvView& c, int heads, int64_t max_q);
+// The largest max_q, up to this one, that it takes (0: none).
+int64_t attn_step_most(const KvView& c, int heads, int64_t max_q);
 int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
 cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);
 cudaError_t attn_step_read_device_error(unsigned int* bits, bool clear);

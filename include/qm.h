@@ -82,7 +82,7 @@ extern "C" {
                                    memory was out of range (see
                                    qm_device_status)                             */
 #define QM_ERR_WORKSPACE (-11)  /* the workspace is smaller than
-                                   qm_attn_workspace says                        */
+                                   qm_attn_workspace_exact says                  */
 
 /* Element types of keys, values, queries and attention outputs. */
 #define QM_F32 0
@@ -489,12 +489,19 @@ typedef struct qm_attn_args {
 QM_API int qm_attn_q4_0(const qm_kv_cache* cache, const qm_attn_args* args, void* stream);
 
 /*
- * qm_attn_workspace — bytes of workspace that qm_attn_q4_0 needs for calls of
- * at most these sizes (weights != 0: with accumulated weights).  Host only.
- * Returns the bytes (0: none is needed) or a negative status.
+ * qm_attn_workspace — bytes of workspace that qm_attn_q4_0 needs for any call
+ * of at most these sizes (weights != 0: with or without accumulated weights).
+ * Calls of few rows take another kernel than those of many, and may need more:
+ * with weights, up to 24 rows and query heads of a kv head (256 in small
+ * batches) keep 4 * max_len bytes for each until the call is over.
+ * qm_attn_workspace_exact — the bytes for a call of exactly these sizes, with
+ * weights as given: what the call itself asks for.
+ * Host only.  Return the bytes (0: none is needed) or a negative status.
  */
 QM_API int64_t qm_attn_workspace(const qm_kv_cache* cache, int64_t n_heads, int64_t n_tokens,
                                  int64_t max_q, int weights);
+QM_API int64_t qm_attn_workspace_exact(const qm_kv_cache* cache, int64_t n_heads, int64_t n_tokens,
+                                       int64_t max_q, int weights);
 
 /*
  * qm_kv_evict_q4_0 — cuts every (sequence, kv head) of `from` back to `budget`

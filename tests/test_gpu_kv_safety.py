@@ -40,7 +40,7 @@ def test_offsets_that_go_back(qm, dtype, weights):  # noqa: F811
     cache = qm.KVCache(one.k_pages, one.v_pages, one.page_table.repeat(5, 1).contiguous(),
                        torch.full((5,), n, dtype=torch.int32, device="cuda"), head_dim=dim, page_tokens=16)
     qd = to_dtype(q, dtype)
-    need = qm.qm_attn_workspace(cache, heads, new, new, weights)
+    need = qm.qm_attn_workspace(cache, heads, new, new, weights, exact=True)
     guard = 1 << 16
     ws = torch.zeros(need + guard, dtype=torch.uint8, device="cuda")
     ws[need:] = 0xA5
@@ -161,7 +161,7 @@ def test_a_workspace_of_the_callers(qm):  # noqa: F811
     q = torch.randn((2, 8, 128), device="cuda")
     p = torch.randn((160, 8, 128), device="cuda")
     want = [[qm.qm_attn_q4_0(x, y) for y in (q, p)] for x in caches]
-    need = max(qm.qm_attn_workspace(x, 8, n, n // 2) for x in caches for n in (2, 160))
+    need = qm.qm_attn_workspace(caches[0], 8, 160, 80)  # for the steps too
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     ws[:qm.ATTN_WORKSPACE_ZEROED] = 0
     for x, (a, b) in zip(caches, want):
@@ -181,7 +181,7 @@ def test_a_workspace_of_the_callers(qm):  # noqa: F811
         torch.cuda.synchronize()
         assert torch.equal(out, want[0][0])
     with pytest.raises(qm.QMError) as e:
-        qm.qm_attn_q4_0(caches[0], q, workspace=ws[:need // 4])
+        qm.qm_attn_q4_0(caches[0], q, workspace=ws[:qm.qm_attn_workspace(caches[0], 8, 2, 1, exact=True) // 256 * 256 - 256])
     assert e.value.code == qm.QM_ERR_WORKSPACE
     with pytest.raises(TypeError):
         qm.qm_attn_q4_0(caches[0], q, workspace=ws.float())
