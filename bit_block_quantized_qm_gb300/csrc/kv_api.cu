@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "qm.h"
 #include "qm_checks.h"
@@ -22,6 +23,20 @@ constexpr int64_t kMaxLen = int64_t(1) << 30;
 static_assert(qm::kAttnZeroed == QM_ATTN_WORKSPACE_ZEROED, "the header's number");
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+struct Range {
+    const void* p;
+    int64_t n;
+};
+// Whether `a` shares bytes with one of the others.
+bool meets(const Range& a, std::initializer_list<Range> others) {
+    for (const Range& b : others)
+        if (a.p && b.p && overlaps(a.p, a.n, b.p, b.n)) return true;
+    return false;
+}
+Range table_of(const qm_kv_cache* c) { return {c->page_table, int64_t(c->n_seqs) * c->table_stride * 4}; }
+Range lengths_of(const qm_kv_cache* c) { return {c->lengths, int64_t(c->n_seqs) * 4}; }
+Range starts_of(const qm_kv_cache* c, const int32_t* q_starts) { return {q_starts, (int64_t(c->n_seqs) + 1) * 4}; }
 
 // A cache's sizes and pointers; fills the kernels' view and the pool's bytes.
 int check_cache(const qm_kv_cache* c, qm::KvView* view, int64_t* pool_bytes) {
@@ -118,9 +133,9 @@ int qm_kv_append_q4_0(const qm_kv_cache* cache, const void* k, const void* v, in
     if (n_tokens == 0 || view.n_seqs == 0) return QM_OK;
     if (!k || !v) return QM_ERR_NULL;
     if (!aligned(k, 4 * item) || !aligned(v, 4 * item)) return QM_ERR_ALIGN;
-    if (overlaps(k, kb, cache->k_pages, pool) || overlaps(k, kb, cache->v_pages, pool) ||
-        overlaps(v, vb, cache->k_pages, pool) || overlaps(v, vb, cache->v_pages, pool))
-        return QM_ERR_ALIAS;
+    for (const void* p : {cache->k_pages, cache->v_pages})
+        if (meets({p, pool}, {{k, kb}, {v, vb}, table_of(cache), lengths_of(cache), starts_of(cache, q_starts)}))
+            return QM_ERR_ALIAS;
     qm::DeviceInfo dev;
     if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
     rc = check_cache_pointers(cache, dev.device);
@@ -145,10 +160,11 @@ int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t n_toke
     if (!mul_ok(n_tokens, int64_t(view.heads) * view.dim * 4, &bytes)) return QM_ERR_SHAPE;
     if (!k || !v) return QM_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16)) return QM_ERR_ALIGN;
-    if (overlaps(k, bytes, v, bytes) || overlaps(k, bytes, cache->k_pages, pool) ||
-        overlaps(k, bytes, cache->v_pages, pool) || overlaps(v, bytes, cache->k_pages, pool) ||
-        overlaps(v, bytes, cache->v_pages, pool))
-        return QM_ERR_ALIAS;
+    if (overlaps(k, bytes, v, bytes)) return QM_ERR_ALIAS;
+    for (const float* p : {k, v})
+        if (meets({p, bytes}, {{cache->k_pages, pool}, {cache->v_pages, pool}, table_of(cache), lengths_of(cache),
+                               starts_of(cache, q_starts)}))
+            return QM_ERR_ALIAS;
     qm::DeviceInfo dev;
     if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
     rc = check_cache_pointers(cache, dev.device);
@@ -206,21 +222,13 @@ int qm_attn_q4_0(const qm_kv_cache* cache, const qm_attn_args* a, void* stream) 
     if (!aligned(a->q, 4 * item) || !aligned(a->out, 4 * item) || !aligned(a->lse, 4) || !aligned(a->weights, 4) ||
         !aligned(a->workspace, 16))
         return QM_ERR_ALIGN;
-    const struct {
-        const void* p;
-        int64_t n;
-    } outs[4] = {{a->out, ob}, {a->lse, lb}, {a->weights, wb}, {a->workspace, need}},
-      ins[6] = {{a->q, qb},
-                {cache->k_pages, pool},
-                {cache->v_pages, pool},
-                {cache->page_table, int64_t(view.n_seqs) * view.table_stride * 4},
-                {cache->lengths, int64_t(view.n_seqs) * 4},
-                {a->q_starts, a->q_starts ? int64_t(view.n_seqs + 1) * 4 : 0}};
+    const Range outs[4] = {{a->out, ob}, {a->lse, lb}, {a->weights, wb}, {a->workspace, need}};
     for (int i = 0; i < 4; ++i) {
-        for (const auto& in : ins)
-            if (overlaps(outs[i].p, outs[i].n, in.p, in.n)) return QM_ERR_ALIAS;
+        if (meets(outs[i], {{a->q, qb}, {cache->k_pages, pool}, {cache->v_pages, pool}, table_of(cache), lengths_of(cache),
+                            starts_of(cache, a->q_starts)}))
+            return QM_ERR_ALIAS;
         for (int j = 0; j < i; ++j)
-            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QM_ERR_ALIAS;
+            if (meets(outs[i], {outs[j]})) return QM_ERR_ALIAS;
     }
     qm::DeviceInfo dev;
     if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
@@ -272,6 +280,20 @@ int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float
     if (weights_out != weights && overlaps(weights, wb, weights_out, ob)) return QM_ERR_ALIAS;
     if (weights_out == weights && out_stride != weights_stride) return QM_ERR_ALIAS;
     if (overlaps(kept, kb, weights, wb) || overlaps(kept, kb, weights_out, ob)) return QM_ERR_ALIAS;
+    // Two arrays of lengths that share some entries would change under the kernels that read them.
+    if (from->lengths != to->lengths && meets(lengths_of(to), {lengths_of(from)})) return QM_ERR_ALIAS;
+    // What is written (the pools, the lengths, the lists) shares nothing with what else is read or written.
+    const Range ranks[3] = {{kept, kb}, {weights_out, ob}, {weights, wb}};
+    for (const Range& x : ranks)
+        if (meets(x, {{src.k, src_pool}, {src.v, src_pool}, {dst.k, dst_pool}, {dst.v, dst_pool}, lengths_of(to)}))
+            return QM_ERR_ALIAS;
+    for (int i = 0; i < 2; ++i)
+        if (meets(ranks[i], {table_of(from), table_of(to), lengths_of(from)})) return QM_ERR_ALIAS;
+    if (meets(lengths_of(to), {{src.k, src_pool}, {src.v, src_pool}, {dst.k, dst_pool}, {dst.v, dst_pool}, table_of(from),
+                               table_of(to)}))
+        return QM_ERR_ALIAS;
+    for (const void* p : {dst.k, dst.v})
+        if (meets({p, dst_pool}, {table_of(from), table_of(to), lengths_of(from)})) return QM_ERR_ALIAS;
     qm::DeviceInfo dev;
     if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
     rc = check_cache_pointers(from, dev.device);

@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(kThreads)
         int64_t to = -1;
         if (at < end) {
             const int token = kept[at];
-            const int64_t from = kv_cell(src, b, h, token, &g_kv_error);
+            if (token < 0) atomicOr(&g_kv_error, kErrRange);  // (a length that changed meanwhile)
+            const int64_t from = token < 0 ? -1 : kv_cell(src, b, h, token, &g_kv_error);
             to = kv_cell(dst, b, h, at, &g_kv_error);
             if (from < 0) to = -1;
             if (to >= 0) {

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import bit_block_quantized_qm_gb300 as qm
-from test_kv_cache_cpu import FINE, args, attn, cache, lib  # noqa: F401
+from test_kv_cache_cpu import FINE, K, L, O, Q, S, T, V, append, args, attn, cache, evict, lib  # noqa: F401
 
 
 def test_rows_and_heads_are_numbered_in_32_bits(lib):  # noqa: F811
@@ -46,3 +46,43 @@ def test_a_prompts_workspace_runs_the_next_step(lib):  # noqa: F811
                 workspace=1 << 40)
     assert attn(lib, c, args(**step)) in FINE
     assert workspace(lib, c, 32, 2048, 2048, 0, exact=True) < workspace(lib, c, 32, 1, 1, 0, exact=True) <= need
+
+
+# ---- what is written shares no bytes with what else is read or written
+
+@pytest.mark.parametrize("kw,bad", [
+    (dict(page_table=K + 64), {}), (dict(page_table=V + 11516), {}), (dict(lengths=K), {}), (dict(lengths=V - 4), {}),
+    ({}, dict(starts=K + 128)), ({}, dict(starts=V - 8))], ids=str)
+def test_append_writes_pools_alone(lib, kw, bad):  # noqa: F811
+    assert append(lib, cache(**kw), **bad) == qm.QM_ERR_ALIAS
+
+
+@pytest.mark.parametrize("bad", [dict(k=T), dict(v=T - 16), dict(k=L), dict(v=L - 3056), dict(starts=Q + 8),
+                                 dict(starts=O + 3068), dict(k=T - 3056)], ids=str)
+def test_read_writes_rows_alone(lib, bad):  # noqa: F811
+    d = dict(k=Q, v=O, starts=S)
+    d.update(bad)
+    c = cache()
+    assert lib.qm_kv_read_q4_0(ctypes.addressof(c), d["k"], d["v"], 6, d["starts"], None) == qm.QM_ERR_ALIAS
+
+
+FAR = dict(k_pages=K + (1 << 24), v_pages=V + (1 << 24), page_table=T + 4096, lengths=L + 4096)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kept=K + 16), dict(kept=V - 4), dict(kept=K + (1 << 24)), dict(kept=V + (1 << 24) + 11516), dict(kept=T),
+    dict(kept=T + 4096), dict(kept=L - 600), dict(kept=L + 4096), dict(wo=K), dict(wo=V + 64), dict(wo=K + (1 << 24)),
+    dict(wo=T + 36), dict(wo=T + 4100), dict(wo=L + 4), dict(wo=L + 4100), dict(w=K + (1 << 24)), dict(w=L + 4096 - 1276),
+    dict(w=V + (1 << 24)), dict(to=cache(**{**FAR, "lengths": L + 4})), dict(to=cache(**{**FAR, "lengths": L - 4})),
+    dict(to=cache(**{**FAR, "lengths": T + 8})), dict(to=cache(**{**FAR, "lengths": K + 256})),
+    dict(to=cache(**{**FAR, "page_table": K + (1 << 24) + 512})), dict(to=cache(**{**FAR, "k_pages": T - 64})),
+    dict(to=cache(**{**FAR, "v_pages": L - 64}))], ids=lambda x: str(x)[:60])
+def test_evict_writes_what_it_says_alone(lib, bad):  # noqa: F811
+    assert evict(lib, **bad) == qm.QM_ERR_ALIAS
+
+
+def test_evict_with_shared_lengths_and_shared_pools_passes(lib):  # noqa: F811
+    assert evict(lib, to=cache(**{**FAR, "lengths": L})) in FINE
+    assert evict(lib, to=cache(page_table=T + 4096, lengths=L + 4096)) in FINE  # the same pools, other pages
+    assert evict(lib, to=cache(lengths=L + 4096)) in FINE  # in place, lengths apart
+    assert evict(lib, to=cache(lengths=L + 8)) in FINE  # lengths side by side
