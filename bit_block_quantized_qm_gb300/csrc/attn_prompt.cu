@@ -563,8 +563,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                 x.q[y] = make_uint4(0, 0, 0, 0);
                 x.sc[y] = 0;
                 if (off >= 0) {
-                    x.q[y] = __ldg(reinterpret_cast<const uint4*>(pool + off + in_cell + y * kStride * 256));
-                    x.sc[y] = __ldg(reinterpret_cast<const uint16_t*>(pool + off + in_scales + y * kStride * 2));
+                    x.q[y] = *reinterpret_cast<const uint4*>(pool + off + in_cell + y * kStride * 256);
+                    x.sc[y] = *reinterpret_cast<const uint16_t*>(pool + off + in_scales + y * kStride * 2);
                 }
             }
         };
@@ -764,8 +764,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             for (int e = 0; e < kWords; e += 4) {
                 uint4 y = make_uint4(0, 0, 0, 0), z = y;
                 if (off >= 0) {
-                    y = __ldg(reinterpret_cast<const uint4*>(c.k + at + 4 * e));
-                    z = __ldg(reinterpret_cast<const uint4*>(c.v + at + 4 * e));
+                    y = *reinterpret_cast<const uint4*>(c.k + at + 4 * e);
+                    z = *reinterpret_cast<const uint4*>(c.v + at + 4 * e);
                 }
                 x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
                 v[e] = z.x, v[e + 1] = z.y, v[e + 2] = z.z, v[e + 3] = z.w;

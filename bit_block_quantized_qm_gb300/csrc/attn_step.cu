@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(256) attn_step_weights_kernel(KvView c, KvRows
     const float* lse = reinterpret_cast<const float*>(a.ws + plan.lse_off) + h * group;
     for (int x = threadIdx.x; x < count * group; x += 256) {
         const int i = x / group;
-        row_lse[x] = __ldg(lse + static_cast<int64_t>(first + i) * a.heads + (x - i * group));
+        row_lse[x] = lse[static_cast<int64_t>(first + i) * a.heads + (x - i * group)];
     }
     __syncthreads();
     if (j >= L) return;

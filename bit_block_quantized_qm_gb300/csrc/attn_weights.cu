@@ -42,7 +42,7 @@ struct WShape {
 
 template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_weights_kernel(KvView c, KvRows r, AttnCall a, QueryTiles qt, const float* __restrict__ lse2, uint32_t k1024) {
+    attn_weights_kernel(KvView c, KvRows r, AttnCall a, QueryTiles qt, const float* lse2, uint32_t k1024) {
     using S = WShape<D, F32>;
     constexpr int NB = S::kBlocks;
     extern __shared__ __align__(1024) uint8_t smem_raw[];

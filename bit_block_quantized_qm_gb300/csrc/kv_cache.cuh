@@ -1,5 +1,8 @@
 // The paged Q4_0 key/value cache as the kernels see it: layout of cells and
-// pages, the rows of a call, and bounds-checked look-ups.
+// pages, the rows of a call, and bounds-checked look-ups.  Everything is read by
+// plain loads: a kernel may start while the one before it still writes lengths,
+// tables or cells, and read-only loads want memory that nothing writes as long as
+// the kernel lives.
 #pragma once
 
 #include "qm_device.cuh"
@@ -17,7 +20,7 @@ __host__ __device__ constexpr int cell_scales(int D) { return 8 * D; }  // offse
 
 // Tokens in the cache of sequence b, and what is wrong with the number.
 __device__ __forceinline__ int kv_length(const KvView& c, int b, unsigned int* err) {
-    const int n = __ldg(c.lengths + b);
+    const int n = c.lengths[b];
     if (n < 0 || n > c.max_len) {
         atomicOr(err, kErrRange);
         return n < 0 ? 0 : static_cast<int>(c.max_len);
@@ -32,7 +35,7 @@ __device__ __forceinline__ void kv_rows(const KvRows& r, int b, int* first, int*
         *count = r.uniform;
         return;
     }
-    int a = __ldg(r.starts + b), e = __ldg(r.starts + b + 1);
+    int a = r.starts[b], e = r.starts[b + 1];
     if (a < 0 || e < a || e > r.n_tokens || e - a > r.max_q) {
         atomicOr(err, kErrRange);
         a = min(max(a, 0), r.n_tokens);
@@ -45,7 +48,7 @@ __device__ __forceinline__ void kv_rows(const KvRows& r, int b, int* first, int*
 // The page that holds token `pos` of sequence b; -1 past the page table.
 __device__ __forceinline__ int kv_page_id(const KvView& c, int b, int pos) {
     const int page = pos >> c.page_shift;
-    return page < c.table_stride ? __ldg(c.table + b * c.table_stride + page) : -1;
+    return page < c.table_stride ? c.table[b * c.table_stride + page] : -1;
 }
 // Byte offset in the pool of the cell that holds token `pos` of a sequence, in page
 // `id`, of kv head h; -1 (and the error bit) where `id` is no page.
@@ -67,10 +70,10 @@ __device__ __forceinline__ int kv_seq_of_row(const KvRows& r, int n_seqs, int ro
     int lo = 0, hi = n_seqs;  // the last b with starts[b] <= row
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(r.starts + mid + 1) <= row) lo = mid + 1;
+        if (r.starts[mid + 1] <= row) lo = mid + 1;
         else hi = mid;
     }
-    return lo < n_seqs && __ldg(r.starts + lo) <= row ? lo : -1;
+    return lo < n_seqs && r.starts[lo] <= row ? lo : -1;
 }
 
 }  // namespace qm
