@@ -18,6 +18,8 @@
 // A CTA of 18 warps per (sequence, kv head, 128 tokens), the tokens that most rows
 // see first: 16 warps sum (four per 32 tokens, a quarter of the rows each), one
 // issues the MMAs into two TMEM buffers, one loads.
+#include <type_traits>
+
 #include "tcgen05.cuh"
 
 namespace qm {
@@ -162,17 +164,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float v[32];
                 tmem_ld32(tmem + lanes + 128 * buf + col, v);
                 tc_wait_ld();
-                if (__any_sync(0xFFFFFFFFu, sees != ~0u)) {
+                // Hidden rows are taken out of the addends, not of the scores: a row whose
+                // logarithm is NaN would make NaN of any score.
+                auto add = [&](auto masked) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((sees >> e) & 1u)) v[e] = -INFINITY;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float4 f = *reinterpret_cast<const float4*>(&factor[at][2 * (col + e)]);  // units, then logarithms
-                    const float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
-                    sum = add2(sum, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
-                }
+                    for (int e = 0; e < 32; e += 2) {
+                        const float4 f = *reinterpret_cast<const float4*>(&factor[at][2 * (col + e)]);  // units, then logarithms
+                        const float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+                        float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        if (decltype(masked)::value) {
+                            if (!((sees >> e) & 1u)) p.x = 0.f;
+                            if (!((sees >> (e + 1)) & 1u)) p.y = 0.f;
+                        }
+                        sum = add2(sum, p);
+                    }
+                };
+                if (__any_sync(0xFFFFFFFFu, sees != ~0u)) add(std::true_type{});
+                else add(std::false_type{});
                 acc += sum.x + sum.y;
             }
             tc_fence_before();

@@ -50,3 +50,33 @@ def test_statistics_of_bf16_rows(qm, case):  # noqa: F811
     # every row has given 1 for each query head
     rows = np.asarray(new) * 8.0
     assert np.allclose(got.sum((1, 2)), rows, rtol=4 * ds.max() + 2.0 ** -18)
+
+
+# ---- a bad row's weights
+
+@pytest.mark.parametrize("dim", [128, 64, 96])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", [(300, 1, 0, 0), (300, 6, 0, 0), (300, 200, 0, 0), (420, 300, 60, 3)],
+                         ids=["step", "draft", "prompt", "window"])
+def test_a_bad_rows_weights_stay_with_the_tokens_it_sees(qm, case, dtype, dim):  # noqa: F811
+    """A row whose query is not finite makes the weights of the tokens that it sees
+    NaN; those that it does not see keep what the other rows give them."""
+    n, new, window, sinks = case
+    c = ko.Cache([n], 1, dim, 16, seed=39)
+    q = np.random.default_rng(40).standard_normal((new, 4, dim)).astype(np.float32)
+    bad = new // 2
+    good = q.copy()
+    good[bad, 1] = 0
+    spoiled = good.copy()
+    spoiled[bad, 1, 7] = np.nan
+    cache = device(qm, c)
+    ws = []
+    for x in (good, spoiled):
+        w = torch.full((1, 1, cache.max_len), 0.25, device="cuda")
+        qm.qm_attn_q4_0(cache, to_dtype(x, dtype), window=window, sinks=sinks, weights=w)
+        ws.append(w[0, 0].cpu().numpy())
+    sees = ko.visible([n - new + bad], n, window, sinks)[0]
+    assert np.isnan(ws[1][:n][sees]).all()
+    assert np.array_equal(ws[1][:n][~sees], ws[0][:n][~sees])
+    assert (ws[1][n:] == 0.25).all()
+    assert qm.qm_device_status(clear=True) == qm.QM_OK
