@@ -13,17 +13,27 @@
 //     to the top of f16's range; each block of 32 is scaled by d_jb in f32.
 //   output  o = sum_j (p_j d_jb) (n_j - 8): dims are the rows, query rows again
 //     two columns each, p_j d_jb as f16 and the exact f16 remainder (two packed
-//     FMAs per two tokens).  p is scaled by 2^14, or less where the largest
-//     scale seen would take p d out of f16's range (then the sums follow).
-// The softmax runs in one pass with a running maximum and sum in f32.
+//     FMAs per two tokens).
+// The softmax runs in one pass with a running maximum and sum in f32.  Each tile has
+// its own maximum per row (rounded up to a whole power of two, so the factor to the
+// running one is exact) and its own power of two for the value scales: p d then
+// begins at the top of f16's range whatever the scores and scales are, and a pair
+// holds 2^-21 of it down to 2^-18 of the tile's largest, 2^-17 down to 2^-22.  A tile
+// that spans more (scores of deviation 3 or so, or scales far apart) takes three
+// bf16 pieces (24 bits, f32's range) in a loop of its own: 64 sequences of 8192 tokens
+// 188 us in place of 136 where every tile does.  A tile's products join the sums by
+// f32 FMAs.  (Sums left in the tensor cores' accumulators, one power of two for all
+// tiles and p from the running maximum took 129 us, but were off by 3e-6 over 16384
+// values of one sign, by 2^-10 and more among scales far apart, and 206 us with one
+// token 8 nats above the others, where this takes 138.)
 //
 // Bytes are its floor: 9 D / 8 per token and kv head.  A tensor-core product covers
 // 256 quants = 144 bytes, which HBM delivers in 6 cycles per SM; unpacking on
 // the FP32 pipe alone (one FMA per quant and query row) would need 3 times
-// that at four rows.  What bounds it as it is: 345 instructions per 16 tokens,
-// keys, softmax and values together (issue slots 60% busy).  Measured, 32 heads
-// of 8 kv heads, D = 128: 64 sequences of 8192 tokens 129 us, 4.7 TB/s; ragged
-// ones of up to 8192 97 us, 3.9 TB/s; one of 131071 47 us, 3.2 TB/s.
+// that at four rows.  What bounds it as it is: 366 instructions per 16 tokens,
+// keys, softmax and values together, in chains that 12 warps per SM cannot hide.
+// Measured, 32 heads of 8 kv heads, D = 128: 64 sequences of 8192 tokens 136 us,
+// 4.4 TB/s; ragged ones of up to 8192 101 us, 3.7 TB/s; one of 131071 48 us, 3.1 TB/s.
 //
 // Split.  All (sequence, kv head, 4 or 8 rows) lists of 64-token tiles lie end to
 // end, and every CTA of a grid that fills the GPU once takes an equal stretch
@@ -48,7 +58,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;  // tokens of a warp's tile
 constexpr int kStages = 2;  // tiles in a warp's ring
 constexpr int kCtasPerSm = 3;
-constexpr float kTiny = 0x1p-23f, kTinyLog = -23.f;
+// How far (log2) below a tile's largest p d its smallest may lie in f16 pairs.
+constexpr float kPairSpan = 22.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -117,6 +128,14 @@ __device__ __forceinline__ void mma_f16_first(float c[4], uint32_t a0, uint32_t 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// The bf16 product, from zero and onto a sum.
+__device__ __forceinline__ void mma_bf16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // lo in bits 0..15
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -165,10 +184,38 @@ __device__ __forceinline__ uint32_t minus8_high(uint32_t w, uint32_t k1024) {
                            as_half2(0xD480D480u)));                                      // - 72
 }
 
+// n - 8 as bf16 pairs for the low nibbles of bytes 0 and 2: OR-ed into the mantissa of
+// 128 a nibble reads 128 + n.
+__device__ __forceinline__ uint32_t minus8_bf16(uint32_t w) {
+    const uint32_t x = (w & 0x000F000Fu) | 0x43004300u, m136 = 0xC308C308u;
+    const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&m136));
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
+// Three bf16 pieces of two f32 numbers (lo in bits 0..15): 24 bits, with f32's range.
+__device__ __forceinline__ void pieces_bf16(float lo, float hi, uint32_t w[3]) {
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+        w[e] = *reinterpret_cast<const uint32_t*>(&y);
+        lo -= __uint_as_float(w[e] << 16);
+        hi -= __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// o += acc f, two at a time.
+__device__ __forceinline__ void add_to(float o[4], const float acc[4], float f) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+        asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; mov.b64 z, {%0, %1};\n"
+            "fma.rn.f32x2 z, x, y, z; mov.b64 {%0, %1}, z;}"
+            : "+f"(o[e]), "+f"(o[e + 1])
+            : "f"(acc[e]), "f"(acc[e + 1]), "f"(f));
 }
 
 // 2^e for e in -126 .. 127.
@@ -432,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][k][0][e] = o[j][k][1][e] = 0.f;
     }
-    int v_up = 14;  // p is scaled by 2^v_up
     const uint32_t k1024 = plan.k1024;
 
     // Scores of a tile, to base 2: s[cell][j][0] of token 16 cell + g, [1]: 8 further.
@@ -475,8 +521,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
             s[cell][j][1] *= to_log2[j];
         }
     };
-    // o += sum over the cell's tokens of 2^v_up p d (n - 8); s holds p.
-    auto output_cell = [&](const uint8_t* vt, int cell, const float (&s)[4][NT][2], float up) {
+    // o += f * sum over the cell's tokens of up p d (n - 8); s holds p.  The products of a
+    // cell start from zero: the tensor cores cut their sums off instead of rounding them,
+    // which over many tiles would show (3e-6 of sums of one sign after 64 tiles).
+    auto output_cell = [&](const uint8_t* vt, int cell, const float (&s)[4][NT][2], float up, const float (&f)[NT]) {
         const uint8_t* cp = vt + cell * cell_bytes(D);
         // p of tokens 2 t, 2 t + 1 and 8 further, of row 4 j + g / 2: f16 value
         // and remainder, fetched from the lanes that hold them.
@@ -523,22 +571,54 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
                     const __half2 ra = __hfma2(as_half2(pl[j][0]), da, __hfma2(pa, da, __hneg2(xa)));
                     const __half2 rb = __hfma2(as_half2(pl[j][1]), db, __hfma2(pb, db, __hneg2(xb)));
                     const uint32_t b0 = as_word((g & 1) ? ra : xa), b1 = as_word((g & 1) ? rb : xb);
-                    mma_f16(o[j][k][0], l0, l1, l2, l3, b0, b1);
-                    mma_f16(o[j][k][1], h0, h1, h2, h3, b0, b1);
+                    float acc[4];
+                    mma_f16_first(acc, l0, l1, l2, l3, b0, b1);
+                    add_to(o[j][k][0], acc, f[j]);
+                    mma_f16_first(acc, h0, h1, h2, h3, b0, b1);
+                    add_to(o[j][k][1], acc, f[j]);
                 }
             }
         }
     };
-    auto scale_o = [&](float f) {
+    // The same where p d spans more than f16 pairs hold: three bf16 pieces of p d (24
+    // bits, f32's range) in three of every four columns of two products.
+    auto output_wide = [&](const uint8_t* cp, const float (&s)[NT][2], const float (&f)[NT]) {
+        const int from = 8 * t + (g >> 1);
+        float p[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int k = 0; k < NB; ++k)
+            for (int e = 0; e < 4; ++e) p[j][e] = __shfl_sync(0xFFFFFFFFu, s[j][e >> 1], from + 4 * (e & 1));
+        uint32_t dw[2][NB];
+        load_words<NB>(cp + cell_scales(D) + 2 * t * 2 * NB, dw[0]);
+        load_words<NB>(cp + cell_scales(D) + (2 * t + 8) * 2 * NB, dw[1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[j][k][0][e] *= f;
-                    o[j][k][1][e] *= f;
+        for (int k2 = 0; k2 < NB; k2 += 2) {
+            uint32_t w[4];
+            ldmatrix_x4_trans(smem_addr(cp) + k2 * 256 + lane * 16, w);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = k2 + u;
+                const uint32_t sel = u ? 0x7632u : 0x5410u;
+                const float2 da = __half22float2(as_half2(__byte_perm(dw[0][k2 / 2], dw[0][NB / 2 + k2 / 2], sel)));
+                const float2 db = __half22float2(as_half2(__byte_perm(dw[1][k2 / 2], dw[1][NB / 2 + k2 / 2], sel)));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t x[3], y[3];
+                    pieces_bf16(p[j][0] * da.x, p[j][1] * da.y, x);
+                    pieces_bf16(p[j][2] * db.x, p[j][3] * db.y, y);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t w0 = w[2 * u] >> (4 * half), w1 = w[2 * u + 1] >> (4 * half);
+                        const uint32_t a[4] = {minus8_bf16(w0), minus8_bf16(w0 >> 8), minus8_bf16(w1), minus8_bf16(w1 >> 8)};
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_bf16(acc, a, (g & 1) ? 0u : x[2], (g & 1) ? 0u : y[2]);
+                        mma_bf16(acc, a, (g & 1) ? x[1] : x[0], (g & 1) ? y[1] : y[0]);
+                        add_to(o[j][k][half], acc, f[j]);
+                    }
                 }
+            }
+        }
     };
 
     float s[4][NT][2];
@@ -553,54 +633,76 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
 #pragma unroll
         for (int cell = 0; cell < 4; ++cell) score_cell(kt, cell, s);
 
-        // Scales of the values: where none reaches 2 (a bit of the exponent)
-        // and no token is past the end, nothing is to be done.
+        // Scales of the values: the largest and the smallest that is not 0.  Tokens past
+        // the end and those with a scale that is not finite get scales of 0.
         uint32_t bad0 = 0, bad1 = 0;  // tokens with a scale that is not finite
-        {
-            uint32_t w[NB];
-            load_words<NB>(vt + (lane >> 3) * cell_bytes(D) + cell_scales(D) + (lane & 7) * 4 * NB, w);
-            uint32_t any = w[0];
+        uint32_t top, low;            // bits of the largest; of the smallest, less 1
+        uint32_t w[NB];               // two tokens' scales
+        uint8_t* const my_scales = vt + (lane >> 3) * cell_bytes(D) + cell_scales(D) + (lane & 7) * 4 * NB;
+        auto extremes = [&]() {
+            load_words<NB>(my_scales, w);
+            uint32_t hi2 = 0x80008000u, lo2 = 0xFFFFFFFFu;
 #pragma unroll
-            for (int e = 1; e < NB; ++e) any |= w[e];
-            if (__any_sync(0xFFFFFFFFu, (any & 0x40004000u) != 0) || key0 + kTile > seen_len) {
-                uint32_t top = 0;
+            for (int e = 0; e < NB; ++e) {
+                const uint32_t y = w[e] | 0x80008000u;
+                hi2 = __vmaxu2(hi2, y);
+                lo2 = __vminu2(lo2, (y - 0x00010001u) ^ 0x80008000u);  // (0 becomes the largest)
+            }
+            top = __reduce_max_sync(0xFFFFFFFFu, max(hi2 & 0x7FFFu, (hi2 >> 16) & 0x7FFFu));
+            low = __reduce_min_sync(0xFFFFFFFFu, min(lo2 & 0xFFFFu, lo2 >> 16));
+        };
+        extremes();
+        if (top >= 0x7C00u || key0 + kTile > seen_len) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int key = u * 32 + lane;
-                    uint8_t* sc = vt + (key >> 4) * cell_bytes(D) + cell_scales(D) + (key & 15) * 2 * NB;
-                    uint32_t y[NB / 2];
-                    load_words<NB / 2>(sc, y);
-                    uint32_t mx = y[0] & 0x7FFF7FFFu;
+            for (int u = 0; u < 2; ++u) {
+                const int key = u * 32 + lane;
+                uint8_t* sc = vt + (key >> 4) * cell_bytes(D) + cell_scales(D) + (key & 15) * 2 * NB;
+                uint32_t y[NB / 2];
+                load_words<NB / 2>(sc, y);
+                uint32_t mx = y[0] & 0x7FFF7FFFu;
 #pragma unroll
-                    for (int e = 1; e < NB / 2; ++e) mx = __vmaxu2(mx, y[e] & 0x7FFF7FFFu);
-                    mx = max(mx & 0xFFFFu, mx >> 16);
-                    const bool past = key0 + key >= seen_len;
-                    const bool wild = !past && mx >= 0x7C00u;
-                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, wild);
-                    if (u == 0) bad0 = bits;
-                    else bad1 = bits;
-                    if (past || wild) {  // such tokens' products are 0; NaN comes with the scores
+                for (int e = 1; e < NB / 2; ++e) mx = __vmaxu2(mx, y[e] & 0x7FFF7FFFu);
+                mx = max(mx & 0xFFFFu, mx >> 16);
+                const bool past = key0 + key >= seen_len;
+                const bool wild = !past && mx >= 0x7C00u;
+                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, wild);
+                if (u == 0) bad0 = bits;
+                else bad1 = bits;
+                if (past || wild) {  // such tokens' products are 0; NaN comes with the scores
 #pragma unroll
-                        for (int e = 0; e < NB / 2; ++e) reinterpret_cast<uint32_t*>(sc)[e] = 0u;
-                        mx = 0;
-                    }
-                    top = max(top, mx);
-                }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-                __syncwarp();
-                // p 2^v_up d < 2^15 for d < 2^(exponent + 1).
-                const int need = min(14, 14 - (static_cast<int>(top >> 10) - 15));
-                if (need < v_up) {
-                    scale_o(pow2(need - v_up));
-                    v_up = need;
+                    for (int e = 0; e < NB / 2; ++e) reinterpret_cast<uint32_t*>(sc)[e] = 0u;
                 }
             }
+            __syncwarp();
+            extremes();
         }
+        // p d goes to the top of f16's range, p 2^p_up times d 2^d_up below 2^16: p takes
+        // up to 2^15, the scales in shared memory (exactly) what is left.
+        const int top_e = max(1, static_cast<int>(top >> 10));
+        const int p_up = min(15, 30 - top_e), d_up = max(0, 15 - top_e);
+        if (d_up) {
+            const uint32_t twice = static_cast<uint32_t>(15 + d_up) * 0x04000400u;
+#pragma unroll
+            for (int e = 0; e < NB; ++e) reinterpret_cast<uint32_t*>(my_scales)[e] = as_word(__hmul2(as_half2(w[e]), as_half2(twice)));
+            __syncwarp();
+        }
+        // How far below the row's largest a token's p may be for f16 pairs (log2).
+        const float span = low == 0xFFFFu ? kPairSpan
+                                          : kPairSpan - static_cast<float>((__float_as_uint(f16_bits_to_float(top)) >> 23) -
+                                                                           (__float_as_uint(f16_bits_to_float(low + 1)) >> 23));
 
         // What a row does not see, and tokens whose values are not finite.
         const bool all_seen = key0 + kTile <= min(pos_lo + 1, L) && !(bad0 | bad1) &&
                               (a.window == 0 || key0 > pos_hi - a.window || key0 + kTile <= a.sinks);
-        if (!all_seen) {
+        float mn[NT];  // of the scores that the row sees, this thread's
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mn[j] = INFINITY;
+        if (all_seen) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int cell = 0; cell < 4; ++cell) mn[j] = fminf(fminf(mn[j], s[cell][j][0]), s[cell][j][1]);
+        } else {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -612,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
                         const bool sees = key <= pos[j] && key < L &&
                                           (a.window == 0 || key > pos[j] - a.window || key < a.sinks);
                         if (((in_tile < 32 ? bad0 : bad1) >> (in_tile & 31)) & 1u) s[cell][j][e] = NAN;
-                        if (!sees) s[cell][j][e] = -INFINITY;
+                        if (sees) mn[j] = fminf(mn[j], s[cell][j][e]);
+                        else s[cell][j][e] = -INFINITY;
                     }
         }
         if (plan.pad_len) {
@@ -630,23 +733,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
                 }
             }
         }
-        bool small = false;  // some token's p is below kTiny, but not 0
+        // p is taken from the tile's own maximum, rounded up to a whole power of two, and
+        // the tile's sums join the running ones with an exact factor f.
+        bool wide = false;  // p d spans more than f16 pairs hold
+        float f[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            float mx = -INFINITY, mn = INFINITY;
+            float mx = -INFINITY;
 #pragma unroll
-            for (int cell = 0; cell < 4; ++cell)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx = fmaxf(mx, s[cell][j][e]);
-                    mn = fminf(mn, s[cell][j][e]);
-                }
+            for (int cell = 0; cell < 4; ++cell) mx = fmaxf(fmaxf(mx, s[cell][j][0]), s[cell][j][1]);
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, y));
-            const float m2 = fmaxf(m[j], mx);
-            const float base = m2 == -INFINITY ? 0.f : m2;
+            mx = ceilf(mx);
+            const float base = mx == -INFINITY ? 0.f : mx;
+            wide |= base - mn[j] > span;
             if (mx > m[j]) {
-                const float keep = exp2_approx(m[j] - base);
+                const float keep = exp2_approx(m[j] - mx);
+                m[j] = mx;
                 l[j] *= keep;
 #pragma unroll
                 for (int k = 0; k < NB; ++k)
@@ -656,80 +759,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
                         o[j][k][1][e] *= keep;
                     }
             }
-            m[j] = m2;
-            small |= mn - base < kTinyLog;  // (masked tokens too: their p is 0 below)
+            f[j] = exp2_approx(mx - (m[j] == -INFINITY ? 0.f : m[j]));
+            float sum = 0.f;
 #pragma unroll
             for (int cell = 0; cell < 4; ++cell) {
                 s[cell][j][0] = exp2_approx(s[cell][j][0] - base);
                 s[cell][j][1] = exp2_approx(s[cell][j][1] - base);
-                l[j] += s[cell][j][0] + s[cell][j][1];
+                sum += s[cell][j][0] + s[cell][j][1];
+            }
+            l[j] = fmaf(f[j], sum, l[j]);
+        }
+        if (!__any_sync(0xFFFFFFFFu, wide)) {
+            const float up = pow2(p_up), unit = pow2(-p_up - d_up);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) f[j] *= unit;
+#pragma unroll
+            for (int cell = 0; cell < 4; ++cell) output_cell(vt, cell, s, up, f);
+        } else {
+            const float unit = pow2(-d_up);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) f[j] *= unit;
+#pragma unroll 1
+            for (int cell = 0; cell < 4; ++cell) {
+                float one[NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        one[j][e] = cell == 0 ? s[0][j][e] : cell == 1 ? s[1][j][e] : cell == 2 ? s[2][j][e] : s[3][j][e];
+                output_wide(vt + cell * cell_bytes(D), one, f);
             }
         }
-        const float up = pow2(v_up);
-        small = __any_sync(0xFFFFFFFFu, small);
-        if (small) {
-            // An f16 pair holds p to 2^-17 of itself down to 2^-23 of the running
-            // maximum.  Tokens below that (rare: 16 in natural logarithm) go in
-            // passes of their own with everything lifted by 2^23, so a dim where
-            // the large ones happen to be 0 keeps its precision; below 2^-92
-            // they count as 0.
-            float rest[4][NT][2];
-            float lift = 1.f;
-#pragma unroll 1
-            for (;;) {
-                bool more = false;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int cell = 0; cell < 4; ++cell)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float p = s[cell][j][e];
-                            const bool below = p < kTiny;  // (false for NaN)
-                            more |= below && p > 0.f;
-                            rest[cell][j][e] = below ? p * (1.f / kTiny) : 0.f;
-                            if (below) s[cell][j][e] = 0.f;
-                        }
-                more = __any_sync(0xFFFFFFFFu, more) && lift < 0x1p69f;
-                if (!more) break;
-                // The tokens at hand now, the others lifted next.
-#pragma unroll 1
-                for (int cell = 0; cell < 4; ++cell) {
-                    float one[4][NT][2];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            one[0][j][e] = cell == 0 ? s[0][j][e] : cell == 1 ? s[1][j][e] : cell == 2 ? s[2][j][e] : s[3][j][e];
-                    output_cell(vt + cell * cell_bytes(D), 0, one, up);
-                }
-                lift *= 1.f / kTiny;
-                scale_o(1.f / kTiny);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int cell = 0; cell < 4; ++cell) s[cell][j][0] = rest[cell][j][0], s[cell][j][1] = rest[cell][j][1];
-            }
-            if (lift != 1.f) {  // the last pass, below, adds at the lifted scale: taken here instead
-#pragma unroll 1
-                for (int cell = 0; cell < 4; ++cell) {
-                    float one[4][NT][2];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            one[0][j][e] = cell == 0 ? s[0][j][e] : cell == 1 ? s[1][j][e] : cell == 2 ? s[2][j][e] : s[3][j][e];
-                    output_cell(vt + cell * cell_bytes(D), 0, one, up);
-                }
-                scale_o(1.f / lift);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int cell = 0; cell < 4; ++cell) s[cell][j][0] = s[cell][j][1] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int cell = 0; cell < 4; ++cell) output_cell(vt, cell, s, up);
         __syncwarp();
         const int nx = x + kStages;
         if (nx < my_tiles) {
@@ -749,7 +809,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
     // The warps' sums meet in shared memory: [row][D] sums, then maxima, then l.
     __syncthreads();
     float* mine = reinterpret_cast<float*>(my_ring);
-    const float unit = pow2(-v_up);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -760,9 +819,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
             const float* lo = o[j][k][0];
             const float* hi = o[j][k][1];
             *reinterpret_cast<float2*>(dst + 32 * k) =
-                make_float2((lo[0] + lo[1]) * unit, (lo[2] + lo[3]) * unit);
+                make_float2(lo[0] + lo[1], lo[2] + lo[3]);
             *reinterpret_cast<float2*>(dst + 32 * k + 16) =
-                make_float2((hi[0] + hi[1]) * unit, (hi[2] + hi[3]) * unit);
+                make_float2(hi[0] + hi[1], hi[2] + hi[3]);
         }
         if (g == 0) {
             mine[S::kRows * D + 4 * j + t] = m[j];

@@ -52,6 +52,97 @@ def test_statistics_of_bf16_rows(qm, case):  # noqa: F811
     assert np.allclose(got.sum((1, 2)), rows, rtol=4 * ds.max() + 2.0 ** -18)
 
 
+# ---- value scales anywhere in binary16's range, and mixed ones
+
+def step_and_prompt(new):
+    return pytest.mark.parametrize("new", new, ids=["step", "draft", "prompt"][:len(new)])
+
+
+@pytest.mark.parametrize("v_scale", [2.0 ** -16, 2.0 ** -20, 2.0 ** -22])
+@step_and_prompt([1, 3, 90])
+def test_small_value_scales(qm, new, v_scale):  # noqa: F811
+    """Scales that are small or subnormal in binary16."""
+    for seed in (33, 34):
+        c = ko.Cache([310], 1, 128, 16, seed=seed)
+        s = scales_of(c, c.v)
+        s[:] = (s.astype(np.float32) * (v_scale / 0.1)).astype(np.float16)
+        check_attend(qm, c, [new], 4, F32)
+
+
+@pytest.mark.parametrize("far", [8, 14, 20, 26])
+@pytest.mark.parametrize("v_scale", [2.0 ** -13, 2.0 ** -6, 4.0])
+@step_and_prompt([1, 3, 90])
+def test_a_dominant_token_whose_value_is_nothing(qm, new, v_scale, far):  # noqa: F811
+    """Token 40 outweighs every other by 2^far or so and its values are 0: the output is
+    made of the others alone, and they keep their bits."""
+    n, dim = 300, 128
+    c = ko.Cache([n], 1, dim, 16, seed=35)
+    s = scales_of(c, c.v)
+    s[:] = (s.astype(np.float32) * (v_scale / 0.1)).astype(np.float16)
+    t = 40
+    quants_of(c, 0, 0, t)(c.v)[:] = 0x88
+    for j in range(n):  # keys: 0 but for the first element, 1 for token 40
+        quants_of(c, 0, 0, j)(c.k)[:] = 0x88
+        c.scales(c.k, 0, 0, j)[:] = 0.125
+    quants_of(c, 0, 0, t)(c.k)[0, 0] = 0x80  # element 0: -8
+    q = np.zeros((new, 4, dim))
+    q[..., 0] = -far * np.log(2.0)  # score of token 40 (scale 1): far bits
+    q[..., 0] *= 1 + 0.01 * np.arange(4)
+    check_attend(qm, c, [new], 4, F32, scale=1.0, q=q)
+
+
+@pytest.mark.parametrize("big,small", [(4e4, 2e-3), (500.0, 1e-4), (1.0, 1e-6), (60.0, 0.02)])
+@pytest.mark.parametrize("other_block", [True, False], ids=["other block", "same block"])
+@step_and_prompt([1, 3])
+def test_mixed_value_scales(qm, new, other_block, big, small):  # noqa: F811
+    """One token with a large value scale, in one block of its head or in all of them
+    but with values of 0 there, among tokens with small ones."""
+    c = ko.Cache([200], 1, 128, 16, seed=36)
+    s = scales_of(c, c.v)
+    s[:] = (np.sign(s.astype(np.float32)) * small * np.random.default_rng(37).uniform(0.5, 1.5, s.shape)).astype(np.float16)
+    t = 77
+    if other_block:
+        c.scales(c.v, 0, 0, t)[0] = big
+    else:
+        c.scales(c.v, 0, 0, t)[:] = big
+        quants_of(c, 0, 0, t)(c.v)[:] = 0x88
+    check_attend(qm, c, [new], 4, F32)
+
+
+# ---- long sums
+
+@pytest.mark.parametrize("case", [(64, 16384, 8, 1, 128), (16, 24000, 8, 2, 64), (1, 120000, 1, 4, 128)],
+                         ids=["64x16384", "16x24000", "1x120000"])
+def test_long_sums_of_one_sign(qm, case):  # noqa: F811
+    """Queries of 0 make every probability the same, so the output is the mean of the
+    values; all positive, so every rounding that leans one way would show.  Products
+    and sums in f32: 2^-21 for the products and as much for the sums, whose
+    roundings are random (the values are): 2^-20 of the mean."""
+    seqs, n, heads, group, dim = case
+    gen = torch.Generator(device="cuda").manual_seed(38)
+    page, pages = 256, -(-n // 256)
+    shape = (seqs * pages, heads, 16)
+    quants = torch.randint(9, 16, (*shape, 8 * dim, 2), dtype=torch.uint8, device="cuda", generator=gen)
+    d = (0.05 + 0.1 * torch.rand((*shape, dim // 2), device="cuda", generator=gen)).half()
+    pool = torch.cat([quants[..., 0] | (quants[..., 1] << 4), d.view(torch.uint8)], -1).reshape(seqs * pages, heads, -1)
+    del quants
+    table = torch.randperm(seqs * pages, generator=gen, device="cuda").to(torch.int32).reshape(seqs, pages)
+    lengths = torch.full((seqs,), n, dtype=torch.int32, device="cuda")
+    cache = qm.KVCache(pool.clone(), pool, table, lengths, head_dim=dim, page_tokens=page)
+    q = torch.zeros((seqs, heads * group, dim), device="cuda")
+    out, lse = qm.qm_attn_q4_0(cache, q, return_lse=True)
+    assert qm.qm_device_status(clear=True) == qm.QM_OK
+    # (the values read one sequence at a time, in f64)
+    for b in range(0, seqs, max(1, seqs // 4)):
+        one = qm.KVCache(cache.k_pages, cache.v_pages, table[b:b + 1].contiguous(), lengths[b:b + 1].contiguous(),
+                         head_dim=dim, page_tokens=page)
+        _, v = qm.qm_kv_read_q4_0(one, n)
+        want = v.double().mean(0).repeat_interleave(group, 0)
+        off = ((out[b].double() - want).abs() / want).max().item()
+        assert off <= 2.0 ** -20, off * 2 ** 20
+        assert (lse[b].double() - np.log(n)).abs().max().item() <= 2.0 ** -20 * (1 + np.log(n))
+
+
 # ---- a bad row's weights
 
 @pytest.mark.parametrize("dim", [128, 64, 96])
