@@ -7,7 +7,9 @@
 // top of f16's range, a key tile by the power of two that takes its largest
 // scale to 2^11 .. 2^12; both are then f16 pieces.
 // A value tile is scaled likewise, and P takes that on (P = exp2(s + e - maximum of
-// s + e)), so f16's range serves any scale.
+// s + e)).  A value is 15 bits times its tile's power of two and never below 2^-24 of
+// binary16, so two pieces hold every one exactly, unless a tile has scales of 2^12 and
+// more among some below 2^-10: then its rows are done again by the plain kernel.
 //   f32 rows: two pieces each (22 bits of Q and P, K and V exact) and the three
 //     products that are not 2^-22 of the first, smallest first.  P's second
 //     piece is kept 2^11 up, with an accumulator of its own.  Every token tile's
@@ -125,10 +127,10 @@ template <bool F32>
 constexpr float kFarBelow = F32 ? 34.f : 26.f;
 // An element is safe from what is lost if it is this much times the square root
 // of the number of tokens: each one's error is at most 2^-25 in P's last piece
-// times a value of at most 2^6, either sign, to be 2^-18 (2^-11) of the element
+// times a value of at most 2^15, either sign, to be 2^-18 (2^-11) of the element
 // with a margin of 4.
 template <bool F32>
-constexpr float kSafe = F32 ? 0x1p-10f : 0x1p-6f;
+constexpr float kSafe = F32 ? 0x1p-1f : 0x1p3f;
 constexpr float kLowUp = 2048.f;  // f32: what P's second piece is scaled by
 
 // Token tiles that rows at positions pos_lo .. pos_hi read.
@@ -190,12 +192,14 @@ struct RowEnd {
             }
         }
     }
-    __device__ __forceinline__ void finish(float top, float lowest, int n_tiles) {
+    // `coarse`: some tile's values did not fit their pieces.
+    __device__ __forceinline__ void finish(float top, float lowest, int n_tiles, bool coarse) {
         if (!in) return;
         const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum) - kPTop<F32>;
         if (a.lse) a.lse[item] = lse2 * kLn2;
         if (plan.lse2) plan.lse2[item] = lse2;
-        if (lowest < top - kFarBelow<F32> && least < sqrtf(static_cast<float>(n_tiles * kTile)) * kSafe<F32>) {
+        if (coarse ||
+            (lowest < top - kFarBelow<F32> && least < sqrtf(static_cast<float>(n_tiles * kTile)) * kSafe<F32>)) {
             // (Once per row, unless row offsets that go back give a row to two sequences.)
             const unsigned at = atomicAdd(plan.redo_n, 1u);
             if (at < plan.redo_room) plan.redo[at] = static_cast<unsigned>(item);
@@ -220,6 +224,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Bars bar;
     __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t s_coarse;           // a tile's value scales span more than its pieces do
     __shared__ float row_unit[kM * kTile];  // 1 / (power of two that a row of Q was scaled by)
     __shared__ float key_unit[kRing];       // the same of a key tile, tile i in i % kRing
     __shared__ float value_exp[kRing];          // log2 of the same of a value tile
@@ -249,6 +254,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             mbar_init(&bar.pv_done[i], 1);
         }
         mbar_init(&bar.o_free, 4);
+        s_coarse = 0;
         fence_barrier_init();
     }
     grid_dependency_wait();
@@ -531,7 +537,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                 }
                 end.store32(v, q);
             }
-            end.finish(mx_used, lowest, n_tiles);
+            end.finish(mx_used, lowest, n_tiles, s_coarse != 0);
         }
     } else if (warp < kSoftmaxWarps + kDecodeWarps) {
         // ---- decode: cells -> swizzled tiles.  A thread has a token and every other
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
             RowEnd<D, true, T> end(a, plan, first, group, h, rr, rr < n_rows, half_max[n_tiles & 1][0][row]);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) end.store32(o + 32 * x, x);
-            end.finish(row_top[row], half_max[n_tiles & 1][1][row], n_tiles);
+            end.finish(row_top[row], half_max[n_tiles & 1][1][row], n_tiles, s_coarse != 0);
         }
     } else {
         regs_down<S::kOtherRegs>();
@@ -776,7 +782,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < n_tiles && ok; ++i) {
             const int left = seen_len - tiles.at(i) * kTile - 4 * lane;  // of this lane's tokens that count
-            uint32_t top = 0, top_v = 0, bad = 0;
+            uint32_t top = 0, top_v = 0, low_v = 0xFFFFu, bad = 0;  // (low_v: the smallest that is not 0)
 #pragma unroll
             for (int e = 0; e < kWords; ++e) {
                 const int u = e / (NB / 2);
@@ -785,18 +791,22 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
                 if (u < left) {
                     top = max(top, max(a0 < 0x7C00u ? a0 : 0u, a1 < 0x7C00u ? a1 : 0u));
                     top_v = max(top_v, max(v0 < 0x7C00u ? v0 : 0u, v1 < 0x7C00u ? v1 : 0u));
+                    low_v = min(low_v, min(v0 ? v0 : 0xFFFFu, v1 ? v1 : 0xFFFFu));
                     if (v0 >= 0x7C00u || v1 >= 0x7C00u) bad |= 1u << u;
                 }
             }
             fetch(i + 1);
             top = __reduce_max_sync(0xFFFFFFFFu, top);
             top_v = __reduce_max_sync(0xFFFFFFFFu, top_v);
+            low_v = __reduce_min_sync(0xFFFFFFFFu, low_v);
             // The decode warps have begun tile i - 1, so at most kRing tiles are in use.
             if (i > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar.exam_go, (i - 1) & 1, err));
             wild[i % kRing][lane] = static_cast<uint8_t>(bad);
             if (lane == 0) {
                 const int up = 26 - max(1, static_cast<int>(top >> 10));      // largest scale to 2^11 .. 2^12
-                const int up_v = 17 - max(1, static_cast<int>(top_v >> 10));  // to 2^2 .. 2^3
+                const int up_v = 26 - max(1, static_cast<int>(top_v >> 10));
+                // Bits of n d below 2^-24: there are some if a scale's last bit goes below it.
+                if (max(1, static_cast<int>(low_v >> 10)) < 1 - up_v) s_coarse = 1;
                 key_up[i % kRing] = pow2(up);
                 key_unit[i % kRing] = pow2(-up);
                 value_up[i % kRing] = pow2(up_v);

@@ -91,10 +91,11 @@ def test_a_dominant_token_whose_value_is_nothing(qm, new, v_scale, far):  # noqa
     check_attend(qm, c, [new], 4, F32, scale=1.0, q=q)
 
 
-@pytest.mark.parametrize("big,small", [(4e4, 2e-3), (500.0, 1e-4), (1.0, 1e-6), (60.0, 0.02)])
+@pytest.mark.parametrize("big,small", [(4e4, 2e-3), (6e4, 3e-5), (500.0, 1e-4), (1.0, 1e-6), (60.0, 0.02)])
 @pytest.mark.parametrize("other_block", [True, False], ids=["other block", "same block"])
-@step_and_prompt([1, 3])
-def test_mixed_value_scales(qm, new, other_block, big, small):  # noqa: F811
+@step_and_prompt([1, 3, 90])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_mixed_value_scales(qm, dtype, new, other_block, big, small):  # noqa: F811
     """One token with a large value scale, in one block of its head or in all of them
     but with values of 0 there, among tokens with small ones."""
     c = ko.Cache([200], 1, 128, 16, seed=36)
@@ -106,7 +107,7 @@ def test_mixed_value_scales(qm, new, other_block, big, small):  # noqa: F811
     else:
         c.scales(c.v, 0, 0, t)[:] = big
         quants_of(c, 0, 0, t)(c.v)[:] = 0x88
-    check_attend(qm, c, [new], 4, F32)
+    check_attend(qm, c, [new], 4, dtype)
 
 
 # ---- long sums
