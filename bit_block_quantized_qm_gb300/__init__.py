@@ -657,7 +657,8 @@ def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts
     to head_dim ** -0.5; ``window`` > 0 with ``sinks`` limits what a row sees to
     its last ``window`` tokens and the first ``sinks``; ``weights`` f32 ``[n_seqs,
     n_kv_heads, >= max_len]`` is added each token's attention weight; ``max_q``
-    bounds the rows of one sequence (default: all rows).
+    bounds the rows of one sequence (default: all rows, which makes a prompt's call of
+    a batch of single tokens with ``q_starts``: give it there).
 
     ``workspace``: a uint8 tensor of at least ``qm_attn_workspace`` bytes whose first
     ``ATTN_WORKSPACE_ZEROED`` were zeroed once; calls that cannot run at the same time

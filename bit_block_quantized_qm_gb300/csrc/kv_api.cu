@@ -84,6 +84,7 @@ int check_rows(const qm_kv_cache* c, int64_t n_tokens, int64_t max_q, const int3
         max_q = uniform;
     }
     if (max_q > n_tokens) max_q = n_tokens;
+    if (max_q < 1 && n_tokens > 0) max_q = 1;  // (no kernel is made for sequences of no rows at all)
     *rows = {q_starts, static_cast<int>(uniform), static_cast<int>(n_tokens), static_cast<int>(max_q)};
     return QM_OK;
 }

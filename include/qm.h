@@ -449,7 +449,10 @@ QM_API int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t
  *              the query heads that read kv head h.  What qm_kv_evict_q4_0
  *              ranks by.
  *   max_q    : no sequence has more rows than this in the call (ignored
- *              without q_starts).
+ *              without q_starts; 0 counts as 1).  The kernels and their grids
+ *              are chosen by it: where it is far above the rows that there are
+ *              (n_tokens for a batch of single tokens), a call takes a kernel
+ *              for many rows and a grid of mostly idle blocks.
  *   workspace: qm_attn_workspace bytes, 16-byte aligned, its first
  *              QM_ATTN_WORKSPACE_ZEROED bytes zeroed once before its first use;
  *              every call leaves it fit for the next one, of this cache or

@@ -193,3 +193,22 @@ def test_a_workspace_of_the_callers(qm):  # noqa: F811
     got = qm.qm_attn_q4_0(caches[1], q, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(got, want[1][0])
+
+
+# ---- calls that were refused though nothing is wrong with them
+
+@pytest.mark.parametrize("weights", [False, True], ids=["", "weights"])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+def test_rows_that_no_sequence_has_and_a_max_q_of_0(qm, dim, weights):  # noqa: F811
+    """max_q = 0 says that no sequence has rows: nothing is touched, and one that has more
+    than a row all the same is reported."""
+    cache = device(qm, ko.Cache([40, 50], 1, dim, 16, seed=47))
+    q = torch.randn((6, 2, dim), device="cuda")
+    out = torch.full_like(q, 3.0)
+    w = torch.full((2, 1, cache.max_len), 0.5, device="cuda") if weights else None
+    kw = dict(out=out, max_q=0, weights=w)
+    qm.qm_attn_q4_0(cache, q, q_starts=torch.zeros(3, dtype=torch.int32, device="cuda"), **kw)
+    assert qm.qm_device_status(clear=True) == qm.QM_OK
+    assert (out == 3.0).all() and (w is None or (w == 0.5).all())
+    qm.qm_attn_q4_0(cache, q, q_starts=torch.tensor([0, 3, 6], dtype=torch.int32, device="cuda"), **kw)
+    assert qm.qm_device_status(clear=True) == qm.QM_ERR_RANGE
