@@ -267,19 +267,19 @@ int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float
     if (!mul_ok(lists * 4, weights_stride, &wb) || !mul_ok(lists * 4, out_stride, &ob) || !mul_ok(lists * 4, budget, &kb))
         return QM_ERR_SHAPE;
     if (src.n_seqs == 0) return QM_OK;
-    if (!weights || (budget > 0 && (!kept || !weights_out))) return QM_ERR_NULL;
+    if ((src.max_len > 0 && !weights) || (budget > 0 && (!kept || !weights_out))) return QM_ERR_NULL;
     if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(weights_out, 4)) return QM_ERR_ALIGN;
     // In place: the same pages in the same order.  Otherwise the two caches
     // may share pools (on different pages), but then not half a cache.
     const bool in_place = src.k == dst.k && src.v == dst.v && src.table == dst.table;
-    if (in_place && (src.page_shift != dst.page_shift || src.n_pages != dst.n_pages ||
+    if (in_place && src.table && (src.page_shift != dst.page_shift || src.n_pages != dst.n_pages ||
                      src.table_stride != dst.table_stride))
         return QM_ERR_SHAPE;
     if (!in_place && (src.table == dst.table || overlaps(src.k, src_pool, dst.v, dst_pool) ||
                       overlaps(src.v, src_pool, dst.k, dst_pool)))
         return QM_ERR_ALIAS;
     if (weights_out != weights && overlaps(weights, wb, weights_out, ob)) return QM_ERR_ALIAS;
-    if (weights_out == weights && out_stride != weights_stride) return QM_ERR_ALIAS;
+    if (weights && weights_out == weights && out_stride != weights_stride) return QM_ERR_ALIAS;
     if (overlaps(kept, kb, weights, wb) || overlaps(kept, kb, weights_out, ob)) return QM_ERR_ALIAS;
     // Two arrays of lengths that share some entries would change under the kernels that read them.
     if (from->lengths != to->lengths && meets(lengths_of(to), {lengths_of(from)})) return QM_ERR_ALIAS;

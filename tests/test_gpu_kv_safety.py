@@ -212,3 +212,17 @@ def test_rows_that_no_sequence_has_and_a_max_q_of_0(qm, dim, weights):  # noqa: 
     assert (out == 3.0).all() and (w is None or (w == 0.5).all())
     qm.qm_attn_q4_0(cache, q, q_starts=torch.tensor([0, 3, 6], dtype=torch.int32, device="cuda"), **kw)
     assert qm.qm_device_status(clear=True) == qm.QM_ERR_RANGE
+
+
+def test_evicting_caches_that_can_hold_nothing(qm):  # noqa: F811
+    def empty():
+        return qm.KVCache(torch.empty((0, 2, 576), dtype=torch.uint8, device="cuda"),
+                          torch.empty((0, 2, 576), dtype=torch.uint8, device="cuda"),
+                          torch.empty((3, 0), dtype=torch.int32, device="cuda"),
+                          torch.zeros(3, dtype=torch.int32, device="cuda"), head_dim=64, page_tokens=16)
+
+    a, b = empty(), empty()
+    b.lengths += 7
+    kept, w = qm.qm_kv_evict_q4_0(a, b, torch.empty((3, 2, 0), device="cuda"), 5, sinks=1, recent=2)
+    assert (kept == -1).all() and (w == 0).all() and kept.shape == (3, 2, 5)
+    assert b.lengths.tolist() == [0, 0, 0] and qm.qm_device_status(clear=True) == qm.QM_OK

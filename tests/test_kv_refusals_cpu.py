@@ -86,3 +86,13 @@ def test_evict_with_shared_lengths_and_shared_pools_passes(lib):  # noqa: F811
     assert evict(lib, to=cache(page_table=T + 4096, lengths=L + 4096)) in FINE  # the same pools, other pages
     assert evict(lib, to=cache(lengths=L + 4096)) in FINE  # in place, lengths apart
     assert evict(lib, to=cache(lengths=L + 8)) in FINE  # lengths side by side
+
+
+def test_evicting_caches_that_can_hold_nothing_passes(lib):  # noqa: F811
+    """With max_len 0 there are no weights to read, and an empty tensor has no address."""
+    c = dict(max_len=0, k_pages=None, v_pages=None, page_table=None, n_pages=0, table_stride=0)
+    assert evict(lib, cache(**c), to=cache(**{**c, "lengths": L + 4096}), w=None, ws=0, budget=12) in FINE
+    assert evict(lib, cache(**c), to=cache(**{**c, "page_tokens": 64}), w=None, ws=0, budget=12) in FINE
+    assert evict(lib, cache(**c), to=cache(**c), w=None, ws=8, budget=0, sinks=0, recent=0, kept=None, wo=None, os_=0) in FINE
+    assert evict(lib, cache(**c), to=cache(**c), w=None, ws=0, budget=0, sinks=0, recent=0, kept=None, wo=None, os_=0) in FINE
+    assert evict(lib, cache(**c), to=cache(**{**c, "lengths": L + 4096}), w=None, ws=0, budget=12, wo=None) == qm.QM_ERR_NULL
