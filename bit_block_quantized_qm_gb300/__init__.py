@@ -589,7 +589,7 @@ def _rows(t, heads, dim, name):
     if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
         raise ValueError(f"{name} must be [n_tokens, heads, {dim}]")
     stride = t.stride()
-    if stride[2] != 1 or stride[1] != dim:
+    if stride[2] != 1 or (stride[1] != dim and shape[1] != 1 and shape[0] != 0):  # (one head has no stride)
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return code, (stride[0] if shape[0] > 1 else shape[1] * dim)
 

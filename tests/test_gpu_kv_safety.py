@@ -226,3 +226,22 @@ def test_evicting_caches_that_can_hold_nothing(qm):  # noqa: F811
     kept, w = qm.qm_kv_evict_q4_0(a, b, torch.empty((3, 2, 0), device="cuda"), 5, sinks=1, recent=2)
     assert (kept == -1).all() and (w == 0).all() and kept.shape == (3, 2, 5)
     assert b.lengths.tolist() == [0, 0, 0] and qm.qm_device_status(clear=True) == qm.QM_OK
+
+
+def test_one_heads_stride_does_not_count(qm):  # noqa: F811
+    """A single head's rows as a view whose head stride is anything."""
+    c = ko.Cache([60], 1, 64, 16, seed=48)
+    cache = device(qm, c)
+    x = torch.randn((1, 5, 64), device="cuda")
+    view = x.transpose(0, 1)  # [5, 1, 64], head stride 320
+    assert view.stride() == (64, 320, 1)
+    qm.qm_kv_append_q4_0(cache, view, view)
+    k, v = qm.qm_kv_read_q4_0(cache, 5)
+    qm.qm_kv_append_q4_0(cache, view.clone(memory_format=torch.contiguous_format), view.contiguous())
+    again = qm.qm_kv_read_q4_0(cache, 5)
+    assert torch.equal(k, again[0]) and torch.equal(v, again[1])
+    out = torch.empty((1, 5, 64), device="cuda").transpose(0, 1)
+    got = qm.qm_attn_q4_0(cache, view, out=out)
+    assert torch.equal(got, qm.qm_attn_q4_0(cache, x[0].unsqueeze(1).contiguous()))
+    with pytest.raises(ValueError):  # two heads that do not lie together
+        qm.qm_attn_q4_0(cache, torch.randn((2, 5, 64), device="cuda").transpose(0, 1))
