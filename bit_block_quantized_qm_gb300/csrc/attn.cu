@@ -6,8 +6,6 @@
 
 namespace qm {
 
-__device__ unsigned int g_attn_error = 0;
-
 namespace {
 
 constexpr int kWarps = 4;
@@ -44,9 +42,9 @@ __device__ __forceinline__ void attn_plain_row(const KvView& c, const KvRows& r,
     const int b = kv_seq_of_row(r, c.n_seqs, row);
     if (b < 0) return;
     int first, count;
-    kv_rows(r, b, &first, &count, &g_attn_error);
+    kv_rows(r, b, &first, &count, c.err);
     if (row - first >= count) return;
-    const int pos = kv_length(c, b, &g_attn_error) - count + (row - first);
+    const int pos = kv_length(c, b, c.err) - count + (row - first);
     const int h = head / (a.heads / c.heads);
     const T* q = static_cast<const T*>(a.q) + row * a.q_stride + static_cast<int64_t>(head) * c.dim;
     float qv[NB], o[NB];
@@ -67,7 +65,7 @@ __device__ __forceinline__ void attn_plain_row(const KvView& c, const KvRows& r,
         for (int u = 0; u < 4; ++u) {
             const int x = min(x0 + u, n - 1);
             const int j = x < n_first ? x : lo + (x - n_first);
-            const int64_t off = kv_cell(c, b, h, j, &g_attn_error);
+            const int64_t off = kv_cell(c, b, h, j, c.err);
             s[u] = 0.f;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
@@ -169,11 +167,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_weights_plain_kernel(KvView 
     const int lane = threadIdx.x & 31;
     const int j = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int h = blockIdx.y, b = blockIdx.z;
-    const int L = kv_length(c, b, &g_attn_error);
+    const int L = kv_length(c, b, c.err);
     if (j >= L) return;
     int first, count;
-    kv_rows(r, b, &first, &count, &g_attn_error);
-    const int64_t off = kv_cell(c, b, h, j, &g_attn_error);
+    kv_rows(r, b, &first, &count, c.err);
+    const int64_t off = kv_cell(c, b, h, j, c.err);
     if (off < 0) return;
     float k[NB];
 #pragma unroll
@@ -280,18 +278,6 @@ cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cud
         case 7: return launch_plain<7>(c, r, a, stream);
         default: return launch_plain<8>(c, r, a, stream);
     }
-}
-
-cudaError_t attn_read_device_error(unsigned int* bits, bool clear) {
-    unsigned int v = 0;
-    cudaError_t err = cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(v));
-    if (err != cudaSuccess) return err;
-    *bits |= v;
-    if (clear && v) {
-        const unsigned int zero = 0;
-        err = cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero));
-    }
-    return err;
 }
 
 }  // namespace qm

@@ -62,8 +62,6 @@
 
 namespace qm {
 
-__device__ unsigned int g_attn_prompt_error = 0;
-
 namespace {
 
 constexpr int kSoftmaxWarps = 8, kDecodeWarps = 8;
@@ -157,6 +155,7 @@ struct PromptPlan {
     QueryTiles q;        // where the queries' pieces go, if they are wanted
     unsigned* redo_n;    // how many rows are listed to be done again,
     unsigned* redo;      // and which: row * heads + head
+    unsigned int* err;
     unsigned redo_room;  // entries that the list has room for: each row once
 };
 
@@ -203,7 +202,7 @@ struct RowEnd {
             // (Once per row, unless row offsets that go back give a row to two sequences.)
             const unsigned at = atomicAdd(plan.redo_n, 1u);
             if (at < plan.redo_room) plan.redo[at] = static_cast<unsigned>(item);
-            else atomicOr(&g_attn_prompt_error, kErrRange);
+            else atomicOr(plan.err, kErrRange);
         }
     }
 };
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
     uint8_t* q_sm = base;                             // [kM][pieces]
     uint8_t* k_sm = q_sm + kM * S::kOperand;          // [stages][pieces]
     uint8_t* v_sm = k_sm + S::kStagesK * S::kOperandK;  // [stages][pieces]
-    unsigned int* const err = &g_attn_prompt_error;
+    unsigned int* const err = c.err;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
@@ -842,6 +841,7 @@ cudaError_t launch_prompt(const KvView& c, const KvRows& r, const AttnCall& a, f
     p.q = qt;
     p.redo_n = redo_n;
     p.redo = redo;
+    p.err = c.err;
     p.redo_room = static_cast<unsigned>(static_cast<int64_t>(r.n_tokens) * a.heads);
     const int64_t grid = static_cast<int64_t>(p.items_per_list) * c.n_seqs * c.heads;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
@@ -861,18 +861,6 @@ cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall&
                                       : launch_prompt<64, false, __nv_bfloat16>(c, r, a, lse2, qt, redo_n, redo, stream);
     return a.type == KvType::kF32 ? launch_prompt<128, true, float>(c, r, a, lse2, qt, redo_n, redo, stream)
                                   : launch_prompt<128, false, __nv_bfloat16>(c, r, a, lse2, qt, redo_n, redo, stream);
-}
-
-cudaError_t attn_prompt_read_device_error(unsigned int* bits, bool clear) {
-    unsigned int v = 0;
-    cudaError_t err = cudaMemcpyFromSymbol(&v, g_attn_prompt_error, sizeof(v));
-    if (err != cudaSuccess) return err;
-    *bits |= v;
-    if (clear && v) {
-        const unsigned int zero = 0;
-        err = cudaMemcpyToSymbol(g_attn_prompt_error, &zero, sizeof(zero));
-    }
-    return err;
 }
 
 }  // namespace qm

@@ -49,8 +49,6 @@
 
 namespace qm {
 
-__device__ unsigned int g_attn_step_error = 0;
-
 namespace {
 
 constexpr int kWarps = 4;
@@ -235,8 +233,8 @@ struct StepShape {
 // rows (their outputs are written even if they see nothing).
 __device__ __forceinline__ TileList seq_tiles(const KvView& c, const KvRows& r, const AttnCall& a, int b, int* first,
                                               int* count, int* L) {
-    kv_rows(r, b, first, count, &g_attn_step_error);
-    *L = kv_length(c, b, &g_attn_step_error);
+    kv_rows(r, b, first, count, c.err);
+    *L = kv_length(c, b, c.err);
     TileList t{0, 0, 0};
     if (*count > 0) {
         t = tile_list(*L, max(*L - *count, 0), a.window, a.sinks);
@@ -398,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
         if (i >= tile_end) return -1;
         const int p = tiles.at(i) * kTile + (lane & 3) * 16;
         if (p >= seen_len || (whole && (lane & 3))) return -1;
-        return kv_cell(c, b, h, p, &g_attn_step_error);
+        return kv_cell(c, b, h, p, c.err);
     };
     int64_t off4 = look_up(0), off4_next = look_up(1);
     auto issue = [&](int x, int stage) {  // this warp's tile x, looked up
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
         const int stage = n % kStages;
         const uint8_t* kt = my_ring + stage * 2 * S::kHalf;
         uint8_t* vt = my_ring + stage * 2 * S::kHalf + S::kHalf;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bars[warp][stage], (n / kStages) & 1, &g_attn_step_error));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bars[warp][stage], (n / kStages) & 1, c.err));
         if (!ok) break;
         const int key0 = tiles.at(tile_first + x * kWarps) * kTile;
 #pragma unroll
@@ -803,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2)
     }
     if (!ok) {  // a copy that did not land: wait for the other stage's too
         if (x + 1 < my_tiles)
-            mbar_wait_bounded(&bars[warp][(n + 1) % kStages], ((n + 1) / kStages) & 1, &g_attn_step_error);
+            mbar_wait_bounded(&bars[warp][(n + 1) % kStages], ((n + 1) / kStages) & 1, c.err);
     }
 
     // The warps' sums meet in shared memory: [row][D] sums, then maxima, then l.
@@ -939,8 +937,8 @@ __global__ void __launch_bounds__(256) attn_step_weights_kernel(KvView c, KvRows
     const int h = blockIdx.y, b = blockIdx.z;
     const int j = blockIdx.x * 256 + threadIdx.x;
     int first, count;
-    kv_rows(r, b, &first, &count, &g_attn_step_error);
-    const int L = kv_length(c, b, &g_attn_step_error);
+    kv_rows(r, b, &first, &count, c.err);
+    const int L = kv_length(c, b, c.err);
     const int group = a.heads / c.heads;
     const float* lse = reinterpret_cast<const float*>(a.ws + plan.lse_off) + h * group;
     for (int x = threadIdx.x; x < count * group; x += 256) {
@@ -1036,18 +1034,6 @@ cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a
                                       : launch_step<64, __nv_bfloat16>(c, r, a, stream);
     return a.type == KvType::kF32 ? launch_step<128, float>(c, r, a, stream)
                                   : launch_step<128, __nv_bfloat16>(c, r, a, stream);
-}
-
-cudaError_t attn_step_read_device_error(unsigned int* bits, bool clear) {
-    unsigned int v = 0;
-    cudaError_t err = cudaMemcpyFromSymbol(&v, g_attn_step_error, sizeof(v));
-    if (err != cudaSuccess) return err;
-    *bits |= v;
-    if (clear && v) {
-        const unsigned int zero = 0;
-        err = cudaMemcpyToSymbol(g_attn_step_error, &zero, sizeof(zero));
-    }
-    return err;
 }
 
 }  // namespace qm

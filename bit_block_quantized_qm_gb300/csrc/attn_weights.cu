@@ -24,8 +24,6 @@
 
 namespace qm {
 
-__device__ unsigned int g_attn_weights_error = 0;
-
 namespace {
 
 constexpr int kSumWarps = 16;
@@ -57,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* k_sm = base;                 // [2 pieces]
     uint8_t* q_sm = k_sm + 2 * S::kPiece;  // [stages][pieces]
-    unsigned int* const err = &g_attn_weights_error;
+    unsigned int* const err = c.err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
     if (threadIdx.x == 0) {
@@ -293,18 +291,6 @@ cudaError_t launch_attn_weights(const KvView& c, const KvRows& r, const AttnCall
                                       : launch<64, false>(c, r, a, qt, lse2, stream);
     return a.type == KvType::kF32 ? launch<128, true>(c, r, a, qt, lse2, stream)
                                   : launch<128, false>(c, r, a, qt, lse2, stream);
-}
-
-cudaError_t attn_weights_read_device_error(unsigned int* bits, bool clear) {
-    unsigned int v = 0;
-    cudaError_t err = cudaMemcpyFromSymbol(&v, g_attn_weights_error, sizeof(v));
-    if (err != cudaSuccess) return err;
-    *bits |= v;
-    if (clear && v) {
-        const unsigned int zero = 0;
-        err = cudaMemcpyToSymbol(g_attn_weights_error, &zero, sizeof(zero));
-    }
-    return err;
 }
 
 }  // namespace qm

@@ -59,8 +59,14 @@ int check_cache(const qm_kv_cache* c, qm::KvView* view, int64_t* pool_bytes) {
     int shift = 4;
     while ((1 << shift) < c->page_tokens) ++shift;
     *view = {static_cast<uint8_t*>(c->k_pages), static_cast<uint8_t*>(c->v_pages), c->page_table, c->lengths,
-             c->table_stride, c->max_len, static_cast<int>(c->n_pages), c->n_seqs, c->n_kv_heads, c->head_dim, shift};
+             c->table_stride, c->max_len, static_cast<int>(c->n_pages), c->n_seqs, c->n_kv_heads, c->head_dim, shift, nullptr};
     return QM_OK;
+}
+
+// The current device, and what the kernels need to know of it.
+int on_device(qm::DeviceInfo* dev, qm::KvView* view) {
+    if (qm::current_device_info(dev) != cudaSuccess) return QM_ERR_CUDA;
+    return from_cuda(qm::kv_error_word(dev->device, &view->err));
 }
 
 int check_cache_pointers(const qm_kv_cache* c, int device) {
@@ -138,7 +144,7 @@ int qm_kv_append_q4_0(const qm_kv_cache* cache, const void* k, const void* v, in
         if (meets({p, pool}, {{k, kb}, {v, vb}, table_of(cache), lengths_of(cache), starts_of(cache, q_starts)}))
             return QM_ERR_ALIAS;
     qm::DeviceInfo dev;
-    if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
+    if (on_device(&dev, &view) != QM_OK) return QM_ERR_CUDA;
     rc = check_cache_pointers(cache, dev.device);
     if (rc == QM_OK) rc = check_pointer(k, dev.device);
     if (rc == QM_OK) rc = check_pointer(v, dev.device);
@@ -167,7 +173,7 @@ int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t n_toke
                                starts_of(cache, q_starts)}))
             return QM_ERR_ALIAS;
     qm::DeviceInfo dev;
-    if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
+    if (on_device(&dev, &view) != QM_OK) return QM_ERR_CUDA;
     rc = check_cache_pointers(cache, dev.device);
     if (rc == QM_OK) rc = check_pointer(k, dev.device);
     if (rc == QM_OK) rc = check_pointer(v, dev.device);
@@ -232,7 +238,7 @@ int qm_attn_q4_0(const qm_kv_cache* cache, const qm_attn_args* a, void* stream) 
             if (meets(outs[i], {outs[j]})) return QM_ERR_ALIAS;
     }
     qm::DeviceInfo dev;
-    if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
+    if (on_device(&dev, &view) != QM_OK) return QM_ERR_CUDA;
     rc = check_cache_pointers(cache, dev.device);
     const void* more[5] = {a->q, a->out, a->lse, a->weights, a->q_starts};
     for (const void* p : more)
@@ -296,7 +302,7 @@ int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float
     for (const void* p : {dst.k, dst.v})
         if (meets({p, dst_pool}, {table_of(from), table_of(to), lengths_of(from)})) return QM_ERR_ALIAS;
     qm::DeviceInfo dev;
-    if (qm::current_device_info(&dev) != cudaSuccess) return QM_ERR_CUDA;
+    if (on_device(&dev, &src) != QM_OK) return QM_ERR_CUDA;
     rc = check_cache_pointers(from, dev.device);
     if (rc == QM_OK) rc = check_cache_pointers(to, dev.device);
     const void* more[3] = {weights, kept, weights_out};

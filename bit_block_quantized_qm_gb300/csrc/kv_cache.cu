@@ -6,6 +6,8 @@
 
 namespace qm {
 
+// The error word of every kernel of the cache (KvView::err): one word, so that
+// qm_device_status has one more to read, not one for each file.
 __device__ unsigned int g_kv_error = 0;
 
 namespace {
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 6)
     kv_append_kernel(KvView c, KvRows r, const T* k, const T* v, int64_t k_stride, int64_t v_stride, int heads_each) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const RowWork<NB> w(c, r, heads_each, &g_kv_error);
+    const RowWork<NB> w(c, r, heads_each, c.err);
     const T* src = (w.is_v ? v + w.row * v_stride : k + w.row * k_stride) + 32 * w.blk + 8 * w.i;
     uint8_t* pool = w.is_v ? c.v : c.k;
     const int slot = w.pos & 15;
@@ -177,7 +179,7 @@ template <int NB>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(KvView c, KvRows r, float* k, float* v, int heads_each) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const RowWork<NB> w(c, r, heads_each, &g_kv_error);
+    const RowWork<NB> w(c, r, heads_each, c.err);
     if (!w.in) return;
     const uint8_t* pool = w.is_v ? c.v : c.k;
     const int slot = w.pos & 15;
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(KvView c, EvictC
     __shared__ int s_bin, s_need;
     const int h = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x;
-    const int L = kv_length(c, b, &g_kv_error);
+    const int L = kv_length(c, b, c.err);
     const float* w = e.weights + (static_cast<int64_t>(b) * c.heads + h) * e.weights_stride;
     float* wo = e.weights_out + (static_cast<int64_t>(b) * c.heads + h) * e.out_stride;
     int32_t* kept = e.kept + (static_cast<int64_t>(b) * c.heads + h) * e.budget;
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kThreads)
     grid_dependency_wait();
     const int h = blockIdx.y, b = blockIdx.z;
     const int32_t* kept = kept_all + (static_cast<int64_t>(b) * src.heads + h) * budget;
-    const int n_keep = min(kv_length(src, b, &g_kv_error), budget);
+    const int n_keep = min(kv_length(src, b, src.err), budget);
     const int end = in_place ? n_keep : min(n_keep, static_cast<int>(blockIdx.x + 1) * kThreads);
     for (int at0 = in_place ? 0 : blockIdx.x * kThreads; at0 < end; at0 += kThreads) {
         const int at = at0 + threadIdx.x;
@@ -363,9 +365,9 @@ __global__ void __launch_bounds__(kThreads)
         int64_t to = -1;
         if (at < end) {
             const int token = kept[at];
-            if (token < 0) atomicOr(&g_kv_error, kErrRange);  // (a length that changed meanwhile)
-            const int64_t from = token < 0 ? -1 : kv_cell(src, b, h, token, &g_kv_error);
-            to = kv_cell(dst, b, h, at, &g_kv_error);
+            if (token < 0) atomicOr(src.err, kErrRange);  // (a length that changed meanwhile)
+            const int64_t from = token < 0 ? -1 : kv_cell(src, b, h, token, src.err);
+            to = kv_cell(dst, b, h, at, src.err);
             if (from < 0) to = -1;
             if (to >= 0) {
 #pragma unroll
@@ -401,7 +403,7 @@ __global__ void kv_lengths_kernel(KvView src, int32_t* out, int budget) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
-    if (b < src.n_seqs) out[b] = min(kv_length(src, b, &g_kv_error), budget);
+    if (b < src.n_seqs) out[b] = min(kv_length(src, b, src.err), budget);
 }
 
 }  // namespace
@@ -491,6 +493,20 @@ cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCal
     note_launch();
     return launch_pdl(kv_lengths_kernel, dim3((src.n_seqs + 127) / 128), dim3(128), 0, stream, src, e.lengths_out,
                       e.budget);
+}
+
+cudaError_t kv_error_word(int device, unsigned int** word) {
+    static unsigned int* words[64];
+    unsigned int* w = device < 64 ? __atomic_load_n(&words[device], __ATOMIC_ACQUIRE) : nullptr;
+    if (!w) {
+        void* p;
+        const cudaError_t err = cudaGetSymbolAddress(&p, g_kv_error);
+        if (err != cudaSuccess) return err;
+        w = static_cast<unsigned int*>(p);
+        if (device < 64) __atomic_store_n(&words[device], w, __ATOMIC_RELEASE);
+    }
+    *word = w;
+    return cudaSuccess;
 }
 
 cudaError_t kv_read_device_error(unsigned int* bits, bool clear) {

@@ -493,10 +493,6 @@ int qm_device_status(void* stream, int clear) {
     if (qm::gemv_tc_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
     if (qm::gemv_list_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
     if (qm::kv_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
-    if (qm::attn_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
-    if (qm::attn_step_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
-    if (qm::attn_prompt_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
-    if (qm::attn_weights_read_device_error(&bits, clear != 0) != cudaSuccess) return QM_ERR_CUDA;
     if (bits & qm::kErrWaitTimeout) return QM_ERR_TIMEOUT;
     return bits ? QM_ERR_RANGE : QM_OK;
 }

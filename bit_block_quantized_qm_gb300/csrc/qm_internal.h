@@ -7,8 +7,8 @@
 
 namespace qm {
 
-// Device error bits (one word per translation unit that sets them; read back
-// by qm_device_status).
+// Device error bits (one word per translation unit that sets them, one for all of
+// the cache's; read back by qm_device_status).
 constexpr unsigned int kErrWaitTimeout = 1u;  // a bounded wait gave up
 constexpr unsigned int kErrRange = 2u;  // a page, length or row offset that only the device sees is out of range
 
@@ -164,6 +164,7 @@ struct KvView {
     int heads;
     int dim;
     int page_shift;  // log2(page_tokens)
+    unsigned int* err;  // the device's error word
 };
 
 // The rows of a call: sequence b owns rows starts[b] .. starts[b + 1] - 1, or
@@ -224,7 +225,6 @@ bool attn_step_takes(const KvView& c, int heads, int64_t max_q);
 int64_t attn_step_most(const KvView& c, int heads, int64_t max_q);
 int64_t attn_step_workspace(const KvView& c, int heads, int64_t n_tokens, int64_t max_q, bool weights);
 cudaError_t launch_attn_step(const KvView& c, const KvRows& r, const AttnCall& a, cudaStream_t stream);
-cudaError_t attn_step_read_device_error(unsigned int* bits, bool clear);
 
 // Many rows (attn_prompt.cu): head dimensions 64 and 128.  lse2, when not null,
 // gets [n_tokens][heads] logarithms to base 2 of the sums.  redo
@@ -254,8 +254,6 @@ cudaError_t launch_attn_prompt(const KvView& c, const KvRows& r, const AttnCall&
                                unsigned* redo_n, unsigned* redo, cudaStream_t stream);
 cudaError_t launch_attn_weights(const KvView& c, const KvRows& r, const AttnCall& a, const QueryTiles& qt,
                                 const float* lse2, cudaStream_t stream);
-cudaError_t attn_weights_read_device_error(unsigned int* bits, bool clear);
-cudaError_t attn_prompt_read_device_error(unsigned int* bits, bool clear);
 
 // Opts a kernel into `bytes` of dynamic shared memory, once per device: one
 // static object per kernel.
@@ -292,7 +290,8 @@ struct EvictCall {
 };
 cudaError_t launch_kv_evict(const KvView& src, const KvView& dst, const EvictCall& e, cudaStream_t stream);
 cudaError_t kv_read_device_error(unsigned int* bits, bool clear);
-cudaError_t attn_read_device_error(unsigned int* bits, bool clear);
+// The address of the cache kernels' error word on the current device (looked up once).
+cudaError_t kv_error_word(int device, unsigned int** word);
 
 // Count one kernel enqueued by the library.
 void note_launch();

@@ -16,3 +16,14 @@ def test_no_read_only_loads(name):
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()
     assert not re.findall(r"__ldg\b|__restrict__|ld\.global\.nc|ld\.global\.[a-z:0-9_.]*\bnc\b", text)
+
+
+def test_one_error_word_for_all_of_the_caches_kernels():
+    """qm_device_status reads each word by a synchronous copy: what calls it after every
+    step should not pay for a copy per file."""
+    words = []
+    for name in os.listdir(CSRC):
+        if name.startswith(("kv_", "attn")):
+            with open(os.path.join(CSRC, name)) as f:
+                words += re.findall(r"__device__ unsigned int (g_\w+)", f.read())
+    assert words == ["g_kv_error"]
