@@ -229,7 +229,7 @@ cudaError_t launch_plain(const KvView& c, const KvRows& r, const AttnCall& a, cu
         err = launch_attn_prompt(c, r, a, lse, qt, redo_n, redo, stream);
         if (err != cudaSuccess) return err;
         note_launch();
-        err = launch_pdl(attn_redo_kernel<NB, T>, dim3(152), dim3(kRedoWarps * 32), 0, stream, c, r, a, lse, redo_n,
+        err = launch_pdl(attn_redo_kernel<NB, T>, dim3(c.sms), dim3(kRedoWarps * 32), 0, stream, c, r, a, lse, redo_n,
                          static_cast<const unsigned*>(redo));
         if (err != cudaSuccess || !a.weights) return err;
         return launch_attn_weights(c, r, a, qt, lse, stream);

@@ -62,8 +62,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The grid: as many CTAs as the GPU holds at once (three per SM), each with an
-// equal share of all tiles.
-constexpr int kMaxCtas = 152 * kCtasPerSm;
+// equal share of all tiles, but no more than the workspace has room for.
+constexpr int kMaxCtas = 456;
 
 struct StepPlan {
     int groups;   // row groups
@@ -994,7 +994,8 @@ cudaError_t launch_step(const KvView& c, const KvRows& r, const AttnCall& a, con
     const int64_t n_lists = static_cast<int64_t>(c.n_seqs) * c.heads * p.groups;
     // At most this many tiles (a window or shorter sequences make fewer).
     const int64_t tiles = std::max<int64_t>(1, (c.max_len + kTile - 1) / kTile) * n_lists;
-    const int grid = static_cast<int>(std::min<int64_t>(152 * (NT == 1 ? kCtasPerSm : 2), std::max((tiles + kWarps - 1) / kWarps, n_lists)));
+    const int64_t room = std::min(kMaxCtas, c.sms * (NT == 1 ? kCtasPerSm : 2));
+    const int grid = static_cast<int>(std::min(room, std::max((tiles + kWarps - 1) / kWarps, n_lists)));
     err = launch_pdl(attn_step_kernel<D, NT, T>, dim3(grid), dim3(kThreads), S::kSmem, stream, c, r, a, p);
     if (err != cudaSuccess || !a.weights || c.max_len == 0) return err;
     note_launch();

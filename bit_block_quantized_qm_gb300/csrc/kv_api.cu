@@ -59,13 +59,14 @@ int check_cache(const qm_kv_cache* c, qm::KvView* view, int64_t* pool_bytes) {
     int shift = 4;
     while ((1 << shift) < c->page_tokens) ++shift;
     *view = {static_cast<uint8_t*>(c->k_pages), static_cast<uint8_t*>(c->v_pages), c->page_table, c->lengths,
-             c->table_stride, c->max_len, static_cast<int>(c->n_pages), c->n_seqs, c->n_kv_heads, c->head_dim, shift, nullptr};
+             c->table_stride, c->max_len, static_cast<int>(c->n_pages), c->n_seqs, c->n_kv_heads, c->head_dim, shift, nullptr, 0};
     return QM_OK;
 }
 
 // The current device, and what the kernels need to know of it.
 int on_device(qm::DeviceInfo* dev, qm::KvView* view) {
     if (qm::current_device_info(dev) != cudaSuccess) return QM_ERR_CUDA;
+    view->sms = dev->sm_count;
     return from_cuda(qm::kv_error_word(dev->device, &view->err));
 }
 

@@ -206,7 +206,7 @@ template <int NB>
 unsigned row_warps(const KvView& c, const KvRows& r, int* heads_each) {
     const int64_t groups = (static_cast<int64_t>(r.n_tokens) + RowWork<NB>::kTokens - 1) / RowWork<NB>::kTokens;
     int each = 1;
-    while (each < 8 && each < c.heads && groups * 2 * c.heads / (2 * each) >= 152 * 64) each *= 2;
+    while (each < 8 && each < c.heads && groups * 2 * c.heads / (2 * each) >= c.sms * 64) each *= 2;
     *heads_each = each;
     return static_cast<unsigned>(groups * 2 * ((c.heads + each - 1) / each));
 }

@@ -165,6 +165,7 @@ struct KvView {
     int dim;
     int page_shift;  // log2(page_tokens)
     unsigned int* err;  // the device's error word
+    int sms;            // and its SMs
 };
 
 // The rows of a call: sequence b owns rows starts[b] .. starts[b + 1] - 1, or

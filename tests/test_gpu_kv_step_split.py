@@ -37,7 +37,7 @@ def split(lengths, new, kv, group, max_len, window, sinks):
     tiles = [tile_count(n, m, window, sinks) for n, m in zip(lengths, new)]
     n_lists = len(lengths) * lists
     most = max(1, -(-max_len // TILE)) * n_lists
-    grid = min(152 * (3 if rows_cta == 4 else 2), max(-(-most // WARPS), n_lists))
+    grid = min(456, 152 * (3 if rows_cta == 4 else 2), max(-(-most // WARPS), n_lists))
     total = sum(tiles) * lists
     per = max(WARPS, -(-(-(-total // grid)) // WARPS) * WARPS)
     p = per

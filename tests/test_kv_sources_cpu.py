@@ -27,3 +27,10 @@ def test_one_error_word_for_all_of_the_caches_kernels():
             with open(os.path.join(CSRC, name)) as f:
                 words += re.findall(r"__device__ unsigned int (g_\w+)", f.read())
     assert words == ["g_kv_error"]
+
+
+@pytest.mark.parametrize("name", ["kv_cache.cu", "attn.cu", "attn_step.cu", "attn_prompt.cu", "attn_weights.cu"])
+def test_the_number_of_sms_is_asked_for(name):
+    with open(os.path.join(CSRC, name)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.findall(r"\b152\b", code)
