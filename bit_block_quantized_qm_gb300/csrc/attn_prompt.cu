@@ -131,23 +131,6 @@ template <bool F32>
 constexpr float kSafe = F32 ? 0x1p-1f : 0x1p3f;
 constexpr float kLowUp = 2048.f;  // f32: what P's second piece is scaled by
 
-// Token tiles that rows at positions pos_lo .. pos_hi read.
-struct TileList {
-    int n1, t2, count;
-    __device__ __forceinline__ int at(int i) const { return i < n1 ? i : t2 + (i - n1); }
-};
-__device__ __forceinline__ TileList tile_list(int seen_len, int pos_lo, int window, int sinks) {
-    const int total = (seen_len + kTile - 1) / kTile;
-    TileList t{0, 0, total};
-    if (window > 0) {
-        const int lo = max(0, pos_lo - window + 1);
-        t.n1 = min((min(sinks, lo) + kTile - 1) / kTile, total);
-        t.t2 = max(t.n1, lo / kTile);
-        t.count = t.n1 + max(0, total - t.t2);
-    }
-    return t;
-}
-
 struct PromptPlan {
     int items_per_list;  // row tiles (or pairs of them) of a (sequence, kv head) at most
     uint32_t k1024;      // two f16 1024, kept from the compiler (see attn_step.cu)
@@ -274,7 +257,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
     const int pos_lo = base_pos + row0 / group;
     const int pos_hi = base_pos + min(n_rows - 1, row0 + kM * kTile - 1) / group;
     const int seen_len = max(0, min(L, pos_hi + 1));
-    const TileList tiles = tile_list(seen_len, max(pos_lo, 0), a.window, a.sinks);
+    const TileList tiles = tile_list<kTile>(seen_len, max(pos_lo, 0), a.window, a.sinks);
     const int n_tiles = tiles.count;
 
     if (warp == S::kIssuer) {

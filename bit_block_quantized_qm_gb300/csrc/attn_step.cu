@@ -77,26 +77,6 @@ struct StepPlan {
 constexpr int64_t kCtrBytes = kAttnZeroed;
 static_assert(kMaxCtas * 4 <= kCtrBytes - 16, "a counter for each (the last 16 bytes are the prompt kernel's)");
 
-// Tiles that rows at positions pos0 .. L - 1 read: all of 0 .. L - 1, or the
-// first ones' and those from the window's lower end on.
-struct TileList {
-    int n1;     // tiles 0 .. n1 - 1, then
-    int t2;     // tiles t2 ..
-    int count;
-    __device__ __forceinline__ int at(int i) const { return i < n1 ? i : t2 + (i - n1); }
-};
-__device__ __forceinline__ TileList tile_list(int L, int pos0, int window, int sinks) {
-    const int total = (L + kTile - 1) / kTile;
-    TileList t{0, 0, total};
-    if (window > 0) {
-        const int lo = max(0, pos0 - window + 1);
-        t.n1 = min((min(sinks, lo) + kTile - 1) / kTile, total);
-        t.t2 = max(t.n1, lo / kTile);
-        t.count = t.n1 + max(0, total - t.t2);
-    }
-    return t;
-}
-
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t r[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -140,19 +120,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // lo in bit
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 __device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-
-__device__ __forceinline__ float4 load_q4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load_q4(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xFFFF0000u));
-}
-__device__ __forceinline__ void store_o4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store_o4(__nv_bfloat16* p, float4 v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
 // N consecutive 32-bit words, aligned to all of them (N = 1, 2 or 4).
 template <int N>
@@ -200,12 +167,6 @@ __device__ __forceinline__ void pieces_bf16(float lo, float hi, uint32_t w[3]) {
     }
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // o += acc f, two at a time.
 __device__ __forceinline__ void add_to(float o[4], const float acc[4], float f) {
 #pragma unroll
@@ -215,9 +176,6 @@ __device__ __forceinline__ void add_to(float o[4], const float acc[4], float f) 
             : "+f"(o[e]), "+f"(o[e + 1])
             : "f"(acc[e]), "f"(acc[e + 1]), "f"(f));
 }
-
-// 2^e for e in -126 .. 127.
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 template <int D, int NT>
 struct StepShape {
@@ -237,7 +195,7 @@ __device__ __forceinline__ TileList seq_tiles(const KvView& c, const KvRows& r, 
     *L = kv_length(c, b, c.err);
     TileList t{0, 0, 0};
     if (*count > 0) {
-        t = tile_list(*L, max(*L - *count, 0), a.window, a.sinks);
+        t = tile_list<kTile>(*L, max(*L - *count, 0), a.window, a.sinks);
         t.count = max(t.count, 1);
     }
     return t;

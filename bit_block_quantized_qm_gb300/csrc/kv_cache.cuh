@@ -76,4 +76,47 @@ __device__ __forceinline__ int kv_seq_of_row(const KvRows& r, int n_seqs, int ro
     return lo < n_seqs && r.starts[lo] <= row ? lo : -1;
 }
 
+// Tiles of kTokens tokens that rows at positions pos_lo and up read of seen_len
+// tokens: all, or the first ones' and those from the window's lower end on.
+struct TileList {
+    int n1;  // tiles 0 .. n1 - 1, then
+    int t2;  // tiles t2 ..
+    int count;
+    __device__ __forceinline__ int at(int i) const { return i < n1 ? i : t2 + (i - n1); }
+};
+template <int kTokens>
+__device__ __forceinline__ TileList tile_list(int seen_len, int pos_lo, int window, int sinks) {
+    const int total = (seen_len + kTokens - 1) / kTokens;
+    TileList t{0, 0, total};
+    if (window > 0) {
+        const int lo = max(0, pos_lo - window + 1);
+        t.n1 = min((min(sinks, lo) + kTokens - 1) / kTokens, total);
+        t.t2 = max(t.n1, lo / kTokens);
+        t.count = t.n1 + max(0, total - t.t2);
+    }
+    return t;
+}
+
+// Four elements of a row, 16-byte (bf16: 8-byte) aligned.
+__device__ __forceinline__ float4 load_q4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load_q4(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store_o4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store_o4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^e for e in -126 .. 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
 }  // namespace qm
