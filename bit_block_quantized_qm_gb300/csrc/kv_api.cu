@@ -265,7 +265,8 @@ int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float
     if (rc == QM_OK) rc = check_cache(to, &dst, &dst_pool);
     if (rc != QM_OK) return rc;
     if (src.n_seqs != dst.n_seqs || src.heads != dst.heads || src.dim != dst.dim) return QM_ERR_SHAPE;
-    if (budget < 0 || budget > kMaxLen || sinks < 0 || recent < 0 || sinks + recent > budget) return QM_ERR_SHAPE;
+    if (budget < 0 || budget > kMaxLen || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
+        return QM_ERR_SHAPE;
     const int64_t most = budget < src.max_len ? budget : src.max_len;  // tokens a sequence can keep
     if (dst.max_len < most) return QM_ERR_SHAPE;
     if (weights_stride < src.max_len || out_stride < budget) return QM_ERR_SHAPE;

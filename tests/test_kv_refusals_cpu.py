@@ -96,3 +96,10 @@ def test_evicting_caches_that_can_hold_nothing_passes(lib):  # noqa: F811
     assert evict(lib, cache(**c), to=cache(**c), w=None, ws=8, budget=0, sinks=0, recent=0, kept=None, wo=None, os_=0) in FINE
     assert evict(lib, cache(**c), to=cache(**c), w=None, ws=0, budget=0, sinks=0, recent=0, kept=None, wo=None, os_=0) in FINE
     assert evict(lib, cache(**c), to=cache(**{**c, "lengths": L + 4096}), w=None, ws=0, budget=12, wo=None) == qm.QM_ERR_NULL
+
+
+@pytest.mark.parametrize("bad", [dict(sinks=1 << 62, recent=1 << 62), dict(sinks=(1 << 63) - 1, recent=1),
+                                 dict(sinks=1, recent=(1 << 63) - 1), dict(sinks=1 << 32), dict(recent=1 << 32)], ids=str)
+def test_first_and_recent_tokens_that_do_not_add_up(lib, bad):  # noqa: F811
+    """Their sum may pass 2^63."""
+    assert evict(lib, **bad) == qm.QM_ERR_SHAPE
