@@ -211,7 +211,7 @@ int qm_attn_q4_0(const qm_kv_cache* cache, const qm_attn_args* a, void* stream) 
         return QM_ERR_SHAPE;
     if ((rc = attn_sizes(cache, a->n_heads)) != QM_OK) return rc;
     if ((rc = check_rows(cache, a->n_tokens, a->max_q, a->q_starts, &rows)) != QM_OK) return rc;
-    if (a->n_tokens * a->n_heads > 0xFFFFFFFFll) return QM_ERR_SHAPE;  // rows and heads are numbered in 32 bits
+    if (a->n_tokens * a->n_heads > 0x7FFFFFFF) return QM_ERR_SHAPE;  // rows and heads are numbered in an int
     const int64_t row = int64_t(a->n_heads) * view.dim, item = a->dtype == QM_F32 ? 4 : 2;
     int64_t qb, ob, lb, wb = 0;
     if ((rc = span(a->n_tokens, a->q_stride, row, item, &qb)) != QM_OK ||

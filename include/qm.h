@@ -483,7 +483,7 @@ typedef struct qm_attn_args {
     int64_t weights_stride;
     int64_t window; /* 0: none */
     int64_t sinks;
-    int64_t n_heads; /* a multiple of n_kv_heads; n_tokens * n_heads < 2^32 */
+    int64_t n_heads; /* a multiple of n_kv_heads; n_tokens * n_heads < 2^31 */
     float scale;
     int32_t dtype;    /* QM_F32 or QM_BF16 */
     int32_t reserved; /* 0 */
