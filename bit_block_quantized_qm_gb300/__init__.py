@@ -478,8 +478,8 @@ def qm_launch_count() -> int:
 
 
 def qm_device_status(stream=None, clear: bool = True) -> int:
-    """Synchronize the stream and return the device error status (QM_OK or
-    QM_ERR_TIMEOUT); see include/qm.h."""
+    """Synchronize the stream and return the device error status (QM_OK,
+    QM_ERR_TIMEOUT or QM_ERR_RANGE); see include/qm.h."""
     return load_library().qm_device_status(_stream_handle(stream), 1 if clear else 0)
 
 

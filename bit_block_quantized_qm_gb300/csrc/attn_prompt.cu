@@ -24,7 +24,13 @@
 // They can matter only to an output element to which all larger tokens add up
 // to about nothing: rows that have both are listed and done again by the plain
 // kernel.  (bf16 pieces, which have the range, need 4 products for 2^-17, or
-// give 2^-9.)
+// give 2^-9.)  The sign of it that the kernel goes by, an element near 0, is a
+// cautious one, and a row that is done again costs a CTA its whole context: where
+// rows put most of their weight on one token, or values have channels that are
+// always 0, that is most rows and most of the time.  4096 rows, bf16 / f32:
+// scores of deviation 1 0.19 / 0.38 ms, 2 0.54 / 0.38, 3 1.2 / 0.38; deviation 2 and
+// the first token 4 nats above the others 5.0 / 0.38, 8 nats 196 / 0.74, 12 nats 246 /
+// 48; deviation 4 and 16 channels of 0 246 / 233.
 //
 // What bounds it: f32 rows the tensor cores (6 products of 2^21 MACs per pair of
 // tiles at D = 128) behind the roles' waits for one another; bf16 rows (3

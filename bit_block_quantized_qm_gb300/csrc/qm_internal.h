@@ -210,16 +210,16 @@ cudaError_t launch_attn(const KvView& c, const KvRows& r, const AttnCall& a, cud
 // up to 128, but each of its CTAs reads a whole context alone.  So it takes few
 // rows of a list, kStepRows, and up to kStepRowsFew where there are few in all,
 // kStepAll over all sequences and heads.  Both sides, this kernel against the prompt kernel
-// (f32; its bf16 form is 15% faster), 32 heads of 8 kv heads, context 4096:
-//   16 sequences:  16 rows 61 / 93 us, 32 rows 113 / 93, 64 rows 211 / 95
-//   1 sequence:    128 rows (1024 in all) 37 / 93, 256 (2048) 60 / 93,
-//                  512 (4096) 109 / 94
-//   context 1024:  256 rows (2048) 20 / 35, 512 (4096) 47 / 35
+// (f32), 32 heads of 8 kv heads, context 4096:
+//   16 sequences:  16 rows 65 / 94 us, 32 rows 122 / 94, 64 rows 226 / 96
+//   1 sequence:    128 rows (1024 in all) 39 / 94, 256 (2048) 63 / 94,
+//                  512 (4096) 118 / 95
+//   context 1024:  256 rows (2048) 21 / 35, 512 (4096) 48 / 35
 // and with weights, whose kernel goes through a list's rows one by one (the rule
 // does not look at them, so that asking for them changes no output):
-//   1 sequence:    128 rows (1024) 64 / 111 us, 256 (2048) 110 / 117
-//   context 1024:  64 rows (512) 27 / 41, 256 (2048) 60 / 50
-//   2 kv heads of 4: 256 rows (512) 68 / 95, 1024 (2048) 234 / 110
+//   1 sequence:    128 rows (1024) 62 / 108 us, 256 (2048) 105 / 110
+//   context 1024:  64 rows (512) 28 / 39, 256 (2048) 58 / 44
+//   2 kv heads of 4: 256 rows (512) 63 / 102, 1024 (2048) 201 / 111
 constexpr int kStepRows = 24, kStepRowsFew = 256, kStepAll = 2048;
 bool attn_step_takes(const KvView& c, int heads, int64_t max_q);
 // The largest max_q, up to this one, that it takes (0: none).

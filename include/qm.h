@@ -373,7 +373,9 @@ QM_API int qm_gemv_plan(int64_t M, int64_t N, int64_t K, int packed, int sm_coun
  * high nibble).  A page is page_tokens / 16 cells of one kv head in token
  * order; a pool is [n_pages][n_kv_heads] pages, one pool for keys and one for
  * values, same page numbers.  Token t of sequence b lives in page
- * page_table[b * table_stride + t / page_tokens].
+ * page_table[b * table_stride + t / page_tokens].  Sequences may share pages
+ * that a call only reads; one that it writes (qm_kv_append_q4_0, the `to` of
+ * qm_kv_evict_q4_0) has a single place in the table.
  *
  * Rows of a call.  lengths[b] counts the tokens of sequence b including the
  * call's own; the call's rows of sequence b are its last ones, rows
@@ -459,9 +461,10 @@ QM_API int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t
  *              another.  Calls that may run at the same time need a workspace
  *              each, and one that a CUDA graph uses lives as long as the graph.
  * Precision: scores, statistics and sums in f32; products to about 2^-21 of
- * each |q_i k_i| and |p_j v_j| for QM_F32; for QM_BF16, where the output keeps
- * 8 bits, the probabilities and values of its sum may be rounded to 11 bits
- * (lse and weights are those of a QM_F32 call on the same queries).  Tokens that a row does not see do not reach it, whatever their
+ * each |q_i k_i| and |p_j v_j| for QM_F32 (2^-17 of a |p_j v_j| that is 2^-18 of
+ * the largest of the tokens around it, and less); for QM_BF16, where the output
+ * keeps 8 bits, the probabilities and values of its sum may be rounded to 11
+ * bits (lse and weights are those of a QM_F32 call on the same queries).  Tokens that a row does not see do not reach it, whatever their
  * bytes hold.  A token that a row sees and whose scales are not finite makes
  * at least those entries of the row non-finite that the formula does.  The
  * same call on the same inputs gives bitwise the same results (no atomics
