@@ -464,11 +464,12 @@ QM_API int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t
  * each |q_i k_i| and |p_j v_j| for QM_F32 (2^-17 of a |p_j v_j| that is 2^-18 of
  * the largest of the tokens around it, and less); for QM_BF16, where the output
  * keeps 8 bits, the probabilities and values of its sum may be rounded to 11
- * bits (lse and weights are those of a QM_F32 call on the same queries).  Tokens that a row does not see do not reach it, whatever their
- * bytes hold.  A token that a row sees and whose scales are not finite makes
- * at least those entries of the row non-finite that the formula does.  The
- * same call on the same inputs gives bitwise the same results (no atomics
- * on floating values).
+ * bits, probabilities below 2^-24 of the row's largest to 9 (lse and weights are
+ * those of a QM_F32 call on the same queries).  Tokens that a row does not see
+ * do not reach it, whatever their bytes hold.  A token that a row sees and
+ * whose scales are not finite makes at least those entries of the row
+ * non-finite that the formula does.  The same call on the same inputs gives
+ * bitwise the same results (no atomics on floating values).
  * Returns QM_OK or a negative status.
  */
 typedef struct qm_attn_args {
