@@ -266,6 +266,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::kThreads, 1)
     const TileList tiles = tile_list<kTile>(seen_len, max(pos_lo, 0), a.window, a.sinks);
     const int n_tiles = tiles.count;
 
+    // (The GEMM takes its TMEM before it waits for the kernel before it; it cannot
+    // do so beside a CTA of this one, which leaves fewer registers than it needs.)
     if (warp == S::kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot))
                      : "memory");

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t_lo = i_lo * group / kTile, t_hi = ((i_hi + 1) * group - 1) / kTile;
     const int64_t tile0 = query_tile(qt, h, first, b, group);  // of the sequence's rows
 
+    // (As in attn_prompt.cu, no CTA that takes its TMEM early fits beside this one.)
     if (warp == kSumWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_addr(&tmem_slot))
                      : "memory");
