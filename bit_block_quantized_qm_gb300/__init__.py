@@ -18,6 +18,11 @@ Entry points (same names as the C ABI):
 * ``KVCache(k_pages, v_pages, page_table, lengths, ...)``: a paged 4-bit
   key/value cache, with ``qm_kv_append_q4_0``, ``qm_kv_read_q4_0``,
   ``qm_attn_q4_0`` and ``qm_kv_evict_q4_0`` over it
+* ``qm_add_rmsnorm(x, weight, residual=None, ...)``: the norm that adds the
+  residual, with an output in Q8_0 where asked
+* ``qm_route_experts(logits, top_k, ...)`` -> each token's experts and weights
+* ``Experts(w_gate, w_up, w_down, ...)``: a layer's experts, with
+  ``qm_experts_q4_0(experts, x, ids, weights)`` over them
 * ``qm_device_status(stream=None, clear=True)``, ``qm_status_string(code)``,
   ``qm_version()``
 
@@ -48,6 +53,8 @@ __all__ = [
     "QM_ERR_RANGE", "QM_ERR_WORKSPACE", "QM_F32", "QM_BF16", "QmKVCache", "QmAttnArgs", "KVCache", "kv_page_bytes",
     "ATTN_WORKSPACE_ZEROED",
     "qm_kv_append_q4_0", "qm_kv_read_q4_0", "qm_attn_q4_0", "qm_attn_workspace", "qm_kv_evict_q4_0",
+    "QM_SCORE_SOFTMAX", "QM_SCORE_SIGMOID", "QM_ACT_NONE", "QM_ACT_SILU", "QM_ACT_GELU", "QmRmsnormArgs", "QmRouteArgs",
+    "QmExperts", "QmExpertsArgs", "Experts", "qm_add_rmsnorm", "qm_route_experts", "qm_experts_workspace", "qm_experts_q4_0",
 ]
 
 QM_OK = 0
@@ -65,6 +72,13 @@ QM_ERR_WORKSPACE = -11
 
 QM_F32 = 0
 QM_BF16 = 1
+
+QM_SCORE_SOFTMAX = 0
+QM_SCORE_SIGMOID = 1
+
+QM_ACT_NONE = 0
+QM_ACT_SILU = 1
+QM_ACT_GELU = 2
 
 ATTN_WORKSPACE_ZEROED = 4096
 
@@ -85,7 +99,8 @@ EXPORTED_SYMBOLS = ("qm_version", "qm_status_string", "qm_dequant_q4_0", "qm_mat
                     "qm_matmul_q4_0_noalloc", "qm_dequant_q8_0", "qm_quantize_q8_0",
                     "qm_selftest_wait_timeout", "qm_gemv_q4_0_list", "qm_matmul_q4_0_q8act",
                     "qm_gemv_q4_0_q8act_list", "qm_kv_append_q4_0", "qm_kv_read_q4_0", "qm_attn_q4_0",
-                    "qm_attn_workspace", "qm_attn_workspace_exact", "qm_kv_evict_q4_0")
+                    "qm_attn_workspace", "qm_attn_workspace_exact", "qm_kv_evict_q4_0", "qm_add_rmsnorm",
+                    "qm_route_experts", "qm_experts_workspace", "qm_experts_q4_0")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libqm.so")
@@ -120,6 +135,48 @@ class QmAttnArgs(ctypes.Structure):
 
 _ATTN_ARGS = struct.Struct("@6P9qfii4x")  # the same, packed
 assert _ATTN_ARGS.size == ctypes.sizeof(QmAttnArgs)
+
+
+class QmRmsnormArgs(ctypes.Structure):
+    """The C struct qm_rmsnorm_args (see include/qm.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("sum", ctypes.c_void_p), ("q8", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("sum_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class QmRouteArgs(ctypes.Structure):
+    """The C struct qm_route_args (see include/qm.h)."""
+    _fields_ = [("logits", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_int64), ("logits_stride", ctypes.c_int64), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("scoring", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class QmExperts(ctypes.Structure):
+    """The C struct qm_experts (see include/qm.h)."""
+    _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("up_stride", ctypes.c_int64), ("down_stride", ctypes.c_int64),
+                ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64), ("n_experts", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
+
+
+class QmExpertsArgs(ctypes.Structure):
+    """The C struct qm_experts_args (see include/qm.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64), ("n_tokens", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
+
+
+# The structs of the calls, packed (see _ATTN_ARGS).
+_RMSNORM_ARGS = struct.Struct("@6P6qffii")
+_ROUTE_ARGS = struct.Struct("@4P2q7ifii")
+_EXPERTS_ARGS = struct.Struct("@5P4qii8x")
+assert _RMSNORM_ARGS.size == ctypes.sizeof(QmRmsnormArgs) and _ROUTE_ARGS.size == ctypes.sizeof(QmRouteArgs)
+assert _EXPERTS_ARGS.size == ctypes.sizeof(QmExpertsArgs)
 
 
 class QMError(RuntimeError):
@@ -189,6 +246,14 @@ def load_library() -> ctypes.CDLL:
             lib.qm_attn_workspace_exact.restype = i64
             lib.qm_kv_evict_q4_0.argtypes = [p, p, p, i64, i64, i64, i64, p, p, i64, p]
             lib.qm_kv_evict_q4_0.restype = i32
+            lib.qm_add_rmsnorm.argtypes = [p, p]
+            lib.qm_add_rmsnorm.restype = i32
+            lib.qm_route_experts.argtypes = [p, p]
+            lib.qm_route_experts.restype = i32
+            lib.qm_experts_workspace.argtypes = [p, i64, i32]
+            lib.qm_experts_workspace.restype = i64
+            lib.qm_experts_q4_0.argtypes = [p, p, p]
+            lib.qm_experts_q4_0.restype = i32
             lib.qm_launch_count.argtypes = []
             lib.qm_launch_count.restype = ctypes.c_uint64
             _lib = lib
@@ -735,3 +800,199 @@ def qm_kv_evict_q4_0(cache, to, weights, budget: int, sinks: int = 0, recent: in
                                            _stream_handle(stream)),
            "qm_kv_evict_q4_0")
     return kept, weights_out
+
+
+# ------------------------------------------------ a layer's norm, routing and experts
+
+def _matrix(t, name, width=None, like=None):
+    """Check a [rows, width] f32 or bf16 tensor whose rows may be strided; (dtype code, row stride)."""
+    torch = _torch or _torch_module()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.float32:
+        code = QM_F32
+    elif t.dtype == torch.bfloat16:
+        code = QM_BF16
+    else:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    if len(shape) != 2 or (width is not None and shape[1] != width):
+        raise ValueError(f"{name} must be 2-D" + (f" [rows, {width}]" if width is not None else ""))
+    if like is not None and (shape[0] != like.shape[0] or t.dtype != like.dtype):
+        raise ValueError(f"{name} differs in type or number of rows")
+    stride = t.stride()
+    if stride[1] != 1 and shape[1] != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return code, (stride[0] if shape[0] > 1 else shape[1])
+
+
+def qm_add_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, out=None, sum_out=None,
+                   want_q8: bool = False, q8_out=None, want_out: bool = True, stream=None):
+    """Root-mean-square norm of the rows ``x`` (f32 or bf16 ``[rows, width]``,
+    rows may be strided) plus ``residual``: with ``s = x + residual``, ``y = s /
+    sqrt(mean(s^2) + eps) * (weight_offset + weight)``.  Returns ``(out, sum_out,
+    q8)``: y, s (None without a residual, unless ``sum_out`` is given; it may be ``x`` or
+    ``residual``) and, with ``want_q8`` (or ``q8_out``), the Q8_0 blocks of y, uint8
+    ``[rows, width / 32 * 34]``.  ``want_out=False`` leaves y out."""
+    torch = _torch or _torch_module()
+    code, xs = _matrix(x, "x")
+    rows, width = x.shape
+    rs = os_ = ss = width
+    if residual is not None:
+        rs = _matrix(residual, "residual", width, x)[1]
+        if sum_out is None:
+            sum_out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+    if weight is not None:
+        _require(weight, torch.float32, "weight")
+        if weight.numel() != width:
+            raise ValueError("weight must have width elements")
+    if out is not None:
+        os_ = _matrix(out, "out", width, x)[1]
+    elif want_out:
+        out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+    if sum_out is not None:
+        ss = _matrix(sum_out, "sum_out", width, x)[1]
+    if want_q8 or q8_out is not None:
+        if width % BLOCK_ELEMS:
+            raise ValueError("Q8_0 rows need a width that is a multiple of 32")
+        row = width // BLOCK_ELEMS * Q8_0_BLOCK_BYTES
+        if q8_out is None:
+            q8_out = torch.empty((rows, row), dtype=torch.uint8, device=x.device)
+        else:
+            _require(q8_out, torch.uint8, "q8_out")
+            if q8_out.numel() != rows * row:
+                raise ValueError("q8_out must be [rows, width / 32 * 34]")
+    args = _RMSNORM_ARGS.pack(x.data_ptr(), 0 if residual is None else residual.data_ptr(),
+                              0 if weight is None else weight.data_ptr(), 0 if out is None else out.data_ptr(),
+                              0 if sum_out is None else sum_out.data_ptr(), 0 if q8_out is None else q8_out.data_ptr(), rows,
+                              width, xs, rs, os_, ss, eps, weight_offset, code, 0)
+    _check(load_library().qm_add_rmsnorm(args, _stream_handle(stream)), "qm_add_rmsnorm")
+    return out, sum_out, q8_out
+
+
+def qm_route_experts(logits, top_k: int, bias=None, scoring: int = QM_SCORE_SOFTMAX, n_groups: int = 1, top_groups: int = 1,
+                     group_top: int = 2, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """Each token's ``top_k`` experts and their weights, ``(ids, weights)`` int32 and
+    f32 ``[tokens, top_k]``, from ``logits`` f32 or bf16 ``[tokens, experts]`` (rows may be
+    strided); ``bias`` f32 ``[experts]`` counts in the choice alone.  See include/qm.h."""
+    torch = _torch or _torch_module()
+    code, stride = _matrix(logits, "logits")
+    tokens, experts = logits.shape
+    if bias is not None:
+        _require(bias, torch.float32, "bias")
+        if bias.numel() != experts:
+            raise ValueError("bias must have an element for each expert")
+    if ids is None:
+        ids = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
+    for t, dtype, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        _require(t, dtype, name)
+        if tuple(t.shape) != (tokens, top_k):
+            raise ValueError(f"{name} must be [tokens, top_k]")
+    args = _ROUTE_ARGS.pack(logits.data_ptr(), 0 if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                            tokens, stride, experts, top_k, n_groups, top_groups, group_top, scoring, 1 if renormalize else 0,
+                            scale, code, 0)
+    _check(load_library().qm_route_experts(args, _stream_handle(stream)), "qm_route_experts")
+    return ids, weights
+
+
+class Experts:
+    """The experts of a decoder layer over the caller's Q4_0 tensors (see
+    include/qm.h): ``w_gate`` (or None) and ``w_up`` uint8 ``[n_experts, inner, hidden /
+    32 * 18]``, ``w_down`` uint8 ``[n_experts, hidden, inner / 32 * 18]``.  An expert's matrix is
+    contiguous; the experts may be strided, so gate and up may be halves of one
+    tensor.  Keeps the tensors alive, and one workspace for each stream it is
+    used on (see qm_experts_q4_0)."""
+
+    def __init__(self, w_gate, w_up, w_down, activation: int = QM_ACT_SILU):
+        import torch
+        n, inner = w_up.shape[0], w_up.shape[1]
+        hidden = w_up.shape[2] // BLOCK_BYTES * BLOCK_ELEMS
+        row, row_down = hidden // BLOCK_ELEMS * BLOCK_BYTES, inner // BLOCK_ELEMS * BLOCK_BYTES
+        for t, shape, name in ((w_gate, (n, inner, row), "w_gate"), (w_up, (n, inner, row), "w_up"),
+                               (w_down, (n, hidden, row_down), "w_down")):
+            if t is None and name == "w_gate":
+                continue
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+                raise TypeError(f"{name} must be a torch.uint8 tensor")
+            if not t.is_cuda or t.device != w_up.device:
+                raise ValueError(f"{name} must be a CUDA tensor, all of one device")
+            if tuple(t.shape) != shape or inner % BLOCK_ELEMS:
+                raise ValueError(f"{name} must be {shape}, and inner a multiple of 32")
+            if t.stride()[1:] != (shape[2], 1):
+                raise ValueError(f"{name}: an expert's matrix must be contiguous")
+        self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
+        self.n_experts, self.hidden, self.inner, self.activation = n, hidden, inner, activation
+        self.struct = QmExperts(None if w_gate is None else w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+                                0 if w_gate is None else w_gate.stride(0), w_up.stride(0), w_down.stride(0), hidden, inner, n,
+                                activation)
+        self.ref = ctypes.addressof(self.struct)
+        self._workspaces = {}
+        self._sizes = {}
+
+    def _workspace(self, n_tokens: int, top_k: int, stream: int, current: bool):
+        need = self._sizes.get((n_tokens, top_k))
+        if need is None:
+            need = qm_experts_workspace(self, n_tokens, top_k)
+            if len(self._sizes) > 256:
+                self._sizes.clear()
+            self._sizes[n_tokens, top_k] = need
+        torch = _torch or _torch_module()
+        if current:
+            capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            with _on_stream(self.w_up.device, stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+        # (A call that is captured has its own, from the graph's memory: the graph keeps the address.)
+        ws = None if capturing else self._workspaces.get(stream)
+        if ws is None or ws.numel() < need:
+            with _on_stream(self.w_up.device, stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=self.w_up.device)
+            if not capturing:
+                self._workspaces[stream] = ws
+        return ws
+
+
+def qm_experts_workspace(experts, n_tokens: int, top_k: int) -> int:
+    """Bytes of workspace that qm_experts_q4_0 needs for any call of at most these sizes."""
+    n = load_library().qm_experts_workspace(experts.ref, n_tokens, top_k)
+    if n < 0:
+        raise QMError(n, "qm_experts_workspace")
+    return n
+
+
+def qm_experts_q4_0(experts, x, ids, weights, out=None, stream=None, workspace=None):
+    """The experts' feed-forward block of the rows ``x`` (f32 or bf16 ``[tokens,
+    hidden]``, rows may be strided): the sum over a token's experts ``ids`` (int32
+    ``[tokens, top_k]``, negative for none) of their outputs times ``weights`` (f32
+    ``[tokens, top_k]``); what qm_route_experts gives.
+
+    ``workspace``: a uint8 tensor of at least ``qm_experts_workspace`` bytes; calls that
+    cannot run at the same time can share it, those of other layers too.  Without it the
+    experts have their own, one per stream, kept at its largest size; a call that is
+    captured into a CUDA graph gets one from the graph's memory."""
+    torch = _torch or _torch_module()
+    code, xs = _matrix(x, "x", experts.hidden)
+    tokens = x.shape[0]
+    _require(ids, torch.int32, "ids")
+    _require(weights, torch.float32, "weights")
+    if ids.dim() != 2 or ids.shape[0] != tokens or weights.shape != ids.shape:
+        raise ValueError("ids and weights must be [tokens, top_k]")
+    top_k = ids.shape[1]
+    if out is None:
+        out, os_ = torch.empty((tokens, experts.hidden), dtype=x.dtype, device=x.device), experts.hidden
+    else:
+        os_ = _matrix(out, "out", experts.hidden, x)[1]
+    handle = _stream_handle(stream)
+    if workspace is None:
+        ws = experts._workspace(tokens, top_k, handle, stream is None)
+    else:
+        ws = workspace
+        _require(ws, torch.uint8, "workspace")
+    args = _EXPERTS_ARGS.pack(x.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(),
+                              tokens, xs, os_, top_k, code)
+    _check(load_library().qm_experts_q4_0(experts.ref, args, handle), "qm_experts_q4_0")
+    return out

@@ -294,6 +294,57 @@ cudaError_t kv_read_device_error(unsigned int* bits, bool clear);
 // The address of the cache kernels' error word on the current device (looked up once).
 cudaError_t kv_error_word(int device, unsigned int** word);
 
+// ---- a layer's norm, routing and experts (rmsnorm.cu, route.cu, experts*.cu) -
+
+struct NormCall {
+    const void* x;
+    const void* residual;
+    const float* weight;
+    void* out;
+    void* sum;
+    uint8_t* q8;
+    int64_t rows, x_stride, residual_stride, out_stride, sum_stride;
+    int width;
+    float eps, weight_offset;
+    KvType type;
+};
+cudaError_t launch_add_rmsnorm(const NormCall& c, const DeviceInfo& dev, cudaStream_t stream);
+
+struct RouteCall {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int64_t n_tokens, stride;
+    int experts, top_k, groups, top_groups, group_top;
+    bool sigmoid, renormalize;
+    float scale;
+    KvType type;
+};
+cudaError_t launch_route_experts(const RouteCall& c, cudaStream_t stream);
+
+struct ExpertsView {
+    const uint8_t* gate;  // or null
+    const uint8_t* up;
+    const uint8_t* down;
+    int64_t gate_stride, up_stride, down_stride;  // bytes
+    int hidden, inner, n, activation;
+};
+struct ExpertsCall {
+    const void* x;
+    void* out;
+    const int32_t* ids;
+    const float* weights;
+    uint8_t* ws;
+    int64_t x_stride, out_stride;
+    int n_tokens, top_k;
+    KvType type;
+    unsigned int* err;  // the device's error word
+};
+// Bytes of workspace of launch_experts for at most these sizes.
+int64_t experts_workspace(const ExpertsView& e, int64_t n_tokens, int64_t top_k);
+cudaError_t launch_experts(const ExpertsView& e, const ExpertsCall& c, const DeviceInfo& dev, cudaStream_t stream);
+
 // Count one kernel enqueued by the library.
 void note_launch();
 

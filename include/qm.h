@@ -1,7 +1,8 @@
 /*
  * qm.h — C ABI of libqm: the GGML Q4_0 x f32 quantized matmul, the Q4_0
- * dequant, the Q8_0 dequant and quantize, and a 4-bit key/value cache with its
- * attention, as hand-written CUDA kernels for sm_103a (GB300).
+ * dequant, the Q8_0 dequant and quantize, a 4-bit key/value cache with its
+ * attention, and the norm, routing and expert products of a decoder's layer, as
+ * hand-written CUDA kernels for sm_103a (GB300).
  *
  * Operations (defined in "fuel-vulkan-kernels — quantized (GGML) kernel
  * contracts", fuel-dispatch 0.20.71, kernel-contracts/vulkan/quantized.fkc.md):
@@ -42,7 +43,7 @@
  *     stream finishes; it reads and writes memory only after that kernel has
  *     completed, so stream order is kept exactly as for ordinary launches.
  *   - Operands are contiguous; no strides, offsets or broadcasts (but the rows
- *     that the key/value cache's entry points take may be strided).
+ *     that the key/value cache's and the layer's entry points take may be strided).
  *   - Arguments are checked on the host before anything is enqueued; a
  *     failed check returns a negative status and leaves memory untouched.
  *   - An output never aliases an input: overlapping byte ranges are rejected.
@@ -78,11 +79,12 @@ extern "C" {
                                    device                                        */
 #define QM_ERR_TOO_LARGE (-9)   /* beyond the fixed scratch of
                                    qm_matmul_q4_0_noalloc (M > 8)               */
-#define QM_ERR_RANGE (-10)      /* a page number, length or row offset in device
-                                   memory was out of range (see
+#define QM_ERR_RANGE (-10)      /* a page number, length, row offset or expert in
+                                   device memory was out of range (see
                                    qm_device_status)                             */
 #define QM_ERR_WORKSPACE (-11)  /* the workspace is smaller than
-                                   qm_attn_workspace_exact says                  */
+                                   qm_attn_workspace_exact (or
+                                   qm_experts_workspace) says                    */
 
 /* Element types of keys, values, queries and attention outputs. */
 #define QM_F32 0
@@ -532,6 +534,171 @@ QM_API int64_t qm_attn_workspace_exact(const qm_kv_cache* cache, int64_t n_heads
 QM_API int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, const float* weights,
                             int64_t weights_stride, int64_t budget, int64_t sinks, int64_t recent,
                             int32_t* kept, float* weights_out, int64_t out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * What stands between a decoder's attention and its next one: the norm that
+ * adds the residual, the choice of each token's experts, and the experts'
+ * products.  No counterpart on the kernel-contract pages.  Rows may be strided
+ * (strides in elements).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * qm_add_rmsnorm — for every row, in f32:
+ *   s = x + residual (x without one),
+ *   y = s / sqrt(mean(s^2) + eps) * (weight_offset + weight).
+ * Written are, where wanted: s and y, each rounded once to `dtype`, and the Q8_0
+ * blocks of y as qm_quantize_q8_0 makes them of f32 rows (not of rounded ones).
+ *   x, residual, out, sum : [n_rows][width] of `dtype`, aligned to an element.
+ *              residual, out and sum may be NULL; sum may be x or residual
+ *              itself (same stride).
+ *   weight   : [width] f32, or NULL for none (y = s / sqrt(..)).
+ *   q8       : NULL, or n_rows * width / 32 blocks of 34 bytes, 2-byte aligned;
+ *              needs width % 32 == 0.
+ *   width    : 1 .. 2^20.  Rows of 8 elements' multiples, 16-byte aligned, take
+ *              the fast path.
+ * A row whose squares pass f32's range, or that holds infinities or NaN, gives
+ * what f32 arithmetic makes of the formula.  Deterministic.
+ * Returns QM_OK or a negative status.
+ */
+typedef struct qm_rmsnorm_args {
+    const void* x;
+    const void* residual;
+    const float* weight;
+    void* out;
+    void* sum;
+    void* q8;
+    int64_t n_rows;
+    int64_t width;
+    int64_t x_stride;
+    int64_t residual_stride;
+    int64_t out_stride;
+    int64_t sum_stride;
+    float eps;           /* >= 0 */
+    float weight_offset; /* 0, or 1 for weights held as their distance from 1 */
+    int32_t dtype;       /* QM_F32 or QM_BF16 */
+    int32_t reserved;    /* 0 */
+} qm_rmsnorm_args;
+
+QM_API int qm_add_rmsnorm(const qm_rmsnorm_args* args, void* stream);
+
+/*
+ * qm_route_experts — each token's experts and their weights.  Of a token's logits
+ * l: scores s = softmax(l) or 1 / (1 + exp(-l)); choices c = s + bias.  With
+ * n_groups > 1 the experts are in n_groups equal ranges; a group counts as much
+ * as its group_top (1 or 2) largest choices together, and the experts of all
+ * but the top_groups largest groups are out.  ids get the top_k experts of the
+ * largest choices, largest first; weights their scores (without the bias),
+ * divided by their sum with `renormalize` (0 where that is 0), times `scale`.
+ * Equal choices, and equal groups, go to the lower index; without a bias the
+ * experts' order is that of the logits.  Choices that lie so close that f32
+ * could turn them around are compared in f64.
+ *   logits : [n_tokens] rows of n_experts of `dtype`, aligned to an element.
+ *   bias   : [n_experts] f32, or NULL.
+ *   ids, weights : [n_tokens][top_k] int32 and f32, contiguous.
+ *   n_experts 1 .. 1024, a multiple of n_groups; n_groups 1 .. 64; top_k 1 .. 32,
+ *   at most the experts of top_groups groups.
+ * A logit of -infinity has the score 0 (a row of nothing else, weights 0).  NaN
+ * ranks below every number.  With softmax, a row with NaN or +infinity has NaN
+ * weights.  The ids are experts, each at most once, whatever the logits hold.
+ * Deterministic.  Returns QM_OK or a negative status.
+ */
+#define QM_SCORE_SOFTMAX 0
+#define QM_SCORE_SIGMOID 1
+
+typedef struct qm_route_args {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int64_t n_tokens;
+    int64_t logits_stride;
+    int32_t n_experts;
+    int32_t top_k;
+    int32_t n_groups;
+    int32_t top_groups;
+    int32_t group_top;   /* 1 or 2 */
+    int32_t scoring;     /* QM_SCORE_* */
+    int32_t renormalize; /* 0 or 1 */
+    float scale;
+    int32_t dtype;       /* QM_F32 or QM_BF16 */
+    int32_t reserved;    /* 0 */
+} qm_route_args;
+
+QM_API int qm_route_experts(const qm_route_args* args, void* stream);
+
+/*
+ * qm_experts_q4_0 — the feed-forward block of a decoder with experts:
+ *   out[t] = sum_j weights[t][j] * W_down[e] (act(W_gate[e] x[t]) * (W_up[e] x[t])),
+ * e = ids[t][j]; without w_gate, W_down[e] act(W_up[e] x[t]).  One expert with
+ * top_k = 1 and ids of 0 is an ordinary feed-forward block.
+ * The experts (qm_experts): Q4_0 block streams, each 16-byte aligned,
+ *   w_gate, w_up : [n_experts] matrices of `inner` rows of hidden / 32 blocks,
+ *   w_down       : [n_experts] matrices of `hidden` rows of inner / 32 blocks,
+ *   *_stride     : bytes from one expert's matrix to the next (a multiple of 16,
+ *                  so gate and up may be halves of one tensor).
+ * The call:
+ *   x, out    : [n_tokens][hidden] of `dtype`, rows x_stride and out_stride
+ *               elements apart (multiples of 4), 16-byte aligned (8-byte for
+ *               QM_BF16).  out may not be x.
+ *   ids       : [n_tokens][top_k] int32.  A negative id is no expert (a row of
+ *               padding, an expert that is elsewhere): nothing is added, and a
+ *               token without experts gets 0.  The same expert twice counts
+ *               twice.  An id from n_experts up sets the device error word
+ *               (QM_ERR_RANGE from qm_device_status) and counts as none.
+ *   weights   : [n_tokens][top_k] f32.
+ *   workspace : qm_experts_workspace bytes, 16-byte aligned; its contents do not
+ *               matter before or after a call.  Calls that may run at the same
+ *               time need a workspace each, and one that a CUDA graph uses lives
+ *               as long as the graph.
+ * Precision: sums in f32, the inner activations in f32; for QM_F32 products to
+ * about 2^-21 of |x_k w_k|, and 2^-38 of the row's largest |x| times |w_k|; for
+ * QM_BF16 weights rounded to 11 bits, and inner activations to 11 bits (or 2^-38
+ * of the row's largest).  Sums that come out infinite or NaN are taken again,
+ * element by element in f32, from x (the inner activations) and the blocks.
+ * Deterministic: the same call gives bitwise the same result.
+ * Returns QM_OK or a negative status.
+ */
+#define QM_ACT_NONE 0
+#define QM_ACT_SILU 1 /* a / (1 + exp(-a)) */
+#define QM_ACT_GELU 2 /* a / 2 * (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) */
+
+typedef struct qm_experts {
+    const void* w_gate; /* or NULL */
+    const void* w_up;
+    const void* w_down;
+    int64_t gate_stride;
+    int64_t up_stride;
+    int64_t down_stride;
+    int64_t hidden; /* a multiple of 32, 32 .. 65536 */
+    int64_t inner;  /* likewise */
+    int32_t n_experts;  /* 1 .. 1024 */
+    int32_t activation; /* QM_ACT_* */
+    int32_t reserved[2]; /* 0 */
+} qm_experts;
+
+typedef struct qm_experts_args {
+    const void* x;
+    void* out;
+    const int32_t* ids;
+    const float* weights;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t n_tokens;
+    int64_t x_stride;
+    int64_t out_stride;
+    int32_t top_k;    /* 1 .. 1024; n_tokens * top_k < 2^24 */
+    int32_t dtype;    /* QM_F32 or QM_BF16 */
+    int32_t reserved[2]; /* 0 */
+} qm_experts_args;
+
+QM_API int qm_experts_q4_0(const qm_experts* experts, const qm_experts_args* args, void* stream);
+
+/*
+ * qm_experts_workspace — bytes of workspace that qm_experts_q4_0 needs for any
+ * call of at most n_tokens tokens and top_k experts each, of either type.
+ * Host only.  Returns the bytes or a negative status.
+ */
+QM_API int64_t qm_experts_workspace(const qm_experts* experts, int64_t n_tokens, int32_t top_k);
 
 /*
  * qm_launch_count — the number of kernels this library has enqueued in this
