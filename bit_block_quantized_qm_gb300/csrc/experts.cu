@@ -1,18 +1,21 @@
 // The feed-forward block of a decoder with experts (qm_experts_q4_0): the pairs of
 // tokens and experts in the experts' order, the products, and their weighted sum.
-#include <cuda_bf16.h>
-
-#include "qm_device.cuh"
+#include "experts.cuh"
+#include "tcgen05.cuh"
 
 namespace qm {
 
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kCounters = 256;  // of shared tiles, for each of the two products
+static_assert(kCounters >= kExpertCtas, "a counter for every tile left over");
+constexpr int kSetupThreads = 512;
 
 // Where the parts of the workspace are.
 struct Parts {
-    int64_t starts, order, inner, part, bytes;
+    int64_t starts, order, counters, x_pieces, x_unit, inner, i_pieces, i_unit, part, split, bytes;
+    int split_cols;
 };
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 Parts layout(const ExpertsView& e, int64_t n_tokens, int64_t top_k) {
@@ -24,37 +27,45 @@ Parts layout(const ExpertsView& e, int64_t n_tokens, int64_t top_k) {
         at += up256(bytes);
         return a;
     };
+    p.split_cols = static_cast<int>(pairs < kExpertTokens ? (pairs + 15) / 16 * 16 : kExpertTokens);
     p.starts = take((e.n + 1) * 4);
     p.order = take(pairs * 4);
+    p.counters = take(2 * kCounters * 4);
+    p.x_pieces = take(pairs * piece_pitch(e.hidden) * 4);
+    p.x_unit = take(pairs * 4);
     p.inner = take(pairs * e.inner * 4);
+    p.i_pieces = take(pairs * piece_pitch(e.inner) * 4);
+    p.i_unit = take(pairs * 4);
     p.part = take(pairs * e.hidden * 4);
+    p.split = take(int64_t(2 * kExpertCtas) * 256 * p.split_cols * 4);
     p.bytes = at;
     return p;
 }
 
-// The pairs of expert blockIdx.x in ascending order, order[starts[e] ..
-// starts[e + 1]), by one CTA that goes over all ids: it counts those of lower
-// experts too, so that no CTA waits for another.  Every thread has a range of
-// consecutive ids.
-__global__ void __launch_bounds__(1024) experts_order(const int32_t* ids, int pairs, int n, int32_t* starts, int32_t* order,
-                                                      unsigned int* err) {
-    __shared__ int sums[2][32];
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int e = blockIdx.x;
-    const int each = (pairs + blockDim.x - 1) / blockDim.x;
-    const int lo = min(pairs, static_cast<int>(threadIdx.x) * each), hi = min(pairs, lo + each);
-    int below = 0, mine = 0;
-    bool range = false;
-    for (int i = lo; i < hi; ++i) {
+// How many of the pairs 0 .. pairs - 1 have experts below e, and how many of the threads'
+// ranges up to this thread's own have e: every thread goes over a range of consecutive ids.
+struct Ranks {
+    int lo, hi;        // this thread's range
+    int below, mine;   // of all pairs; of its range
+    int before;        // pairs of e in lower threads' ranges
+    bool range;        // an id of its range is no expert's
+};
+__device__ __forceinline__ Ranks rank_pairs(int e, const int32_t* ids, int pairs, int n) {
+    __shared__ int sums[2][kSetupThreads / 32];
+    Ranks r;
+    const int each = (pairs + kSetupThreads - 1) / kSetupThreads;
+    r.lo = min(pairs, static_cast<int>(threadIdx.x) * each), r.hi = min(pairs, r.lo + each);
+    int below = 0;
+    r.mine = 0;
+    r.range = false;
+    for (int i = r.lo; i < r.hi; ++i) {
         const int id = ids[i];
         below += id >= 0 && id < e;
-        mine += id == e;
-        range |= id >= n;
+        r.mine += id == e;
+        r.range |= id >= n;
     }
-    if (range && e == 0) atomicOr(err, kErrRange);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int upto = mine;  // of this warp's lanes up to this one
+    int upto = r.mine;  // of this warp's lanes up to this one
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int v = __shfl_up_sync(kAll, upto, d);
@@ -64,85 +75,135 @@ __global__ void __launch_bounds__(1024) experts_order(const int32_t* ids, int pa
     if (lane == 31) sums[0][warp] = upto;
     if (lane == 0) sums[1][warp] = below;
     __syncthreads();
-    const int before_all = __reduce_add_sync(kAll, sums[1][lane]);
-    const int before = __reduce_add_sync(kAll, lane < warp ? sums[0][lane] : 0);
-    int at = before_all + before + upto - mine;
-    if (mine)
-        for (int i = lo; i < hi; ++i)
+    constexpr int kWarps = kSetupThreads / 32;
+    r.below = __reduce_add_sync(kAll, lane < kWarps ? sums[1][lane] : 0);
+    r.before = __reduce_add_sync(kAll, lane < kWarps && lane < warp ? sums[0][lane] : 0) + upto - r.mine;
+    return r;
+}
+
+// The pairs of expert e in ascending order, order[starts[e] .. starts[e + 1]), by one CTA
+// that goes over all ids: it counts those of lower experts too, so that no CTA waits for
+// another.
+__device__ __forceinline__ void order_pairs(int e, const int32_t* ids, int pairs, int n, int32_t* starts, int32_t* order,
+                                            unsigned int* err) {
+    const Ranks r = rank_pairs(e, ids, pairs, n);
+    if (r.range && e == 0) atomicOr(err, kErrRange);
+    int at = r.below + r.before;
+    if (r.mine)
+        for (int i = r.lo; i < r.hi; ++i)
             if (ids[i] == e) order[at++] = i;
-    if (threadIdx.x == 0) starts[e] = before_all;
-    if (threadIdx.x == blockDim.x - 1 && e == n - 1) starts[n] = before_all + before + upto;
+    if (threadIdx.x == 0) starts[e] = r.below;
+    if (threadIdx.x == kSetupThreads - 1 && e == n - 1) starts[n] = r.below + r.before + r.mine;
 }
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) { return load_q4(p); }
 
-__device__ __forceinline__ float activate(float a, int kind) {
-    if (kind == 1) return a / (1.f + expf(-a));
-    if (kind == 2) return 0.5f * a * (1.f + tanhf(0.7978845608028654f * (a + 0.044715f * a * a * a)));
-    return a;
-}
-
-// A warp's dot product of a row of K / 32 blocks with K values.
-template <typename T>
-__device__ __forceinline__ float row_dot(const uint8_t* blocks, const T* x, int K, int lane) {
-    float s = 0.f;
-    for (int b = 0; b < K / 32; ++b) {
-        const uint8_t* blk = blocks + 18 * b;
-        const float d = f16_bits_to_float(*reinterpret_cast<const uint16_t*>(blk));
-        const uint32_t byte = blk[2 + (lane & 15)];
-        const int q = static_cast<int>(lane < 16 ? byte & 15u : byte >> 4) - 8;
-        s = fmaf(load1(x + 32 * b + lane), static_cast<float>(q) * d, s);
+// A row as f16 pieces, times the power of two that takes its largest value to 2^13 ..
+// 2^14; a thread has 8 elements of a block, those that a word's quants are for, in the
+// order in which they unpack.  The products keep 2^-38 of the largest value.
+template <bool LO, int THREADS, typename T>
+__device__ __forceinline__ void split_row(const T* x, int K, __half* hi, __half* lo, float* unit) {
+    __shared__ float part[THREADS / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto from = [&](int c) { return x + 32 * (c >> 2) + 4 * (c & 3); };
+    const int chunks = K / 8;
+    constexpr int kHeld = 4;  // chunks of a thread that stay in registers
+    float4 a[kHeld], b[kHeld];
+    auto largest = [](float4 v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); };
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int c = threadIdx.x + i * THREADS;
+        a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < chunks) a[i] = load4(from(c)), b[i] = load4(from(c) + 16);
     }
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(kAll, s, d);
-    return s;
-}
-
-__device__ __forceinline__ int expert_of(const int32_t* starts, int n, int p) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (starts[mid + 1] <= p) lo = mid + 1;
-        else hi = mid;
+    for (int i = 0; i < kHeld; ++i) amax = fmaxf(amax, fmaxf(largest(a[i]), largest(b[i])));
+    for (int c = threadIdx.x + kHeld * THREADS; c < chunks; c += THREADS)
+        amax = fmaxf(amax, fmaxf(largest(load4(from(c))), largest(load4(from(c) + 16))));
+    amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
+    if (lane == 0) part[warp] = amax;
+    __syncthreads();
+    amax = __uint_as_float(__reduce_max_sync(kAll, lane < THREADS / 32 ? __float_as_uint(part[lane]) : 0u));
+    const int up = min(126, 13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127));
+    const float f = pow2(up);
+    if (threadIdx.x == 0) *unit = pow2(-up);
+    auto store = [&](int c, float4 a, float4 b) {
+        const float v[8] = {a.x, a.z, a.y, a.w, b.x, b.z, b.y, b.w};
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float v0 = v[2 * e] * f, v1 = v[2 * e + 1] * f;
+            const __half2 x2 = __floats2half2_rn(v0, v1);
+            h[e] = word(x2);
+            const float2 back = __half22float2(x2);
+            if (LO) l[e] = word(__floats2half2_rn(v0 - back.x, v1 - back.y));
+        }
+        *reinterpret_cast<uint4*>(hi + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (LO) *reinterpret_cast<uint4*>(lo + 8 * c) = make_uint4(l[0], l[1], l[2], l[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int c = threadIdx.x + i * THREADS;
+        if (c < chunks) store(c, a[i], b[i]);
     }
-    return lo;
+    for (int c = threadIdx.x + kHeld * THREADS; c < chunks; c += THREADS) store(c, load4(from(c)), load4(from(c) + 16));
 }
 
-// inner[p][i] = act(gate) * up of sorted pair p = blockIdx.y; a warp per i.
+// CTAs 0 .. n - 1: the pairs in the experts' order.  With `rows`, the CTAs after them: a
+// pair's token row each, as pieces at the pair's sorted place, which the CTA counts itself.
 template <typename T>
-__global__ void __launch_bounds__(256) experts_up_rows(const ExpertsView e, const ExpertsCall c, const int32_t* starts,
-                                                       const int32_t* order, float* inner) {
+__global__ void __launch_bounds__(kSetupThreads)
+    experts_setup(const ExpertsCall c, int n, int K, int32_t* starts, int32_t* order, unsigned* counters, __half* hi,
+                  __half* lo, float* unit) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, p = blockIdx.x;
-    if (p >= starts[e.n]) return;
-    const int ex = expert_of(starts, e.n, p);
-    const T* x = static_cast<const T*>(c.x) + static_cast<int64_t>(order[p] / c.top_k) * c.x_stride;
-    const int64_t row_bytes = e.hidden / 32 * 18;
-    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < e.inner; i += gridDim.y * 8) {
-        const float u = row_dot(e.up + ex * e.up_stride + i * row_bytes, x, e.hidden, lane);
-        float h;
-        if (e.gate) h = activate(row_dot(e.gate + ex * e.gate_stride + i * row_bytes, x, e.hidden, lane), e.activation) * u;
-        else h = activate(u, e.activation);
-        if (lane == 0) inner[static_cast<int64_t>(p) * e.inner + i] = h;
+    const int pairs = c.n_tokens * c.top_k;
+    if (static_cast<int>(blockIdx.x) < n) {
+        if (blockIdx.x == 0) counters[threadIdx.x] = 0;
+        static_assert(2 * kCounters == kSetupThreads, "a counter for each thread");
+        order_pairs(blockIdx.x, c.ids, pairs, n, starts, order, c.err);
+        return;
     }
+    const int pair = blockIdx.x - n, e = c.ids[pair];
+    if (e < 0 || e >= n) return;
+    __shared__ int place;
+    const Ranks r = rank_pairs(e, c.ids, pairs, n);
+    if (r.lo <= pair && pair < r.hi) {
+        int p = r.below + r.before;
+        for (int i = r.lo; i < pair; ++i) p += c.ids[i] == e;
+        place = p;
+    }
+    __syncthreads();
+    const int64_t p = place, pitch = piece_pitch(K);
+    const T* x = static_cast<const T*>(c.x) + static_cast<int64_t>(pair / c.top_k) * c.x_stride;
+    split_row<sizeof(T) == 4, kSetupThreads>(x, K, hi + p * pitch, lo + p * pitch, unit + p);
 }
 
-// part[pair][i], the pair's place among all pairs.
-__global__ void __launch_bounds__(256) experts_down_rows(const ExpertsView e, const int32_t* starts, const int32_t* order,
-                                                         const float* inner, float* part) {
+// Rows as pieces, a sorted row each: those of the pairs' tokens (top_k > 0), or the inner
+// activations as they lie.
+template <bool LO, int THREADS, typename T>
+__global__ void __launch_bounds__(THREADS)
+    experts_split(const T* x, int64_t x_stride, int top_k, int K, const int32_t* starts, const int32_t* order, int n, __half* hi,
+                  __half* lo, float* unit) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, p = blockIdx.x;
-    if (p >= starts[e.n]) return;
-    const int ex = expert_of(starts, e.n, p);
-    const int64_t row_bytes = e.inner / 32 * 18;
-    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < e.hidden; i += gridDim.y * 8) {
-        const float y = row_dot(e.down + ex * e.down_stride + i * row_bytes, inner + static_cast<int64_t>(p) * e.inner,
-                                e.inner, lane);
-        if (lane == 0) part[static_cast<int64_t>(order[p]) * e.hidden + i] = y;
-    }
+    const int64_t p = blockIdx.x, pitch = piece_pitch(K);
+    if (p >= starts[n]) return;
+    const int64_t row = top_k > 0 ? order[p] / top_k : p;
+    split_row<LO, THREADS>(x + row * x_stride, K, hi + p * pitch, lo + p * pitch, unit + p);
+}
+// Few rows take many threads each, for the latency; many few.
+template <bool LO, typename T>
+cudaError_t launch_split(const T* x, int64_t x_stride, int top_k, int K, const int32_t* starts, const int32_t* order, int n,
+                         __half* hi, __half* lo, float* unit, int rows, cudaStream_t stream) {
+    note_launch();
+    if (rows <= 512)
+        return launch_pdl(experts_split<LO, 512, T>, dim3(rows), dim3(512), 0, stream, x, x_stride, top_k, K, starts, order, n, hi,
+                          lo, unit);
+    return launch_pdl(experts_split<LO, 128, T>, dim3(rows), dim3(128), 0, stream, x, x_stride, top_k, K, starts, order, n, hi, lo,
+                      unit);
 }
 
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -174,27 +235,45 @@ __global__ void __launch_bounds__(128) experts_combine(const ExpertsCall c, int 
 }
 
 template <typename T>
-cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, cudaStream_t stream) {
+cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const DeviceInfo& dev, cudaStream_t stream) {
+    constexpr bool kLo = sizeof(T) == 4;
     const Parts at = layout(e, c.n_tokens, c.top_k);
     const int pairs = c.n_tokens * c.top_k;
-    int32_t* starts = reinterpret_cast<int32_t*>(c.ws + at.starts);
-    int32_t* order = reinterpret_cast<int32_t*>(c.ws + at.order);
-    float* inner = reinterpret_cast<float*>(c.ws + at.inner);
-    float* part = reinterpret_cast<float*>(c.ws + at.part);
-    cudaError_t err = launch_pdl(experts_order, dim3(e.n), dim3(1024), 0, stream, c.ids, pairs, e.n, starts, order, c.err);
-    if (err == cudaSuccess) {
-        note_launch();
-        err = launch_pdl(experts_up_rows<T>, dim3(pairs, 16), dim3(256), 0, stream, e, c, starts, order, inner);
+    auto words = [&](int64_t offset) { return reinterpret_cast<int32_t*>(c.ws + offset); };
+    auto floats = [&](int64_t offset) { return reinterpret_cast<float*>(c.ws + offset); };
+    auto halves = [&](int64_t offset) { return reinterpret_cast<__half*>(c.ws + offset); };
+    int32_t *starts = words(at.starts), *order = words(at.order);
+    unsigned* counters = reinterpret_cast<unsigned*>(words(at.counters));
+    float *inner = floats(at.inner), *part = floats(at.part);
+    __half *x_hi = halves(at.x_pieces), *x_lo = x_hi + pairs * piece_pitch(e.hidden);
+    __half *i_hi = halves(at.i_pieces), *i_lo = i_hi + pairs * piece_pitch(e.inner);
+
+    // Up to this many pairs a row's CTA counts its own place, which saves a launch; the counting
+    // takes (pairs / 512) ids a thread in every CTA.
+    constexpr int kOwnPlace = 1024;
+    const bool own_place = pairs <= kOwnPlace;
+    cudaError_t err = launch_pdl(experts_setup<T>, dim3(e.n + (own_place ? pairs : 0)), dim3(kSetupThreads), 0, stream, c, e.n,
+                                 e.hidden, starts, order, counters, x_hi, x_lo, floats(at.x_unit));
+    if (err != cudaSuccess) return err;
+    note_launch();
+    if (!own_place) {
+        err = launch_split<kLo>(static_cast<const T*>(c.x), c.x_stride, c.top_k, e.hidden, starts, order, e.n, x_hi, x_lo,
+                                floats(at.x_unit), pairs, stream);
+        if (err != cudaSuccess) return err;
     }
-    if (err == cudaSuccess) {
-        note_launch();
-        err = launch_pdl(experts_down_rows, dim3(pairs, 16), dim3(256), 0, stream, e, starts, order, inner, part);
-    }
-    if (err == cudaSuccess) {
-        note_launch();
-        err = launch_pdl(experts_combine<T>, dim3((e.hidden + 511) / 512, c.n_tokens < 4096 ? c.n_tokens : 4096), dim3(128), 0,
-                         stream, c, e.hidden, e.n, part);
-    }
+    ExpertsMm m = {starts, order, floats(at.x_unit), inner, floats(at.split), counters, c.err, c.x, c.x_stride,
+                   {e.gate ? e.gate : e.up, e.up}, {e.gate ? e.gate_stride : e.up_stride, e.up_stride},
+                   e.n, e.hidden, e.inner, c.top_k, e.activation, at.split_cols, 0x64006400u};
+    if ((err = launch_experts_mm(m, e, false, c.type, x_hi, x_lo, pairs, dev, stream)) != cudaSuccess) return err;
+    err = launch_split<kLo>(static_cast<const float*>(inner), e.inner, 0, e.inner, starts, order, e.n, i_hi, i_lo,
+                            floats(at.i_unit), pairs, stream);
+    if (err != cudaSuccess) return err;
+    m = {starts, order, floats(at.i_unit), part, floats(at.split), counters + kCounters, c.err, inner, e.inner,
+         {e.down, e.down}, {e.down_stride, e.down_stride}, e.n, e.inner, e.hidden, c.top_k, e.activation, at.split_cols,
+         0x64006400u};
+    if ((err = launch_experts_mm(m, e, true, c.type, i_hi, i_lo, pairs, dev, stream)) != cudaSuccess) return err;
+    err = launch_pdl(experts_combine<T>, dim3((e.hidden + 511) / 512, c.n_tokens < 4096 ? c.n_tokens : 4096), dim3(128), 0,
+                     stream, c, e.hidden, e.n, part);
     if (err == cudaSuccess) note_launch();
     return err;
 }
@@ -203,8 +282,8 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, cudaStream_t
 
 int64_t experts_workspace(const ExpertsView& e, int64_t n_tokens, int64_t top_k) { return layout(e, n_tokens, top_k).bytes; }
 
-cudaError_t launch_experts(const ExpertsView& e, const ExpertsCall& c, const DeviceInfo&, cudaStream_t stream) {
-    return c.type == KvType::kF32 ? launch_type<float>(e, c, stream) : launch_type<__nv_bfloat16>(e, c, stream);
+cudaError_t launch_experts(const ExpertsView& e, const ExpertsCall& c, const DeviceInfo& dev, cudaStream_t stream) {
+    return c.type == KvType::kF32 ? launch_type<float>(e, c, dev, stream) : launch_type<__nv_bfloat16>(e, c, dev, stream);
 }
 
 }  // namespace qm
