@@ -49,31 +49,52 @@ constexpr float kWeightUnit = 0x1p-8f;
 
 template <bool F32, bool WIDE>
 struct Cfg {
-    static constexpr int kPieces = F32 ? 2 : 1;
     static constexpr int kTokens = F32 ? kExpertTokens / 2 : kExpertTokens;
-    static constexpr int kTokenTile = kTokens * 128;  // bytes of a piece's 64 elements of all rows
-    static constexpr int kSums = F32 ? 2 : 1;         // sets of sums in TMEM
+    static constexpr int kPanel = kTokens * 128;  // bytes of a piece's 64 elements of all token rows
+    static constexpr int kSums = F32 ? 2 : 1;     // sets of sums in TMEM
+    // A stage of unpacked weights (there are two, each filled by the warps of one phase) and of
+    // token rows: 128 columns of TMEM, two panels.
+    static constexpr int kStageK = F32 ? 64 : 128;
     static constexpr int kPitch = WIDE ? 176 : 144;  // bytes of a raw row in shared memory, an odd number of 16s
     static constexpr int kRawBytes = 2 * kHalf * kPitch;
-    static constexpr int kRawStages = WIDE ? 3 : 4;
-    static constexpr int kTokenBytes = kPieces * kTokenTile;
-    static constexpr int kTokenStages = 4;
-    static constexpr int kAStages = 4 / kPieces;  // of 64 elements, in TMEM
+    static constexpr int kRawStages = F32 && !WIDE ? 4 : 3;
+    static constexpr int kTokenBytes = 2 * kPanel;
+    static constexpr int kTokenStages = F32 ? 4 : WIDE ? 2 : 3;
     static constexpr int kSmem = kRawStages * kRawBytes + kTokenStages * kTokenBytes + 1024;
 };
 
 struct Barriers {
     uint64_t raw_full[4], raw_empty[4];
     uint64_t tok_full[4], tok_empty[4];
-    uint64_t a_full[4], a_empty[4];
+    uint64_t a_full[2], a_empty[2];
     uint64_t acc_full[2], acc_empty[2];
 };
 
+// EXACT: to a few units of f32 (f32 rows); otherwise to about 2^-20.
+template <bool EXACT>
 __device__ __forceinline__ float activate(float a, int kind) {
-    if (kind == 1) return a / (1.f + expf(-a));
-    if (kind == 2) return 0.5f * a * (1.f + tanhf(0.7978845608028654f * (a + 0.044715f * a * a * a)));
-    return a;
+    if (kind == 0) return a;
+    const float z = kind == 1 ? a : 1.5957691216057308f * (a + 0.044715f * a * a * a);  // tanh(y) = 2 sigmoid(2 y) - 1
+    return EXACT ? a / (1.f + expf(-z)) : __fdividef(a, 1.f + __expf(-z));
 }
+
+// A whole warp's bounded waits; the answer is the same for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, unsigned int* err) {
+    for (uint32_t i = 0; i < kMaxWaitPolls; ++i)
+        if (__all_sync(kAll, mbar_try_wait(a, pa))) return true;
+    atomicOr(err, kErrWaitTimeout);
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, unsigned int* err) {
+    for (uint32_t i = 0; i < kMaxWaitPolls; ++i) {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+        if (__all_sync(kAll, x && y)) return true;
+    }
+    atomicOr(err, kErrWaitTimeout);
+    return false;
+}
+// A value that all lanes have, in a uniform register.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
 // The sum of a row of weights with a row of numbers, element by element: for sums that
 // came out infinite or NaN.
@@ -161,13 +182,13 @@ __device__ __forceinline__ void unpack_store(const uint32_t (&w)[9], uint32_t ad
     }
 }
 
-// Words of the 64-element pieces PH and PH + 2 of a unit's row.
-template <int PH, bool WIDE>
+// Words of the 64-element pieces KS0 and KS0 + STEP of a unit's row.
+template <int KS0, int STEP, bool WIDE>
 __device__ __forceinline__ void load_words(const uint8_t* row, int shift, uint32_t (&w)[2][9]) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         constexpr int kStep = 36;
-        const int ks = PH + 2 * j;
+        const int ks = KS0 + STEP * j;
         if constexpr (!WIDE) {
             // Bytes 36 ks .. + 35 lie ks words into the 48 bytes from the 16-byte boundary below.
             uint32_t v[12];
@@ -195,7 +216,7 @@ template <bool F32, bool DOWN, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     experts_mm_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
                       const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo,
-                      const ExpertsMm m, const bool bf16_rows) {
+                      const ExpertsMm m) {
     using C = Cfg<F32, WIDE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* tok = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -203,6 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Barriers bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int tiles_before[1024 + 1];  // token tiles of all lower experts
+    __shared__ int rows_before[1024 + 1];   // their sorted rows
+    __shared__ float units[2][C::kTokens];  // of the columns of this tile and the one before
+    __shared__ int pairs[2][C::kTokens];
     __shared__ int last_of_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* const err = m.err;
@@ -213,10 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.raw_empty[i], kDecodeWarps);
             mbar_init(&bar.tok_full[i], 1);
             mbar_init(&bar.tok_empty[i], 1);
-            mbar_init(&bar.a_full[i], 8);
-            mbar_init(&bar.a_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.a_full[i], 8);
+            mbar_init(&bar.a_empty[i], 1);
             mbar_init(&bar.acc_full[i], 1);
             mbar_init(&bar.acc_empty[i], kDecodeWarps);
         }
@@ -240,17 +264,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         int sum = 0;
         for (int e0 = 0; e0 < m.n; e0 += 32) {
             const int e = e0 + lane;
-            const int count = e < m.n ? m.starts[e + 1] - m.starts[e] : 0;
+            const int end = e < m.n ? m.starts[e + 1] : 0, count = e < m.n ? end - m.starts[e] : 0;
             int v = (count + C::kTokens - 1) / C::kTokens;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(kAll, v, d);
                 if (lane >= d) v += o;
             }
-            if (e < m.n) tiles_before[e + 1] = sum + v;
+            if (e < m.n) tiles_before[e + 1] = sum + v, rows_before[e + 1] = end;
             sum += __shfl_sync(kAll, v, 31);
         }
-        if (lane == 0) tiles_before[0] = 0;
+        if (lane == 0) tiles_before[0] = rows_before[0] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -280,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Place p;
         p.expert = lo;
         p.block = tile - tt * blocks;
-        p.p0 = m.starts[lo] + (tt - tiles_before[lo]) * C::kTokens;
-        p.n = min(C::kTokens, m.starts[lo + 1] - p.p0);
+        p.p0 = rows_before[lo] + (tt - tiles_before[lo]) * C::kTokens;
+        p.n = min(C::kTokens, rows_before[lo + 1] - p.p0);
         return p;
     };
     const int row_bytes = m.K / 32 * 18;
@@ -296,14 +320,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int together = WIDE ? 16 / (row_bytes & -row_bytes) : 1;
         const int shift = WIDE ? (r % together) * row_bytes & 15 : 0;
         const int slot = half * kHalf + (WIDE ? (r % together) * (kHalf / together) + r / together : r);
-        const uint32_t a_cols = tmem + lanes + kTmemA + half * 32 * C::kPieces;
+        const uint32_t a_cols = tmem + lanes + kTmemA + ph * 128 + half * 64;
         bool ok = true;
-        uint32_t it = 0, sums = 0;  // units, sets of sums
-        uint32_t uses[2] = {0, 0};  // of this warp's stages of TMEM
+        uint32_t it = 0, sums = 0, n_items = 0;  // units, sets of sums
+        uint32_t uses = 0;                       // of this phase's stage
         float v0[16], v1[16];  // F32: this thread's sums, columns 16 group .. + 15 of both halves
         // Waits for the set of sums number `sums`.
         auto wait_sums = [&] {
-            if (ok) ok = __all_sync(kAll, mbar_wait_bounded(&bar.acc_full[sums % C::kSums], (sums / C::kSums) & 1, err));
+            ok = ok && warp_wait(&bar.acc_full[sums % C::kSums], (sums / C::kSums) & 1, err);
             tc_fence_after();
         };
         auto free_sums = [&] {
@@ -331,72 +355,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         while (next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
+            const int buf = n_items++ & 1;
+            if (static_cast<int>(threadIdx.x) < C::kTokens) {
+                const int p = pl.p0 + min(static_cast<int>(threadIdx.x), pl.n - 1);
+                units[buf][threadIdx.x] = m.unit[p] * kWeightUnit;
+                if (DOWN) pairs[buf][threadIdx.x] = m.order[p];
+            }
             if constexpr (F32) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.f;
             }
             for (int u = item.u0; u < item.u1; ++u, ++it) {
                 const int stage = it % C::kRawStages;
-                if (ok) ok = __all_sync(kAll, mbar_wait_bounded(&bar.raw_full[stage], (it / C::kRawStages) & 1, err));
+                ok = ok && warp_wait(&bar.raw_full[stage], (it / C::kRawStages) & 1, err);
                 const uint8_t* row = raw + stage * C::kRawBytes + slot * C::kPitch;
                 uint32_t w[2][9];
                 const int left = m.K - 256 * u;
-                if (ph) load_words<1, WIDE>(row, shift, w);
-                else load_words<0, WIDE>(row, shift, w);
+                if (F32 && ph) load_words<1, 2, WIDE>(row, shift, w);
+                else if (F32) load_words<0, 2, WIDE>(row, shift, w);
+                else if (ph) load_words<2, 1, WIDE>(row, shift, w);
+                else load_words<0, 1, WIDE>(row, shift, w);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.raw_empty[stage]);
+                // bf16 rows: 128 elements, a stage; f32 rows: 64 elements twice.
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int ks = ph + 2 * j;
-                    if (64 * ks >= left) continue;
-                    const int a = ks % C::kAStages, c = C::kAStages == 4 ? j : 0;
-                    if (ok && uses[c] > 0)
-                        ok = __all_sync(kAll, mbar_wait_bounded(&bar.a_empty[a], (uses[c] - 1) & 1, err));
-                    ++uses[c];
-                    tc_fence_after();
-                    unpack_store<F32>(w[j], a_cols + a * 64 * C::kPieces, m.k1024);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.a_full[a]);
+                    const int ks = F32 ? ph + 2 * j : 2 * ph + j;
+                    if (F32 ? 64 * ks >= left : 128 * ph >= left) break;
+                    if (F32 || j == 0) {
+                        ok = ok && (uses == 0 || warp_wait(&bar.a_empty[ph], (uses - 1) & 1, err));
+                        ++uses;
+                        tc_fence_after();
+                    }
+                    unpack_store<F32>(w[j], a_cols + (F32 ? 0 : 32 * j), m.k1024);
+                    if (F32 || j == 1) {
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.a_full[ph]);
+                    }
                 }
                 if (F32 && u > item.u0) collect(pl.n);  // of the unit before
             }
             if constexpr (F32) collect(pl.n);
             else wait_sums();
+            named_barrier_sync(2, kDecodeWarps * 32);  // the units and pairs are there
             const bool whole = item.u1 - item.u0 == plan.ku;
             const int f0 = pl.block * block_rows + r, f1 = two ? f0 : f0 + kHalf;
             // Columns 16 ch .. 16 ch + 15 of both halves, as sums of whole rows.
             auto finish = [&](int ch) {
-                const int col = 16 * ch + (lane & 15);
-                const int p = pl.p0 + min(col, pl.n - 1);
-                const int pair = m.order[p];
-                const float unit = m.unit[p] * kWeightUnit;
                 auto again = [&](int which, int f, int c) {
                     const uint8_t* w = m.w[which] + pl.expert * m.w_stride[which] + static_cast<int64_t>(f) * row_bytes;
                     if (DOWN) return exact_dot(w, m.K, static_cast<const float*>(m.x) + (pl.p0 + c) * m.x_stride);
                     const int64_t at = (m.order[pl.p0 + c] / m.top_k) * m.x_stride;
-                    if (bf16_rows) return exact_dot(w, m.K, static_cast<const __nv_bfloat16*>(m.x) + at);
+                    if (!F32) return exact_dot(w, m.K, static_cast<const __nv_bfloat16*>(m.x) + at);
                     return exact_dot(w, m.K, static_cast<const float*>(m.x) + at);
                 };
+                float* out = m.out + static_cast<int64_t>(pl.p0 + 16 * ch) * m.rows + f0;
+                const int f_step = f1 - f0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float s = __shfl_sync(kAll, unit, i);
-                    const int64_t at = DOWN ? __shfl_sync(kAll, pair, i) : pl.p0 + 16 * ch + i;
-                    if (16 * ch + i >= pl.n) break;
+                    const int c = 16 * ch + i;
+                    if (c >= pl.n) break;
+                    const float s = units[buf][c];
                     float a = v0[i] * s, b = v1[i] * s;
-                    if (f0 < m.rows && !isfinite(a)) a = again(0, f0, 16 * ch + i);
-                    if (f1 < m.rows && !isfinite(b)) b = again(1, f1, 16 * ch + i);
-                    float* out = m.out + at * m.rows;
-                    if constexpr (DOWN) {
-                        if (f0 < m.rows) out[f0] = a;
-                        if (f1 < m.rows) out[f1] = b;
-                    } else if (two) {
-                        if (f0 < m.rows) out[f0] = activate(a, m.activation) * b;
-                    } else {
-                        if (f0 < m.rows) out[f0] = activate(a, m.activation);
-                        if (f1 < m.rows) out[f1] = activate(b, m.activation);
+                    if (!(fabsf(a) + fabsf(b) < INFINITY)) {
+                        if (f0 < m.rows && !isfinite(a)) a = again(0, f0, c);
+                        if (f1 < m.rows && !isfinite(b)) b = again(1, f1, c);
                     }
+                    if (DOWN) {
+                        out = m.out + static_cast<int64_t>(pairs[buf][c]) * m.rows + f0;
+                        if (f0 < m.rows) out[0] = a;
+                        if (f1 < m.rows) out[kHalf] = b;
+                    } else if (two) {
+                        if (f0 < m.rows) out[0] = activate<F32>(a, m.activation) * b;
+                    } else {
+                        if (f0 < m.rows) out[0] = activate<F32>(a, m.activation);
+                        if (f1 < m.rows) out[f_step] = activate<F32>(b, m.activation);
+                    }
+                    if (!DOWN) out += m.rows;
                 }
             };
             auto load_sums = [&](int ch) {
@@ -468,8 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Place pl = place(item.tile);
             for (int u = item.u0; u < item.u1 && ok; ++u, ++it) {
                 const int stage = it % C::kRawStages;
-                if (it >= C::kRawStages)
-                    ok = __all_sync(kAll, mbar_wait_bounded(&bar.raw_empty[stage], (it / C::kRawStages - 1) & 1, err));
+                if (it >= C::kRawStages) ok = warp_wait(&bar.raw_empty[stage], (it / C::kRawStages - 1) & 1, err);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[stage], C::kRawBytes);
                 __syncwarp();
@@ -494,17 +530,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Place pl = place(item.tile);
             const int n16 = (pl.n + 15) & ~15;
             const int k_end = min(m.K, 256 * item.u1);
-            for (int k = 256 * item.u0; k < k_end && ok; k += 64, ++kt) {
+            for (int k = 256 * item.u0; k < k_end && ok; k += C::kStageK, ++kt) {
                 const int stage = kt % C::kTokenStages;
-                if (kt >= C::kTokenStages)
-                    ok = __all_sync(kAll, mbar_wait_bounded(&bar.tok_empty[stage], (kt / C::kTokenStages - 1) & 1, err));
+                if (kt >= C::kTokenStages) ok = warp_wait(&bar.tok_empty[stage], (kt / C::kTokenStages - 1) & 1, err);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.tok_full[stage], C::kPieces * n16 * 128);
+                const bool both = F32 || k + 64 < k_end;  // (the last 64 elements of a row may be a stage)
+                if (lane == 0) mbar_arrive_expect_tx(&bar.tok_full[stage], (both ? 2 : 1) * n16 * 128);
                 __syncwarp();
                 uint8_t* dst = tok + stage * C::kTokenBytes;
                 if (16 * lane < n16) {
                     tma_load_2d(dst + lane * 2048, &map_hi, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
-                    if (F32) tma_load_2d(dst + C::kTokenTile + lane * 2048, &map_lo, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
+                    if (F32) tma_load_2d(dst + C::kPanel + lane * 2048, &map_lo, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
+                    else if (both) tma_load_2d(dst + C::kPanel + lane * 2048, &map_hi, k + 64, pl.p0 + 16 * lane, &bar.tok_full[stage]);
                 }
                 __syncwarp();
             }
@@ -515,55 +552,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- products
         const uint32_t lead = elect_one();
         bool ok = true;
-        uint32_t kt = 0, sums = 0;
+        uint32_t sums = 0, stage = 0, round = 0;
         uint32_t a_phase = 0;  // a bit per stage
+        const uint64_t b_first = desc_base(smem_addr(tok), 16);
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
-            const uint32_t id = idesc_f16((pl.n + 15) & ~15, false);
-            const int k_begin = 256 * item.u0, k_end = min(m.K, 256 * item.u1);
+            const uint32_t id = idesc_f16(uniform(pl.n + 15) & ~15, false);
+            const int k_begin = uniform(256 * item.u0), k_end = uniform(min(m.K, 256 * item.u1));
             uint32_t acc = 0, d_set = 0;
-            for (int k = k_begin; k < k_end && ok; k += 64, ++kt) {
+            for (int k = k_begin; k < k_end && ok; k += C::kStageK) {
                 if (k == k_begin || (F32 && k % 256 == 0)) {  // a set of sums: F32 a unit's, else the item's
                     if (sums >= C::kSums)
-                        ok = __all_sync(kAll, mbar_wait_bounded(&bar.acc_empty[sums % C::kSums], (sums / C::kSums - 1) & 1, err));
+                        ok = warp_wait(&bar.acc_empty[sums % C::kSums], (sums / C::kSums - 1) & 1, err);
                     if (!ok) break;
                     d_set = (sums % C::kSums) * 2 * C::kTokens;
                     acc = 0;
                 }
-                const int ks = (k >> 6) & 3, a = ks % C::kAStages, stage = kt % C::kTokenStages;
-                ok = __all_sync(kAll, mbar_wait_bounded(&bar.tok_full[stage], (kt / C::kTokenStages) & 1, err));
-                ok = ok && __all_sync(kAll, mbar_wait_bounded(&bar.a_full[a], (a_phase >> a) & 1, err));
+                const int a = (k / C::kStageK) & 1;
+                ok = warp_wait(&bar.tok_full[stage], round & 1, &bar.a_full[a], (a_phase >> a) & 1, err);
                 if (!ok) break;
                 a_phase ^= 1u << a;
                 tc_fence_after();
-                const uint64_t b_hi = desc_base(smem_addr(tok + stage * C::kTokenBytes), 16);
-                const uint64_t b_lo = desc_base(smem_addr(tok + stage * C::kTokenBytes + C::kTokenTile), 16);
-                const int steps = min(4, (m.K - k) >> 4);
+                const uint64_t b = b_first + stage * (C::kTokenBytes >> 4);
+                const uint32_t d = tmem + d_set, w = tmem + kTmemA + a * 128;
+                const int steps = min(C::kStageK, k_end - k) >> 4;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t d = tmem + d_set + half * C::kTokens;
-                    const uint32_t w_hi = tmem + kTmemA + (a * 2 + half) * 32 * C::kPieces;
-                    for (int s = 0; s < steps; ++s) {
-                        mma_ts(d, w_hi + 8 * s, b_hi + 2 * s, id, s > 0 ? 1 : acc, lead);
+                for (int s = 0; s < C::kStageK / 16; ++s) {
+                    if (s >= steps) break;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t dh = d + half * C::kTokens, wh = w + half * 64 + 8 * s;
+                        const uint64_t bs = b + (F32 ? 2 * s : (s >> 2) * (C::kPanel >> 4) + 2 * (s & 3));
+                        mma_ts(dh, wh, bs, id, s > 0 ? 1 : acc, lead);
                         if (F32) {
-                            mma_ts(d, w_hi + 8 * s, b_lo + 2 * s, id, 1, lead);
-                            mma_ts(d, w_hi + 32 + 8 * s, b_hi + 2 * s, id, 1, lead);
+                            mma_ts(dh, wh, bs + (C::kPanel >> 4), id, 1, lead);
+                            mma_ts(dh, wh + 32, bs, id, 1, lead);
                         }
                     }
                 }
                 acc = 1;
                 mma_commit(&bar.a_empty[a], lead);
                 mma_commit(&bar.tok_empty[stage], lead);
-                if (k + 64 >= k_end || (F32 && k % 256 == 192)) {
+                if (k + C::kStageK >= k_end || (F32 && k % 256 == 192)) {
                     mma_commit(&bar.acc_full[sums % C::kSums], lead);
                     ++sums;
                 }
+                if (++stage == C::kTokenStages) stage = 0, ++round;
             }
         }
         // Products still under way (after a wait that gave up) end before the TMEM is given back.
         if (!ok) {
             mma_commit(&bar.acc_full[sums % C::kSums], lead);
-            mbar_wait_bounded(&bar.acc_full[sums % C::kSums], (sums / C::kSums) & 1, err);
+            warp_wait(&bar.acc_full[sums % C::kSums], (sums / C::kSums) & 1, err);
         }
     }
 
@@ -585,7 +625,7 @@ cudaError_t weight_map(CUtensorMap* map, const uint8_t* w, int64_t stride, int64
 }
 
 template <bool F32, bool DOWN, bool WIDE>
-cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, bool bf16_rows, const void* hi, const void* lo,
+cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, const void* hi, const void* lo,
                           int64_t n_pieces, const DeviceInfo& dev, cudaStream_t stream) {
     using C = Cfg<F32, WIDE>;
     static SmemOnce once;
@@ -604,8 +644,7 @@ cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, bool bf16_ro
         if (err != cudaSuccess) return err;
     }
     const int ctas = dev.sm_count < kExpertCtas ? dev.sm_count : kExpertCtas;
-    err = launch_pdl(experts_mm_kernel<F32, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi, t_lo, m,
-                     bf16_rows);
+    err = launch_pdl(experts_mm_kernel<F32, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi, t_lo, m);
     if (err == cudaSuccess) note_launch();
     return err;
 }
@@ -615,7 +654,7 @@ cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, bool bf16_ro
 cudaError_t launch_experts_mm(const ExpertsMm& m, const ExpertsView& e, bool down, KvType type, const void* hi,
                               const void* lo, int64_t n_pieces, const DeviceInfo& dev, cudaStream_t stream) {
     const bool f32 = type == KvType::kF32, wide = m.K % 256 != 0;
-    auto go = [&](auto kernel) { return kernel(m, e, !f32, hi, f32 ? lo : hi, n_pieces, dev, stream); };
+    auto go = [&](auto kernel) { return kernel(m, e, hi, f32 ? lo : hi, n_pieces, dev, stream); };
     if (f32) {
         if (down) return wide ? go(launch_kernel<true, true, true>) : go(launch_kernel<true, true, false>);
         return wide ? go(launch_kernel<true, false, true>) : go(launch_kernel<true, false, false>);
