@@ -1,5 +1,7 @@
 // The feed-forward block of a decoder with experts (qm_experts_q4_0): the pairs of
 // tokens and experts in the experts' order, the products, and their weighted sum.
+#include <type_traits>
+
 #include "experts.cuh"
 #include "tcgen05.cuh"
 
@@ -14,7 +16,7 @@ constexpr int kSetupThreads = 512;
 
 // Where the parts of the workspace are.
 struct Parts {
-    int64_t starts, order, counters, x_pieces, x_unit, inner, i_pieces, i_unit, part, split, bytes;
+    int64_t starts, order, place, counters, x_pieces, x_unit, inner, i_pieces, i_unit, part, split, bytes;
     int split_cols;
 };
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -30,6 +32,7 @@ Parts layout(const ExpertsView& e, int64_t n_tokens, int64_t top_k) {
     p.split_cols = static_cast<int>(pairs < kExpertTokens ? (pairs + 15) / 16 * 16 : kExpertTokens);
     p.starts = take((e.n + 1) * 4);
     p.order = take(pairs * 4);
+    p.place = take(pairs * 4);
     p.counters = take(2 * kCounters * 4);
     p.x_pieces = take(pairs * piece_pitch(e.hidden) * 4);
     p.x_unit = take(pairs * 4);
@@ -81,19 +84,77 @@ __device__ __forceinline__ Ranks rank_pairs(int e, const int32_t* ids, int pairs
     return r;
 }
 
-// The pairs of expert e in ascending order, order[starts[e] .. starts[e + 1]), by one CTA
-// that goes over all ids: it counts those of lower experts too, so that no CTA waits for
-// another.
+// The pairs of expert e in ascending order, order[starts[e] .. starts[e + 1]), and the place of
+// each of them there (-1 of a pair without an expert), by one CTA that goes over all ids: it
+// counts those of lower experts too, so that no CTA waits for another.
 __device__ __forceinline__ void order_pairs(int e, const int32_t* ids, int pairs, int n, int32_t* starts, int32_t* order,
-                                            unsigned int* err) {
+                                            int32_t* place, unsigned int* err) {
     const Ranks r = rank_pairs(e, ids, pairs, n);
     if (r.range && e == 0) atomicOr(err, kErrRange);
     int at = r.below + r.before;
-    if (r.mine)
-        for (int i = r.lo; i < r.hi; ++i)
-            if (ids[i] == e) order[at++] = i;
+    if (r.mine || e == 0)
+        for (int i = r.lo; i < r.hi; ++i) {
+            const int id = ids[i];
+            if (id == e) {
+                order[at] = i;
+                place[i] = at++;
+            } else if (e == 0 && (id < 0 || id >= n)) {
+                place[i] = -1;
+            }
+        }
     if (threadIdx.x == 0) starts[e] = r.below;
     if (threadIdx.x == kSetupThreads - 1 && e == n - 1) starts[n] = r.below + r.before + r.mine;
+}
+
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// The sum of a row of weights with a row of numbers, element by element: for sums that
+// came out infinite or NaN.
+template <typename T>
+__device__ __noinline__ float exact_dot(const uint8_t* blocks, int K, const T* x) {
+    float s = 0.f;
+    for (int b = 0; b < K / 32; ++b) {
+        const uint8_t* blk = blocks + 18 * b;
+        const float d = f16_bits_to_float(*reinterpret_cast<const uint16_t*>(blk));
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t byte = blk[2 + (j & 15)];
+            const float q = magic_minus8((j < 16 ? byte & 15u : byte >> 4) | kMagicBits);
+            s = fmaf(load1(x + 32 * b + j), q * d, s);
+        }
+    }
+    return s;
+}
+__device__ __forceinline__ bool finite4(float4 v) { return fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f))) == 0.f; }
+
+// The expert of sorted row p.
+__device__ __forceinline__ int expert_of(const int32_t* starts, int n, int p) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid + 1] <= p) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Inner activations of sorted row p that are not finite, four from `at` on: again, from x.
+template <typename T>
+__device__ __forceinline__ float4 inner_again(const ExpertsView& e, const ExpertsCall& c, const int32_t* starts,
+                                           const int32_t* order, int p, int at, float4 v) {
+    const int ex = expert_of(starts, e.n, p);
+    const T* x = static_cast<const T*>(c.x) + static_cast<int64_t>(order[p] / c.top_k) * c.x_stride;
+    const int64_t row_bytes = e.hidden / 32 * 18;
+    float* vs = &v.x;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        if (isfinite(vs[i])) continue;
+        const float u = exact_dot(e.up + ex * e.up_stride + (at + i) * row_bytes, e.hidden, x);
+        if (e.gate)
+            vs[i] = activate<true>(exact_dot(e.gate + ex * e.gate_stride + (at + i) * row_bytes, e.hidden, x), e.activation) * u;
+        else vs[i] = activate<true>(u, e.activation);
+    }
+    return v;
 }
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -102,8 +163,13 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) { return load_q4
 // A row as f16 pieces, times the power of two that takes its largest value to 2^13 ..
 // 2^14; a thread has 8 elements of a block, those that a word's quants are for, in the
 // order in which they unpack.  The products keep 2^-38 of the largest value.
-template <bool LO, int THREADS, typename T>
-__device__ __forceinline__ void split_row(const T* x, int K, __half* hi, __half* lo, float* unit) {
+// With `mend` not null, a row with elements that are not finite is handed to it first.
+struct NoMend {
+    static constexpr bool kThere = false;
+    __device__ __forceinline__ void operator()(int) const {}
+};
+template <bool LO, int THREADS, typename T, typename F>
+__device__ __forceinline__ void split_row(const T* x, int K, __half* hi, __half* lo, float* unit, F&& mend) {
     __shared__ float part[THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto from = [&](int c) { return x + 32 * (c >> 2) + 4 * (c & 3); };
@@ -111,17 +177,32 @@ __device__ __forceinline__ void split_row(const T* x, int K, __half* hi, __half*
     constexpr int kHeld = 4;  // chunks of a thread that stay in registers
     float4 a[kHeld], b[kHeld];
     auto largest = [](float4 v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); };
-    float amax = 0.f;
+    float amax;
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+        amax = 0.f;
+        bool fine = true;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int c = threadIdx.x + i * THREADS;
-        a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < chunks) a[i] = load4(from(c)), b[i] = load4(from(c) + 16);
+        for (int i = 0; i < kHeld; ++i) {
+            const int c = threadIdx.x + i * THREADS;
+            a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < chunks) a[i] = load4(from(c)), b[i] = load4(from(c) + 16);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            amax = fmaxf(amax, fmaxf(largest(a[i]), largest(b[i])));
+            if (std::decay_t<F>::kThere) fine = fine && finite4(a[i]) && finite4(b[i]);
+        }
+        for (int c = threadIdx.x + kHeld * THREADS; c < chunks; c += THREADS) {
+            const float4 u = load4(from(c)), v = load4(from(c) + 16);
+            amax = fmaxf(amax, fmaxf(largest(u), largest(v)));
+            if (std::decay_t<F>::kThere) fine = fine && finite4(u) && finite4(v);
+        }
+        if (!std::decay_t<F>::kThere || round == 1 || !__syncthreads_or(!fine)) break;
+#pragma unroll 1
+        for (int q = threadIdx.x; q < K / 4; q += THREADS) mend(4 * q);
+        __syncthreads();  // (what a thread mends, another may read)
     }
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) amax = fmaxf(amax, fmaxf(largest(a[i]), largest(b[i])));
-    for (int c = threadIdx.x + kHeld * THREADS; c < chunks; c += THREADS)
-        amax = fmaxf(amax, fmaxf(largest(load4(from(c))), largest(load4(from(c) + 16))));
     amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
     if (lane == 0) part[warp] = amax;
     __syncthreads();
@@ -155,55 +236,70 @@ __device__ __forceinline__ void split_row(const T* x, int K, __half* hi, __half*
 // pair's token row each, as pieces at the pair's sorted place, which the CTA counts itself.
 template <typename T>
 __global__ void __launch_bounds__(kSetupThreads)
-    experts_setup(const ExpertsCall c, int n, int K, int32_t* starts, int32_t* order, unsigned* counters, __half* hi,
-                  __half* lo, float* unit) {
+    experts_setup(const ExpertsCall c, int n, int K, int32_t* starts, int32_t* order, int32_t* place,
+                  unsigned* counters, __half* hi, __half* lo, float* unit) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int pairs = c.n_tokens * c.top_k;
     if (static_cast<int>(blockIdx.x) < n) {
         if (blockIdx.x == 0) counters[threadIdx.x] = 0;
         static_assert(2 * kCounters == kSetupThreads, "a counter for each thread");
-        order_pairs(blockIdx.x, c.ids, pairs, n, starts, order, c.err);
+        order_pairs(blockIdx.x, c.ids, pairs, n, starts, order, place, c.err);
         return;
     }
     const int pair = blockIdx.x - n, e = c.ids[pair];
     if (e < 0 || e >= n) return;
-    __shared__ int place;
+    __shared__ int own;
     const Ranks r = rank_pairs(e, c.ids, pairs, n);
     if (r.lo <= pair && pair < r.hi) {
         int p = r.below + r.before;
         for (int i = r.lo; i < pair; ++i) p += c.ids[i] == e;
-        place = p;
+        own = p;
     }
     __syncthreads();
-    const int64_t p = place, pitch = piece_pitch(K);
+    const int64_t p = own, pitch = piece_pitch(K);
     const T* x = static_cast<const T*>(c.x) + static_cast<int64_t>(pair / c.top_k) * c.x_stride;
-    split_row<sizeof(T) == 4, kSetupThreads>(x, K, hi + p * pitch, lo + p * pitch, unit + p);
+    split_row<sizeof(T) == 4, kSetupThreads>(x, K, hi + p * pitch, lo + p * pitch, unit + p, NoMend{});
 }
 
-// Rows as pieces, a sorted row each: those of the pairs' tokens (top_k > 0), or the inner
-// activations as they lie.
-template <bool LO, int THREADS, typename T>
+// The pairs' tokens as pieces, a sorted row each.
+template <int THREADS, typename T>
 __global__ void __launch_bounds__(THREADS)
-    experts_split(const T* x, int64_t x_stride, int top_k, int K, const int32_t* starts, const int32_t* order, int n, __half* hi,
-                  __half* lo, float* unit) {
+    experts_split(const ExpertsCall c, int K, const int32_t* starts, const int32_t* order, int n, __half* hi, __half* lo, float* unit) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t p = blockIdx.x, pitch = piece_pitch(K);
     if (p >= starts[n]) return;
-    const int64_t row = top_k > 0 ? order[p] / top_k : p;
-    split_row<LO, THREADS>(x + row * x_stride, K, hi + p * pitch, lo + p * pitch, unit + p);
+    const T* x = static_cast<const T*>(c.x) + static_cast<int64_t>(order[p] / c.top_k) * c.x_stride;
+    split_row<sizeof(T) == 4, THREADS>(x, K, hi + p * pitch, lo + p * pitch, unit + p, NoMend{});
 }
-// Few rows take many threads each, for the latency; many few.
-template <bool LO, typename T>
-cudaError_t launch_split(const T* x, int64_t x_stride, int top_k, int K, const int32_t* starts, const int32_t* order, int n,
-                         __half* hi, __half* lo, float* unit, int rows, cudaStream_t stream) {
-    note_launch();
-    if (rows <= 512)
-        return launch_pdl(experts_split<LO, 512, T>, dim3(rows), dim3(512), 0, stream, x, x_stride, top_k, K, starts, order, n, hi,
-                          lo, unit);
-    return launch_pdl(experts_split<LO, 128, T>, dim3(rows), dim3(128), 0, stream, x, x_stride, top_k, K, starts, order, n, hi, lo,
-                      unit);
+
+template <typename T>
+struct Mend {
+    static constexpr bool kThere = true;
+    const ExpertsView& e;
+    const ExpertsCall& c;
+    const int32_t *starts, *order;
+    float* row;
+    int p;
+    __device__ __forceinline__ void operator()(int at) const {
+        float4 v = *reinterpret_cast<const float4*>(row + at);
+        if (!finite4(v)) *reinterpret_cast<float4*>(row + at) = inner_again<T>(e, c, starts, order, p, at, v);
+    }
+};
+
+// The inner activations as pieces, those that are not finite taken again first.
+template <int THREADS, typename T>
+__global__ void __launch_bounds__(THREADS)
+    experts_inner(const ExpertsView e, const ExpertsCall c, float* inner, const int32_t* starts, const int32_t* order, __half* hi,
+                  __half* lo, float* unit) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t p = blockIdx.x, pitch = piece_pitch(e.inner);
+    if (p >= starts[e.n]) return;
+    float* row = inner + p * e.inner;
+    const Mend<T> mend{e, c, starts, order, row, static_cast<int>(p)};
+    split_row<sizeof(T) == 4, THREADS>(row, e.inner, hi + p * pitch, lo + p * pitch, unit + p, mend);
 }
 
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -213,21 +309,37 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// Outputs of sorted row p's expert that are not finite, four from `at` on: again, from the inner
+// activations.
+__device__ __forceinline__ float4 down_again(const ExpertsView& e, const int32_t* starts, const float* inner, int p, int at,
+                                          float4 v) {
+    const uint8_t* w = e.down + expert_of(starts, e.n, p) * e.down_stride;
+    float* vs = &v.x;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)
+        if (!isfinite(vs[i]))
+            vs[i] = exact_dot(w + static_cast<int64_t>(at + i) * (e.inner / 32 * 18), e.inner, inner + static_cast<int64_t>(p) * e.inner);
+    return v;
+}
+
 // out[t] = the weighted sum of the token's pairs, in their order.
 template <typename T>
-__global__ void __launch_bounds__(128) experts_combine(const ExpertsCall c, int hidden, int n, const float* part) {
+__global__ void __launch_bounds__(128)
+    experts_combine(const ExpertsView e, const ExpertsCall c, const int32_t* starts, const int32_t* place, const float* inner,
+                    const float* part) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int at = (blockIdx.x * 128 + threadIdx.x) * 4;
-    if (at >= hidden) return;
+    if (at >= e.hidden) return;
     for (int t = blockIdx.y; t < c.n_tokens; t += gridDim.y) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j = 0; j < c.top_k; ++j) {
             const int64_t pair = static_cast<int64_t>(t) * c.top_k + j;
-            const int id = c.ids[pair];
-            if (id < 0 || id >= n) continue;
+            const int p = place[pair];
+            if (p < 0) continue;
             const float w = c.weights[pair];
-            const float4 y = *reinterpret_cast<const float4*>(part + pair * hidden + at);
+            float4 y = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * e.hidden + at);
+            if (!finite4(y)) y = down_again(e, starts, inner, p, at, y);
             s.x = fmaf(w, y.x, s.x), s.y = fmaf(w, y.y, s.y), s.z = fmaf(w, y.z, s.z), s.w = fmaf(w, y.w, s.w);
         }
         store4(static_cast<T*>(c.out) + t * c.out_stride + at, s);
@@ -236,13 +348,12 @@ __global__ void __launch_bounds__(128) experts_combine(const ExpertsCall c, int 
 
 template <typename T>
 cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const DeviceInfo& dev, cudaStream_t stream) {
-    constexpr bool kLo = sizeof(T) == 4;
     const Parts at = layout(e, c.n_tokens, c.top_k);
     const int pairs = c.n_tokens * c.top_k;
     auto words = [&](int64_t offset) { return reinterpret_cast<int32_t*>(c.ws + offset); };
     auto floats = [&](int64_t offset) { return reinterpret_cast<float*>(c.ws + offset); };
     auto halves = [&](int64_t offset) { return reinterpret_cast<__half*>(c.ws + offset); };
-    int32_t *starts = words(at.starts), *order = words(at.order);
+    int32_t *starts = words(at.starts), *order = words(at.order), *place = words(at.place);
     unsigned* counters = reinterpret_cast<unsigned*>(words(at.counters));
     float *inner = floats(at.inner), *part = floats(at.part);
     __half *x_hi = halves(at.x_pieces), *x_lo = x_hi + pairs * piece_pitch(e.hidden);
@@ -253,27 +364,34 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
     constexpr int kOwnPlace = 1024;
     const bool own_place = pairs <= kOwnPlace;
     cudaError_t err = launch_pdl(experts_setup<T>, dim3(e.n + (own_place ? pairs : 0)), dim3(kSetupThreads), 0, stream, c, e.n,
-                                 e.hidden, starts, order, counters, x_hi, x_lo, floats(at.x_unit));
+                                 e.hidden, starts, order, place, counters, x_hi, x_lo, floats(at.x_unit));
     if (err != cudaSuccess) return err;
     note_launch();
+    // Few rows take many threads each, for the latency; many few.
+    const bool wide = pairs <= 512;
     if (!own_place) {
-        err = launch_split<kLo>(static_cast<const T*>(c.x), c.x_stride, c.top_k, e.hidden, starts, order, e.n, x_hi, x_lo,
-                                floats(at.x_unit), pairs, stream);
+        err = wide ? launch_pdl(experts_split<512, T>, dim3(pairs), dim3(512), 0, stream, c, e.hidden, starts, order, e.n, x_hi, x_lo,
+                                floats(at.x_unit))
+                   : launch_pdl(experts_split<128, T>, dim3(pairs), dim3(128), 0, stream, c, e.hidden, starts, order, e.n, x_hi, x_lo,
+                                floats(at.x_unit));
         if (err != cudaSuccess) return err;
+        note_launch();
     }
-    ExpertsMm m = {starts, order, floats(at.x_unit), inner, floats(at.split), counters, c.err, c.x, c.x_stride,
+    ExpertsMm m = {starts, floats(at.x_unit), inner, floats(at.split), counters, c.err,
                    {e.gate ? e.gate : e.up, e.up}, {e.gate ? e.gate_stride : e.up_stride, e.up_stride},
-                   e.n, e.hidden, e.inner, c.top_k, e.activation, at.split_cols, 0x64006400u};
+                   e.n, e.hidden, e.inner, e.activation, at.split_cols, 0x64006400u};
     if ((err = launch_experts_mm(m, e, false, c.type, x_hi, x_lo, pairs, dev, stream)) != cudaSuccess) return err;
-    err = launch_split<kLo>(static_cast<const float*>(inner), e.inner, 0, e.inner, starts, order, e.n, i_hi, i_lo,
-                            floats(at.i_unit), pairs, stream);
+    err = wide ? launch_pdl(experts_inner<512, T>, dim3(pairs), dim3(512), 0, stream, e, c, inner, starts, order, i_hi, i_lo,
+                            floats(at.i_unit))
+               : launch_pdl(experts_inner<128, T>, dim3(pairs), dim3(128), 0, stream, e, c, inner, starts, order, i_hi, i_lo,
+                            floats(at.i_unit));
     if (err != cudaSuccess) return err;
-    m = {starts, order, floats(at.i_unit), part, floats(at.split), counters + kCounters, c.err, inner, e.inner,
-         {e.down, e.down}, {e.down_stride, e.down_stride}, e.n, e.inner, e.hidden, c.top_k, e.activation, at.split_cols,
-         0x64006400u};
+    note_launch();
+    m = {starts, floats(at.i_unit), part, floats(at.split), counters + kCounters, c.err, {e.down, e.down},
+         {e.down_stride, e.down_stride}, e.n, e.inner, e.hidden, e.activation, at.split_cols, 0x64006400u};
     if ((err = launch_experts_mm(m, e, true, c.type, i_hi, i_lo, pairs, dev, stream)) != cudaSuccess) return err;
     err = launch_pdl(experts_combine<T>, dim3((e.hidden + 511) / 512, c.n_tokens < 4096 ? c.n_tokens : 4096), dim3(128), 0,
-                     stream, c, e.hidden, e.n, part);
+                     stream, e, c, starts, place, inner, part);
     if (err == cudaSuccess) note_launch();
     return err;
 }

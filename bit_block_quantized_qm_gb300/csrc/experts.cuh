@@ -3,6 +3,7 @@
 
 #include <cuda_bf16.h>
 
+#include "qm.h"
 #include "qm_device.cuh"
 
 namespace qm {
@@ -17,17 +18,14 @@ constexpr int kExpertTokens = 128;
 // rows, sorted by expert.
 struct ExpertsMm {
     const int32_t* starts;  // [n + 1] sorted rows of each expert
-    const int32_t* order;   // the pair (token * top_k + j) of each sorted row
     const float* unit;      // what a sorted row's pieces are to be multiplied by
-    float* out;             // inner [sorted row][rows], or part [pair][rows]
+    float* out;             // [sorted row][rows]
     float* split;           // partial sums of tiles that several CTAs share
     unsigned* counters;     // and how much of each is there
     unsigned int* err;
-    const void* x;          // the token rows as they were, for sums done again
-    int64_t x_stride;
     const uint8_t* w[2];    // the matrices of a tile's two halves
     int64_t w_stride[2];    // bytes
-    int n, K, rows, top_k;
+    int n, K, rows;
     int activation;
     int split_cols;         // columns of a partial tile
     uint32_t k1024;         // 0x64006400
@@ -40,7 +38,13 @@ __host__ __device__ inline int64_t piece_pitch(int K) { return (K + 63) / 64 * 6
 cudaError_t launch_experts_mm(const ExpertsMm& m, const ExpertsView& e, bool down, KvType type, const void* hi,
                               const void* lo, int64_t n_pieces, const DeviceInfo& dev, cudaStream_t stream);
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+// EXACT: to a few units of f32; otherwise to about 2^-20.
+template <bool EXACT>
+__device__ __forceinline__ float activate(float a, int kind) {
+    if (kind == QM_ACT_NONE) return a;
+    const float z = kind == QM_ACT_SILU ? a : 1.5957691216057308f * (a + 0.044715f * a * a * a);  // tanh(y) = 2 sigmoid(2 y) - 1
+    // (The approximate division is off by 2 units, and 0 where the divisor is 2^126 and more.)
+    return __fdividef(a, 1.f + (EXACT ? expf(-z) : __expf(-z)));
+}
 
 }  // namespace qm

@@ -31,7 +31,15 @@
 // K) of those left over are dealt out evenly, and the CTA that comes last to a shared tile
 // adds its parts in the CTAs' order.
 //
+// Sums that come out infinite or NaN (a scale of 32 and more overflows f16) are left so, and
+// taken again by the kernels that read them.
+//
+// No register may spill here: with most of the SM's memory shared memory, what is spilled comes
+// back from L2, and each reload costs some 300 cycles (products at 817 instead of 1065 TFLOP/s).
+//
 // Every wait is bounded; a wait that gives up sets the device error word.
+#include <type_traits>
+
 #include "experts.cuh"
 #include "tcgen05.cuh"
 
@@ -42,8 +50,8 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kHalf = 128;  // weight rows of a half tile
 constexpr int kDecodeWarps = 16;
-constexpr int kRawWarp = 16, kTokenWarp = 17, kMmaWarp = 18;
-constexpr int kThreads = 19 * 32;
+constexpr int kRawWarp = 16, kTokenWarp = 17, kMmaWarp = 18;  // and 19: the products of a half each
+constexpr int kThreads = 20 * 32;
 constexpr int kTmemA = 256;  // columns 0 .. 255: sums, [set][half][token row]
 constexpr float kWeightUnit = 0x1p-8f;
 
@@ -52,6 +60,9 @@ struct Cfg {
     static constexpr int kTokens = F32 ? kExpertTokens / 2 : kExpertTokens;
     static constexpr int kPanel = kTokens * 128;  // bytes of a piece's 64 elements of all token rows
     static constexpr int kSums = F32 ? 2 : 1;     // sets of sums in TMEM
+    // F32, up to 32 rows: the second pieces are columns of their own beside the first ones', so that
+    // a product of both is one instruction.
+    static __device__ __forceinline__ bool joined(int n) { return F32 && n <= kTokens / 2; }
     // A stage of unpacked weights (there are two, each filled by the warps of one phase) and of
     // token rows: 128 columns of TMEM, two panels.
     static constexpr int kStageK = F32 ? 64 : 128;
@@ -70,12 +81,17 @@ struct Barriers {
     uint64_t acc_full[2], acc_empty[2];
 };
 
-// EXACT: to a few units of f32 (f32 rows); otherwise to about 2^-20.
-template <bool EXACT>
-__device__ __forceinline__ float activate(float a, int kind) {
-    if (kind == 0) return a;
-    const float z = kind == 1 ? a : 1.5957691216057308f * (a + 0.044715f * a * a * a);  // tanh(y) = 2 sigmoid(2 y) - 1
-    return EXACT ? a / (1.f + expf(-z)) : __fdividef(a, 1.f + __expf(-z));
+// Whether phase `parity` is complete, without waiting (try_wait may wait a while).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // A whole warp's bounded waits; the answer is the same for all lanes.
@@ -93,38 +109,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, uint64_t* b,
     atomicOr(err, kErrWaitTimeout);
     return false;
 }
-// A value that all lanes have, in a uniform register.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
-
-// The sum of a row of weights with a row of numbers, element by element: for sums that
-// came out infinite or NaN.
-template <typename T>
-__device__ __noinline__ float exact_dot(const uint8_t* blocks, int K, const T* x) {
-    float s = 0.f;
-    for (int b = 0; b < K / 32; ++b) {
-        const uint8_t* blk = blocks + 18 * b;
-        const float d = f16_bits_to_float(*reinterpret_cast<const uint16_t*>(blk));
-        for (int j = 0; j < 32; ++j) {
-            const uint32_t byte = blk[2 + (j & 15)];
-            const float q = magic_minus8((j < 16 ? byte & 15u : byte >> 4) | kMagicBits);
-            s = fmaf(load1(x + 32 * b + j), q * d, s);
-        }
-    }
-    return s;
-}
+// A value (>= 0) that all lanes have, in a uniform register: what is computed from it, and the
+// branches on it, stay warp-uniform for the compiler too.  An issuing warp whose descriptors go
+// through vector registers takes 48 cycles for a product of 16 columns instead of 9.
+__device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce_max_sync(kAll, static_cast<unsigned>(v))); }
 
 // What a CTA does, one piece after the other: tiles, each with a range of units.
 struct Plan {
     int tiles, full, rest, ku, ctas, cta;
     bool share;  // the tiles left over are shared by all CTAs
-    __device__ __forceinline__ int64_t unit_of(int c) const { return static_cast<int64_t>(rest) * ku * c / ctas; }
+    __device__ __forceinline__ int unit_of(int c) const { return rest * ku * c / ctas; }  // (rest < 160, ku <= 256)
 };
 struct Item {
     int tile, u0, u1;
 };
 struct Cursor {
     int next;     // of the whole tiles
-    int64_t at, end;  // units of shared tiles
+    int at, end;  // units of shared tiles
 };
 __device__ __forceinline__ Cursor first_item(const Plan& p) {
     Cursor c{p.cta, 0, 0};
@@ -134,10 +135,10 @@ __device__ __forceinline__ Cursor first_item(const Plan& p) {
 // Shared tiles first: the CTA that comes last to one has others to go on with.
 __device__ __forceinline__ bool next_item(const Plan& p, Cursor& c, Item* item) {
     if (c.at < c.end) {
-        const int t = static_cast<int>(c.at / p.ku);
+        const int t = c.at / p.ku;
         item->tile = p.full + t;
-        item->u0 = static_cast<int>(c.at - static_cast<int64_t>(t) * p.ku);
-        item->u1 = static_cast<int>(min(static_cast<int64_t>(p.ku), item->u0 + (c.end - c.at)));
+        item->u0 = c.at - t * p.ku;
+        item->u1 = min(p.ku, item->u0 + (c.end - c.at));
         c.at += item->u1 - item->u0;
         return true;
     }
@@ -152,6 +153,12 @@ struct Place {
     int expert, block, p0, n;
 };
 
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // 64 elements of a weight row: words 0 .. 8 are bytes 0 .. 35 of its two blocks.  Stored to
 // columns `addr` .. + 31 (F32: the second pieces to the 32 after).
 template <bool F32>
@@ -161,53 +168,51 @@ __device__ __forceinline__ void unpack_store(const uint32_t (&w)[9], uint32_t ad
         const uint32_t d_bits = __byte_perm(b ? w[4] : w[0], 0, b ? 0x3232 : 0x1010);
         const __half2 d = __hmul2(half2_of(d_bits), half2_of(0x5C005C00u));  // times 2^8
         const __half2 m1032 = half2_of(0xE408E408u), sixteenth = half2_of(0x2C002C00u), m72 = half2_of(0xD480D480u);
-        uint32_t h[16], l[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t q = b ? w[5 + k] : __byte_perm(w[k], w[k + 1], 0x5432);
-            const uint32_t y = q >> 8;
-            const __half2 n[4] = {__hadd2(half2_of((q & 0x000F000Fu) | k1024), m1032),
-                                  __hadd2(half2_of((y & 0x000F000Fu) | k1024), m1032),
-                                  __hfma2(half2_of((q & 0x00F000F0u) | k1024), sixteenth, m72),
-                                  __hfma2(half2_of((y & 0x00F000F0u) | k1024), sixteenth, m72)};
+        for (int k0 = 0; k0 < 4; k0 += 2) {
+            uint32_t h[8], l[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __half2 x = __hmul2(n[e], d);
-                h[4 * k + e] = word(x);
-                if (F32) l[4 * k + e] = word(__hfma2(n[e], d, __hneg2(x)));
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t q = b ? w[5 + k0 + k] : __byte_perm(w[k0 + k], w[k0 + k + 1], 0x5432);
+                const uint32_t y = q >> 8;
+                const __half2 n[4] = {__hadd2(half2_of((q & 0x000F000Fu) | k1024), m1032),
+                                      __hadd2(half2_of((y & 0x000F000Fu) | k1024), m1032),
+                                      __hfma2(half2_of((q & 0x00F000F0u) | k1024), sixteenth, m72),
+                                      __hfma2(half2_of((y & 0x00F000F0u) | k1024), sixteenth, m72)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 x = __hmul2(n[e], d);
+                    h[4 * k + e] = word(x);
+                    if (F32) l[4 * k + e] = word(__hfma2(n[e], d, __hneg2(x)));
+                }
             }
+            tmem_st8(addr + 16 * b + 4 * k0, h);
+            if (F32) tmem_st8(addr + 32 + 16 * b + 4 * k0, l);
         }
-        tmem_st16(addr + 16 * b, h);
-        if (F32) tmem_st16(addr + 32 + 16 * b, l);
     }
 }
 
-// Words of the 64-element pieces KS0 and KS0 + STEP of a unit's row.
-template <int KS0, int STEP, bool WIDE>
-__device__ __forceinline__ void load_words(const uint8_t* row, int shift, uint32_t (&w)[2][9]) {
+// The nine words of a unit's 64 elements number KS.
+template <int KS, bool WIDE>
+__device__ __forceinline__ void load_words(const uint8_t* row, int shift, uint32_t (&w)[9]) {
+    if constexpr (!WIDE) {
+        // Bytes 36 KS .. + 35 lie KS words into the 48 bytes from the 16-byte boundary below.
+        uint32_t v[12];
+        constexpr int kFrom = 36 * KS & ~15;
+        *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(row + kFrom);
+        *reinterpret_cast<uint4*>(v + 4) = *reinterpret_cast<const uint4*>(row + kFrom + 16);
+        *reinterpret_cast<uint4*>(v + 8) = *reinterpret_cast<const uint4*>(row + kFrom + 32);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        constexpr int kStep = 36;
-        const int ks = KS0 + STEP * j;
-        if constexpr (!WIDE) {
-            // Bytes 36 ks .. + 35 lie ks words into the 48 bytes from the 16-byte boundary below.
-            uint32_t v[12];
-            const int from = kStep * ks & ~15;
-            *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(row + from);
-            *reinterpret_cast<uint4*>(v + 4) = *reinterpret_cast<const uint4*>(row + from + 16);
-            *reinterpret_cast<uint4*>(v + 8) = *reinterpret_cast<const uint4*>(row + from + 32);
+        for (int i = 0; i < 9; ++i) w[i] = v[i + KS];
+    } else {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(row + 36 * KS + (shift & ~3));
+        const uint32_t sel = shift & 2 ? 0x5432 : 0x3210;
+        uint32_t v = p[0];
 #pragma unroll
-            for (int i = 0; i < 9; ++i) w[j][i] = v[i + ks];
-        } else {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(row + kStep * ks + (shift & ~3));
-            const uint32_t sel = shift & 2 ? 0x5432 : 0x3210;
-            uint32_t v = p[0];
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-                const uint32_t next = p[i + 1];
-                w[j][i] = __byte_perm(v, next, sel);
-                v = next;
-            }
+        for (int i = 0; i < 9; ++i) {
+            const uint32_t next = p[i + 1];
+            w[i] = __byte_perm(v, next, sel);
+            v = next;
         }
     }
 }
@@ -225,8 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int tiles_before[1024 + 1];  // token tiles of all lower experts
     __shared__ int rows_before[1024 + 1];   // their sorted rows
-    __shared__ float units[2][C::kTokens];  // of the columns of this tile and the one before
-    __shared__ int pairs[2][C::kTokens];
+    __shared__ alignas(16) float units[3][C::kTokens];  // of the columns of this tile, the one before and the one after
     __shared__ int last_of_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* const err = m.err;
@@ -236,12 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.raw_full[i], 1);
             mbar_init(&bar.raw_empty[i], kDecodeWarps);
             mbar_init(&bar.tok_full[i], 1);
-            mbar_init(&bar.tok_empty[i], 1);
+            mbar_init(&bar.tok_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.a_full[i], 8);
-            mbar_init(&bar.a_empty[i], 1);
-            mbar_init(&bar.acc_full[i], 1);
+            mbar_init(&bar.a_empty[i], 2);
+            mbar_init(&bar.acc_full[i], 2);
             mbar_init(&bar.acc_empty[i], kDecodeWarps);
         }
         fence_barrier_init();
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int block_rows = two ? kHalf : 2 * kHalf;
     const int blocks = (m.rows + block_rows - 1) / block_rows;
     Plan plan;
-    plan.tiles = tiles_before[m.n] * blocks;
+    plan.tiles = uniform(tiles_before[m.n]) * blocks;
     plan.ctas = gridDim.x;
     plan.cta = blockIdx.x;
     plan.ku = (m.K + 255) / 256;
@@ -302,10 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             else hi = mid;
         }
         Place p;
-        p.expert = lo;
+        p.expert = uniform(lo);
         p.block = tile - tt * blocks;
-        p.p0 = rows_before[lo] + (tt - tiles_before[lo]) * C::kTokens;
-        p.n = min(C::kTokens, rows_before[lo + 1] - p.p0);
+        p.p0 = uniform(rows_before[lo] + (tt - tiles_before[lo]) * C::kTokens);
+        p.n = uniform(min(C::kTokens, rows_before[lo + 1] - p.p0));
         return p;
     };
     const int row_bytes = m.K / 32 * 18;
@@ -322,9 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = half * kHalf + (WIDE ? (r % together) * (kHalf / together) + r / together : r);
         const uint32_t a_cols = tmem + lanes + kTmemA + ph * 128 + half * 64;
         bool ok = true;
-        uint32_t it = 0, sums = 0, n_items = 0;  // units, sets of sums
-        uint32_t uses = 0;                       // of this phase's stage
-        float v0[16], v1[16];  // F32: this thread's sums, columns 16 group .. + 15 of both halves
+        uint32_t it = 0, sums = 0;  // units, sets of sums
+        uint32_t uses = 0;          // of this phase's stage
+        float v0[16], v1[16];  // sums of columns 16 ch .. + 15 of both halves (F32: kept from unit to unit, ch = group)
         // Waits for the set of sums number `sums`.
         auto wait_sums = [&] {
             ok = ok && warp_wait(&bar.acc_full[sums % C::kSums], (sums / C::kSums) & 1, err);
@@ -341,99 +345,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_sums();
             if (16 * group < n) {
                 const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kTokens + 16 * group;
+                const int second = C::joined(n) ? (n + 15) & ~15 : 0;  // where the products with the second pieces are
                 float a[16];
-                tmem_ld16(d, a);
-                tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v0[i] += a[i];
-                tmem_ld16(d + C::kTokens, a);
-                tc_wait_ld();
+                for (int half = 0; half < 2; ++half) {
+                    float(&v)[16] = half ? v1 : v0;
+                    tmem_ld16(d + half * C::kTokens, a);
+                    tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v1[i] += a[i];
+                    for (int i = 0; i < 16; ++i) v[i] += a[i];
+                    if (second) {
+                        tmem_ld16(d + half * C::kTokens + second, a);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] += a[i];
+                    }
+                }
             }
             free_sums();
         };
-        while (next_item(plan, cur, &item)) {
-            const Place pl = place(item.tile);
-            const int buf = n_items++ & 1;
-            if (static_cast<int>(threadIdx.x) < C::kTokens) {
-                const int p = pl.p0 + min(static_cast<int>(threadIdx.x), pl.n - 1);
-                units[buf][threadIdx.x] = m.unit[p] * kWeightUnit;
-                if (DOWN) pairs[buf][threadIdx.x] = m.order[p];
-            }
-            if constexpr (F32) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.f;
-            }
-            for (int u = item.u0; u < item.u1; ++u, ++it) {
-                const int stage = it % C::kRawStages;
-                ok = ok && warp_wait(&bar.raw_full[stage], (it / C::kRawStages) & 1, err);
-                const uint8_t* row = raw + stage * C::kRawBytes + slot * C::kPitch;
-                uint32_t w[2][9];
-                const int left = m.K - 256 * u;
-                if (F32 && ph) load_words<1, 2, WIDE>(row, shift, w);
-                else if (F32) load_words<0, 2, WIDE>(row, shift, w);
-                else if (ph) load_words<2, 1, WIDE>(row, shift, w);
-                else load_words<0, 1, WIDE>(row, shift, w);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.raw_empty[stage]);
-                // bf16 rows: 128 elements, a stage; f32 rows: 64 elements twice.
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int ks = F32 ? ph + 2 * j : 2 * ph + j;
-                    if (F32 ? 64 * ks >= left : 128 * ph >= left) break;
-                    if (F32 || j == 0) {
-                        ok = ok && (uses == 0 || warp_wait(&bar.a_empty[ph], (uses - 1) & 1, err));
-                        ++uses;
-                        tc_fence_after();
-                    }
-                    unpack_store<F32>(w[j], a_cols + (F32 ? 0 : 32 * j), m.k1024);
-                    if (F32 || j == 1) {
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.a_full[ph]);
-                    }
+        auto unpack_unit = [&](int u) {
+            const int stage = it % C::kRawStages;
+            ok = ok && warp_wait(&bar.raw_full[stage], (it / C::kRawStages) & 1, err);
+            ++it;
+            const uint8_t* row = raw + stage * C::kRawBytes + slot * C::kPitch;
+            const int left = m.K - 256 * u;
+            // bf16 rows: 128 elements, a stage; f32 rows: 64 elements twice.
+            auto half_unit = [&](auto number) {
+                constexpr int j = decltype(number)::value;
+                uint32_t w[9];
+                if (ph) load_words<F32 ? 1 + 2 * j : 2 + j, WIDE>(row, shift, w);
+                else load_words<F32 ? 2 * j : j, WIDE>(row, shift, w);
+                if (j == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.raw_empty[stage]);
                 }
-                if (F32 && u > item.u0) collect(pl.n);  // of the unit before
-            }
+                const bool there = F32 ? 64 * (ph + 2 * j) < left : 128 * ph < left;
+                if (there && (F32 || j == 0)) {
+                    ok = ok && (uses == 0 || warp_wait(&bar.a_empty[ph], (uses - 1) & 1, err));
+                    ++uses;
+                    tc_fence_after();
+                }
+                if (there) unpack_store<F32>(w, a_cols + (F32 ? 0 : 32 * j), m.k1024);
+                if (there && (F32 || j == 1)) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.a_full[ph]);
+                }
+            };
+            half_unit(std::integral_constant<int, 0>{});
+            half_unit(std::integral_constant<int, 1>{});
+        };
+        // A tile's outputs, once all of its products are done.
+        auto outputs = [&](int tile, int n_units, uint32_t mine_buf) {
+            const Place pl = place(tile);
             if constexpr (F32) collect(pl.n);
             else wait_sums();
-            named_barrier_sync(2, kDecodeWarps * 32);  // the units and pairs are there
-            const bool whole = item.u1 - item.u0 == plan.ku;
+            named_barrier_sync(2, kDecodeWarps * 32);  // the factors and pairs are there
+            const bool whole = n_units == plan.ku;
             const int f0 = pl.block * block_rows + r, f1 = two ? f0 : f0 + kHalf;
+            const bool in0 = f0 < m.rows, in1 = f1 < m.rows;
             // Columns 16 ch .. 16 ch + 15 of both halves, as sums of whole rows.
             auto finish = [&](int ch) {
-                auto again = [&](int which, int f, int c) {
-                    const uint8_t* w = m.w[which] + pl.expert * m.w_stride[which] + static_cast<int64_t>(f) * row_bytes;
-                    if (DOWN) return exact_dot(w, m.K, static_cast<const float*>(m.x) + (pl.p0 + c) * m.x_stride);
-                    const int64_t at = (m.order[pl.p0 + c] / m.top_k) * m.x_stride;
-                    if (!F32) return exact_dot(w, m.K, static_cast<const __nv_bfloat16*>(m.x) + at);
-                    return exact_dot(w, m.K, static_cast<const float*>(m.x) + at);
-                };
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 s = *reinterpret_cast<const float4*>(&units[mine_buf][16 * ch + i]);
+                    v0[i] *= s.x, v0[i + 1] *= s.y, v0[i + 2] *= s.z, v0[i + 3] *= s.w;
+                    v1[i] *= s.x, v1[i + 1] *= s.y, v1[i + 2] *= s.z, v1[i + 3] *= s.w;
+                }
+                if (!DOWN) {
+                    const int kind = m.activation;
+                    if (kind == QM_ACT_SILU) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v0[i] = activate<F32>(v0[i], QM_ACT_SILU);
+                            if (!two) v1[i] = activate<F32>(v1[i], QM_ACT_SILU);
+                        }
+                    } else if (kind == QM_ACT_GELU) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v0[i] = activate<F32>(v0[i], QM_ACT_GELU);
+                            if (!two) v1[i] = activate<F32>(v1[i], QM_ACT_GELU);
+                        }
+                    }
+                    if (two) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v0[i] *= v1[i];
+                    }
+                }
                 float* out = m.out + static_cast<int64_t>(pl.p0 + 16 * ch) * m.rows + f0;
-                const int f_step = f1 - f0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int c = 16 * ch + i;
-                    if (c >= pl.n) break;
-                    const float s = units[buf][c];
-                    float a = v0[i] * s, b = v1[i] * s;
-                    if (!(fabsf(a) + fabsf(b) < INFINITY)) {
-                        if (f0 < m.rows && !isfinite(a)) a = again(0, f0, c);
-                        if (f1 < m.rows && !isfinite(b)) b = again(1, f1, c);
-                    }
-                    if (DOWN) {
-                        out = m.out + static_cast<int64_t>(pairs[buf][c]) * m.rows + f0;
-                        if (f0 < m.rows) out[0] = a;
-                        if (f1 < m.rows) out[kHalf] = b;
-                    } else if (two) {
-                        if (f0 < m.rows) out[0] = activate<F32>(a, m.activation) * b;
-                    } else {
-                        if (f0 < m.rows) out[0] = activate<F32>(a, m.activation);
-                        if (f1 < m.rows) out[f_step] = activate<F32>(b, m.activation);
-                    }
-                    if (!DOWN) out += m.rows;
+                    if (16 * ch + i >= pl.n) break;
+                    if (in0) out[0] = v0[i];
+                    if (in1 && !two) out[kHalf] = v1[i];
+                    asm volatile("" ::: "memory");
+                    out += m.rows;
                 }
             };
             auto load_sums = [&](int ch) {
@@ -449,51 +457,100 @@ __global__ void __launch_bounds__(kThreads, 1)
                     finish(ch);
                 }
                 if constexpr (!F32) free_sums();
-                continue;
+                return;
             }
             // A part of the tile: kept in this CTA's place, [half][column][row].
             const int64_t place_floats = static_cast<int64_t>(2 * kHalf) * m.split_cols;
-            const int shared_tile = item.tile - plan.full;
+            const int shared_tile = tile - plan.full;
             auto part_of = [&](int c) {  // CTA c's part of this tile
-                const int first = static_cast<int>(plan.unit_of(c) / plan.ku);
+                const int first = plan.unit_of(c) / plan.ku;
                 return m.split + (2 * c + (shared_tile - first)) * place_floats;
             };
             float* mine = part_of(plan.cta);
             for (int ch = group; 16 * ch < pl.n; ch += 4) {
                 load_sums(ch);
+                float* at = mine + 16 * ch * kHalf + r;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    mine[(16 * ch + i) * kHalf + r] = v0[i];
-                    mine[(m.split_cols + 16 * ch + i) * kHalf + r] = v1[i];
+                    at[i * kHalf] = v0[i];
+                    at[(m.split_cols + i) * kHalf] = v1[i];
                 }
             }
             if constexpr (!F32) free_sums();
             __threadfence();
             named_barrier_sync(1, kDecodeWarps * 32);
             if (threadIdx.x == 0) {
-                const unsigned n = static_cast<unsigned>(item.u1 - item.u0);
+                const unsigned n = static_cast<unsigned>(n_units);
                 last_of_tile = atomicAdd(&m.counters[shared_tile], n) + n == static_cast<unsigned>(plan.ku);
                 __threadfence();
             }
             named_barrier_sync(1, kDecodeWarps * 32);
-            if (!last_of_tile) continue;
+            if (!last_of_tile) return;
             // The CTAs that have units of it, in order.
-            const int64_t total = static_cast<int64_t>(plan.rest) * plan.ku, u_lo = static_cast<int64_t>(shared_tile) * plan.ku;
-            const int c_lo = static_cast<int>(((u_lo + 1) * plan.ctas - 1) / total);
-            const int c_hi = static_cast<int>(((u_lo + plan.ku) * plan.ctas - 1) / total);
+            const int total = plan.rest * plan.ku, u_lo = shared_tile * plan.ku;
+            const int c_lo = ((u_lo + 1) * plan.ctas - 1) / total, c_hi = ((u_lo + plan.ku) * plan.ctas - 1) / total;
             for (int ch = group; 16 * ch < pl.n; ch += 4) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.f;
-                for (int c = c_lo; c <= c_hi; ++c) {
-                    if (plan.unit_of(c) == plan.unit_of(c + 1)) continue;
-                    const float* part = part_of(c);
+                for (int half = 0; half < 2; ++half) {
+                    float(&v)[16] = half ? v1 : v0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        v0[i] += __ldcg(part + (16 * ch + i) * kHalf + r);
-                        v1[i] += __ldcg(part + (m.split_cols + 16 * ch + i) * kHalf + r);
+                    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+#pragma unroll 1
+                    for (int c = c_lo; c <= c_hi; ++c) {
+                        if (plan.unit_of(c) == plan.unit_of(c + 1)) continue;
+                        const float* part = part_of(c) + (half * m.split_cols + 16 * ch) * kHalf + r;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (i % 8 == 0) asm volatile("" ::: "memory");  // (8 loads on their way: more would cost registers)
+                            v[i] += __ldcg(part + i * kHalf);
+                        }
                     }
                 }
                 finish(ch);
+            }
+        };
+
+        // Unit by unit.  A tile's outputs wait until the next tile's first unit is unpacked, so that the
+        // products of that one can begin as soon as there is room for its sums.
+        int done_tile = 0, done_units = 0, n_now = 0;
+        uint32_t buf = 0, buf_done = 0;  // of 3 sets of factors: a warp may be two tiles ahead of another's outputs
+        bool more = next_item(plan, cur, &item), due = false;
+        int u = 0;
+        auto begin = [&] {
+            const Place pl = place(item.tile);
+            n_now = pl.n;
+            u = item.u0;
+            buf = buf == 2 ? 0 : buf + 1;
+            if (static_cast<int>(threadIdx.x) < C::kTokens) {
+                const int p = pl.p0 + min(static_cast<int>(threadIdx.x), pl.n - 1);
+                units[buf][threadIdx.x] = m.unit[p] * kWeightUnit;
+            }
+        };
+        if (more) begin();
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.f;
+        }
+#pragma unroll 1
+        while (more || due) {
+            if (more) {
+                unpack_unit(u);
+                if constexpr (F32)
+                    if (u > item.u0) collect(n_now);  // of the unit before
+            }
+            if (due) {
+                outputs(done_tile, done_units, buf_done);
+                due = false;
+                if constexpr (F32) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.f;
+                }
+            }
+            if (more && ++u == item.u1) {
+                done_tile = item.tile, done_units = item.u1 - item.u0, buf_done = buf;
+                due = true;
+                more = next_item(plan, cur, &item);
+                if (more) begin();
             }
         }
     } else if (warp == kRawWarp) {
@@ -540,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t* dst = tok + stage * C::kTokenBytes;
                 if (16 * lane < n16) {
                     tma_load_2d(dst + lane * 2048, &map_hi, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
-                    if (F32) tma_load_2d(dst + C::kPanel + lane * 2048, &map_lo, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
+                    if (F32) tma_load_2d(dst + (C::joined(pl.n) ? n16 * 128 : C::kPanel) + lane * 2048, &map_lo, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
                     else if (both) tma_load_2d(dst + C::kPanel + lane * 2048, &map_hi, k + 64, pl.p0 + 16 * lane, &bar.tok_full[stage]);
                 }
                 __syncwarp();
@@ -549,55 +606,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = kt > C::kTokenStages ? kt - C::kTokenStages : 0; !ok && i < kt; ++i)
             mbar_wait_bounded(&bar.tok_full[i % C::kTokenStages], (i / C::kTokenStages) & 1, err);
     } else {
-        // ---- products
+        // ---- products of a half of the weight rows
         const uint32_t lead = elect_one();
+        const int half = warp - kMmaWarp;
         bool ok = true;
         uint32_t sums = 0, stage = 0, round = 0;
         uint32_t a_phase = 0;  // a bit per stage
         const uint64_t b_first = desc_base(smem_addr(tok), 16);
+        const uint32_t d_half = tmem + half * C::kTokens, w_half = tmem + kTmemA + half * 64;
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
-            const uint32_t id = idesc_f16(uniform(pl.n + 15) & ~15, false);
-            const int k_begin = uniform(256 * item.u0), k_end = uniform(min(m.K, 256 * item.u1));
-            uint32_t acc = 0, d_set = 0;
+            const int n16 = (pl.n + 15) & ~15;
+            const bool joined = C::joined(pl.n);
+            const uint32_t id = idesc_f16(n16, false), id_both = idesc_f16(2 * n16, false);
+            const int k_begin = 256 * item.u0, k_end = min(m.K, 256 * item.u1);
+            uint32_t acc = 0, d = d_half;
+            bool ready = false;  // this stage's barriers have been seen complete
             for (int k = k_begin; k < k_end && ok; k += C::kStageK) {
                 if (k == k_begin || (F32 && k % 256 == 0)) {  // a set of sums: F32 a unit's, else the item's
                     if (sums >= C::kSums)
                         ok = warp_wait(&bar.acc_empty[sums % C::kSums], (sums / C::kSums - 1) & 1, err);
-                    if (!ok) break;
-                    d_set = (sums % C::kSums) * 2 * C::kTokens;
+                    d = d_half + (sums % C::kSums) * 2 * C::kTokens;
                     acc = 0;
                 }
                 const int a = (k / C::kStageK) & 1;
-                ok = warp_wait(&bar.tok_full[stage], round & 1, &bar.a_full[a], (a_phase >> a) & 1, err);
+                if (!ready) ok = ok && warp_wait(&bar.tok_full[stage], round & 1, &bar.a_full[a], (a_phase >> a) & 1, err);
                 if (!ok) break;
                 a_phase ^= 1u << a;
                 tc_fence_after();
                 const uint64_t b = b_first + stage * (C::kTokenBytes >> 4);
-                const uint32_t d = tmem + d_set, w = tmem + kTmemA + a * 128;
-                const int steps = min(C::kStageK, k_end - k) >> 4;
-#pragma unroll
-                for (int s = 0; s < C::kStageK / 16; ++s) {
-                    if (s >= steps) break;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t dh = d + half * C::kTokens, wh = w + half * 64 + 8 * s;
-                        const uint64_t bs = b + (F32 ? 2 * s : (s >> 2) * (C::kPanel >> 4) + 2 * (s & 3));
-                        mma_ts(dh, wh, bs, id, s > 0 ? 1 : acc, lead);
-                        if (F32) {
-                            mma_ts(dh, wh, bs + (C::kPanel >> 4), id, 1, lead);
-                            mma_ts(dh, wh + 32, bs, id, 1, lead);
+                const uint32_t w = w_half + a * 128;
+                if (++stage == C::kTokenStages) stage = 0, ++round;
+                auto step = [&](int s, uint32_t add) {
+                    if constexpr (F32) {
+                        if (joined) {
+                            mma_ts(d, w + 8 * s, b + 2 * s, id_both, add, lead);
+                            mma_ts(d, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
+                        } else {
+                            mma_ts(d, w + 8 * s, b + 2 * s, id, add, lead);
+                            mma_ts(d, w + 8 * s, b + (C::kPanel >> 4) + 2 * s, id, 1, lead);
+                            mma_ts(d, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
                         }
+                    } else {
+                        mma_ts(d, w + 8 * s, b + (s >> 2) * (C::kPanel >> 4) + 2 * (s & 3), id, add, lead);
                     }
-                }
+                };
+                constexpr int kSteps = C::kStageK / 16;
+                step(0, acc);
                 acc = 1;
+                ready = false;
+                if (k_end - k >= C::kStageK) {
+                    // Halfway the next stage's barriers are looked at, while products are queued.
+#pragma unroll
+                    for (int s = 1; s < kSteps / 2; ++s) step(s, 1);
+                    if (k + C::kStageK < k_end) {
+                        const bool x = mbar_test(&bar.tok_full[stage], round & 1);
+                        const bool y = mbar_test(&bar.a_full[a ^ 1], (a_phase >> (a ^ 1)) & 1);
+                        ready = __all_sync(kAll, x && y);
+                    }
+#pragma unroll
+                    for (int s = kSteps / 2; s < kSteps; ++s) step(s, 1);
+                } else {
+                    const int steps = (k_end - k) >> 4;
+#pragma unroll 1
+                    for (int s = 1; s < steps; ++s) step(s, 1);
+                }
                 mma_commit(&bar.a_empty[a], lead);
-                mma_commit(&bar.tok_empty[stage], lead);
+                mma_commit(&bar.tok_empty[stage == 0 ? C::kTokenStages - 1 : stage - 1], lead);
                 if (k + C::kStageK >= k_end || (F32 && k % 256 == 192)) {
                     mma_commit(&bar.acc_full[sums % C::kSums], lead);
                     ++sums;
                 }
-                if (++stage == C::kTokenStages) stage = 0, ++round;
             }
         }
         // Products still under way (after a wait that gave up) end before the TMEM is given back.
