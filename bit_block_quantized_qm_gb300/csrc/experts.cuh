@@ -11,7 +11,7 @@ namespace qm {
 // The products run on at most this many CTAs (one per SM): a bound for the
 // workspace, whose size the host gives without asking a device.
 constexpr int kExpertCtas = 160;
-// Most token rows of a tile of the products (f32 rows: half of it).
+// Most token rows of a tile of the products.
 constexpr int kExpertTokens = 128;
 
 // One of the two products: rows of W (gate and up, or down) with the pieces of token

@@ -52,47 +52,36 @@ constexpr int kHalf = 128;  // weight rows of a half tile
 constexpr int kDecodeWarps = 16;
 constexpr int kRawWarp = 16, kTokenWarp = 17, kMmaWarp = 18;  // and 19: the products of a half each
 constexpr int kThreads = 20 * 32;
-constexpr int kTmemA = 256;  // columns 0 .. 255: sums, [set][half][token row]
 constexpr float kWeightUnit = 0x1p-8f;
 
-template <bool F32, bool WIDE>
+template <bool F32, int TOKENS, bool WIDE>
 struct Cfg {
-    static constexpr int kTokens = F32 ? kExpertTokens / 2 : kExpertTokens;
-    static constexpr int kPanel = kTokens * 128;  // bytes of a piece's 64 elements of all token rows
-    static constexpr int kSums = F32 ? 2 : 1;     // sets of sums in TMEM
-    // F32, up to 32 rows: the second pieces are columns of their own beside the first ones', so that
-    // a product of both is one instruction.
-    static __device__ __forceinline__ bool joined(int n) { return F32 && n <= kTokens / 2; }
-    // A stage of unpacked weights (there are two, each filled by the warps of one phase) and of
-    // token rows: 128 columns of TMEM, two panels.
+    static constexpr int kTokens = TOKENS;  // token rows of a tile
+    // F32: the second pieces are columns of their own beside the first ones', so that a product with
+    // both is one instruction.
+    static constexpr int kColumns = F32 ? 2 * kTokens : kTokens;  // of a half's sums
+    static constexpr int kSums = kTokens > 32 ? 1 : 2;            // sets of sums in TMEM
+    static constexpr int kChunk = kTokens > 32 ? 16 : 8;          // columns that a thread has at a time
+    // Unpacked weights in TMEM: stages of 128 columns (bf16 rows: 128 elements, f32 rows: 64).  Long
+    // ones, because an issuing warp takes some 300 cycles for a stage besides its products.
     static constexpr int kStageK = F32 ? 64 : 128;
+    static constexpr int kTmemA = kSums * 2 * kColumns;  // (the sums come first)
+    static constexpr int kAStages = (512 - kTmemA) / 128;
     static constexpr int kPitch = WIDE ? 176 : 144;  // bytes of a raw row in shared memory, an odd number of 16s
     static constexpr int kRawBytes = 2 * kHalf * kPitch;
-    static constexpr int kRawStages = F32 && !WIDE ? 4 : 3;
-    static constexpr int kTokenBytes = 2 * kPanel;
-    static constexpr int kTokenStages = F32 ? 4 : WIDE ? 2 : 3;
+    static constexpr int kTokenBytes = (kStageK / 64) * kColumns * 128;
+    static constexpr int kTokenStages = kTokens > 32 ? (WIDE ? 2 : 3) : F32 ? 8 : 6;
+    static constexpr int kRawStages = kTokens > 32 || WIDE ? 3 : 4;
     static constexpr int kSmem = kRawStages * kRawBytes + kTokenStages * kTokenBytes + 1024;
+    static_assert(kTmemA % 128 == 0 && kAStages >= 2, "room for the weights");
 };
 
 struct Barriers {
     uint64_t raw_full[4], raw_empty[4];
-    uint64_t tok_full[4], tok_empty[4];
-    uint64_t a_full[2], a_empty[2];
+    uint64_t tok_full[8], tok_empty[8];
+    uint64_t a_full[4], a_empty[4];
     uint64_t acc_full[2], acc_empty[2];
 };
-
-// Whether phase `parity` is complete, without waiting (try_wait may wait a while).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 
 // A whole warp's bounded waits; the answer is the same for all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, unsigned int* err) {
@@ -153,41 +142,34 @@ struct Place {
     int expert, block, p0, n;
 };
 
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+__device__ __forceinline__ void tmem_ldn(uint32_t addr, float (&v)[16]) { tmem_ld16(addr, v); }
+__device__ __forceinline__ void tmem_ldn(uint32_t addr, float (&v)[8]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
 }
 
-// 64 elements of a weight row: words 0 .. 8 are bytes 0 .. 35 of its two blocks.  Stored to
-// columns `addr` .. + 31 (F32: the second pieces to the 32 after).
+// A block of a weight row, number `b` of the two that words 0 .. 8 (36 bytes) hold, in the order in
+// which its quants unpack; F32: with the second pieces.
 template <bool F32>
-__device__ __forceinline__ void unpack_store(const uint32_t (&w)[9], uint32_t addr, uint32_t k1024) {
+__device__ __forceinline__ void unpack_block(const uint32_t (&w)[9], int b, uint32_t k1024, uint32_t* h, uint32_t* l) {
+    const uint32_t d_bits = __byte_perm(b ? w[4] : w[0], 0, b ? 0x3232 : 0x1010);
+    const __half2 d = __hmul2(half2_of(d_bits), half2_of(0x5C005C00u));  // times 2^8
+    const __half2 m1032 = half2_of(0xE408E408u), sixteenth = half2_of(0x2C002C00u), m72 = half2_of(0xD480D480u);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const uint32_t d_bits = __byte_perm(b ? w[4] : w[0], 0, b ? 0x3232 : 0x1010);
-        const __half2 d = __hmul2(half2_of(d_bits), half2_of(0x5C005C00u));  // times 2^8
-        const __half2 m1032 = half2_of(0xE408E408u), sixteenth = half2_of(0x2C002C00u), m72 = half2_of(0xD480D480u);
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t q = b ? w[5 + k] : __byte_perm(w[k], w[k + 1], 0x5432);
+        const uint32_t y = q >> 8;
+        const __half2 n[4] = {__hadd2(half2_of((q & 0x000F000Fu) | k1024), m1032),
+                              __hadd2(half2_of((y & 0x000F000Fu) | k1024), m1032),
+                              __hfma2(half2_of((q & 0x00F000F0u) | k1024), sixteenth, m72),
+                              __hfma2(half2_of((y & 0x00F000F0u) | k1024), sixteenth, m72)};
 #pragma unroll
-        for (int k0 = 0; k0 < 4; k0 += 2) {
-            uint32_t h[8], l[8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t q = b ? w[5 + k0 + k] : __byte_perm(w[k0 + k], w[k0 + k + 1], 0x5432);
-                const uint32_t y = q >> 8;
-                const __half2 n[4] = {__hadd2(half2_of((q & 0x000F000Fu) | k1024), m1032),
-                                      __hadd2(half2_of((y & 0x000F000Fu) | k1024), m1032),
-                                      __hfma2(half2_of((q & 0x00F000F0u) | k1024), sixteenth, m72),
-                                      __hfma2(half2_of((y & 0x00F000F0u) | k1024), sixteenth, m72)};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 x = __hmul2(n[e], d);
-                    h[4 * k + e] = word(x);
-                    if (F32) l[4 * k + e] = word(__hfma2(n[e], d, __hneg2(x)));
-                }
-            }
-            tmem_st8(addr + 16 * b + 4 * k0, h);
-            if (F32) tmem_st8(addr + 32 + 16 * b + 4 * k0, l);
+        for (int e = 0; e < 4; ++e) {
+            const __half2 x = __hmul2(n[e], d);
+            h[4 * k + e] = word(x);
+            if (F32) l[4 * k + e] = word(__hfma2(n[e], d, __hneg2(x)));
         }
     }
 }
@@ -217,12 +199,12 @@ __device__ __forceinline__ void load_words(const uint8_t* row, int shift, uint32
     }
 }
 
-template <bool F32, bool DOWN, bool WIDE>
+template <bool F32, int TOKENS, bool DOWN, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     experts_mm_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
                       const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo,
                       const ExpertsMm m) {
-    using C = Cfg<F32, WIDE>;
+    using C = Cfg<F32, TOKENS, WIDE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* tok = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     uint8_t* raw = tok + C::kTokenStages * C::kTokenBytes;
@@ -239,12 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bar.raw_full[i], 1);
             mbar_init(&bar.raw_empty[i], kDecodeWarps);
+            mbar_init(&bar.a_full[i], 8);
+            mbar_init(&bar.a_empty[i], 2);
+        }
+        for (int i = 0; i < 8; ++i) {
             mbar_init(&bar.tok_full[i], 1);
             mbar_init(&bar.tok_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.a_full[i], 8);
-            mbar_init(&bar.a_empty[i], 2);
             mbar_init(&bar.acc_full[i], 2);
             mbar_init(&bar.acc_empty[i], kDecodeWarps);
         }
@@ -324,11 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int together = WIDE ? 16 / (row_bytes & -row_bytes) : 1;
         const int shift = WIDE ? (r % together) * row_bytes & 15 : 0;
         const int slot = half * kHalf + (WIDE ? (r % together) * (kHalf / together) + r / together : r);
-        const uint32_t a_cols = tmem + lanes + kTmemA + ph * 128 + half * 64;
+        const uint32_t a_cols = tmem + lanes + C::kTmemA + half * 64;
         bool ok = true;
         uint32_t it = 0, sums = 0;  // units, sets of sums
-        uint32_t uses = 0;          // of this phase's stage
-        float v0[16], v1[16];  // sums of columns 16 ch .. + 15 of both halves (F32: kept from unit to unit, ch = group)
+        // This phase's next stage of unpacked weights, and how often it has been filled (a unit has two stages,
+        // f32 rows' four; phase p fills every second one).
+        uint32_t a_stage = ph, a_round = 0;
+        constexpr int kChunk = C::kChunk;
+        float v0[kChunk], v1[kChunk];  // sums of a chunk of columns of both halves (F32: number `group`, kept from unit to unit)
         // Waits for the set of sums number `sums`.
         auto wait_sums = [&] {
             ok = ok && warp_wait(&bar.acc_full[sums % C::kSums], (sums / C::kSums) & 1, err);
@@ -343,22 +330,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // F32: adds the sums of a unit to those of the units before it.
         auto collect = [&](int n) {
             wait_sums();
-            if (16 * group < n) {
-                const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kTokens + 16 * group;
-                const int second = C::joined(n) ? (n + 15) & ~15 : 0;  // where the products with the second pieces are
-                float a[16];
+            if constexpr (F32) {
+                if (kChunk * group < n) {
+                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kColumns + kChunk * group;
+                    const int second = (n + 15) & ~15;  // where the products with the second pieces are
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float(&v)[16] = half ? v1 : v0;
-                    tmem_ld16(d + half * C::kTokens, a);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += a[i];
-                    if (second) {
-                        tmem_ld16(d + half * C::kTokens + second, a);
+                    for (int half = 0; half < 2; ++half) {
+                        float(&v)[kChunk] = half ? v1 : v0;
+                        float a[kChunk], b[kChunk];
+                        tmem_ldn(d + half * C::kColumns, a);
+                        tmem_ldn(d + half * C::kColumns + second, b);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] += a[i];
+                        for (int i = 0; i < kChunk; ++i) v[i] += a[i] + b[i];
                     }
                 }
             }
@@ -369,33 +353,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && warp_wait(&bar.raw_full[stage], (it / C::kRawStages) & 1, err);
             ++it;
             const uint8_t* row = raw + stage * C::kRawBytes + slot * C::kPitch;
-            const int left = m.K - 256 * u;
-            // bf16 rows: 128 elements, a stage; f32 rows: 64 elements twice.
-            auto half_unit = [&](auto number) {
-                constexpr int j = decltype(number)::value;
-                uint32_t w[9];
-                if (ph) load_words<F32 ? 1 + 2 * j : 2 + j, WIDE>(row, shift, w);
-                else load_words<F32 ? 2 * j : j, WIDE>(row, shift, w);
-                if (j == 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.raw_empty[stage]);
-                }
-                const bool there = F32 ? 64 * (ph + 2 * j) < left : 128 * ph < left;
-                if (there && (F32 || j == 0)) {
-                    ok = ok && (uses == 0 || warp_wait(&bar.a_empty[ph], (uses - 1) & 1, err));
-                    ++uses;
-                    tc_fence_after();
-                }
-                if (there) unpack_store<F32>(w, a_cols + (F32 ? 0 : 32 * j), m.k1024);
-                if (there && (F32 || j == 1)) {
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.a_full[ph]);
-                }
+            [[maybe_unused]] const int left = m.K - 256 * u;
+            auto begin_stage = [&] {
+                ok = ok && (a_round == 0 || warp_wait(&bar.a_empty[a_stage], (a_round - 1) & 1, err));
+                tc_fence_after();
             };
-            half_unit(std::integral_constant<int, 0>{});
-            half_unit(std::integral_constant<int, 1>{});
+            auto end_stage = [&] {
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.a_full[a_stage]);
+                a_stage += 2;
+                if (a_stage >= C::kAStages) a_stage -= C::kAStages, ++a_round;
+            };
+            auto load = [&](auto first, auto second, uint32_t(&w)[9]) {
+                if (ph) load_words<decltype(second)::value, WIDE>(row, shift, w);
+                else load_words<decltype(first)::value, WIDE>(row, shift, w);
+            };
+            auto done_with_row = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.raw_empty[stage]);
+            };
+            using I = std::integral_constant<int, 0>;
+            // (As much as there are registers for is unpacked before the wait for room.  Stages past a
+            // row's end are handed over empty.)
+            uint32_t w[9];
+            if constexpr (F32) {  // the unit's 64 elements number ph, then ph + 2
+                auto unpack_64 = [&](bool there) {
+                    uint32_t h[16], l[16];
+                    unpack_block<true>(w, 0, m.k1024, h, l);
+                    begin_stage();
+                    const uint32_t at = a_cols + a_stage * 128;
+                    if (there) {
+                        tmem_st16(at, h);
+                        tmem_st16(at + 32, l);
+                        unpack_block<true>(w, 1, m.k1024, h, l);
+                        tmem_st16(at + 16, h);
+                        tmem_st16(at + 48, l);
+                    }
+                    end_stage();
+                };
+                load(I{}, std::integral_constant<int, 1>{}, w);
+                unpack_64(64 * ph < left);
+                load(std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{}, w);
+                done_with_row();
+                unpack_64(64 * (ph + 2) < left);
+            } else {  // its elements 128 ph .. + 127
+                uint32_t h[32];
+                load(I{}, std::integral_constant<int, 2>{}, w);
+                unpack_block<false>(w, 0, m.k1024, h, nullptr);
+                unpack_block<false>(w, 1, m.k1024, h + 16, nullptr);
+                load(std::integral_constant<int, 1>{}, std::integral_constant<int, 3>{}, w);
+                done_with_row();
+                begin_stage();
+                const uint32_t at = a_cols + a_stage * 128;
+                tmem_st32(at, reinterpret_cast<const float*>(h));
+                unpack_block<false>(w, 0, m.k1024, h, nullptr);
+                unpack_block<false>(w, 1, m.k1024, h + 16, nullptr);
+                tmem_st32(at + 32, reinterpret_cast<const float*>(h));
+                end_stage();
+            }
         };
         // A tile's outputs, once all of its products are done.
         auto outputs = [&](int tile, int n_units, uint32_t mine_buf) {
@@ -406,11 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = n_units == plan.ku;
             const int f0 = pl.block * block_rows + r, f1 = two ? f0 : f0 + kHalf;
             const bool in0 = f0 < m.rows, in1 = f1 < m.rows;
-            // Columns 16 ch .. 16 ch + 15 of both halves, as sums of whole rows.
+            // Chunk ch of the columns of both halves, as sums of whole rows.
             auto finish = [&](int ch) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 s = *reinterpret_cast<const float4*>(&units[mine_buf][16 * ch + i]);
+                for (int i = 0; i < kChunk; i += 4) {
+                    const float4 s = *reinterpret_cast<const float4*>(&units[mine_buf][kChunk * ch + i]);
                     v0[i] *= s.x, v0[i + 1] *= s.y, v0[i + 2] *= s.z, v0[i + 3] *= s.w;
                     v1[i] *= s.x, v1[i + 1] *= s.y, v1[i + 2] *= s.z, v1[i + 3] *= s.w;
                 }
@@ -418,26 +435,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int kind = m.activation;
                     if (kind == QM_ACT_SILU) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < kChunk; ++i) {
                             v0[i] = activate<F32>(v0[i], QM_ACT_SILU);
                             if (!two) v1[i] = activate<F32>(v1[i], QM_ACT_SILU);
                         }
                     } else if (kind == QM_ACT_GELU) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < kChunk; ++i) {
                             v0[i] = activate<F32>(v0[i], QM_ACT_GELU);
                             if (!two) v1[i] = activate<F32>(v1[i], QM_ACT_GELU);
                         }
                     }
                     if (two) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v0[i] *= v1[i];
+                        for (int i = 0; i < kChunk; ++i) v0[i] *= v1[i];
                     }
                 }
-                float* out = m.out + static_cast<int64_t>(pl.p0 + 16 * ch) * m.rows + f0;
+                float* out = m.out + static_cast<int64_t>(pl.p0 + kChunk * ch) * m.rows + f0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (16 * ch + i >= pl.n) break;
+                for (int i = 0; i < kChunk; ++i) {
+                    if (kChunk * ch + i >= pl.n) break;
                     if (in0) out[0] = v0[i];
                     if (in1 && !two) out[kHalf] = v1[i];
                     asm volatile("" ::: "memory");
@@ -446,13 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto load_sums = [&](int ch) {
                 if constexpr (!F32) {
-                    tmem_ld16(tmem + lanes + 16 * ch, v0);
-                    tmem_ld16(tmem + lanes + C::kTokens + 16 * ch, v1);
+                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kColumns + kChunk * ch;
+                    tmem_ldn(d, v0);
+                    tmem_ldn(d + C::kColumns, v1);
                     tc_wait_ld();
                 }
             };
             if (whole) {
-                for (int ch = group; 16 * ch < pl.n; ch += 4) {
+                for (int ch = group; kChunk * ch < pl.n; ch += 4) {
                     load_sums(ch);
                     finish(ch);
                 }
@@ -467,11 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return m.split + (2 * c + (shared_tile - first)) * place_floats;
             };
             float* mine = part_of(plan.cta);
-            for (int ch = group; 16 * ch < pl.n; ch += 4) {
+            for (int ch = group; kChunk * ch < pl.n; ch += 4) {
                 load_sums(ch);
-                float* at = mine + 16 * ch * kHalf + r;
+                float* at = mine + kChunk * ch * kHalf + r;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < kChunk; ++i) {
                     at[i * kHalf] = v0[i];
                     at[(m.split_cols + i) * kHalf] = v1[i];
                 }
@@ -489,18 +507,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The CTAs that have units of it, in order.
             const int total = plan.rest * plan.ku, u_lo = shared_tile * plan.ku;
             const int c_lo = ((u_lo + 1) * plan.ctas - 1) / total, c_hi = ((u_lo + plan.ku) * plan.ctas - 1) / total;
-            for (int ch = group; 16 * ch < pl.n; ch += 4) {
+            for (int ch = group; kChunk * ch < pl.n; ch += 4) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    float(&v)[16] = half ? v1 : v0;
+                    float(&v)[kChunk] = half ? v1 : v0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+                    for (int i = 0; i < kChunk; ++i) v[i] = 0.f;
 #pragma unroll 1
                     for (int c = c_lo; c <= c_hi; ++c) {
                         if (plan.unit_of(c) == plan.unit_of(c + 1)) continue;
-                        const float* part = part_of(c) + (half * m.split_cols + 16 * ch) * kHalf + r;
+                        const float* part = part_of(c) + (half * m.split_cols + kChunk * ch) * kHalf + r;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < kChunk; ++i) {
                             if (i % 8 == 0) asm volatile("" ::: "memory");  // (8 loads on their way: more would cost registers)
                             v[i] += __ldcg(part + i * kHalf);
                         }
@@ -529,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) begin();
         if constexpr (F32) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.f;
+            for (int i = 0; i < kChunk; ++i) v0[i] = v1[i] = 0.f;
         }
 #pragma unroll 1
         while (more || due) {
@@ -543,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 due = false;
                 if constexpr (F32) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.f;
+                    for (int i = 0; i < kChunk; ++i) v0[i] = v1[i] = 0.f;
                 }
             }
             if (more && ++u == item.u1) {
@@ -580,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = it > C::kRawStages ? it - C::kRawStages : 0; !ok && i < it; ++i)  // what is still on its way
             mbar_wait_bounded(&bar.raw_full[i % C::kRawStages], (i / C::kRawStages) & 1, err);
     } else if (warp == kTokenWarp) {
-        // ---- token pieces
+        // ---- token pieces (bf16 rows: two panels of 64 elements)
+        constexpr int kPanel = C::kTokens * 128;
         bool ok = true;
         uint32_t kt = 0;
         while (ok && next_item(plan, cur, &item)) {
@@ -597,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t* dst = tok + stage * C::kTokenBytes;
                 if (16 * lane < n16) {
                     tma_load_2d(dst + lane * 2048, &map_hi, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
-                    if (F32) tma_load_2d(dst + (C::joined(pl.n) ? n16 * 128 : C::kPanel) + lane * 2048, &map_lo, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
-                    else if (both) tma_load_2d(dst + C::kPanel + lane * 2048, &map_hi, k + 64, pl.p0 + 16 * lane, &bar.tok_full[stage]);
+                    if (F32) tma_load_2d(dst + n16 * 128 + lane * 2048, &map_lo, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
+                    else if (both) tma_load_2d(dst + kPanel + lane * 2048, &map_hi, k + 64, pl.p0 + 16 * lane, &bar.tok_full[stage]);
                 }
                 __syncwarp();
             }
@@ -610,70 +629,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lead = elect_one();
         const int half = warp - kMmaWarp;
         bool ok = true;
-        uint32_t sums = 0, stage = 0, round = 0;
-        uint32_t a_phase = 0;  // a bit per stage
+        uint32_t sums = 0, stage = 0, round = 0;  // sets of sums; stages of tokens
+        uint32_t a = 0, a_round = 0;              // and of weights
         const uint64_t b_first = desc_base(smem_addr(tok), 16);
-        const uint32_t d_half = tmem + half * C::kTokens, w_half = tmem + kTmemA + half * 64;
+        const uint32_t d_half = tmem + half * C::kColumns, w_half = tmem + C::kTmemA + half * 64;
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
             const int n16 = (pl.n + 15) & ~15;
-            const bool joined = C::joined(pl.n);
-            const uint32_t id = idesc_f16(n16, false), id_both = idesc_f16(2 * n16, false);
-            const int k_begin = 256 * item.u0, k_end = min(m.K, 256 * item.u1);
+            const uint32_t id = idesc_f16(n16, false), id_both = idesc_f16(F32 ? 2 * n16 : n16, false);
+            const int k_begin = 256 * item.u0, k_end = 256 * item.u1;
             uint32_t acc = 0, d = d_half;
-            bool ready = false;  // this stage's barriers have been seen complete
             for (int k = k_begin; k < k_end && ok; k += C::kStageK) {
                 if (k == k_begin || (F32 && k % 256 == 0)) {  // a set of sums: F32 a unit's, else the item's
                     if (sums >= C::kSums)
                         ok = warp_wait(&bar.acc_empty[sums % C::kSums], (sums / C::kSums - 1) & 1, err);
-                    d = d_half + (sums % C::kSums) * 2 * C::kTokens;
+                    d = d_half + (sums % C::kSums) * 2 * C::kColumns;
                     acc = 0;
                 }
-                const int a = (k / C::kStageK) & 1;
-                if (!ready) ok = ok && warp_wait(&bar.tok_full[stage], round & 1, &bar.a_full[a], (a_phase >> a) & 1, err);
+                if (k < m.K) ok = ok && warp_wait(&bar.tok_full[stage], round & 1, &bar.a_full[a], a_round & 1, err);
+                else ok = ok && warp_wait(&bar.a_full[a], a_round & 1, err);
                 if (!ok) break;
-                a_phase ^= 1u << a;
                 tc_fence_after();
                 const uint64_t b = b_first + stage * (C::kTokenBytes >> 4);
                 const uint32_t w = w_half + a * 128;
-                if (++stage == C::kTokenStages) stage = 0, ++round;
                 auto step = [&](int s, uint32_t add) {
                     if constexpr (F32) {
-                        if (joined) {
-                            mma_ts(d, w + 8 * s, b + 2 * s, id_both, add, lead);
-                            mma_ts(d, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
-                        } else {
-                            mma_ts(d, w + 8 * s, b + 2 * s, id, add, lead);
-                            mma_ts(d, w + 8 * s, b + (C::kPanel >> 4) + 2 * s, id, 1, lead);
-                            mma_ts(d, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
-                        }
+                        mma_ts(d, w + 8 * s, b + 2 * s, id_both, add, lead);
+                        mma_ts(d, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
                     } else {
-                        mma_ts(d, w + 8 * s, b + (s >> 2) * (C::kPanel >> 4) + 2 * (s & 3), id, add, lead);
+                        mma_ts(d, w + 8 * s, b + (s >> 2) * (C::kTokens * 128 >> 4) + 2 * (s & 3), id, add, lead);
                     }
                 };
-                constexpr int kSteps = C::kStageK / 16;
-                step(0, acc);
-                acc = 1;
-                ready = false;
-                if (k_end - k >= C::kStageK) {
-                    // Halfway the next stage's barriers are looked at, while products are queued.
+                if (k + C::kStageK <= m.K) {
+                    step(0, acc);
 #pragma unroll
-                    for (int s = 1; s < kSteps / 2; ++s) step(s, 1);
-                    if (k + C::kStageK < k_end) {
-                        const bool x = mbar_test(&bar.tok_full[stage], round & 1);
-                        const bool y = mbar_test(&bar.a_full[a ^ 1], (a_phase >> (a ^ 1)) & 1);
-                        ready = __all_sync(kAll, x && y);
-                    }
-#pragma unroll
-                    for (int s = kSteps / 2; s < kSteps; ++s) step(s, 1);
-                } else {
-                    const int steps = (k_end - k) >> 4;
+                    for (int s = 1; s < C::kStageK / 16; ++s) step(s, 1);
+                } else if (k < m.K) {
+                    const int steps = (m.K - k) >> 4;
+                    step(0, acc);
 #pragma unroll 1
                     for (int s = 1; s < steps; ++s) step(s, 1);
                 }
+                acc = 1;
                 mma_commit(&bar.a_empty[a], lead);
-                mma_commit(&bar.tok_empty[stage == 0 ? C::kTokenStages - 1 : stage - 1], lead);
-                if (k + C::kStageK >= k_end || (F32 && k % 256 == 192)) {
+                if (++a == C::kAStages) a = 0, ++a_round;
+                if (k < m.K) {
+                    mma_commit(&bar.tok_empty[stage], lead);
+                    if (++stage == C::kTokenStages) stage = 0, ++round;
+                }
+                if (k + C::kStageK == k_end || (F32 && k % 256 == 192)) {
                     mma_commit(&bar.acc_full[sums % C::kSums], lead);
                     ++sums;
                 }
@@ -703,12 +707,12 @@ cudaError_t weight_map(CUtensorMap* map, const uint8_t* w, int64_t stride, int64
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 3, dims, strides, box);
 }
 
-template <bool F32, bool DOWN, bool WIDE>
+template <bool F32, int TOKENS, bool DOWN, bool WIDE>
 cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, const void* hi, const void* lo,
                           int64_t n_pieces, const DeviceInfo& dev, cudaStream_t stream) {
-    using C = Cfg<F32, WIDE>;
+    using C = Cfg<F32, TOKENS, WIDE>;
     static SmemOnce once;
-    cudaError_t err = once.set(experts_mm_kernel<F32, DOWN, WIDE>, C::kSmem);
+    cudaError_t err = once.set(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, C::kSmem);
     if (err != cudaSuccess) return err;
     const int64_t row_bytes = m.K / 32 * 18;
     const int together = WIDE ? 16 / static_cast<int>(row_bytes & -row_bytes) : 1;
@@ -723,7 +727,7 @@ cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, const void* 
         if (err != cudaSuccess) return err;
     }
     const int ctas = dev.sm_count < kExpertCtas ? dev.sm_count : kExpertCtas;
-    err = launch_pdl(experts_mm_kernel<F32, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi, t_lo, m);
+    err = launch_pdl(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi, t_lo, m);
     if (err == cudaSuccess) note_launch();
     return err;
 }
@@ -732,14 +736,18 @@ cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, const void* 
 
 cudaError_t launch_experts_mm(const ExpertsMm& m, const ExpertsView& e, bool down, KvType type, const void* hi,
                               const void* lo, int64_t n_pieces, const DeviceInfo& dev, cudaStream_t stream) {
-    const bool f32 = type == KvType::kF32, wide = m.K % 256 != 0;
-    auto go = [&](auto kernel) { return kernel(m, e, hi, f32 ? lo : hi, n_pieces, dev, stream); };
-    if (f32) {
-        if (down) return wide ? go(launch_kernel<true, true, true>) : go(launch_kernel<true, true, false>);
-        return wide ? go(launch_kernel<true, false, true>) : go(launch_kernel<true, false, false>);
-    }
-    if (down) return wide ? go(launch_kernel<false, true, true>) : go(launch_kernel<false, true, false>);
-    return wide ? go(launch_kernel<false, false, true>) : go(launch_kernel<false, false, false>);
+    const bool wide = m.K % 256 != 0;
+    auto go = [&](auto f32, auto tokens) {
+        constexpr bool kF32 = decltype(f32)::value;
+        constexpr int kTokens = decltype(tokens)::value;
+        auto run = [&](auto kernel) { return kernel(m, e, hi, kF32 ? lo : hi, n_pieces, dev, stream); };
+        if (down) return wide ? run(launch_kernel<kF32, kTokens, true, true>) : run(launch_kernel<kF32, kTokens, true, false>);
+        return wide ? run(launch_kernel<kF32, kTokens, false, true>) : run(launch_kernel<kF32, kTokens, false, false>);
+    };
+    if (type == KvType::kF32) return go(std::true_type{}, std::integral_constant<int, 32>{});
+    // Narrow tiles where experts have few rows: two sets of sums, and three stages of weights.
+    if (n_pieces <= 16 * static_cast<int64_t>(e.n)) return go(std::false_type{}, std::integral_constant<int, 32>{});
+    return go(std::false_type{}, std::integral_constant<int, kExpertTokens>{});
 }
 
 }  // namespace qm
