@@ -56,34 +56,34 @@ constexpr float kWeightUnit = 0x1p-8f;
 
 template <bool F32, int TOKENS, bool WIDE>
 struct Cfg {
-    static constexpr int kTokens = TOKENS;  // token rows of a tile
-    // F32: the second pieces are columns of their own beside the first ones', so that a product with
-    // both is one instruction.
-    static constexpr int kColumns = F32 ? 2 * kTokens : kTokens;  // of a half's sums
-    static constexpr int kSums = kTokens > 32 ? 1 : 2;            // sets of sums in TMEM
-    static constexpr int kChunk = kTokens > 32 ? 16 : 8;          // columns that a thread has at a time
-    // Unpacked weights in TMEM: stages of 128 columns (bf16 rows: 128 elements, f32 rows: 64).  Long
-    // ones, because an issuing warp takes some 300 cycles for a stage besides its products.
+    static constexpr int kTokens = TOKENS;              // token rows of a tile
+    static constexpr int kSums = kTokens > 32 ? 1 : 2;  // sets of sums in TMEM
+    static constexpr int kChunk = kTokens > 32 ? 16 : 8;  // columns of sums that a thread has at a time
+    // CTAs come in pairs that take the same token rows (and blocks of weights next to each other):
+    // each loads half of them for both.
+    static constexpr int kPair = kTokens > 32 ? 2 : 1;
+    // Stages of unpacked weights, 128 columns of TMEM (bf16 rows: 128 elements, f32 rows: 64), and of
+    // the token rows that they meet.  Long ones, because an issuing warp takes 300 cycles and more for a
+    // stage besides its products.
     static constexpr int kStageK = F32 ? 64 : 128;
-    static constexpr int kTmemA = kSums * 2 * kColumns;  // (the sums come first)
-    static constexpr int kAStages = (512 - kTmemA) / 128;
+    static constexpr int kTmemA = kSums * 2 * kTokens;  // (the sums come first)
+    static constexpr int kStages = (512 - kTmemA) / 128;
     static constexpr int kPitch = WIDE ? 176 : 144;  // bytes of a raw row in shared memory, an odd number of 16s
     static constexpr int kRawBytes = 2 * kHalf * kPitch;
-    static constexpr int kTokenBytes = (kStageK / 64) * kColumns * 128;
-    static constexpr int kTokenStages = kTokens > 32 ? (WIDE ? 2 : 3) : F32 ? 8 : 6;
-    static constexpr int kRawStages = kTokens > 32 || WIDE ? 3 : 4;
+    static constexpr int kTokenBytes = 2 * kTokens * 128;  // bf16 rows: two panels of 64 elements, f32 rows: two pieces
+    static constexpr int kTokenStages = kTokens > 32 ? (WIDE ? 2 : 3) : 8;
+    static constexpr int kRawStages = WIDE || kTokens > 32 ? 3 : 4;
     static constexpr int kSmem = kRawStages * kRawBytes + kTokenStages * kTokenBytes + 1024;
-    static_assert(kTmemA % 128 == 0 && kAStages >= 2, "room for the weights");
+    static_assert(kTmemA % 128 == 0 && kStages >= 2, "room for the weights");
 };
 
 struct Barriers {
     uint64_t raw_full[4], raw_empty[4];
     uint64_t tok_full[8], tok_empty[8];
-    uint64_t a_full[4], a_empty[4];
+    uint64_t full[3], empty[3];
     uint64_t acc_full[2], acc_empty[2];
 };
 
-// A whole warp's bounded waits; the answer is the same for all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, unsigned int* err) {
     for (uint32_t i = 0; i < kMaxWaitPolls; ++i)
         if (__all_sync(kAll, mbar_try_wait(a, pa))) return true;
@@ -98,6 +98,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, uint64_t* b,
     atomicOr(err, kErrWaitTimeout);
     return false;
 }
+// A TMA box into the same place of both CTAs of a pair, and an arrival of each on its barrier.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// Products done: an arrival on the barrier of both CTAs of a pair.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+            smem_addr(bar)),
+        "r"(lead), "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
 // A value (>= 0) that all lanes have, in a uniform register: what is computed from it, and the
 // branches on it, stay warp-uniform for the compiler too.  An issuing warp whose descriptors go
 // through vector registers takes 48 cycles for a product of 16 columns instead of 9.
@@ -105,7 +124,7 @@ __device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce
 
 // What a CTA does, one piece after the other: tiles, each with a range of units.
 struct Plan {
-    int tiles, full, rest, ku, ctas, cta;
+    int tiles, full, rest, ku, ctas, cta;  // (of pairs of CTAs where they come in pairs)
     bool share;  // the tiles left over are shared by all CTAs
     __device__ __forceinline__ int unit_of(int c) const { return rest * ku * c / ctas; }  // (rest < 160, ku <= 256)
 };
@@ -221,12 +240,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bar.raw_full[i], 1);
             mbar_init(&bar.raw_empty[i], kDecodeWarps);
-            mbar_init(&bar.a_full[i], 8);
-            mbar_init(&bar.a_empty[i], 2);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bar.full[i], 8);   // the warps that unpack
+            mbar_init(&bar.empty[i], 2);  // the products of both halves
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&bar.tok_full[i], 1);
-            mbar_init(&bar.tok_empty[i], 2);
+            mbar_init(&bar.tok_empty[i], 2 * C::kPair);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.acc_full[i], 2);
@@ -267,16 +288,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // (Every CTA's barriers are initialised before the other of a pair can arrive on them.)
+    if constexpr (C::kPair > 1) cluster_sync_all();
     grid_launch_dependents();
     const uint32_t tmem = tmem_slot;
 
     const bool two = m.w[0] != m.w[1];  // gate and up
     const int block_rows = two ? kHalf : 2 * kHalf;
-    const int blocks = (m.rows + block_rows - 1) / block_rows;
+    const int blocks = (m.rows + block_rows * C::kPair - 1) / (block_rows * C::kPair);  // (of a pair)
+    const int rank = C::kPair > 1 ? static_cast<int>(blockIdx.x & 1) : 0;
     Plan plan;
     plan.tiles = uniform(tiles_before[m.n]) * blocks;
-    plan.ctas = gridDim.x;
-    plan.cta = blockIdx.x;
+    plan.ctas = gridDim.x / C::kPair;
+    plan.cta = blockIdx.x / C::kPair;
     plan.ku = (m.K + 255) / 256;
     plan.full = plan.tiles / plan.ctas * plan.ctas;
     plan.rest = plan.tiles - plan.full;
@@ -291,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Place p;
         p.expert = uniform(lo);
-        p.block = tile - tt * blocks;
+        p.block = (tile - tt * blocks) * C::kPair + rank;
         p.p0 = uniform(rows_before[lo] + (tt - tiles_before[lo]) * C::kTokens);
         p.n = uniform(min(C::kTokens, rows_before[lo + 1] - p.p0));
         return p;
@@ -332,18 +356,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_sums();
             if constexpr (F32) {
                 if (kChunk * group < n) {
-                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kColumns + kChunk * group;
-                    const int second = (n + 15) & ~15;  // where the products with the second pieces are
+                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kTokens + kChunk * group;
+                    float a[kChunk], b[kChunk];
+                    tmem_ldn(d, a);
+                    tmem_ldn(d + C::kTokens, b);
+                    tc_wait_ld();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float(&v)[kChunk] = half ? v1 : v0;
-                        float a[kChunk], b[kChunk];
-                        tmem_ldn(d + half * C::kColumns, a);
-                        tmem_ldn(d + half * C::kColumns + second, b);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < kChunk; ++i) v[i] += a[i] + b[i];
-                    }
+                    for (int i = 0; i < kChunk; ++i) v0[i] += a[i], v1[i] += b[i];
                 }
             }
             free_sums();
@@ -355,16 +374,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* row = raw + stage * C::kRawBytes + slot * C::kPitch;
             [[maybe_unused]] const int left = m.K - 256 * u;
             auto begin_stage = [&] {
-                ok = ok && (a_round == 0 || warp_wait(&bar.a_empty[a_stage], (a_round - 1) & 1, err));
+                ok = ok && (a_round == 0 || warp_wait(&bar.empty[a_stage], (a_round - 1) & 1, err));
                 tc_fence_after();
             };
             auto end_stage = [&] {
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.a_full[a_stage]);
+                if (lane == 0) mbar_arrive(&bar.full[a_stage]);
                 a_stage += 2;
-                if (a_stage >= C::kAStages) a_stage -= C::kAStages, ++a_round;
+                if (a_stage >= C::kStages) a_stage -= C::kStages, ++a_round;
             };
             auto load = [&](auto first, auto second, uint32_t(&w)[9]) {
                 if (ph) load_words<decltype(second)::value, WIDE>(row, shift, w);
@@ -463,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto load_sums = [&](int ch) {
                 if constexpr (!F32) {
-                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kColumns + kChunk * ch;
+                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kTokens + kChunk * ch;
                     tmem_ldn(d, v0);
-                    tmem_ldn(d + C::kColumns, v1);
+                    tmem_ldn(d + C::kTokens, v1);
                     tc_wait_ld();
                 }
             };
@@ -482,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int shared_tile = tile - plan.full;
             auto part_of = [&](int c) {  // CTA c's part of this tile
                 const int first = plan.unit_of(c) / plan.ku;
-                return m.split + (2 * c + (shared_tile - first)) * place_floats;
+                return m.split + ((2 * c + (shared_tile - first)) * C::kPair + rank) * place_floats;
             };
             float* mine = part_of(plan.cta);
             for (int ch = group; kChunk * ch < pl.n; ch += 4) {
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_barrier_sync(1, kDecodeWarps * 32);
             if (threadIdx.x == 0) {
                 const unsigned n = static_cast<unsigned>(n_units);
-                last_of_tile = atomicAdd(&m.counters[shared_tile], n) + n == static_cast<unsigned>(plan.ku);
+                last_of_tile = atomicAdd(&m.counters[shared_tile * C::kPair + rank], n) + n == static_cast<unsigned>(plan.ku);
                 __threadfence();
             }
             named_barrier_sync(1, kDecodeWarps * 32);
@@ -598,26 +617,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = it > C::kRawStages ? it - C::kRawStages : 0; !ok && i < it; ++i)  // what is still on its way
             mbar_wait_bounded(&bar.raw_full[i % C::kRawStages], (i / C::kRawStages) & 1, err);
     } else if (warp == kTokenWarp) {
-        // ---- token pieces (bf16 rows: two panels of 64 elements)
-        constexpr int kPanel = C::kTokens * 128;
+        // ---- token rows
         bool ok = true;
         uint32_t kt = 0;
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
             const int n16 = (pl.n + 15) & ~15;
             const int k_end = min(m.K, 256 * item.u1);
-            for (int k = 256 * item.u0; k < k_end && ok; k += C::kStageK, ++kt) {
+            for (int k = 256 * item.u0; k < k_end; k += C::kStageK, ++kt) {
                 const int stage = kt % C::kTokenStages;
                 if (kt >= C::kTokenStages) ok = warp_wait(&bar.tok_empty[stage], (kt / C::kTokenStages - 1) & 1, err);
                 if (!ok) break;
                 const bool both = F32 || k + 64 < k_end;  // (the last 64 elements of a row may be a stage)
                 if (lane == 0) mbar_arrive_expect_tx(&bar.tok_full[stage], (both ? 2 : 1) * n16 * 128);
                 __syncwarp();
-                uint8_t* dst = tok + stage * C::kTokenBytes;
-                if (16 * lane < n16) {
-                    tma_load_2d(dst + lane * 2048, &map_hi, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
-                    if (F32) tma_load_2d(dst + n16 * 128 + lane * 2048, &map_lo, k, pl.p0 + 16 * lane, &bar.tok_full[stage]);
-                    else if (both) tma_load_2d(dst + kPanel + lane * 2048, &map_hi, k + 64, pl.p0 + 16 * lane, &bar.tok_full[stage]);
+                // Lane i: 16 rows; of a pair's CTAs one takes the even ones, one the odd ones.
+                uint8_t* dst = tok + stage * C::kTokenBytes + lane * 2048;
+                if (16 * lane < n16 && (C::kPair == 1 || (lane & 1) == rank)) {
+                    const int p = pl.p0 + 16 * lane;
+                    const CUtensorMap* second = F32 ? &map_lo : &map_hi;
+                    const int k2 = F32 ? k : k + 64;
+                    if constexpr (C::kPair > 1) {
+                        tma_load_2d_pair(dst, &map_hi, k, p, &bar.tok_full[stage]);
+                        if (both) tma_load_2d_pair(dst + C::kTokens * 128, second, k2, p, &bar.tok_full[stage]);
+                    } else {
+                        tma_load_2d(dst, &map_hi, k, p, &bar.tok_full[stage]);
+                        if (both) tma_load_2d(dst + C::kTokens * 128, second, k2, p, &bar.tok_full[stage]);
+                    }
                 }
                 __syncwarp();
             }
@@ -629,35 +655,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lead = elect_one();
         const int half = warp - kMmaWarp;
         bool ok = true;
-        uint32_t sums = 0, stage = 0, round = 0;  // sets of sums; stages of tokens
-        uint32_t a = 0, a_round = 0;              // and of weights
+        uint32_t sums = 0, stage = 0, round = 0;  // sets of sums, stages of weights
+        uint32_t t_stage = 0, t_round = 0;        // stages of tokens
         const uint64_t b_first = desc_base(smem_addr(tok), 16);
-        const uint32_t d_half = tmem + half * C::kColumns, w_half = tmem + C::kTmemA + half * 64;
+        const uint32_t d_half = tmem + half * C::kTokens, w_half = tmem + C::kTmemA + half * 64;
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
-            const int n16 = (pl.n + 15) & ~15;
-            const uint32_t id = idesc_f16(n16, false), id_both = idesc_f16(F32 ? 2 * n16 : n16, false);
+            const uint32_t id = idesc_f16((pl.n + 15) & ~15, false);
             const int k_begin = 256 * item.u0, k_end = 256 * item.u1;
             uint32_t acc = 0, d = d_half;
             for (int k = k_begin; k < k_end && ok; k += C::kStageK) {
                 if (k == k_begin || (F32 && k % 256 == 0)) {  // a set of sums: F32 a unit's, else the item's
                     if (sums >= C::kSums)
                         ok = warp_wait(&bar.acc_empty[sums % C::kSums], (sums / C::kSums - 1) & 1, err);
-                    d = d_half + (sums % C::kSums) * 2 * C::kColumns;
+                    d = d_half + (sums % C::kSums) * 2 * C::kTokens;
                     acc = 0;
                 }
-                if (k < m.K) ok = ok && warp_wait(&bar.tok_full[stage], round & 1, &bar.a_full[a], a_round & 1, err);
-                else ok = ok && warp_wait(&bar.a_full[a], a_round & 1, err);
+                if (k < m.K) ok = ok && warp_wait(&bar.tok_full[t_stage], t_round & 1, &bar.full[stage], round & 1, err);
+                else ok = ok && warp_wait(&bar.full[stage], round & 1, err);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t b = b_first + stage * (C::kTokenBytes >> 4);
-                const uint32_t w = w_half + a * 128;
+                const uint64_t b = b_first + t_stage * (C::kTokenBytes >> 4);
+                const uint32_t w = w_half + stage * 128;
+                constexpr uint32_t kSecond = C::kTokens * 128 >> 4;
                 auto step = [&](int s, uint32_t add) {
                     if constexpr (F32) {
-                        mma_ts(d, w + 8 * s, b + 2 * s, id_both, add, lead);
+                        mma_ts(d, w + 8 * s, b + 2 * s, id, add, lead);
+                        mma_ts(d, w + 8 * s, b + kSecond + 2 * s, id, 1, lead);
                         mma_ts(d, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
                     } else {
-                        mma_ts(d, w + 8 * s, b + (s >> 2) * (C::kTokens * 128 >> 4) + 2 * (s & 3), id, add, lead);
+                        mma_ts(d, w + 8 * s, b + (s >> 2) * kSecond + 2 * (s & 3), id, add, lead);
                     }
                 };
                 if (k + C::kStageK <= m.K) {
@@ -671,11 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int s = 1; s < steps; ++s) step(s, 1);
                 }
                 acc = 1;
-                mma_commit(&bar.a_empty[a], lead);
-                if (++a == C::kAStages) a = 0, ++a_round;
+                mma_commit(&bar.empty[stage], lead);
+                if (++stage == C::kStages) stage = 0, ++round;
                 if (k < m.K) {
-                    mma_commit(&bar.tok_empty[stage], lead);
-                    if (++stage == C::kTokenStages) stage = 0, ++round;
+                    if constexpr (C::kPair > 1) mma_commit_pair(&bar.tok_empty[t_stage], lead);
+                    else mma_commit(&bar.tok_empty[t_stage], lead);
+                    if (++t_stage == C::kTokenStages) t_stage = 0, ++t_round;
                 }
                 if (k + C::kStageK == k_end || (F32 && k % 256 == 192)) {
                     mma_commit(&bar.acc_full[sums % C::kSums], lead);
@@ -693,6 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // Neither CTA of a pair leaves while the other may still write to its shared memory.  (Every thread
+    // comes here, whatever its waits returned.)
+    if constexpr (C::kPair > 1) cluster_sync_all();
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
@@ -726,8 +757,13 @@ cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, const void* 
                            CU_TENSOR_MAP_SWIZZLE_128B);
         if (err != cudaSuccess) return err;
     }
-    const int ctas = dev.sm_count < kExpertCtas ? dev.sm_count : kExpertCtas;
-    err = launch_pdl(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi, t_lo, m);
+    const int ctas = (dev.sm_count < kExpertCtas ? dev.sm_count : kExpertCtas) / C::kPair * C::kPair;
+    if constexpr (C::kPair > 1)
+        err = launch_pdl_cluster(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, C::kPair,
+                                 w0, w1, t_hi, t_lo, m);
+    else
+        err = launch_pdl(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi,
+                         t_lo, m);
     if (err == cudaSuccess) note_launch();
     return err;
 }
