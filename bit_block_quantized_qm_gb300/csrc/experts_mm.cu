@@ -71,7 +71,10 @@ struct Cfg {
     static constexpr int kPitch = WIDE ? 176 : 144;  // bytes of a raw row in shared memory, an odd number of 16s
     static constexpr int kRawBytes = 2 * kHalf * kPitch;
     static constexpr int kTokenBytes = 2 * kTokens * 128;  // bf16 rows: two panels of 64 elements, f32 rows: two pieces
-    static constexpr int kTokenStages = kTokens > 32 ? (WIDE ? 2 : 3) : 8;
+    // Narrow tiles: a stage of weights and its token rows have one barrier.  Pairs: the token rows have
+    // stages of their own, further ahead.
+    static constexpr bool kJoint = kPair == 1;
+    static constexpr int kTokenStages = kJoint ? kStages : WIDE ? 2 : 3;
     static constexpr int kRawStages = WIDE || kTokens > 32 ? 3 : 4;
     static constexpr int kSmem = kRawStages * kRawBytes + kTokenStages * kTokenBytes + 1024;
     static_assert(kTmemA % 128 == 0 && kStages >= 2, "room for the weights");
@@ -79,7 +82,7 @@ struct Cfg {
 
 struct Barriers {
     uint64_t raw_full[4], raw_empty[4];
-    uint64_t tok_full[8], tok_empty[8];
+    uint64_t tok_full[3], tok_empty[3];
     uint64_t full[3], empty[3];
     uint64_t acc_full[2], acc_empty[2];
 };
@@ -242,12 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.raw_empty[i], kDecodeWarps);
         }
         for (int i = 0; i < 3; ++i) {
-            mbar_init(&bar.full[i], 8);   // the warps that unpack
+            mbar_init(&bar.full[i], C::kJoint ? 9 : 8);  // the warps that unpack, and the token rows
             mbar_init(&bar.empty[i], 2);  // the products of both halves
         }
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.tok_full[i], 1);
-            mbar_init(&bar.tok_empty[i], 2 * C::kPair);
+            mbar_init(&bar.tok_empty[i], 2 * C::kPair);  // the products of both halves of both CTAs
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.acc_full[i], 2);
@@ -623,40 +626,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
             const int n16 = (pl.n + 15) & ~15;
-            const int k_end = min(m.K, 256 * item.u1);
-            for (int k = 256 * item.u0; k < k_end; k += C::kStageK, ++kt) {
+            for (int k = 256 * item.u0; k < 256 * item.u1; k += C::kStageK) {
+                if (!C::kJoint && k >= m.K) break;
                 const int stage = kt % C::kTokenStages;
-                if (kt >= C::kTokenStages) ok = warp_wait(&bar.tok_empty[stage], (kt / C::kTokenStages - 1) & 1, err);
+                uint64_t* const full = C::kJoint ? &bar.full[stage] : &bar.tok_full[stage];
+                uint64_t* const empty = C::kJoint ? &bar.empty[stage] : &bar.tok_empty[stage];
+                if (kt >= C::kTokenStages) ok = warp_wait(empty, (kt / C::kTokenStages - 1) & 1, err);
                 if (!ok) break;
-                const bool both = F32 || k + 64 < k_end;  // (the last 64 elements of a row may be a stage)
-                if (lane == 0) mbar_arrive_expect_tx(&bar.tok_full[stage], (both ? 2 : 1) * n16 * 128);
+                const int parts = k >= m.K ? 0 : F32 || k + 64 < m.K ? 2 : 1;  // (a row's last stage may be half one, or none)
+                if (lane == 0) mbar_arrive_expect_tx(full, parts * n16 * 128);
                 __syncwarp();
                 // Lane i: 16 rows; of a pair's CTAs one takes the even ones, one the odd ones.
                 uint8_t* dst = tok + stage * C::kTokenBytes + lane * 2048;
-                if (16 * lane < n16 && (C::kPair == 1 || (lane & 1) == rank)) {
+                if (16 * lane < n16 && parts > 0 && (C::kPair == 1 || (lane & 1) == rank)) {
                     const int p = pl.p0 + 16 * lane;
                     const CUtensorMap* second = F32 ? &map_lo : &map_hi;
                     const int k2 = F32 ? k : k + 64;
                     if constexpr (C::kPair > 1) {
-                        tma_load_2d_pair(dst, &map_hi, k, p, &bar.tok_full[stage]);
-                        if (both) tma_load_2d_pair(dst + C::kTokens * 128, second, k2, p, &bar.tok_full[stage]);
+                        tma_load_2d_pair(dst, &map_hi, k, p, full);
+                        if (parts > 1) tma_load_2d_pair(dst + C::kTokens * 128, second, k2, p, full);
                     } else {
-                        tma_load_2d(dst, &map_hi, k, p, &bar.tok_full[stage]);
-                        if (both) tma_load_2d(dst + C::kTokens * 128, second, k2, p, &bar.tok_full[stage]);
+                        tma_load_2d(dst, &map_hi, k, p, full);
+                        if (parts > 1) tma_load_2d(dst + C::kTokens * 128, second, k2, p, full);
                     }
                 }
                 __syncwarp();
+                ++kt;
             }
         }
         for (uint32_t i = kt > C::kTokenStages ? kt - C::kTokenStages : 0; !ok && i < kt; ++i)
-            mbar_wait_bounded(&bar.tok_full[i % C::kTokenStages], (i / C::kTokenStages) & 1, err);
+            mbar_wait_bounded(C::kJoint ? &bar.full[i % C::kStages] : &bar.tok_full[i % C::kTokenStages], (i / C::kTokenStages) & 1, err);
     } else {
         // ---- products of a half of the weight rows
         const uint32_t lead = elect_one();
         const int half = warp - kMmaWarp;
         bool ok = true;
         uint32_t sums = 0, stage = 0, round = 0;  // sets of sums, stages of weights
-        uint32_t t_stage = 0, t_round = 0;        // stages of tokens
+        [[maybe_unused]] uint32_t t_stage = 0, t_round = 0;  // stages of tokens
         const uint64_t b_first = desc_base(smem_addr(tok), 16);
         const uint32_t d_half = tmem + half * C::kTokens, w_half = tmem + C::kTmemA + half * 64;
         while (ok && next_item(plan, cur, &item)) {
@@ -671,11 +677,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     d = d_half + (sums % C::kSums) * 2 * C::kTokens;
                     acc = 0;
                 }
-                if (k < m.K) ok = ok && warp_wait(&bar.tok_full[t_stage], t_round & 1, &bar.full[stage], round & 1, err);
+                if (!C::kJoint && k < m.K) ok = ok && warp_wait(&bar.tok_full[t_stage], t_round & 1, &bar.full[stage], round & 1, err);
                 else ok = ok && warp_wait(&bar.full[stage], round & 1, err);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t b = b_first + t_stage * (C::kTokenBytes >> 4);
+                const uint64_t b = b_first + (C::kJoint ? stage : t_stage) * (C::kTokenBytes >> 4);
                 const uint32_t w = w_half + stage * 128;
                 constexpr uint32_t kSecond = C::kTokens * 128 >> 4;
                 auto step = [&](int s, uint32_t add) {
@@ -700,10 +706,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc = 1;
                 mma_commit(&bar.empty[stage], lead);
                 if (++stage == C::kStages) stage = 0, ++round;
-                if (k < m.K) {
-                    if constexpr (C::kPair > 1) mma_commit_pair(&bar.tok_empty[t_stage], lead);
-                    else mma_commit(&bar.tok_empty[t_stage], lead);
-                    if (++t_stage == C::kTokenStages) t_stage = 0, ++t_round;
+                if constexpr (!C::kJoint) {
+                    if (k < m.K) {
+                        mma_commit_pair(&bar.tok_empty[t_stage], lead);
+                        if (++t_stage == C::kTokenStages) t_stage = 0, ++t_round;
+                    }
                 }
                 if (k + C::kStageK == k_end || (F32 && k % 256 == 192)) {
                     mma_commit(&bar.acc_full[sums % C::kSums], lead);
