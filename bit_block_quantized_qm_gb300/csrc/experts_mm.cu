@@ -11,9 +11,10 @@
 // scales from 2^-10 up out of f16's subnormal numbers.  Token rows come as f16 pieces of
 // x times a power of two that takes the row's largest value to 2^13 .. 2^14 (one piece
 // holds a bf16 row's 8 bits, two an f32 row's 22).  f32 rows take three products, the
-// fourth being 2^-22 of the first.  Tensor cores cut sums off instead of rounding them: 48
-// additions (a unit of three products) cost 8e-7 of a sum of mixed signs, so f32 rows' sums
-// go to registers after every unit and are added there; bf16 rows' stay in TMEM.  The element order inside a block of 32 is that in
+// fourth being 2^-22 of the first.  Tensor cores cut sums off instead of rounding them, each
+// addition by 2^-26 of the sum and more (256 of them 4e-6), so f32 rows' large products have
+// sums apart from the small ones', and go to registers after every unit (16 additions) to be
+// added there; bf16 rows' stay in TMEM.  The element order inside a block of 32 is that in
 // which quants unpack, in weights and pieces alike.
 //
 // Weights never lie unpacked in shared memory: raw Q4_0 rows come by TMA, 256 elements
@@ -56,17 +57,25 @@ constexpr float kWeightUnit = 0x1p-8f;
 
 template <bool F32, int TOKENS, bool WIDE>
 struct Cfg {
-    static constexpr int kTokens = TOKENS;              // token rows of a tile
-    static constexpr int kSums = kTokens > 32 ? 1 : 2;  // sets of sums in TMEM
-    static constexpr int kChunk = kTokens > 32 ? 16 : 8;  // columns of sums that a thread has at a time
+    static constexpr int kTokens = TOKENS;  // token rows of a tile
+    // Columns of a half's sums.  F32: the second pieces' products are columns of their own beside the
+    // first ones', so that a product with both is one instruction.
+    static constexpr int kColumns = F32 ? 2 * kTokens : kTokens;
+    static constexpr int kSums = F32 || kTokens > 32 ? 1 : 2;     // sets of sums in TMEM
+    static constexpr int kChunk = kTokens > 32 ? 16 : 8;          // columns of sums that a thread has at a time
+    // The warps that unpack and keep sums get registers from the others: what the CTA has at launch,
+    // 20 * 96 a lane, is 16 * 112 + 4 * 32.
+    static constexpr bool kMoveRegs = F32 && kTokens > 32;
+    static constexpr int kLaunchRegs = 96, kDecodeRegs = 112, kOtherRegs = 32;
+    static_assert(kDecodeWarps * kDecodeRegs + 4 * kOtherRegs <= 20 * kLaunchRegs, "a warp would wait for ever");
     // CTAs come in pairs that take the same token rows (and blocks of weights next to each other):
     // each loads half of them for both.
-    static constexpr int kPair = kTokens > 32 ? 2 : 1;
+    static constexpr int kPair = !F32 && kTokens > 32 ? 2 : 1;
     // Stages of unpacked weights, 128 columns of TMEM (bf16 rows: 128 elements, f32 rows: 64), and of
     // the token rows that they meet.  Long ones, because an issuing warp takes 300 cycles and more for a
     // stage besides its products.
     static constexpr int kStageK = F32 ? 64 : 128;
-    static constexpr int kTmemA = kSums * 2 * kTokens;  // (the sums come first)
+    static constexpr int kTmemA = kSums * 2 * kColumns;  // (the sums come first)
     static constexpr int kStages = (512 - kTmemA) / 128;
     static constexpr int kPitch = WIDE ? 176 : 144;  // bytes of a raw row in shared memory, an odd number of 16s
     static constexpr int kRawBytes = 2 * kHalf * kPitch;
@@ -75,7 +84,7 @@ struct Cfg {
     // stages of their own, further ahead.
     static constexpr bool kJoint = kPair == 1;
     static constexpr int kTokenStages = kJoint ? kStages : WIDE ? 2 : 3;
-    static constexpr int kRawStages = WIDE || kTokens > 32 ? 3 : 4;
+    static constexpr int kRawStages = WIDE || kPair > 1 ? 3 : 4;
     static constexpr int kSmem = kRawStages * kRawBytes + kTokenStages * kTokenBytes + 1024;
     static_assert(kTmemA % 128 == 0 && kStages >= 2, "room for the weights");
 };
@@ -147,14 +156,14 @@ __device__ __forceinline__ Cursor first_item(const Plan& p) {
 __device__ __forceinline__ bool next_item(const Plan& p, Cursor& c, Item* item) {
     if (c.at < c.end) {
         const int t = c.at / p.ku;
-        item->tile = p.full + t;
-        item->u0 = c.at - t * p.ku;
-        item->u1 = min(p.ku, item->u0 + (c.end - c.at));
+        item->tile = uniform(p.full + t);
+        item->u0 = uniform(c.at - t * p.ku);
+        item->u1 = uniform(min(p.ku, item->u0 + (c.end - c.at)));
         c.at += item->u1 - item->u0;
         return true;
     }
     if (c.next >= (p.share ? p.full : p.tiles)) return false;
-    *item = {c.next, 0, p.ku};
+    *item = {uniform(c.next), 0, uniform(p.ku)};
     c.next += p.ctas;
     return true;
 }
@@ -164,6 +173,11 @@ struct Place {
     int expert, block, p0, n;
 };
 
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_ldn(uint32_t addr, float (&v)[16]) { tmem_ld16(addr, v); }
 __device__ __forceinline__ void tmem_ldn(uint32_t addr, float (&v)[8]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -172,15 +186,15 @@ __device__ __forceinline__ void tmem_ldn(uint32_t addr, float (&v)[8]) {
                  : "r"(addr));
 }
 
-// A block of a weight row, number `b` of the two that words 0 .. 8 (36 bytes) hold, in the order in
-// which its quants unpack; F32: with the second pieces.
-template <bool F32>
+// Quant words K0 .. K0 + N - 1 (of 4) of a block of a weight row, number `b` of the two that words 0 .. 8
+// (36 bytes) hold, in the order in which quants unpack; F32: with the second pieces.
+template <bool F32, int K0 = 0, int N = 4>
 __device__ __forceinline__ void unpack_block(const uint32_t (&w)[9], int b, uint32_t k1024, uint32_t* h, uint32_t* l) {
     const uint32_t d_bits = __byte_perm(b ? w[4] : w[0], 0, b ? 0x3232 : 0x1010);
     const __half2 d = __hmul2(half2_of(d_bits), half2_of(0x5C005C00u));  // times 2^8
     const __half2 m1032 = half2_of(0xE408E408u), sixteenth = half2_of(0x2C002C00u), m72 = half2_of(0xD480D480u);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = K0; k < K0 + N; ++k) {
         const uint32_t q = b ? w[5 + k] : __byte_perm(w[k], w[k + 1], 0x5432);
         const uint32_t y = q >> 8;
         const __half2 n[4] = {__hadd2(half2_of((q & 0x000F000Fu) | k1024), m1032),
@@ -190,8 +204,8 @@ __device__ __forceinline__ void unpack_block(const uint32_t (&w)[9], int b, uint
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const __half2 x = __hmul2(n[e], d);
-            h[4 * k + e] = word(x);
-            if (F32) l[4 * k + e] = word(__hfma2(n[e], d, __hneg2(x)));
+            h[4 * (k - K0) + e] = word(x);
+            if (F32) l[4 * (k - K0) + e] = word(__hfma2(n[e], d, __hneg2(x)));
         }
     }
 }
@@ -236,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int rows_before[1024 + 1];   // their sorted rows
     __shared__ alignas(16) float units[3][C::kTokens];  // of the columns of this tile, the one before and the one after
     __shared__ int last_of_tile;
+    __shared__ Plan plan;  // (not in registers, of which there are few)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* const err = m.err;
 
@@ -300,14 +315,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int block_rows = two ? kHalf : 2 * kHalf;
     const int blocks = (m.rows + block_rows * C::kPair - 1) / (block_rows * C::kPair);  // (of a pair)
     const int rank = C::kPair > 1 ? static_cast<int>(blockIdx.x & 1) : 0;
-    Plan plan;
-    plan.tiles = uniform(tiles_before[m.n]) * blocks;
-    plan.ctas = gridDim.x / C::kPair;
-    plan.cta = blockIdx.x / C::kPair;
-    plan.ku = (m.K + 255) / 256;
-    plan.full = plan.tiles / plan.ctas * plan.ctas;
-    plan.rest = plan.tiles - plan.full;
-    plan.share = plan.rest > 0 && plan.rest * 8 <= plan.ctas * 7 && plan.ku > 1;
+    if (threadIdx.x == 0) {
+        Plan p;
+        p.tiles = tiles_before[m.n] * blocks;
+        p.ctas = gridDim.x / C::kPair;
+        p.cta = blockIdx.x / C::kPair;
+        p.ku = (m.K + 255) / 256;
+        p.full = p.tiles / p.ctas * p.ctas;
+        p.rest = p.tiles - p.full;
+        p.share = p.rest > 0 && p.rest * 8 <= p.ctas * 7 && p.ku > 1;
+        plan = p;
+    }
+    __syncthreads();
     auto place = [&](int tile) {
         const int tt = tile / blocks;
         int lo = 0, hi = m.n;  // the first expert with tiles_before[e + 1] > tt
@@ -329,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kDecodeWarps) {
         // ---- unpacking, then the outputs
+        if constexpr (C::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kDecodeRegs));
         const int group = warp >> 2, half = group & 1, ph = group >> 1;
         const int r = 32 * (warp & 3) + lane;  // this thread's weight row of the half, and its TMEM lane
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -354,23 +374,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar.acc_empty[sums % C::kSums]);
             ++sums;
         };
-        // F32: adds the sums of a unit to those of the units before it.
+        // F32: adds the sums of a unit (of `n` rows) to those of the units before it.
         auto collect = [&](int n) {
             wait_sums();
             if constexpr (F32) {
                 if (kChunk * group < n) {
-                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kTokens + kChunk * group;
-                    float a[kChunk], b[kChunk];
-                    tmem_ldn(d, a);
-                    tmem_ldn(d + C::kTokens, b);
-                    tc_wait_ld();
+                    const uint32_t d = tmem + lanes + kChunk * group;
+                    const int second = (n + 15) & ~15;  // where the products with the second pieces are
+                    auto add = [&](float(&v)[kChunk], uint32_t from) {
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) v0[i] += a[i], v1[i] += b[i];
+                        for (int e0 = 0; e0 < kChunk; e0 += 8) {
+                            float a[8], b[8];
+                            tmem_ldn(from + e0, a);
+                            tmem_ldn(from + second + e0, b);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e0 + e] += a[e] + b[e];
+                        }
+                    };
+                    add(v0, d);
+                    add(v1, d + C::kColumns);
                 }
             }
             free_sums();
         };
-        auto unpack_unit = [&](int u) {
+        auto unpack_unit = [&](int u, int n_before) {
             const int stage = it % C::kRawStages;
             ok = ok && warp_wait(&bar.raw_full[stage], (it / C::kRawStages) & 1, err);
             ++it;
@@ -402,21 +430,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[9];
             if constexpr (F32) {  // the unit's 64 elements number ph, then ph + 2
                 auto unpack_64 = [&](bool there) {
-                    uint32_t h[16], l[16];
-                    unpack_block<true>(w, 0, m.k1024, h, l);
+                    uint32_t h[8], l[8];
+                    unpack_block<true, 0, 2>(w, 0, m.k1024, h, l);
                     begin_stage();
                     const uint32_t at = a_cols + a_stage * 128;
                     if (there) {
-                        tmem_st16(at, h);
-                        tmem_st16(at + 32, l);
-                        unpack_block<true>(w, 1, m.k1024, h, l);
-                        tmem_st16(at + 16, h);
-                        tmem_st16(at + 48, l);
+                        tmem_st8(at, h);
+                        tmem_st8(at + 32, l);
+                        unpack_block<true, 2, 2>(w, 0, m.k1024, h, l);
+                        tmem_st8(at + 8, h);
+                        tmem_st8(at + 40, l);
+                        unpack_block<true, 0, 2>(w, 1, m.k1024, h, l);
+                        tmem_st8(at + 16, h);
+                        tmem_st8(at + 48, l);
+                        unpack_block<true, 2, 2>(w, 1, m.k1024, h, l);
+                        tmem_st8(at + 24, h);
+                        tmem_st8(at + 56, l);
                     }
                     end_stage();
                 };
                 load(I{}, std::integral_constant<int, 1>{}, w);
                 unpack_64(64 * ph < left);
+                if (n_before) collect(n_before);  // (of the unit before: there is one set of sums)
                 load(std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{}, w);
                 done_with_row();
                 unpack_64(64 * (ph + 2) < left);
@@ -439,8 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A tile's outputs, once all of its products are done.
         auto outputs = [&](int tile, int n_units, uint32_t mine_buf) {
             const Place pl = place(tile);
-            if constexpr (F32) collect(pl.n);
-            else wait_sums();
+            if constexpr (!F32) wait_sums();
             named_barrier_sync(2, kDecodeWarps * 32);  // the factors and pairs are there
             const bool whole = n_units == plan.ku;
             const int f0 = pl.block * block_rows + r, f1 = two ? f0 : f0 + kHalf;
@@ -485,9 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto load_sums = [&](int ch) {
                 if constexpr (!F32) {
-                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kTokens + kChunk * ch;
+                    const uint32_t d = tmem + lanes + (sums % C::kSums) * 2 * C::kColumns + kChunk * ch;
                     tmem_ldn(d, v0);
-                    tmem_ldn(d + C::kTokens, v1);
+                    tmem_ldn(d + C::kColumns, v1);
                     tc_wait_ld();
                 }
             };
@@ -552,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // Unit by unit.  A tile's outputs wait until the next tile's first unit is unpacked, so that the
         // products of that one can begin as soon as there is room for its sums.
-        int done_tile = 0, done_units = 0, n_now = 0;
+        int done_tile = 0, done_units = 0, n_now = 0, n_due = 0;
         uint32_t buf = 0, buf_done = 0;  // of 3 sets of factors: a warp may be two tiles ahead of another's outputs
         bool more = next_item(plan, cur, &item), due = false;
         int u = 0;
@@ -574,11 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         while (more || due) {
             if (more) {
-                unpack_unit(u);
-                if constexpr (F32)
-                    if (u > item.u0) collect(n_now);  // of the unit before
+                unpack_unit(u, u > item.u0 ? n_now : due ? n_due : 0);
             }
             if (due) {
+                if (F32 && !more) collect(n_due);
                 outputs(done_tile, done_units, buf_done);
                 due = false;
                 if constexpr (F32) {
@@ -587,13 +620,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (more && ++u == item.u1) {
+                n_due = n_now;
                 done_tile = item.tile, done_units = item.u1 - item.u0, buf_done = buf;
                 due = true;
                 more = next_item(plan, cur, &item);
                 if (more) begin();
             }
         }
-    } else if (warp == kRawWarp) {
+    } else {
+    if constexpr (C::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if (warp == kRawWarp) {
         // ---- raw weights
         bool ok = true;
         uint32_t it = 0;
@@ -647,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (parts > 1) tma_load_2d_pair(dst + C::kTokens * 128, second, k2, p, full);
                     } else {
                         tma_load_2d(dst, &map_hi, k, p, full);
-                        if (parts > 1) tma_load_2d(dst + C::kTokens * 128, second, k2, p, full);
+                        if (parts > 1) tma_load_2d(dst + (F32 ? n16 : C::kTokens) * 128, second, k2, p, full);
                     }
                 }
                 __syncwarp();
@@ -664,17 +700,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sums = 0, stage = 0, round = 0;  // sets of sums, stages of weights
         [[maybe_unused]] uint32_t t_stage = 0, t_round = 0;  // stages of tokens
         const uint64_t b_first = desc_base(smem_addr(tok), 16);
-        const uint32_t d_half = tmem + half * C::kTokens, w_half = tmem + C::kTmemA + half * 64;
+        const uint32_t d_half = tmem + half * C::kColumns, w_half = tmem + C::kTmemA + half * 64;
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
-            const uint32_t id = idesc_f16((pl.n + 15) & ~15, false);
+            const int n16 = (pl.n + 15) & ~15;
+            const uint32_t id = idesc_f16(n16, false), id_both = idesc_f16(F32 ? 2 * n16 : n16, false);
             const int k_begin = 256 * item.u0, k_end = 256 * item.u1;
             uint32_t acc = 0, d = d_half;
             for (int k = k_begin; k < k_end && ok; k += C::kStageK) {
                 if (k == k_begin || (F32 && k % 256 == 0)) {  // a set of sums: F32 a unit's, else the item's
                     if (sums >= C::kSums)
                         ok = warp_wait(&bar.acc_empty[sums % C::kSums], (sums / C::kSums - 1) & 1, err);
-                    d = d_half + (sums % C::kSums) * 2 * C::kTokens;
+                    d = d_half + (sums % C::kSums) * 2 * C::kColumns;
                     acc = 0;
                 }
                 if (!C::kJoint && k < m.K) ok = ok && warp_wait(&bar.tok_full[t_stage], t_round & 1, &bar.full[stage], round & 1, err);
@@ -683,14 +720,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint64_t b = b_first + (C::kJoint ? stage : t_stage) * (C::kTokenBytes >> 4);
                 const uint32_t w = w_half + stage * 128;
-                constexpr uint32_t kSecond = C::kTokens * 128 >> 4;
                 auto step = [&](int s, uint32_t add) {
                     if constexpr (F32) {
-                        mma_ts(d, w + 8 * s, b + 2 * s, id, add, lead);
-                        mma_ts(d, w + 8 * s, b + kSecond + 2 * s, id, 1, lead);
-                        mma_ts(d, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
+                        mma_ts(d, w + 8 * s, b + 2 * s, id_both, add, lead);
+                        mma_ts(d + n16, w + 32 + 8 * s, b + 2 * s, id, 1, lead);
                     } else {
-                        mma_ts(d, w + 8 * s, b + (s >> 2) * kSecond + 2 * (s & 3), id, add, lead);
+                        mma_ts(d, w + 8 * s, b + (s >> 2) * (C::kTokens * 128 >> 4) + 2 * (s & 3), id, add, lead);
                     }
                 };
                 if (k + C::kStageK <= m.K) {
@@ -724,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_wait(&bar.acc_full[sums % C::kSums], (sums / C::kSums) & 1, err);
         }
     }
+    }
 
     tc_fence_before();
     __syncthreads();
@@ -750,7 +786,7 @@ cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, const void* 
                           int64_t n_pieces, const DeviceInfo& dev, cudaStream_t stream) {
     using C = Cfg<F32, TOKENS, WIDE>;
     static SmemOnce once;
-    cudaError_t err = once.set(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, C::kSmem);
+    cudaError_t err = once.set(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, C::kSmem, C::kMoveRegs ? C::kLaunchRegs : 0);
     if (err != cudaSuccess) return err;
     const int64_t row_bytes = m.K / 32 * 18;
     const int together = WIDE ? 16 / static_cast<int>(row_bytes & -row_bytes) : 1;
@@ -787,9 +823,11 @@ cudaError_t launch_experts_mm(const ExpertsMm& m, const ExpertsView& e, bool dow
         if (down) return wide ? run(launch_kernel<kF32, kTokens, true, true>) : run(launch_kernel<kF32, kTokens, true, false>);
         return wide ? run(launch_kernel<kF32, kTokens, false, true>) : run(launch_kernel<kF32, kTokens, false, false>);
     };
-    if (type == KvType::kF32) return go(std::true_type{}, std::integral_constant<int, 32>{});
-    // Narrow tiles where experts have few rows: two sets of sums, and three stages of weights.
-    if (n_pieces <= 16 * static_cast<int64_t>(e.n)) return go(std::false_type{}, std::integral_constant<int, 32>{});
+    // Narrow tiles where experts have few rows: three stages of weights, bf16 rows two sets of sums.
+    const bool narrow = n_pieces <= 16 * static_cast<int64_t>(e.n);
+    if (type == KvType::kF32)
+        return narrow ? go(std::true_type{}, std::integral_constant<int, 32>{}) : go(std::true_type{}, std::integral_constant<int, 64>{});
+    if (narrow) return go(std::false_type{}, std::integral_constant<int, 32>{});
     return go(std::false_type{}, std::integral_constant<int, kExpertTokens>{});
 }
 
