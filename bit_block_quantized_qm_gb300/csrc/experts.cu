@@ -45,42 +45,38 @@ Parts layout(const ExpertsView& e, int64_t n_tokens, int64_t top_k) {
     return p;
 }
 
-// How many of the pairs 0 .. pairs - 1 have experts below e, and how many of the threads'
-// ranges up to this thread's own have e: every thread goes over a range of consecutive ids.
+// How many of the pairs 0 .. pairs - 1 have experts below e, and how many e in the ranges of
+// the warps before this one: every warp goes over a range of consecutive ids, 32 at a time.
 struct Ranks {
-    int lo, hi;        // this thread's range
-    int below, mine;   // of all pairs; of its range
-    int before;        // pairs of e in lower threads' ranges
-    bool range;        // an id of its range is no expert's
+    int lo, hi;      // this warp's range
+    int below, all;  // pairs of lower experts; pairs of e
+    int before;      // pairs of e in lower warps' ranges
+    bool range;      // an id of its lane's is no expert's
 };
 __device__ __forceinline__ Ranks rank_pairs(int e, const int32_t* ids, int pairs, int n) {
-    __shared__ int sums[2][kSetupThreads / 32];
+    constexpr int kWarps = kSetupThreads / 32;
+    __shared__ int sums[2][kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Ranks r;
-    const int each = (pairs + kSetupThreads - 1) / kSetupThreads;
-    r.lo = min(pairs, static_cast<int>(threadIdx.x) * each), r.hi = min(pairs, r.lo + each);
-    int below = 0;
-    r.mine = 0;
+    const int each = (pairs + kSetupThreads - 1) / kSetupThreads * 32;
+    r.lo = min(pairs, warp * each), r.hi = min(pairs, r.lo + each);
+    int below = 0, mine = 0;
     r.range = false;
-    for (int i = r.lo; i < r.hi; ++i) {
+#pragma unroll 8
+    for (int i = r.lo + lane; i < r.hi; i += 32) {
         const int id = ids[i];
         below += id >= 0 && id < e;
-        r.mine += id == e;
+        mine += id == e;
         r.range |= id >= n;
     }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int upto = r.mine;  // of this warp's lanes up to this one
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(kAll, upto, d);
-        if (lane >= d) upto += v;
-    }
     below = __reduce_add_sync(kAll, below);
-    if (lane == 31) sums[0][warp] = upto;
-    if (lane == 0) sums[1][warp] = below;
+    mine = __reduce_add_sync(kAll, mine);
+    if (lane == 0) sums[0][warp] = mine, sums[1][warp] = below;
     __syncthreads();
-    constexpr int kWarps = kSetupThreads / 32;
+    const int m = lane < kWarps ? sums[0][lane] : 0;
     r.below = __reduce_add_sync(kAll, lane < kWarps ? sums[1][lane] : 0);
-    r.before = __reduce_add_sync(kAll, lane < kWarps && lane < warp ? sums[0][lane] : 0) + upto - r.mine;
+    r.all = __reduce_add_sync(kAll, m);
+    r.before = __reduce_add_sync(kAll, lane < warp ? m : 0);
     return r;
 }
 
@@ -91,19 +87,23 @@ __device__ __forceinline__ void order_pairs(int e, const int32_t* ids, int pairs
                                             int32_t* place, unsigned int* err) {
     const Ranks r = rank_pairs(e, ids, pairs, n);
     if (r.range && e == 0) atomicOr(err, kErrRange);
+    const int lane = threadIdx.x & 31;
     int at = r.below + r.before;
-    if (r.mine || e == 0)
-        for (int i = r.lo; i < r.hi; ++i) {
-            const int id = ids[i];
-            if (id == e) {
-                order[at] = i;
-                place[i] = at++;
-            } else if (e == 0 && (id < 0 || id >= n)) {
-                place[i] = -1;
-            }
+#pragma unroll 4
+    for (int i0 = r.lo; i0 < r.hi; i0 += 32) {
+        const int i = i0 + lane, id = i < r.hi ? ids[i] : -2;
+        const unsigned here = __ballot_sync(kAll, id == e);
+        if (id == e) {
+            const int p = at + __popc(here & ((1u << lane) - 1u));
+            order[p] = i;
+            place[i] = p;
+        } else if (e == 0 && i < r.hi && (id < 0 || id >= n)) {
+            place[i] = -1;
         }
+        at += __popc(here);
+    }
     if (threadIdx.x == 0) starts[e] = r.below;
-    if (threadIdx.x == kSetupThreads - 1 && e == n - 1) starts[n] = r.below + r.before + r.mine;
+    if (threadIdx.x == 0 && e == n - 1) starts[n] = r.below + r.all;
 }
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -252,9 +252,11 @@ __global__ void __launch_bounds__(kSetupThreads)
     __shared__ int own;
     const Ranks r = rank_pairs(e, c.ids, pairs, n);
     if (r.lo <= pair && pair < r.hi) {
-        int p = r.below + r.before;
-        for (int i = r.lo; i < pair; ++i) p += c.ids[i] == e;
-        own = p;
+        const int lane = threadIdx.x & 31;
+        int p = 0;
+        for (int i = r.lo + lane; i < pair; i += 32) p += c.ids[i] == e;
+        p = __reduce_add_sync(kAll, p);
+        if (lane == 0) own = r.below + r.before + p;
     }
     __syncthreads();
     const int64_t p = own, pitch = piece_pitch(K);

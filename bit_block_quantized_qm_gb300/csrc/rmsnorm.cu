@@ -25,8 +25,22 @@ __device__ __forceinline__ void load8(const float* p, float v[8]) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float v[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
+// 8 elements as they are loaded.
+struct F32x8 {
+    float4 a, b;
+};
+template <typename T>
+struct RawOf {
+    using type = F32x8;
+};
+template <>
+struct RawOf<__nv_bfloat16> {
+    using type = uint4;
+};
+__device__ __forceinline__ void unpack8(const F32x8& r, float v[8]) {
+    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w, v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
+}
+__device__ __forceinline__ void unpack8(const uint4& w, float v[8]) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -85,55 +99,78 @@ __device__ __forceinline__ void store_q8(uint8_t* row, int at, const float v[8],
         q[e] = static_cast<uint16_t>(q8_quant_byte(v[2 * e], d, r) | q8_quant_byte(v[2 * e + 1], d, r) << 8);
 }
 
-// Rows of up to 8 * VEC elements a thread, 16-byte aligned.
+// Rows of up to 8 * VEC elements a thread, 16-byte aligned.  A CTA takes every gridDim.x-th
+// row: it keeps the weights, and asks for the next row's elements before it waits for the sum
+// over the one at hand.
 template <int VEC, typename T>
 __global__ void __launch_bounds__(512) rmsnorm_rows(const NormCall c) {
-    __shared__ float part[32];
+    __shared__ float part[2][32];
     grid_launch_dependents();
-    const int64_t r = blockIdx.x;
     const int stride = blockDim.x * 8;
-    float w[VEC][8];
-    grid_dependency_wait();
-    const T* x = static_cast<const T*>(c.x) + r * c.x_stride;
-    const T* res = static_cast<const T*>(c.residual) + r * c.residual_stride;
-    float v[VEC][8];
-    float squares = 0.f;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const int at = i * stride + threadIdx.x * 8;
-        if (at >= c.width) continue;
-        load8(x + at, v[i]);
-        if (c.residual) {
-            float y[8];
-            load8(res + at, y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] += y[e];
-        }
-        if (c.weight) load8(c.weight + at, w[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) squares = fmaf(v[i][e], v[i][e], squares);
-    }
-    if (c.sum) {
-        T* sum = static_cast<T*>(c.sum) + r * c.sum_stride;
+    float w[VEC][8], v[VEC][8];
+    using Raw = typename RawOf<T>::type;
+    Raw x_raw[VEC], r_raw[VEC];
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const int at = i * stride + threadIdx.x * 8;
-            if (at < c.width) store8(sum + at, v[i]);
+            if (at >= c.width) continue;
+            x_raw[i] = *reinterpret_cast<const Raw*>(static_cast<const T*>(c.x) + r * c.x_stride + at);
+            if (c.residual) r_raw[i] = *reinterpret_cast<const Raw*>(static_cast<const T*>(c.residual) + r * c.residual_stride + at);
         }
-    }
-    const float f = row_factor(c, cta_sum(squares, part));
-    T* out = static_cast<T*>(c.out) + r * c.out_stride;
-    uint8_t* q8 = c.q8 + r * (c.width / 32 * 34);
+    };
+    grid_dependency_wait();
+    fetch(blockIdx.x);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const int at = i * stride + threadIdx.x * 8;
-        const bool in = at < c.width;
-        if (in) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * (c.weight ? c.weight_offset + w[i][e] : 1.f);
-            if (c.out) store8(out + at, v[i]);
+        for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
+        if (!c.weight || at >= c.width) continue;
+        load8(c.weight + at, w[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[i][e] += c.weight_offset;
+    }
+    int buf = 0;
+#pragma unroll 1
+    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x, buf ^= 1) {
+        float squares = 0.f;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            if (i * stride + static_cast<int>(threadIdx.x) * 8 >= c.width) continue;
+            unpack8(x_raw[i], v[i]);
+            if (c.residual) {
+                float y[8];
+                unpack8(r_raw[i], y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] += y[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) squares = fmaf(v[i][e], v[i][e], squares);
         }
-        if (c.q8) store_q8(q8, at, v[i], in);
+        if (r + gridDim.x < c.rows) fetch(r + gridDim.x);
+        if (c.sum) {
+            T* sum = static_cast<T*>(c.sum) + r * c.sum_stride;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int at = i * stride + threadIdx.x * 8;
+                if (at < c.width) store8(sum + at, v[i]);
+            }
+        }
+        const float f = row_factor(c, cta_sum(squares, part[buf]));
+        T* out = static_cast<T*>(c.out) + r * c.out_stride;
+        uint8_t* q8 = c.q8 + r * (c.width / 32 * 34);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int at = i * stride + threadIdx.x * 8;
+            const bool in = at < c.width;
+            if (in) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * w[i][e];
+                if (c.out) store8(out + at, v[i]);
+            }
+            if (c.q8) store_q8(q8, at, v[i], in);
+        }
     }
 }
 
@@ -178,7 +215,7 @@ __global__ void __launch_bounds__(512) rmsnorm_any(const NormCall c) {
 }
 
 template <typename T>
-cudaError_t launch_type(const NormCall& c, cudaStream_t stream) {
+cudaError_t launch_type(const NormCall& c, const DeviceInfo& dev, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(c.rows));
     auto fits = [](const void* p, int64_t stride) {
         return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * sizeof(T)) % 16 == 0;
@@ -189,17 +226,22 @@ cudaError_t launch_type(const NormCall& c, cudaStream_t stream) {
                       (!c.out || fits(c.out, one ? 0 : c.out_stride)) && (!c.sum || fits(c.sum, one ? 0 : c.sum_stride)) &&
                       fits(c.weight, 0);
     note_launch();
-    auto threads = [&](int vec) { return dim3((c.width + vec * 256 - 1) / (vec * 256) * 32); };
     if (!fast) return launch_pdl(rmsnorm_any<T>, grid, dim3(512), 0, stream, c);
-    if (c.width <= 512 * 8) return launch_pdl(rmsnorm_rows<1, T>, grid, threads(1), 0, stream, c);
-    if (c.width <= 512 * 16) return launch_pdl(rmsnorm_rows<2, T>, grid, threads(2), 0, stream, c);
-    return launch_pdl(rmsnorm_rows<4, T>, grid, threads(4), 0, stream, c);
+    // Few rows: a thread an element group, a CTA a row.  Many: fewer threads with more in flight,
+    // as many CTAs as the SMs hold at once.
+    const int vec = c.width <= 512 * 8 ? 1 : c.width <= 512 * 16 ? 2 : 4;
+    const int threads = (c.width + vec * 256 - 1) / (vec * 256) * 32;
+    const int64_t resident = static_cast<int64_t>(dev.sm_count) * (2048 / (threads < 64 ? 64 : threads)) * 3 / 4;
+    const dim3 block(threads), rows(static_cast<unsigned>(c.rows < resident ? c.rows : resident));
+    if (vec == 1) return launch_pdl(rmsnorm_rows<1, T>, rows, block, 0, stream, c);
+    if (vec == 2) return launch_pdl(rmsnorm_rows<2, T>, rows, block, 0, stream, c);
+    return launch_pdl(rmsnorm_rows<4, T>, rows, block, 0, stream, c);
 }
 
 }  // namespace
 
-cudaError_t launch_add_rmsnorm(const NormCall& c, const DeviceInfo&, cudaStream_t stream) {
-    return c.type == KvType::kF32 ? launch_type<float>(c, stream) : launch_type<__nv_bfloat16>(c, stream);
+cudaError_t launch_add_rmsnorm(const NormCall& c, const DeviceInfo& dev, cudaStream_t stream) {
+    return c.type == KvType::kF32 ? launch_type<float>(c, dev, stream) : launch_type<__nv_bfloat16>(c, dev, stream);
 }
 
 }  // namespace qm

@@ -4,10 +4,13 @@
 // A warp per token; lane l holds the experts l, l + 32, ...  A choice becomes a
 // 32-bit key whose unsigned order is the choices' order, so that one step of the
 // selection is two warp-wide integer reductions: the largest key, and the lowest
-// expert that has it.  Scores are computed in f32.  Where selected choices, or the
-// groups at the border, lie closer than the scores' error, the row is done again
-// with f64 choices (64-bit keys), so the ids are those of the formula and not of a
-// rounding; without a bias the logits themselves are compared, which is exact.
+// expert that has it.  Scores are computed in f32.  Where selected choices lie closer
+// than the scores' error, those that could change places (a lane each) are put in order
+// by f64 choices (64-bit keys); where groups at the border do, the whole row is done
+// again in f64.  So the ids are those of the formula and not of a rounding; without a
+// bias the logits themselves are compared, which is exact.  (f64 is slow here: a row
+// done again takes some 10 us, and one in a thousand asks for it; with the few of them
+// in order by themselves 4096 tokens, 256 experts in 8 groups take MEASURED.)
 #include <cuda_bf16.h>
 
 #include "qm_device.cuh"
@@ -132,36 +135,66 @@ __device__ __forceinline__ bool drop_groups(const RouteCall& c, const F (&choice
     return close;
 }
 
-// The row's experts, largest choice first: lane j gets the j-th.  With `ordered`
-// not null the key after the last is looked at too and *ordered says whether all of
-// them are more than `near` and 2^-22 of themselves apart.  (Of two of different size
-// the larger counts: an expert masked by a bias of -infinity is far from all others.)
+// The row's experts, largest choice first: lane j gets the j-th.  With `near` not negative
+// (32-bit keys) the next lanes get the ones after the last that could change places with one
+// of them, *n is how many lanes have one, and *ordered says whether all of the first top_k
+// are more than `near` and 2^-22 of themselves apart from each other and from the rest.  (Of
+// two of different size the larger counts: an expert masked by a bias of -infinity is far
+// from all others.)
 template <int PER, typename K>
-__device__ __forceinline__ int select(const RouteCall& c, K (&key)[PER], int lane, float near, bool* ordered) {
+__device__ __forceinline__ int select(const RouteCall& c, K (&key)[PER], int lane, float near, bool* ordered, int* n) {
     int id = 0;
     K last = 0;
-    for (int j = 0; j < c.top_k; ++j) {
+    for (int j = 0; j <= 32; ++j) {
+        if (j >= c.top_k && near < 0.f) break;
         K top;
         int e;
         largest(key, lane, &top, &e);
-        if (lane == j) id = e;
         if constexpr (sizeof(K) == 4) {
-            if (ordered && j > 0 && !apart(last, top, near)) *ordered = false;
+            if (near >= 0.f) {
+                const bool far = j == 0 || !top || apart(last, top, near);
+                if (!far) *ordered = false;
+                if (j >= c.top_k && far) break;
+            }
         }
+        *n = j + 1;
+        if (j == 32) break;
+        if (lane == j) id = e;
         last = top;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (e == 32 * i + lane) key[i] = 0;
     }
-    if constexpr (sizeof(K) == 4) {
-        if (ordered) {
-            K top;
-            int e;
-            largest(key, lane, &top, &e);
-            if (top && !apart(last, top, near)) *ordered = false;
-        }
-    }
     return id;
+}
+
+// The same experts in the order of their f64 choices: lanes 0 .. n - 1 have one each.
+template <int PER, typename T>
+__device__ __noinline__ int order_f64(const RouteCall& c, const T* row, int lane, int id, int n, float mx) {
+    double score;
+    const double x = static_cast<double>(logit(row + id));
+    if (c.sigmoid) {
+        score = 1.0 / (1.0 + exp(-x));
+    } else {
+        double sum = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < PER; ++i) {
+            const int e = 32 * i + lane;
+            if (e < c.experts) sum += exp(static_cast<double>(logit(row + e)) - mx);
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        score = exp(x - mx) / sum;
+    }
+    uint64_t key = lane < n ? key_of(score + static_cast<double>(c.bias[id])) : 0;
+    int sorted = 0;
+    for (int j = 0; j < c.top_k; ++j) {
+        const uint64_t top = warp_max(key);
+        const int e = static_cast<int>(__reduce_min_sync(kAll, key == top && lane < n ? static_cast<unsigned>(id) : kAll));
+        if (lane == j) sorted = e;
+        if (id == e && lane < n) key = 0;
+    }
+    return sorted;
 }
 
 // A row's experts from f64 choices.
@@ -202,7 +235,8 @@ __device__ __noinline__ int select_f64(const RouteCall& c, const T* row, int lan
         if (e < c.experts) key[i] = key_of(c.bias ? choice[i] : static_cast<double>(logit(row + e)));
     }
     if (c.groups > 1) drop_groups(c, choice, key, lane, 0.0);
-    return select(c, key, lane, 0.f, nullptr);
+    int n;
+    return select(c, key, lane, -1.f, nullptr, &n);
 }
 
 template <int PER, typename T>
@@ -263,10 +297,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteCall c) {
         // all of that.
         near = 0x1p-22f * (c.sigmoid ? 4.f * s_top : (9.f + PER) * s_top);
     }
-    if (c.groups > 1) ordered = !drop_groups(c, choice, key, lane, 2.f * near);
+    bool again = false;
+    if (c.groups > 1) again = drop_groups(c, choice, key, lane, 2.f * near);
     // Logits are compared as they are.
-    int id = select(c, key, lane, c.bias ? near : 0.f, c.bias ? &ordered : nullptr);
-    if (!ordered && !bad) id = select_f64<PER>(c, row, lane);
+    int n;
+    int id = select(c, key, lane, c.bias && !again ? near : -1.f, &ordered, &n);
+    if (!bad && (again || (!ordered && n > 32))) id = select_f64<PER>(c, row, lane);
+    else if (!bad && !ordered) id = order_f64<PER>(c, row, lane, id, n, mx);
     // The chosen scores, one per lane.
     float w = 0.f;
     for (int j = 0; j < c.top_k; ++j) {
