@@ -1,9 +1,10 @@
 // The norm that adds the residual (qm_add_rmsnorm).
 //
-// Bound: memory, each input read once and each output written once; few rows:
-// the latency of one load, one reduction over the CTA and one store.  A row belongs
-// to one CTA, whose threads keep their 8 (or 16, 24, 32) elements of it in registers
-// between the sum of squares and the outputs.  Statistics and products are f32;
+// Bound: memory, each input read once and each output written once (8192 rows of 4096
+// bf16 with a residual and both outputs, 268 MB: 42 us, 6.4 TB/s; f32: 80 us, 6.7 TB/s);
+// few rows: the latency of one load, one reduction over the CTA and one store (600 rows:
+// 4 us).  A row belongs to one CTA, whose threads keep their 8 (or 16, 32) elements of it
+// in registers between the sum of squares and the outputs.  Statistics and products are f32;
 // outputs are rounded once.  The row's Q8_0 blocks are made from the f32 values by
 // four lanes a block, as quantize_q8_0 does.
 #include <cuda_bf16.h>
@@ -227,11 +228,17 @@ cudaError_t launch_type(const NormCall& c, const DeviceInfo& dev, cudaStream_t s
                       fits(c.weight, 0);
     note_launch();
     if (!fast) return launch_pdl(rmsnorm_any<T>, grid, dim3(512), 0, stream, c);
-    // Few rows: a thread an element group, a CTA a row.  Many: fewer threads with more in flight,
-    // as many CTAs as the SMs hold at once.
-    const int vec = c.width <= 512 * 8 ? 1 : c.width <= 512 * 16 ? 2 : 4;
+    // Few rows: many threads each, for the latency.  Many rows: fewer threads with more loads on their
+    // way (8192 bf16 rows of 4096: 42 us against 49 with 512 threads), and as many CTAs as the SMs hold
+    // at once, which keep the weights (42 against 46 with a CTA a row; 60000 rows of 128: 17 against 61).
+    // f32 rows of 64 threads or more are better off with a CTA each, whose weights are the smaller part
+    // (8192 rows of 4096: 80 us against 85; 40000 of 512: 52 against 55; 60000 of 128: 61 against 23).
+    const int most = c.rows <= 2 * dev.sm_count ? 512 : 128;
+    const int vec = c.width <= most * 8 ? 1 : c.width <= most * 16 ? 2 : 4;
     const int threads = (c.width + vec * 256 - 1) / (vec * 256) * 32;
-    const int64_t resident = static_cast<int64_t>(dev.sm_count) * (2048 / (threads < 64 ? 64 : threads)) * 3 / 4;
+    const int64_t resident = sizeof(T) == 4 && threads >= 64
+                                 ? c.rows
+                                 : static_cast<int64_t>(dev.sm_count) * (1536 / (threads < 64 ? 64 : threads));
     const dim3 block(threads), rows(static_cast<unsigned>(c.rows < resident ? c.rows : resident));
     if (vec == 1) return launch_pdl(rmsnorm_rows<1, T>, rows, block, 0, stream, c);
     if (vec == 2) return launch_pdl(rmsnorm_rows<2, T>, rows, block, 0, stream, c);
