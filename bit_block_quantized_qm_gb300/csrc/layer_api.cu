@@ -62,7 +62,8 @@ int check_experts(const qm_experts* e, qm::ExpertsView* view, int64_t bytes[3]) 
     const int64_t matrix = e->hidden * e->inner / 32 * 18;
     const int64_t strides[3] = {e->w_gate ? e->gate_stride : matrix, e->up_stride, e->down_stride};
     for (int i = 0; i < 3; ++i) {
-        if (e->n_experts > 1 && (strides[i] < matrix || strides[i] % 16)) return QM_ERR_SHAPE;
+        if (e->n_experts > 1 && (strides[i] < matrix || strides[i] % 16 || strides[i] >= int64_t(1) << 40))
+            return QM_ERR_SHAPE;
         if (!mul_ok(e->n_experts - 1, e->n_experts > 1 ? strides[i] : 0, &bytes[i]) || bytes[i] > INT64_MAX / 2)
             return QM_ERR_SHAPE;
         bytes[i] += matrix;

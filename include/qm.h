@@ -666,7 +666,7 @@ typedef struct qm_experts {
     const void* w_gate; /* or NULL */
     const void* w_up;
     const void* w_down;
-    int64_t gate_stride;
+    int64_t gate_stride; /* bytes, below 2^40 */
     int64_t up_stride;
     int64_t down_stride;
     int64_t hidden; /* a multiple of 32, 32 .. 65536 */

@@ -123,7 +123,7 @@ def test_route_refusals(lib):
 @pytest.mark.parametrize("bad", [dict(hidden=0), dict(hidden=48), dict(hidden=65568), dict(inner=16), dict(inner=100),
                                  dict(inner=-256), dict(n_experts=0), dict(n_experts=1025), dict(activation=3),
                                  dict(activation=-1), dict(up_stride=MATRIX - 16), dict(down_stride=MATRIX + 8),
-                                 dict(gate_stride=0), dict(up_stride=1 << 62), dict(reserved=(ctypes.c_int32 * 2)(0, 1))],
+                                 dict(gate_stride=0), dict(up_stride=1 << 62), dict(down_stride=1 << 40), dict(reserved=(ctypes.c_int32 * 2)(0, 1))],
                          ids=str)
 def test_expert_shapes_refused(lib, bad):
     e = weights(**bad)
