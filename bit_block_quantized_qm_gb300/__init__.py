@@ -840,6 +840,8 @@ def qm_add_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, weight_offs
     code, xs = _matrix(x, "x")
     rows, width = x.shape
     rs = os_ = ss = width
+    if sum_out is not None:
+        ss = _matrix(sum_out, "sum_out", width, x)[1]
     if residual is not None:
         rs = _matrix(residual, "residual", width, x)[1]
         if sum_out is None:
@@ -852,8 +854,6 @@ def qm_add_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, weight_offs
         os_ = _matrix(out, "out", width, x)[1]
     elif want_out:
         out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
-    if sum_out is not None:
-        ss = _matrix(sum_out, "sum_out", width, x)[1]
     if want_q8 or q8_out is not None:
         if width % BLOCK_ELEMS:
             raise ValueError("Q8_0 rows need a width that is a multiple of 32")
@@ -884,14 +884,16 @@ def qm_route_experts(logits, top_k: int, bias=None, scoring: int = QM_SCORE_SOFT
         _require(bias, torch.float32, "bias")
         if bias.numel() != experts:
             raise ValueError("bias must have an element for each expert")
+    for t, dtype, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if t is None:
+            continue
+        _require(t, dtype, name)
+        if tuple(t.shape) != (tokens, top_k):
+            raise ValueError(f"{name} must be [tokens, top_k]")
     if ids is None:
         ids = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
     if weights is None:
         weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
-    for t, dtype, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
-        _require(t, dtype, name)
-        if tuple(t.shape) != (tokens, top_k):
-            raise ValueError(f"{name} must be [tokens, top_k]")
     args = _ROUTE_ARGS.pack(logits.data_ptr(), 0 if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
                             tokens, stride, experts, top_k, n_groups, top_groups, group_top, scoring, 1 if renormalize else 0,
                             scale, code, 0)

@@ -265,15 +265,15 @@ __global__ void __launch_bounds__(kSetupThreads)
 }
 
 // The pairs' tokens as pieces, a sorted row each.
-template <int THREADS, typename T>
-__global__ void __launch_bounds__(THREADS)
+template <typename T>
+__global__ void __launch_bounds__(128)
     experts_split(const ExpertsCall c, int K, const int32_t* starts, const int32_t* order, int n, __half* hi, __half* lo, float* unit) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t p = blockIdx.x, pitch = piece_pitch(K);
     if (p >= starts[n]) return;
     const T* x = static_cast<const T*>(c.x) + static_cast<int64_t>(order[p] / c.top_k) * c.x_stride;
-    split_row<sizeof(T) == 4, THREADS>(x, K, hi + p * pitch, lo + p * pitch, unit + p, NoMend{});
+    split_row<sizeof(T) == 4, 128>(x, K, hi + p * pitch, lo + p * pitch, unit + p, NoMend{});
 }
 
 template <typename T>
@@ -372,10 +372,8 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
     // Few rows take many threads each, for the latency; many few.
     const bool wide = pairs <= 512;
     if (!own_place) {
-        err = wide ? launch_pdl(experts_split<512, T>, dim3(pairs), dim3(512), 0, stream, c, e.hidden, starts, order, e.n, x_hi, x_lo,
-                                floats(at.x_unit))
-                   : launch_pdl(experts_split<128, T>, dim3(pairs), dim3(128), 0, stream, c, e.hidden, starts, order, e.n, x_hi, x_lo,
-                                floats(at.x_unit));
+        err = launch_pdl(experts_split<T>, dim3(pairs), dim3(128), 0, stream, c, e.hidden, starts, order, e.n, x_hi, x_lo,
+                         floats(at.x_unit));
         if (err != cudaSuccess) return err;
         note_launch();
     }
