@@ -13,6 +13,8 @@ namespace qm {
 constexpr int kExpertCtas = 160;
 // Most token rows of a tile of the products.
 constexpr int kExpertTokens = 128;
+constexpr int kExpertHalf = 128;  // weight rows of a half tile
+constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // One of the two products: rows of W (gate and up, or down) with the pieces of token
 // rows, sorted by expert.
@@ -38,6 +40,10 @@ __host__ __device__ inline int64_t piece_pitch(int K) { return (K + 63) / 64 * 6
 cudaError_t launch_experts_mm(const ExpertsMm& m, const ExpertsView& e, bool down, KvType type, const void* hi,
                               const void* lo, int64_t n_pieces, const DeviceInfo& dev, cudaStream_t stream);
 
+// The same for few rows an expert.
+cudaError_t launch_experts_few(const ExpertsMm& m, const ExpertsView& e, KvType type, const void* hi, const void* lo,
+                               const DeviceInfo& dev, cudaStream_t stream);
+
 // EXACT: to a few units of f32; otherwise to about 2^-20.
 template <bool EXACT>
 __device__ __forceinline__ float activate(float a, int kind) {
@@ -45,6 +51,65 @@ __device__ __forceinline__ float activate(float a, int kind) {
     const float z = kind == QM_ACT_SILU ? a : 1.5957691216057308f * (a + 0.044715f * a * a * a);  // tanh(y) = 2 sigmoid(2 y) - 1
     // (The approximate division is off by 2 units, and 0 where the divisor is 2^126 and more.)
     return __fdividef(a, 1.f + (EXACT ? expf(-z) : __expf(-z)));
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, unsigned int* err) {
+    for (uint32_t i = 0; i < kMaxWaitPolls; ++i)
+        if (__all_sync(kAll, mbar_try_wait(a, pa))) return true;
+    atomicOr(err, kErrWaitTimeout);
+    return false;
+}
+// A value (>= 0) that all lanes have, in a uniform register: what is computed from it, and the
+// branches on it, stay warp-uniform for the compiler too.
+__device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce_max_sync(kAll, static_cast<unsigned>(v))); }
+
+// What a CTA does, one piece after the other: tiles, each with a range of units.
+struct Plan {
+    int tiles, full, rest, ku, ctas, cta;  // (of pairs of CTAs where they come in pairs)
+    bool share;  // the tiles left over are shared by all CTAs
+    __device__ __forceinline__ int unit_of(int c) const { return rest * ku * c / ctas; }  // (rest < 160, ku <= 256)
+};
+struct Item {
+    int tile, u0, u1;
+};
+struct Cursor {
+    int next;     // of the whole tiles
+    int at, end;  // units of shared tiles
+};
+__device__ __forceinline__ Cursor first_item(const Plan& p) {
+    Cursor c{p.cta, 0, 0};
+    if (p.share) c.at = p.unit_of(p.cta), c.end = p.unit_of(p.cta + 1);
+    return c;
+}
+// Shared tiles first: the CTA that comes last to one has others to go on with.
+__device__ __forceinline__ bool next_item(const Plan& p, Cursor& c, Item* item) {
+    if (c.at < c.end) {
+        const int t = c.at / p.ku;
+        item->tile = uniform(p.full + t);
+        item->u0 = uniform(c.at - t * p.ku);
+        item->u1 = uniform(min(p.ku, item->u0 + (c.end - c.at)));
+        c.at += item->u1 - item->u0;
+        return true;
+    }
+    if (c.next >= (p.share ? p.full : p.tiles)) return false;
+    *item = {uniform(c.next), 0, uniform(p.ku)};
+    c.next += p.ctas;
+    return true;
+}
+
+// Where a tile lies: its expert, its block of weight rows, its token rows.
+struct Place {
+    int expert, block, p0, n;
+};
+
+// A matrix tensor as groups of `together` rows (a multiple of 16 bytes), one box the rows of
+// one number within 128 / together groups.
+inline cudaError_t weight_map(CUtensorMap* map, const uint8_t* w, int64_t stride, int64_t row_bytes, int rows, int n, int together,
+                       int pitch) {
+    const int64_t dims[3] = {row_bytes * together, rows / together, n};
+    const int64_t strides[2] = {row_bytes * together, stride};
+    const int box[3] = {pitch, kExpertHalf / together, 1};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 3, dims, strides, box);
 }
 
 }  // namespace qm

@@ -48,8 +48,7 @@ namespace qm {
 
 namespace {
 
-constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kHalf = 128;  // weight rows of a half tile
+constexpr int kHalf = kExpertHalf;
 constexpr int kDecodeWarps = 16;
 constexpr int kRawWarp = 16, kTokenWarp = 17, kMmaWarp = 18;  // and 19: the products of a half each
 constexpr int kThreads = 20 * 32;
@@ -96,12 +95,7 @@ struct Barriers {
     uint64_t acc_full[2], acc_empty[2];
 };
 
-__device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, unsigned int* err) {
-    for (uint32_t i = 0; i < kMaxWaitPolls; ++i)
-        if (__all_sync(kAll, mbar_try_wait(a, pa))) return true;
-    atomicOr(err, kErrWaitTimeout);
-    return false;
-}
+using qm::warp_wait;
 __device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, unsigned int* err) {
     for (uint32_t i = 0; i < kMaxWaitPolls; ++i) {
         const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
@@ -128,50 +122,6 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t lead) {
         "r"(lead), "h"(static_cast<uint16_t>(3))
         : "memory");
 }
-
-// A value (>= 0) that all lanes have, in a uniform register: what is computed from it, and the
-// branches on it, stay warp-uniform for the compiler too.  An issuing warp whose descriptors go
-// through vector registers takes 48 cycles for a product of 16 columns instead of 9.
-__device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce_max_sync(kAll, static_cast<unsigned>(v))); }
-
-// What a CTA does, one piece after the other: tiles, each with a range of units.
-struct Plan {
-    int tiles, full, rest, ku, ctas, cta;  // (of pairs of CTAs where they come in pairs)
-    bool share;  // the tiles left over are shared by all CTAs
-    __device__ __forceinline__ int unit_of(int c) const { return rest * ku * c / ctas; }  // (rest < 160, ku <= 256)
-};
-struct Item {
-    int tile, u0, u1;
-};
-struct Cursor {
-    int next;     // of the whole tiles
-    int at, end;  // units of shared tiles
-};
-__device__ __forceinline__ Cursor first_item(const Plan& p) {
-    Cursor c{p.cta, 0, 0};
-    if (p.share) c.at = p.unit_of(p.cta), c.end = p.unit_of(p.cta + 1);
-    return c;
-}
-// Shared tiles first: the CTA that comes last to one has others to go on with.
-__device__ __forceinline__ bool next_item(const Plan& p, Cursor& c, Item* item) {
-    if (c.at < c.end) {
-        const int t = c.at / p.ku;
-        item->tile = uniform(p.full + t);
-        item->u0 = uniform(c.at - t * p.ku);
-        item->u1 = uniform(min(p.ku, item->u0 + (c.end - c.at)));
-        c.at += item->u1 - item->u0;
-        return true;
-    }
-    if (c.next >= (p.share ? p.full : p.tiles)) return false;
-    *item = {uniform(c.next), 0, uniform(p.ku)};
-    c.next += p.ctas;
-    return true;
-}
-
-// Where a tile lies: its expert, its block of weight rows, its token rows.
-struct Place {
-    int expert, block, p0, n;
-};
 
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
@@ -769,16 +719,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (C::kPair > 1) cluster_sync_all();
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-}
-
-// A matrix tensor as groups of `together` rows (a multiple of 16 bytes), one box the rows of
-// one number within 128 / together groups.
-cudaError_t weight_map(CUtensorMap* map, const uint8_t* w, int64_t stride, int64_t row_bytes, int rows, int n, int together,
-                       int pitch) {
-    const int64_t dims[3] = {row_bytes * together, rows / together, n};
-    const int64_t strides[2] = {row_bytes * together, stride};
-    const int box[3] = {pitch, kHalf / together, 1};
-    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 3, dims, strides, box);
 }
 
 template <bool F32, int TOKENS, bool DOWN, bool WIDE>
