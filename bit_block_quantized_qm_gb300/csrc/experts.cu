@@ -9,8 +9,7 @@ namespace qm {
 
 namespace {
 
-constexpr int kCounters = 256;  // of shared tiles, for each of the two products
-static_assert(kCounters >= kExpertCtas, "a counter for every tile left over");
+constexpr int kCounters = 16 * kExpertCtas;  // of shared tiles (and their warps), for each of the two products
 constexpr int kSetupThreads = 512;
 
 // Where the parts of the workspace are.
@@ -241,8 +240,8 @@ __global__ void __launch_bounds__(kSetupThreads)
     grid_dependency_wait();
     const int pairs = c.n_tokens * c.top_k;
     if (static_cast<int>(blockIdx.x) < n) {
-        if (blockIdx.x == 0) counters[threadIdx.x] = 0;
-        static_assert(2 * kCounters == kSetupThreads, "a counter for each thread");
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < 2 * kCounters; i += kSetupThreads) counters[i] = 0;
         order_pairs(blockIdx.x, c.ids, pairs, n, starts, order, place, c.err);
         return;
     }
@@ -334,14 +333,25 @@ __global__ void __launch_bounds__(128)
     if (at >= e.hidden) return;
     for (int t = blockIdx.y; t < c.n_tokens; t += gridDim.y) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < c.top_k; ++j) {
-            const int64_t pair = static_cast<int64_t>(t) * c.top_k + j;
-            const int p = place[pair];
-            if (p < 0) continue;
-            const float w = c.weights[pair];
-            float4 y = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * e.hidden + at);
-            if (!finite4(y)) y = down_again(e, starts, inner, p, at, y);
-            s.x = fmaf(w, y.x, s.x), s.y = fmaf(w, y.y, s.y), s.z = fmaf(w, y.z, s.z), s.w = fmaf(w, y.w, s.w);
+        constexpr int kAtOnce = 8;  // pairs whose loads are on their way together
+#pragma unroll 1
+        for (int j0 = 0; j0 < c.top_k; j0 += kAtOnce) {
+            const int64_t pair = static_cast<int64_t>(t) * c.top_k + j0;
+            const int n = min(kAtOnce, c.top_k - j0);
+            int p[kAtOnce];
+            float w[kAtOnce];
+            float4 y[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) p[j] = j < n ? place[pair + j] : -1, w[j] = j < n ? c.weights[pair + j] : 0.f;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+                if (p[j] >= 0) y[j] = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p[j]) * e.hidden + at);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                if (p[j] < 0) continue;
+                if (!finite4(y[j])) y[j] = down_again(e, starts, inner, p[j], at, y[j]);
+                s.x = fmaf(w[j], y[j].x, s.x), s.y = fmaf(w[j], y[j].y, s.y), s.z = fmaf(w[j], y[j].z, s.z), s.w = fmaf(w[j], y[j].w, s.w);
+            }
         }
         store4(static_cast<T*>(c.out) + t * c.out_stride + at, s);
     }
@@ -368,8 +378,6 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
                                  e.hidden, starts, order, place, counters, x_hi, x_lo, floats(at.x_unit));
     if (err != cudaSuccess) return err;
     note_launch();
-    // Few rows take many threads each, for the latency; many few.
-    const bool wide = pairs <= 512;
     if (!own_place) {
         err = launch_pdl(experts_split<T>, dim3(pairs), dim3(128), 0, stream, c, e.hidden, starts, order, e.n, x_hi, x_lo,
                          floats(at.x_unit));
@@ -387,7 +395,10 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
                    : launch_experts_mm(m, e, down, c.type, hi, lo, pairs, dev, stream);
     };
     if ((err = products(false, x_hi, x_lo)) != cudaSuccess) return err;
-    err = wide ? launch_pdl(experts_inner<512, T>, dim3(pairs), dim3(512), 0, stream, e, c, inner, starts, order, i_hi, i_lo,
+    // Few rows take many threads each, for the latency, and so do long ones, which stay in registers between
+    // their maximum and their pieces; many short ones few.
+    const bool wide = pairs <= 512;
+    err = wide || e.inner > 4096 ? launch_pdl(experts_inner<512, T>, dim3(pairs), dim3(512), 0, stream, e, c, inner, starts, order, i_hi, i_lo,
                             floats(at.i_unit))
                : launch_pdl(experts_inner<128, T>, dim3(pairs), dim3(128), 0, stream, e, c, inner, starts, order, i_hi, i_lo,
                             floats(at.i_unit));

@@ -66,8 +66,9 @@ __device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce
 // What a CTA does, one piece after the other: tiles, each with a range of units.
 struct Plan {
     int tiles, full, rest, ku, ctas, cta;  // (of pairs of CTAs where they come in pairs)
+    int each, more;  // units of shared tiles that a CTA has, and how many CTAs have one more
     bool share;  // the tiles left over are shared by all CTAs
-    __device__ __forceinline__ int unit_of(int c) const { return rest * ku * c / ctas; }  // (rest < 160, ku <= 256)
+    __device__ __forceinline__ int unit_of(int c) const { return c * each + min(c, more); }  // (without a division: it is cold code)
 };
 struct Item {
     int tile, u0, u1;
@@ -95,6 +96,14 @@ __device__ __forceinline__ bool next_item(const Plan& p, Cursor& c, Item* item) 
     *item = {uniform(c.next), 0, uniform(p.ku)};
     c.next += p.ctas;
     return true;
+}
+
+// What this thread, and those it has met at a barrier, have written before is seen by whoever finds the
+// counter changed.  (A fence of every thread and a plain atomic take some 3 us more.)
+__device__ __forceinline__ unsigned atom_add_acq_rel(unsigned* p, unsigned n) {
+    unsigned before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(before) : "l"(p), "r"(n) : "memory");
+    return before;
 }
 
 // Where a tile lies: its expert, its block of weight rows, its token rows.

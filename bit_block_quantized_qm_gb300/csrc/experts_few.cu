@@ -46,12 +46,12 @@ __device__ __forceinline__ void unpack(uint32_t q, uint32_t k1024, uint32_t (&n)
     n[3] = word(__hfma2(half2_of((y & 0x00F000F0u) | k1024), sixteenth, m72));
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // A lane's two rows of a unit, its blocks 0 .. blocks - 1, with GROUPS x 8 columns.
@@ -74,9 +74,10 @@ __device__ __forceinline__ void unit_sums(const uint8_t* row0, const uint8_t* ro
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             const uint4 x = *reinterpret_cast<const uint4*>(column + g * 8 * kColumnPitch + b * 64 + t * 16);
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(s, n0[0], n1[0], n0[1], n1[1], x.x, x.y);
-            mma16816(s, n0[2], n1[2], n0[3], n1[3], x.z, x.w);
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[4];
+            mma16816(s, zero, n0[0], n1[0], n0[1], n1[1], x.x, x.y);
+            mma16816(s, s, n0[2], n1[2], n0[3], n1[3], x.z, x.w);
             acc[g][0] = fmaf(d0, s[0], acc[g][0]);
             acc[g][1] = fmaf(d0, s[1], acc[g][1]);
             acc[g][2] = fmaf(d1, s[2], acc[g][2]);
@@ -98,7 +99,7 @@ __device__ __forceinline__ void unit_sums(const uint8_t* row0, const uint8_t* ro
         block(b, q0, q1, scale(row0, at - 2), scale(row1, at - 2));
     };
     if (!WIDE || blocks == 8) {
-#pragma unroll
+#pragma unroll 2
         for (int b = 0; b < 8; b += 2) {
             even_block(b);
             odd_block(b + 1);
@@ -110,6 +111,17 @@ __device__ __forceinline__ void unit_sums(const uint8_t* row0, const uint8_t* ro
             if (b + 1 < blocks) odd_block(b + 1);
         }
     }
+}
+
+// A TMA box that is read once: the first to leave L2.
+__device__ __forceinline__ void tma_load_3d_once(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b64 once;\n\t"
+        "createpolicy.fractional.L2::evict_first.b64 once;\n\t"
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], once;\n\t}" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
 }
 
 struct Barriers {
@@ -127,7 +139,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Barriers bar;
     __shared__ int tiles_before[1024 + 1];  // token tiles of all lower experts
     __shared__ int rows_before[1024 + 1];   // their sorted rows
-    __shared__ int last_of_tile;
     __shared__ Plan plan;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* const err = m.err;
@@ -171,6 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.ku = (m.K + 255) / 256;
             p.full = p.tiles / p.ctas * p.ctas;
             p.rest = p.tiles - p.full;
+            p.each = p.rest * p.ku / p.ctas;
+            p.more = p.rest * p.ku - p.each * p.ctas;
             p.share = p.rest > 0 && p.rest * 8 <= p.ctas * 7 && p.ku > 1;
             plan = p;
         }
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int i = lane & 15, half = lane >> 4;
                 if (i < together) {
                     const int row0 = pl.block * block_rows + (two ? 0 : half * kExpertHalf);
-                    tma_load_3d(dst + (half * kExpertHalf + i * (kExpertHalf / together)) * C::kPitch, half ? &map_w1 : &map_w0,
+                    tma_load_3d_once(dst + (half * kExpertHalf + i * (kExpertHalf / together)) * C::kPitch, half ? &map_w1 : &map_w0,
                                 (i * row_bytes & ~15) + 144 * u, row0 / together, pl.expert, &bar.full[stage]);
                 }
                 if (lane < columns)
@@ -244,6 +257,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool odd = shift & 2;
     const int row_at = slot * C::kPitch + (shift & ~3);
     constexpr int kValues = F32 ? 4 : 8;  // sums of a thread: [columns of a group of 8][both halves]
+    const int64_t place_floats = 8 * kWarps * 32;
+    // The sums of a tile, scaled and activated.
+    auto store = [&](const Place& pl, float(&v)[kValues]) {
+        const int f0 = pl.block * block_rows + r, f1 = two ? f0 : f0 + kExpertHalf;
+        const bool in0 = f0 < m.rows, in1 = !two && f1 < m.rows;
+#pragma unroll
+        for (int i = 0; i < kValues; i += 2) {
+            const int c = F32 ? 4 * (i >> 1) + t : 8 * (i >> 2) + 2 * t + (i >> 1 & 1);
+            if (c >= pl.n) continue;
+            const float unit = m.unit[pl.p0 + c];
+            float a = v[i] * unit, b = v[i + 1] * unit;
+            a = activate<F32>(a, m.activation);
+            if (two) a *= b;
+            else b = activate<F32>(b, m.activation);
+            float* out = m.out + static_cast<int64_t>(pl.p0 + c) * m.rows;
+            if (in0) out[f0] = a;
+            if (in1) out[f1] = b;
+        }
+    };
+    // CTA c's part of the shared tile that begins with unit `begin`: the second one where the CTA begins before it.
+    auto part_of = [&](int c, int begin) {
+        return m.split + (2 * c + (plan.unit_of(c) < begin)) * place_floats + threadIdx.x;
+    };
     while (next_item(plan, cur, &item)) {
         const Place pl = place(item.tile);
         const bool many = (F32 ? 2 * pl.n : pl.n) > 8;
@@ -270,52 +306,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 v[4 * c] = acc[c][0], v[4 * c + 1] = acc[c][2], v[4 * c + 2] = acc[c][1], v[4 * c + 3] = acc[c][3];
             }
-        if (item.u1 - item.u0 != plan.ku) {
-            // A part of the tile: kept in this CTA's place.
-            const int shared_tile = item.tile - plan.full;
-            auto part_of = [&](int c) {
-                const int first = plan.unit_of(c) / plan.ku;
-                return m.split + static_cast<int64_t>(2 * c + (shared_tile - first)) * (8 * kWarps * 32) + threadIdx.x;
-            };
-            float* mine = part_of(plan.cta);
+        if (item.u1 - item.u0 == plan.ku) {
+            store(pl, v);
+        } else {
+            float* mine = part_of(plan.cta, (item.tile - plan.full) * plan.ku);
 #pragma unroll
             for (int i = 0; i < kValues; ++i) mine[i * kWarps * 32] = v[i];
-            __threadfence();
-            named_barrier_sync(1, kWarps * 32);
-            if (threadIdx.x == 0) {
-                const unsigned n = static_cast<unsigned>(item.u1 - item.u0);
-                last_of_tile = atomicAdd(&m.counters[shared_tile], n) + n == static_cast<unsigned>(plan.ku);
-                __threadfence();
-            }
-            named_barrier_sync(1, kWarps * 32);
-            if (!last_of_tile) continue;
-            const int total = plan.rest * plan.ku, u_lo = shared_tile * plan.ku;
-            const int c_lo = ((u_lo + 1) * plan.ctas - 1) / total, c_hi = ((u_lo + plan.ku) * plan.ctas - 1) / total;
-#pragma unroll
-            for (int i = 0; i < kValues; ++i) v[i] = 0.f;
-#pragma unroll 2
-            for (int c = c_lo; c <= c_hi; ++c) {
-                if (plan.unit_of(c) == plan.unit_of(c + 1)) continue;
-                const float* part = part_of(c);
-#pragma unroll
-                for (int i = 0; i < kValues; ++i) v[i] += __ldcg(part + i * kWarps * 32);
-            }
         }
-        const int f0 = pl.block * block_rows + r, f1 = two ? f0 : f0 + kExpertHalf;
-        const bool in0 = f0 < m.rows, in1 = !two && f1 < m.rows;
+    }
+    // The parts of shared tiles: a warp's meet those of the same warp of other CTAs, and the warp that comes
+    // last adds them, in the CTAs' order.  Here, behind all of the CTA's copies: among them, whatever goes
+    // to memory and back takes 5 us, and all of the CTA would wait.
+    const int from = plan.share ? plan.unit_of(plan.cta) : 0, to = plan.share ? plan.unit_of(plan.cta + 1) : 0;
+    if (from == to) return;
+    // (A CTA's units are less than a tile's: they are of two tiles at most, which lanes 0 and 1 count in.)
+    const int first_tile = from / plan.ku, begin = (first_tile + lane) * plan.ku;
+    bool last = false;
+    __syncwarp();
+    if (lane < 2 && begin < to) {
+        const unsigned n = static_cast<unsigned>(min(to, begin + plan.ku) - max(from, begin));
+        last = atom_add_acq_rel(&m.counters[(first_tile + lane) * kWarps + warp], n) + n == static_cast<unsigned>(plan.ku);
+    }
+    const unsigned lasts = __ballot_sync(kAll, last);
+    __syncwarp();
+#pragma unroll 1
+    for (int shared_tile = first_tile; shared_tile < first_tile + 2; ++shared_tile) {
+        if (!(lasts >> (shared_tile - first_tile) & 1)) continue;
+        const int begin = shared_tile * plan.ku;
+        int c = plan.cta;
+        while (plan.unit_of(c) > begin) --c;
+        float v[kValues] = {};
+        while (plan.unit_of(c) < begin + plan.ku) {  // four parts on their way at a time
+            float a[4][kValues];
 #pragma unroll
-        for (int i = 0; i < kValues; i += 2) {
-            const int c = F32 ? 4 * (i >> 1) + t : 8 * (i >> 2) + 2 * t + (i >> 1 & 1);
-            if (c >= pl.n) continue;
-            const float unit = m.unit[pl.p0 + c];
-            float a = v[i] * unit, b = v[i + 1] * unit;
-            a = activate<F32>(a, m.activation);
-            if (two) a *= b;
-            else b = activate<F32>(b, m.activation);
-            float* out = m.out + static_cast<int64_t>(pl.p0 + c) * m.rows;
-            if (in0) out[f0] = a;
-            if (in1) out[f1] = b;
+            for (int i = 0; i < 4; ++i) {
+                const bool there = plan.unit_of(c + i) < begin + plan.ku;
+                const float* part = part_of(there ? c + i : c, begin);
+#pragma unroll
+                for (int k = 0; k < kValues; ++k) a[i][k] = there ? __ldcg(part + k * kWarps * 32) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < kValues; ++k) v[k] += a[i][k];
+            c += 4;
         }
+        store(place(plan.full + shared_tile), v);
     }
 }
 

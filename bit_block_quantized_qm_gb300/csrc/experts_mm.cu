@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.ku = (m.K + 255) / 256;
         p.full = p.tiles / p.ctas * p.ctas;
         p.rest = p.tiles - p.full;
+        p.each = p.rest * p.ku / p.ctas;
+        p.more = p.rest * p.ku - p.each * p.ctas;
         p.share = p.rest > 0 && p.rest * 8 <= p.ctas * 7 && p.ku > 1;
         plan = p;
     }
@@ -487,8 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t place_floats = static_cast<int64_t>(2 * kHalf) * m.split_cols;
             const int shared_tile = tile - plan.full;
             auto part_of = [&](int c) {  // CTA c's part of this tile
-                const int first = plan.unit_of(c) / plan.ku;
-                return m.split + ((2 * c + (shared_tile - first)) * C::kPair + rank) * place_floats;
+                return m.split + ((2 * c + (plan.unit_of(c) < shared_tile * plan.ku)) * C::kPair + rank) * place_floats;
             };
             float* mine = part_of(plan.cta);
             for (int ch = group; kChunk * ch < pl.n; ch += 4) {
@@ -501,18 +502,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if constexpr (!F32) free_sums();
-            __threadfence();
             named_barrier_sync(1, kDecodeWarps * 32);
             if (threadIdx.x == 0) {
                 const unsigned n = static_cast<unsigned>(n_units);
-                last_of_tile = atomicAdd(&m.counters[shared_tile * C::kPair + rank], n) + n == static_cast<unsigned>(plan.ku);
-                __threadfence();
+                last_of_tile = atom_add_acq_rel(&m.counters[shared_tile * C::kPair + rank], n) + n == static_cast<unsigned>(plan.ku);
             }
             named_barrier_sync(1, kDecodeWarps * 32);
             if (!last_of_tile) return;
             // The CTAs that have units of it, in order.
-            const int total = plan.rest * plan.ku, u_lo = shared_tile * plan.ku;
-            const int c_lo = ((u_lo + 1) * plan.ctas - 1) / total, c_hi = ((u_lo + plan.ku) * plan.ctas - 1) / total;
+            const int begin = shared_tile * plan.ku;
+            int c_lo = plan.cta;
+            while (plan.unit_of(c_lo) > begin) --c_lo;
             for (int ch = group; kChunk * ch < pl.n; ch += 4) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -520,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) v[i] = 0.f;
 #pragma unroll 1
-                    for (int c = c_lo; c <= c_hi; ++c) {
-                        if (plan.unit_of(c) == plan.unit_of(c + 1)) continue;
+                    for (int c = c_lo; plan.unit_of(c) < begin + plan.ku; ++c) {
                         const float* part = part_of(c) + (half * m.split_cols + kChunk * ch) * kHalf + r;
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i) {
