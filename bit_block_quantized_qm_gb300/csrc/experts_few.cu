@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane < 2 && begin < to) {
         const unsigned n = static_cast<unsigned>(min(to, begin + plan.ku) - max(from, begin));
-        last = atom_add_acq_rel(&m.counters[(first_tile + lane) * kWarps + warp], n) + n == static_cast<unsigned>(plan.ku);
+        last = n != static_cast<unsigned>(plan.ku) &&  // (a whole tile after all: stored above)
+               atom_add_acq_rel(&m.counters[(first_tile + lane) * kWarps + warp], n) + n == static_cast<unsigned>(plan.ku);
     }
     const unsigned lasts = __ballot_sync(kAll, last);
     __syncwarp();

@@ -257,6 +257,29 @@ def test_experts(qm, n, hidden, inner, tokens, top_k, dtype):
     b.check(x, ids, weights)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n,hidden,inner,tokens,top_k", [
+    (40, 288, 320, 40, 4), (16, 64, 640, 16, 8), (9, 2048, 32, 12, 6), (1024, 96, 64, 70, 3), (24, 1280, 800, 6, 24),
+    (12, 352, 544, 24, 4), (4, 4096, 1408, 1, 4), (2, 4096, 4096, 3, 2),  # up to 8 rows an expert
+    (4, 352, 288, 25, 2), (3, 1024, 544, 40, 1), (20, 64, 512, 60, 5)])  # 8 to 16
+def test_experts_with_few_rows(qm, n, hidden, inner, tokens, top_k, dtype):
+    """Few rows an expert on average, some with many and some with none; lengths that are odd multiples of a block."""
+    b = Block(qm, n, hidden, inner, seed=n + inner)
+    b.check(*b.rows(tokens, top_k, dtype, skew=2.0))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 100])
+def test_experts_rows_in_one_of_many(qm, rows, dtype):
+    """All rows to the last of many experts: around the sizes of its tiles, and several of them."""
+    b = Block(qm, 33, 512, 288, seed=rows)
+    x, ids, weights = b.rows(rows, 2, dtype)
+    ids[:, 0], ids[:, 1] = 32, -1
+    b.check(x, ids, weights)
+    ids[:, 1] = 32  # the same expert twice
+    b.check(x, ids, weights)
+
+
 @pytest.mark.parametrize("kind", [0, 1, 2])
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("tokens", [2, 90])
