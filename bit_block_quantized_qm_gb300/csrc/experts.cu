@@ -370,9 +370,9 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
     __half *x_hi = halves(at.x_pieces), *x_lo = x_hi + pairs * piece_pitch(e.hidden);
     __half *i_hi = halves(at.i_pieces), *i_lo = i_hi + pairs * piece_pitch(e.inner);
 
-    // Up to this many pairs a row's CTA counts its own place, which saves a launch; the counting
-    // takes (pairs / 512) ids a thread in every CTA.
-    constexpr int kOwnPlace = 1024;
+    // Up to this many pairs a row's CTA counts its own place, which saves a launch (one token: 65 us against 67, 35
+    // against 37); the counting takes (pairs / 512) ids a thread in every CTA (1024 pairs: 126 us against 121).
+    constexpr int kOwnPlace = 256;
     const bool own_place = pairs <= kOwnPlace;
     cudaError_t err = launch_pdl(experts_setup<T>, dim3(e.n + (own_place ? pairs : 0)), dim3(kSetupThreads), 0, stream, c, e.n,
                                  e.hidden, starts, order, place, counters, x_hi, x_lo, floats(at.x_unit));
@@ -387,16 +387,17 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
     ExpertsMm m = {starts, floats(at.x_unit), inner, floats(at.split), counters, c.err,
                    {e.gate ? e.gate : e.up, e.up}, {e.gate ? e.gate_stride : e.up_stride, e.up_stride},
                    e.n, e.hidden, e.inner, e.activation, at.split_cols, 0x64006400u};
-    // Few rows an expert: experts_few.cu (16 experts of 4096 x 4096, 8 rows each: bf16 136 us against 147, f32
-    // 194 against 221; 16 rows each: 182 against 150, 288 against 226).
+    // Few rows an expert: experts_few.cu (16 experts of 4096 x 4096, 8 rows each: bf16 127 us against 143, f32
+    // 191 against 221; 12 rows each: 152 against 141, 244 against 219).
     const bool few = pairs <= 8 * static_cast<int64_t>(e.n);
     auto products = [&](bool down, const __half* hi, const __half* lo) {
         return few ? launch_experts_few(m, e, c.type, hi, lo, dev, stream)
                    : launch_experts_mm(m, e, down, c.type, hi, lo, pairs, dev, stream);
     };
     if ((err = products(false, x_hi, x_lo)) != cudaSuccess) return err;
-    // Few rows take many threads each, for the latency, and so do long ones, which stay in registers between
-    // their maximum and their pieces; many short ones few.
+    // Few rows take many threads each, for the latency (192 rows of 4096: 219 us in all against 221), and so do long
+    // ones, which stay in registers between their maximum and their pieces (8192 rows of 14336: 133 us against
+    // 146); many short ones few (64 experts with 48 rows of 1408 each: 163 us in all against 173).
     const bool wide = pairs <= 512;
     err = wide || e.inner > 4096 ? launch_pdl(experts_inner<512, T>, dim3(pairs), dim3(512), 0, stream, e, c, inner, starts, order, i_hi, i_lo,
                             floats(at.i_unit))

@@ -1,8 +1,14 @@
 // The experts' products (qm_experts_q4_0) on tcgen05 tensor cores.
 //
 // The weights are the 128-row operand and the token rows the columns, so a tile is
-// 256 weight rows (128 of gate and 128 of up, or 256 of one matrix) by 1 to 128 rows of
-// one expert, rounded up to 16: the same kernel serves one token and thousands.
+// 256 weight rows (128 of gate and 128 of up, or 256 of one matrix) by up to 128 rows of
+// one expert, rounded up to 16.
+//
+// Bound: many rows, the tensor cores (8192 rows through 8 experts of 14336 x 4096, three products:
+// 2.13 ms in all, 1340 TFLOP/s; an instruction with 128 columns takes 64 cycles, one with 16 nine);
+// fewer, the unpacking: 8 weights of each lane of a warp take 21 cycles, fp16 and integer
+// instructions going at half rate, and a unit (256 rows by 256 of K) 1340, where memory would
+// bring one every 1570.
 //
 //   D[w][t] = sum_k (q_wk - 8) d_wb  x_tk
 //
@@ -35,8 +41,9 @@
 // Sums that come out infinite or NaN (a scale of 32 and more overflows f16) are left so, and
 // taken again by the kernels that read them.
 //
-// No register may spill here: with most of the SM's memory shared memory, what is spilled comes
-// back from L2, and each reload costs some 300 cycles (products at 817 instead of 1065 TFLOP/s).
+// No register may spill in the loop over units: with most of the SM's memory shared memory, what is
+// spilled comes back from L2, and each reload costs some 300 cycles (bf16 rows' products went at 817
+// instead of 1065 TFLOP/s).  f32 rows' tiles of 64 spill 76 to 132 bytes.
 //
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include <type_traits>
@@ -68,7 +75,7 @@ struct Cfg {
     static constexpr int kLaunchRegs = 96, kDecodeRegs = 112, kOtherRegs = 32;
     static_assert(kDecodeWarps * kDecodeRegs + 4 * kOtherRegs <= 20 * kLaunchRegs, "a warp would wait for ever");
     // CTAs come in pairs that take the same token rows (and blocks of weights next to each other):
-    // each loads half of them for both.
+    // each loads half of them for both (1357 TFLOP/s against 1190: L2 gives an SM some 32 bytes a cycle).
     static constexpr int kPair = !F32 && kTokens > 32 ? 2 : 1;
     // Stages of unpacked weights, 128 columns of TMEM (bf16 rows: 128 elements, f32 rows: 64), and of
     // the token rows that they meet.  Long ones, because an issuing warp takes 300 cycles and more for a
@@ -762,8 +769,10 @@ cudaError_t launch_experts_mm(const ExpertsMm& m, const ExpertsView& e, bool dow
         if (down) return wide ? run(launch_kernel<kF32, kTokens, true, true>) : run(launch_kernel<kF32, kTokens, true, false>);
         return wide ? run(launch_kernel<kF32, kTokens, false, true>) : run(launch_kernel<kF32, kTokens, false, false>);
     };
-    // Narrow tiles where experts have few rows: three stages of weights, bf16 rows two sets of sums.
-    const bool narrow = n_pieces <= 16 * static_cast<int64_t>(e.n);
+    // Narrow tiles where experts have few rows: three stages of weights, bf16 rows two sets of sums (16 experts of
+    // 4096 x 4096 with 24 rows each: bf16 152 us against 162, f32 249 against 292; with 32 rows each 201 against 166,
+    // 331 against 310).
+    const bool narrow = n_pieces <= 24 * static_cast<int64_t>(e.n);
     if (type == KvType::kF32)
         return narrow ? go(std::true_type{}, std::integral_constant<int, 32>{}) : go(std::true_type{}, std::integral_constant<int, 64>{});
     if (narrow) return go(std::false_type{}, std::integral_constant<int, 32>{});

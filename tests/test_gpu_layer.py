@@ -416,6 +416,40 @@ def test_experts_same_again(qm, tokens, dtype):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_experts_two_streams_at_once(qm, dtype):
+    """Calls of all sizes on two streams at once, while a captured one is replayed on a third: each has its own
+    workspace."""
+    b = Block(qm, 8, 1024, 512, seed=22)
+    calls = [b.rows(tokens, 2, dtype, skew=1.0) for tokens in (1, 20, 70, 300)]
+    want = [qm.qm_experts_q4_0(b.handle, *c) for c in calls]
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want[1])
+    with torch.cuda.graph(graph):
+        qm.qm_experts_q4_0(b.handle, *calls[1], out=out)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        got += [(j, qm.qm_experts_q4_0(b.handle, *calls[j], stream=streams[s])) for s, j in enumerate((i % 4, (i + i // 4) % 4))]
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+    torch.cuda.synchronize()
+    for j, g in got:
+        assert torch.equal(g, want[j])
+    assert torch.equal(out, want[1])
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 60, 200])
+def test_experts_of_zeros(qm, tokens):
+    """Weights that are all 0 (quants of 8) give exactly 0, whatever their scales and the rows."""
+    b = Block(qm, 4, 512, 320, seed=23)
+    for w in (b.up, b.down):
+        w.view(*w.shape[:-1], -1, 18)[..., 2:] = 0x88
+    for dtype in (F32, BF16):
+        x, ids, weights = b.rows(tokens, 2, dtype)
+        assert (qm.qm_experts_q4_0(b.handle, 100 * x, ids, weights) == 0).all()
+
+
 def test_experts_one_token_is_a_row_of_many(qm):
     """What a token gets hardly depends on who is with it: within the tolerance, by whichever path."""
     b = Block(qm, 8, 1024, 512, seed=20)
