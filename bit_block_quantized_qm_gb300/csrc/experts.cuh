@@ -31,6 +31,7 @@ struct ExpertsMm {
     int activation;
     int split_cols;         // columns of a partial tile
     uint32_t k1024;         // 0x64006400
+    bool early;             // (few rows) this kernel may read weights and `starts` before its wait
 };
 
 // Values of f16 pieces per row: the contraction's length, padded to whole 128-byte lines.

@@ -2,14 +2,16 @@
 //
 //   D[w][c] = sum_b d_wb sum_(k in b) (q_wk - 8) x_ck
 //
-// Bound: memory, the chosen experts' weights, and close to it the instructions: a warp takes some 46 issue
-// slots for a block of 16 rows, and 1490 of a unit's 1570 cycles at memory's rate would be taken.  One row
-// through 2 experts of 14336 x 4096 (198 MB): 65 us in all; 16 rows through an expert of 4096 x 4096 each: 77 us;
-// the copies alone go at 6.8 TB/s, the products of gate and up at 4 to 4.5.  An instruction m16n8k16 takes 16 weight rows (8 of
-// either half of the tile) by 8 columns, each a token row's f16 piece (f32 rows have two, next to each
-// other): (q - 8) is exact in f16, the sum over a block is scaled by d in f32.  A lane unpacks the four
-// bytes of each of two rows' blocks that its place in the fragment asks for, straight from the raw bytes;
-// no unpacked weight is stored anywhere, and no warp waits for another but for the copies.
+// Bound: memory, the chosen experts' weights, and close to it the instructions: a warp takes 46 issue
+// slots for a block of 16 rows, so 1490 of the 1570 cycles in which memory brings a unit.  One row through 2
+// experts of 14336 x 4096 (198 MB) takes 62 us in all, 16 rows through an expert of 4096 x 4096 each 76; the
+// copies alone go at 6.8 TB/s, the products of gate and up at 4 to 4.5.
+//
+// An instruction m16n8k16 takes 16 weight rows (8 of either half of the tile) by 8 columns, each a token
+// row's f16 piece (f32 rows have two, next to each other): (q - 8) is exact in f16, the sum over a block is
+// scaled by d in f32.  A lane unpacks the four bytes of each of two rows' blocks that its place in the
+// fragment asks for, straight from the raw bytes; no unpacked weight is stored anywhere, and no warp waits
+// for another but for the copies.
 //
 // A CTA (one per SM) takes tiles of 256 weight rows by up to 16 columns, in units of 256 elements of K:
 // one warp copies units (TMA) and their columns into a ring, sixteen warps have 16 rows each.  An
@@ -157,8 +159,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&map_w0);
         prefetch_tensormap(&map_w1);
     }
-    grid_launch_dependents();
-    grid_dependency_wait();
+    // The down product begins before the kernel that makes its columns has ended: with whose weights, the
+    // setup has said, which has ended long since (the kernel between them begins when all CTAs of the first
+    // product are past their wait for it).
+    if (!m.early) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
     const bool two = m.w[0] != m.w[1];  // gate and up
     const int block_rows = two ? kExpertHalf : 2 * kExpertHalf;
     const int blocks = (m.rows + block_rows - 1) / block_rows;
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int sum = 0;
         for (int e0 = 0; e0 < m.n; e0 += 32) {
             const int e = e0 + lane;
-            const int end = e < m.n ? m.starts[e + 1] : 0, count = e < m.n ? end - m.starts[e] : 0;
+            const int end = e < m.n ? __ldcg(m.starts + e + 1) : 0, count = e < m.n ? end - __ldcg(m.starts + e) : 0;
             int v = (count + kTokens - 1) / kTokens;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -214,35 +221,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor cur = first_item(plan);
     Item item;
     bool ok = true;
-    uint32_t it = 0;
 
     if (warp == kWarps) {
         // ---- copies
+        uint32_t it = 0;
         const int64_t pitch = piece_pitch(m.K) * 2;
         const uint8_t* pieces = static_cast<const uint8_t*>(F32 && (lane & 1) ? lo : hi);
+        auto column_bytes = [&](int u) {
+            const int64_t left = pitch - 512 * static_cast<int64_t>(u);
+            return left < 512 ? static_cast<uint32_t>(left) : 512u;
+        };
+        auto copy_weights = [&](const Place& pl, int u, int stage) {
+            uint8_t* dst = ring + stage * C::kStageBytes;
+            if (lane == 0)
+                mbar_arrive_expect_tx(&bar.full[stage], C::kRawBytes + (F32 ? 2 * pl.n : pl.n) * column_bytes(u));
+            __syncwarp();
+            // Lanes i and 16 + i: the rows i of each group of the two halves.
+            const int i = lane & 15, half = lane >> 4;
+            if (i < together) {
+                const int row0 = pl.block * block_rows + (two ? 0 : half * kExpertHalf);
+                tma_load_3d_once(dst + (half * kExpertHalf + i * (kExpertHalf / together)) * C::kPitch, half ? &map_w1 : &map_w0,
+                                 (i * row_bytes & ~15) + 144 * u, row0 / together, pl.expert, &bar.full[stage]);
+            }
+        };
+        uint32_t ahead = 0;  // units whose weights are on their way before the wait
+        if (m.early) {
+            Cursor first = cur;
+            while (ahead < kStages && next_item(plan, first, &item)) {
+                const Place pl = place(item.tile);
+                for (int u = item.u0; u < item.u1 && ahead < kStages; ++u, ++ahead) copy_weights(pl, u, ahead);
+            }
+            grid_dependency_wait();
+            grid_launch_dependents();
+        }
         while (ok && next_item(plan, cur, &item)) {
             const Place pl = place(item.tile);
-            const int columns = F32 ? 2 * pl.n : pl.n;
             for (int u = item.u0; u < item.u1; ++u, ++it) {
                 const int stage = it % kStages;
                 if (it >= kStages) ok = warp_wait(&bar.empty[stage], (it / kStages - 1) & 1, err);
                 if (!ok) break;
-                uint8_t* dst = ring + stage * C::kStageBytes;
-                const int64_t left = pitch - 512 * static_cast<int64_t>(u);
-                const uint32_t column_bytes = left < 512 ? static_cast<uint32_t>(left) : 512u;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.full[stage], C::kRawBytes + columns * column_bytes);
-                __syncwarp();
-                // Lanes i and 16 + i: the rows i of each group of the two halves.
-                const int i = lane & 15, half = lane >> 4;
-                if (i < together) {
-                    const int row0 = pl.block * block_rows + (two ? 0 : half * kExpertHalf);
-                    tma_load_3d_once(dst + (half * kExpertHalf + i * (kExpertHalf / together)) * C::kPitch, half ? &map_w1 : &map_w0,
-                                (i * row_bytes & ~15) + 144 * u, row0 / together, pl.expert, &bar.full[stage]);
-                }
-                if (lane < columns)
-                    bulk_load_1d(dst + C::kRawBytes + lane * kColumnPitch,
-                                 pieces + (pl.p0 + (F32 ? lane >> 1 : lane)) * pitch + 512 * static_cast<int64_t>(u), column_bytes,
-                                 &bar.full[stage]);
+                if (it >= ahead) copy_weights(pl, u, stage);
+                if (lane < (F32 ? 2 * pl.n : pl.n))
+                    bulk_load_1d(ring + stage * C::kStageBytes + C::kRawBytes + lane * kColumnPitch,
+                                 pieces + (pl.p0 + (F32 ? lane >> 1 : lane)) * pitch + 512 * static_cast<int64_t>(u),
+                                 column_bytes(u), &bar.full[stage]);
                 __syncwarp();
             }
         }
@@ -260,7 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool odd = shift & 2;
     const int row_at = slot * C::kPitch + (shift & ~3);
     constexpr int kValues = F32 ? 4 : 8;  // sums of a thread: [columns of a group of 8][both halves]
+    int stage = 0;
+    uint32_t parity = 0;
     const int64_t place_floats = 8 * kWarps * 32;
+    if (m.early) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
     // The sums of a tile, scaled and activated.
     auto store = [&](const Place& pl, float(&v)[kValues]) {
         const int f0 = pl.block * block_rows + r, f1 = two ? f0 : f0 + kExpertHalf;
@@ -287,9 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Place pl = place(item.tile);
         const bool many = (F32 ? 2 * pl.n : pl.n) > 8;
         float acc[2][4] = {};
-        for (int u = item.u0; u < item.u1; ++u, ++it) {
-            const int stage = it % kStages;
-            ok = ok && warp_wait(&bar.full[stage], (it / kStages) & 1, err);
+        for (int u = item.u0; u < item.u1; ++u) {
+            ok = ok && warp_wait(&bar.full[stage], parity, err);
             const uint8_t* raw = ring + stage * C::kStageBytes;
             const uint8_t* row0 = raw + row_at;
             const uint8_t* row1 = row0 + kExpertHalf * C::kPitch;
@@ -299,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else unit_sums<1, WIDE>(row0, row1, odd, column, t, n_blocks, m.k1024, acc);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.empty[stage]);
+            if (++stage == kStages) stage = 0, parity ^= 1;
         }
         // F32: columns 2 t and 2 t + 1 are a row's pieces.
         float v[kValues];
