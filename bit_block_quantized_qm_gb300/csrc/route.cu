@@ -184,7 +184,7 @@ __device__ __noinline__ int order_f64(const RouteCall& c, const T* row, int lane
         }
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-        score = exp(x - mx) / sum;
+        score = mx == -INFINITY ? 0.0 : exp(x - mx) / sum;  // (a row of nothing but -infinity: the bias alone)
     }
     uint64_t key = lane < n ? key_of(score + static_cast<double>(c.bias[id])) : 0;
     int sorted = 0;

@@ -194,6 +194,22 @@ def test_route_masked(qm, low):
     check_route(qm, torch.randn((20, 48), generator=gen).cuda(), 30, bias=bias.cuda(), sigmoid=True)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_of_nothing_by_close_biases(qm, sigmoid):
+    """Rows whose mask leaves nothing: the biases choose, next to each other as they are."""
+    gen = generator(4)
+    bias = 1 + torch.randperm(40, generator=gen).float() * 2.0 ** -23
+    logits = torch.full((5, 40), -math.inf)
+    logits[0] = 0
+    logits[1, 7] = 3
+    ids, weights = qm.qm_route_experts(logits.cuda(), 6, bias=bias.cuda(),
+                                       scoring=qm.QM_SCORE_SIGMOID if sigmoid else qm.QM_SCORE_SOFTMAX)
+    order = torch.argsort(bias, descending=True)
+    assert torch.equal(ids[2:].long().cpu(), order[:6].expand(3, 6)) and (weights[2:] == 0).all()
+    assert torch.equal(ids[0].long().cpu(), order[:6])
+    assert ids[1, 0] == 7 and torch.equal(ids[1, 1:].long().cpu(), order[order != 7][:5])
+
+
 def test_route_bad_rows(qm):
     """NaN and infinities: the ids are experts, each once; other rows are as ever."""
     gen = generator(4)
