@@ -844,8 +844,8 @@ def qm_add_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, weight_offs
         ss = _matrix(sum_out, "sum_out", width, x)[1]
     if residual is not None:
         rs = _matrix(residual, "residual", width, x)[1]
-        if sum_out is None:
-            sum_out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        if sum_out is None:  # (empty_like is the cheaper, but takes over strides)
+            sum_out = torch.empty_like(x) if x.is_contiguous() else torch.empty((rows, width), dtype=x.dtype, device=x.device)
     if weight is not None:
         _require(weight, torch.float32, "weight")
         if weight.numel() != width:
@@ -853,7 +853,7 @@ def qm_add_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, weight_offs
     if out is not None:
         os_ = _matrix(out, "out", width, x)[1]
     elif want_out:
-        out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty((rows, width), dtype=x.dtype, device=x.device)
     if want_q8 or q8_out is not None:
         if width % BLOCK_ELEMS:
             raise ValueError("Q8_0 rows need a width that is a multiple of 32")

@@ -41,9 +41,9 @@
 // Sums that come out infinite or NaN (a scale of 32 and more overflows f16) are left so, and
 // taken again by the kernels that read them.
 //
-// No register may spill in the loop over units: with most of the SM's memory shared memory, what is
-// spilled comes back from L2, and each reload costs some 300 cycles (bf16 rows' products went at 817
-// instead of 1065 TFLOP/s).  f32 rows' tiles of 64 spill 76 to 132 bytes.
+// No register may spill: with most of the SM's memory shared memory, what is spilled comes back from L2,
+// and each reload costs some 300 cycles (bf16 rows' products went at 817 instead of 1065 TFLOP/s; f32 rows'
+// tiles of 64 keep in shared memory what they need once a tile, which took 500 rows from 1211 to 1187 us).
 //
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include <type_traits>
@@ -208,6 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ alignas(16) float units[3][C::kTokens];  // of the columns of this tile, the one before and the one after
     __shared__ int last_of_tile;
     __shared__ Plan plan;  // (not in registers, of which there are few)
+    // What an unpacking warp needs once a tile.  All lanes write the same, and meet between writing and reading.
+    struct Seldom {
+        Cursor cur;
+        int tile, units, n;  // of the tile whose outputs are due
+        uint32_t buf;
+    };
+    __shared__ Seldom seldom_of[kDecodeWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* const err = m.err;
 
@@ -542,9 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // Unit by unit.  A tile's outputs wait until the next tile's first unit is unpacked, so that the
         // products of that one can begin as soon as there is room for its sums.
-        int done_tile = 0, done_units = 0, n_now = 0, n_due = 0;
-        uint32_t buf = 0, buf_done = 0;  // of 3 sets of factors: a warp may be two tiles ahead of another's outputs
-        bool more = next_item(plan, cur, &item), due = false;
+        int n_now = 0;
+        Seldom in_registers;
+        Seldom& seldom = C::kMoveRegs ? seldom_of[warp] : in_registers;
+        uint32_t buf = 0;  // of 3 sets of factors: a warp may be two tiles ahead of another's outputs
+        auto next = [&](Cursor c) {
+            const bool got = next_item(plan, c, &item);
+            __syncwarp();
+            seldom.cur = c;
+            __syncwarp();
+            return got;
+        };
+        bool more = next(cur), due = false;
         int u = 0;
         auto begin = [&] {
             const Place pl = place(item.tile);
@@ -564,11 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         while (more || due) {
             if (more) {
-                unpack_unit(u, u > item.u0 ? n_now : due ? n_due : 0);
+                unpack_unit(u, u > item.u0 ? n_now : due ? seldom.n : 0);
             }
             if (due) {
-                if (F32 && !more) collect(n_due);
-                outputs(done_tile, done_units, buf_done);
+                if (F32 && !more) collect(seldom.n);
+                outputs(seldom.tile, seldom.units, seldom.buf);
                 due = false;
                 if constexpr (F32) {
 #pragma unroll
@@ -576,10 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (more && ++u == item.u1) {
-                n_due = n_now;
-                done_tile = item.tile, done_units = item.u1 - item.u0, buf_done = buf;
+                __syncwarp();
+                seldom.n = n_now;
+                seldom.tile = item.tile, seldom.units = item.u1 - item.u0, seldom.buf = buf;
                 due = true;
-                more = next_item(plan, cur, &item);
+                more = next(seldom.cur);
                 if (more) begin();
             }
         }
