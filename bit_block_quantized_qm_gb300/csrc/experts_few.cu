@@ -169,22 +169,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool two = m.w[0] != m.w[1];  // gate and up
     const int block_rows = two ? kExpertHalf : 2 * kExpertHalf;
     const int blocks = (m.rows + block_rows - 1) / block_rows;
+    for (int e = threadIdx.x; e <= m.n; e += kThreads) rows_before[e] = __ldcg(m.starts + e);
+    __syncthreads();
     if (warp == 0) {
         int sum = 0;
         for (int e0 = 0; e0 < m.n; e0 += 32) {
             const int e = e0 + lane;
-            const int end = e < m.n ? __ldcg(m.starts + e + 1) : 0, count = e < m.n ? end - __ldcg(m.starts + e) : 0;
+            const int count = e < m.n ? rows_before[e + 1] - rows_before[e] : 0;
             int v = (count + kTokens - 1) / kTokens;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(kAll, v, d);
                 if (lane >= d) v += o;
             }
-            if (e < m.n) tiles_before[e + 1] = sum + v, rows_before[e + 1] = end;
+            if (e < m.n) tiles_before[e + 1] = sum + v;
             sum += __shfl_sync(kAll, v, 31);
         }
         if (lane == 0) {
-            tiles_before[0] = rows_before[0] = 0;
+            tiles_before[0] = 0;
             Plan p;
             p.tiles = sum * blocks;
             p.ctas = gridDim.x;
