@@ -65,6 +65,21 @@ def test_norm(qm, n, width, pad, shift, dtype, residual, weight, offset):
         near(total, s, b_sum)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("width", [33, 255, 257, 1023, 4097, 8191, 8193, 16383, 16385])
+def test_norm_of_odd_widths(qm, width, dtype):
+    gen = generator(width)
+    x, r = rows(5, width, dtype, gen), rows(5, width, dtype, gen)
+    w = torch.randn(width, generator=gen).cuda()
+    want, s = lp.norm(x, w, r, 1e-5, 1.0)
+    bounds = lp.norm_bounds(want, s, dtype, width // 512 + 50)
+    out, total, _ = qm.qm_add_rmsnorm(x, w, residual=r, eps=1e-5, weight_offset=1.0)
+    near(out, want, bounds[0])
+    near(total, s, bounds[1])
+    again, same, _ = qm.qm_add_rmsnorm(x, w, residual=r, eps=1e-5, weight_offset=1.0, sum_out=r)
+    assert same is r and torch.equal(r, total) and torch.equal(again, out)
+
+
 @pytest.mark.parametrize("width", [32, 96, 4096, 8224, 16416])
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_norm_to_8_bits(qm, width, dtype):
