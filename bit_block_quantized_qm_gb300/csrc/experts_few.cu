@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kValues = F32 ? 4 : 8;  // sums of a thread: [columns of a group of 8][both halves]
     int stage = 0;
     uint32_t parity = 0;
-    const int64_t place_floats = 8 * kWarps * 32;
+    constexpr int64_t place_floats = 8 * kWarps * 32;  // (the workspace has room for 256 rows by 16 columns and more)
     if (m.early) {
         grid_dependency_wait();
         grid_launch_dependents();
