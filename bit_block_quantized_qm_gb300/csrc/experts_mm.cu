@@ -35,7 +35,7 @@
 // starts at the 16-byte boundary below, and the unpacking threads shift.
 //
 // Work: whole tiles, a CTA each, as long as they fill all CTAs; the units (256 elements of
-// K) of those left over are dealt out evenly, and the CTA that comes last to a shared tile
+// K) of those left over are dealt out evenly, where that saves more than it costs, and the CTA that comes last to a shared tile
 // adds its parts in the CTAs' order.
 //
 // Sums that come out infinite or NaN (a scale of 32 and more overflows f16) are left so, and
@@ -77,6 +77,10 @@ struct Cfg {
     // CTAs come in pairs that take the same token rows (and blocks of weights next to each other):
     // each loads half of them for both (1357 TFLOP/s against 1190: L2 gives an SM some 32 bytes a cycle).
     static constexpr int kPair = !F32 && kTokens > 32 ? 2 : 1;
+    // Sharing the tiles left over saves ku (ctas - rest) / ctas units, and the joining costs what this many do
+    // (64 experts of 2048 x 1408, 64 bf16 rows each: shared above 1 saved 191 us, above 9 176; 32 f32 rows
+    // each: above 1 236, above 6 250).
+    static constexpr int kJoinUnits = F32 ? 2 : 9;
     // Stages of unpacked weights, 128 columns of TMEM (bf16 rows: 128 elements, f32 rows: 64), and of
     // the token rows that they meet.  Long ones, because an issuing warp takes 300 cycles and more for a
     // stage besides its products.
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.rest = p.tiles - p.full;
         p.each = p.rest * p.ku / p.ctas;
         p.more = p.rest * p.ku - p.each * p.ctas;
-        p.share = p.rest > 0 && p.rest * 8 <= p.ctas * 7 && p.ku > 1;
+        p.share = p.rest > 0 && p.ku * (p.ctas - p.rest) > C::kJoinUnits * p.ctas;
         plan = p;
     }
     __syncthreads();

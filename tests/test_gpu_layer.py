@@ -300,6 +300,17 @@ def test_experts_with_few_rows(qm, n, hidden, inner, tokens, top_k, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n,hidden,inner,tokens,top_k", [
+    (2, 4096, 512, 24, 1), (2, 4384, 512, 150, 1), (2, 512, 4096, 150, 2), (3, 288, 4704, 20, 2), (5, 4384, 4704, 9, 2)])
+def test_experts_of_long_rows(qm, n, hidden, inner, tokens, top_k, dtype):
+    """Few tiles of many units, which several thread blocks share."""
+    b = Block(qm, n, hidden, inner, seed=n * hidden)
+    x, ids, weights = b.rows(tokens, top_k, dtype, skew=1.0)
+    out = b.check(x, ids, weights)
+    assert torch.equal(qm.qm_experts_q4_0(b.handle, x, ids, weights), out)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 100])
 def test_experts_rows_in_one_of_many(qm, rows, dtype):
     """All rows to the last of many experts: around the sizes of its tiles, and several of them."""
