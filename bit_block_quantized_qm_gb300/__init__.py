@@ -981,11 +981,13 @@ def qm_experts_q4_0(experts, x, ids, weights, out=None, stream=None, workspace=N
     tokens = x.shape[0]
     _require(ids, torch.int32, "ids")
     _require(weights, torch.float32, "weights")
-    if ids.dim() != 2 or ids.shape[0] != tokens or weights.shape != ids.shape:
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != tokens or weights.shape != shape:
         raise ValueError("ids and weights must be [tokens, top_k]")
-    top_k = ids.shape[1]
+    top_k = shape[1]
     if out is None:
-        out, os_ = torch.empty((tokens, experts.hidden), dtype=x.dtype, device=x.device), experts.hidden
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty((tokens, experts.hidden), dtype=x.dtype, device=x.device)
+        os_ = experts.hidden
     else:
         os_ = _matrix(out, "out", experts.hidden, x)[1]
     handle = _stream_handle(stream)
