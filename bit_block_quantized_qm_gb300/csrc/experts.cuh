@@ -31,6 +31,7 @@ struct ExpertsMm {
     int activation;
     int split_cols;         // columns of a partial tile
     uint32_t k1024;         // 0x64006400
+    bool gated;             // the halves are gate and up, whose products are multiplied (which may be one matrix)
     bool early;             // (few rows) this kernel may read weights and `starts` before its wait
 };
 

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_launch_dependents();
     const uint32_t tmem = tmem_slot;
 
-    const bool two = m.w[0] != m.w[1];  // gate and up
+    const bool two = m.gated;
     const int block_rows = two ? kHalf : 2 * kHalf;
     const int blocks = (m.rows + block_rows * C::kPair - 1) / (block_rows * C::kPair);  // (of a pair)
     const int rank = C::kPair > 1 ? static_cast<int>(blockIdx.x & 1) : 0;
