@@ -13,6 +13,8 @@
 // in order by themselves 4096 tokens, 256 experts in 8 groups take 19 us against 34.)
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "qm_device.cuh"
 
 namespace qm {
@@ -68,9 +70,9 @@ __device__ __forceinline__ void largest(const K (&key)[PER], int lane, K* top, i
     *which = static_cast<int>(__reduce_min_sync(kAll, e));
 }
 
-// Sum of a group's one or two largest choices, on every lane.
+// Sum of a group's one or two largest choices, and the second, on every lane.
 template <typename F>
-__device__ __forceinline__ F warp_top(F a, F b, int group_top) {
+__device__ __forceinline__ F warp_top(F a, F b, bool both, F* second) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
         const F a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
@@ -79,17 +81,21 @@ __device__ __forceinline__ F warp_top(F a, F b, int group_top) {
         b = b < b2 ? b2 : b;
         b = b < lo ? lo : b;
     }
-    return group_top == 2 ? a + b : a;
+    *second = b;
+    return both ? a + b : a;
 }
 
 // Clears the keys of the experts whose groups do not count among the top_groups
-// largest.  True if the groups at the border are closer than `near` and 2^-21 of
-// themselves.
+// largest.  True if one of those may be as large as one that stays, in f32: a group's sum a + b
+// is off by `near` for its scores and by 2^-24 (|a| + |b| + |a + b|) for the roundings of choices
+// and sum, where a and b may be far larger than a + b.
 template <int PER, typename F, typename K>
-__device__ __forceinline__ bool drop_groups(const RouteCall& c, const F (&choice)[PER], K (&key)[PER], int lane, F near) {
+__device__ __forceinline__ bool drop_groups(const RouteCall& c, const F (&choice)[PER], K (&key)[PER], int lane, float near) {
     const int size = c.experts / c.groups;
     constexpr F kLow = -INFINITY;
-    F mine[2] = {kLow, kLow};  // groups `lane` and lane + 32
+    const bool both = c.group_top == 2 && size > 1;
+    F mine[2] = {kLow, kLow};                // groups `lane` and lane + 32
+    [[maybe_unused]] F second[2] = {0, 0};  // and their second choices, where those count
     for (int g = 0; g < c.groups; ++g) {
         F a = kLow, b = kLow;
 #pragma unroll
@@ -105,27 +111,41 @@ __device__ __forceinline__ bool drop_groups(const RouteCall& c, const F (&choice
                 }
             }
         }
-        const F s = warp_top(a, b, size > 1 ? c.group_top : 1);
-        if (lane == (g & 31)) mine[g >> 5] = s;
+        F b_top;
+        const F s = warp_top(a, b, both, &b_top);
+        if (lane == (g & 31)) {
+            mine[g >> 5] = s;
+            if (sizeof(F) == 4 && both) second[g >> 5] = b_top;
+        }
     }
     K gkey[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) gkey[i] = 32 * i + lane < c.groups ? key_of(mine[i]) : 0;
     uint64_t stays = 0;
-    F last = 0;
-    bool close = false;
-    for (int n = 0; n <= c.top_groups && n < c.groups; ++n) {
+    for (int n = 0; n < c.top_groups; ++n) {
         K top;
         int g;
         largest(gkey, lane, &top, &g);
-        const F v = __shfl_sync(kAll, (g >> 5) ? mine[1] : mine[0], g & 31);
-        if (n == c.top_groups) {  // the first that is out
-            close = !(last - v > near + static_cast<F>(0x1p-21) * fabs(last));
-            break;
-        }
-        last = v;
         stays |= uint64_t(1) << g;
         if (lane == (g & 31)) gkey[g >> 5] = 0;
+    }
+    bool close = false;
+    if constexpr (sizeof(F) == 4) {
+        // The most that a group that is out may be, and the least of one that stays.  (A sum past f32's range is the
+        // end of that range at least.  One that counts a masked expert is -infinity, or NaN, in any precision:
+        // out, it is above no other.)
+        uint32_t most = 0, least = 0;  // keys, of `least` the complement
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int g = 32 * i + lane;
+            if (g >= c.groups) continue;
+            const float at = fminf(fmaxf(mine[i], -FLT_MAX), FLT_MAX);  // (NaN: the lowest)
+            // (|a| <= |a + b| + |b|; and 2^-24 of the sum for the rounding of at +- by)
+            const float by = isfinite(mine[i]) ? near + 0x1.01p-23f * (2.f * fabsf(mine[i]) + fabsf(second[i])) : 0.f;
+            if ((stays >> g) & 1u) least = max(least, ~key_of(at - by));
+            else if ((both ? second[i] : mine[i]) != kLow) most = max(most, key_of(at + by));
+        }
+        close = c.top_groups < c.groups && warp_max(most) >= ~warp_max(least);
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -234,7 +254,7 @@ __device__ __noinline__ int select_f64(const RouteCall& c, const T* row, int lan
         key[i] = 0;
         if (e < c.experts) key[i] = key_of(c.bias ? choice[i] : static_cast<double>(logit(row + e)));
     }
-    if (c.groups > 1) drop_groups(c, choice, key, lane, 0.0);
+    if (c.groups > 1) drop_groups(c, choice, key, lane, 0.f);
     int n;
     return select(c, key, lane, -1.f, nullptr, &n);
 }
@@ -293,12 +313,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteCall c) {
         // Twice what a choice may be off by: a score s = exp(d) / sum by (|d| + 8) 2^-23 of
         // itself (d's rounding, exp's 2 units, the sum's PER + 5 roundings of terms that are
         // mostly small, the products), where s |d| is s_top / e at most; a sigmoid by 4 units.
-        // The bias adds a rounding of the choice (2^-24 of it), a group's sum of two doubles
-        // all of that.
+        // The bias adds a rounding of the choice (2^-24 of it).  A group's sum of two is off by
+        // `near` at most, and the roundings (drop_groups).
         near = 0x1p-22f * (c.sigmoid ? 4.f * s_top : (9.f + PER) * s_top);
     }
     bool again = false;
-    if (c.groups > 1) again = drop_groups(c, choice, key, lane, 2.f * near);
+    if (c.groups > 1) again = drop_groups(c, choice, key, lane, near);
     // Logits are compared as they are.
     int n;
     int id = select(c, key, lane, c.bias && !again ? near : -1.f, &ordered, &n);

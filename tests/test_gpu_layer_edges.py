@@ -23,3 +23,32 @@ def test_experts_whose_gate_is_up(qm, tokens, kind, dtype):  # noqa: F811
     b.gate = b.up
     b.handle = qm.Experts(b.up, b.up, b.down, activation=kind)
     b.check(*b.rows(tokens, 2, dtype))
+
+
+# ---- routing
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("size", [5.0, 300.0, 3e4])
+def test_route_groups_of_large_biases(qm, size, sigmoid):  # noqa: F811
+    """Groups whose two choices are far larger than their sum: f32 loses of the choices what tells the sums apart.
+    All experts of the groups that stay are chosen."""
+    gen = generator(31)
+    logits = torch.randn((300, 128), generator=gen)
+    bias = torch.tensor([size, -size]).repeat(64).cuda()
+    check_route(qm, logits.cuda(), 32, bias=bias, sigmoid=sigmoid, groups=64, top_groups=16)
+    check_route(qm, logits.cuda(), 32, bias=bias, sigmoid=sigmoid, groups=64, top_groups=16, group_top=1)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(F32).min, -3e38, 3e38])
+def test_route_groups_of_extreme_biases(qm, low, sigmoid):  # noqa: F811
+    """Groups masked in part or whole by biases whose sums f32 holds, loses everything in, or cannot hold."""
+    gen = generator(32)
+    logits = torch.randn((40, 64), generator=gen)
+    bias = torch.zeros((16, 4))
+    bias[::3] = low
+    bias[1::3, 1:] = low
+    bias = bias.reshape(-1).cuda()
+    for top_groups in (2, 8, 13):
+        for group_top in (1, 2):
+            check_route(qm, logits.cuda(), 4, bias=bias, sigmoid=sigmoid, groups=16, top_groups=top_groups, group_top=group_top)
