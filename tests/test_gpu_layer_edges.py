@@ -52,3 +52,24 @@ def test_route_groups_of_extreme_biases(qm, low, sigmoid):  # noqa: F811
     for top_groups in (2, 8, 13):
         for group_top in (1, 2):
             check_route(qm, logits.cuda(), 4, bias=bias, sigmoid=sigmoid, groups=16, top_groups=top_groups, group_top=group_top)
+
+
+def test_route_weights_of_small_scores(qm):  # noqa: F811
+    """Scores below f32's range have weights all the same where they are divided by their sum."""
+    gen = generator(33)
+    logits = torch.randn((50, 40), generator=gen)
+    for at in (-60.0, -85.0, -88.0, -95.0, -110.0, -300.0, -600.0):
+        check_route(qm, (logits + at).cuda(), 5, sigmoid=True, scale=2.5)
+        check_route(qm, (logits + at).cuda(), 5, sigmoid=True, groups=4, top_groups=2)
+    # Experts that their biases choose, far below the largest.
+    for at in (-60.0, -100.0, -300.0):
+        for sigmoid in (False, True):
+            far = logits.clone()
+            far[:, 10:] += at
+            bias = torch.zeros(40)
+            bias[10:20] = 4 + torch.randperm(10, generator=gen).float()
+            check_route(qm, far.cuda(), 5, bias=bias.cuda(), sigmoid=sigmoid)
+    # Below f64's, and masked: 0 (the formula's sum is).
+    for at in (-1e4, -math.inf):
+        _, weights = qm.qm_route_experts(torch.full((3, 40), at, device="cuda"), 5, scoring=qm.QM_SCORE_SIGMOID)
+        assert (weights == 0).all()
