@@ -907,7 +907,7 @@ class Experts:
     32 * 18]``, ``w_down`` uint8 ``[n_experts, hidden, inner / 32 * 18]``.  An expert's matrix is
     contiguous; the experts may be strided, so gate and up may be halves of one
     tensor.  Keeps the tensors alive, and one workspace for each stream it is
-    used on (see qm_experts_q4_0)."""
+    used on (see qm_experts_q4_0).  Threads may share it, on one stream too."""
 
     def __init__(self, w_gate, w_up, w_down, activation: int = QM_ACT_SILU):
         import torch
@@ -934,6 +934,9 @@ class Experts:
         self.ref = ctypes.addressof(self.struct)
         self._workspaces = {}
         self._sizes = {}
+        # Held from the choice of a workspace until the call's kernels are enqueued: those of another call on
+        # the same stream, from another thread, would come between them.
+        self._lock = threading.Lock()
 
     def _workspace(self, n_tokens: int, top_k: int, stream: int, current: bool):
         need = self._sizes.get((n_tokens, top_k))
@@ -973,7 +976,8 @@ def qm_experts_q4_0(experts, x, ids, weights, out=None, stream=None, workspace=N
     ``[tokens, top_k]``); what qm_route_experts gives.
 
     ``workspace``: a uint8 tensor of at least ``qm_experts_workspace`` bytes; calls that
-    cannot run at the same time can share it, those of other layers too.  Without it the
+    cannot run at the same time, and that one thread makes after the other, can share it, those of
+    other layers too.  Without it the
     experts have their own, one per stream, kept at its largest size; a call that is
     captured into a CUDA graph gets one from the graph's memory."""
     torch = _torch or _torch_module()
@@ -991,12 +995,17 @@ def qm_experts_q4_0(experts, x, ids, weights, out=None, stream=None, workspace=N
     else:
         os_ = _matrix(out, "out", experts.hidden, x)[1]
     handle = _stream_handle(stream)
+
+    def call(ws):
+        args = _EXPERTS_ARGS.pack(x.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(),
+                                  tokens, xs, os_, top_k, code)
+        return load_library().qm_experts_q4_0(experts.ref, args, handle)
+
     if workspace is None:
-        ws = experts._workspace(tokens, top_k, handle, stream is None)
+        with experts._lock:
+            rc = call(experts._workspace(tokens, top_k, handle, stream is None))
     else:
-        ws = workspace
-        _require(ws, torch.uint8, "workspace")
-    args = _EXPERTS_ARGS.pack(x.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(),
-                              tokens, xs, os_, top_k, code)
-    _check(load_library().qm_experts_q4_0(experts.ref, args, handle), "qm_experts_q4_0")
+        _require(workspace, torch.uint8, "workspace")
+        rc = call(workspace)
+    _check(rc, "qm_experts_q4_0")
     return out

@@ -649,8 +649,10 @@ QM_API int qm_route_experts(const qm_route_args* args, void* stream);
  *   weights   : [n_tokens][top_k] f32.
  *   workspace : qm_experts_workspace bytes, 16-byte aligned; its contents do not
  *               matter before or after a call.  Calls that may run at the same
- *               time need a workspace each, and one that a CUDA graph uses lives
- *               as long as the graph.
+ *               time need a workspace each, and so do calls that threads make at
+ *               the same time, on one stream too (a call is several kernels, and
+ *               another's may come between them).  One that a CUDA graph uses
+ *               lives as long as the graph.
  * Precision: sums in f32, the inner activations in f32; for QM_F32 products to
  * about 2^-21 of |x_k w_k|, and 2^-38 of the row's largest |x| times |w_k|; for
  * QM_BF16 weights rounded to 11 bits, and inner activations to 11 bits (or 2^-38

@@ -73,3 +73,25 @@ def test_route_weights_of_small_scores(qm):  # noqa: F811
     for at in (-1e4, -math.inf):
         _, weights = qm.qm_route_experts(torch.full((3, 40), at, device="cuda"), 5, scoring=qm.QM_SCORE_SIGMOID)
         assert (weights == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_experts_of_threads_on_one_stream(qm, dtype):  # noqa: F811
+    """Threads that call the same experts on the same stream, each with rows of its own."""
+    import threading
+    b = Block(qm, 8, 512, 320, seed=40)
+    calls = [b.rows(tokens, 2, dtype, skew=1.0) for tokens in (1, 30, 64, 300)]
+    want = [qm.qm_experts_q4_0(b.handle, *c) for c in calls]
+    torch.cuda.synchronize()
+    wrong = [0] * len(calls)
+    stream = torch.cuda.current_stream()
+
+    def work(i):
+        for _ in range(60):
+            wrong[i] += not torch.equal(qm.qm_experts_q4_0(b.handle, *calls[i], stream=stream), want[i])
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0] * len(calls)
