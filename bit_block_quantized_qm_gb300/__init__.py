@@ -562,7 +562,8 @@ class KVCache:
     ``[n_seqs, pages]``, ``lengths`` int32 ``[n_seqs]``.  ``max_len`` bounds the
     lengths (default, and at most: what the page table can hold); a tighter
     bound may be set at any time and gives smaller launches.  Keeps the tensors alive, and
-    one attention workspace for each stream it is used on (see qm_attn_q4_0)."""
+    one attention workspace for each stream it is used on (see qm_attn_q4_0).  Threads may attend to it at the
+    same time, on one stream too."""
 
     def __init__(self, k_pages, v_pages, page_table, lengths, head_dim: int, page_tokens: int, max_len=None):
         import torch
@@ -589,6 +590,7 @@ class KVCache:
         self.max_len = self.capacity if max_len is None else max_len
         self._workspaces = {}
         self._sizes = {}
+        self._lock = threading.Lock()  # (see Experts)
 
     @property
     def max_len(self) -> int:
@@ -759,18 +761,23 @@ def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts
     elif max_q is None:
         max_q = n_tokens
     handle = _stream_handle(stream)
+
+    def call(ws):
+        # (The struct's bytes; filling a ctypes object field by field takes 2 us more.)
+        args = _ATTN_ARGS.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
+                               weights.data_ptr() if weights is not None else 0, starts,
+                               ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0, n_tokens, max_q,
+                               qs, os_, ws_stride, window, sinks, n_heads,
+                               cache.head_dim ** -0.5 if scale is None else scale, code, 0)
+        return load_library().qm_attn_q4_0(cache.ref, args, handle)
+
     if workspace is None:
-        ws = cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle, stream is None)
+        with cache._lock:
+            rc = call(cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle, stream is None))
     else:
-        ws = workspace
-        _require(ws, torch.uint8, "workspace")
-    # (The struct's bytes; filling a ctypes object field by field takes 2 us more.)
-    args = _ATTN_ARGS.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
-                           weights.data_ptr() if weights is not None else 0, starts,
-                           ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0, n_tokens, max_q,
-                           qs, os_, ws_stride, window, sinks, n_heads,
-                           cache.head_dim ** -0.5 if scale is None else scale, code, 0)
-    _check(load_library().qm_attn_q4_0(cache.ref, args, handle), "qm_attn_q4_0")
+        _require(workspace, torch.uint8, "workspace")
+        rc = call(workspace)
+    _check(rc, "qm_attn_q4_0")
     return out if lse is None else (out, lse)
 
 

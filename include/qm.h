@@ -461,7 +461,9 @@ QM_API int qm_kv_read_q4_0(const qm_kv_cache* cache, float* k, float* v, int64_t
  *              QM_ATTN_WORKSPACE_ZEROED bytes zeroed once before its first use;
  *              every call leaves it fit for the next one, of this cache or
  *              another.  Calls that may run at the same time need a workspace
- *              each, and one that a CUDA graph uses lives as long as the graph.
+ *              each, and so do calls that threads make at the same time, on one
+ *              stream too (a call may be several kernels).  One that a CUDA graph
+ *              uses lives as long as the graph.
  * Precision: scores, statistics and sums in f32; products to about 2^-21 of
  * each |q_i k_i| and |p_j v_j| for QM_F32 (2^-17 of a |p_j v_j| that is 2^-18 of
  * the largest of the tokens around it, and less); for QM_BF16, where the output

@@ -95,3 +95,37 @@ def test_experts_of_threads_on_one_stream(qm, dtype):  # noqa: F811
     for t in threads:
         t.join()
     assert wrong == [0] * len(calls)
+
+
+# ---- the key/value cache
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_attention_of_threads_on_one_stream(qm, dtype):  # noqa: F811
+    """Threads that attend to the same cache on the same stream: single tokens and prompts whose rows are done again,
+    with weights and without."""
+    import threading
+
+    from test_gpu_kv_cache import device, to_dtype
+    from test_gpu_kv_safety import sharp
+    c, q = sharp(300, 90)
+    cache = device(qm, c)
+    qs = [to_dtype(q[-new:], dtype) for new in (1, 90, 1, 40)]
+
+    def attend(i, stream=None):
+        w = torch.zeros((1, 1, cache.max_len), device="cuda") if i > 1 else None
+        out = qm.qm_attn_q4_0(cache, qs[i], weights=w, stream=stream)
+        return (out,) if w is None else (out, w)
+    want = [attend(i) for i in range(4)]
+    torch.cuda.synchronize()
+    wrong = [0] * 4
+    stream = torch.cuda.current_stream()
+
+    def work(i):
+        for _ in range(60):
+            wrong[i] += not all(torch.equal(a, b) for a, b in zip(attend(i, stream), want[i]))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0] * 4

@@ -86,3 +86,14 @@ def test_experts_of_two_threads(patched):
     run(lambda: qm.qm_experts_q4_0(experts, x, ids, weights, out=out))
     assert w.calls == 16 and not w.met
     assert len(experts._workspaces) == 1
+
+
+def test_attention_of_two_threads(patched):
+    w = patched("qm_attn_q4_0", qm._ATTN_ARGS, 5)
+    pages = [on_gpu(9, 1, qm.kv_page_bytes(64, 64), dtype=torch.uint8) for _ in range(2)]
+    cache = qm.KVCache(*pages, on_gpu(2, 4, dtype=torch.int32), on_gpu(2, dtype=torch.int32), head_dim=64, page_tokens=64)
+    q, out = on_gpu(2, 2, 64, dtype=torch.float32), on_gpu(2, 2, 64, dtype=torch.float32)
+    weights = on_gpu(2, 1, 256, dtype=torch.float32)
+    run(lambda: qm.qm_attn_q4_0(cache, q, out=out, weights=weights))
+    assert w.calls == 16 and not w.met
+    assert len(cache._workspaces) == 1
