@@ -384,9 +384,10 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
         if (err != cudaSuccess) return err;
         note_launch();
     }
-    ExpertsMm m = {starts, floats(at.x_unit), inner, floats(at.split), counters, c.err,
-                   {e.gate ? e.gate : e.up, e.up}, {e.gate ? e.gate_stride : e.up_stride, e.up_stride},
-                   e.n, e.hidden, e.inner, e.activation, at.split_cols, 0x64006400u, e.gate != nullptr, false};
+    const uint8_t* const gate = e.gate ? e.gate : e.up;
+    ExpertsMm m = {starts, floats(at.x_unit), inner, floats(at.split), counters, c.err, {e.gate ? nullptr : e.up, e.up},
+                   {e.gate ? e.gate_stride : e.up_stride, e.up_stride}, e.n, e.hidden, e.inner, e.activation, at.split_cols,
+                   0x64006400u, false, {gate, e.up}};
     // Few rows an expert: experts_few.cu (16 experts of 4096 x 4096, 8 rows each: bf16 127 us against 143, f32
     // 191 against 221; 12 rows each: 152 against 141, 244 against 219).
     const bool few = pairs <= 8 * static_cast<int64_t>(e.n);
@@ -406,7 +407,7 @@ cudaError_t launch_type(const ExpertsView& e, const ExpertsCall& c, const Device
     if (err != cudaSuccess) return err;
     note_launch();
     m = {starts, floats(at.i_unit), part, floats(at.split), counters + kCounters, c.err, {e.down, e.down},
-         {e.down_stride, e.down_stride}, e.n, e.inner, e.hidden, QM_ACT_NONE, at.split_cols, 0x64006400u, false, true};
+         {e.down_stride, e.down_stride}, e.n, e.inner, e.hidden, QM_ACT_NONE, at.split_cols, 0x64006400u, true, {e.down, e.down}};
     if ((err = products(true, i_hi, i_lo)) != cudaSuccess) return err;
     err = launch_pdl(experts_combine<T>, dim3((e.hidden + 511) / 512, c.n_tokens < 4096 ? c.n_tokens : 4096), dim3(128), 0,
                      stream, e, c, starts, place, inner, part);

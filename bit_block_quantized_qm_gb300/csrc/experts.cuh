@@ -25,14 +25,15 @@ struct ExpertsMm {
     float* split;           // partial sums of tiles that several CTAs share
     unsigned* counters;     // and how much of each is there
     unsigned int* err;
-    const uint8_t* w[2];    // the matrices of a tile's two halves
-    int64_t w_stride[2];    // bytes
+    const void* half[2];    // what a tile's two halves are of: equal for one matrix, different for gate and up (also
+                            // where those are the same memory).  Not read
+    int64_t w_stride[2];    // bytes from an expert's matrix to the next
     int n, K, rows;
     int activation;
     int split_cols;         // columns of a partial tile
     uint32_t k1024;         // 0x64006400
-    bool gated;             // the halves are gate and up, whose products are multiplied (which may be one matrix)
     bool early;             // (few rows) this kernel may read weights and `starts` before its wait
+    const uint8_t* w[2];    // the halves' matrices
 };
 
 // Values of f16 pieces per row: the contraction's length, padded to whole 128-byte lines.

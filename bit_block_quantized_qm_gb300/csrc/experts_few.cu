@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         grid_dependency_wait();
         grid_launch_dependents();
     }
-    const bool two = m.gated;
+    const bool two = m.half[0] != m.half[1];  // gate and up
     const int block_rows = two ? kExpertHalf : 2 * kExpertHalf;
     const int blocks = (m.rows + block_rows - 1) / block_rows;
     for (int e = threadIdx.x; e <= m.n; e += kThreads) rows_before[e] = __ldcg(m.starts + e);

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_launch_dependents();
     const uint32_t tmem = tmem_slot;
 
-    const bool two = m.gated;
+    const bool two = m.half[0] != m.half[1];  // gate and up (a flag would cost registers: f32 rows' tiles of 64 would spill)
     const int block_rows = two ? kHalf : 2 * kHalf;
     const int blocks = (m.rows + block_rows * C::kPair - 1) / (block_rows * C::kPair);  // (of a pair)
     const int rank = C::kPair > 1 ? static_cast<int>(blockIdx.x & 1) : 0;
