@@ -68,7 +68,7 @@ __device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce
 
 // What a CTA does, one piece after the other: tiles, each with a range of units.
 struct Plan {
-    int tiles, full, rest, ku, ctas, cta;  // (of pairs of CTAs where they come in pairs)
+    int tiles, full, rest, ku, ctas, cta;
     int each, more;  // units of shared tiles that a CTA has, and how many CTAs have one more
     bool share;  // the tiles left over are shared by all CTAs
     __device__ __forceinline__ int unit_of(int c) const { return c * each + min(c, more); }  // (without a division: it is cold code)

@@ -4,11 +4,11 @@
 // 256 weight rows (128 of gate and 128 of up, or 256 of one matrix) by up to 128 rows of
 // one expert, rounded up to 16.
 //
-// Bound: many rows, the tensor cores (8192 rows through 8 experts of 14336 x 4096, three products:
-// 2.13 ms in all, 1340 TFLOP/s; an instruction with 128 columns takes 64 cycles, one with 16 nine);
-// fewer, the unpacking: 8 weights of each lane of a warp take 21 cycles, fp16 and integer
-// instructions going at half rate, and a unit (256 rows by 256 of K) 1340, where memory would
-// bring one every 1570.
+// Bound: many rows, what L2 gives an SM, some 32 bytes a cycle, for token rows that every CTA loads for
+// itself (8192 rows through 8 experts of 14336 x 4096, three products: 2.46 ms in all, 1170 TFLOP/s; an
+// instruction with 128 columns takes 64 cycles, one with 16 nine); fewer, the unpacking: 8 weights of
+// each lane of a warp take 21 cycles, fp16 and integer instructions going at half rate, and a unit (256
+// rows by 256 of K) 1340, where memory would bring one every 1570.
 //
 //   D[w][t] = sum_k (q_wk - 8) d_wb  x_tk
 //
@@ -74,12 +74,9 @@ struct Cfg {
     static constexpr bool kMoveRegs = F32 && kTokens > 32;
     static constexpr int kLaunchRegs = 96, kDecodeRegs = 112, kOtherRegs = 32;
     static_assert(kDecodeWarps * kDecodeRegs + 4 * kOtherRegs <= 20 * kLaunchRegs, "a warp would wait for ever");
-    // CTAs come in pairs that take the same token rows (and blocks of weights next to each other):
-    // each loads half of them for both (1357 TFLOP/s against 1190: L2 gives an SM some 32 bytes a cycle).
-    static constexpr int kPair = !F32 && kTokens > 32 ? 2 : 1;
     // Sharing the tiles left over saves ku (ctas - rest) / ctas units, and the joining costs what this many do
-    // (64 experts of 2048 x 1408, 64 bf16 rows each: shared above 1 saved 191 us, above 9 176; 32 f32 rows
-    // each: above 1 236, above 6 250).
+    // (16 experts of 4096 x 4096, 64 bf16 rows each: shared above 4 saved 181 us, above 9 177; 2 of 8192 x 2048,
+    // 512 each: 156 and 145; 64 of 2048 x 1408, 32 f32 rows each: above 1 236, above 6 250).
     static constexpr int kJoinUnits = F32 ? 2 : 9;
     // Stages of unpacked weights, 128 columns of TMEM (bf16 rows: 128 elements, f32 rows: 64), and of
     // the token rows that they meet.  Long ones, because an issuing warp takes 300 cycles and more for a
@@ -90,11 +87,12 @@ struct Cfg {
     static constexpr int kPitch = WIDE ? 176 : 144;  // bytes of a raw row in shared memory, an odd number of 16s
     static constexpr int kRawBytes = 2 * kHalf * kPitch;
     static constexpr int kTokenBytes = 2 * kTokens * 128;  // bf16 rows: two panels of 64 elements, f32 rows: two pieces
-    // Narrow tiles: a stage of weights and its token rows have one barrier.  Pairs: the token rows have
-    // stages of their own, further ahead.
-    static constexpr bool kJoint = kPair == 1;
+    // Narrow tiles: a stage of weights and its token rows have one barrier.  Wide ones of bf16 rows: the
+    // token rows have stages of their own, further ahead (4096 tokens through 2 of 8 of 14336 x 4096: 2460 us
+    // against 2530 with one barrier).
+    static constexpr bool kJoint = F32 || kTokens <= 32;
     static constexpr int kTokenStages = kJoint ? kStages : WIDE ? 2 : 3;
-    static constexpr int kRawStages = WIDE || kPair > 1 ? 3 : 4;
+    static constexpr int kRawStages = WIDE || !kJoint ? 3 : 4;
     static constexpr int kSmem = kRawStages * kRawBytes + kTokenStages * kTokenBytes + 1024;
     static_assert(kTmemA % 128 == 0 && kStages >= 2, "room for the weights");
 };
@@ -115,25 +113,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, uint64_t* b,
     atomicOr(err, kErrWaitTimeout);
     return false;
 }
-// A TMA box into the same place of both CTAs of a pair, and an arrival of each on its barrier.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-// Products done: an arrival on the barrier of both CTAs of a pair.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t lead) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
-            smem_addr(bar)),
-        "r"(lead), "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -233,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.tok_full[i], 1);
-            mbar_init(&bar.tok_empty[i], 2 * C::kPair);  // the products of both halves of both CTAs
+            mbar_init(&bar.tok_empty[i], 2);  // the products of both halves
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.acc_full[i], 2);
@@ -274,20 +253,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // (Every CTA's barriers are initialised before the other of a pair can arrive on them.)
-    if constexpr (C::kPair > 1) cluster_sync_all();
     grid_launch_dependents();
     const uint32_t tmem = tmem_slot;
 
     const bool two = m.half[0] != m.half[1];  // gate and up (a flag would cost registers: f32 rows' tiles of 64 would spill)
     const int block_rows = two ? kHalf : 2 * kHalf;
-    const int blocks = (m.rows + block_rows * C::kPair - 1) / (block_rows * C::kPair);  // (of a pair)
-    const int rank = C::kPair > 1 ? static_cast<int>(blockIdx.x & 1) : 0;
+    const int blocks = (m.rows + block_rows - 1) / block_rows;
     if (threadIdx.x == 0) {
         Plan p;
         p.tiles = tiles_before[m.n] * blocks;
-        p.ctas = gridDim.x / C::kPair;
-        p.cta = blockIdx.x / C::kPair;
+        p.ctas = gridDim.x;
+        p.cta = blockIdx.x;
         p.ku = (m.K + 255) / 256;
         p.full = p.tiles / p.ctas * p.ctas;
         p.rest = p.tiles - p.full;
@@ -307,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Place p;
         p.expert = uniform(lo);
-        p.block = (tile - tt * blocks) * C::kPair + rank;
+        p.block = tile - tt * blocks;
         p.p0 = uniform(rows_before[lo] + (tt - tiles_before[lo]) * C::kTokens);
         p.n = uniform(min(C::kTokens, rows_before[lo + 1] - p.p0));
         return p;
@@ -507,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t place_floats = static_cast<int64_t>(2 * kHalf) * m.split_cols;
             const int shared_tile = tile - plan.full;
             auto part_of = [&](int c) {  // CTA c's part of this tile
-                return m.split + ((2 * c + (plan.unit_of(c) < shared_tile * plan.ku)) * C::kPair + rank) * place_floats;
+                return m.split + (2 * c + (plan.unit_of(c) < shared_tile * plan.ku)) * place_floats;
             };
             float* mine = part_of(plan.cta);
             for (int ch = group; kChunk * ch < pl.n; ch += 4) {
@@ -523,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_barrier_sync(1, kDecodeWarps * 32);
             if (threadIdx.x == 0) {
                 const unsigned n = static_cast<unsigned>(n_units);
-                last_of_tile = atom_add_acq_rel(&m.counters[shared_tile * C::kPair + rank], n) + n == static_cast<unsigned>(plan.ku);
+                last_of_tile = atom_add_acq_rel(&m.counters[shared_tile], n) + n == static_cast<unsigned>(plan.ku);
             }
             named_barrier_sync(1, kDecodeWarps * 32);
             if (!last_of_tile) return;
@@ -649,19 +625,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int parts = k >= m.K ? 0 : F32 || k + 64 < m.K ? 2 : 1;  // (a row's last stage may be half one, or none)
                 if (lane == 0) mbar_arrive_expect_tx(full, parts * n16 * 128);
                 __syncwarp();
-                // Lane i: 16 rows; of a pair's CTAs one takes the even ones, one the odd ones.
+                // Lane i: 16 rows.
                 uint8_t* dst = tok + stage * C::kTokenBytes + lane * 2048;
-                if (16 * lane < n16 && parts > 0 && (C::kPair == 1 || (lane & 1) == rank)) {
+                if (16 * lane < n16 && parts > 0) {
                     const int p = pl.p0 + 16 * lane;
                     const CUtensorMap* second = F32 ? &map_lo : &map_hi;
                     const int k2 = F32 ? k : k + 64;
-                    if constexpr (C::kPair > 1) {
-                        tma_load_2d_pair(dst, &map_hi, k, p, full);
-                        if (parts > 1) tma_load_2d_pair(dst + C::kTokens * 128, second, k2, p, full);
-                    } else {
-                        tma_load_2d(dst, &map_hi, k, p, full);
-                        if (parts > 1) tma_load_2d(dst + (F32 ? n16 : C::kTokens) * 128, second, k2, p, full);
-                    }
+                    tma_load_2d(dst, &map_hi, k, p, full);
+                    if (parts > 1) tma_load_2d(dst + (F32 ? n16 : C::kTokens) * 128, second, k2, p, full);
                 }
                 __syncwarp();
                 ++kt;
@@ -720,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++stage == C::kStages) stage = 0, ++round;
                 if constexpr (!C::kJoint) {
                     if (k < m.K) {
-                        mma_commit_pair(&bar.tok_empty[t_stage], lead);
+                        mma_commit(&bar.tok_empty[t_stage], lead);
                         if (++t_stage == C::kTokenStages) t_stage = 0, ++t_round;
                     }
                 }
@@ -741,9 +712,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // Neither CTA of a pair leaves while the other may still write to its shared memory.  (Every thread
-    // comes here, whatever its waits returned.)
-    if constexpr (C::kPair > 1) cluster_sync_all();
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
@@ -767,13 +735,8 @@ cudaError_t launch_kernel(const ExpertsMm& m, const ExpertsView& e, const void* 
                            CU_TENSOR_MAP_SWIZZLE_128B);
         if (err != cudaSuccess) return err;
     }
-    const int ctas = (dev.sm_count < kExpertCtas ? dev.sm_count : kExpertCtas) / C::kPair * C::kPair;
-    if constexpr (C::kPair > 1)
-        err = launch_pdl_cluster(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, C::kPair,
-                                 w0, w1, t_hi, t_lo, m);
-    else
-        err = launch_pdl(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi,
-                         t_lo, m);
+    const int ctas = dev.sm_count < kExpertCtas ? dev.sm_count : kExpertCtas;
+    err = launch_pdl(experts_mm_kernel<F32, TOKENS, DOWN, WIDE>, dim3(ctas), dim3(kThreads), C::kSmem, stream, w0, w1, t_hi, t_lo, m);
     if (err == cudaSuccess) note_launch();
     return err;
 }
@@ -791,8 +754,8 @@ cudaError_t launch_experts_mm(const ExpertsMm& m, const ExpertsView& e, bool dow
         return wide ? run(launch_kernel<kF32, kTokens, false, true>) : run(launch_kernel<kF32, kTokens, false, false>);
     };
     // Narrow tiles where experts have few rows: three stages of weights, bf16 rows two sets of sums (16 experts of
-    // 4096 x 4096 with 24 rows each: bf16 152 us against 162, f32 249 against 292; with 32 rows each 201 against 166,
-    // 331 against 310).
+    // 4096 x 4096 with 24 rows each: bf16 146 us against 157, f32 249 against 292; with more, some experts' rows
+    // take two tiles: 48 bf16 rows each 247 against 168, uneven f32 rows, 32 on average, 331 against 310).
     const bool narrow = n_pieces <= 24 * static_cast<int64_t>(e.n);
     if (type == KvType::kF32)
         return narrow ? go(std::true_type{}, std::integral_constant<int, 32>{}) : go(std::true_type{}, std::integral_constant<int, 64>{});
