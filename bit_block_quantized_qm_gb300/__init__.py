@@ -918,6 +918,10 @@ class Experts:
 
     def __init__(self, w_gate, w_up, w_down, activation: int = QM_ACT_SILU):
         import torch
+        if not isinstance(w_up, torch.Tensor):
+            raise TypeError("w_up must be a torch.uint8 tensor")
+        if w_up.dim() != 3:
+            raise ValueError("w_up must be 3-D [n_experts, inner, hidden / 32 * 18]")
         n, inner = w_up.shape[0], w_up.shape[1]
         hidden = w_up.shape[2] // BLOCK_BYTES * BLOCK_ELEMS
         row, row_down = hidden // BLOCK_ELEMS * BLOCK_BYTES, inner // BLOCK_ELEMS * BLOCK_BYTES
