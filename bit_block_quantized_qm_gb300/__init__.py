@@ -346,6 +346,7 @@ def qm_gemv_q4_0_q8act_list_ptr(problems, M: int, counters: int = 0, stream: int
 # ------------------------------------------------------------ torch tensors
 
 _torch = None
+_UNSHARED = contextlib.nullcontext()  # in a lock's place, where the workspace is the caller's
 
 
 def _torch_module():
@@ -761,22 +762,19 @@ def qm_attn_q4_0(cache, q, scale=None, window: int = 0, sinks: int = 0, q_starts
     elif max_q is None:
         max_q = n_tokens
     handle = _stream_handle(stream)
-
-    def call(ws):
+    with cache._lock if workspace is None else _UNSHARED:
+        if workspace is None:
+            ws = cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle, stream is None)
+        else:
+            ws = workspace
+            _require(ws, torch.uint8, "workspace")
         # (The struct's bytes; filling a ctypes object field by field takes 2 us more.)
         args = _ATTN_ARGS.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
                                weights.data_ptr() if weights is not None else 0, starts,
                                ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0, n_tokens, max_q,
                                qs, os_, ws_stride, window, sinks, n_heads,
                                cache.head_dim ** -0.5 if scale is None else scale, code, 0)
-        return load_library().qm_attn_q4_0(cache.ref, args, handle)
-
-    if workspace is None:
-        with cache._lock:
-            rc = call(cache._workspace(n_heads, n_tokens, max_q, weights is not None, handle, stream is None))
-    else:
-        _require(workspace, torch.uint8, "workspace")
-        rc = call(workspace)
+        rc = load_library().qm_attn_q4_0(cache.ref, args, handle)
     _check(rc, "qm_attn_q4_0")
     return out if lse is None else (out, lse)
 
@@ -1006,17 +1004,14 @@ def qm_experts_q4_0(experts, x, ids, weights, out=None, stream=None, workspace=N
     else:
         os_ = _matrix(out, "out", experts.hidden, x)[1]
     handle = _stream_handle(stream)
-
-    def call(ws):
+    with experts._lock if workspace is None else _UNSHARED:
+        if workspace is None:
+            ws = experts._workspace(tokens, top_k, handle, stream is None)
+        else:
+            ws = workspace
+            _require(ws, torch.uint8, "workspace")
         args = _EXPERTS_ARGS.pack(x.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(),
                                   tokens, xs, os_, top_k, code)
-        return load_library().qm_experts_q4_0(experts.ref, args, handle)
-
-    if workspace is None:
-        with experts._lock:
-            rc = call(experts._workspace(tokens, top_k, handle, stream is None))
-    else:
-        _require(workspace, torch.uint8, "workspace")
-        rc = call(workspace)
+        rc = load_library().qm_experts_q4_0(experts.ref, args, handle)
     _check(rc, "qm_experts_q4_0")
     return out
