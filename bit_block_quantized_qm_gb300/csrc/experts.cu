@@ -288,7 +288,9 @@ struct Mend {
     }
 };
 
-// The inner activations as pieces, those that are not finite taken again first.
+// The inner activations as pieces, those that are not finite taken again first.  bf16 calls: one piece, 11 bits,
+// whose rounding (2^-11, as that of the weights where rows are many) is an eighth of the output's own; a second
+// piece would be another product.
 template <int THREADS, typename T>
 __global__ void __launch_bounds__(THREADS)
     experts_inner(const ExpertsView e, const ExpertsCall c, float* inner, const int32_t* starts, const int32_t* order, __half* hi,

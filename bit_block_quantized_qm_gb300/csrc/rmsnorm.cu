@@ -4,7 +4,8 @@
 // bf16 with a residual and both outputs, 268 MB: 42 us, 6.4 TB/s; f32: 80 us, 6.7 TB/s);
 // few rows: the latency of one load, one reduction over the CTA and one store (600 rows:
 // 4 us).  A row belongs to one CTA, whose threads keep their 8 (or 16, 32) elements of it
-// in registers between the sum of squares and the outputs.  Statistics and products are f32;
+// in registers between the sum of squares and the outputs (but for 19 words of a thread with 32 f32 elements,
+// beside its weights and the next row's; those come back from L1).  Statistics and products are f32;
 // outputs are rounded once.  The row's Q8_0 blocks are made from the f32 values by
 // four lanes a block, as quantize_q8_0 does.
 #include <cuda_bf16.h>

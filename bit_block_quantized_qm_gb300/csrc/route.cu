@@ -10,7 +10,7 @@
 // again in f64.  So the ids are those of the formula and not of a rounding; without a
 // bias the logits themselves are compared, which is exact.  (f64 is slow here: a row
 // done again takes some 10 us, and one in a thousand asks for it; with the few of them
-// in order by themselves 4096 tokens, 256 experts in 8 groups take 19 us against 34.)
+// in order by themselves 4096 tokens, 256 experts in 8 groups take 18 us against 34.)
 #include <cuda_bf16.h>
 
 #include <cfloat>

@@ -558,8 +558,8 @@ QM_API int qm_kv_evict_q4_0(const qm_kv_cache* from, const qm_kv_cache* to, cons
  *              needs width % 32 == 0.
  *   width    : 1 .. 2^20.  Rows of 8 elements' multiples, 16-byte aligned, take
  *              the fast path.
- * A row whose squares pass f32's range, or that holds infinities or NaN, gives
- * what f32 arithmetic makes of the formula.  Deterministic.
+ * A row whose squares leave f32's range at either end, or that holds infinities
+ * or NaN, gives what f32 arithmetic makes of the formula.  Deterministic.
  * Returns QM_OK or a negative status.
  */
 typedef struct qm_rmsnorm_args {
