@@ -363,8 +363,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasOf<PER>) route_kernel(const 
         float sum = w;
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-        // (Scores near the end of f32's range have few bits there, or none.)
-        if (sum < 0x1p-100f) return small_weights<T>(c, t, lane, id, mx);
+        // (Scores near the end of f32's range have few bits there, or none: they lose 2^-128 at most, and
+        // weights so 2^-102.)
+        if (sum < 0x1p-26f) return small_weights<T>(c, t, lane, id, mx);
         w /= sum;
     }
     if (lane < c.top_k) {

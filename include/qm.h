@@ -590,8 +590,8 @@ QM_API int qm_add_rmsnorm(const qm_rmsnorm_args* args, void* stream);
  * as its group_top (1 or 2) largest choices together, and the experts of all
  * but the top_groups largest groups are out.  ids get the top_k experts of the
  * largest choices, largest first; weights their scores (without the bias),
- * divided by their sum with `renormalize` (0 where that is 0; a sum near the end of
- * f32's range is taken again in f64), times `scale`.
+ * divided by their sum with `renormalize` (0 where that is 0; sums below 2^-26 are
+ * taken again in f64, so that small scores keep their bits), times `scale`.
  * Equal choices, and equal groups, go to the lower index; without a bias the
  * experts' order is that of the logits.  Choices that lie so close that f32
  * could turn them around are compared in f64.

@@ -129,3 +129,16 @@ def test_attention_of_threads_on_one_stream(qm, dtype):  # noqa: F811
     for t in threads:
         t.join()
     assert wrong == [0] * 4
+
+
+@pytest.mark.parametrize("at", [-20.0, -65.0, -80.0, -95.0])
+def test_route_weights_of_scores_far_apart(qm, at):  # noqa: F811
+    """Chosen scores of which some are below f32's range and their sum is not.  The bound is check_route's, and 2^-102:
+    a score of f32 is off by 2^-128 at most (1 / (1 + exp(88.8)) comes out 0), divided by a sum of 2^-26 and more."""
+    logits = (at + 12 * torch.randn((60, 40), generator=generator(34))).cuda()
+    ids, weights = qm.qm_route_experts(logits, 32, scoring=qm.QM_SCORE_SIGMOID)
+    want_ids, want = lp.route(logits, 32, None, True, 1, 1, 2, True, 1.0)
+    assert torch.equal(ids.cpu(), want_ids)
+    x = logits.double().cpu()
+    dist = (x - x.amax(-1, keepdim=True)).abs().gather(1, want_ids.long()).amax(-1, keepdim=True)
+    near(weights, want, (dist + 64) * 2.0 ** -24 * want.abs() * 2 + 2.0 ** -102)
