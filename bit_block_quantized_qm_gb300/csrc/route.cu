@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasOf<PER>) route_kernel(const 
         // mostly small, the products), where s |d| is s_top / e at most; a sigmoid by 4 units.
         // The bias adds a rounding of the choice (2^-24 of it).  A group's sum of two is off by
         // `near` at most, and the roundings (drop_groups).
-        near = 0x1p-22f * (c.sigmoid ? 4.f * s_top : (9.f + PER) * s_top);
+        // Scores near the end of f32's range are off by 2^-128 at most.
+        near = 0x1p-22f * (c.sigmoid ? 4.f * s_top : (9.f + PER) * s_top) + 0x1p-126f;
     }
     bool again = false;
     if (c.groups > 1) again = drop_groups(c, choice, key, lane, near);

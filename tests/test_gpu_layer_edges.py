@@ -142,3 +142,18 @@ def test_route_weights_of_scores_far_apart(qm, at):  # noqa: F811
     x = logits.double().cpu()
     dist = (x - x.amax(-1, keepdim=True)).abs().gather(1, want_ids.long()).amax(-1, keepdim=True)
     near(weights, want, (dist + 64) * 2.0 ** -24 * want.abs() * 2 + 2.0 ** -102)
+
+
+@pytest.mark.parametrize("at", [-86.0, -88.5, -91.0, -103.0])
+def test_route_groups_of_small_scores(qm, at):  # noqa: F811
+    """Groups whose scores are near the end of f32's range, or below it."""
+    gen = generator(35)
+    for dtype in (F32, BF16):
+        logits = (at + torch.randn((200, 64), generator=gen)).to(dtype).cuda()
+        for group_top in (1, 2):
+            check_route(qm, logits, 9, sigmoid=True, groups=16, top_groups=5, group_top=group_top)
+            check_route(qm, logits, 9, sigmoid=True, groups=16, top_groups=5, group_top=group_top, bias=torch.zeros(64, device="cuda"))
+    far = torch.zeros((200, 64))
+    far[:, 1:] = at + torch.randn((200, 63), generator=gen)
+    check_route(qm, far.cuda(), 9, groups=16, top_groups=5, renormalize=False)
+    check_route(qm, far.cuda(), 9, renormalize=False, bias=torch.zeros(64, device="cuda"))
